@@ -346,7 +346,7 @@ __device__ __forceinline__ long long slot_of(const DevPool &p, int page_size, in
     return -1;
   }
   const int page = __ldg(p.pt + (long long)req * p.pt_stride + pi);
-  if (page < 0 || (long long)(page + 1) * page_size > p.num_slots) {
+  if (page < 0 || ((long long)page + 1) * page_size > p.num_slots) {
     atomicOr(status, KAMERA_DEVICE_SLOT_OOB);
     return -1;
   }

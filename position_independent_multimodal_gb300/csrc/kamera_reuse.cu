@@ -415,7 +415,7 @@ __device__ __forceinline__ void run_task(const ReuseArgs &a, unsigned char *smem
                    : "=r"(page)
                    : "r"(pg_op + s * P.pages_stage + 4 * (pg - p_first)));
       __nv_bfloat16 *dst = nullptr;
-      if (page >= 0 && (long long)(page + 1) * lay.page_size <= a.pool.num_slots)
+      if (page >= 0 && ((long long)page + 1) * lay.page_size <= a.pool.num_slots)
         dst = pool + ((long long)page * lay.page_size + in_page) * row;
       else
         atomicOr(a.status, KAMERA_DEVICE_SLOT_OOB);

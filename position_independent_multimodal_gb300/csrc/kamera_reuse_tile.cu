@@ -229,7 +229,7 @@ __device__ __forceinline__ void task_loop(const ReuseArgs &a, uint32_t s0, unsig
           int pg, in_page;
           psd.split(it.start_tok + t0 + rr, &pg, &in_page);
           const int page = __ldg(ptab + pg);
-          if (page >= 0 && (long long)(page + 1) * ps <= a.pool.num_slots) {
+          if (page >= 0 && ((long long)page + 1) * ps <= a.pool.num_slots) {
             const __nv_bfloat16 *src =
                 pool_ch + ((long long)layer * a.pool.num_slots + (long long)page * ps + in_page) *
                               row + tile.col0 + 8 * lc;
@@ -401,7 +401,7 @@ __device__ __forceinline__ void task_loop(const ReuseArgs &a, uint32_t s0, unsig
           const int page = lds_i32t(pg_op + s * P.pages_stage +
                                     4 * (f * P.pg_per_member + pg - p_first));
           int slot = -1;
-          if (page >= 0 && (long long)(page + 1) * ps <= a.pool.num_slots)
+          if (page >= 0 && ((long long)page + 1) * ps <= a.pool.num_slots)
             slot = page * ps + in_page;
           else
             atomicOr(a.status, KAMERA_DEVICE_SLOT_OOB);
@@ -413,7 +413,7 @@ __device__ __forceinline__ void task_loop(const ReuseArgs &a, uint32_t s0, unsig
       psd.split(it.start_tok + t0, &p_first, &off0);
       const int page = lds_i32t(pg_op + s * P.pages_stage + 4 * (pg - p_first));
       unsigned long long dst = 0;
-      if (page >= 0 && (long long)(page + 1) * ps <= a.pool.num_slots)
+      if (page >= 0 && ((long long)page + 1) * ps <= a.pool.num_slots)
         dst = static_cast<unsigned long long>(__cvta_generic_to_global(
             (ch == 0 ? a.pool.k : a.pool.v) +
             ((long long)layer * a.pool.num_slots + (long long)page * ps + in_page) * row +
@@ -1339,7 +1339,7 @@ __global__ void __launch_bounds__(kThrT, 2) reuse_persist_kernel(const __grid_co
         const int page = lds_i32t(pg_op + s * P.pages_stage +
                                   4 * (f * P.pg_per_member + pg - p_first));
         int slot = -1;
-        if (page >= 0 && (long long)(page + 1) * ps <= a.pool.num_slots)
+        if (page >= 0 && ((long long)page + 1) * ps <= a.pool.num_slots)
           slot = page * ps + in_page;
         else
           atomicOr(a.status, KAMERA_DEVICE_SLOT_OOB);
