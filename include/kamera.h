@@ -56,6 +56,8 @@ typedef enum kamera_status {
                                        kamera_reuse makes on the host; none of it was written */
 #define KAMERA_DEVICE_TIMEOUT 0x4u  /* a tensor-core tile did not complete within 2 s; its
                                        rows were not written (never expected)               */
+#define KAMERA_DEVICE_NO_PAGES 0x8u /* kamera_fork, kamera_extend: the free pages ran out before
+                                       an item; nothing of it was done                       */
 
 /* Attention families (§3 "One mechanism for MLA, GQA, and MHA"). MHA is GQA with one KV head
  * per query head. */
@@ -387,6 +389,158 @@ kamera_status kamera_decode_attention(const kamera_handle *handle, const kamera_
                                       int32_t num_q_heads, const int32_t *d_ctx_len,
                                       int32_t max_ctx, float scale, float *d_out, float *d_lse,
                                       void *d_workspace, size_t workspace_bytes,
+                                      uint32_t *d_status, kamera_stream_t stream);
+
+/*
+ * New tokens into the pool (the pages start from a pool that an engine has filled; this is the
+ * filling, in the pool's own layout). For each of num_tokens tokens of one layer, in one pass:
+ *   GQA: every query head becomes R(p) (q * rsqrt(mean(q^2) + eps) * q_weight), every key head
+ *        likewise with k_weight, written to the token's K row; v is copied to its V row.
+ *   MLA: c_KV * rsqrt(mean(c_KV^2) + eps) * k_weight and R(p) k_pe are written to the token's
+ *        row; of each absorbed query the latent part is copied and the rope part turned.
+ * R(p) rotates by the token's absolute position with the layout's pairing, base and M-RoPE
+ * sections (as kamera_reanchor). float32 arithmetic, one rounding to bf16 per element.
+ * q        : bf16, token t's num_q_heads heads of Dk (GQA head_dim, MLA latent + rope) at
+ *            q + t * q_stride; NULL with num_q_heads 0 appends keys and values alone.
+ * k, v     : bf16, token t's K row at k + t * k_stride (MLA: c_KV || k_pe), its V row at
+ *            v + t * v_stride; v is NULL for MLA. Strides are in elements, at least a row and
+ *            multiples of 8: q, k and v may be columns of one projection's output.
+ * q_weight : bf16 [head_dim], or NULL: the queries are turned without a norm. NULL for MLA.
+ * k_weight : bf16 [head_dim] (MLA: [latent_dim]), or NULL likewise.
+ * positions: int64 [num_tokens], or [num_tokens][3] = (t, h, w) for M-RoPE layouts.
+ * req, tok : int32 [num_tokens]: the page-table row and logical token of each. A negative req
+ *            marks a row of padding: nothing of it is read but req and tok, nothing written.
+ * q_out    : bf16, heads of token t at q_out + t * q_out_stride; may be q itself (with the same
+ *            stride), and overlaps none of the inputs otherwise.
+ * All device memory; q, k, v, weights and q_out 16-byte aligned, positions 8, req and tok 4.
+ * A req or tok outside the page table sets KAMERA_DEVICE_BAD_ITEM and nothing of that token is
+ * written; a page outside the pool sets KAMERA_DEVICE_SLOT_OOB and the token's K and V are not
+ * written (its queries are). Tokens must not share a slot.
+ */
+typedef struct kamera_new_tokens {
+  const void *q;
+  const void *k;
+  const void *v;
+  const void *q_weight;
+  const void *k_weight;
+  const int64_t *positions;
+  const int32_t *req;
+  const int32_t *tok;
+  void *q_out;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+  int64_t q_out_stride;
+  int32_t num_tokens;
+  int32_t num_q_heads;
+  float eps; /* >= 0 and finite */
+  int32_t reserved; /* set to 0 */
+} kamera_new_tokens;
+
+kamera_status kamera_append(const kamera_handle *handle, const kamera_pool *pool, int32_t layer,
+                            const kamera_new_tokens *tokens, uint32_t *d_status,
+                            kamera_stream_t stream);
+
+/*
+ * The life of the pool's pages (App. E "Context management as reversible state edits" edits a
+ * window; these calls give an engine the pages to do it in). The caller keeps d_refs, int32
+ * [num_slots / page_size] on the device: how many page-table entries hold each page; 0 is free.
+ * The calls below write d_refs and the pool's page table (which the other calls only read) and
+ * leave every entry that they do not name as it was. New pages are handed out lowest first, in
+ * the order of the items, so results depend on the arguments alone. Item arrays are device
+ * memory, checked on the device: an item out of range sets KAMERA_DEVICE_BAD_ITEM and is
+ * skipped. Tokens [a, b) of a request hold the page-table entries ceil(a / page_size) up to
+ * ceil(b / page_size): a span that starts inside a page starts behind that page.
+ *
+ * kamera_fork: request `child` continues request `parent` after its first num_tokens tokens.
+ *   The whole pages are shared (the child's entries name them, their counts rise); a last page
+ *   that is not full is copied to a new page in every layer (its first num_tokens % page_size
+ *   rows). The child's row must hold nothing before. No request is a child twice, or a child
+ *   and a parent, in one call; one parent may have many children.
+ * kamera_extend: pages for tokens [from_tok, to_tok) of a request, each with count 1.
+ *   When the free pages run out before an item of kamera_fork or kamera_extend, that item and
+ *   later ones that need pages set KAMERA_DEVICE_NO_PAGES and nothing of them is done.
+ * kamera_free: the entries of tokens [from_tok, to_tok) become -1 and their pages' counts drop;
+ *   a page with count 0 is free. from_tok 0 releases a request, a later one its tail. An entry
+ *   outside the pool sets KAMERA_DEVICE_SLOT_OOB, a page that nothing held
+ *   KAMERA_DEVICE_BAD_ITEM; an entry that two items name is released once.
+ * kamera_compact: the live pages (count not 0) come to lie in pages 0 .. live - 1: the k-th live
+ *   page above that border moves to the k-th free page below it, in every layer; counts and
+ *   every page-table entry that names a moved page follow. The rows of the freed pages are left
+ *   as they were. d_num_live (int32, device) gets the number of live pages.
+ * kamera_copy_pages: page d_src[i] onto page d_dst[i] for i < num_pairs (int32, device), every
+ *   layer, K and V. d_dst names no page twice and none of d_src. A page outside the pool sets
+ *   KAMERA_DEVICE_SLOT_OOB and the pair is skipped. Table and counts stay.
+ * d_workspace: kamera_page_workspace(handle, num_slots, num_items) bytes of device memory,
+ *   16-byte aligned (num_items 0 for kamera_compact); contents ignored and left undefined.
+ * num_items and num_pairs at most 65535; items 4-byte aligned.
+ */
+typedef struct kamera_fork_item {
+  int32_t parent;
+  int32_t child;
+  int32_t num_tokens;
+} kamera_fork_item;
+
+typedef struct kamera_page_span {
+  int32_t req;
+  int32_t from_tok;
+  int32_t to_tok;
+} kamera_page_span;
+
+size_t kamera_page_workspace(const kamera_handle *handle, int64_t num_slots, int32_t num_items);
+
+kamera_status kamera_fork(const kamera_handle *handle, const kamera_pool *pool,
+                          const kamera_fork_item *d_items, int32_t num_items, int32_t *d_refs,
+                          void *d_workspace, size_t workspace_bytes, uint32_t *d_status,
+                          kamera_stream_t stream);
+kamera_status kamera_extend(const kamera_handle *handle, const kamera_pool *pool,
+                            const kamera_page_span *d_items, int32_t num_items, int32_t *d_refs,
+                            void *d_workspace, size_t workspace_bytes, uint32_t *d_status,
+                            kamera_stream_t stream);
+kamera_status kamera_free(const kamera_handle *handle, const kamera_pool *pool,
+                          const kamera_page_span *d_items, int32_t num_items, int32_t *d_refs,
+                          uint32_t *d_status, kamera_stream_t stream);
+kamera_status kamera_compact(const kamera_handle *handle, const kamera_pool *pool,
+                             int32_t *d_refs, int32_t *d_num_live, void *d_workspace,
+                             size_t workspace_bytes, uint32_t *d_status, kamera_stream_t stream);
+kamera_status kamera_copy_pages(const kamera_handle *handle, const kamera_pool *pool,
+                                const int32_t *d_src, const int32_t *d_dst, int32_t num_pairs,
+                                uint32_t *d_status, kamera_stream_t stream);
+
+/*
+ * Decode attention of a batch whose requests share prefixes (§5 "Reorder" and "Recall": many
+ * requests over the same reused chunks). As kamera_decode_attention, one query token per
+ * request over its tokens [0, ctx_len[r]), but the requests come in groups, and the first
+ * prefix_len[g] tokens of a group's requests are the same: they are attended once for all the
+ * group's query rows, through the page-table row of its first request with a context that is
+ * not empty, and joined to each request's own part by their log-sum-exp (§1:
+ * o = (1 - mu) o_B + mu o_A). After kamera_fork the prefix of parent and children is such a one.
+ * d_q          : bf16 [num_reqs][num_q_heads][Dk], device, 16-byte aligned.
+ * d_group_start: int32 [num_groups + 1]: requests group_start[g] .. group_start[g + 1] - 1 are
+ *                group g; from 0 to num_reqs, never falling. Otherwise the whole call sets
+ *                KAMERA_DEVICE_BAD_ITEM and writes no output. 1 <= num_groups <= num_reqs.
+ * d_prefix_len : int32 [num_groups], 0 for a group that shares nothing.
+ * d_ctx_len    : int32 [num_reqs]: 0 (an empty context: o = 0, lse = -inf) or at least the
+ *                group's prefix, and at most pt_stride * page_size. Another value sets
+ *                KAMERA_DEVICE_BAD_ITEM and that request's outputs are not written.
+ * d_out        : bf16 [num_reqs][num_q_heads][Dv]; d_lse: float32 [num_reqs][num_q_heads]
+ *                (natural log).
+ * d_workspace  : kamera_prefix_attention_workspace(handle, num_reqs, num_q_heads) bytes of
+ *                device memory, 16-byte aligned; contents ignored and left undefined.
+ * GQA and MLA as in kamera_decode_attention; softmax statistics and sums in float32. Layouts
+ * that take the tensor cores round the softmax weights to bf16. Pages outside the pool set
+ * KAMERA_DEVICE_SLOT_OOB and their tokens are left out. Limits: num_reqs <= 65535 and at most
+ * the pool's num_reqs, num_q_heads <= 256 (GQA: a multiple of num_kv_heads), Dk <= 1024.
+ */
+size_t kamera_prefix_attention_workspace(const kamera_handle *handle, int32_t num_reqs,
+                                         int32_t num_q_heads);
+
+kamera_status kamera_prefix_attention(const kamera_handle *handle, const kamera_pool *pool,
+                                      int32_t layer, const void *d_q, int32_t num_reqs,
+                                      int32_t num_q_heads, const int32_t *d_group_start,
+                                      const int32_t *d_prefix_len, int32_t num_groups,
+                                      const int32_t *d_ctx_len, float scale, void *d_out,
+                                      float *d_lse, void *d_workspace, size_t workspace_bytes,
                                       uint32_t *d_status, kamera_stream_t stream);
 
 /*

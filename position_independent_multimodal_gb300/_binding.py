@@ -22,6 +22,8 @@ KAMERA_ERR_UNSUPPORTED = 2
 KAMERA_ERR_CUDA = 3
 KAMERA_DEVICE_SLOT_OOB = 0x1
 KAMERA_DEVICE_BAD_ITEM = 0x2
+KAMERA_DEVICE_TIMEOUT = 0x4
+KAMERA_DEVICE_NO_PAGES = 0x8
 KAMERA_GQA = 0
 KAMERA_MLA = 1
 KAMERA_ROPE_NEOX_HALF = 0
@@ -74,6 +76,17 @@ class kamera_anchor_item(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class kamera_new_tokens(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("req", ctypes.c_void_p),
+                ("tok", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64),
+                ("num_tokens", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
 ITEM_BYTES = ctypes.sizeof(kamera_item)
 _lib = None
 
@@ -120,6 +133,23 @@ def lib() -> ctypes.CDLL:
                                         i64, vp, i64, vp, vp, ctypes.c_size_t, vp]
         L.kamera_form_patch_static_scratch.argtypes = [vp, i64, i64, i32, i32, i32, vp, i64,
                                                        i32, i32, i32, vp, i64, vp, i64, vp, vp]
+        st = ctypes.c_size_t
+        pp = ctypes.POINTER(kamera_pool)
+        L.kamera_append.argtypes = [vp, pp, i32, ctypes.POINTER(kamera_new_tokens), vp, vp]
+        L.kamera_page_workspace.argtypes = [vp, i64, i32]
+        L.kamera_page_workspace.restype = st
+        L.kamera_fork.argtypes = [vp, pp, vp, i32, vp, vp, st, vp, vp]
+        L.kamera_extend.argtypes = [vp, pp, vp, i32, vp, vp, st, vp, vp]
+        L.kamera_free.argtypes = [vp, pp, vp, i32, vp, vp, vp]
+        L.kamera_compact.argtypes = [vp, pp, vp, vp, vp, st, vp, vp]
+        L.kamera_copy_pages.argtypes = [vp, pp, vp, vp, i32, vp, vp]
+        L.kamera_prefix_attention_workspace.argtypes = [vp, i32, i32]
+        L.kamera_prefix_attention_workspace.restype = st
+        L.kamera_prefix_attention.argtypes = [vp, pp, i32, vp, i32, i32, vp, vp, i32, vp,
+                                              ctypes.c_float, vp, vp, vp, st, vp, vp]
+        for f in ("kamera_append", "kamera_fork", "kamera_extend", "kamera_free",
+                  "kamera_compact", "kamera_copy_pages", "kamera_prefix_attention"):
+            getattr(L, f).restype = ctypes.c_int
         for f in ("kamera_create", "kamera_destroy", "kamera_relocate", "kamera_reuse",
                   "kamera_set_option", "kamera_set_batch_workspace",
                   "kamera_batch_reuse", "kamera_rope_phases", "kamera_batch_reuse_timed",
@@ -336,6 +366,221 @@ def kamera_decode_attention(handle: Handle, pool: Pool, layer: int, q: torch.Ten
                                          int(max_ctx), float(scale), _ptr(out), _ptr(lse),
                                          _ptr(workspace), int(nbytes), _ptr(status),
                                          _stream(stream)), "kamera_decode_attention")
+
+
+def _need(what: str, t, dtype, device: int, contiguous: bool = True) -> None:
+    """Raise ValueError unless ``t`` is a tensor of ``dtype`` on CUDA device ``device``."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.get_device() != device or \
+            (contiguous and not t.is_contiguous()):
+        raise ValueError(f"{what} must be a{' contiguous' if contiguous else ''} {dtype} tensor "
+                         f"on the current CUDA device")
+
+
+def _pool_device(pool: Pool) -> int:
+    """The device of a pool's tensors, which has to be the current one: kernels are launched
+    there, on the current stream unless another is given."""
+    dev = pool.k.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("the pool must be on the current CUDA device")
+    _need("pool.k", pool.k, torch.bfloat16, dev)
+    if pool.v is not None:
+        _need("pool.v", pool.v, torch.bfloat16, dev)
+    _need("pool.page_table", pool.page_table, torch.int32, dev, contiguous=False)
+    if pool.page_table.dim() != 2 or pool.page_table.stride(1) != 1:
+        raise ValueError("pool.page_table must be [num_reqs][pt_stride]")
+    return dev
+
+
+def _pool_shape(handle: Handle, pool: Pool) -> None:
+    """Raise ValueError unless the pool's tensors have the handle's layers and row widths."""
+    c = handle._c
+    gqa = c.kind == KAMERA_GQA
+    row = c.num_kv_heads * c.head_dim if gqa else c.latent_dim + c.rope_dim
+    want = (c.num_layers, pool.num_slots, row)
+    if tuple(pool.k.shape) != want or (pool.v is not None and tuple(pool.v.shape) != want) or \
+            (pool.v is None) == gqa:
+        raise ValueError(f"the pool's tensors must be {want}, K and V for GQA, K alone for MLA")
+
+
+def _items(what: str, t: torch.Tensor, dev: int) -> None:
+    _need(what, t, torch.int32, dev)
+    if t.dim() != 2 or t.shape[1] != 3:
+        raise ValueError(f"{what} must be [n][3]")
+
+
+def _bytes(t: Optional[torch.Tensor], dev: int) -> int:
+    if t is None:
+        return 0
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("the workspace must be a contiguous tensor on the current CUDA device")
+    return t.numel() * t.element_size()
+
+
+def _heads(what: str, t: torch.Tensor, dev: int, tokens: int, heads: int, width: int) -> int:
+    """The token stride of bf16 [tokens][heads][width] whose heads lie side by side."""
+    _need(what, t, torch.bfloat16, dev, contiguous=False)
+    if tuple(t.shape) != (tokens, heads, width) or t.stride(2) != 1 or \
+            (heads > 1 and t.stride(1) != width):
+        raise ValueError(f"{what} must be [{tokens}][{heads}][{width}] with contiguous heads")
+    return t.stride(0) if tokens > 1 else max(t.stride(0), heads * width)
+
+
+def kamera_append(handle: Handle, pool: Pool, layer: int, q: Optional[torch.Tensor],
+                  k: torch.Tensor, v: Optional[torch.Tensor], q_weight: Optional[torch.Tensor],
+                  k_weight: Optional[torch.Tensor], positions: torch.Tensor, req: torch.Tensor,
+                  tok: torch.Tensor, eps: float, q_out: Optional[torch.Tensor],
+                  status: torch.Tensor, stream=None) -> None:
+    """Norm, rotation and append of new tokens: ``q`` [T][H_q][Dk] (or None) into ``q_out``,
+    ``k`` [T][H_kv][head_dim] (MLA: [T][1][latent + rope]) and ``v`` [T][H_kv][head_dim] (MLA:
+    None) into the pool's layer, for tokens ``tok`` of page-table rows ``req`` (int32 [T]) at
+    ``positions`` (int64 [T], or [T][3] under M-RoPE). Token strides are free."""
+    dev = _pool_device(pool)
+    _pool_shape(handle, pool)
+    c = handle._c
+    gqa = c.kind == KAMERA_GQA
+    T = int(k.shape[0])
+    dk, hk = (c.head_dim, c.num_kv_heads) if gqa else (c.latent_dim + c.rope_dim, 1)
+    t = kamera_new_tokens(k=k.data_ptr(), num_tokens=T, eps=float(eps))
+    t.k_stride = _heads("k", k, dev, T, hk, dk)
+    if (v is None) == gqa:
+        raise ValueError("v is given for GQA and None for MLA")
+    if gqa:
+        t.v, t.v_stride = v.data_ptr(), _heads("v", v, dev, T, hk, dk)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out are given together")
+    if q is not None:
+        t.num_q_heads = int(q.shape[1])
+        t.q, t.q_stride = q.data_ptr(), _heads("q", q, dev, T, t.num_q_heads, dk)
+        t.q_out = q_out.data_ptr()
+        t.q_out_stride = _heads("q_out", q_out, dev, T, t.num_q_heads, dk)
+    for name, w, n in (("q_weight", q_weight, dk), ("k_weight", k_weight,
+                                                    dk if gqa else c.latent_dim)):
+        if w is not None:
+            _need(name, w, torch.bfloat16, dev)
+            if w.numel() != n:
+                raise ValueError(f"{name} must have {n} elements")
+            setattr(t, name, w.data_ptr())
+    for name, x, dtype, n in (("positions", positions, torch.int64,
+                               T * (3 if any(c.mrope_section) else 1)),
+                              ("req", req, torch.int32, T), ("tok", tok, torch.int32, T)):
+        _need(name, x, dtype, dev)
+        if x.numel() != n:
+            raise ValueError(f"{name} must have {n} elements")
+        setattr(t, name, x.data_ptr())
+    _need("status", status, torch.int32, dev)
+    p = pool.c()
+    _check(lib().kamera_append(handle.ptr, ctypes.byref(p), int(layer), ctypes.byref(t),
+                               status.data_ptr(), _stream(stream)), "kamera_append")
+
+
+def kamera_page_workspace(handle: Handle, num_slots: int, num_items: int) -> int:
+    """Bytes of workspace for kamera_fork and kamera_extend of up to num_items items, and (with
+    0) for kamera_compact."""
+    return int(lib().kamera_page_workspace(handle.ptr, int(num_slots), int(num_items)))
+
+
+def _page_call(name: str, handle: Handle, pool: Pool, items: torch.Tensor, refs: torch.Tensor,
+               workspace, status: torch.Tensor, stream) -> None:
+    dev = _pool_device(pool)
+    _pool_shape(handle, pool)
+    _items("items", items, dev)
+    _need("refs", refs, torch.int32, dev)
+    _need("status", status, torch.int32, dev)
+    if refs.numel() * handle._c.page_size != pool.num_slots:
+        raise ValueError("refs must have one count for each page of the pool")
+    p = pool.c()
+    args = [handle.ptr, ctypes.byref(p), items.data_ptr(), int(items.shape[0]), refs.data_ptr()]
+    if workspace is not False:
+        args += [_ptr(workspace), _bytes(workspace, dev)]
+    _check(getattr(lib(), name)(*args, status.data_ptr(), _stream(stream)), name)
+
+
+def kamera_fork(handle: Handle, pool: Pool, items: torch.Tensor, refs: torch.Tensor,
+                workspace: torch.Tensor, status: torch.Tensor, stream=None) -> None:
+    """``items`` int32 [n][3] on the device: (parent, child, num_tokens)."""
+    _page_call("kamera_fork", handle, pool, items, refs, workspace, status, stream)
+
+
+def kamera_extend(handle: Handle, pool: Pool, items: torch.Tensor, refs: torch.Tensor,
+                  workspace: torch.Tensor, status: torch.Tensor, stream=None) -> None:
+    """``items`` int32 [n][3] on the device: (req, from_tok, to_tok)."""
+    _page_call("kamera_extend", handle, pool, items, refs, workspace, status, stream)
+
+
+def kamera_free(handle: Handle, pool: Pool, items: torch.Tensor, refs: torch.Tensor,
+                status: torch.Tensor, stream=None) -> None:
+    """``items`` int32 [n][3] on the device: (req, from_tok, to_tok)."""
+    _page_call("kamera_free", handle, pool, items, refs, False, status, stream)
+
+
+def kamera_compact(handle: Handle, pool: Pool, refs: torch.Tensor, num_live: torch.Tensor,
+                   workspace: torch.Tensor, status: torch.Tensor, stream=None) -> None:
+    """Live pages drawn together below the number of live pages, which goes to ``num_live``
+    (int32 [1])."""
+    dev = _pool_device(pool)
+    _pool_shape(handle, pool)
+    _need("refs", refs, torch.int32, dev)
+    _need("num_live", num_live, torch.int32, dev)
+    _need("status", status, torch.int32, dev)
+    if refs.numel() * handle._c.page_size != pool.num_slots:
+        raise ValueError("refs must have one count for each page of the pool")
+    p = pool.c()
+    _check(lib().kamera_compact(handle.ptr, ctypes.byref(p), refs.data_ptr(),
+                                num_live.data_ptr(), _ptr(workspace), _bytes(workspace, dev),
+                                status.data_ptr(), _stream(stream)), "kamera_compact")
+
+
+def kamera_copy_pages(handle: Handle, pool: Pool, src: torch.Tensor, dst: torch.Tensor,
+                      status: torch.Tensor, stream=None) -> None:
+    """Page ``src[i]`` onto page ``dst[i]`` (int32 on the device), every layer, K and V."""
+    dev = _pool_device(pool)
+    _pool_shape(handle, pool)
+    for name, x in (("src", src), ("dst", dst), ("status", status)):
+        _need(name, x, torch.int32, dev)
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst must have as many pages")
+    p = pool.c()
+    _check(lib().kamera_copy_pages(handle.ptr, ctypes.byref(p), src.data_ptr(), dst.data_ptr(),
+                                   src.numel(), status.data_ptr(), _stream(stream)),
+           "kamera_copy_pages")
+
+
+def kamera_prefix_attention_workspace(handle: Handle, num_reqs: int, num_q_heads: int) -> int:
+    """Bytes of workspace for kamera_prefix_attention of up to num_reqs requests."""
+    return int(lib().kamera_prefix_attention_workspace(handle.ptr, int(num_reqs),
+                                                       int(num_q_heads)))
+
+
+def kamera_prefix_attention(handle: Handle, pool: Pool, layer: int, q: torch.Tensor,
+                            group_start: torch.Tensor, prefix_len: torch.Tensor,
+                            ctx_len: torch.Tensor, scale: float, out: torch.Tensor,
+                            lse: torch.Tensor, workspace: torch.Tensor, status: torch.Tensor,
+                            stream=None) -> None:
+    """Decode attention of ``q`` bf16 [R][H_q][Dk] over pool layer ``layer``, requests
+    ``group_start[g]`` .. ``group_start[g + 1] - 1`` sharing their first ``prefix_len[g]``
+    tokens, into ``out`` bf16 [R][H_q][Dv] and ``lse`` float32 [R][H_q]."""
+    dev = _pool_device(pool)
+    _pool_shape(handle, pool)
+    c = handle._c
+    dk, dv = (c.head_dim, c.head_dim) if c.kind == KAMERA_GQA else \
+        (c.latent_dim + c.rope_dim, c.latent_dim)
+    for name, x, dtype in (("q", q, torch.bfloat16), ("out", out, torch.bfloat16),
+                           ("lse", lse, torch.float32), ("group_start", group_start, torch.int32),
+                           ("prefix_len", prefix_len, torch.int32),
+                           ("ctx_len", ctx_len, torch.int32), ("status", status, torch.int32)):
+        _need(name, x, dtype, dev)
+    R, hq = int(q.shape[0]), int(q.shape[1])
+    if tuple(q.shape) != (R, hq, dk) or tuple(out.shape) != (R, hq, dv) or \
+            tuple(lse.shape) != (R, hq) or ctx_len.numel() != R or \
+            group_start.numel() != prefix_len.numel() + 1:
+        raise ValueError(f"q [R][H_q][{dk}], out [R][H_q][{dv}], lse [R][H_q], ctx_len [R], "
+                         "group_start [G + 1] and prefix_len [G] are wanted")
+    p = pool.c()
+    _check(lib().kamera_prefix_attention(
+        handle.ptr, ctypes.byref(p), int(layer), q.data_ptr(), R, hq, group_start.data_ptr(),
+        prefix_len.data_ptr(), prefix_len.numel(), ctx_len.data_ptr(), float(scale),
+        out.data_ptr(), lse.data_ptr(), _ptr(workspace), _bytes(workspace, dev),
+        status.data_ptr(), _stream(stream)), "kamera_prefix_attention")
 
 
 def kamera_rope_phases(handle: Handle, d_deltas: torch.Tensor, d_out: torch.Tensor,

@@ -574,6 +574,220 @@ kamera_status kamera_decode_attention(const kamera_handle *h, const kamera_pool 
   return from_cuda(kamera::launch_attention(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+kamera_status kamera_append(const kamera_handle *h, const kamera_pool *pool, int32_t layer,
+                            const kamera_new_tokens *t, uint32_t *d_status,
+                            kamera_stream_t stream) {
+  if (!h || !t || !d_status) return KAMERA_ERR_INVALID_ARG;
+  kamera::AppendArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.lay = h->lay;
+  kamera_status st = check_pool(h->lay, pool, &a.pool);
+  if (st != KAMERA_OK) return st;
+  const DevLayout &l = h->lay;
+  if (layer < 0 || layer >= l.L || t->num_tokens < 0 || t->num_q_heads < 0 || t->reserved != 0)
+    return KAMERA_ERR_INVALID_ARG;
+  if (!(t->eps >= 0.f) || !std::isfinite(t->eps)) return KAMERA_ERR_INVALID_ARG;
+  if (t->num_q_heads > 256) return KAMERA_ERR_UNSUPPORTED;
+  const bool gqa = l.kind == KAMERA_GQA;
+  const long long q_row = (long long)t->num_q_heads * (gqa ? l.hd : l.row_k);
+  const bool queries = t->num_q_heads > 0;
+  if (t->num_tokens == 0) return KAMERA_OK;
+  auto mis = [](const void *p, uintptr_t al) {
+    return !p || (reinterpret_cast<uintptr_t>(p) & (al - 1));
+  };
+  auto bad_stride = [](int64_t s, long long row) { return s < row || (s & 7) != 0; };
+  if (mis(t->k, 16) || bad_stride(t->k_stride, l.row_k)) return KAMERA_ERR_INVALID_ARG;
+  if (gqa ? (mis(t->v, 16) || bad_stride(t->v_stride, l.row_v)) : t->v != nullptr)
+    return KAMERA_ERR_INVALID_ARG;
+  if (queries && (mis(t->q, 16) || mis(t->q_out, 16) || bad_stride(t->q_stride, q_row) ||
+                  bad_stride(t->q_out_stride, q_row)))
+    return KAMERA_ERR_INVALID_ARG;
+  if (queries && t->q == t->q_out && t->q_stride != t->q_out_stride) return KAMERA_ERR_INVALID_ARG;
+  if ((t->q_weight && (mis(t->q_weight, 16) || !gqa)) || (t->k_weight && mis(t->k_weight, 16)))
+    return KAMERA_ERR_INVALID_ARG;
+  if (mis(t->positions, 8) || mis(t->req, 4) || mis(t->tok, 4)) return KAMERA_ERR_INVALID_ARG;
+  auto bf = [](const void *p) { return static_cast<const __nv_bfloat16 *>(p); };
+  a.layer = layer;
+  a.hq = t->num_q_heads;
+  a.T = t->num_tokens;
+  a.q = bf(t->q);
+  a.k = bf(t->k);
+  a.v = bf(t->v);
+  a.q_stride = t->q_stride;
+  a.k_stride = t->k_stride;
+  a.v_stride = t->v_stride;
+  a.q_out_stride = t->q_out_stride;
+  a.q_weight = bf(t->q_weight);
+  a.k_weight = bf(t->k_weight);
+  a.positions = reinterpret_cast<const long long *>(t->positions);
+  a.req = t->req;
+  a.tok = t->tok;
+  a.q_out = static_cast<__nv_bfloat16 *>(t->q_out);
+  a.eps = t->eps;
+  a.status = d_status;
+  a.freq = h->freq;
+  return from_cuda(kamera::launch_append(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// What the page calls share: the pool, the counts and the workspace (bytes < 0: none needed).
+kamera_status page_args(const kamera_handle *h, const kamera_pool *pool, const void *items,
+                        int32_t n, bool listed, int32_t *d_refs, bool counted, void *ws,
+                        size_t ws_bytes, bool planned, uint32_t *d_status, kamera::PageArgs *a) {
+  if (!h || !d_status) return KAMERA_ERR_INVALID_ARG;
+  std::memset(a, 0, sizeof(*a));
+  a->lay = h->lay;
+  const kamera_status st = check_pool(h->lay, pool, &a->pool);
+  if (st != KAMERA_OK) return st;
+  if (n < 0) return KAMERA_ERR_INVALID_ARG;
+  if (n > 65535) return KAMERA_ERR_UNSUPPORTED;
+  a->num_pages = pool->num_slots / h->lay.page_size;
+  a->table = const_cast<int32_t *>(pool->page_table);
+  a->n = n;
+  a->status = d_status;
+  if (listed && n == 0) return KAMERA_OK;
+  auto mis = [](const void *p, uintptr_t al) {
+    return !p || (reinterpret_cast<uintptr_t>(p) & (al - 1));
+  };
+  if ((listed && mis(items, 4)) || (counted && mis(d_refs, 4))) return KAMERA_ERR_INVALID_ARG;
+  if (planned && (mis(ws, 16) || ws_bytes < kamera::page_workspace(a->num_pages, n)))
+    return KAMERA_ERR_INVALID_ARG;
+  a->refs = d_refs;
+  a->ws = ws;
+  return KAMERA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kamera_page_workspace(const kamera_handle *h, int64_t num_slots, int32_t num_items) {
+  if (!h || num_slots < 0 || num_items < 0) return 0;
+  return kamera::page_workspace(num_slots / h->lay.page_size, num_items);
+}
+
+kamera_status kamera_fork(const kamera_handle *h, const kamera_pool *pool,
+                          const kamera_fork_item *d_items, int32_t num_items, int32_t *d_refs,
+                          void *d_workspace, size_t workspace_bytes, uint32_t *d_status,
+                          kamera_stream_t stream) {
+  kamera::PageArgs a;
+  const kamera_status st = page_args(h, pool, d_items, num_items, true, d_refs, true, d_workspace,
+                                     workspace_bytes, true, d_status, &a);
+  if (st != KAMERA_OK || num_items == 0) return st;
+  a.forks = d_items;
+  return from_cuda(kamera::launch_fork(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kamera_status kamera_extend(const kamera_handle *h, const kamera_pool *pool,
+                            const kamera_page_span *d_items, int32_t num_items, int32_t *d_refs,
+                            void *d_workspace, size_t workspace_bytes, uint32_t *d_status,
+                            kamera_stream_t stream) {
+  kamera::PageArgs a;
+  const kamera_status st = page_args(h, pool, d_items, num_items, true, d_refs, true, d_workspace,
+                                     workspace_bytes, true, d_status, &a);
+  if (st != KAMERA_OK || num_items == 0) return st;
+  a.spans = d_items;
+  return from_cuda(kamera::launch_extend(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kamera_status kamera_free(const kamera_handle *h, const kamera_pool *pool,
+                          const kamera_page_span *d_items, int32_t num_items, int32_t *d_refs,
+                          uint32_t *d_status, kamera_stream_t stream) {
+  kamera::PageArgs a;
+  const kamera_status st = page_args(h, pool, d_items, num_items, true, d_refs, true, nullptr, 0,
+                                     false, d_status, &a);
+  if (st != KAMERA_OK || num_items == 0) return st;
+  a.spans = d_items;
+  return from_cuda(kamera::launch_free(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kamera_status kamera_compact(const kamera_handle *h, const kamera_pool *pool, int32_t *d_refs,
+                             int32_t *d_num_live, void *d_workspace, size_t workspace_bytes,
+                             uint32_t *d_status, kamera_stream_t stream) {
+  kamera::PageArgs a;
+  const kamera_status st = page_args(h, pool, nullptr, 0, false, d_refs, true, d_workspace,
+                                     workspace_bytes, true, d_status, &a);
+  if (st != KAMERA_OK) return st;
+  if (!d_num_live || (reinterpret_cast<uintptr_t>(d_num_live) & 3u)) return KAMERA_ERR_INVALID_ARG;
+  a.num_live = d_num_live;
+  return from_cuda(kamera::launch_compact(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kamera_status kamera_copy_pages(const kamera_handle *h, const kamera_pool *pool,
+                                const int32_t *d_src, const int32_t *d_dst, int32_t num_pairs,
+                                uint32_t *d_status, kamera_stream_t stream) {
+  kamera::PageArgs a;
+  const kamera_status st = page_args(h, pool, d_src, num_pairs, true, nullptr, false, nullptr, 0,
+                                     false, d_status, &a);
+  if (st != KAMERA_OK || num_pairs == 0) return st;
+  if (!d_dst || (reinterpret_cast<uintptr_t>(d_dst) & 3u)) return KAMERA_ERR_INVALID_ARG;
+  a.src = d_src;
+  a.dst = d_dst;
+  return from_cuda(kamera::launch_copy_pages(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t kamera_prefix_attention_workspace(const kamera_handle *h, int32_t num_reqs,
+                                         int32_t num_q_heads) {
+  if (!h || num_reqs < 0 || num_q_heads < 0) return 0;
+  const int dv = h->lay.kind == KAMERA_GQA ? h->lay.hd : h->lay.latent;
+  return kamera::prefix_workspace(h->lay, num_reqs, num_q_heads, dv);
+}
+
+kamera_status kamera_prefix_attention(const kamera_handle *h, const kamera_pool *pool,
+                                      int32_t layer, const void *d_q, int32_t num_reqs,
+                                      int32_t num_q_heads, const int32_t *d_group_start,
+                                      const int32_t *d_prefix_len, int32_t num_groups,
+                                      const int32_t *d_ctx_len, float scale, void *d_out,
+                                      float *d_lse, void *d_workspace, size_t workspace_bytes,
+                                      uint32_t *d_status, kamera_stream_t stream) {
+  if (!h || !d_status) return KAMERA_ERR_INVALID_ARG;
+  kamera::PrefixArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.lay = h->lay;
+  kamera_status st = check_pool(h->lay, pool, &a.pool);
+  if (st != KAMERA_OK) return st;
+  const DevLayout &l = h->lay;
+  const bool gqa = l.kind == KAMERA_GQA;
+  if (layer < 0 || layer >= l.L || num_reqs < 0 || num_q_heads < 1) return KAMERA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return KAMERA_ERR_INVALID_ARG;
+  if (num_q_heads > 256 || num_reqs > 65535) return KAMERA_ERR_UNSUPPORTED;
+  if (gqa && num_q_heads % l.H != 0) return KAMERA_ERR_INVALID_ARG;
+  const int dk = gqa ? l.hd : l.latent + l.rope_d, dv = gqa ? l.hd : l.latent;
+  if (dk > 1024) return KAMERA_ERR_UNSUPPORTED;
+  if (num_reqs > a.pool.num_reqs) return KAMERA_ERR_INVALID_ARG;
+  if (num_reqs == 0) return KAMERA_OK;
+  if (num_groups < 1 || num_groups > num_reqs) return KAMERA_ERR_INVALID_ARG;
+  auto mis = [](const void *p, uintptr_t al) {
+    return !p || (reinterpret_cast<uintptr_t>(p) & (al - 1));
+  };
+  if (mis(d_q, 16) || mis(d_group_start, 4) || mis(d_prefix_len, 4) || mis(d_ctx_len, 4) ||
+      mis(d_out, 16) || mis(d_lse, 4) || mis(d_workspace, 16))
+    return KAMERA_ERR_INVALID_ARG;
+  if (workspace_bytes < kamera::prefix_workspace(l, num_reqs, num_q_heads, dv))
+    return KAMERA_ERR_INVALID_ARG;
+  a.layer = layer;
+  a.q = static_cast<const __nv_bfloat16 *>(d_q);
+  a.group_start = d_group_start;
+  a.prefix_len = d_prefix_len;
+  a.ctx_len = d_ctx_len;
+  a.n_reqs = num_reqs;
+  a.n_groups = num_groups;
+  a.hq = num_q_heads;
+  a.n_kv = gqa ? l.H : 1;
+  a.dk = dk;
+  a.dv = dv;
+  kamera::prefix_shape(l, &a.rb, &a.tile, &a.vh, &a.n_ctas);
+  a.scale = scale;
+  a.ws = d_workspace;
+  a.out = static_cast<__nv_bfloat16 *>(d_out);
+  a.lse = d_lse;
+  a.status = d_status;
+  return from_cuda(kamera::launch_prefix_attention(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 kamera_status kamera_rope_phases(const kamera_handle *h, const int64_t *d_deltas,
                                  int32_t num_deltas, float *d_out, kamera_stream_t stream) {
   if (!h || num_deltas < 0) return KAMERA_ERR_INVALID_ARG;

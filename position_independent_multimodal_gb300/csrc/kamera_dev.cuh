@@ -159,6 +159,56 @@ struct AttnArgs {
   unsigned *status;
 };
 
+struct AppendArgs {
+  DevLayout lay;
+  DevPool pool;
+  int layer, hq;
+  long long T;
+  const __nv_bfloat16 *q, *k, *v;  // token t at q + t * q_stride, ...
+  long long q_stride, k_stride, v_stride, q_out_stride;
+  const __nv_bfloat16 *q_weight, *k_weight;  // null: no norm
+  const long long *positions;                // [T] or [T][3]
+  const int *req, *tok;                      // [T]
+  __nv_bfloat16 *q_out;
+  float eps;
+  unsigned *status;
+  FreqQ64 freq;
+};
+
+struct PageArgs {
+  DevLayout lay;
+  DevPool pool;
+  int32_t *table;                  // the pool's page table, written
+  long long num_pages;
+  int *refs;                       // [num_pages]
+  const kamera_fork_item *forks;   // one of the two, neither for compaction and copies
+  const kamera_page_span *spans;
+  const int *src, *dst;            // copies
+  int n;                           // items
+  int *num_live;                   // compaction
+  void *ws;
+  unsigned *status;
+};
+
+constexpr int kPrefixCtas = 152;  // SMs of a GB300
+
+struct PrefixArgs {
+  DevLayout lay;
+  DevPool pool;
+  int layer;
+  const __nv_bfloat16 *q;  // [n_reqs][hq][dk]
+  const int *group_start;  // [n_groups + 1]
+  const int *prefix_len;   // [n_groups]
+  const int *ctx_len;      // [n_reqs]
+  int n_reqs, n_groups, hq, n_kv, dk, dv;
+  int rb, tile, vh, n_ctas;  // rows of a block, tokens of a tile, column halves of V, CTAs
+  float scale;
+  void *ws;
+  __nv_bfloat16 *out;      // [n_reqs][hq][dv]
+  float *lse;              // [n_reqs][hq]
+  unsigned *status;
+};
+
 // The rules an item must satisfy (host: kamera_reuse; device: each batch item).
 __host__ __device__ inline bool aligned16(const void *p) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
@@ -559,6 +609,16 @@ size_t attn_workspace(long long n_reqs, int hq, int max_ctx, int dv);  // kamera
 size_t attn_smem(int dk, int dv);
 int attn_split_tokens(const DevLayout &l);
 cudaError_t launch_attention(const AttnArgs &a, cudaStream_t s);
+cudaError_t launch_append(const AppendArgs &a, cudaStream_t s);     // kamera_append.cu
+size_t page_workspace(long long num_pages, int n);                  // kamera_pages.cu
+cudaError_t launch_fork(const PageArgs &a, cudaStream_t s);
+cudaError_t launch_extend(const PageArgs &a, cudaStream_t s);
+cudaError_t launch_free(const PageArgs &a, cudaStream_t s);
+cudaError_t launch_compact(const PageArgs &a, cudaStream_t s);
+cudaError_t launch_copy_pages(const PageArgs &a, cudaStream_t s);
+void prefix_shape(const DevLayout &l, int *rb, int *tile, int *vh, int *n_ctas);  // kamera_prefix.cu
+size_t prefix_workspace(const DevLayout &l, long long n_reqs, int hq, int dv);
+cudaError_t launch_prefix_attention(const PrefixArgs &a, cudaStream_t s);
 cudaError_t launch_rope_phases(const FreqQ64 &f, int npairs, const long long *deltas, int n,
                                float *out, cudaStream_t s);
 
