@@ -437,6 +437,7 @@ __global__ void __launch_bounds__(kThr) prefix_merge_kernel(const __grid_constan
 }  // namespace
 
 void prefix_shape(const DevLayout &l, int *rb, int *tile, int *vh, int *n_ctas) {
+  if (prefix_tc_layout(l)) return prefix_tc_shape(l, rb, tile, vh, n_ctas);
   *rb = kRows;
   *tile = kTile;
   *vh = 1;
@@ -461,6 +462,7 @@ cudaError_t launch_prefix_attention(const PrefixArgs &a, cudaStream_t s) {
     if (!configured[dev]) {
       e = cudaFuncSetAttribute(prefix_gen_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                gen_plan(1024, 1024).total);
+      if (e == cudaSuccess) e = prepare_prefix_tc();
       if (e != cudaSuccess) return e;
       configured[dev] = 1;
     }
@@ -468,8 +470,12 @@ cudaError_t launch_prefix_attention(const PrefixArgs &a, cudaStream_t s) {
   prefix_plan_kernel<<<1, kPlanThr, 0, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  prefix_gen_kernel<<<a.n_ctas, kThr, gen_plan(a.dk, a.dv).total, s>>>(a);
-  e = cudaGetLastError();
+  if (prefix_tc_layout(a.lay)) {
+    e = launch_prefix_tc(a, s);
+  } else {
+    prefix_gen_kernel<<<a.n_ctas, kThr, gen_plan(a.dk, a.dv).total, s>>>(a);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
   const long long warps = (long long)a.n_reqs * a.hq * a.vh;
   prefix_merge_kernel<<<(unsigned)((warps + kThr / 32 - 1) / (kThr / 32)), kThr, 0, s>>>(a);
