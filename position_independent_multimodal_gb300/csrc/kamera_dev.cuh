@@ -616,11 +616,12 @@ cudaError_t launch_extend(const PageArgs &a, cudaStream_t s);
 cudaError_t launch_free(const PageArgs &a, cudaStream_t s);
 cudaError_t launch_compact(const PageArgs &a, cudaStream_t s);
 cudaError_t launch_copy_pages(const PageArgs &a, cudaStream_t s);
-void prefix_shape(const DevLayout &l, int *rb, int *tile, int *vh, int *n_ctas);  // kamera_prefix.cu
+// kamera_prefix.cu
+void prefix_shape(const DevLayout &l, int hq, int *rb, int *tile, int *vh, int *n_ctas);
 size_t prefix_workspace(const DevLayout &l, long long n_reqs, int hq, int dv);
 cudaError_t launch_prefix_attention(const PrefixArgs &a, cudaStream_t s);
 bool prefix_tc_layout(const DevLayout &l);                          // kamera_prefix_tc.cu
-void prefix_tc_shape(const DevLayout &l, int *rb, int *tile, int *vh, int *n_ctas);
+void prefix_tc_shape(const DevLayout &l, int hq, int *rb, int *tile, int *vh, int *n_ctas);
 cudaError_t prepare_prefix_tc();
 cudaError_t launch_prefix_tc(const PrefixArgs &a, cudaStream_t s);
 cudaError_t launch_rope_phases(const FreqQ64 &f, int npairs, const long long *deltas, int n,

@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_cons
     p.req_at[r] = r - s0;
     p.req_size[r] = a.group_start[lo + 1] - s0;
     p.req_tiles[r] = active ? ceil_div(prefix, a.tile) : 0;
-    p.req_own[r] = active ? ceil_div(ctx - prefix, a.tile) : 0;
+    p.req_own[r] = active ? tiles_of(prefix, ctx, a.tile) : 0;
   }
   __syncthreads();
   // groups: units of each prefix
@@ -239,8 +239,8 @@ __global__ void __launch_bounds__(kThr) prefix_gen_kernel(const __grid_constant_
         gqa ? a.pool.v + (long long)a.layer * a.pool.num_slots * lay.row_v + s.kvh * lay.hd
             : a.pool.k + (long long)a.layer * a.pool.num_slots * lay.row_k;
     const int vrow = gqa ? lay.row_v : lay.row_k;
-    for (int t0 = s.tok0; t0 < s.tok1; t0 += kTile) {
-      const int n = min(kTile, s.tok1 - t0);
+    for (int t0 = s.tok0, n; t0 < s.tok1; t0 += n) {
+      n = min(kTile - t0 % kTile, s.tok1 - t0);
       __syncthreads();  // the last tile's slots and weights have been read
       const long long slot =
           tid < n ? slot_of(a.pool, lay.page_size, s.lead, (long long)t0 + tid, a.status) : -1;
@@ -436,8 +436,8 @@ __global__ void __launch_bounds__(kThr) prefix_merge_kernel(const __grid_constan
 
 }  // namespace
 
-void prefix_shape(const DevLayout &l, int *rb, int *tile, int *vh, int *n_ctas) {
-  if (prefix_tc_layout(l)) return prefix_tc_shape(l, rb, tile, vh, n_ctas);
+void prefix_shape(const DevLayout &l, int hq, int *rb, int *tile, int *vh, int *n_ctas) {
+  if (prefix_tc_layout(l)) return prefix_tc_shape(l, hq, rb, tile, vh, n_ctas);
   *rb = kRows;
   *tile = kTile;
   *vh = 1;
@@ -446,7 +446,7 @@ void prefix_shape(const DevLayout &l, int *rb, int *tile, int *vh, int *n_ctas) 
 
 size_t prefix_workspace(const DevLayout &l, long long n_reqs, int hq, int dv) {
   int rb, tile, vh, n;
-  prefix_shape(l, &rb, &tile, &vh, &n);
+  prefix_shape(l, hq, &rb, &tile, &vh, &n);
   return prefix_plan(nullptr, n_reqs, hq, dv, vh, rb, n).total;
 }
 

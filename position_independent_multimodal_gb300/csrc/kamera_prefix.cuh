@@ -5,6 +5,7 @@
 // (request, query head) rows of a group for the group's prefix, or one request's rows for the
 // tokens after it. A unit is one tile of `tile` tokens of one block; units are numbered prefix
 // blocks first (group, KV head and column half, row block, tile), then own blocks (request, ...).
+// Tiles lie at multiples of `tile` tokens, so a request's own part starts and ends inside one.
 // CTA c of n takes units [c U / n, (c + 1) U / n), so every CTA has the same number of tiles
 // whatever the lengths; a range cuts at most its first and last block. A block's first segment
 // writes its rows' partial output to the rows' home place, a segment that starts inside a block
@@ -83,7 +84,12 @@ __host__ __device__ inline PrefixPlan prefix_plan(void *ws, long long R, int hq,
   return p;
 }
 
-__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+__host__ __device__ inline int ceil_div(int a, int b) { return (int)(((unsigned)a + b - 1) / b); }
+
+// Tiles that tokens [from, to) lie in.
+__host__ __device__ inline int tiles_of(int from, int to, int tile) {
+  return to > from ? ceil_div(to, tile) - from / tile : 0;
+}
 
 // A run of tiles of one block, as an attention CTA takes it.
 struct Segment {
@@ -144,7 +150,7 @@ struct SegmentWalk {
       to = p.g_prefix[i];
       rows_all = p.g_size[i] * hpk;
     }
-    tiles = ceil_div(to - from, a.tile);
+    tiles = tiles_of(from, to, a.tile);
     const int nrb = ceil_div(rows_all, a.rb);
     const long long b = (u - base) / tiles;  // block: (KV head, half, row block)
     const int t = (int)(u - base - b * tiles);
@@ -157,8 +163,8 @@ struct SegmentWalk {
     s->rows = min(a.rb, rows_all - s->row0);
     const long long left = end - u;
     const int nt = (int)(left < tiles - t ? left : tiles - t);
-    s->tok0 = from + t * a.tile;
-    s->tok1 = t + nt == tiles ? to : from + (t + nt) * a.tile;
+    s->tok0 = t == 0 ? from : (from / a.tile + t) * a.tile;
+    s->tok1 = t + nt == tiles ? to : (from / a.tile + t + nt) * a.tile;
     s->carry = t > 0;
     u += nt;
     return true;

@@ -12,18 +12,22 @@
 // float32 weights, so l and the log-sum-exp carry no bf16 rounding.
 //
 // Roles: warps 0-3 and 4-7 one query row per thread (softmax, rescaling, output), warps 8-11
-// gather K and V rows through the page table (cp.async, 16 bytes each, zero-filled where a token
-// has no slot) into a ring of stages, warp 12 issues the MMAs, warps 13-15 load Q.
+// bring K and V rows through the page table into a ring of stages, warp 12 issues the MMAs, warp
+// 13 loads Q. Whole tiles of pages of 8, 16, 32 or 64 slots, or a multiple of 128, come as
+// tensor-map copies, one per page and 64 columns; tiles with tokens left out (the ends of a
+// context, pages outside the pool) and other page sizes as 16-byte cp.async, zero-filled where a
+// token has no slot, so that nothing of a row that no token holds is ever multiplied.
 //   GQA: two tiles of 128 query rows share each K and V tile; the MMAs of one run during the
 //        softmax of the other.
 //   MLA: one tile of 128 rows and half of V's columns a CTA (O takes 256 TMEM columns; all 512
 //        would leave none for S), S of the next tile issued before P V of this one.
 // Layout: every operand tile is 128 rows of 128 bytes (64 elements), swizzled in 128-byte rows;
 // V is read MN-major, so its rows land unchanged too.
-#include <mutex>
+#include <cuda.h>
 
 #include "kamera_prefix.cuh"
 #include "kamera_ptx.cuh"
+#include "kamera_smem.cuh"
 
 namespace kamera {
 
@@ -65,6 +69,15 @@ using Gqa128 = Shape<2, 2, 2, 2, 5>;
 using Gqa64 = Shape<1, 1, 2, 1, 12>;
 using Mla512 = Shape<9, 4, 1, 1, 5>;
 
+// Tensor maps of a call: pool rows of the layer (boxes of 64 columns and `box` slots) and query
+// rows (64 columns; a block of a group's rows, or one request's).
+struct Maps {
+  CUtensorMap k, v, q_group, q_own;
+  int box;                    // slots per copy; 0: rows come by cp.async
+  int q_step;                 // 1: the rows of a block are consecutive rows of q
+  int group_bytes, own_bytes; // of the query copies
+};
+
 // Wait for a phase, giving up after kWaitNs or when another thread has (then the kernel runs to
 // its end without waiting, and reports it).
 __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, volatile uint32_t *gave_up) {
@@ -91,23 +104,38 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-// Number of the first stage of K tile i and V tile i in a segment of n tiles, in the order in
-// which the MMAs read them: QT 2: K0 V0 K1 V1 ...; QT 1: K0 K1 V0 K2 V1 ... V(n-1).
-template <class S>
-__device__ __forceinline__ long long k_seq(int i) {
-  constexpr int k = S::DK / S::UC, v = S::DV / S::UC;
-  if (S::QT == 2) return (long long)i * (k + v);
-  return i == 0 ? 0 : k + (long long)(i - 1) * (k + v);
+template <int V>
+struct Int {
+  static constexpr int v = V;
+};
+
+// A place in the ring of N stages and the parity of its phase.
+template <int N>
+struct Place {
+  uint32_t st = 0, ph = 0;
+  __device__ __forceinline__ void advance(int n) {
+    st += n;
+    while (st >= (uint32_t)N) {
+      st -= N;
+      ph ^= 1;
+    }
+  }
+};
+
+// Halves of the matrix descriptors (kamera_ptx.cuh): the start address and leading offset, to
+// which the steps inside a tile are added, and the constant rest.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t addr) {
+  return (addr >> 4) | (uint32_t)(kChunk >> 4) << 16;
 }
-template <class S>
-__device__ __forceinline__ long long v_seq(int i, int n) {
-  constexpr int k = S::DK / S::UC, v = S::DV / S::UC;
-  if (S::QT == 2) return (long long)i * (k + v) + k;
-  return k + (long long)i * (k + v) + (i == n - 1 ? 0 : k);
+__device__ __forceinline__ uint64_t desc(uint32_t lo) {
+  return (uint64_t)kDescHi << 32 | lo;
 }
 
 template <class S>
-__global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constant__ PrefixArgs a) {
+__global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constant__ PrefixArgs a,
+                                                          const __grid_constant__ Maps maps) {
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t sb = ptx::smem_addr(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -130,7 +158,7 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
       ptx::mbar_init(bar(S::full + i), 128);
       ptx::mbar_init(bar(S::empty + i), 1);
     }
-    ptx::mbar_init(bar(S::q_full), 96);
+    ptx::mbar_init(bar(S::q_full), 1);
     ptx::mbar_init(bar(S::q_empty), 1);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bar(S::s_full + i), 1);
@@ -161,11 +189,11 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
     const bool flip = a.scale < 0.f;
     const float neg_inf = -__int_as_float(0x7f800000);
     const uint32_t o_t = tmem + S::o_col + (S::QT == 2 ? w * 128 : 0) + lane_off;
-    uint32_t used[2] = {0, 0};  // S buffers taken so far
+    uint32_t s_ph = 0;          // parity of each S buffer
     uint32_t tiles = 0;         // tiles of this query tile so far (phases of pv_done)
     uint32_t seen = 0;          // tiles the loader has masked so far
     while (walk.next(a, plan, &s)) {
-      const int n = (s.tok1 - s.tok0 + kTok - 1) / kTok;
+      const int n = tiles_of(s.tok0, s.tok1, kTok);
       if (S::QT == 2 ? (w == 1 && s.rows <= kRow) : w == 1) {
         seen += n;
         continue;
@@ -174,9 +202,9 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
       float m = neg_inf, l = 0.f;
       for (int i = 0; i < n; ++i, ++seen, ++tiles) {
         const int b = S::QT == 2 ? w : (i & 1);
-        wait(bar(S::s_full + b), used[b] & 1, gave_up);
+        wait(bar(S::s_full + b), (s_ph >> b) & 1, gave_up);
         __syncwarp();
-        ++used[b];
+        s_ph ^= 1u << b;
         ptx::tc_fence_after();
         if (live) {
           const uint32_t st = tmem + b * 128 + lane_off;
@@ -185,28 +213,31 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
           __syncwarp();
           const uint4 msk = *reinterpret_cast<const uint4 *>(smem + S::mask + 16 * mk);
           const bool whole = (msk.x & msk.y & msk.z & msk.w) == 0xffffffffu;
+          // pass 1: the tile's maximum, 32 columns in flight while 32 are compared
           float mx = m;
+          uint32_t r[2][32];
+          ptx::tmem_ld32(st, r[0]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            uint32_t r[32];
-            ptx::tmem_ld32(st + 32 * j, r);
+            uint32_t *x = r[j & 1];
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) ptx::tmem_ld_wait(r + e);
+            for (int e = 0; e < 32; e += 8) ptx::tmem_ld_wait(x + e);
+            if (j < 3) ptx::tmem_ld32(st + 32 * (j + 1), r[(j + 1) & 1]);
             if (!whole || flip) {
               const uint32_t bits = j == 0 ? msk.x : j == 1 ? msk.y : j == 2 ? msk.z : msk.w;
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
-                const float x = __uint_as_float(r[e]);
-                mx = (bits >> e) & 1 ? fmaxf(mx, flip ? -x : x) : mx;
+                const float y = __uint_as_float(x[e]);
+                mx = (bits >> e) & 1 ? fmaxf(mx, flip ? -y : y) : mx;
               }
             } else {
               float m0 = mx, m1 = mx, m2 = mx, m3 = mx;
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                m0 = fmaxf(m0, __uint_as_float(r[e]));
-                m1 = fmaxf(m1, __uint_as_float(r[e + 1]));
-                m2 = fmaxf(m2, __uint_as_float(r[e + 2]));
-                m3 = fmaxf(m3, __uint_as_float(r[e + 3]));
+              for (int e = 0; e < 32; e += 8) {
+                m0 = fmaxf(fmaxf(m0, __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
+                m1 = fmaxf(fmaxf(m1, __uint_as_float(x[e + 2])), __uint_as_float(x[e + 3]));
+                m2 = fmaxf(fmaxf(m2, __uint_as_float(x[e + 4])), __uint_as_float(x[e + 5]));
+                m3 = fmaxf(fmaxf(m3, __uint_as_float(x[e + 6])), __uint_as_float(x[e + 7]));
               }
               mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
             }
@@ -223,46 +254,52 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
               l *= f;
 #pragma unroll 1
               for (int j = 0; j < S::DV * 2; ++j) {
-                uint32_t r[32];
-                ptx::tmem_ld32(o_t + 32 * j, r);
+                uint32_t *y = r[1];
+                ptx::tmem_ld32(o_t + 32 * j, y);
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) ptx::tmem_ld_wait(r + e);
+                for (int e = 0; e < 32; e += 8) ptx::tmem_ld_wait(y + e);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-                ptx::tmem_st32(o_t + 32 * j, r);
+                for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+                ptx::tmem_st32(o_t + 32 * j, y);
               }
             }
           }
           const float base = m > neg_inf ? m * c : 0.f;
           const float cs = flip ? -c : c;
-          float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+          const f32x2 cs2 = f2(cs, cs), nb2 = f2(-base, -base);
+          f32x2 la = f2(0.f, 0.f), lb = la;
+          // pass 2: weights, 32 columns in flight while 32 are computed
+          ptx::tmem_ld32(st, r[0]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            uint32_t r[32];
-            ptx::tmem_ld32(st + 32 * j, r);
+            uint32_t *x = r[j & 1];
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) ptx::tmem_ld_wait(r + e);
-            float p[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) p[e] = exp2_approx(fmaf(__uint_as_float(r[e]), cs, -base));
-            if (!whole) {
-              const uint32_t bits = j == 0 ? msk.x : j == 1 ? msk.y : j == 2 ? msk.z : msk.w;
-#pragma unroll
-              for (int e = 0; e < 32; ++e) p[e] = (bits >> e) & 1 ? p[e] : 0.f;
-            }
+            for (int e = 0; e < 32; e += 8) ptx::tmem_ld_wait(x + e);
+            if (j < 3) ptx::tmem_ld32(st + 32 * (j + 1), r[(j + 1) & 1]);
+            const uint32_t bits = j == 0 ? msk.x : j == 1 ? msk.y : j == 2 ? msk.z : msk.w;
             uint32_t h[16];
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              l0 += p[e];
-              l1 += p[e + 1];
-              l2 += p[e + 2];
-              l3 += p[e + 3];
-              h[e / 2] = pack_bf16(p[e], p[e + 1]);
-              h[e / 2 + 1] = pack_bf16(p[e + 2], p[e + 3]);
+            for (int e = 0; e < 32; e += 2) {
+              float p0, p1;
+              f2_split(fma2(f2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), cs2, nb2), p0,
+                       p1);
+              p0 = exp2_approx(p0);
+              p1 = exp2_approx(p1);
+              if (!whole) {
+                p0 = (bits >> e) & 1 ? p0 : 0.f;
+                p1 = (bits >> (e + 1)) & 1 ? p1 : 0.f;
+              }
+              if (e & 2)
+                lb = add2(lb, f2(p0, p1));
+              else
+                la = add2(la, f2(p0, p1));
+              h[e / 2] = pack_bf16(p0, p1);
             }
             ptx::tmem_st16(st + 16 * j, h);
           }
-          l += (l0 + l1) + (l2 + l3);
+          float l0, l1;
+          f2_split(add2(la, lb), l0, l1);
+          l += l0 + l1;
           ptx::tmem_st_wait();
         }
         ptx::tc_fence_before();
@@ -306,176 +343,249 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
     }
   } else if (warp < 12) {
     // ---- K and V rows into the ring ----
-    const int lt = tid - 256;
+    const int lt = tid - 256;  // this thread's token of a tile
     const bool gqa = lay.kind == KAMERA_GQA;
-    const long long layer_k = (long long)a.layer * a.pool.num_slots * lay.row_k;
-    const long long layer_v = (long long)a.layer * a.pool.num_slots * lay.row_v;
+    const __nv_bfloat16 *lk = a.pool.k + (long long)a.layer * a.pool.num_slots * lay.row_k;
+    const __nv_bfloat16 *lv =
+        gqa ? a.pool.v + (long long)a.layer * a.pool.num_slots * lay.row_v : lk;
+    const int vrow = gqa ? lay.row_v : lay.row_k;
     int *slots = reinterpret_cast<int *>(smem + S::slot);
     uint32_t *masks = reinterpret_cast<uint32_t *>(smem + S::mask);
-    const int piece = lt & 7, t_lo = lt >> 3;  // 16-byte piece of a row, first token
+    const int piece = lt & 7, t_lo = lt >> 3;  // cp.async: 16-byte piece of a row, first token
+    const bool first_of_box = maps.box && lt % maps.box == 0;
     uint32_t seq = 0, tile_no = 0;             // stages and tiles so far
     while (walk.next(a, plan, &s)) {
-      const int n = (s.tok1 - s.tok0 + kTok - 1) / kTok;
-      const __nv_bfloat16 *kb = a.pool.k + layer_k + (gqa ? s.kvh * lay.hd : 0) + 8 * piece;
-      const __nv_bfloat16 *vb = gqa ? a.pool.v + layer_v + s.kvh * lay.hd + 8 * piece
-                                    : a.pool.k + layer_k + s.half * (S::DV * 64) + 8 * piece;
-      const int vrow = gqa ? lay.row_v : lay.row_k;
-      // `chunks` chunks of the tile whose slots are sl into the next stages
-      auto issue = [&](const __nv_bfloat16 *src, int row, int chunks, const int *sl) {
+      const int n = tiles_of(s.tok0, s.tok1, kTok), a0 = s.tok0 / kTok;
+      const int kcol = gqa ? s.kvh * lay.hd : 0;
+      const int vcol = gqa ? kcol : s.half * (S::DV * 64);
+      auto slot_at = [&](int i) -> int {  // of this thread's token of tile i
+        const long long tok = (long long)(a0 + i) * kTok + lt;
+        if (tok < s.tok0 || tok >= s.tok1) return -1;
+        return (int)slot_of(a.pool, lay.page_size, s.lead, tok, a.status);
+      };
+      // The next stages: `chunks` chunks from column `col` of a tile's rows. slot: this thread's
+      // token's; tile: the tile's number, for the other tokens' slots; whole: every token is in.
+      auto issue = [&](const void *map, const __nv_bfloat16 *rows, int row, int col, int chunks,
+                       int slot, uint32_t tile, bool whole) {
+        if (maps.box && whole) {
+          for (int u = 0; u < chunks / S::UC; ++u, ++seq) {
+            const int st = seq % S::NST;
+            wait(bar(S::empty + st), (seq / S::NST + 1) & 1, gave_up);
+            const uint32_t dst = sb + S::ring + st * S::kStage + lt * 128;
+            if (first_of_box) {
+              ptx::mbar_arrive_expect_tx(bar(S::full + st), S::UC * maps.box * 128);
+#pragma unroll
+              for (int k = 0; k < S::UC; ++k)
+                ptx::tma_2d(dst + k * kChunk, map, col + (u * S::UC + k) * 64, slot,
+                            bar(S::full + st));
+            } else {
+              ptx::mbar_arrive(bar(S::full + st));
+            }
+          }
+          return;
+        }
+        int sl[kTok / 16];
+#pragma unroll
+        for (int j = 0; j < kTok / 16; ++j) sl[j] = slots[(tile % kSlots) * kTok + t_lo + 16 * j];
         for (int u = 0; u < chunks / S::UC; ++u, ++seq) {
           const int st = seq % S::NST;
           wait(bar(S::empty + st), (seq / S::NST + 1) & 1, gave_up);
           const uint32_t dst = sb + S::ring + st * S::kStage;
+          const __nv_bfloat16 *src = rows + col + u * S::UC * 64 + 8 * piece;
 #pragma unroll
           for (int j = 0; j < kTok / 16; ++j) {
-            const int t = t_lo + 16 * j, slot = sl[t];
-            const __nv_bfloat16 *p = slot >= 0 ? src + (long long)slot * row + u * S::UC * 64
-                                               : a.pool.k;
+            const int t = t_lo + 16 * j;
+            const __nv_bfloat16 *p = sl[j] >= 0 ? src + (long long)sl[j] * row : a.pool.k;
 #pragma unroll
             for (int k = 0; k < S::UC; ++k)
-              ptx::cp_async16(dst + k * kChunk + t * 128 + ((piece ^ (t & 7)) << 4), p + k * 64,
-                              slot >= 0 ? 16u : 0u);
+              ptx::cp_async16(dst + k * kChunk + t * 128 + ((piece ^ (t & 7)) << 4),
+                              sl[j] >= 0 ? p + k * 64 : p, sl[j] >= 0 ? 16u : 0u);
           }
           ptx::cp_async_mbar_arrive(bar(S::full + st));
         }
       };
+      int slot = slot_at(0), slot_k = 0, slot_v = 0;  // of the next tile, of K's and of V's
+      bool whole_k = false, whole_v = false;
+      uint32_t tile_k = 0, tile_v = 0;
       auto load_k = [&](int i) {
-        const long long tok = s.tok0 + (long long)i * kTok + lt;
-        int slot = -1;
-        if (tok < s.tok1) slot = (int)slot_of(a.pool, lay.page_size, s.lead, tok, a.status);
-        const int k = tile_no % kSlots, mk = tile_no % kMasks;
-        ++tile_no;
-        slots[k * kTok + lt] = slot;
-        const uint32_t bits = __ballot_sync(0xffffffffu, slot >= 0);
+        slot_k = slot;
+        tile_k = tile_no++;
+        if (i + 1 < n) slot = slot_at(i + 1);  // ahead of its use
+        slots[(tile_k % kSlots) * kTok + lt] = slot_k;
+        const uint32_t bits = __ballot_sync(0xffffffffu, slot_k >= 0);
+        const int mk = tile_k % kMasks;
         if (lane == 0) {
           masks[4 * mk + (warp & 3)] = bits;
           ptx::mbar_arrive(bar(S::mk_full + mk));
         }
         __syncwarp();
         asm volatile("bar.sync 1, 128;" ::: "memory");
-        issue(kb, lay.row_k, S::DK, slots + k * kTok);
+        const uint4 m = *reinterpret_cast<const uint4 *>(masks + 4 * mk);
+        whole_k = (m.x & m.y & m.z & m.w) == 0xffffffffu;
+        issue(&maps.k, lk, lay.row_k, kcol, S::DK, slot_k, tile_k, whole_k);
       };
-      const uint32_t t0 = tile_no;
-      auto load_v = [&](int i) {
-        issue(vb, vrow, S::DV, slots + ((t0 + i) % kSlots) * kTok);
+      auto keep = [&]() {  // V of this tile comes later
+        slot_v = slot_k;
+        tile_v = tile_k;
+        whole_v = whole_k;
+      };
+      auto load_v = [&](int sv, uint32_t tv, bool wv) {
+        issue(&maps.v, lv, vrow, vcol, S::DV, sv, tv, wv);
       };
       load_k(0);
       for (int i = 0; i < n; ++i) {
+        keep();
         if (S::QT == 1 && i + 1 < n) load_k(i + 1);
-        load_v(i);
+        load_v(slot_v, tile_v, whole_v);
         if (S::QT == 2 && i + 1 < n) load_k(i + 1);
       }
     }
     ptx::cp_async_wait_all();
   } else if (warp == 12) {
-    // ---- MMAs, one thread ----
+    // ---- MMAs, one thread. Issuing one takes a few instructions only: the descriptors of a
+    // tile's steps differ by constants ----
     if (lane == 0) {
-      const uint32_t id_s = ptx::idesc_bf16_f32(kRow, kTok);
-      const uint32_t id_o = ptx::idesc_bf16_f32(kRow, S::UC * 64) | (1u << 16);  // V MN-major
-      uint32_t base = 0;                 // stages of earlier segments
-      uint32_t segs = 0, p_used[2] = {0, 0}, o_used[2] = {0, 0};
-      while (walk.next(a, plan, &s)) {
-        const int n = (s.tok1 - s.tok0 + kTok - 1) / kTok;
-        const int qt = S::QT == 2 ? (s.rows > kRow ? 2 : 1) : 1;
-        // S of query tile t (TMEM buffer b) against K tile i; `first`: the stages' first reader
-        auto mma_s = [&](int t, int b, int i, bool first, bool last) {
-          const uint32_t q = sb + S::q + t * S::DK * kChunk;
-          for (int u = 0; u < S::DK / S::UC; ++u) {
-            const uint32_t seq = base + (uint32_t)k_seq<S>(i) + u, st = seq % S::NST;
-            if (first) {
-              wait(bar(S::full + st), (seq / S::NST) & 1, gave_up);
-              ptx::fence_proxy_async_smem();
-            }
-            const uint32_t k = sb + S::ring + st * S::kStage;
+      constexpr uint32_t id_s = 1u << 4 | 1u << 7 | 1u << 10 | (kTok >> 3) << 17 | (kRow >> 4) << 24;
+      // V is MN-major
+      constexpr uint32_t id_o =
+          1u << 4 | 1u << 7 | 1u << 10 | 1u << 16 | (S::UC * 64 >> 3) << 17 | (kRow >> 4) << 24;
+      constexpr int ku = S::DK / S::UC, vu = S::DV / S::UC;  // stages of a K and a V tile
+      const uint32_t ring = sb + S::ring;
+      Place<S::NST> kp, vp;
+      uint32_t q_ph = 0, p_ph = 0, o_ph = 0, o_any = 0;  // a bit for each S buffer, query tile
+      const uint32_t q0 = desc_k(sb + S::q);             // [chunk][query tile][128 rows]
+      // S of query tile t into TMEM buffer b against the K tile at kp; Ends: bit 0 the first,
+      // bit 1 the last reader of its stages
+      auto mma_s = [&](auto t, uint32_t b, auto ends) {
+        const uint32_t d = tmem + b * 128;
+        Place<S::NST> at = kp;
 #pragma unroll
-            for (int x = 0; x < S::UC * 4; ++x) {
-              const uint32_t off = (x >> 2) * kChunk + (x & 3) * 32;
-              ptx::mma_bf16(tmem + b * 128, ptx::smem_desc_sw128(q + u * S::UC * kChunk + off),
-                            ptx::smem_desc_sw128(k + off), id_s, (u | x) ? 1u : 0u);
-            }
-            if (last) ptx::mma_commit(bar(S::empty + st));
+        for (int u = 0; u < ku; ++u) {
+          if (ends.v & 1) {
+            wait(bar(S::full) + 8 * at.st, at.ph, gave_up);
+            ptx::fence_proxy_async_smem();
           }
-          ptx::mma_commit(bar(S::s_full + b));
-        };
-        auto mma_o = [&](int t, int b, int i, bool first, bool last) {
-          wait(bar(S::p_full + b), p_used[b] & 1, gave_up);
-          ++p_used[b];
-          if (i == 0) {  // the last segment's output has been read
-            if (o_used[t]) wait(bar(S::o_free + t), (o_used[t] - 1) & 1, gave_up);
-            ++o_used[t];
-          }
-          ptx::tc_fence_after();
-          for (int u = 0; u < S::DV / S::UC; ++u) {
-            const uint32_t seq = base + (uint32_t)v_seq<S>(i, n) + u, st = seq % S::NST;
-            if (first) {
-              wait(bar(S::full + st), (seq / S::NST) & 1, gave_up);
-              ptx::fence_proxy_async_smem();
-            }
-            const uint32_t v = sb + S::ring + st * S::kStage;
+          const uint32_t k = desc_k(ring + at.st * S::kStage);
 #pragma unroll
-            for (int x = 0; x < kTok / 16; ++x)
-              ptx::mma_bf16_ta(tmem + S::o_col + t * 128 + u * S::UC * 64, tmem + b * 128 + 8 * x,
-                               ptx::smem_desc_sw128_mn(v + x * 2048, kChunk), id_o,
-                               (i | x) ? 1u : 0u);
-            if (last) ptx::mma_commit(bar(S::empty + st));
-          }
-          ptx::mma_commit(bar(S::pv_done + t));
-        };
-        wait(bar(S::q_full), segs & 1, gave_up);
-        ++segs;
-        ptx::fence_proxy_async_smem();
-        ptx::tc_fence_after();
-        if (S::QT == 2) {
-          for (int t = 0; t < qt; ++t) mma_s(t, t, 0, t == 0, t == qt - 1);
-          if (n == 1) ptx::mma_commit(bar(S::q_empty));
-          for (int i = 0; i < n; ++i)
-            for (int t = 0; t < qt; ++t) {
-              mma_o(t, t, i, t == 0, t == qt - 1);
-              if (i + 1 < n) {
-                mma_s(t, t, i + 1, t == 0, t == qt - 1);
-                if (i + 2 == n && t == qt - 1) ptx::mma_commit(bar(S::q_empty));
-              }
-            }
-        } else {
-          mma_s(0, 0, 0, true, true);
-          if (n == 1) ptx::mma_commit(bar(S::q_empty));
-          for (int i = 0; i < n; ++i) {
-            if (i + 1 < n) {
-              mma_s(0, (i + 1) & 1, i + 1, true, true);
-              if (i + 2 == n) ptx::mma_commit(bar(S::q_empty));
-            }
-            mma_o(0, i & 1, i, true, true);
-          }
+          for (int x = 0; x < S::UC * 4; ++x)
+            ptx::mma_bf16(d,
+                          desc(q0 + ((((u * S::UC + (x >> 2)) * S::QT + t.v) * kChunk +
+                                      (x & 3) * 32) >> 4)),
+                          desc(k + (((x >> 2) * kChunk + (x & 3) * 32) >> 4)), id_s,
+                          (u | x) ? 1u : 0u);
+          if (ends.v & 2) ptx::mma_commit(bar(S::empty) + 8 * at.st);
+          at.advance(1);
         }
-        base += n * ((S::DK + S::DV) / S::UC);
+        ptx::mma_commit(bar(S::s_full) + 8 * b);
+        if (ends.v & 2) kp = at;
+      };
+      // O of query tile t (+)= P in buffer b times the V tile at vp
+      auto mma_o = [&](auto t, uint32_t b, bool first_tile, auto ends) {
+        const uint32_t p = tmem + b * 128, d = tmem + S::o_col + t.v * 128;
+        Place<S::NST> at = vp;
+        if (ends.v & 1) {  // V is there long before P
+          wait(bar(S::full) + 8 * at.st, at.ph, gave_up);
+          ptx::fence_proxy_async_smem();
+        }
+        if (first_tile) {  // the last segment's output has been read
+          if ((o_any >> t.v) & 1) {
+            wait(bar(S::o_free + t.v), (o_ph >> t.v) & 1, gave_up);
+            o_ph ^= 1u << t.v;
+          }
+          o_any |= 1u << t.v;
+        }
+        wait(bar(S::p_full) + 8 * b, (p_ph >> b) & 1, gave_up);
+        p_ph ^= 1u << b;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int u = 0; u < vu; ++u) {
+          if ((ends.v & 1) && u > 0) {
+            wait(bar(S::full) + 8 * at.st, at.ph, gave_up);
+            ptx::fence_proxy_async_smem();
+          }
+          const uint32_t v = desc_mn(ring + at.st * S::kStage);
+#pragma unroll
+          for (int x = 0; x < kTok / 16; ++x)
+            ptx::mma_bf16_ta(d + u * S::UC * 64, p + 8 * x, desc(v + x * (2048 >> 4)), id_o,
+                             x ? 1u : (first_tile ? 0u : 1u));
+          if (ends.v & 2) ptx::mma_commit(bar(S::empty) + 8 * at.st);
+          at.advance(1);
+        }
+        ptx::mma_commit(bar(S::pv_done + t.v));
+        if (ends.v & 2) vp = at;
+      };
+      constexpr Int<0> t0;
+      constexpr Int<1> t1, first;
+      constexpr Int<2> last;
+      constexpr Int<3> only;
+      while (walk.next(a, plan, &s)) {
+        const int n = tiles_of(s.tok0, s.tok1, kTok);
+        // the stages come in the order in which they are read:
+        // QT 2: K0 V0 K1 V1 ...; QT 1: K0 K1 V0 K2 V1 ... V(n-1)
+        vp = kp;
+        vp.advance(S::QT == 1 && n > 1 ? 2 * ku : ku);
+        wait(bar(S::q_full), q_ph, gave_up);
+        q_ph ^= 1;
+        ptx::fence_proxy_async_smem();
+        if (S::QT == 2 && s.rows > kRow) {
+          mma_s(t0, 0, first);
+          mma_s(t1, 1, last);
+          for (int i = 0; i + 1 < n; ++i) {
+            kp.advance(vu);
+            mma_o(t0, 0, i == 0, first);
+            mma_s(t0, 0, first);
+            mma_o(t1, 1, i == 0, last);
+            mma_s(t1, 1, last);
+            vp.advance(ku);
+          }
+          ptx::mma_commit(bar(S::q_empty));
+          mma_o(t0, 0, n == 1, first);
+          mma_o(t1, 1, n == 1, last);
+        } else if (S::QT == 2) {
+          mma_s(t0, 0, only);
+          for (int i = 0; i + 1 < n; ++i) {
+            kp.advance(vu);
+            mma_o(t0, 0, i == 0, only);
+            mma_s(t0, 0, only);
+            vp.advance(ku);
+          }
+          ptx::mma_commit(bar(S::q_empty));
+          mma_o(t0, 0, n == 1, only);
+        } else {
+          mma_s(t0, 0, only);
+          for (int i = 0; i + 1 < n; ++i) {
+            if (i > 0) kp.advance(vu);
+            mma_s(t0, (i + 1) & 1, only);
+            mma_o(t0, i & 1, i == 0, only);
+            if (i + 2 < n) vp.advance(ku);
+          }
+          ptx::mma_commit(bar(S::q_empty));
+          mma_o(t0, (n - 1) & 1, n == 1, only);
+        }
+        kp = vp;  // the segment's end
       }
       ptx::mma_commit(bar(S::last));  // no MMA is in flight when the TMEM goes back
       if (!ptx::mbar_wait(bar(S::last), 0, kWaitNs)) *gave_up = 1;
     }
     __syncwarp();
-  } else {
-    // ---- Q ----
-    const int lt = tid - 13 * 32;
-    uint32_t segs = 0;
-    while (walk.next(a, plan, &s)) {
-      if (segs) wait(bar(S::q_empty), (segs - 1) & 1, gave_up);
-      ++segs;
-      const int rows = s.rows > kRow ? 2 * kRow : kRow;
-      for (int e = lt; e < rows * S::DK * 8; e += 96) {
-        const int piece = e & 7, x = e >> 3, ch = x % S::DK, i = x / S::DK;
-        const uint32_t dst = sb + S::q + ((i >> 7) * S::DK + ch) * kChunk + (i & 127) * 128 +
-                             ((piece ^ (i & 7)) << 4);
-        const __nv_bfloat16 *src = a.q;
-        if (i < s.rows) {
-          int r, h;
-          segment_row(a, s, i, &r, &h);
-          src += ((long long)r * a.hq + h) * a.dk + ch * 64 + piece * 8;
-        }
-        ptx::cp_async16(dst, src, i < s.rows ? 16u : 0u);
+  } else if (warp == 13) {
+    // ---- Q, one thread. Rows of a copy past the block's are other requests' or zero: their
+    // results go nowhere ----
+    if (lane == 0) {
+      const int hpk = a.hq / a.n_kv;
+      uint32_t segs = 0;
+      while (walk.next(a, plan, &s)) {
+        if (segs) wait(bar(S::q_empty), (segs - 1) & 1, gave_up);
+        ++segs;
+        ptx::mbar_arrive_expect_tx(bar(S::q_full), s.own ? maps.own_bytes : maps.group_bytes);
+        const int y = maps.q_step ? 0 : s.kvh * hpk;
+        const int z = maps.q_step ? s.r0 * a.hq + s.row0 : s.r0 + s.row0 / hpk;
+        for (int c = 0; c < S::DK; ++c)
+          ptx::tma_3d(sb + S::q + c * S::QT * kChunk, s.own ? &maps.q_own : &maps.q_group, c * 64,
+                      y, z, bar(S::q_full));
       }
-      ptx::cp_async_mbar_arrive(bar(S::q_full));
     }
-    ptx::cp_async_wait_all();
+    __syncwarp();
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -489,9 +599,66 @@ cudaError_t configure() {
                               S::total);
 }
 
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                             const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                             const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+// bf16 [n2][n1][n0] (row strides in elements), boxes of 64 x b1 x b2, 128-byte swizzle.
+bool encode(CUtensorMap *m, const void *base, int rank, uint64_t n0, uint64_t n1, uint64_t n2,
+            uint64_t s1, uint64_t s2, uint32_t b1, uint32_t b2) {
+  const cuuint64_t dims[3] = {n0, n1, n2}, strides[2] = {2 * s1, 2 * s2};
+  const cuuint32_t box[3] = {64, b1, b2}, step[3] = {1, 1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims,
+                     strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <class S>
 cudaError_t launch(const PrefixArgs &a, cudaStream_t s) {
-  prefix_tc_kernel<S><<<a.n_ctas, kThr, S::total, s>>>(a);
+  if (!encode_fn()) return cudaErrorNotSupported;
+  Maps m;
+  const DevLayout &l = a.lay;
+  const int ps = l.page_size, hpk = a.hq / a.n_kv;
+  m.box = ps % kTok == 0 ? kTok : (ps >= 8 && kTok % ps == 0 ? ps : 0);
+  const uint32_t box = m.box ? m.box : 8;
+  const long long slots = a.pool.num_slots;
+  const __nv_bfloat16 *k = a.pool.k + a.layer * slots * l.row_k;
+  const __nv_bfloat16 *v = l.kind == KAMERA_GQA ? a.pool.v + a.layer * slots * l.row_v : k;
+  const int vrow = l.kind == KAMERA_GQA ? l.row_v : l.row_k;
+  bool ok = encode(&m.k, k, 2, l.row_k, slots, 1, l.row_k, 0, box, 1) &&
+            encode(&m.v, v, 2, vrow, slots, 1, vrow, 0, box, 1);
+  m.q_step = a.n_kv == 1;
+  if (m.q_step) {  // a block's rows follow one another
+    const uint64_t rows = (uint64_t)a.n_reqs * a.hq;
+    const int own = a.hq < a.rb ? a.hq : a.rb;
+    ok = ok && encode(&m.q_group, a.q, 3, a.dk, 1, rows, a.dk, a.dk, 1, a.rb) &&
+         encode(&m.q_own, a.q, 3, a.dk, 1, rows, a.dk, a.dk, 1, own);
+    m.group_bytes = S::DK * 128 * a.rb;
+    m.own_bytes = S::DK * 128 * own;
+  } else {
+    const uint64_t req = (uint64_t)a.hq * a.dk;
+    ok = ok && encode(&m.q_group, a.q, 3, a.dk, a.hq, a.n_reqs, a.dk, req, hpk, a.rb / hpk) &&
+         encode(&m.q_own, a.q, 3, a.dk, a.hq, a.n_reqs, a.dk, req, hpk, 1);
+    m.group_bytes = S::DK * 128 * a.rb;
+    m.own_bytes = S::DK * 128 * hpk;
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  prefix_tc_kernel<S><<<a.n_ctas, kThr, S::total, s>>>(a, m);
   return cudaGetLastError();
 }
 
@@ -502,9 +669,11 @@ bool prefix_tc_layout(const DevLayout &l) {
          (l.kind == KAMERA_MLA && l.latent == 512 && l.rope_d == 64);
 }
 
-void prefix_tc_shape(const DevLayout &l, int *rb, int *tile, int *vh, int *n_ctas) {
+void prefix_tc_shape(const DevLayout &l, int hq, int *rb, int *tile, int *vh, int *n_ctas) {
   const bool gqa = l.kind == KAMERA_GQA;
-  *rb = gqa ? 2 * kRow : kRow;
+  const int most = gqa ? 2 * kRow : kRow, hpk = hq / (gqa ? l.H : 1);
+  // several KV heads: whole requests, so that one copy brings a block's queries
+  *rb = gqa && l.H > 1 && hpk > 0 ? most / hpk * hpk : most;
   *tile = kTok;
   *vh = gqa ? 1 : 2;
   *n_ctas = kPrefixCtas;
