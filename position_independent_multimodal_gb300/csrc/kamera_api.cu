@@ -779,7 +779,7 @@ kamera_status kamera_prefix_attention(const kamera_handle *h, const kamera_pool 
   a.n_kv = gqa ? l.H : 1;
   a.dk = dk;
   a.dv = dv;
-  kamera::prefix_shape(l, num_q_heads, &a.rb, &a.tile, &a.vh, &a.n_ctas);
+  a.shape = kamera::prefix_shape(l, num_q_heads);
   a.scale = scale;
   a.ws = d_workspace;
   a.out = static_cast<__nv_bfloat16 *>(d_out);

@@ -190,7 +190,17 @@ struct PageArgs {
   unsigned *status;
 };
 
-constexpr int kPrefixCtas = 152;  // SMs of a GB300
+constexpr int kSms = 152;  // of a GB300
+
+// How a layout's attention over shared prefixes is divided (kamera_prefix.cuh).
+struct PrefixClass {
+  int rb, tile, vh, n;  // rows of a block, tokens of a tile, column halves of V, workers
+  int least;            // units a worker takes at least
+};
+struct PrefixShape {
+  PrefixClass cls[2];   // wide, thin
+  int wide_rows;        // blocks of more rows are wide
+};
 
 struct PrefixArgs {
   DevLayout lay;
@@ -201,7 +211,7 @@ struct PrefixArgs {
   const int *prefix_len;   // [n_groups]
   const int *ctx_len;      // [n_reqs]
   int n_reqs, n_groups, hq, n_kv, dk, dv;
-  int rb, tile, vh, n_ctas;  // rows of a block, tokens of a tile, column halves of V, CTAs
+  PrefixShape shape;
   float scale;
   void *ws;
   __nv_bfloat16 *out;      // [n_reqs][hq][dv]
@@ -616,14 +626,16 @@ cudaError_t launch_extend(const PageArgs &a, cudaStream_t s);
 cudaError_t launch_free(const PageArgs &a, cudaStream_t s);
 cudaError_t launch_compact(const PageArgs &a, cudaStream_t s);
 cudaError_t launch_copy_pages(const PageArgs &a, cudaStream_t s);
-// kamera_prefix.cu
-void prefix_shape(const DevLayout &l, int hq, int *rb, int *tile, int *vh, int *n_ctas);
+PrefixShape prefix_shape(const DevLayout &l, int hq);               // kamera_prefix.cu
 size_t prefix_workspace(const DevLayout &l, long long n_reqs, int hq, int dv);
 cudaError_t launch_prefix_attention(const PrefixArgs &a, cudaStream_t s);
 bool prefix_tc_layout(const DevLayout &l);                          // kamera_prefix_tc.cu
-void prefix_tc_shape(const DevLayout &l, int hq, int *rb, int *tile, int *vh, int *n_ctas);
+PrefixClass prefix_tc_class(const DevLayout &l, int hq);
 cudaError_t prepare_prefix_tc();
 cudaError_t launch_prefix_tc(const PrefixArgs &a, cudaStream_t s);
+PrefixClass prefix_thin_class(const DevLayout &l);                  // kamera_prefix_thin.cu
+cudaError_t prepare_prefix_thin();
+cudaError_t launch_prefix_thin(const PrefixArgs &a, cudaStream_t s);
 cudaError_t launch_rope_phases(const FreqQ64 &f, int npairs, const long long *deltas, int n,
                                float *out, cudaStream_t s);
 

@@ -5,9 +5,10 @@
 // softmaxes weighted by their masses, o = sum_i e^(lse_i - lse) o_i, lse = log sum_i e^(lse_i).
 //
 // prefix_plan_kernel lists the groups and requests with tokens and numbers their units
-// (kamera_prefix.cuh), an attention kernel works the units off, prefix_merge_kernel joins the
-// parts. This file has the attention kernel for any layout (CUDA cores); the layouts with
-// tensor-core tiles take the kernel of kamera_prefix_tc.cu.
+// (kamera_prefix.cuh), the attention kernels work the units off, prefix_merge_kernel joins the
+// parts. This file has the attention kernel for any layout (CUDA cores); GQA with head_dim 64 or
+// 128 and MLA with 512 + 64 take those of kamera_prefix_tc.cu (wide blocks) and
+// kamera_prefix_thin.cu.
 #include <mutex>
 
 #include "kamera_prefix.cuh"
@@ -18,38 +19,61 @@ namespace kamera {
 namespace {
 
 constexpr int kPlanThr = 1024;
+constexpr int kPlanNear = 1024;  // groups and listed entries kept in shared memory
 
-// Inclusive scan over the CTA's threads; every thread also gets the total.
-__device__ __forceinline__ long long plan_scan(long long x, long long *total) {
-  __shared__ long long part[kPlanThr / 32];
+// Inclusive scans of N values at a time over the CTA's threads, in place; total: their sums.
+template <int N>
+__device__ __forceinline__ void plan_scan(long long (&x)[N], long long (&total)[N]) {
+  __shared__ long long part[N][kPlanThr / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+  for (int k = 0; k < N; ++k)
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x[k], o);
+      if (lane >= o) x[k] += y;
+    }
+  __syncthreads();  // earlier readers of part are done
+  if (lane == 31)
+#pragma unroll
+    for (int k = 0; k < N; ++k) part[k][warp] = x[k];
+  __syncthreads();
+  if (warp < N) {  // warp k scans the warps' sums of value k
+    long long y = part[warp][lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
+    }
+    part[warp][lane] = y;
   }
   __syncthreads();
-  if (lane == 31) part[warp] = x;
-  __syncthreads();
-  long long before = 0, sum = 0;
-  for (int w = 0; w < kPlanThr / 32; ++w) {
-    if (w < warp) before += part[w];
-    sum += part[w];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    if (warp > 0) x[k] += part[k][warp - 1];
+    total[k] = part[k][kPlanThr / 32 - 1];
   }
-  *total = sum;
-  return x + before;
 }
 
+// One CTA: checks the arguments, lists the groups and requests that have units, and finds each
+// worker's first block. Bound: the latency of its few dependent steps.
 __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_constant__ PrefixArgs a) {
-  const PrefixPlan p = prefix_plan(a.ws, a.n_reqs, a.hq, a.dv, a.vh, a.rb, a.n_ctas);
+  const PrefixPlan p = prefix_plan(a.shape, a.ws, a.n_reqs, a.hq, a.dv);
+  __shared__ int near_start[kPlanNear + 1], near_lead[kPlanNear];
+  __shared__ long long near_u0[2][kPlanNear], near_r[kPlanNear];
   __shared__ int broken;
   const int tid = threadIdx.x, R = a.n_reqs, G = a.n_groups;
-  const int hpk = a.hq / a.n_kv, blocks = a.n_kv * a.vh;
+  const int hpk = a.hq / a.n_kv, own_cls = class_of(a.shape, hpk);
   const long long cap = (long long)a.pool.pt_stride * a.lay.page_size;
+  const bool near_g = G <= kPlanNear;
+  const int *start = near_g ? near_start : a.group_start;
+  int *lead = near_g ? near_lead : p.lead;
   if (tid == 0) broken = 0;
   __syncthreads();
   for (int g = tid; g <= G; g += kPlanThr) {
     const int s = a.group_start[g];
+    if (near_g) near_start[g] = s;
+    if (g < G) lead[g] = 0x7FFFFFFF;
     if (s < 0 || s > R || (g == 0 && s != 0) || (g == G && s != R) ||
         (g > 0 && a.group_start[g - 1] > s))
       broken = 1;
@@ -57,96 +81,133 @@ __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_cons
   __syncthreads();
   if (broken) {  // the groups do not partition the requests: nothing is written
     for (int r = tid; r < R; r += kPlanThr) p.req_state[r] = 0;
-    if (tid < 8) p.head[tid] = 0;
+    if (tid < 16) p.head[tid] = 0;
     if (tid == 0) atomicOr(a.status, KAMERA_DEVICE_BAD_ITEM);
     return;
   }
-  // requests: their group, whether they keep its rules, their tiles
-  for (int g = tid; g < G; g += kPlanThr) p.lead[g] = 0x7FFFFFFF;
-  __syncthreads();
+  // requests: their group, whether they keep its rules
   for (int r = tid; r < R; r += kPlanThr) {
+    const int ctx = a.ctx_len[r];
     int lo = 0, hi = G - 1;  // the last group that starts at or before r (empty ones come first)
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (a.group_start[mid] <= r)
+      if (start[mid] <= r)
         lo = mid;
       else
         hi = mid - 1;
     }
-    const int s0 = a.group_start[lo], prefix = a.prefix_len[lo], ctx = a.ctx_len[r];
+    const int s0 = start[lo], prefix = a.prefix_len[lo];
     const bool wrong =
         prefix < 0 || prefix > cap || ctx < 0 || ctx > cap || (ctx > 0 && ctx < prefix);
     if (wrong) atomicOr(a.status, KAMERA_DEVICE_BAD_ITEM);
     const bool active = !wrong && ctx > 0;
-    if (active) atomicMin(p.lead + lo, r);
+    if (active) atomicMin(lead + lo, r);
     p.req_state[r] = !wrong;
     p.req_group[r] = active ? lo : -1;
     p.req_at[r] = r - s0;
-    p.req_size[r] = a.group_start[lo + 1] - s0;
-    p.req_tiles[r] = active ? ceil_div(prefix, a.tile) : 0;
-    p.req_own[r] = active ? tiles_of(prefix, ctx, a.tile) : 0;
+    p.req_size[r] = start[lo + 1] - s0;
+    p.req_prefix[r] = prefix;
   }
   __syncthreads();
-  // groups: units of each prefix
-  long long base = 0, listed = 0;
+  // groups: the blocks of each prefix. units and listed ones per class, counts packed
+  long long base[2] = {0, 0};
+  int listed[2] = {0, 0};
   for (int g0 = 0; g0 < G; g0 += kPlanThr) {
     const int g = g0 + tid;
-    int s0 = 0, n = 0, prefix = 0, lead = 0x7FFFFFFF;
+    int s0 = 0, n = 0, prefix = 0, l = 0x7FFFFFFF, c = 0;
     long long units = 0;
     if (g < G) {
-      s0 = a.group_start[g];
-      n = a.group_start[g + 1] - s0;
+      s0 = start[g];
+      n = start[g + 1] - s0;
       prefix = a.prefix_len[g];
-      lead = __ldcg(p.lead + g);
-      if (lead != 0x7FFFFFFF && prefix > 0)
-        units = (long long)blocks * ceil_div(n * hpk, a.rb) * ceil_div(prefix, a.tile);
-    }
-    long long total, count;
-    const long long at = base + plan_scan(units, &total) - units;
-    const long long k = listed + plan_scan(units > 0, &count) - (units > 0);
-    if (g < G) {
-      p.gr_u0[g] = units > 0 ? at : -1;
-      if (units > 0) {
-        p.g_u0[k] = at;
-        p.g_list[k] = s0;
-        p.g_size[k] = n;
-        p.g_prefix[k] = prefix;
-        p.g_lead[k] = lead;
+      l = near_g ? near_lead[g] : __ldcg(p.lead + g);
+      if (l != 0x7FFFFFFF && prefix > 0) {
+        c = class_of(a.shape, n * hpk);
+        const PrefixClass &k = a.shape.cls[c];
+        units = (long long)a.n_kv * k.vh * ceil_div(n * hpk, k.rb) * ceil_div(prefix, k.tile);
       }
     }
-    base += total;
-    listed += count;
+    const long long one = units > 0 ? 1ll << (32 * c) : 0;
+    long long x[3] = {c == 0 ? units : 0, c == 1 ? units : 0, one}, total[3];
+    plan_scan(x, total);
+    if (g < G) {
+      const long long at = base[c] + x[c] - units;
+      if (units > 0) {
+        const int k = listed[c] + (int)((x[2] - one) >> (32 * c));
+        p.cls[c].g_u0[k] = at;
+        if (k < kPlanNear) near_u0[c][k] = at;
+        p.cls[c].g_first[k] = s0;
+        p.cls[c].g_size[k] = n;
+        p.cls[c].g_prefix[k] = prefix;
+        p.cls[c].g_lead[k] = l;
+      }
+      p.gr_u0[g] = units > 0 ? at : -1;
+    }
+    for (int k = 0; k < 2; ++k) {
+      base[k] += total[k];
+      listed[k] += (int)(total[2] >> (32 * k));
+    }
   }
   __syncthreads();
-  const long long prefix_units = base, groups = listed;
-  // requests: units of their own tokens
-  listed = 0;
+  // requests: the blocks of their own tokens
+  const long long prefix_units[2] = {base[0], base[1]};
+  const PrefixClass &ok = a.shape.cls[own_cls];
+  const int blocks = a.n_kv * ok.vh * ceil_div(hpk, ok.rb);
+  int own_listed = 0;
   for (int r0 = 0; r0 < R; r0 += kPlanThr) {
     const int r = r0 + tid;
-    const int tiles = r < R ? p.req_own[r] : 0, g = r < R ? p.req_group[r] : -1;
-    const long long units = (long long)blocks * ceil_div(hpk, a.rb) * tiles;
-    long long total, count;
-    const long long at = base + plan_scan(units, &total) - units;
-    const long long k = listed + plan_scan(units > 0, &count) - (units > 0);
+    const int g = r < R ? p.req_group[r] : -1;
+    const int prefix = g >= 0 ? p.req_prefix[r] : 0, ctx = g >= 0 ? a.ctx_len[r] : 0;
+    const long long units = (long long)blocks * tiles_of(prefix, ctx, ok.tile);
+    long long x[2] = {units, units > 0}, total[2];
+    plan_scan(x, total);
     if (r < R) {
+      const long long at = base[own_cls] + x[0] - units;
       p.req_pu0[r] = g >= 0 ? p.gr_u0[g] : -1;
       p.req_ou0[r] = units > 0 ? at : -1;
       if (units > 0) {
+        const int k = own_listed + (int)x[1] - 1;
         p.r_u0[k] = at;
+        if (k < kPlanNear) near_r[k] = at;
         p.r_list[k] = r;
-        p.r_from[k] = a.prefix_len[g];
-        p.r_to[k] = a.ctx_len[r];
+        p.r_from[k] = prefix;
+        p.r_to[k] = ctx;
       }
     }
-    base += total;
-    listed += count;
+    base[own_cls] += total[0];
+    own_listed += (int)total[1];
   }
-  if (tid == 0) {
-    p.head[0] = base;
-    p.head[1] = groups;
-    p.head[2] = listed;
-    p.head[3] = base < a.n_ctas ? base : a.n_ctas;
-    p.head[4] = prefix_units;
+  __syncthreads();
+  // workers: with fewer units than would give each `least`, fewer have any
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const PrefixClass &k = a.shape.cls[c];
+    const long long U = base[c], few = (U + k.least - 1) / k.least;
+    const int n = (int)(few < k.n ? few : k.n);
+    for (int w = tid; w < n; w += kPlanThr) {
+      const long long u = U * w / n;
+      const bool own = u >= prefix_units[c];
+      const int count = own ? own_listed : listed[c];
+      const long long *u0 = count <= kPlanNear ? (own ? near_r : near_u0[c])
+                                               : (own ? p.r_u0 : p.cls[c].g_u0);
+      int lo = 0, hi = count - 1;  // the last listed one that starts at or before u
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (u0[mid] <= u)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      p.cls[c].start[w] = lo;
+    }
+    if (tid == 0) {
+      long long *head = p.head + 8 * c;
+      head[0] = U;
+      head[1] = listed[c];
+      head[2] = c == own_cls ? own_listed : 0;
+      head[3] = n;
+      head[4] = prefix_units[c];
+    }
   }
 }
 
@@ -194,7 +255,7 @@ __host__ __device__ inline GenPlan gen_plan(int dk, int dv) {
 __global__ void __launch_bounds__(kThr) prefix_gen_kernel(const __grid_constant__ PrefixArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   const GenPlan P = gen_plan(a.dk, a.dv);
-  const PrefixPlan plan = prefix_plan(a.ws, a.n_reqs, a.hq, a.dv, a.vh, a.rb, a.n_ctas);
+  const PrefixPlan plan = prefix_plan(a.shape, a.ws, a.n_reqs, a.hq, a.dv);
   f32x2 *qs = reinterpret_cast<f32x2 *>(smem + P.q);
   float *ps = reinterpret_cast<float *>(smem + P.p);
   long long *slots = reinterpret_cast<long long *>(smem + P.slot);
@@ -208,7 +269,7 @@ __global__ void __launch_bounds__(kThr) prefix_gen_kernel(const __grid_constant_
   const int chunks = dv >> 3, lanes = kThr / chunks;
   const int c = tid % chunks, tl = tid / chunks;
   const bool gqa = lay.kind == KAMERA_GQA;
-  SegmentWalk walk;
+  SegmentWalk<1> walk;
   walk.start(a, plan, blockIdx.x);
   Segment s;
   while (walk.next(a, plan, &s)) {
@@ -359,95 +420,137 @@ __global__ void __launch_bounds__(kThr) prefix_gen_kernel(const __grid_constant_
       float sum = 0.f;
       for (int i = 0; i < lanes; ++i) sum += red[(i * kRows + g) * dv + d];
       float *o, *lse;
-      segment_out(a, plan, s, blockIdx.x, g, &o, &lse);
+      segment_out<1>(a, plan, s, blockIdx.x, g, &o, &lse);
       o[d] = l[g] == 0.f ? 0.f : sum / l[g];
       if (d == 0) *lse = l[g] == 0.f ? neg_inf : m[g] + logf(l[g]);
     }
   }
 }
 
-// One warp per (request, query head, column half): the row's parts weighted by
-// exp(lse_i - lse), rounded to bf16 once.
-__global__ void __launch_bounds__(kThr) prefix_merge_kernel(const __grid_constant__ PrefixArgs a) {
-  const PrefixPlan p = prefix_plan(a.ws, a.n_reqs, a.hq, a.dv, a.vh, a.rb, a.n_ctas);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * (kThr / 32) + warp;
+// ---------------------------------------------------------------------------------------
+// Merge: one warp per (request, query head) and kCols columns. The parts of a row are its home
+// places and the carries of the workers that start inside its blocks: the lanes take their
+// log-sum-exps, then every lane adds up its columns of eight parts at a time. One rounding to
+// bf16. Bound: latency, then the bytes of the parts.
+// ---------------------------------------------------------------------------------------
+
+constexpr int kCols = 128;  // columns of a warp: four a lane
+
+__global__ void __launch_bounds__(kThr) prefix_merge_kernel(const __grid_constant__ PrefixArgs a,
+                                                            int slices) {
+  const PrefixPlan p = prefix_plan(a.shape, a.ws, a.n_reqs, a.hq, a.dv);
+  const int lane = threadIdx.x & 31;
+  const long long w = (long long)blockIdx.x * (kThr / 32) + (threadIdx.x >> 5);
   const long long n_rh = (long long)a.n_reqs * a.hq;
-  if (w >= n_rh * a.vh) return;
-  const long long rh = w / a.vh;
-  const int half = (int)(w - rh * a.vh);
+  if (w >= n_rh * slices) return;
+  const long long rh = w / slices;
+  const int col = (int)(w - rh * slices) * kCols;
   const int r = (int)(rh / a.hq), h = (int)(rh - (long long)r * a.hq);
   if (!p.req_state[r]) return;
-  const int hpk = a.hq / a.n_kv, kvh = h / hpk, dvh = a.dv / a.vh;
+  const int hpk = a.hq / a.n_kv, kvh = h / hpk;
   const float neg_inf = -__int_as_float(0x7f800000);
-  const long long U = p.head[0], n = p.head[3];
-  // the two blocks of the row: first unit, tiles, index of the row in its block, carries
-  int c0[2] = {0, 0}, nc[2] = {0, 0}, at[2] = {0, 0};
-  bool have[2];
-  float top = neg_inf;
+  // the row's blocks: prefix, own part. Part 0 of a block is the home place, part i > 0 the
+  // carry of worker c0 + i - 1.
+  const float *home_o[2], *home_z[2], *carry_o[2], *carry_z[2];
+  int parts[2] = {0, 0}, rb[2], dvh[2];
+#pragma unroll
   for (int b = 0; b < 2; ++b) {
     const long long base = b ? p.req_ou0[r] : p.req_pu0[r];
-    have[b] = base >= 0;
-    if (!have[b]) continue;
-    const int tiles = b ? p.req_own[r] : p.req_tiles[r];
+    if (base < 0) continue;
+    const int rows = (b ? 1 : p.req_size[r]) * hpk, prefix = p.req_prefix[r];
+    const int c = class_of(a.shape, rows);
+    const PrefixClass &k = a.shape.cls[c];
+    const int tiles = b ? tiles_of(prefix, a.ctx_len[r], k.tile) : ceil_div(prefix, k.tile);
     const int row = (b ? 0 : p.req_at[r] * hpk) + (h - kvh * hpk);
-    const int rows_all = (b ? 1 : p.req_size[r]) * hpk;
-    const int nrb = ceil_div(rows_all, a.rb), blk = row / a.rb;
-    at[b] = row - blk * a.rb;
-    const long long u0 = base + (((long long)kvh * a.vh + half) * nrb + blk) * tiles;
+    const int nrb = ceil_div(rows, k.rb), blk = row / k.rb, at = row - blk * k.rb;
+    dvh[b] = a.dv / k.vh;
+    const int half = col / dvh[b], off = col - half * dvh[b];
+    const long long U = p.head[8 * c], n = p.head[8 * c + 3];
+    const long long u0 = base + (((long long)kvh * k.vh + half) * nrb + blk) * tiles;
     const long long u1 = u0 + tiles;
-    // CTAs that start inside the block: c U / n in (u0, u1)
+    // workers that start inside the block: c U / n in (u0, u1)
     long long lo = u0 * n / U;
     while (lo * U / n <= u0) ++lo;
-    long long hi = lo;
-    while (hi < n && hi * U / n < u1) ++hi;
-    c0[b] = (int)lo;
-    nc[b] = (int)(hi - lo);
-    top = fmaxf(top, p.home_lse[((long long)b * a.vh + half) * n_rh + rh]);
-    for (int i = 0; i < nc[b]; ++i)
-      top = fmaxf(top, p.carry_lse[(long long)(c0[b] + i) * a.rb + at[b]]);
+    long long hi = u1 * n / U;
+    while (hi > lo && (hi >= n || hi * U / n >= u1)) --hi;
+    parts[b] = 1 + (lo < n && lo * U / n < u1 ? (int)(hi - lo) + 1 : 0);
+    rb[b] = k.rb;
+    home_o[b] = p.home_o + (b * n_rh + rh) * a.dv + col;
+    home_z[b] = p.home_lse + (b * 2ll + half) * n_rh + rh;
+    carry_o[b] = p.cls[c].carry_o + (lo * k.rb + at) * dvh[b] + off;
+    carry_z[b] = p.cls[c].carry_lse + lo * k.rb + at;
   }
-  float sum = 0.f;
-  float acc[32];  // columns lane, lane + 32, ...
+  const int np = parts[0] + parts[1];
+  auto block_of = [&](int i) { return i >= parts[0]; };
+  auto lse_of = [&](int i) {
+    const int b = block_of(i), k = b ? i - parts[0] : i;
+    const float *z = b ? (k ? carry_z[1] : home_z[1]) : (k ? carry_z[0] : home_z[0]);
+    return k ? z[(long long)(k - 1) * (b ? rb[1] : rb[0])] : *z;
+  };
+  float top = neg_inf;
+  for (int i = lane; i < np; i += 32) top = fmaxf(top, lse_of(i));
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const int mine = col + 4 * lane;
+  const bool in = mine < a.dv;
+  float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int i0 = 0; i0 < np; i0 += 32) {
+    // a part of no mass is left out; a NaN goes on
+    const float z = i0 + lane < np ? lse_of(i0 + lane) : neg_inf;
+    const float wt = z == neg_inf ? 0.f : exp2_approx((z - top) * kLog2e);
+    float s = wt;
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    sum += s;
+    const int m = min(32, np - i0);
+    for (int j0 = 0; j0 < m; j0 += 8) {
+      float4 v[8];
 #pragma unroll
-  for (int e = 0; e < 32; ++e) acc[e] = 0.f;
-  for (int b = 0; b < 2; ++b) {
-    if (!have[b]) continue;
-    for (int i = -1; i < nc[b]; ++i) {
-      const long long k = (long long)(c0[b] + i) * a.rb + at[b];
-      const float z = i < 0 ? p.home_lse[((long long)b * a.vh + half) * n_rh + rh] : p.carry_lse[k];
-      if (z == neg_inf) continue;  // nothing to add; a NaN goes on
-      const float wt = expf(z - top);
-      const float *o = i < 0 ? p.home_o + (b * n_rh + rh) * a.dv + half * dvh : p.carry_o + k * dvh;
-      sum += wt;
+      for (int j = 0; j < 8; ++j) {
+        const int i = i0 + j0 + j, b = block_of(i), k = b ? i - parts[0] : i;
+        const float *o = b ? (k ? carry_o[1] : home_o[1]) : (k ? carry_o[0] : home_o[0]);
+        if (k) o += (long long)(k - 1) * (b ? rb[1] * dvh[1] : rb[0] * dvh[0]);
+        v[j] = in && j0 + j < m ? *reinterpret_cast<const float4 *>(o + 4 * lane)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
 #pragma unroll
-      for (int e = 0; e < 32; ++e)
-        if (lane + 32 * e < dvh) acc[e] = fmaf(wt, o[lane + 32 * e], acc[e]);
+      for (int j = 0; j < 8; ++j) {
+        const float f = __shfl_sync(0xffffffffu, wt, (j0 + j) & 31);
+        if (j0 + j < m && f != 0.f) {
+          acc[0] = fmaf(f, v[j].x, acc[0]);
+          acc[1] = fmaf(f, v[j].y, acc[1]);
+          acc[2] = fmaf(f, v[j].z, acc[2]);
+          acc[3] = fmaf(f, v[j].w, acc[3]);
+        }
+      }
     }
   }
-  const bool empty = sum == 0.f;
-#pragma unroll
-  for (int e = 0; e < 32; ++e)
-    if (lane + 32 * e < dvh)
-      a.out[rh * a.dv + half * dvh + lane + 32 * e] =
-          __float2bfloat16_rn(empty ? 0.f : acc[e] / sum);
-  if (lane == 0 && half == 0) a.lse[rh] = empty ? neg_inf : top + logf(sum);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  if (in) {
+    uint2 v;
+    v.x = pack_bf16(acc[0] * inv, acc[1] * inv);
+    v.y = pack_bf16(acc[2] * inv, acc[3] * inv);
+    *reinterpret_cast<uint2 *>(a.out + rh * a.dv + mine) = v;
+  }
+  if (lane == 0 && col == 0) a.lse[rh] = sum == 0.f ? neg_inf : top + logf(sum);
 }
 
 }  // namespace
 
-void prefix_shape(const DevLayout &l, int hq, int *rb, int *tile, int *vh, int *n_ctas) {
-  if (prefix_tc_layout(l)) return prefix_tc_shape(l, hq, rb, tile, vh, n_ctas);
-  *rb = kRows;
-  *tile = kTile;
-  *vh = 1;
-  *n_ctas = 2 * kPrefixCtas;
+PrefixShape prefix_shape(const DevLayout &l, int hq) {
+  PrefixShape s;
+  if (prefix_tc_layout(l)) {
+    s.cls[0] = prefix_tc_class(l, hq);
+    s.cls[1] = prefix_thin_class(l);
+    s.wide_rows = 32;
+  } else {
+    s.cls[0] = {1, 128, 1, 1, 1};  // not used: no block is wide
+    s.cls[1] = {kRows, kTile, 1, 2 * kSms, 1};
+    s.wide_rows = 0x7FFFFFFF;
+  }
+  return s;
 }
 
 size_t prefix_workspace(const DevLayout &l, long long n_reqs, int hq, int dv) {
-  int rb, tile, vh, n;
-  prefix_shape(l, hq, &rb, &tile, &vh, &n);
-  return prefix_plan(nullptr, n_reqs, hq, dv, vh, rb, n).total;
+  return prefix_plan(prefix_shape(l, hq), nullptr, n_reqs, hq, dv).total;
 }
 
 cudaError_t launch_prefix_attention(const PrefixArgs &a, cudaStream_t s) {
@@ -463,6 +566,7 @@ cudaError_t launch_prefix_attention(const PrefixArgs &a, cudaStream_t s) {
       e = cudaFuncSetAttribute(prefix_gen_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                gen_plan(1024, 1024).total);
       if (e == cudaSuccess) e = prepare_prefix_tc();
+      if (e == cudaSuccess) e = prepare_prefix_thin();
       if (e != cudaSuccess) return e;
       configured[dev] = 1;
     }
@@ -470,15 +574,20 @@ cudaError_t launch_prefix_attention(const PrefixArgs &a, cudaStream_t s) {
   prefix_plan_kernel<<<1, kPlanThr, 0, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  const int hpk = a.hq / a.n_kv;
   if (prefix_tc_layout(a.lay)) {
-    e = launch_prefix_tc(a, s);
+    // blocks can be wide only where the largest group would be, thin only where one request is
+    if ((long long)a.n_reqs * hpk > a.shape.wide_rows) e = launch_prefix_tc(a, s);
+    if (e == cudaSuccess && hpk <= a.shape.wide_rows) e = launch_prefix_thin(a, s);
   } else {
-    prefix_gen_kernel<<<a.n_ctas, kThr, gen_plan(a.dk, a.dv).total, s>>>(a);
+    prefix_gen_kernel<<<a.shape.cls[1].n, kThr, gen_plan(a.dk, a.dv).total, s>>>(a);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  const long long warps = (long long)a.n_reqs * a.hq * a.vh;
-  prefix_merge_kernel<<<(unsigned)((warps + kThr / 32 - 1) / (kThr / 32)), kThr, 0, s>>>(a);
+  const int slices = (a.dv + kCols - 1) / kCols;
+  const long long warps = (long long)a.n_reqs * a.hq * slices;
+  prefix_merge_kernel<<<(unsigned)((warps + kThr / 32 - 1) / (kThr / 32)), kThr, 0, s>>>(a,
+                                                                                         slices);
   return cudaGetLastError();
 }
 

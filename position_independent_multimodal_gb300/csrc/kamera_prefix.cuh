@@ -1,15 +1,18 @@
 // Work division of attention over shared prefixes, used by its plan, attention and merge
 // kernels.
 //
-// A block is a set of query rows that read the same KV head and the same tokens: up to `rb`
-// (request, query head) rows of a group for the group's prefix, or one request's rows for the
-// tokens after it. A unit is one tile of `tile` tokens of one block; units are numbered prefix
-// blocks first (group, KV head and column half, row block, tile), then own blocks (request, ...).
-// Tiles lie at multiples of `tile` tokens, so a request's own part starts and ends inside one.
-// CTA c of n takes units [c U / n, (c + 1) U / n), so every CTA has the same number of tiles
-// whatever the lengths; a range cuts at most its first and last block. A block's first segment
-// writes its rows' partial output to the rows' home place, a segment that starts inside a block
-// to its CTA's carry place, and the merge kernel adds up a row's parts by their log-sum-exp.
+// A block is a set of query rows that read the same KV head and the same tokens: (request, query
+// head) rows of a group for the group's prefix, or one request's rows for the tokens after it.
+// Blocks come in two classes, each with an attention kernel of its own: wide ones (more rows
+// than `wide_rows`, tcgen05 tiles of 128 rows) and thin ones (few rows: the bytes of K and V
+// bound them, and a tile of 128 rows would be idle for the most part). A unit is one tile of
+// tokens (at multiples of the class's tile) of one block of at most `rb` rows. A class's units
+// are numbered prefix blocks first (group, KV head and column half, row block, tile), then own
+// blocks (request, ...), and worker c of n takes units [c U / n, (c + 1) U / n): every worker has
+// the same number of tiles whatever the lengths, and cuts at most its first and last block. A
+// block's first segment writes its rows' partial output to the rows' home place, a segment that
+// starts inside a block to its worker's carry place; the merge kernel joins a row's parts by
+// their log-sum-exp.
 #pragma once
 
 #include "kamera_dev.cuh"
@@ -18,34 +21,34 @@ namespace kamera {
 
 // What the plan kernel leaves for the others, in the workspace.
 struct PrefixPlan {
-  long long *head;      // [0] units, [1] groups with a prefix, [2] requests with own tokens,
-                        // [3] CTAs with units, [4] units of the prefixes
-  long long *g_u0;      // [R] first unit of the i-th listed group
-  long long *r_u0;      // [R] first unit of the i-th listed request
-  long long *req_pu0;   // [R] request r: first unit of its group's prefix, -1 without one
-  long long *req_ou0;   // [R] request r: first own unit, -1 without own tokens
-  int *g_list;          // [R] listed groups: first request, requests, prefix, leader
-  int *g_size, *g_prefix, *g_lead;
-  int *r_list;          // [R] listed requests
-  int *r_from;          // [R] of each listed request: first own token
-  int *r_to;            //     and the end of its context
-  long long *gr_u0;     // [R] group g: first unit of its prefix, -1 without one
-  int *lead;            // [R] group g: first request with tokens
-  int *req_state;       // [R] 0: outputs not written, 1: written
-  int *req_group;       // [R] request r: its group, -1 when it has no tokens
-  int *req_at;          // [R] request r: its place in its group
-  int *req_size;        // [R] request r: requests of its group
-  int *req_tiles;       // [R] request r: tiles of its group's prefix
-  int *req_own;         // [R] request r: tiles of its own tokens
-  float *home_lse;      // [2][vh][R][hq]
-  float *carry_lse;     // [n][rb]
-  float *home_o;        // [2][R][hq][dv]
-  float *carry_o;       // [n][rb][dv / vh]
+  // per class c at head[8 c + .]: 0 units, 1 groups listed, 2 requests listed, 3 workers with
+  // units, 4 units of the prefixes
+  long long *head;
+  struct Lists {          // blocks of a class
+    long long *g_u0;      // [R] first unit of the i-th listed group
+    int *g_first, *g_size, *g_prefix, *g_lead;  // first request, requests, prefix, leader
+    int *start;           // [n] list index of each worker's first block
+    float *carry_lse;     // [n][rb]
+    float *carry_o;       // [n][rb][dv / vh]
+  } cls[2];
+  long long *r_u0;        // [R] first own unit of the i-th listed request
+  int *r_list;            // [R] listed requests
+  int *r_from, *r_to;     // [R] of each: first own token and the end of its context
+  long long *gr_u0;       // [R] group g: first unit of its prefix, -1 without one
+  int *lead;              // [R] group g: first request with tokens
+  long long *req_pu0;     // [R] request r: first unit of its group's prefix, -1 without one
+  long long *req_ou0;     // [R] request r: first own unit, -1 without own tokens
+  int *req_state;         // [R] 0: outputs not written, 1: written
+  int *req_group;         // [R] request r: its group, -1 when it has no tokens
+  int *req_at, *req_size; // [R] request r: its place in its group, requests of the group
+  int *req_prefix;        // [R] request r: tokens of its group's prefix
+  float *home_lse;        // [2][2][R][hq]: prefix and own part, column half
+  float *home_o;          // [2][R][hq][dv]
   size_t total;
 };
 
-__host__ __device__ inline PrefixPlan prefix_plan(void *ws, long long R, int hq, int dv, int vh,
-                                                  int rb, int n) {
+__host__ __device__ inline PrefixPlan prefix_plan(const PrefixShape &sh, void *ws, long long R,
+                                                  int hq, int dv) {
   PrefixPlan p;
   unsigned char *b = static_cast<unsigned char *>(ws);
   size_t o = 0;
@@ -55,31 +58,35 @@ __host__ __device__ inline PrefixPlan prefix_plan(void *ws, long long R, int hq,
     return at;
   };
   auto i64 = [&]() { return reinterpret_cast<long long *>(take(8 * R)); };
-  auto i32 = [&]() { return reinterpret_cast<int *>(take(4 * R)); };
-  p.head = reinterpret_cast<long long *>(take(64));
-  p.g_u0 = i64();
+  auto i32 = [&](long long n) { return reinterpret_cast<int *>(take(4 * n)); };
+  auto f32 = [&](long long n) { return reinterpret_cast<float *>(take(4 * n)); };
+  p.head = reinterpret_cast<long long *>(take(128));
+  for (int c = 0; c < 2; ++c) {
+    const PrefixClass &k = sh.cls[c];
+    p.cls[c].g_u0 = i64();
+    p.cls[c].g_first = i32(R);
+    p.cls[c].g_size = i32(R);
+    p.cls[c].g_prefix = i32(R);
+    p.cls[c].g_lead = i32(R);
+    p.cls[c].start = i32(k.n);
+    p.cls[c].carry_lse = f32((long long)k.n * k.rb);
+    p.cls[c].carry_o = f32((long long)k.n * k.rb * (dv / k.vh));
+  }
   p.r_u0 = i64();
+  p.gr_u0 = i64();
   p.req_pu0 = i64();
   p.req_ou0 = i64();
-  p.gr_u0 = i64();
-  p.lead = i32();
-  p.g_list = i32();
-  p.g_size = i32();
-  p.g_prefix = i32();
-  p.g_lead = i32();
-  p.r_list = i32();
-  p.r_from = i32();
-  p.r_to = i32();
-  p.req_state = i32();
-  p.req_group = i32();
-  p.req_at = i32();
-  p.req_size = i32();
-  p.req_tiles = i32();
-  p.req_own = i32();
-  p.home_lse = reinterpret_cast<float *>(take((size_t)8 * vh * R * hq));
-  p.carry_lse = reinterpret_cast<float *>(take((size_t)4 * n * rb));
-  p.home_o = reinterpret_cast<float *>(take((size_t)8 * R * hq * dv));
-  p.carry_o = reinterpret_cast<float *>(take((size_t)4 * n * rb * (dv / vh)));
+  p.r_list = i32(R);
+  p.r_from = i32(R);
+  p.r_to = i32(R);
+  p.lead = i32(R);
+  p.req_state = i32(R);
+  p.req_group = i32(R);
+  p.req_at = i32(R);
+  p.req_size = i32(R);
+  p.req_prefix = i32(R);
+  p.home_lse = f32(4 * R * hq);
+  p.home_o = f32(2 * R * hq * dv);
   p.total = o;
   return p;
 }
@@ -91,7 +98,12 @@ __host__ __device__ inline int tiles_of(int from, int to, int tile) {
   return to > from ? ceil_div(to, tile) - from / tile : 0;
 }
 
-// A run of tiles of one block, as an attention CTA takes it.
+// The class of a block with that many rows.
+__host__ __device__ inline int class_of(const PrefixShape &sh, int rows) {
+  return rows > sh.wide_rows ? 0 : 1;
+}
+
+// A run of tiles of one block, as a worker takes it.
 struct Segment {
   int own;          // 0: a group's prefix, 1: a request's own tokens
   int r0;           // first request of the rows (own: the request)
@@ -102,71 +114,78 @@ struct Segment {
   int carry;        // 1: starts inside its block
 };
 
-// Walks the segments of units [u, end).
+// Walks the segments of a worker of class C.
+template <int C>
 struct SegmentWalk {
-  long long u, end;
-  int i;            // index in the group or request list
-  __device__ __forceinline__ void start(const PrefixArgs &a, const PrefixPlan &p, int c) {
-    const long long U = p.head[0], n = p.head[3];
-    u = end = 0;
-    i = 0;
-    if (c >= n) return;
-    // U < 2^62 / n: at most 2^31 requests' tiles
-    u = U * c / n;
-    end = U * (c + 1) / n;
-    const bool own = u >= p.head[4];
-    const long long *u0 = own ? p.r_u0 : p.g_u0;
-    int lo = 0, hi = (int)(own ? p.head[2] : p.head[1]) - 1;
-    while (lo < hi) {  // the last listed one that starts at or before u
-      const int mid = (lo + hi + 1) >> 1;
-      if (u0[mid] <= u)
-        lo = mid;
-      else
-        hi = mid - 1;
+  long long u, end;          // units left: [u, end)
+  int i, own;                // list index, which list
+  int first, size, lead, from, to;  // the listed group or request
+  int tiles, nrb;            // tiles and row blocks of each of its blocks
+  int rbk, kh, t;            // the next block (row block, KV head x half) and tile
+
+  __device__ __forceinline__ void entry(const PrefixArgs &a, const PrefixPlan &p) {
+    if (own) {
+      first = lead = p.r_list[i];
+      size = 1;
+      from = p.r_from[i];
+      to = p.r_to[i];
+    } else {
+      first = p.cls[C].g_first[i];
+      size = p.cls[C].g_size[i];
+      lead = p.cls[C].g_lead[i];
+      from = 0;
+      to = p.cls[C].g_prefix[i];
     }
-    i = lo;
+    tiles = tiles_of(from, to, a.shape.cls[C].tile);
+    nrb = ceil_div(size * (a.hq / a.n_kv), a.shape.cls[C].rb);
+    rbk = kh = t = 0;
+  }
+  __device__ __forceinline__ void start(const PrefixArgs &a, const PrefixPlan &p, int worker) {
+    const long long *head = p.head + 8 * C;
+    const long long U = head[0], n = head[3];
+    u = end = 0;
+    if (worker >= n) return;
+    u = U * worker / n;  // U < 2^49, n < 2^11
+    end = U * (worker + 1) / n;
+    own = u >= head[4];
+    i = p.cls[C].start[worker];
+    entry(a, p);
+    const long long d = u - (own ? p.r_u0 : p.cls[C].g_u0)[i];
+    const long long b = d / tiles;
+    t = (int)(d - b * tiles);
+    kh = (int)(b / nrb);
+    rbk = (int)(b - (long long)kh * nrb);
   }
   // The next segment; false when there is none.
   __device__ __forceinline__ bool next(const PrefixArgs &a, const PrefixPlan &p, Segment *s) {
     if (u >= end) return false;
-    const bool own = u >= p.head[4];
-    const int n_kv = a.n_kv, hpk = a.hq / n_kv;
-    int rows_all, tiles, from, to;
-    long long base;
-    if (own) {
-      if (u == p.head[4]) i = 0;
-      if (i + 1 < (int)p.head[2] && u >= p.r_u0[i + 1]) ++i;
-      base = p.r_u0[i];
-      s->r0 = s->lead = p.r_list[i];
-      from = p.r_from[i];
-      to = p.r_to[i];
-      rows_all = hpk;
-    } else {
-      if (i + 1 < (int)p.head[1] && u >= p.g_u0[i + 1]) ++i;
-      base = p.g_u0[i];
-      s->r0 = p.g_list[i];
-      s->lead = p.g_lead[i];
-      from = 0;
-      to = p.g_prefix[i];
-      rows_all = p.g_size[i] * hpk;
+    const PrefixClass &k = a.shape.cls[C];
+    if (kh == a.n_kv * k.vh) {  // the entry is done
+      ++i;
+      if (!own && i == (int)p.head[8 * C + 1]) {
+        own = 1;
+        i = 0;
+      }
+      entry(a, p);
     }
-    tiles = tiles_of(from, to, a.tile);
-    const int nrb = ceil_div(rows_all, a.rb);
-    const long long b = (u - base) / tiles;  // block: (KV head, half, row block)
-    const int t = (int)(u - base - b * tiles);
-    const long long kh = b / nrb;
-    const int rbk = (int)(b - kh * nrb);
     s->own = own;
-    s->kvh = (int)(kh / a.vh);
-    s->half = (int)(kh - (long long)s->kvh * a.vh);
-    s->row0 = rbk * a.rb;
-    s->rows = min(a.rb, rows_all - s->row0);
+    s->r0 = first;
+    s->lead = lead;
+    s->kvh = k.vh == 1 ? kh : kh >> 1;
+    s->half = k.vh == 1 ? 0 : kh & 1;
+    s->row0 = rbk * k.rb;
+    s->rows = min(k.rb, size * (a.hq / a.n_kv) - s->row0);
     const long long left = end - u;
-    const int nt = (int)(left < tiles - t ? left : tiles - t);
-    s->tok0 = t == 0 ? from : (from / a.tile + t) * a.tile;
-    s->tok1 = t + nt == tiles ? to : (from / a.tile + t + nt) * a.tile;
+    const int nt = (int)(left < tiles - t ? left : tiles - t), t0 = from / k.tile;
+    s->tok0 = t == 0 ? from : (t0 + t) * k.tile;
+    s->tok1 = t + nt == tiles ? to : (t0 + t + nt) * k.tile;
     s->carry = t > 0;
     u += nt;
+    t = 0;
+    if (++rbk == nrb) {
+      rbk = 0;
+      ++kh;
+    }
     return true;
   }
 };
@@ -180,22 +199,39 @@ __device__ __forceinline__ void segment_row(const PrefixArgs &a, const Segment &
   *h = s.kvh * hpk + (k - d * hpk);
 }
 
-// Where row i of the segment of CTA c goes: its output row (dv / vh columns) and its lse.
+// Where row i of the segment of a worker goes: its output row (dv / vh columns) and its lse.
+template <int C>
 __device__ __forceinline__ void segment_out(const PrefixArgs &a, const PrefixPlan &p,
-                                            const Segment &s, int c, int i, float **o,
+                                            const Segment &s, int worker, int i, float **o,
                                             float **lse) {
-  const int dvh = a.dv / a.vh;
+  const PrefixClass &c = a.shape.cls[C];
+  const int dvh = a.dv / c.vh;
   if (s.carry) {
-    const long long k = (long long)c * a.rb + i;
-    *o = p.carry_o + k * dvh;
-    *lse = p.carry_lse + k;
+    const long long k = (long long)worker * c.rb + i;
+    *o = p.cls[C].carry_o + k * dvh;
+    *lse = p.cls[C].carry_lse + k;
     return;
   }
   int r, h;
   segment_row(a, s, i, &r, &h);
   const long long rh = (long long)r * a.hq + h, n = (long long)a.n_reqs * a.hq;
   *o = p.home_o + (s.own * n + rh) * a.dv + s.half * dvh;
-  *lse = p.home_lse + ((long long)s.own * a.vh + s.half) * n + rh;
+  *lse = p.home_lse + ((long long)s.own * 2 + s.half) * n + rh;
 }
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two float32 rounded to a pair of bf16, lo in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 }  // namespace kamera

@@ -1,6 +1,6 @@
-// Attention over shared prefixes on the tensor cores: GQA with head_dim 64 or 128, MLA with a
-// latent of 512 and a rope band of 64. One persistent CTA per SM works its share of tiles off
-// (kamera_prefix.cuh); a tile is 128 tokens against a block's query rows.
+// Wide blocks of attention over shared prefixes, on the tensor cores: GQA with head_dim 64 or
+// 128, MLA with a latent of 512 and a rope band of 64. One persistent CTA per SM works its share
+// of tiles off (kamera_prefix.cuh); a tile is 128 tokens against a block's query rows.
 //
 //   S [128 rows x 128 tokens] = Q K^T           tcgen05, Q and K from shared memory
 //   P = bf16(2^(c S - c m)),  c = |scale| log2 e  one thread per row, P back into TMEM over S
@@ -40,7 +40,6 @@ constexpr int kChunk = kTok * 128;     // bytes of a 128 x 64 bf16 operand tile
 constexpr int kSlots = 4;              // tiles whose slots are kept
 constexpr int kMasks = 8;              // tiles whose token masks are kept
 constexpr unsigned long long kWaitNs = 2000000000ull;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // DK, DV: 64-column chunks of K and of the CTA's V columns; QT: tiles of query rows; UC: chunks
 // per ring stage; NST: ring stages.
@@ -92,18 +91,6 @@ __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, volatile uin
   }
 }
 
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 template <int V>
 struct Int {
   static constexpr int v = V;
@@ -139,7 +126,7 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t sb = ptx::smem_addr(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const PrefixPlan plan = prefix_plan(a.ws, a.n_reqs, a.hq, a.dv, a.vh, a.rb, a.n_ctas);
+  const PrefixPlan plan = prefix_plan(a.shape, a.ws, a.n_reqs, a.hq, a.dv);
   const DevLayout &lay = a.lay;
   volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem + S::misc);
   volatile uint32_t *gave_up = misc + 1;
@@ -176,7 +163,7 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
   ptx::tc_fence_after();
   const uint32_t tmem = misc[0];
 
-  SegmentWalk walk;
+  SegmentWalk<0> walk;
   walk.start(a, plan, blockIdx.x);
   Segment s;
 
@@ -315,7 +302,7 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
       const int i = kRow * w + row;
       if (live) {
         float *o = nullptr, *lse = nullptr;
-        if (i < s.rows) segment_out(a, plan, s, blockIdx.x, i, &o, &lse);
+        if (i < s.rows) segment_out<0>(a, plan, s, blockIdx.x, i, &o, &lse);
         const bool ok = l != 0.f && !*gave_up;
         const float inv = 1.f / l;
 #pragma unroll 1
@@ -633,7 +620,7 @@ cudaError_t launch(const PrefixArgs &a, cudaStream_t s) {
   if (!encode_fn()) return cudaErrorNotSupported;
   Maps m;
   const DevLayout &l = a.lay;
-  const int ps = l.page_size, hpk = a.hq / a.n_kv;
+  const int ps = l.page_size, hpk = a.hq / a.n_kv, rb = a.shape.cls[0].rb;
   m.box = ps % kTok == 0 ? kTok : (ps >= 8 && kTok % ps == 0 ? ps : 0);
   const uint32_t box = m.box ? m.box : 8;
   const long long slots = a.pool.num_slots;
@@ -645,20 +632,20 @@ cudaError_t launch(const PrefixArgs &a, cudaStream_t s) {
   m.q_step = a.n_kv == 1;
   if (m.q_step) {  // a block's rows follow one another
     const uint64_t rows = (uint64_t)a.n_reqs * a.hq;
-    const int own = a.hq < a.rb ? a.hq : a.rb;
-    ok = ok && encode(&m.q_group, a.q, 3, a.dk, 1, rows, a.dk, a.dk, 1, a.rb) &&
+    const int own = a.hq < rb ? a.hq : rb;
+    ok = ok && encode(&m.q_group, a.q, 3, a.dk, 1, rows, a.dk, a.dk, 1, rb) &&
          encode(&m.q_own, a.q, 3, a.dk, 1, rows, a.dk, a.dk, 1, own);
-    m.group_bytes = S::DK * 128 * a.rb;
+    m.group_bytes = S::DK * 128 * rb;
     m.own_bytes = S::DK * 128 * own;
   } else {
     const uint64_t req = (uint64_t)a.hq * a.dk;
-    ok = ok && encode(&m.q_group, a.q, 3, a.dk, a.hq, a.n_reqs, a.dk, req, hpk, a.rb / hpk) &&
+    ok = ok && encode(&m.q_group, a.q, 3, a.dk, a.hq, a.n_reqs, a.dk, req, hpk, rb / hpk) &&
          encode(&m.q_own, a.q, 3, a.dk, a.hq, a.n_reqs, a.dk, req, hpk, 1);
-    m.group_bytes = S::DK * 128 * a.rb;
+    m.group_bytes = S::DK * 128 * rb;
     m.own_bytes = S::DK * 128 * hpk;
   }
   if (!ok) return cudaErrorInvalidValue;
-  prefix_tc_kernel<S><<<a.n_ctas, kThr, S::total, s>>>(a, m);
+  prefix_tc_kernel<S><<<a.shape.cls[0].n, kThr, S::total, s>>>(a, m);
   return cudaGetLastError();
 }
 
@@ -669,14 +656,17 @@ bool prefix_tc_layout(const DevLayout &l) {
          (l.kind == KAMERA_MLA && l.latent == 512 && l.rope_d == 64);
 }
 
-void prefix_tc_shape(const DevLayout &l, int hq, int *rb, int *tile, int *vh, int *n_ctas) {
+PrefixClass prefix_tc_class(const DevLayout &l, int hq) {
   const bool gqa = l.kind == KAMERA_GQA;
   const int most = gqa ? 2 * kRow : kRow, hpk = hq / (gqa ? l.H : 1);
+  PrefixClass c;
   // several KV heads: whole requests, so that one copy brings a block's queries
-  *rb = gqa && l.H > 1 && hpk > 0 ? most / hpk * hpk : most;
-  *tile = kTok;
-  *vh = gqa ? 1 : 2;
-  *n_ctas = kPrefixCtas;
+  c.rb = gqa && l.H > 1 && hpk > 0 ? most / hpk * hpk : most;
+  c.tile = kTok;
+  c.vh = gqa ? 1 : 2;
+  c.n = kSms;
+  c.least = 1;
+  return c;
 }
 
 cudaError_t prepare_prefix_tc() {
