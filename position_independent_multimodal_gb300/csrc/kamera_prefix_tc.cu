@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
   } else if (warp == 12) {
     // ---- MMAs, one thread. Issuing one takes a few instructions only: the descriptors of a
     // tile's steps differ by constants ----
-    if (lane == 0) {
+    if (ptx::elect_one()) {
       constexpr uint32_t id_s = 1u << 4 | 1u << 7 | 1u << 10 | (kTok >> 3) << 17 | (kRow >> 4) << 24;
       // V is MN-major
       constexpr uint32_t id_o =
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
   } else if (warp == 13) {
     // ---- Q, one thread. Rows of a copy past the block's are other requests' or zero: their
     // results go nowhere ----
-    if (lane == 0) {
+    if (ptx::elect_one()) {
       const int hpk = a.hq / a.n_kv;
       uint32_t segs = 0;
       while (walk.next(a, plan, &s)) {

@@ -135,6 +135,19 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const void *map, int x, int
       : "memory");
 }
 
+// True in one thread of a converged warp. The compiler knows that at most one thread runs what
+// the result guards, so operands that an instruction takes in uniform registers (tcgen05.mma)
+// go there directly, without a loop over the threads that might differ.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one = 0;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "@p mov.s32 %0, 1;\n\t}"
+      : "+r"(one));
+  return one != 0;
+}
+
 // ---- tcgen05: tensor memory ----
 // Allocate ncols (power of two >= 32) TMEM columns; the address is written to smem at dst.
 // Executed by one whole warp.
