@@ -779,6 +779,11 @@ kamera_status kamera_prefix_attention(const kamera_handle *h, const kamera_pool 
   a.n_kv = gqa ? l.H : 1;
   a.dk = dk;
   a.dv = dv;
+  a.hpk = num_q_heads / a.n_kv;
+  a.hpk_magic = ((1ull << 40) + a.hpk - 1) / a.hpk;
+  a.page_shift = -1;
+  for (int s = 0; s < 31; ++s)
+    if (l.page_size == 1 << s) a.page_shift = s;
   a.shape = kamera::prefix_shape(l, num_q_heads);
   a.scale = scale;
   a.ws = d_workspace;

@@ -211,6 +211,9 @@ struct PrefixArgs {
   const int *prefix_len;   // [n_groups]
   const int *ctx_len;      // [n_reqs]
   int n_reqs, n_groups, hq, n_kv, dk, dv;
+  int hpk;                 // query heads of a KV head
+  unsigned long long hpk_magic;  // ceil(2^40 / hpk)
+  int page_shift;          // log2 of the page size, -1 when that is no power of two
   PrefixShape shape;
   float scale;
   void *ws;

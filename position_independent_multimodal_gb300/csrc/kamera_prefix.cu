@@ -18,7 +18,7 @@ namespace kamera {
 
 namespace {
 
-constexpr int kPlanThr = 1024;
+constexpr int kPlanThr = 256;
 constexpr int kPlanNear = 1024;  // groups and listed entries kept in shared memory
 
 // Inclusive scans of N values at a time over the CTA's threads, in place; total: their sums.
@@ -39,13 +39,13 @@ __device__ __forceinline__ void plan_scan(long long (&x)[N], long long (&total)[
     for (int k = 0; k < N; ++k) part[k][warp] = x[k];
   __syncthreads();
   if (warp < N) {  // warp k scans the warps' sums of value k
-    long long y = part[warp][lane];
+    long long y = lane < kPlanThr / 32 ? part[warp][lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long z = __shfl_up_sync(0xffffffffu, y, o);
       if (lane >= o) y += z;
     }
-    part[warp][lane] = y;
+    if (lane < kPlanThr / 32) part[warp][lane] = y;
   }
   __syncthreads();
 #pragma unroll
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_cons
   __shared__ long long near_u0[2][kPlanNear], near_r[kPlanNear];
   __shared__ int broken;
   const int tid = threadIdx.x, R = a.n_reqs, G = a.n_groups;
-  const int hpk = a.hq / a.n_kv, own_cls = class_of(a.shape, hpk);
+  const int hpk = a.hpk, own_cls = class_of(a.shape, hpk);
   const long long cap = (long long)a.pool.pt_stride * a.lay.page_size;
   const bool near_g = G <= kPlanNear;
   const int *start = near_g ? near_start : a.group_start;
@@ -179,17 +179,24 @@ __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_cons
   }
   __syncthreads();
   // workers: with fewer units than would give each `least`, fewer have any
-#pragma unroll
+#pragma unroll 1
   for (int c = 0; c < 2; ++c) {
-    const PrefixClass &k = a.shape.cls[c];
-    const long long U = base[c], few = (U + k.least - 1) / k.least;
+    const PrefixClass k = a.shape.cls[c];
+    const long long U = c ? base[1] : base[0], own0 = c ? prefix_units[1] : prefix_units[0];
+    const int groups = c ? listed[1] : listed[0];
+    const long long few = div_pos(U + k.least - 1, k.least);
     const int n = (int)(few < k.n ? few : k.n);
+    if (n == 0) {
+      if (tid == 0) p.head[8 * c + 4] = 0;
+      continue;
+    }
+    const long long quot = div_pos(U, n), rem = U - quot * n;
+    const long long *g_u0 = p.cls[c].g_u0;
     for (int w = tid; w < n; w += kPlanThr) {
-      const long long u = U * w / n;
-      const bool own = u >= prefix_units[c];
-      const int count = own ? own_listed : listed[c];
-      const long long *u0 = count <= kPlanNear ? (own ? near_r : near_u0[c])
-                                               : (own ? p.r_u0 : p.cls[c].g_u0);
+      const long long u = first_unit(quot, rem, w);
+      const bool own = u >= own0;
+      const int count = own ? own_listed : groups;
+      const long long *u0 = count <= kPlanNear ? (own ? near_r : near_u0[c]) : (own ? p.r_u0 : g_u0);
       int lo = 0, hi = count - 1;  // the last listed one that starts at or before u
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -198,15 +205,20 @@ __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_cons
         else
           hi = mid - 1;
       }
-      p.cls[c].start[w] = lo;
+      const int from = own ? p.r_from[lo] : 0, to = own ? p.r_to[lo] : p.cls[c].g_prefix[lo];
+      const int tiles = tiles_of(from, to, k.tile);
+      const int nrb = ceil_div((own ? 1 : p.cls[c].g_size[lo]) * hpk, k.rb);
+      const long long d = u - u0[lo], b = div_pos(d, tiles), kh = div_pos(b, nrb);
+      p.cls[c].start[w] = make_int4(lo | (own ? 1 << 30 : 0), (int)(b - kh * nrb), (int)kh,
+                                    (int)(d - b * tiles));
     }
     if (tid == 0) {
       long long *head = p.head + 8 * c;
       head[0] = U;
-      head[1] = listed[c];
-      head[2] = c == own_cls ? own_listed : 0;
-      head[3] = n;
-      head[4] = prefix_units[c];
+      head[1] = groups;
+      head[2] = quot;
+      head[3] = rem;
+      head[4] = n;
     }
   }
 }
@@ -420,7 +432,7 @@ __global__ void __launch_bounds__(kThr) prefix_gen_kernel(const __grid_constant_
       float sum = 0.f;
       for (int i = 0; i < lanes; ++i) sum += red[(i * kRows + g) * dv + d];
       float *o, *lse;
-      segment_out<1>(a, plan, s, blockIdx.x, g, &o, &lse);
+      segment_out<1>(a, plan, s, blockIdx.x, g, d == 0, &o, &lse);
       o[d] = l[g] == 0.f ? 0.f : sum / l[g];
       if (d == 0) *lse = l[g] == 0.f ? neg_inf : m[g] + logf(l[g]);
     }
@@ -440,45 +452,35 @@ __global__ void __launch_bounds__(kThr) prefix_merge_kernel(const __grid_constan
                                                             int slices) {
   const PrefixPlan p = prefix_plan(a.shape, a.ws, a.n_reqs, a.hq, a.dv);
   const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * (kThr / 32) + (threadIdx.x >> 5);
-  const long long n_rh = (long long)a.n_reqs * a.hq;
+  // fewer than 2^31 warps: 65535 requests x 256 heads x 8 slices
+  const unsigned w = blockIdx.x * (kThr / 32) + (threadIdx.x >> 5);
+  const unsigned n_rh = (unsigned)a.n_reqs * a.hq;
   if (w >= n_rh * slices) return;
-  const long long rh = w / slices;
-  const int col = (int)(w - rh * slices) * kCols;
-  const int r = (int)(rh / a.hq), h = (int)(rh - (long long)r * a.hq);
-  if (!p.req_state[r]) return;
-  const int hpk = a.hq / a.n_kv, kvh = h / hpk;
+  const unsigned rh = w / slices;
+  const int col = (int)(w - rh * slices) * kCols, r = (int)(rh / (unsigned)a.hq);
   const float neg_inf = -__int_as_float(0x7f800000);
-  // the row's blocks: prefix, own part. Part 0 of a block is the home place, part i > 0 the
-  // carry of worker c0 + i - 1.
+  const bool have[2] = {p.req_pu0[r] >= 0, p.req_ou0[r] >= 0};
+  if (!p.req_state[r]) return;
+  const int size = p.req_size[r];
+  // the row's blocks: prefix, own part. Part 0 of a block is the home place, the rest are carries
   const float *home_o[2], *home_z[2], *carry_o[2], *carry_z[2];
-  int parts[2] = {0, 0}, rb[2], dvh[2];
+  int parts[2] = {0, 0}, rb[2] = {0, 0}, dvh[2] = {0, 0};
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
-    const long long base = b ? p.req_ou0[r] : p.req_pu0[r];
-    if (base < 0) continue;
-    const int rows = (b ? 1 : p.req_size[r]) * hpk, prefix = p.req_prefix[r];
-    const int c = class_of(a.shape, rows);
-    const PrefixClass &k = a.shape.cls[c];
-    const int tiles = b ? tiles_of(prefix, a.ctx_len[r], k.tile) : ceil_div(prefix, k.tile);
-    const int row = (b ? 0 : p.req_at[r] * hpk) + (h - kvh * hpk);
-    const int nrb = ceil_div(rows, k.rb), blk = row / k.rb, at = row - blk * k.rb;
-    dvh[b] = a.dv / k.vh;
-    const int half = col / dvh[b], off = col - half * dvh[b];
-    const long long U = p.head[8 * c], n = p.head[8 * c + 3];
-    const long long u0 = base + (((long long)kvh * k.vh + half) * nrb + blk) * tiles;
-    const long long u1 = u0 + tiles;
-    // workers that start inside the block: c U / n in (u0, u1)
-    long long lo = u0 * n / U;
-    while (lo * U / n <= u0) ++lo;
-    long long hi = u1 * n / U;
-    while (hi > lo && (hi >= n || hi * U / n >= u1)) --hi;
-    parts[b] = 1 + (lo < n && lo * U / n < u1 ? (int)(hi - lo) + 1 : 0);
-    rb[b] = k.rb;
-    home_o[b] = p.home_o + (b * n_rh + rh) * a.dv + col;
-    home_z[b] = p.home_lse + (b * 2ll + half) * n_rh + rh;
-    carry_o[b] = p.cls[c].carry_o + (lo * k.rb + at) * dvh[b] + off;
-    carry_z[b] = p.cls[c].carry_lse + lo * k.rb + at;
+    const int c = class_of(a.shape, (b ? 1 : size) * a.hpk);
+    const int vh = c ? a.shape.cls[1].vh : a.shape.cls[0].vh;
+    rb[b] = c ? a.shape.cls[1].rb : a.shape.cls[0].rb;
+    dvh[b] = vh == 2 ? a.dv >> 1 : a.dv;
+    const int half = col >= dvh[b], off = col - half * dvh[b];
+    const long long z = (b * 2ll + half) * n_rh + rh;
+    home_o[b] = p.home_o + ((long long)b * n_rh + rh) * a.dv + col;
+    home_z[b] = p.home_lse + z;
+    if (have[b]) {
+      const int2 more = p.home_more[z];
+      parts[b] = 1 + more.y;
+      carry_o[b] = (c ? p.cls[1].carry_o : p.cls[0].carry_o) + (long long)more.x * dvh[b] + off;
+      carry_z[b] = (c ? p.cls[1].carry_lse : p.cls[0].carry_lse) + more.x;
+    }
   }
   const int np = parts[0] + parts[1];
   auto block_of = [&](int i) { return i >= parts[0]; };
@@ -528,7 +530,7 @@ __global__ void __launch_bounds__(kThr) prefix_merge_kernel(const __grid_constan
     uint2 v;
     v.x = pack_bf16(acc[0] * inv, acc[1] * inv);
     v.y = pack_bf16(acc[2] * inv, acc[3] * inv);
-    *reinterpret_cast<uint2 *>(a.out + rh * a.dv + mine) = v;
+    *reinterpret_cast<uint2 *>(a.out + (long long)rh * a.dv + mine) = v;
   }
   if (lane == 0 && col == 0) a.lse[rh] = sum == 0.f ? neg_inf : top + logf(sum);
 }
@@ -574,7 +576,7 @@ cudaError_t launch_prefix_attention(const PrefixArgs &a, cudaStream_t s) {
   prefix_plan_kernel<<<1, kPlanThr, 0, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int hpk = a.hq / a.n_kv;
+  const int hpk = a.hpk;
   if (prefix_tc_layout(a.lay)) {
     // blocks can be wide only where the largest group would be, thin only where one request is
     if ((long long)a.n_reqs * hpk > a.shape.wide_rows) e = launch_prefix_tc(a, s);

@@ -8,11 +8,11 @@
 // bound them, and a tile of 128 rows would be idle for the most part). A unit is one tile of
 // tokens (at multiples of the class's tile) of one block of at most `rb` rows. A class's units
 // are numbered prefix blocks first (group, KV head and column half, row block, tile), then own
-// blocks (request, ...), and worker c of n takes units [c U / n, (c + 1) U / n): every worker has
-// the same number of tiles whatever the lengths, and cuts at most its first and last block. A
-// block's first segment writes its rows' partial output to the rows' home place, a segment that
-// starts inside a block to its worker's carry place; the merge kernel joins a row's parts by
-// their log-sum-exp.
+// blocks (request, ...), and of n workers with units each takes U / n consecutive ones, the first
+// U % n one more: every worker has the same number of tiles whatever the lengths, and cuts at most its first and last block. A
+// block's first segment writes its rows' partial output to the rows' home place, with the number
+// of workers that follow on the block; those write to their carry places. The merge kernel joins
+// a row's parts by their log-sum-exp.
 #pragma once
 
 #include "kamera_dev.cuh"
@@ -21,13 +21,14 @@ namespace kamera {
 
 // What the plan kernel leaves for the others, in the workspace.
 struct PrefixPlan {
-  // per class c at head[8 c + .]: 0 units, 1 groups listed, 2 requests listed, 3 workers with
-  // units, 4 units of the prefixes
+  // per class c at head[8 c + .]: 0 units U, 1 groups listed, 2 U / n and 3 U % n for the n workers
+  // with units, 4 n
   long long *head;
   struct Lists {          // blocks of a class
     long long *g_u0;      // [R] first unit of the i-th listed group
     int *g_first, *g_size, *g_prefix, *g_lead;  // first request, requests, prefix, leader
-    int *start;           // [n] list index of each worker's first block
+    int4 *start;          // [n] each worker's first block: list index (own: + 2^30), row block,
+                          //     KV head x half, tile
     float *carry_lse;     // [n][rb]
     float *carry_o;       // [n][rb][dv / vh]
   } cls[2];
@@ -43,6 +44,8 @@ struct PrefixPlan {
   int *req_at, *req_size; // [R] request r: its place in its group, requests of the group
   int *req_prefix;        // [R] request r: tokens of its group's prefix
   float *home_lse;        // [2][2][R][hq]: prefix and own part, column half
+  int2 *home_more;        // [2][2][R][hq]: of the row's first carry place its index in carry_lse,
+                          // and how many carries follow (each rb further on)
   float *home_o;          // [2][R][hq][dv]
   size_t total;
 };
@@ -68,7 +71,7 @@ __host__ __device__ inline PrefixPlan prefix_plan(const PrefixShape &sh, void *w
     p.cls[c].g_size = i32(R);
     p.cls[c].g_prefix = i32(R);
     p.cls[c].g_lead = i32(R);
-    p.cls[c].start = i32(k.n);
+    p.cls[c].start = reinterpret_cast<int4 *>(take(16ll * k.n));
     p.cls[c].carry_lse = f32((long long)k.n * k.rb);
     p.cls[c].carry_o = f32((long long)k.n * k.rb * (dv / k.vh));
   }
@@ -86,6 +89,7 @@ __host__ __device__ inline PrefixPlan prefix_plan(const PrefixShape &sh, void *w
   p.req_size = i32(R);
   p.req_prefix = i32(R);
   p.home_lse = f32(4 * R * hq);
+  p.home_more = reinterpret_cast<int2 *>(take(32 * R * hq));
   p.home_o = f32(2 * R * hq * dv);
   p.total = o;
   return p;
@@ -103,6 +107,19 @@ __host__ __device__ inline int class_of(const PrefixShape &sh, int rows) {
   return rows > sh.wide_rows ? 0 : 1;
 }
 
+// First unit of worker w; the worker of unit u.
+__device__ __forceinline__ long long first_unit(long long quot, long long rem, long long w) {
+  return w * quot + (w < rem ? w : rem);
+}
+__device__ __forceinline__ long long div_pos(long long a, long long b) {  // a >= 0, b > 0
+  if (((a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
+  return a / b;
+}
+__device__ __forceinline__ int worker_of(long long quot, long long rem, long long u) {
+  const long long edge = rem * (quot + 1);
+  return (int)(u < edge ? div_pos(u, quot + 1) : rem + div_pos(u - edge, quot));
+}
+
 // A run of tiles of one block, as a worker takes it.
 struct Segment {
   int own;          // 0: a group's prefix, 1: a request's own tokens
@@ -112,6 +129,7 @@ struct Segment {
   int kvh, half;    // KV head, column half of V
   int tok0, tok1;   // tokens [tok0, tok1) of the segment
   int carry;        // 1: starts inside its block
+  int more;         // first segment of its block: how many workers follow on the block
 };
 
 // Walks the segments of a worker of class C.
@@ -137,24 +155,21 @@ struct SegmentWalk {
       to = p.cls[C].g_prefix[i];
     }
     tiles = tiles_of(from, to, a.shape.cls[C].tile);
-    nrb = ceil_div(size * (a.hq / a.n_kv), a.shape.cls[C].rb);
-    rbk = kh = t = 0;
+    nrb = ceil_div(size * a.hpk, a.shape.cls[C].rb);
   }
   __device__ __forceinline__ void start(const PrefixArgs &a, const PrefixPlan &p, int worker) {
     const long long *head = p.head + 8 * C;
-    const long long U = head[0], n = head[3];
     u = end = 0;
-    if (worker >= n) return;
-    u = U * worker / n;  // U < 2^49, n < 2^11
-    end = U * (worker + 1) / n;
-    own = u >= head[4];
-    i = p.cls[C].start[worker];
+    if (worker >= head[4]) return;
+    const int4 at = p.cls[C].start[worker];
+    u = first_unit(head[2], head[3], worker);
+    end = first_unit(head[2], head[3], worker + 1);
+    own = at.x >> 30;
+    i = at.x & 0x3FFFFFFF;
     entry(a, p);
-    const long long d = u - (own ? p.r_u0 : p.cls[C].g_u0)[i];
-    const long long b = d / tiles;
-    t = (int)(d - b * tiles);
-    kh = (int)(b / nrb);
-    rbk = (int)(b - (long long)kh * nrb);
+    rbk = at.y;
+    kh = at.z;
+    t = at.w;
   }
   // The next segment; false when there is none.
   __device__ __forceinline__ bool next(const PrefixArgs &a, const PrefixPlan &p, Segment *s) {
@@ -167,6 +182,7 @@ struct SegmentWalk {
         i = 0;
       }
       entry(a, p);
+      kh = 0;
     }
     s->own = own;
     s->r0 = first;
@@ -174,12 +190,17 @@ struct SegmentWalk {
     s->kvh = k.vh == 1 ? kh : kh >> 1;
     s->half = k.vh == 1 ? 0 : kh & 1;
     s->row0 = rbk * k.rb;
-    s->rows = min(k.rb, size * (a.hq / a.n_kv) - s->row0);
+    s->rows = min(k.rb, size * a.hpk - s->row0);
     const long long left = end - u;
     const int nt = (int)(left < tiles - t ? left : tiles - t), t0 = from / k.tile;
     s->tok0 = t == 0 ? from : (t0 + t) * k.tile;
     s->tok1 = t + nt == tiles ? to : (t0 + t + nt) * k.tile;
     s->carry = t > 0;
+    s->more = 0;
+    if (t == 0 && nt < tiles) {
+      const long long *head = p.head + 8 * C;
+      s->more = worker_of(head[2], head[3], u + tiles - 1) - worker_of(head[2], head[3], u);
+    }
     u += nt;
     t = 0;
     if (++rbk == nrb) {
@@ -190,20 +211,22 @@ struct SegmentWalk {
   }
 };
 
-// (request, query head) of row i of a segment's block.
+// (request, query head) of row i of a segment's block. k / hpk by a product: k < 2^24 and
+// magic = ceil(2^40 / hpk) is exact for k < 2^40 / hpk^2.
 __device__ __forceinline__ void segment_row(const PrefixArgs &a, const Segment &s, int i, int *r,
                                             int *h) {
-  const int hpk = a.hq / a.n_kv, k = s.row0 + i;
-  const int d = k / hpk;
+  const int k = s.row0 + i;
+  const int d = (int)((unsigned long long)k * a.hpk_magic >> 40);
   *r = s.r0 + d;
-  *h = s.kvh * hpk + (k - d * hpk);
+  *h = s.kvh * a.hpk + (k - d * a.hpk);
 }
 
-// Where row i of the segment of a worker goes: its output row (dv / vh columns) and its lse.
+// Where row i of the segment of a worker goes: its output row (dv / vh columns) and its lse. A
+// home place also gets what follows on it.
 template <int C>
 __device__ __forceinline__ void segment_out(const PrefixArgs &a, const PrefixPlan &p,
-                                            const Segment &s, int worker, int i, float **o,
-                                            float **lse) {
+                                            const Segment &s, int worker, int i, bool tell,
+                                            float **o, float **lse) {
   const PrefixClass &c = a.shape.cls[C];
   const int dvh = a.dv / c.vh;
   if (s.carry) {
@@ -215,8 +238,29 @@ __device__ __forceinline__ void segment_out(const PrefixArgs &a, const PrefixPla
   int r, h;
   segment_row(a, s, i, &r, &h);
   const long long rh = (long long)r * a.hq + h, n = (long long)a.n_reqs * a.hq;
+  const long long z = ((long long)s.own * 2 + s.half) * n + rh;
   *o = p.home_o + (s.own * n + rh) * a.dv + s.half * dvh;
-  *lse = p.home_lse + ((long long)s.own * 2 + s.half) * n + rh;
+  *lse = p.home_lse + z;
+  if (tell) p.home_more[z] = make_int2((worker + 1) * c.rb + i, s.more);
+}
+
+// Logical token tok's index in the page table and within its page.
+__device__ __forceinline__ int page_index(const PrefixArgs &a, int tok) {
+  return a.page_shift >= 0 ? tok >> a.page_shift
+                           : (int)((unsigned)tok / (unsigned)a.lay.page_size);
+}
+// A page-table entry as loaded, before its check.
+__device__ __forceinline__ int load_page(const PrefixArgs &a, int lead, int tok) {
+  return __ldg(a.pool.pt + (long long)lead * a.pool.pt_stride + page_index(a, tok));
+}
+// Its token's slot; -1 (and the OOB bit) when the page ends outside the pool.
+__device__ __forceinline__ int slot_in(const PrefixArgs &a, int page, int tok) {
+  const int ps = a.lay.page_size;
+  if (page < 0 || ((long long)page + 1) * ps > a.pool.num_slots) {
+    atomicOr(a.status, KAMERA_DEVICE_SLOT_OOB);
+    return -1;
+  }
+  return page * ps + (tok - page_index(a, tok) * ps);
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {

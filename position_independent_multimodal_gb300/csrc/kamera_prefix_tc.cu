@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
       const int i = kRow * w + row;
       if (live) {
         float *o = nullptr, *lse = nullptr;
-        if (i < s.rows) segment_out<0>(a, plan, s, blockIdx.x, i, &o, &lse);
+        if (i < s.rows) segment_out<0>(a, plan, s, blockIdx.x, i, true, &o, &lse);
         const bool ok = l != 0.f && !*gave_up;
         const float inv = 1.f / l;
 #pragma unroll 1
@@ -346,9 +346,9 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
       const int kcol = gqa ? s.kvh * lay.hd : 0;
       const int vcol = gqa ? kcol : s.half * (S::DV * 64);
       auto slot_at = [&](int i) -> int {  // of this thread's token of tile i
-        const long long tok = (long long)(a0 + i) * kTok + lt;
+        const int tok = (a0 + i) * kTok + lt;  // below 2^31: a tile with a token starts below it
         if (tok < s.tok0 || tok >= s.tok1) return -1;
-        return (int)slot_of(a.pool, lay.page_size, s.lead, tok, a.status);
+        return slot_in(a, load_page(a, s.lead, tok), tok);
       };
       // The next stages: `chunks` chunks from column `col` of a tile's rows. slot: this thread's
       // token's; tile: the tile's number, for the other tokens' slots; whole: every token is in.
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
     // ---- Q, one thread. Rows of a copy past the block's are other requests' or zero: their
     // results go nowhere ----
     if (ptx::elect_one()) {
-      const int hpk = a.hq / a.n_kv;
+      const int hpk = a.hpk;
       uint32_t segs = 0;
       while (walk.next(a, plan, &s)) {
         if (segs) wait(bar(S::q_empty), (segs - 1) & 1, gave_up);

@@ -43,20 +43,6 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A page-table entry as loaded, before its check.
-__device__ __forceinline__ int load_page(const PrefixArgs &a, int lead, int tok) {
-  const int pi = (int)((unsigned)tok / (unsigned)a.lay.page_size);
-  return __ldg(a.pool.pt + (long long)lead * a.pool.pt_stride + pi);
-}
-// Its token's slot; -1 (and the OOB bit) when the page ends outside the pool.
-__device__ __forceinline__ int slot_in(const PrefixArgs &a, int page, int tok) {
-  if (page < 0 || ((long long)page + 1) * a.lay.page_size > a.pool.num_slots) {
-    atomicOr(a.status, KAMERA_DEVICE_SLOT_OOB);
-    return -1;
-  }
-  return page * a.lay.page_size + (int)((unsigned)tok % (unsigned)a.lay.page_size);
-}
-
 constexpr int kRows = 16;
 
 // ---------------------------------------------------------------------------------------
@@ -69,7 +55,8 @@ struct Thin {
   static constexpr int kTok = 16;
   static constexpr int kTile = kTok * D * 2;    // bytes of a tile of K, of V and of Q
   static constexpr int kStage = 3 * kTile;
-  static constexpr int total = WARPS * NST * kStage;
+  static constexpr int queue = WARPS * NST * kStage;  // Segment [WARPS][8]
+  static constexpr int total = queue + WARPS * 8 * (int)sizeof(Segment);
   static constexpr int pieces = D / 8;          // 16-byte pieces of a row
   static_assert(NST <= 4, "token masks of the stages share a 64-bit register");
 };
@@ -97,11 +84,20 @@ __global__ void __launch_bounds__(T::WARPS * 32, 1) prefix_thin_kernel(const __g
   const float neg_inf = -__int_as_float(0x7f800000);
   const float c = a.scale * kLog2e;
 
-  // ---- loads: one tile ahead of its issue the page entry, NST - 1 tiles ahead of its use ----
+  // ---- loads: one tile ahead of its issue the page entry, NST - 1 tiles ahead of its use. The
+  // segments go on through a queue: at most NST + 1 are between the loads and the products ----
+  Segment *queue = reinterpret_cast<Segment *>(smem + T::queue) + warp * 8;
   SegmentWalk<1> lw;
   lw.start(a, plan, worker);
   Segment ls;
-  bool l_any = lw.next(a, plan, &ls), l_first = true;
+  int l_seg = 0;
+  auto next_segment = [&]() {
+    if (!lw.next(a, plan, &ls)) ls.rows = 0;  // the end
+    if (lane == 0) queue[l_seg & 7] = ls;
+    ++l_seg;
+    return ls.rows > 0;
+  };
+  bool l_any = next_segment(), l_first = true;
   int l_t = l_any ? ls.tok0 / kTok : 0;  // tile to issue next
   int page = 0;                          // of lane's token of that tile
   auto fetch = [&]() {
@@ -144,7 +140,7 @@ __global__ void __launch_bounds__(T::WARPS * 32, 1) prefix_thin_kernel(const __g
       }
       l_first = false;
       if (++l_t >= ceil_div(ls.tok1, kTok)) {
-        l_any = lw.next(a, plan, &ls);
+        l_any = next_segment();
         l_first = true;
         if (l_any) l_t = ls.tok0 / kTok;
       }
@@ -157,12 +153,12 @@ __global__ void __launch_bounds__(T::WARPS * 32, 1) prefix_thin_kernel(const __g
   for (int i = 0; i < T::NST - 1; ++i) issue();
 
   // ---- attention ----
-  SegmentWalk<1> walk;
-  walk.start(a, plan, worker);
-  Segment s;
   int st = 0;
   const int g = lane >> 2, q4 = lane & 3;  // rows g and g + 8, columns 2 q4, 2 q4 + 1
-  while (walk.next(a, plan, &s)) {
+  for (int seg = 0;; ++seg) {
+    __syncwarp();
+    const Segment s = queue[seg & 7];
+    if (s.rows == 0) break;
     uint32_t qf[D / 16][4];
     float o[D / 8][4], m0 = neg_inf, m1 = neg_inf, l0 = 0.f, l1 = 0.f;
 #pragma unroll
@@ -254,7 +250,7 @@ __global__ void __launch_bounds__(T::WARPS * 32, 1) prefix_thin_kernel(const __g
       const float l = half ? l1 : l0, m = half ? m1 : m0;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       float *dst, *lse;
-      segment_out<1>(a, plan, s, worker, i, &dst, &lse);
+      segment_out<1>(a, plan, s, worker, i, q4 == 0, &dst, &lse);
 #pragma unroll
       for (int j = 0; j < D / 8; ++j) {
         const float2 v = make_float2(l == 0.f ? 0.f : o[j][2 * half] * inv,
@@ -281,7 +277,8 @@ struct ThinMla {
   static constexpr int slot = p + kRows * kTok * 2;  // int [4][kTok]
   static constexpr int wmax = slot + 4 * kTok * 4;   // float [8][16]
   static constexpr int wsum = wmax + 8 * kRows * 4;  // float [8][16]
-  static constexpr int total = wsum + 8 * kRows * 4;
+  static constexpr int queue = wsum + 8 * kRows * 4;  // Segment [8]
+  static constexpr int total = queue + 8 * (int)sizeof(Segment);
 };
 
 // Byte offset of a 16-byte piece (0..71) of a row.
@@ -304,10 +301,18 @@ __global__ void __launch_bounds__(ThinMla::kThr, 1) prefix_thin_mla_kernel(const
   const float c = a.scale * kLog2e;
 
   // ---- loads: slots two tiles ahead, rows one tile ahead ----
-  SegmentWalk<1> sw;  // of the slots
+  Segment *queue = reinterpret_cast<Segment *>(smem + M::queue);
+  SegmentWalk<1> sw;  // of the slots; the segments go on through the queue
   sw.start(a, plan, blockIdx.x);
   Segment ss;
-  bool s_any = sw.next(a, plan, &ss);
+  int s_seg = 0;
+  auto next_segment = [&]() {
+    if (!sw.next(a, plan, &ss)) ss.rows = 0;  // the end
+    if (tid == 0) queue[s_seg & 7] = ss;
+    ++s_seg;
+    return ss.rows > 0;
+  };
+  bool s_any = next_segment();
   int s_t = s_any ? ss.tok0 / M::kTok : 0, s_no = 0;
   auto resolve = [&]() {  // the next tile's slots, one thread a token
     if (!s_any) return;
@@ -318,15 +323,19 @@ __global__ void __launch_bounds__(ThinMla::kThr, 1) prefix_thin_mla_kernel(const
     }
     ++s_no;
     if (++s_t >= ceil_div(ss.tok1, M::kTok)) {
-      s_any = sw.next(a, plan, &ss);
+      s_any = next_segment();
       if (s_any) s_t = ss.tok0 / M::kTok;
     }
   };
-  SegmentWalk<1> lw;
-  lw.start(a, plan, blockIdx.x);
   Segment ls;
-  bool l_any = lw.next(a, plan, &ls), l_first = true;
-  int l_t = l_any ? ls.tok0 / M::kTok : 0, l_no = 0, l_seg = 0;
+  bool l_any = true, l_first = true;
+  int l_t = 0, l_no = 0, l_seg = 0;
+  auto load_segment = [&]() {
+    ls = queue[l_seg & 7];
+    l_any = ls.rows > 0;
+    l_first = true;
+    l_t = ls.tok0 / M::kTok;
+  };
   auto issue = [&]() {  // rows of the next tile, whose slots are there
     if (l_any) {
       const uint32_t dst = sb + M::k + (l_no & 1) * M::kTile;
@@ -356,14 +365,12 @@ __global__ void __launch_bounds__(ThinMla::kThr, 1) prefix_thin_mla_kernel(const
             ptx::cp_async16(sb + M::q + (l_seg & 1) * (kRows * M::kRow) + mla16(i, x + 8 * k),
                             i < ls.rows ? src + 64 * k : src, i < ls.rows ? 16u : 0u);
         }
-        ++l_seg;
       }
       l_first = false;
       ++l_no;
       if (++l_t >= ceil_div(ls.tok1, M::kTok)) {
-        l_any = lw.next(a, plan, &ls);
-        l_first = true;
-        if (l_any) l_t = ls.tok0 / M::kTok;
+        ++l_seg;
+        load_segment();
       }
     }
     ptx::cp_async_commit();
@@ -371,13 +378,13 @@ __global__ void __launch_bounds__(ThinMla::kThr, 1) prefix_thin_mla_kernel(const
   resolve();
   resolve();
   __syncthreads();
+  load_segment();
   issue();
 
-  SegmentWalk<1> walk;
-  walk.start(a, plan, blockIdx.x);
-  Segment s;
-  int no = 0, seg = 0;
-  while (walk.next(a, plan, &s)) {
+  int no = 0;
+  for (int seg = 0;; ++seg) {
+    const Segment s = queue[seg & 7];
+    if (s.rows == 0) break;
     float o[8][4], m0 = neg_inf, m1 = neg_inf, l0 = 0.f, l1 = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
@@ -464,7 +471,6 @@ __global__ void __launch_bounds__(ThinMla::kThr, 1) prefix_thin_mla_kernel(const
         }
       }
     }
-    ++seg;
     // sums over the warps' tokens
 #pragma unroll
     for (int d = 1; d < 4; d <<= 1) {
@@ -489,7 +495,7 @@ __global__ void __launch_bounds__(ThinMla::kThr, 1) prefix_thin_mla_kernel(const
       const float l = half ? l1 : l0, m = half ? m1 : m0;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       float *dst, *lse;
-      segment_out<1>(a, plan, s, blockIdx.x, i, &dst, &lse);
+      segment_out<1>(a, plan, s, blockIdx.x, i, q4 == 0 && warp == 0, &dst, &lse);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float2 v = make_float2(l == 0.f ? 0.f : o[j][2 * half] * inv,
