@@ -3,7 +3,7 @@
 // of tiles off (kamera_prefix.cuh); a tile is 128 tokens against a block's query rows.
 //
 //   S [128 rows x 128 tokens] = Q K^T           tcgen05, Q and K from shared memory
-//   P = bf16(2^(c S - c m)),  c = |scale| log2 e  one thread per row, P back into TMEM over S
+//   P = bf16(2^(c S - c m)),  c = |scale| log2 e  two threads per row, P into TMEM over S
 //   O [128 rows x dims] += P V                   tcgen05, P from TMEM, V from shared memory
 //
 // The running maximum m that P is taken against is raised only when a row's new maximum exceeds
@@ -11,9 +11,9 @@
 // then O is rescaled in TMEM; after the first tiles that is rare. The row sums l take the
 // float32 weights, so l and the log-sum-exp carry no bf16 rounding.
 //
-// Roles: warps 0-3 and 4-7 one query row per thread (softmax, rescaling, output), warps 8-11
-// bring K and V rows through the page table into a ring of stages, warp 12 issues the MMAs, warp
-// 13 loads Q. Whole tiles of pages of 8, 16, 32 or 64 slots, or a multiple of 128, come as
+// Roles: warps 0-15 softmax, rescaling and output, two threads (of two warps) to a query row, 64
+// tokens and half of O's columns each; warps 16 and 17 bring K and V rows through the page table
+// into a ring of stages, warps 18 and 19 issue the MMAs and the copies of Q. Whole tiles of pages of 8, 16, 32 or 64 slots, or a multiple of 128, come as
 // tensor-map copies, one per page and 64 columns; tiles with tokens left out (the ends of a
 // context, pages outside the pool) and other page sizes as 16-byte cp.async, zero-filled where a
 // token has no slot, so that nothing of a row that no token holds is ever multiplied.
@@ -33,11 +33,11 @@ namespace kamera {
 
 namespace {
 
-constexpr int kThr = 512;
+constexpr int kThr = 640;
+constexpr int kLoad = 64;              // threads that load K and V: two tokens each
 constexpr int kTok = 128;              // tokens per tile
 constexpr int kRow = 128;              // query rows per MMA
 constexpr int kChunk = kTok * 128;     // bytes of a 128 x 64 bf16 operand tile
-constexpr int kSlots = 4;              // tiles whose slots are kept
 constexpr int kMasks = 8;              // tiles whose token masks are kept
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
@@ -49,14 +49,14 @@ struct Shape {
   static constexpr int kStage = UC * kChunk;
   static constexpr int q = 0;
   static constexpr int ring = QT * DK * kChunk;
-  static constexpr int slot = ring + NST * kStage;   // int [kSlots][kTok]
-  static constexpr int mask = slot + kSlots * kTok * 4;  // uint32 [kMasks][4]
-  static constexpr int bar = mask + kMasks * 16;
+  static constexpr int mask = ring + NST * kStage;  // uint32 [kMasks][4]
+  static constexpr int xch = mask + kMasks * 16;    // float [2][2][kRow]: maxima, then sums
+  static constexpr int bar = xch + 4 * kRow * 4;
   // mbarriers
-  static constexpr int full = 0, empty = NST, q_full = 2 * NST, q_empty = q_full + 1,
+  static constexpr int full = 0, empty = NST, q_full = empty + NST, q_empty = q_full + 1,
                        s_full = q_empty + 1, p_full = s_full + 2, pv_done = p_full + 2,
-                       o_free = pv_done + 2, mk_full = o_free + 2, last = mk_full + kMasks,
-                       n_bar = last + 1;
+                       o_free = pv_done + 2, o_full = o_free + 2,
+                       mk_full = o_full + 2, last = mk_full + kMasks, n_bar = last + 1;
   static constexpr int misc = bar + n_bar * 8;  // TMEM address, give-up flag
   static constexpr int total = misc + 16;
   static constexpr uint32_t o_col = 256;        // O of tile t at o_col + t * 128
@@ -76,20 +76,6 @@ struct Maps {
   int q_step;                 // 1: the rows of a block are consecutive rows of q
   int group_bytes, own_bytes; // of the query copies
 };
-
-// Wait for a phase, giving up after kWaitNs or when another thread has (then the kernel runs to
-// its end without waiting, and reports it).
-__device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, volatile uint32_t *gave_up) {
-  if (ptx::mbar_try_wait(bar, parity)) return;
-  const uint64_t t0 = ptx::globaltimer();
-  while (!ptx::mbar_try_wait(bar, parity)) {
-    if (*gave_up) return;
-    if (ptx::globaltimer() - t0 > kWaitNs) {
-      *gave_up = 1;
-      return;
-    }
-  }
-}
 
 template <int V>
 struct Int {
@@ -131,29 +117,48 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
   volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem + S::misc);
   volatile uint32_t *gave_up = misc + 1;
   auto bar = [&](int i) { return sb + S::bar + 8 * i; };
+  // Waits for a phase, giving up after kWaitNs or when another thread has. A thread that gave up
+  // runs on to its end without waiting, arriving, copying or multiplying: it keeps step with the
+  // named barriers only, and no barrier gets an arrival that it does not expect.
+  bool dead = false;
+  auto wait = [&](uint32_t b, uint32_t parity) {
+    if (dead || ptx::mbar_try_wait(b, parity)) return;
+    const uint64_t t0 = ptx::globaltimer();
+    while (!ptx::mbar_try_wait(b, parity)) {
+      if (*gave_up || ptx::globaltimer() - t0 > kWaitNs) {
+        *gave_up = 1;
+        dead = true;
+        return;
+      }
+    }
+  };
+  auto arrive = [&](uint32_t b) {
+    if (!dead) ptx::mbar_arrive(b);
+  };
 
   if (sb & 1023u) {  // the swizzled layouts want 1024-byte groups; there is no static memory here
     if (tid == 0) atomicOr(a.status, KAMERA_DEVICE_TIMEOUT);
     return;
   }
-  if (warp == 12) {
+  if (warp == 18) {
     ptx::tmem_alloc(sb + S::misc, 512);
     ptx::tmem_relinquish();
   }
   if (tid == 0) {
     for (int i = 0; i < S::NST; ++i) {
-      ptx::mbar_init(bar(S::full + i), 128);
+      ptx::mbar_init(bar(S::full + i), kLoad);
       ptx::mbar_init(bar(S::empty + i), 1);
     }
     ptx::mbar_init(bar(S::q_full), 1);
     ptx::mbar_init(bar(S::q_empty), 1);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bar(S::s_full + i), 1);
-      ptx::mbar_init(bar(S::p_full + i), 128);
+      ptx::mbar_init(bar(S::p_full + i), 256);
       ptx::mbar_init(bar(S::pv_done + i), 1);
-      ptx::mbar_init(bar(S::o_free + i), 128);
+      ptx::mbar_init(bar(S::o_free + i), 256);
+      ptx::mbar_init(bar(S::o_full + i), 1);
     }
-    for (int i = 0; i < kMasks; ++i) ptx::mbar_init(bar(S::mk_full + i), 4);
+    for (int i = 0; i < kMasks; ++i) ptx::mbar_init(bar(S::mk_full + i), kLoad / 32);
     ptx::mbar_init(bar(S::last), 1);
     ptx::fence_mbar_init();
     *gave_up = 0;
@@ -167,58 +172,64 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
   walk.start(a, plan, blockIdx.x);
   Segment s;
 
-  if (warp < 8) {
-    // ---- softmax: thread = query row ----
-    const int w = warp >> 2;                       // query tile (QT 1: only warps 0-3 work)
-    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+  if (warp < 16) {
+    // ---- softmax: thread = half of a query row ----
+    const int w = S::QT == 2 ? warp >> 3 : 0;      // query tile (QT 1: warps 8-15 have none)
+    const int hf = (warp >> 2) & 1;                // half of the tokens, of O's columns
     const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const float c = fabsf(a.scale) * kLog2e;
     const bool flip = a.scale < 0.f;
     const float neg_inf = -__int_as_float(0x7f800000);
-    const uint32_t o_t = tmem + S::o_col + (S::QT == 2 ? w * 128 : 0) + lane_off;
-    uint32_t s_ph = 0;          // parity of each S buffer
-    uint32_t tiles = 0;         // tiles of this query tile so far (phases of pv_done)
-    uint32_t seen = 0;          // tiles the loader has masked so far
+    const uint32_t o_t = tmem + S::o_col + w * 128 + hf * (S::DV * 32) + lane_off;
+    const uint32_t pv = bar(S::pv_done + w);
+    float *xch = reinterpret_cast<float *>(smem + S::xch);
+    // the two warps of a row's threads
+    auto pair_sync = [&]() {
+      asm volatile("bar.sync %0, 64;" ::"r"(2 + w * 4 + (warp & 3)) : "memory");
+    };
+    uint32_t s_ph = 0;   // parity of each S buffer
+    uint32_t o_ph = 0;   // parity of o_full
+    uint32_t tiles = 0;  // tiles of this query tile so far (phases of pv_done)
+    uint32_t seen = 0;   // tiles the loader has masked so far
     while (walk.next(a, plan, &s)) {
       const int n = tiles_of(s.tok0, s.tok1, kTok);
-      if (S::QT == 2 ? (w == 1 && s.rows <= kRow) : w == 1) {
+      if (S::QT == 2 ? (w == 1 && s.rows <= kRow) : warp >= 8) {
         seen += n;
         continue;
       }
       const bool live = kRow * w + (row & ~31) < s.rows;  // a warp without rows only keeps step
       float m = neg_inf, l = 0.f;
       for (int i = 0; i < n; ++i, ++seen, ++tiles) {
-        const int b = S::QT == 2 ? w : (i & 1);
-        wait(bar(S::s_full + b), (s_ph >> b) & 1, gave_up);
+        const int b = S::QT == 2 ? w : (tiles & 1);
+        wait(bar(S::s_full) + 8 * b, (s_ph >> b) & 1);
         __syncwarp();
         s_ph ^= 1u << b;
         ptx::tc_fence_after();
         if (live) {
-          const uint32_t st = tmem + b * 128 + lane_off;
+          const uint32_t st = tmem + b * 128 + hf * 64 + lane_off;
+          uint32_t x[32];
+          ptx::tmem_ld32(st, x);
           const int mk = seen % kMasks;
-          wait(bar(S::mk_full + mk), (seen / kMasks) & 1, gave_up);
+          wait(bar(S::mk_full) + 8 * mk, (seen / kMasks) & 1);
           __syncwarp();
-          const uint4 msk = *reinterpret_cast<const uint4 *>(smem + S::mask + 16 * mk);
-          const bool whole = (msk.x & msk.y & msk.z & msk.w) == 0xffffffffu;
-          // pass 1: the tile's maximum, 32 columns in flight while 32 are compared
-          float mx = m;
-          uint32_t r[2][32];
-          ptx::tmem_ld32(st, r[0]);
+          const uint2 msk = *reinterpret_cast<const uint2 *>(smem + S::mask + 16 * mk + 8 * hf);
+          const bool whole = (msk.x & msk.y) == 0xffffffffu;
+          // pass 1: the maximum
+          float top = neg_inf;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t *x = r[j & 1];
+          for (int j = 0; j < 2; ++j) {
+            if (j) ptx::tmem_ld32(st + 32, x);
 #pragma unroll
             for (int e = 0; e < 32; e += 8) ptx::tmem_ld_wait(x + e);
-            if (j < 3) ptx::tmem_ld32(st + 32 * (j + 1), r[(j + 1) & 1]);
             if (!whole || flip) {
-              const uint32_t bits = j == 0 ? msk.x : j == 1 ? msk.y : j == 2 ? msk.z : msk.w;
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
                 const float y = __uint_as_float(x[e]);
-                mx = (bits >> e) & 1 ? fmaxf(mx, flip ? -y : y) : mx;
+                top = ((j ? msk.y : msk.x) >> e) & 1 ? fmaxf(top, flip ? -y : y) : top;
               }
             } else {
-              float m0 = mx, m1 = mx, m2 = mx, m3 = mx;
+              float m0 = top, m1 = top, m2 = top, m3 = top;
 #pragma unroll
               for (int e = 0; e < 32; e += 8) {
                 m0 = fmaxf(fmaxf(m0, __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
@@ -226,55 +237,61 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
                 m2 = fmaxf(fmaxf(m2, __uint_as_float(x[e + 4])), __uint_as_float(x[e + 5]));
                 m3 = fmaxf(fmaxf(m3, __uint_as_float(x[e + 6])), __uint_as_float(x[e + 7]));
               }
-              mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+              top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
             }
           }
-          const bool first = m == neg_inf && mx > neg_inf;
-          const bool raise = first || (mx - m) * c > 8.f;
+          // the row's other half
+          float *mine = xch + ((b * 2 + hf) << 7) + row;
+          *mine = top;
+          pair_sync();
+          top = fmaxf(top, xch[((b * 2 + (hf ^ 1)) << 7) + row]);
+          const bool first = m == neg_inf && top > neg_inf;
+          const bool raise = first || (top - m) * c > 8.f;
           if (__any_sync(0xffffffffu, raise)) {
-            const float f = raise ? (first ? 0.f : exp2_approx((m - mx) * c)) : 1.f;
-            if (raise) m = mx;
+            const float f = raise ? (first ? 0.f : exp2_approx((m - top) * c)) : 1.f;
+            if (raise) m = top;
             if (i > 0) {
-              wait(bar(S::pv_done + (S::QT == 2 ? w : 0)), (tiles - 1) & 1, gave_up);
+              // P V of the tile before; that of the one before it is complete (this tile's S
+              // says so) and this tile's waits for this thread, so the parity is unambiguous
+              wait(pv, (tiles - 1) & 1);
               __syncwarp();
               ptx::tc_fence_after();
               l *= f;
 #pragma unroll 1
               for (int j = 0; j < S::DV * 2; ++j) {
-                uint32_t *y = r[1];
-                ptx::tmem_ld32(o_t + 32 * j, y);
+                uint32_t y[16];
+                ptx::tmem_ld16(o_t + 16 * j, y);
+                ptx::tmem_ld_wait(y);
+                ptx::tmem_ld_wait(y + 8);
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) ptx::tmem_ld_wait(y + e);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
-                ptx::tmem_st32(o_t + 32 * j, y);
+                for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+                ptx::tmem_st16(o_t + 16 * j, y);
               }
             }
           }
           const float base = m > neg_inf ? m * c : 0.f;
           const float cs = flip ? -c : c;
-          const f32x2 cs2 = f2(cs, cs), nb2 = f2(-base, -base);
+          const f32x2 c2 = f2(cs, cs), nb2 = f2(-base, -base);
           f32x2 la = f2(0.f, 0.f), lb = la;
-          // pass 2: weights, 32 columns in flight while 32 are computed
-          ptx::tmem_ld32(st, r[0]);
+          // pass 2, the second half of S first (it is still in registers)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t *x = r[j & 1];
+          for (int j = 1; j >= 0; --j) {
+            if (j == 0) {
+              ptx::tmem_ld32(st, x);
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) ptx::tmem_ld_wait(x + e);
-            if (j < 3) ptx::tmem_ld32(st + 32 * (j + 1), r[(j + 1) & 1]);
-            const uint32_t bits = j == 0 ? msk.x : j == 1 ? msk.y : j == 2 ? msk.z : msk.w;
+              for (int e = 0; e < 32; e += 8) ptx::tmem_ld_wait(x + e);
+            }
             uint32_t h[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               float p0, p1;
-              f2_split(fma2(f2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), cs2, nb2), p0,
+              f2_split(fma2(f2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, nb2), p0,
                        p1);
               p0 = exp2_approx(p0);
               p1 = exp2_approx(p1);
-              if (!whole) {
-                p0 = (bits >> e) & 1 ? p0 : 0.f;
-                p1 = (bits >> (e + 1)) & 1 ? p1 : 0.f;
+              if (!whole) {  // and a scale of zero makes NaN of an infinity left out
+                p0 = ((j ? msk.y : msk.x) >> e) & 1 ? p0 : 0.f;
+                p1 = ((j ? msk.y : msk.x) >> (e + 1)) & 1 ? p1 : 0.f;
               }
               if (e & 2)
                 lb = add2(lb, f2(p0, p1));
@@ -282,7 +299,7 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
                 la = add2(la, f2(p0, p1));
               h[e / 2] = pack_bf16(p0, p1);
             }
-            ptx::tmem_st16(st + 16 * j, h);
+            ptx::tmem_st16(st + 32 + 16 * j, h);  // over the second half
           }
           float l0, l1;
           f2_split(add2(la, lb), l0, l1);
@@ -290,23 +307,24 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
           ptx::tmem_st_wait();
         }
         ptx::tc_fence_before();
-        ptx::mbar_arrive(bar(S::p_full + b));
+        arrive(bar(S::p_full) + 8 * b);
       }
-      // S of a tile says that P V two (QT 1) or one (QT 2) tiles before it is complete, so a wait
-      // for the next phase cannot mistake an older one for it; the last two are waited for in turn
-      const uint32_t pv = bar(S::pv_done + (S::QT == 2 ? w : 0));
-      if (S::QT == 1 && n > 1) wait(pv, (tiles - 2) & 1, gave_up);
-      wait(pv, (tiles - 1) & 1, gave_up);
+      wait(bar(S::o_full + w), o_ph);
+      o_ph ^= 1;
       __syncwarp();
       ptx::tc_fence_after();
-      const int i = kRow * w + row;
       if (live) {
+        xch[((w * 2 + hf) << 7) + row] = l;
+        pair_sync();
+        l += xch[((w * 2 + (hf ^ 1)) << 7) + row];
+        pair_sync();  // read before the next segment writes
+        const int i = kRow * w + row;
         float *o = nullptr, *lse = nullptr;
-        if (i < s.rows) segment_out<0>(a, plan, s, blockIdx.x, i, true, &o, &lse);
+        if (i < s.rows) segment_out<0>(a, plan, s, blockIdx.x, i, hf == 0, &o, &lse);
         const bool ok = l != 0.f && !*gave_up;
         const float inv = 1.f / l;
 #pragma unroll 1
-        for (int j = 0; j < S::DV * 2; ++j) {
+        for (int j = 0; j < S::DV; ++j) {
           uint32_t r[32];
           ptx::tmem_ld32(o_t + 32 * j, r);
 #pragma unroll
@@ -319,119 +337,134 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
               v.y = ok ? __uint_as_float(r[e + 1]) * inv : 0.f;
               v.z = ok ? __uint_as_float(r[e + 2]) * inv : 0.f;
               v.w = ok ? __uint_as_float(r[e + 3]) * inv : 0.f;
-              *reinterpret_cast<float4 *>(o + 32 * j + e) = v;
+              *reinterpret_cast<float4 *>(o + hf * (S::DV * 32) + 32 * j + e) = v;
             }
           }
         }
-        if (o) *lse = ok ? (m * c + log2f(l)) * kLn2 : neg_inf;
+        if (o && hf == 0) *lse = ok ? (m * c + log2f(l)) * kLn2 : neg_inf;
       }
       ptx::tc_fence_before();
-      ptx::mbar_arrive(bar(S::o_free + w));
+      arrive(bar(S::o_free + w));
     }
-  } else if (warp < 12) {
-    // ---- K and V rows into the ring ----
-    const int lt = tid - 256;  // this thread's token of a tile
+  } else if (warp < 18) {
+    // ---- K and V rows into the ring: this thread's tokens of a tile are lt and lt + 64 ----
+    const int lt = tid - 512;
     const bool gqa = lay.kind == KAMERA_GQA;
     const __nv_bfloat16 *lk = a.pool.k + (long long)a.layer * a.pool.num_slots * lay.row_k;
     const __nv_bfloat16 *lv =
         gqa ? a.pool.v + (long long)a.layer * a.pool.num_slots * lay.row_v : lk;
     const int vrow = gqa ? lay.row_v : lay.row_k;
-    int *slots = reinterpret_cast<int *>(smem + S::slot);
     uint32_t *masks = reinterpret_cast<uint32_t *>(smem + S::mask);
-    const int piece = lt & 7, t_lo = lt >> 3;  // cp.async: 16-byte piece of a row, first token
-    const bool first_of_box = maps.box && lt % maps.box == 0;
-    uint32_t seq = 0, tile_no = 0;             // stages and tiles so far
+    const int piece = lane & 7;  // cp.async: 16-byte piece of a row
+    const int boxes = maps.box == 0 || lt % maps.box ? 0 : (maps.box == kTok ? 1 : 2);
+    uint32_t seq = 0, tile_no = 0;  // stages and tiles so far
     while (walk.next(a, plan, &s)) {
       const int n = tiles_of(s.tok0, s.tok1, kTok), a0 = s.tok0 / kTok;
       const int kcol = gqa ? s.kvh * lay.hd : 0;
       const int vcol = gqa ? kcol : s.half * (S::DV * 64);
-      auto slot_at = [&](int i) -> int {  // of this thread's token of tile i
-        const int tok = (a0 + i) * kTok + lt;  // below 2^31: a tile with a token starts below it
+      auto slot_at = [&](int i, int k) -> int {  // of token lt + 64 k of tile i
+        const int tok = (a0 + i) * kTok + lt + 64 * k;  // below 2^31: the tile starts below it
         if (tok < s.tok0 || tok >= s.tok1) return -1;
         return slot_in(a, load_page(a, s.lead, tok), tok);
       };
-      // The next stages: `chunks` chunks from column `col` of a tile's rows. slot: this thread's
-      // token's; tile: the tile's number, for the other tokens' slots; whole: every token is in.
+      // The next stages: `chunks` chunks from column `col` of a tile's rows, whose slots are this
+      // thread's s0 and s1 and the other lanes'; whole: every token is in.
       auto issue = [&](const void *map, const __nv_bfloat16 *rows, int row, int col, int chunks,
-                       int slot, uint32_t tile, bool whole) {
-        if (maps.box && whole) {
-          for (int u = 0; u < chunks / S::UC; ++u, ++seq) {
-            const int st = seq % S::NST;
-            wait(bar(S::empty + st), (seq / S::NST + 1) & 1, gave_up);
-            const uint32_t dst = sb + S::ring + st * S::kStage + lt * 128;
-            if (first_of_box) {
-              ptx::mbar_arrive_expect_tx(bar(S::full + st), S::UC * maps.box * 128);
-#pragma unroll
-              for (int k = 0; k < S::UC; ++k)
-                ptx::tma_2d(dst + k * kChunk, map, col + (u * S::UC + k) * 64, slot,
-                            bar(S::full + st));
-            } else {
-              ptx::mbar_arrive(bar(S::full + st));
-            }
-          }
-          return;
-        }
-        int sl[kTok / 16];
-#pragma unroll
-        for (int j = 0; j < kTok / 16; ++j) sl[j] = slots[(tile % kSlots) * kTok + t_lo + 16 * j];
+                       int s0, int s1, bool whole) {
         for (int u = 0; u < chunks / S::UC; ++u, ++seq) {
           const int st = seq % S::NST;
-          wait(bar(S::empty + st), (seq / S::NST + 1) & 1, gave_up);
-          const uint32_t dst = sb + S::ring + st * S::kStage;
-          const __nv_bfloat16 *src = rows + col + u * S::UC * 64 + 8 * piece;
+          const uint32_t dst = sb + S::ring + st * S::kStage, full = bar(S::full) + 8 * st;
+          wait(bar(S::empty) + 8 * st, (seq / S::NST + 1) & 1);
+          if (__any_sync(0xffffffffu, dead)) {
+            dead = true;
+            continue;
+          }
+          if (maps.box && whole) {
+            if (boxes) {
+              ptx::mbar_arrive_expect_tx(full, boxes * S::UC * maps.box * 128);
 #pragma unroll
-          for (int j = 0; j < kTok / 16; ++j) {
-            const int t = t_lo + 16 * j;
-            const __nv_bfloat16 *p = sl[j] >= 0 ? src + (long long)sl[j] * row : a.pool.k;
+              for (int k = 0; k < S::UC; ++k) {
+                const int x = col + (u * S::UC + k) * 64;
+                ptx::tma_2d(dst + k * kChunk + lt * 128, map, x, s0, full);
+                if (boxes == 2) ptx::tma_2d(dst + k * kChunk + (lt + 64) * 128, map, x, s1, full);
+              }
+            } else {
+              arrive(full);
+            }
+            continue;
+          }
+          const __nv_bfloat16 *src = rows + col + u * S::UC * 64 + 8 * piece;
+#pragma unroll 4
+          for (int j = 0; j < 16; ++j) {  // four of this warp's 64 tokens at a time
+            const int q = 4 * j + (lane >> 3);
+            const int sl = __shfl_sync(0xffffffffu, j < 8 ? s0 : s1, q & 31);
+            const int t = (lt & 32) + (q & 31) + (j < 8 ? 0 : 64);
+            const __nv_bfloat16 *p = sl >= 0 ? src + (long long)sl * row : a.pool.k;
 #pragma unroll
             for (int k = 0; k < S::UC; ++k)
               ptx::cp_async16(dst + k * kChunk + t * 128 + ((piece ^ (t & 7)) << 4),
-                              sl[j] >= 0 ? p + k * 64 : p, sl[j] >= 0 ? 16u : 0u);
+                              sl >= 0 ? p + k * 64 : p, sl >= 0 ? 16u : 0u);
           }
-          ptx::cp_async_mbar_arrive(bar(S::full + st));
+          ptx::cp_async_mbar_arrive(full);
         }
       };
-      int slot = slot_at(0), slot_k = 0, slot_v = 0;  // of the next tile, of K's and of V's
-      bool whole_k = false, whole_v = false;
-      uint32_t tile_k = 0, tile_v = 0;
+      int n0 = slot_at(0, 0), n1 = slot_at(0, 1);  // of the next tile
+      int k0 = 0, k1 = 0;                          // of the last K tile
+      bool whole = false;
       auto load_k = [&](int i) {
-        slot_k = slot;
-        tile_k = tile_no++;
-        if (i + 1 < n) slot = slot_at(i + 1);  // ahead of its use
-        slots[(tile_k % kSlots) * kTok + lt] = slot_k;
-        const uint32_t bits = __ballot_sync(0xffffffffu, slot_k >= 0);
-        const int mk = tile_k % kMasks;
+        k0 = n0;
+        k1 = n1;
+        if (i + 1 < n) {  // ahead of its use
+          n0 = slot_at(i + 1, 0);
+          n1 = slot_at(i + 1, 1);
+        }
+        const int mk = tile_no++ % kMasks;
+        const uint32_t b0 = __ballot_sync(0xffffffffu, k0 >= 0);
+        const uint32_t b1 = __ballot_sync(0xffffffffu, k1 >= 0);
         if (lane == 0) {
-          masks[4 * mk + (warp & 3)] = bits;
-          ptx::mbar_arrive(bar(S::mk_full + mk));
+          masks[4 * mk + (warp & 1)] = b0;
+          masks[4 * mk + 2 + (warp & 1)] = b1;
+          arrive(bar(S::mk_full) + 8 * mk);
         }
         __syncwarp();
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        asm volatile("bar.sync 1, 64;" ::: "memory");
         const uint4 m = *reinterpret_cast<const uint4 *>(masks + 4 * mk);
-        whole_k = (m.x & m.y & m.z & m.w) == 0xffffffffu;
-        issue(&maps.k, lk, lay.row_k, kcol, S::DK, slot_k, tile_k, whole_k);
-      };
-      auto keep = [&]() {  // V of this tile comes later
-        slot_v = slot_k;
-        tile_v = tile_k;
-        whole_v = whole_k;
-      };
-      auto load_v = [&](int sv, uint32_t tv, bool wv) {
-        issue(&maps.v, lv, vrow, vcol, S::DV, sv, tv, wv);
+        whole = (m.x & m.y & m.z & m.w) == 0xffffffffu;
+        issue(&maps.k, lk, lay.row_k, kcol, S::DK, k0, k1, whole);
       };
       load_k(0);
       for (int i = 0; i < n; ++i) {
-        keep();
+        const int v0 = k0, v1 = k1;  // V of this tile may come after K of the next
+        const bool vw = whole;
         if (S::QT == 1 && i + 1 < n) load_k(i + 1);
-        load_v(slot_v, tile_v, whole_v);
+        issue(&maps.v, lv, vrow, vcol, S::DV, v0, v1, vw);
         if (S::QT == 2 && i + 1 < n) load_k(i + 1);
       }
     }
     ptx::cp_async_wait_all();
-  } else if (warp == 12) {
-    // ---- MMAs, one thread. Issuing one takes a few instructions only: the descriptors of a
-    // tile's steps differ by constants ----
-    if (ptx::elect_one()) {
+  } else {
+    // ---- MMAs (warp 18) and Q (warp 19), one thread each. QT 2: S and P V of the two query tiles
+    // in turn, so that the tensor core works on one during the softmax of the other; QT 1: S of a
+    // tile before P V of the one before it. Issuing an MMA takes a few instructions only: the
+    // descriptors of a tile's steps differ by constants ----
+    // Q of a segment, once S of the one before is complete. Rows of a copy past the block's are
+    // other requests' or zero: their results go nowhere
+    uint32_t segs = 0;
+    auto load_q = [&]() {
+      if (segs) wait(bar(S::q_empty), (segs - 1) & 1);
+      ++segs;
+      if (dead) return;
+      ptx::mbar_arrive_expect_tx(bar(S::q_full), s.own ? maps.own_bytes : maps.group_bytes);
+      const int y = maps.q_step ? 0 : s.kvh * a.hpk;
+      const int z = maps.q_step ? s.r0 * a.hq + s.row0 : s.r0 + s.row0 / a.hpk;
+      for (int c = 0; c < S::DK; ++c)
+        ptx::tma_3d(sb + S::q + c * S::QT * kChunk, s.own ? &maps.q_own : &maps.q_group, c * 64, y,
+                    z, bar(S::q_full));
+    };
+    if (warp == 19) {
+      if (ptx::elect_one())
+        while (walk.next(a, plan, &s)) load_q();
+    } else if (ptx::elect_one()) {
       constexpr uint32_t id_s = 1u << 4 | 1u << 7 | 1u << 10 | (kTok >> 3) << 17 | (kRow >> 4) << 24;
       // V is MN-major
       constexpr uint32_t id_o =
@@ -439,8 +472,13 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
       constexpr int ku = S::DK / S::UC, vu = S::DV / S::UC;  // stages of a K and a V tile
       const uint32_t ring = sb + S::ring;
       Place<S::NST> kp, vp;
+      uint32_t tiles = 0;                                // QT 1: tile k has S buffer k % 2
       uint32_t q_ph = 0, p_ph = 0, o_ph = 0, o_any = 0;  // a bit for each S buffer, query tile
       const uint32_t q0 = desc_k(sb + S::q);             // [chunk][query tile][128 rows]
+      auto landed = [&](const Place<S::NST> &at) {
+        wait(bar(S::full) + 8 * at.st, at.ph);
+        ptx::fence_proxy_async_smem();
+      };
       // S of query tile t into TMEM buffer b against the K tile at kp; Ends: bit 0 the first,
       // bit 1 the last reader of its stages
       auto mma_s = [&](auto t, uint32_t b, auto ends) {
@@ -448,10 +486,8 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
         Place<S::NST> at = kp;
 #pragma unroll
         for (int u = 0; u < ku; ++u) {
-          if (ends.v & 1) {
-            wait(bar(S::full) + 8 * at.st, at.ph, gave_up);
-            ptx::fence_proxy_async_smem();
-          }
+          if (ends.v & 1) landed(at);
+          if (dead) return;
           const uint32_t k = desc_k(ring + at.st * S::kStage);
 #pragma unroll
           for (int x = 0; x < S::UC * 4; ++x)
@@ -467,39 +503,40 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
         if (ends.v & 2) kp = at;
       };
       // O of query tile t (+)= P in buffer b times the V tile at vp
-      auto mma_o = [&](auto t, uint32_t b, bool first_tile, auto ends) {
+      auto mma_o = [&](auto t, uint32_t b, bool first_tile, bool last_tile, auto ends) {
+        // P of tokens 0-63 in columns 32-63 of S, of 64-127 in 96-127
         const uint32_t p = tmem + b * 128, d = tmem + S::o_col + t.v * 128;
         Place<S::NST> at = vp;
-        if (ends.v & 1) {  // V is there long before P
-          wait(bar(S::full) + 8 * at.st, at.ph, gave_up);
-          ptx::fence_proxy_async_smem();
-        }
+        if (ends.v & 1) landed(at);  // before P is, as a rule
         if (first_tile) {  // the last segment's output has been read
           if ((o_any >> t.v) & 1) {
-            wait(bar(S::o_free + t.v), (o_ph >> t.v) & 1, gave_up);
+            wait(bar(S::o_free + t.v), (o_ph >> t.v) & 1);
             o_ph ^= 1u << t.v;
           }
           o_any |= 1u << t.v;
         }
-        wait(bar(S::p_full) + 8 * b, (p_ph >> b) & 1, gave_up);
+        wait(bar(S::p_full) + 8 * b, (p_ph >> b) & 1);
         p_ph ^= 1u << b;
+        if (dead) return;
         ptx::tc_fence_after();
 #pragma unroll
         for (int u = 0; u < vu; ++u) {
-          if ((ends.v & 1) && u > 0) {
-            wait(bar(S::full) + 8 * at.st, at.ph, gave_up);
-            ptx::fence_proxy_async_smem();
-          }
+          if ((ends.v & 1) && u > 0) landed(at);
+          if (dead) return;
           const uint32_t v = desc_mn(ring + at.st * S::kStage);
 #pragma unroll
           for (int x = 0; x < kTok / 16; ++x)
-            ptx::mma_bf16_ta(d + u * S::UC * 64, p + 8 * x, desc(v + x * (2048 >> 4)), id_o,
+            ptx::mma_bf16_ta(d + u * S::UC * 64, p + 32 + 8 * x + (x < 4 ? 0 : 32), desc(v + x * (2048 >> 4)), id_o,
                              x ? 1u : (first_tile ? 0u : 1u));
           if (ends.v & 2) ptx::mma_commit(bar(S::empty) + 8 * at.st);
           at.advance(1);
         }
         ptx::mma_commit(bar(S::pv_done + t.v));
+        if (last_tile) ptx::mma_commit(bar(S::o_full + t.v));
         if (ends.v & 2) vp = at;
+      };
+      auto q_done = [&]() {
+        if (!dead) ptx::mma_commit(bar(S::q_empty));
       };
       constexpr Int<0> t0;
       constexpr Int<1> t1, first;
@@ -511,43 +548,46 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
         // QT 2: K0 V0 K1 V1 ...; QT 1: K0 K1 V0 K2 V1 ... V(n-1)
         vp = kp;
         vp.advance(S::QT == 1 && n > 1 ? 2 * ku : ku);
-        wait(bar(S::q_full), q_ph, gave_up);
+        wait(bar(S::q_full), q_ph);
         q_ph ^= 1;
         ptx::fence_proxy_async_smem();
-        if (S::QT == 2 && s.rows > kRow) {
-          mma_s(t0, 0, first);
-          mma_s(t1, 1, last);
-          for (int i = 0; i + 1 < n; ++i) {
-            kp.advance(vu);
-            mma_o(t0, 0, i == 0, first);
+        if (S::QT == 2) {
+          if (s.rows > kRow) {
             mma_s(t0, 0, first);
-            mma_o(t1, 1, i == 0, last);
             mma_s(t1, 1, last);
-            vp.advance(ku);
-          }
-          ptx::mma_commit(bar(S::q_empty));
-          mma_o(t0, 0, n == 1, first);
-          mma_o(t1, 1, n == 1, last);
-        } else if (S::QT == 2) {
-          mma_s(t0, 0, only);
-          for (int i = 0; i + 1 < n; ++i) {
-            kp.advance(vu);
-            mma_o(t0, 0, i == 0, only);
+            for (int i = 0; i + 1 < n; ++i) {
+              kp.advance(vu);
+              mma_o(t0, 0, i == 0, false, first);
+              mma_s(t0, 0, first);
+              mma_o(t1, 1, i == 0, false, last);
+              mma_s(t1, 1, last);
+              vp.advance(ku);
+            }
+            q_done();
+            mma_o(t0, 0, n == 1, true, first);
+            mma_o(t1, 1, n == 1, true, last);
+          } else {
             mma_s(t0, 0, only);
-            vp.advance(ku);
+            for (int i = 0; i + 1 < n; ++i) {
+              kp.advance(vu);
+              mma_o(t0, 0, i == 0, false, only);
+              mma_s(t0, 0, only);
+              vp.advance(ku);
+            }
+            q_done();
+            mma_o(t0, 0, n == 1, true, only);
           }
-          ptx::mma_commit(bar(S::q_empty));
-          mma_o(t0, 0, n == 1, only);
         } else {
-          mma_s(t0, 0, only);
+          mma_s(t0, tiles & 1, only);
           for (int i = 0; i + 1 < n; ++i) {
             if (i > 0) kp.advance(vu);
-            mma_s(t0, (i + 1) & 1, only);
-            mma_o(t0, i & 1, i == 0, only);
+            mma_s(t0, (tiles + i + 1) & 1, only);
+            mma_o(t0, (tiles + i) & 1, i == 0, false, only);
             if (i + 2 < n) vp.advance(ku);
           }
-          ptx::mma_commit(bar(S::q_empty));
-          mma_o(t0, (n - 1) & 1, n == 1, only);
+          q_done();
+          mma_o(t0, (tiles + n - 1) & 1, n == 1, true, only);
+          tiles += n;
         }
         kp = vp;  // the segment's end
       }
@@ -555,29 +595,17 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
       if (!ptx::mbar_wait(bar(S::last), 0, kWaitNs)) *gave_up = 1;
     }
     __syncwarp();
-  } else if (warp == 13) {
-    // ---- Q, one thread. Rows of a copy past the block's are other requests' or zero: their
-    // results go nowhere ----
-    if (ptx::elect_one()) {
-      const int hpk = a.hpk;
-      uint32_t segs = 0;
-      while (walk.next(a, plan, &s)) {
-        if (segs) wait(bar(S::q_empty), (segs - 1) & 1, gave_up);
-        ++segs;
-        ptx::mbar_arrive_expect_tx(bar(S::q_full), s.own ? maps.own_bytes : maps.group_bytes);
-        const int y = maps.q_step ? 0 : s.kvh * hpk;
-        const int z = maps.q_step ? s.r0 * a.hq + s.row0 : s.r0 + s.row0 / hpk;
-        for (int c = 0; c < S::DK; ++c)
-          ptx::tma_3d(sb + S::q + c * S::QT * kChunk, s.own ? &maps.q_own : &maps.q_group, c * 64,
-                      y, z, bar(S::q_full));
-      }
-    }
-    __syncwarp();
   }
   ptx::tc_fence_before();
   __syncthreads();
-  if (tid == 0 && *gave_up) atomicOr(a.status, KAMERA_DEVICE_TIMEOUT);
-  if (warp == 12) ptx::tmem_dealloc(tmem, 512);
+  if (*gave_up) {  // copies and MMAs in flight end long before this
+    if (tid == 0) atomicOr(a.status, KAMERA_DEVICE_TIMEOUT);
+    const uint64_t t0 = ptx::globaltimer();
+    while (ptx::globaltimer() - t0 < 1000000) {
+    }
+    __syncthreads();
+  }
+  if (warp == 18) ptx::tmem_dealloc(tmem, 512);
 }
 
 template <class S>
