@@ -273,34 +273,41 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
           const float cs = flip ? -c : c;
           const f32x2 c2 = f2(cs, cs), nb2 = f2(-base, -base);
           f32x2 la = f2(0.f, 0.f), lb = la;
-          // pass 2, the second half of S first (it is still in registers)
+          // pass 2, the second half of S first (it is still in registers). Two copies of the loop:
+          // a test of the mask at each weight would cost as much as the weight
+          auto weights = [&](auto masked) {
 #pragma unroll
-          for (int j = 1; j >= 0; --j) {
-            if (j == 0) {
-              ptx::tmem_ld32(st, x);
+            for (int j = 1; j >= 0; --j) {
+              if (j == 0) {
+                ptx::tmem_ld32(st, x);
 #pragma unroll
-              for (int e = 0; e < 32; e += 8) ptx::tmem_ld_wait(x + e);
-            }
-            uint32_t h[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float p0, p1;
-              f2_split(fma2(f2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, nb2), p0,
-                       p1);
-              p0 = exp2_approx(p0);
-              p1 = exp2_approx(p1);
-              if (!whole) {  // and a scale of zero makes NaN of an infinity left out
-                p0 = ((j ? msk.y : msk.x) >> e) & 1 ? p0 : 0.f;
-                p1 = ((j ? msk.y : msk.x) >> (e + 1)) & 1 ? p1 : 0.f;
+                for (int e = 0; e < 32; e += 8) ptx::tmem_ld_wait(x + e);
               }
-              if (e & 2)
-                lb = add2(lb, f2(p0, p1));
-              else
-                la = add2(la, f2(p0, p1));
-              h[e / 2] = pack_bf16(p0, p1);
+              uint32_t h[16];
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float p0, p1;
+                f2_split(fma2(f2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, nb2), p0,
+                         p1);
+                p0 = exp2_approx(p0);
+                p1 = exp2_approx(p1);
+                if (masked.v) {
+                  p0 = ((j ? msk.y : msk.x) >> e) & 1 ? p0 : 0.f;
+                  p1 = ((j ? msk.y : msk.x) >> (e + 1)) & 1 ? p1 : 0.f;
+                }
+                if (e & 2)
+                  lb = add2(lb, f2(p0, p1));
+                else
+                  la = add2(la, f2(p0, p1));
+                h[e / 2] = pack_bf16(p0, p1);
+              }
+              ptx::tmem_st16(st + 32 + 16 * j, h);  // over the second half
             }
-            ptx::tmem_st16(st + 32 + 16 * j, h);  // over the second half
-          }
+          };
+          if (whole)
+            weights(Int<0>());
+          else
+            weights(Int<1>());
           float l0, l1;
           f2_split(add2(la, lb), l0, l1);
           l += l0 + l1;
@@ -347,8 +354,10 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
       arrive(bar(S::o_free + w));
     }
   } else if (warp < 18) {
-    // ---- K and V rows into the ring: this thread's tokens of a tile are lt and lt + 64 ----
-    const int lt = tid - 512;
+    // ---- K and V rows into the ring. A warp brings 64 tokens of each tile, a lane two of them:
+    // t0 and t0 + 32. Copies by tensor map are issued by one thread of the warp, which stands in
+    // for the others' arrivals ----
+    const int half = warp & 1, t0 = 64 * half + lane;
     const bool gqa = lay.kind == KAMERA_GQA;
     const __nv_bfloat16 *lk = a.pool.k + (long long)a.layer * a.pool.num_slots * lay.row_k;
     const __nv_bfloat16 *lv =
@@ -356,49 +365,72 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
     const int vrow = gqa ? lay.row_v : lay.row_k;
     uint32_t *masks = reinterpret_cast<uint32_t *>(smem + S::mask);
     const int piece = lane & 7;  // cp.async: 16-byte piece of a row
-    const int boxes = maps.box == 0 || lt % maps.box ? 0 : (maps.box == kTok ? 1 : 2);
-    uint32_t seq = 0, tile_no = 0;  // stages and tiles so far
+    const int box = maps.box, boxes = box == kTok ? 1 - half : (box ? 64 / box : 0);
+    Place<S::NST> at;       // the next stage
+    uint32_t tile_no = 0;   // tiles so far
     while (walk.next(a, plan, &s)) {
       const int n = tiles_of(s.tok0, s.tok1, kTok), a0 = s.tok0 / kTok;
       const int kcol = gqa ? s.kvh * lay.hd : 0;
       const int vcol = gqa ? kcol : s.half * (S::DV * 64);
-      auto slot_at = [&](int i, int k) -> int {  // of token lt + 64 k of tile i
-        const int tok = (a0 + i) * kTok + lt + 64 * k;  // below 2^31: the tile starts below it
-        if (tok < s.tok0 || tok >= s.tok1) return -1;
-        return slot_in(a, load_page(a, s.lead, tok), tok);
+      auto token = [&](int i, int k) {  // below 2^31: the tile starts below it
+        const int tok = (a0 + i) * kTok + t0 + 32 * k;
+        return tok >= s.tok0 && tok < s.tok1 ? tok : -1;
+      };
+      auto page_at = [&](int i, int k) {
+        const int tok = token(i, k);
+        return tok >= 0 ? load_page(a, s.lead, tok) : 0;
       };
       // The next stages: `chunks` chunks from column `col` of a tile's rows, whose slots are this
-      // thread's s0 and s1 and the other lanes'; whole: every token is in.
+      // lane's s0 and s1 and the other lanes'; whole: every token is in.
       auto issue = [&](const void *map, const __nv_bfloat16 *rows, int row, int col, int chunks,
                        int s0, int s1, bool whole) {
-        for (int u = 0; u < chunks / S::UC; ++u, ++seq) {
-          const int st = seq % S::NST;
-          const uint32_t dst = sb + S::ring + st * S::kStage, full = bar(S::full) + 8 * st;
-          wait(bar(S::empty) + 8 * st, (seq / S::NST + 1) & 1);
+        if (box && whole) {
+          int y[8];  // first slots of the copies
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            y[k] = __shfl_sync(0xffffffffu, k * box < 32 ? s0 : s1, (k * box) & 31);
+          if (ptx::elect_one()) {
+            Place<S::NST> to = at;
+            for (int u = 0; u < chunks / S::UC; ++u) {
+              const uint32_t full = bar(S::full) + 8 * to.st;
+              uint32_t dst = sb + S::ring + to.st * S::kStage + half * 64 * 128;
+              wait(bar(S::empty) + 8 * to.st, to.ph ^ 1);
+              if (dead) break;
+              if (boxes) {
+                ptx::mbar_arrive_n(full, 31);
+                ptx::mbar_arrive_expect_tx(full, boxes * box * S::UC * 128);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  if (k < boxes) {
+#pragma unroll
+                    for (int c = 0; c < S::UC; ++c)
+                      ptx::tma_2d(dst + c * kChunk, map, col + (u * S::UC + c) * 64, y[k], full);
+                    dst += box * 128;
+                  }
+                }
+              } else {
+                ptx::mbar_arrive_n(full, 32);
+              }
+              to.advance(1);
+            }
+          }
+          __syncwarp();
+          at.advance(chunks / S::UC);
+          return;
+        }
+        for (int u = 0; u < chunks / S::UC; ++u) {
+          const uint32_t dst = sb + S::ring + at.st * S::kStage, full = bar(S::full) + 8 * at.st;
+          wait(bar(S::empty) + 8 * at.st, at.ph ^ 1);
+          at.advance(1);
           if (__any_sync(0xffffffffu, dead)) {
             dead = true;
-            continue;
-          }
-          if (maps.box && whole) {
-            if (boxes) {
-              ptx::mbar_arrive_expect_tx(full, boxes * S::UC * maps.box * 128);
-#pragma unroll
-              for (int k = 0; k < S::UC; ++k) {
-                const int x = col + (u * S::UC + k) * 64;
-                ptx::tma_2d(dst + k * kChunk + lt * 128, map, x, s0, full);
-                if (boxes == 2) ptx::tma_2d(dst + k * kChunk + (lt + 64) * 128, map, x, s1, full);
-              }
-            } else {
-              arrive(full);
-            }
             continue;
           }
           const __nv_bfloat16 *src = rows + col + u * S::UC * 64 + 8 * piece;
 #pragma unroll 4
           for (int j = 0; j < 16; ++j) {  // four of this warp's 64 tokens at a time
-            const int q = 4 * j + (lane >> 3);
+            const int q = 4 * j + (lane >> 3), t = 64 * half + q;
             const int sl = __shfl_sync(0xffffffffu, j < 8 ? s0 : s1, q & 31);
-            const int t = (lt & 32) + (q & 31) + (j < 8 ? 0 : 64);
             const __nv_bfloat16 *p = sl >= 0 ? src + (long long)sl * row : a.pool.k;
 #pragma unroll
             for (int k = 0; k < S::UC; ++k)
@@ -408,22 +440,23 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
           ptx::cp_async_mbar_arrive(full);
         }
       };
-      int n0 = slot_at(0, 0), n1 = slot_at(0, 1);  // of the next tile
-      int k0 = 0, k1 = 0;                          // of the last K tile
+      int p0 = page_at(0, 0), p1 = page_at(0, 1);  // of the next tile, not looked at yet
+      int k0 = 0, k1 = 0;                          // slots of the last K tile
       bool whole = false;
       auto load_k = [&](int i) {
-        k0 = n0;
-        k1 = n1;
+        const int tok0 = token(i, 0), tok1 = token(i, 1);
+        k0 = tok0 >= 0 ? slot_in(a, p0, tok0) : -1;
+        k1 = tok1 >= 0 ? slot_in(a, p1, tok1) : -1;
         if (i + 1 < n) {  // ahead of its use
-          n0 = slot_at(i + 1, 0);
-          n1 = slot_at(i + 1, 1);
+          p0 = page_at(i + 1, 0);
+          p1 = page_at(i + 1, 1);
         }
         const int mk = tile_no++ % kMasks;
         const uint32_t b0 = __ballot_sync(0xffffffffu, k0 >= 0);
         const uint32_t b1 = __ballot_sync(0xffffffffu, k1 >= 0);
         if (lane == 0) {
-          masks[4 * mk + (warp & 1)] = b0;
-          masks[4 * mk + 2 + (warp & 1)] = b1;
+          masks[4 * mk + 2 * half] = b0;
+          masks[4 * mk + 2 * half + 1] = b1;
           arrive(bar(S::mk_full) + 8 * mk);
         }
         __syncwarp();

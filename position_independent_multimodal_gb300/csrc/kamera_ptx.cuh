@@ -76,6 +76,10 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// Arrive n times.
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
 // Arrive once when every cp.async this thread issued so far has completed (the arrival is not
 // counted in advance: the barrier's expected count includes it).
 __device__ __forceinline__ void cp_async_mbar_arrive(uint32_t bar) {
