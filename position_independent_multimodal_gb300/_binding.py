@@ -368,61 +368,65 @@ def kamera_decode_attention(handle: Handle, pool: Pool, layer: int, q: torch.Ten
                                          _stream(stream)), "kamera_decode_attention")
 
 
-def _need(what: str, t, dtype, device: int, contiguous: bool = True) -> None:
-    """Raise ValueError unless ``t`` is a tensor of ``dtype`` on CUDA device ``device``."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.get_device() != device or \
-            (contiguous and not t.is_contiguous()):
-        raise ValueError(f"{what} must be a{' contiguous' if contiguous else ''} {dtype} tensor "
-                         f"on the current CUDA device")
+def _reject(what: str, dtype, contiguous: bool = True) -> None:
+    raise ValueError(f"{what} must be a{' contiguous' if contiguous else ''} {dtype} tensor on the "
+                     "current CUDA device")
 
 
-def _pool_device(pool: Pool) -> int:
-    """The device of a pool's tensors, which has to be the current one: kernels are launched
-    there, on the current stream unless another is given."""
-    dev = pool.k.get_device()
+def _need(what: str, t: torch.Tensor, dtype, dev: int) -> int:
+    """The address of a contiguous tensor of ``dtype`` on CUDA device ``dev``."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _reject(what, dtype)
+    return t.data_ptr()
+
+
+def _pool_c(handle: Handle, pool: Pool) -> tuple[kamera_pool, int]:
+    """The checked C struct of a pool, and its device, which has to be the current one: kernels
+    are launched there, on the current stream unless another is given."""
+    k, v, pt = pool.k, pool.v, pool.page_table
+    dev = k.get_device()
     if dev < 0 or dev != torch.cuda.current_device():
         raise ValueError("the pool must be on the current CUDA device")
-    _need("pool.k", pool.k, torch.bfloat16, dev)
-    if pool.v is not None:
-        _need("pool.v", pool.v, torch.bfloat16, dev)
-    _need("pool.page_table", pool.page_table, torch.int32, dev, contiguous=False)
-    if pool.page_table.dim() != 2 or pool.page_table.stride(1) != 1:
-        raise ValueError("pool.page_table must be [num_reqs][pt_stride]")
-    return dev
-
-
-def _pool_shape(handle: Handle, pool: Pool) -> None:
-    """Raise ValueError unless the pool's tensors have the handle's layers and row widths."""
     c = handle._c
     gqa = c.kind == KAMERA_GQA
-    row = c.num_kv_heads * c.head_dim if gqa else c.latent_dim + c.rope_dim
-    want = (c.num_layers, pool.num_slots, row)
-    if tuple(pool.k.shape) != want or (pool.v is not None and tuple(pool.v.shape) != want) or \
-            (pool.v is None) == gqa:
+    want = (c.num_layers, pool.num_slots,
+            c.num_kv_heads * c.head_dim if gqa else c.latent_dim + c.rope_dim)
+    if k.shape != want or (v is None) == gqa or (gqa and v.shape != want):
         raise ValueError(f"the pool's tensors must be {want}, K and V for GQA, K alone for MLA")
+    if pt.dtype is not torch.int32 or pt.get_device() != dev:
+        _reject("pool.page_table", torch.int32, contiguous=False)
+    st = pt.stride()
+    if len(st) != 2 or st[1] != 1:
+        raise ValueError("pool.page_table must be [num_reqs][pt_stride]")
+    return kamera_pool(_need("pool.k", k, torch.bfloat16, dev),
+                       _need("pool.v", v, torch.bfloat16, dev) if gqa else None, want[1],
+                       pt.data_ptr(), pt.shape[0], st[0]), dev
 
 
-def _items(what: str, t: torch.Tensor, dev: int) -> None:
-    _need(what, t, torch.int32, dev)
-    if t.dim() != 2 or t.shape[1] != 3:
-        raise ValueError(f"{what} must be [n][3]")
+def _stream_on(stream, dev: int) -> int:
+    """The stream's handle; the current stream of the (current) device without one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
 
 
-def _bytes(t: Optional[torch.Tensor], dev: int) -> int:
+def _bytes(t: Optional[torch.Tensor], dev: int) -> tuple[Optional[int], int]:
+    """A workspace's address and size."""
     if t is None:
-        return 0
+        return None, 0
     if t.get_device() != dev or not t.is_contiguous():
         raise ValueError("the workspace must be a contiguous tensor on the current CUDA device")
-    return t.numel() * t.element_size()
+    return t.data_ptr(), t.nbytes
 
 
 def _heads(what: str, t: torch.Tensor, dev: int, tokens: int, heads: int, width: int) -> int:
     """The token stride of bf16 [tokens][heads][width] whose heads lie side by side."""
-    _need(what, t, torch.bfloat16, dev, contiguous=False)
-    if tuple(t.shape) != (tokens, heads, width) or t.stride(2) != 1 or \
-            (heads > 1 and t.stride(1) != width):
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev:
+        _reject(what, torch.bfloat16, contiguous=False)
+    st = t.stride()
+    if t.shape != (tokens, heads, width) or st[2] != 1 or (heads > 1 and st[1] != width):
         raise ValueError(f"{what} must be [{tokens}][{heads}][{width}] with contiguous heads")
-    return t.stride(0) if tokens > 1 else max(t.stride(0), heads * width)
+    return st[0] if tokens > 1 else max(st[0], heads * width)
 
 
 def kamera_append(handle: Handle, pool: Pool, layer: int, q: Optional[torch.Tensor],
@@ -434,43 +438,42 @@ def kamera_append(handle: Handle, pool: Pool, layer: int, q: Optional[torch.Tens
     ``k`` [T][H_kv][head_dim] (MLA: [T][1][latent + rope]) and ``v`` [T][H_kv][head_dim] (MLA:
     None) into the pool's layer, for tokens ``tok`` of page-table rows ``req`` (int32 [T]) at
     ``positions`` (int64 [T], or [T][3] under M-RoPE). Token strides are free."""
-    dev = _pool_device(pool)
-    _pool_shape(handle, pool)
+    p, dev = _pool_c(handle, pool)
     c = handle._c
     gqa = c.kind == KAMERA_GQA
-    T = int(k.shape[0])
     dk, hk = (c.head_dim, c.num_kv_heads) if gqa else (c.latent_dim + c.rope_dim, 1)
-    t = kamera_new_tokens(k=k.data_ptr(), num_tokens=T, eps=float(eps))
-    t.k_stride = _heads("k", k, dev, T, hk, dk)
+    T, hq = k.shape[0], 0
+    k_stride = _heads("k", k, dev, T, hk, dk)
     if (v is None) == gqa:
         raise ValueError("v is given for GQA and None for MLA")
-    if gqa:
-        t.v, t.v_stride = v.data_ptr(), _heads("v", v, dev, T, hk, dk)
+    v_ptr, v_stride = (v.data_ptr(), _heads("v", v, dev, T, hk, dk)) if gqa else (None, 0)
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out are given together")
+    q_ptr = q_stride = out_ptr = out_stride = 0
     if q is not None:
-        t.num_q_heads = int(q.shape[1])
-        t.q, t.q_stride = q.data_ptr(), _heads("q", q, dev, T, t.num_q_heads, dk)
-        t.q_out = q_out.data_ptr()
-        t.q_out_stride = _heads("q_out", q_out, dev, T, t.num_q_heads, dk)
-    for name, w, n in (("q_weight", q_weight, dk), ("k_weight", k_weight,
-                                                    dk if gqa else c.latent_dim)):
-        if w is not None:
-            _need(name, w, torch.bfloat16, dev)
-            if w.numel() != n:
-                raise ValueError(f"{name} must have {n} elements")
-            setattr(t, name, w.data_ptr())
-    for name, x, dtype, n in (("positions", positions, torch.int64,
-                               T * (3 if any(c.mrope_section) else 1)),
-                              ("req", req, torch.int32, T), ("tok", tok, torch.int32, T)):
-        _need(name, x, dtype, dev)
-        if x.numel() != n:
-            raise ValueError(f"{name} must have {n} elements")
-        setattr(t, name, x.data_ptr())
-    _need("status", status, torch.int32, dev)
-    p = pool.c()
-    _check(lib().kamera_append(handle.ptr, ctypes.byref(p), int(layer), ctypes.byref(t),
-                               status.data_ptr(), _stream(stream)), "kamera_append")
+        hq = q.shape[1]
+        q_ptr, q_stride = q.data_ptr(), _heads("q", q, dev, T, hq, dk)
+        out_ptr, out_stride = q_out.data_ptr(), _heads("q_out", q_out, dev, T, hq, dk)
+    qw = kw = None
+    if q_weight is not None:
+        qw = _need("q_weight", q_weight, torch.bfloat16, dev)
+    if k_weight is not None:
+        kw = _need("k_weight", k_weight, torch.bfloat16, dev)
+    if (qw and q_weight.numel() != dk) or \
+            (kw and k_weight.numel() != (dk if gqa else c.latent_dim)):
+        raise ValueError("a weight must have one element for each column that is normed")
+    sec = c.mrope_section
+    if positions.numel() != T * (3 if sec[0] or sec[1] or sec[2] else 1) or \
+            req.numel() != T or tok.numel() != T:
+        raise ValueError(f"positions, req and tok must be of {T} tokens")
+    t = kamera_new_tokens(q_ptr, k.data_ptr(), v_ptr, qw, kw,
+                          _need("positions", positions, torch.int64, dev),
+                          _need("req", req, torch.int32, dev),
+                          _need("tok", tok, torch.int32, dev), out_ptr, q_stride, k_stride,
+                          v_stride, out_stride, T, hq, eps, 0)
+    _check(lib().kamera_append(handle.ptr, ctypes.byref(p), layer, ctypes.byref(t),
+                               _need("status", status, torch.int32, dev),
+                               _stream_on(stream, dev)), "kamera_append")
 
 
 def kamera_page_workspace(handle: Handle, num_slots: int, num_items: int) -> int:
@@ -479,20 +482,24 @@ def kamera_page_workspace(handle: Handle, num_slots: int, num_items: int) -> int
     return int(lib().kamera_page_workspace(handle.ptr, int(num_slots), int(num_items)))
 
 
-def _page_call(name: str, handle: Handle, pool: Pool, items: torch.Tensor, refs: torch.Tensor,
-               workspace, status: torch.Tensor, stream) -> None:
-    dev = _pool_device(pool)
-    _pool_shape(handle, pool)
-    _items("items", items, dev)
-    _need("refs", refs, torch.int32, dev)
-    _need("status", status, torch.int32, dev)
+def _refs(pool: Pool, handle: Handle, refs: torch.Tensor, dev: int) -> int:
     if refs.numel() * handle._c.page_size != pool.num_slots:
         raise ValueError("refs must have one count for each page of the pool")
-    p = pool.c()
-    args = [handle.ptr, ctypes.byref(p), items.data_ptr(), int(items.shape[0]), refs.data_ptr()]
+    return _need("refs", refs, torch.int32, dev)
+
+
+def _page_call(name: str, handle: Handle, pool: Pool, items: torch.Tensor, refs: torch.Tensor,
+               workspace, status: torch.Tensor, stream) -> None:
+    p, dev = _pool_c(handle, pool)
+    shape = items.shape
+    if len(shape) != 2 or shape[1] != 3:
+        raise ValueError("items must be [n][3]")
+    args = [handle.ptr, ctypes.byref(p), _need("items", items, torch.int32, dev), shape[0],
+            _refs(pool, handle, refs, dev)]
     if workspace is not False:
-        args += [_ptr(workspace), _bytes(workspace, dev)]
-    _check(getattr(lib(), name)(*args, status.data_ptr(), _stream(stream)), name)
+        args += _bytes(workspace, dev)
+    _check(getattr(lib(), name)(*args, _need("status", status, torch.int32, dev),
+                                _stream_on(stream, dev)), name)
 
 
 def kamera_fork(handle: Handle, pool: Pool, items: torch.Tensor, refs: torch.Tensor,
@@ -517,32 +524,26 @@ def kamera_compact(handle: Handle, pool: Pool, refs: torch.Tensor, num_live: tor
                    workspace: torch.Tensor, status: torch.Tensor, stream=None) -> None:
     """Live pages drawn together below the number of live pages, which goes to ``num_live``
     (int32 [1])."""
-    dev = _pool_device(pool)
-    _pool_shape(handle, pool)
-    _need("refs", refs, torch.int32, dev)
-    _need("num_live", num_live, torch.int32, dev)
-    _need("status", status, torch.int32, dev)
-    if refs.numel() * handle._c.page_size != pool.num_slots:
-        raise ValueError("refs must have one count for each page of the pool")
-    p = pool.c()
-    _check(lib().kamera_compact(handle.ptr, ctypes.byref(p), refs.data_ptr(),
-                                num_live.data_ptr(), _ptr(workspace), _bytes(workspace, dev),
-                                status.data_ptr(), _stream(stream)), "kamera_compact")
+    p, dev = _pool_c(handle, pool)
+    _check(lib().kamera_compact(handle.ptr, ctypes.byref(p), _refs(pool, handle, refs, dev),
+                                _need("num_live", num_live, torch.int32, dev),
+                                *_bytes(workspace, dev),
+                                _need("status", status, torch.int32, dev),
+                                _stream_on(stream, dev)), "kamera_compact")
 
 
 def kamera_copy_pages(handle: Handle, pool: Pool, src: torch.Tensor, dst: torch.Tensor,
                       status: torch.Tensor, stream=None) -> None:
     """Page ``src[i]`` onto page ``dst[i]`` (int32 on the device), every layer, K and V."""
-    dev = _pool_device(pool)
-    _pool_shape(handle, pool)
-    for name, x in (("src", src), ("dst", dst), ("status", status)):
-        _need(name, x, torch.int32, dev)
-    if src.numel() != dst.numel():
+    p, dev = _pool_c(handle, pool)
+    n = src.numel()
+    if n != dst.numel():
         raise ValueError("src and dst must have as many pages")
-    p = pool.c()
-    _check(lib().kamera_copy_pages(handle.ptr, ctypes.byref(p), src.data_ptr(), dst.data_ptr(),
-                                   src.numel(), status.data_ptr(), _stream(stream)),
-           "kamera_copy_pages")
+    _check(lib().kamera_copy_pages(handle.ptr, ctypes.byref(p),
+                                   _need("src", src, torch.int32, dev),
+                                   _need("dst", dst, torch.int32, dev), n,
+                                   _need("status", status, torch.int32, dev),
+                                   _stream_on(stream, dev)), "kamera_copy_pages")
 
 
 def kamera_prefix_attention_workspace(handle: Handle, num_reqs: int, num_q_heads: int) -> int:
@@ -559,28 +560,24 @@ def kamera_prefix_attention(handle: Handle, pool: Pool, layer: int, q: torch.Ten
     """Decode attention of ``q`` bf16 [R][H_q][Dk] over pool layer ``layer``, requests
     ``group_start[g]`` .. ``group_start[g + 1] - 1`` sharing their first ``prefix_len[g]``
     tokens, into ``out`` bf16 [R][H_q][Dv] and ``lse`` float32 [R][H_q]."""
-    dev = _pool_device(pool)
-    _pool_shape(handle, pool)
+    p, dev = _pool_c(handle, pool)
     c = handle._c
     dk, dv = (c.head_dim, c.head_dim) if c.kind == KAMERA_GQA else \
         (c.latent_dim + c.rope_dim, c.latent_dim)
-    for name, x, dtype in (("q", q, torch.bfloat16), ("out", out, torch.bfloat16),
-                           ("lse", lse, torch.float32), ("group_start", group_start, torch.int32),
-                           ("prefix_len", prefix_len, torch.int32),
-                           ("ctx_len", ctx_len, torch.int32), ("status", status, torch.int32)):
-        _need(name, x, dtype, dev)
-    R, hq = int(q.shape[0]), int(q.shape[1])
-    if tuple(q.shape) != (R, hq, dk) or tuple(out.shape) != (R, hq, dv) or \
-            tuple(lse.shape) != (R, hq) or ctx_len.numel() != R or \
-            group_start.numel() != prefix_len.numel() + 1:
+    R, hq, _ = shape = q.shape
+    G = prefix_len.numel()
+    if shape != (R, hq, dk) or out.shape != (R, hq, dv) or lse.shape != (R, hq) or \
+            ctx_len.numel() != R or group_start.numel() != G + 1:
         raise ValueError(f"q [R][H_q][{dk}], out [R][H_q][{dv}], lse [R][H_q], ctx_len [R], "
                          "group_start [G + 1] and prefix_len [G] are wanted")
-    p = pool.c()
     _check(lib().kamera_prefix_attention(
-        handle.ptr, ctypes.byref(p), int(layer), q.data_ptr(), R, hq, group_start.data_ptr(),
-        prefix_len.data_ptr(), prefix_len.numel(), ctx_len.data_ptr(), float(scale),
-        out.data_ptr(), lse.data_ptr(), _ptr(workspace), _bytes(workspace, dev),
-        status.data_ptr(), _stream(stream)), "kamera_prefix_attention")
+        handle.ptr, ctypes.byref(p), layer, _need("q", q, torch.bfloat16, dev), R, hq,
+        _need("group_start", group_start, torch.int32, dev),
+        _need("prefix_len", prefix_len, torch.int32, dev), G,
+        _need("ctx_len", ctx_len, torch.int32, dev), scale,
+        _need("out", out, torch.bfloat16, dev), _need("lse", lse, torch.float32, dev),
+        *_bytes(workspace, dev), _need("status", status, torch.int32, dev),
+        _stream_on(stream, dev)), "kamera_prefix_attention")
 
 
 def kamera_rope_phases(handle: Handle, d_deltas: torch.Tensor, d_out: torch.Tensor,
