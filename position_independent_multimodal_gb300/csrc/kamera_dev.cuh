@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "kamera.h"
 
 namespace kamera {
@@ -589,6 +591,24 @@ struct FormArgs {
   float *work;              // 2 * max(T, W) * k floats per problem
 };
 
+// Launch of a kernel that starts while the one before it in the stream still runs: it waits for
+// that one's results itself (ptx::wait_for_previous).
+template <class... P, class... A>
+inline cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem,
+                                cudaStream_t s, A &&...args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
 // Kernel launchers.
 size_t form_patch_workspace(long long n, int T, int W, int k);  // kamera_form.cu
 size_t form_patch_smem(int k);  // the largest of the patch-forming kernels
@@ -638,7 +658,7 @@ cudaError_t prepare_prefix_tc();
 cudaError_t launch_prefix_tc(const PrefixArgs &a, cudaStream_t s);
 PrefixClass prefix_thin_class(const DevLayout &l);                  // kamera_prefix_thin.cu
 cudaError_t prepare_prefix_thin();
-cudaError_t launch_prefix_thin(const PrefixArgs &a, cudaStream_t s);
+cudaError_t launch_prefix_thin(const PrefixArgs &a, bool beside, cudaStream_t s);
 cudaError_t launch_rope_phases(const FreqQ64 &f, int npairs, const long long *deltas, int n,
                                float *out, cudaStream_t s);
 

@@ -4,6 +4,11 @@
 // over tokens [0, ctx) of each request; the softmax over a union of token sets is the parts'
 // softmaxes weighted by their masses, o = sum_i e^(lse_i - lse) o_i, lse = log sum_i e^(lse_i).
 //
+// The kernels of a call start early, each while the one before it still runs, and wait for what
+// they read: the attention kernels for the plan, the merge for the attention kernels. Where both
+// of these run, the thin one works beside the wide one's last CTAs (it needs the plan alone, which
+// is complete when every CTA of the wide one has let it start) and waits for it at its end.
+//
 // prefix_plan_kernel lists the groups and requests with tokens and numbers their units
 // (kamera_prefix.cuh), the attention kernels work the units off, prefix_merge_kernel joins the
 // parts. This file has the attention kernel for any layout (CUDA cores); GQA with head_dim 64 or
@@ -12,6 +17,7 @@
 #include <mutex>
 
 #include "kamera_prefix.cuh"
+#include "kamera_ptx.cuh"
 #include "kamera_smem.cuh"
 
 namespace kamera {
@@ -58,6 +64,7 @@ __device__ __forceinline__ void plan_scan(long long (&x)[N], long long (&total)[
 // One CTA: checks the arguments, lists the groups and requests that have units, and finds each
 // worker's first block. Bound: the latency of its few dependent steps.
 __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_constant__ PrefixArgs a) {
+  ptx::launch_dependents();
   const PrefixPlan p = prefix_plan(a.shape, a.ws, a.n_reqs, a.hq, a.dv);
   __shared__ int near_start[kPlanNear + 1], near_lead[kPlanNear];
   __shared__ long long near_u0[2][kPlanNear], near_r[kPlanNear];
@@ -281,6 +288,8 @@ __global__ void __launch_bounds__(kThr) prefix_gen_kernel(const __grid_constant_
   const int chunks = dv >> 3, lanes = kThr / chunks;
   const int c = tid % chunks, tl = tid / chunks;
   const bool gqa = lay.kind == KAMERA_GQA;
+  ptx::launch_dependents();
+  ptx::wait_for_previous();
   SegmentWalk<1> walk;
   walk.start(a, plan, blockIdx.x);
   Segment s;
@@ -459,6 +468,7 @@ __global__ void __launch_bounds__(kThr) prefix_merge_kernel(const __grid_constan
   const unsigned rh = w / slices;
   const int col = (int)(w - rh * slices) * kCols, r = (int)(rh / (unsigned)a.hq);
   const float neg_inf = -__int_as_float(0x7f800000);
+  ptx::wait_for_previous();
   const bool have[2] = {p.req_pu0[r] >= 0, p.req_ou0[r] >= 0};
   if (!p.req_state[r]) return;
   const int size = p.req_size[r];
@@ -579,18 +589,18 @@ cudaError_t launch_prefix_attention(const PrefixArgs &a, cudaStream_t s) {
   const int hpk = a.hpk;
   if (prefix_tc_layout(a.lay)) {
     // blocks can be wide only where the largest group would be, thin only where one request is
-    if ((long long)a.n_reqs * hpk > a.shape.wide_rows) e = launch_prefix_tc(a, s);
-    if (e == cudaSuccess && hpk <= a.shape.wide_rows) e = launch_prefix_thin(a, s);
+    const bool wide = (long long)a.n_reqs * hpk > a.shape.wide_rows;
+    if (wide) e = launch_prefix_tc(a, s);
+    if (e == cudaSuccess && hpk <= a.shape.wide_rows) e = launch_prefix_thin(a, wide, s);
   } else {
-    prefix_gen_kernel<<<a.shape.cls[1].n, kThr, gen_plan(a.dk, a.dv).total, s>>>(a);
-    e = cudaGetLastError();
+    e = launch_early(prefix_gen_kernel, dim3(a.shape.cls[1].n), kThr, gen_plan(a.dk, a.dv).total, s,
+                     a);
   }
   if (e != cudaSuccess) return e;
   const int slices = (a.dv + kCols - 1) / kCols;
   const long long warps = (long long)a.n_reqs * a.hq * slices;
-  prefix_merge_kernel<<<(unsigned)((warps + kThr / 32 - 1) / (kThr / 32)), kThr, 0, s>>>(a,
-                                                                                         slices);
-  return cudaGetLastError();
+  return launch_early(prefix_merge_kernel, dim3((unsigned)((warps + kThr / 32 - 1) / (kThr / 32))),
+                      kThr, 0, s, a, slices);
 }
 
 }  // namespace kamera

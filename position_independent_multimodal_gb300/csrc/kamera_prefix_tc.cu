@@ -168,6 +168,8 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
   ptx::tc_fence_after();
   const uint32_t tmem = misc[0];
 
+  ptx::wait_for_previous();  // the plan
+  ptx::launch_dependents();  // who starts from here on finds the plan complete
   SegmentWalk<0> walk;
   walk.start(a, plan, blockIdx.x);
   Segment s;
@@ -706,8 +708,7 @@ cudaError_t launch(const PrefixArgs &a, cudaStream_t s) {
     m.own_bytes = S::DK * 128 * hpk;
   }
   if (!ok) return cudaErrorInvalidValue;
-  prefix_tc_kernel<S><<<a.shape.cls[0].n, kThr, S::total, s>>>(a, m);
-  return cudaGetLastError();
+  return launch_early(prefix_tc_kernel<S>, dim3(a.shape.cls[0].n), kThr, S::total, s, a, m);
 }
 
 }  // namespace

@@ -71,7 +71,8 @@ __device__ __forceinline__ uint32_t at16(int row, int piece) {
 }
 
 template <class T>
-__global__ void __launch_bounds__(T::WARPS * 32, 1) prefix_thin_kernel(const __grid_constant__ PrefixArgs a) {
+__global__ void __launch_bounds__(T::WARPS * 32, 1) prefix_thin_kernel(const __grid_constant__ PrefixArgs a,
+                                                                         int beside) {
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int D = T::D, kTok = T::kTok;
   const PrefixPlan plan = prefix_plan(a.shape, a.ws, a.n_reqs, a.hq, a.dv);
@@ -83,6 +84,10 @@ __global__ void __launch_bounds__(T::WARPS * 32, 1) prefix_thin_kernel(const __g
   const __nv_bfloat16 *lv = a.pool.v + (long long)a.layer * a.pool.num_slots * lay.row_v;
   const float neg_inf = -__int_as_float(0x7f800000);
   const float c = a.scale * kLog2e;
+
+  // `beside`: the kernel before this one is that of the wide blocks, else the plan
+  if (!beside) ptx::wait_for_previous();
+  ptx::launch_dependents();
 
   // ---- loads: one tile ahead of its issue the page entry, NST - 1 tiles ahead of its use. The
   // segments go on through a queue: at most NST + 1 are between the loads and the products ----
@@ -261,6 +266,7 @@ __global__ void __launch_bounds__(T::WARPS * 32, 1) prefix_thin_kernel(const __g
     }
   }
   cp_wait<0>();
+  if (beside) ptx::wait_for_previous();  // who waits for this kernel waits for that one too
 }
 
 // ---------------------------------------------------------------------------------------
@@ -286,7 +292,8 @@ __device__ __forceinline__ uint32_t mla16(int row, int piece) {
   return row * ThinMla::kRow + ((piece ^ (row & 7)) << 4);
 }
 
-__global__ void __launch_bounds__(ThinMla::kThr, 1) prefix_thin_mla_kernel(const __grid_constant__ PrefixArgs a) {
+__global__ void __launch_bounds__(ThinMla::kThr, 1) prefix_thin_mla_kernel(const __grid_constant__ PrefixArgs a,
+                                                                         int beside) {
   extern __shared__ __align__(128) unsigned char smem[];
   using M = ThinMla;
   const PrefixPlan plan = prefix_plan(a.shape, a.ws, a.n_reqs, a.hq, a.dv);
@@ -299,6 +306,9 @@ __global__ void __launch_bounds__(ThinMla::kThr, 1) prefix_thin_mla_kernel(const
   float *wsum = reinterpret_cast<float *>(smem + M::wsum);
   const float neg_inf = -__int_as_float(0x7f800000);
   const float c = a.scale * kLog2e;
+
+  if (!beside) ptx::wait_for_previous();
+  ptx::launch_dependents();
 
   // ---- loads: slots two tiles ahead, rows one tile ahead ----
   Segment *queue = reinterpret_cast<Segment *>(smem + M::queue);
@@ -506,6 +516,7 @@ __global__ void __launch_bounds__(ThinMla::kThr, 1) prefix_thin_mla_kernel(const
     }
   }
   cp_wait<0>();
+  if (beside) ptx::wait_for_previous();
 }
 
 }  // namespace
@@ -536,14 +547,15 @@ cudaError_t prepare_prefix_thin() {
   return e;
 }
 
-cudaError_t launch_prefix_thin(const PrefixArgs &a, cudaStream_t s) {
+cudaError_t launch_prefix_thin(const PrefixArgs &a, bool beside, cudaStream_t s) {
+  const int b = beside;
   if (a.lay.kind == KAMERA_MLA)
-    prefix_thin_mla_kernel<<<kSms, ThinMla::kThr, ThinMla::total, s>>>(a);
-  else if (a.lay.hd == 128)
-    prefix_thin_kernel<Thin128><<<kSms, Thin128::WARPS * 32, Thin128::total, s>>>(a);
-  else
-    prefix_thin_kernel<Thin64><<<kSms, Thin64::WARPS * 32, Thin64::total, s>>>(a);
-  return cudaGetLastError();
+    return launch_early(prefix_thin_mla_kernel, dim3(kSms), ThinMla::kThr, ThinMla::total, s, a, b);
+  if (a.lay.hd == 128)
+    return launch_early(prefix_thin_kernel<Thin128>, dim3(kSms), Thin128::WARPS * 32,
+                        Thin128::total, s, a, b);
+  return launch_early(prefix_thin_kernel<Thin64>, dim3(kSms), Thin64::WARPS * 32, Thin64::total, s,
+                      a, b);
 }
 
 }  // namespace kamera
