@@ -409,7 +409,7 @@ kamera_status kamera_decode_attention(const kamera_handle *handle, const kamera_
  * k_weight : bf16 [head_dim] (MLA: [latent_dim]), or NULL likewise.
  * positions: int64 [num_tokens], or [num_tokens][3] = (t, h, w) for M-RoPE layouts.
  * req, tok : int32 [num_tokens]: the page-table row and logical token of each. A negative req
- *            marks a row of padding: nothing of it is read but req and tok, nothing written.
+ *            marks a row of padding: what its other inputs hold does not matter, nothing is written.
  * q_out    : bf16, heads of token t at q_out + t * q_out_stride; may be q itself (with the same
  *            stride), and overlaps none of the inputs otherwise.
  * All device memory; q, k, v, weights and q_out 16-byte aligned, positions 8, req and tok 4.

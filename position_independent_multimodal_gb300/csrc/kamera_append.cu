@@ -6,13 +6,14 @@
 //   MLA: the latent c_KV normed with w_k and the k_pe band rotated into the row; the queries
 //        (absorbed form) keep their latent part and turn their rope band.
 //
-// One CTA of 256 threads per kTok tokens. It first builds the tokens' phase table (each (token,
-// pair) once, by the exact Q0.64 range reduction of the other kernels; every head of the token
-// reads it) and resolves their slots. Then W = 2^ceil(log2(band / 16)) lanes take one (token,
-// head) item: a lane holds the two 8-column chunks of a column unit, which are closed under
-// pairing, so the norm is one shuffle reduction over the W lanes and the rotation needs no
-// exchange. Sums of squares, the norm and the rotation are float32; each output is rounded to
-// bf16 once.
+// One CTA of 256 threads per kTok tokens. W = 2^ceil(log2(band / 16)) lanes take one (token, head)
+// item: a lane holds the two 8-column chunks of a column unit, which are closed under pairing, so
+// the norm is one shuffle reduction over the W lanes and the rotation needs no exchange. A group
+// of W lanes stays with one token and takes several of its heads at a time, so that their loads
+// are in flight together, before the phases and slots are known, and its phases are read once.
+// The CTA computes the tokens' phases (each (token, pair) once, by the exact Q0.64 range reduction
+// of the other kernels) and resolves their slots while the first loads run. Sums of squares, the
+// norm and the rotation are float32; each output is rounded to bf16 once.
 // Bound: HBM (every byte is read and written once) at many tokens, latency at few.
 #include "kamera_dev.cuh"
 
@@ -21,7 +22,7 @@ namespace kamera {
 namespace {
 
 constexpr int kThr = 256;
-constexpr int kBatch = 4;  // items a group of lanes has in flight
+constexpr int kBatch = 4;  // items a group of lanes (rows a warp) has in flight
 
 __device__ __forceinline__ float sum_sq8(const float *x) {
   float s = 0.f;
@@ -50,10 +51,43 @@ __global__ void __launch_bounds__(kThr) append_kernel(const __grid_constant__ Ap
   __shared__ long long slots[kTok];  // -1: no slot, K and V are not written
   __shared__ int live[kTok];         // 0: padding or a bad token, nothing is written
   const DevLayout &lay = a.lay;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long t0 = (long long)blockIdx.x * kTok;
   const int nt = (int)min((long long)kTok, a.T - t0);
   const int np = lay.npairs;
+  const bool gqa = lay.kind == KAMERA_GQA;
+
+  // rotated items: the query heads, then the key bands, of this group's token
+  const int band = lay.rope_d, units = band >> 4;
+  int w = 1;
+  while (w < units) w <<= 1;
+  const int q = tid & (w - 1), groups = kThr / w / kTok;  // groups of lanes per token
+  const int sub = tid / w, tk = sub / groups, h_first = sub - tk * groups;
+  const int per_tok = a.hq + (gqa ? lay.H : 1);
+  const bool neox = lay.style == KAMERA_ROPE_NEOX_HALF;
+  const int ca = neox ? 8 * q : 16 * q, cb = neox ? ca + (band >> 1) : ca + 8;
+  const bool mine = q < units && tk < nt;
+  const long long tok = t0 + tk;
+  // column of head h in the queries' or keys' row
+  auto column = [&](int h) {
+    return gqa ? (h < a.hq ? h : h - a.hq) * lay.hd : (h < a.hq ? h * lay.row_k : 0) + lay.latent;
+  };
+  uint4 ra[kBatch], rb[kBatch];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int h = h0 + j * groups;
+      ra[j] = rb[j] = make_uint4(0, 0, 0, 0);
+      if (mine && h < per_tok) {
+        const __nv_bfloat16 *src =
+            (h < a.hq ? a.q + tok * a.q_stride : a.k + tok * a.k_stride) + column(h);
+        ra[j] = ld16(src + ca);
+        rb[j] = ld16(src + cb);
+      }
+    }
+  };
+  load(h_first);
+
   for (int e = tid; e < nt * np; e += kThr) {
     const int t = e / np, i = e - t * np;
     const int axis = lay.mrope ? mrope_axis(lay, i) : 0;
@@ -61,73 +95,42 @@ __global__ void __launch_bounds__(kThr) append_kernel(const __grid_constant__ Ap
     cs[e] = rope_phase(a.freq.q[i], __ldg(a.positions + (t0 + t) * stride + axis));
   }
   if (tid < nt) {
-    const int req = __ldg(a.req + t0 + tid), tok = __ldg(a.tok + t0 + tid);
+    const int req = __ldg(a.req + t0 + tid), at = __ldg(a.tok + t0 + tid);
     const bool padding = req < 0;
-    const bool bad = !padding && (req >= a.pool.num_reqs || tok < 0 ||
-                                  tok >= (long long)a.pool.pt_stride * lay.page_size);
+    const bool bad = !padding && (req >= a.pool.num_reqs || at < 0 ||
+                                  at >= (long long)a.pool.pt_stride * lay.page_size);
     if (bad) atomicOr(a.status, KAMERA_DEVICE_BAD_ITEM);
     live[tid] = !padding && !bad;
-    slots[tid] = padding || bad ? -1 : slot_of(a.pool, lay.page_size, req, tok, a.status);
+    slots[tid] = padding || bad ? -1 : slot_of(a.pool, lay.page_size, req, at, a.status);
   }
   __syncthreads();
 
-  const bool gqa = lay.kind == KAMERA_GQA;
   const long long layer_k = (long long)a.layer * a.pool.num_slots * lay.row_k;
-  // rotated items: the query heads, then the key bands, of each token
-  const int band = lay.rope_d, units = band >> 4;
-  int w = 1;
-  while (w < units) w <<= 1;
-  const int sub = tid / w, q = tid & (w - 1), nsub = kThr / w;
-  const int n_k = gqa ? lay.H : 1;
-  const int per_tok = a.hq + n_k, items = per_tok * nt;
-  const bool neox = lay.style == KAMERA_ROPE_NEOX_HALF;
-  const int ca = neox ? 8 * q : 16 * q, cb = neox ? ca + (band >> 1) : ca + 8;
-  const bool mine = q < units;
-  for (int it0 = sub; it0 < items + sub; it0 += nsub * kBatch) {  // whole warps iterate alike
-    uint4 ra[kBatch], rb[kBatch];
-    __nv_bfloat16 *dst[kBatch];
-    int tk[kBatch];
-    bool isq[kBatch];
+  const long long slot = tk < nt ? slots[tk] : -1;
+  const bool write_q = tk < nt && live[tk];
+  const bool norms = gqa && (a.q_weight || a.k_weight);
+  const float2 *c = cs + tk * np;
+  float2 ph[8];  // NeoX pairs 8 q ..; interleaved pairs of chunk a, then of chunk b: the same ones
+#pragma unroll
+  for (int e = 0; e < 8; ++e) ph[e] = mine ? c[8 * q + e] : make_float2(1.f, 0.f);
+  for (int base = 0; base < per_tok; base += groups * kBatch) {  // whole warps iterate alike
+    if (base > 0) load(base + h_first);
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const int it = it0 + j * nsub;
-      dst[j] = nullptr;
-      tk[j] = 0;
-      isq[j] = false;
-      ra[j] = rb[j] = make_uint4(0, 0, 0, 0);
-      if (it >= items || !mine) continue;
-      const int t = it / per_tok, h = it - t * per_tok;
-      tk[j] = t;
-      const __nv_bfloat16 *src;
-      if (h < a.hq) {
-        if (!live[t]) continue;
-        isq[j] = true;
-        const int off = gqa ? h * lay.hd : h * lay.row_k + lay.latent;
-        src = a.q + (t0 + t) * a.q_stride + off;
-        dst[j] = a.q_out + (t0 + t) * a.q_out_stride + off;
-      } else {
-        if (slots[t] < 0) continue;
-        const int off = gqa ? (h - a.hq) * lay.hd : lay.latent;
-        src = a.k + (t0 + t) * a.k_stride + off;
-        dst[j] = a.pool.k + layer_k + slots[t] * lay.row_k + off;
-      }
-      ra[j] = ld16(src + ca);
-      rb[j] = ld16(src + cb);
-    }
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
+      const int h = base + h_first + j * groups;
+      const bool isq = h < a.hq;
       float xa[8], xb[8];
       unpack8(ra[j], xa);
       unpack8(rb[j], xb);
-      const __nv_bfloat16 *wt = gqa ? (isq[j] ? a.q_weight : a.k_weight) : nullptr;
-      if (gqa && (a.q_weight || a.k_weight)) {  // every lane takes part in the reduction
+      if (norms) {  // every lane takes part in the reduction
+        const __nv_bfloat16 *wt = isq ? a.q_weight : a.k_weight;
         auto mean_sq = [&]() {
           float s = sum_sq8(xa) + sum_sq8(xb);
           for (int o = w >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
           return s / (float)band;
         };
         float mean = mean_sq() + a.eps;
-        const float f = wt ? norm_scale(mean) : 1.f;
+        const float f = wt && h < per_tok ? norm_scale(mean) : 1.f;
         if (__any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -148,46 +151,45 @@ __global__ void __launch_bounds__(kThr) append_kernel(const __grid_constant__ Ap
           }
         }
       }
-      if (!dst[j]) continue;
-      const float2 *c = cs + tk[j] * np;
+      if (!mine || h >= per_tok || (isq ? !write_q : slot < 0)) continue;
       if (neox) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) rot_pair(xa[e], xb[e], c[8 * q + e]);
+        for (int e = 0; e < 8; ++e) rot_pair(xa[e], xb[e], ph[e]);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
-          rot_pair(xa[e], xa[e + 1], c[8 * q + (e >> 1)]);
-          rot_pair(xb[e], xb[e + 1], c[8 * q + 4 + (e >> 1)]);
+          rot_pair(xa[e], xa[e + 1], ph[e >> 1]);
+          rot_pair(xb[e], xb[e + 1], ph[4 + (e >> 1)]);
         }
       }
-      st16(dst[j] + ca, pack8_rn(xa));
-      st16(dst[j] + cb, pack8_rn(xb));
+      __nv_bfloat16 *dst = (isq ? a.q_out + tok * a.q_out_stride
+                                : a.pool.k + layer_k + slot * lay.row_k) +
+                           column(h);
+      st16(dst + ca, pack8_rn(xa));
+      st16(dst + cb, pack8_rn(xb));
     }
   }
 
-  if (gqa) {  // V rows, byte for byte
-    const int nc = lay.row_v >> 3;
-    __nv_bfloat16 *pv = a.pool.v + (long long)a.layer * a.pool.num_slots * lay.row_v;
-    for (int e = tid; e < nt * nc; e += kThr) {
-      const int t = e / nc, c = e - t * nc;
-      if (slots[t] >= 0)
-        st16(pv + slots[t] * lay.row_v + 8 * c, ld16(a.v + (t0 + t) * a.v_stride + 8 * c));
+  if (gqa) {  // V rows, byte for byte: kThr / kTok threads to a token
+    const int nc = lay.row_v >> 3, t = tid / (kThr / kTok);
+    if (t >= nt || slots[t] < 0) return;
+    const __nv_bfloat16 *src = a.v + (t0 + t) * a.v_stride;
+    __nv_bfloat16 *dst =
+        a.pool.v + ((long long)a.layer * a.pool.num_slots + slots[t]) * lay.row_v;
+    for (int e = tid % (kThr / kTok); e < nc; e += kThr / kTok * kBatch) {
+      uint4 v[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (e + j * (kThr / kTok) < nc) v[j] = ld16(src + 8 * (e + j * (kThr / kTok)));
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (e + j * (kThr / kTok) < nc) st16(dst + 8 * (e + j * (kThr / kTok)), v[j]);
     }
     return;
   }
-  // MLA: the queries' latent parts, byte for byte
+  // MLA: the latent rows, a warp to a token
   const int nc = lay.latent >> 3;
-  if (a.q_out != a.q || a.q_out_stride != a.q_stride) {
-    for (int e = tid; e < nt * a.hq * nc; e += kThr) {
-      const int t = e / (a.hq * nc), r = e - t * (a.hq * nc), h = r / nc, c = r - h * nc;
-      if (live[t])
-        st16(a.q_out + (t0 + t) * a.q_out_stride + h * lay.row_k + 8 * c,
-             ld16(a.q + (t0 + t) * a.q_stride + h * lay.row_k + 8 * c));
-    }
-  }
-  // and the latent row, a warp to a token
-  const int lane = tid & 31;
-  for (int t = tid >> 5; t < nt; t += kThr / 32) {
+  for (int t = warp; t < nt; t += kThr / 32) {
     if (slots[t] < 0) continue;
     const __nv_bfloat16 *src = a.k + (t0 + t) * a.k_stride;
     __nv_bfloat16 *dst = a.pool.k + layer_k + slots[t] * lay.row_k;
@@ -210,7 +212,7 @@ __global__ void __launch_bounds__(kThr) append_kernel(const __grid_constant__ Ap
       if (f != 1.f) mean = mean_sq() + a.eps * f * f;
       r = rsqrtf(mean);
     }
-    for (int c = lane; c < nc; c += 32) {
+    for (int c = lane; c < nc; c += 32) {  // read again, from L1
       uint4 v = ld16(src + 8 * c);
       if (a.k_weight) {
         float x[8], wv[8];
@@ -223,12 +225,42 @@ __global__ void __launch_bounds__(kThr) append_kernel(const __grid_constant__ Ap
       st16(dst + 8 * c, v);
     }
   }
+  // and the queries' latent parts, byte for byte: rows of nc chunks dealt to the warps
+  if (a.q_out == a.q) return;
+  const int rows = nt * a.hq;
+  for (int i0 = warp; i0 < rows; i0 += kThr / 32 * kBatch) {
+    for (int c = lane; c < nc; c += 64) {
+      uint4 v[kBatch][2];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = i0 + j * (kThr / 32), t = i / a.hq;
+        const __nv_bfloat16 *src = a.q + (t0 + t) * a.q_stride + (i - t * a.hq) * lay.row_k;
+        if (i < rows && live[t]) {
+          v[j][0] = ld16(src + 8 * c);
+          if (c + 32 < nc) v[j][1] = ld16(src + 8 * (c + 32));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = i0 + j * (kThr / 32), t = i / a.hq;
+        __nv_bfloat16 *dst = a.q_out + (t0 + t) * a.q_out_stride + (i - t * a.hq) * lay.row_k;
+        if (i < rows && live[t]) {
+          st16(dst + 8 * c, v[j][0]);
+          if (c + 32 < nc) st16(dst + 8 * (c + 32), v[j][1]);
+        }
+      }
+    }
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t s) {
-  append_kernel<1><<<(unsigned)a.T, kThr, 0, s>>>(a);
+  // a token to a CTA while that gives every SM no more than a few CTAs, else four
+  if (a.T <= 4 * kSms)
+    append_kernel<1><<<(unsigned)a.T, kThr, 0, s>>>(a);
+  else
+    append_kernel<4><<<(unsigned)((a.T + 3) / 4), kThr, 0, s>>>(a);
   return cudaGetLastError();
 }
 
