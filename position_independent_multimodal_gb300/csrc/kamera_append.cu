@@ -16,13 +16,125 @@
 // norm and the rotation are float32; each output is rounded to bf16 once.
 // Bound: HBM (every byte is read and written once) at many tokens, latency at few.
 #include "kamera_dev.cuh"
+#include "kamera_smem.cuh"
 
 namespace kamera {
 
 namespace {
 
 constexpr int kThr = 256;
-constexpr int kBatch = 4;  // items a group of lanes (rows a warp) has in flight
+constexpr int kBatch = 4;  // query heads a group of lanes (rows a warp) has in flight
+
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 neg2(f32x2 a) { return a ^ 0x8000000080000000ull; }
+
+// The first and second members of a unit's eight pairs, two pairs to a register. NeoX-half: chunk
+// a holds the first members, chunk b the second; interleaved: neighbours, pairs 0-3 in chunk a.
+struct Unit {
+  f32x2 a[4], b[4];
+};
+
+template <bool kNeox>
+__device__ __forceinline__ Unit unpack_unit(const uint4 &ca, const uint4 &cb) {
+  const uint32_t x[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
+  Unit u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (kNeox) {
+      u.a[i] = bf2_to_f2(x[i]);
+      u.b[i] = bf2_to_f2(x[4 + i]);
+    } else {
+      u.a[i] = f2(__uint_as_float(x[2 * i] << 16), __uint_as_float(x[2 * i + 1] << 16));
+      u.b[i] = f2(__uint_as_float(x[2 * i] & 0xFFFF0000u),
+                  __uint_as_float(x[2 * i + 1] & 0xFFFF0000u));
+    }
+  }
+  return u;
+}
+
+template <bool kNeox>
+__device__ __forceinline__ void pack_unit(const Unit &u, uint4 *ca, uint4 *cb) {
+  uint32_t x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (kNeox) {
+      x[i] = f2_to_bf2(u.a[i]);
+      x[4 + i] = f2_to_bf2(u.b[i]);
+    } else {
+      float a0, a1, b0, b1;
+      f2_split(u.a[i], a0, a1);
+      f2_split(u.b[i], b0, b1);
+      x[2 * i] = pack2_rn(a0, b0);
+      x[2 * i + 1] = pack2_rn(a1, b1);
+    }
+  }
+  *ca = make_uint4(x[0], x[1], x[2], x[3]);
+  *cb = make_uint4(x[4], x[5], x[6], x[7]);
+}
+
+// Rotation with the weights folded in: a' = a (w_a cos) - b (w_b sin), b' = b (w_b cos) + a (w_a
+// sin); the norm's factor multiplies the results.
+struct Turn {
+  f32x2 ac[4], bs[4], bc[4], as[4];  // bs negated
+};
+
+template <bool kNeox>
+__device__ __forceinline__ Turn make_turn(const float2 *ph, const __nv_bfloat16 *w, int ca, int cb) {
+  Unit u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) u.a[i] = u.b[i] = f2(1.f, 1.f);
+  if (w)
+    u = unpack_unit<kNeox>(__ldg(reinterpret_cast<const uint4 *>(w + ca)),
+                           __ldg(reinterpret_cast<const uint4 *>(w + cb)));
+  Turn t;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p0 = ph[2 * i], p1 = ph[2 * i + 1];
+    const f32x2 c = f2(p0.x, p1.x), s = f2(p0.y, p1.y);
+    t.ac[i] = mul2(u.a[i], c);
+    t.as[i] = mul2(u.a[i], s);
+    t.bc[i] = mul2(u.b[i], c);
+    t.bs[i] = neg2(mul2(u.b[i], s));
+  }
+  return t;
+}
+
+__device__ __forceinline__ void turn_unit(const Turn &t, Unit &u) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f32x2 a = u.a[i], b = u.b[i];
+    u.a[i] = fma2(a, t.ac[i], mul2(b, t.bs[i]));
+    u.b[i] = fma2(b, t.bc[i], mul2(a, t.as[i]));
+  }
+}
+
+__device__ __forceinline__ void scale_unit(Unit &u, float f) {
+  const f32x2 f2f = f2(f, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    u.a[i] = mul2(u.a[i], f2f);
+    u.b[i] = mul2(u.b[i], f2f);
+  }
+}
+
+// Sum of squares over the unit's group of w lanes.
+__device__ __forceinline__ float unit_sum_sq(const Unit &u, int w) {
+  f32x2 s = f2(0.f, 0.f), v = s;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s = fma2(u.a[i], u.a[i], s);
+    v = fma2(u.b[i], u.b[i], v);
+  }
+  float lo, hi;
+  f2_split(add2(s, v), lo, hi);
+  lo += hi;
+  for (int o = w >> 1; o > 0; o >>= 1) lo += __shfl_xor_sync(0xffffffffu, lo, o);
+  return lo;
+}
 
 __device__ __forceinline__ float sum_sq8(const float *x) {
   float s = 0.f;
@@ -45,8 +157,8 @@ __device__ __forceinline__ void st16(__nv_bfloat16 *p, const uint4 &v) {
   *reinterpret_cast<uint4 *>(p) = v;
 }
 
-template <int kTok>
-__global__ void __launch_bounds__(kThr) append_kernel(const __grid_constant__ AppendArgs a) {
+template <int kTok, bool kNeox>
+__global__ void __launch_bounds__(kThr, 2) append_kernel(const __grid_constant__ AppendArgs a) {
   __shared__ float2 cs[kTok * kMaxPairs];
   __shared__ long long slots[kTok];  // -1: no slot, K and V are not written
   __shared__ int live[kTok];         // 0: padding or a bad token, nothing is written
@@ -57,36 +169,29 @@ __global__ void __launch_bounds__(kThr) append_kernel(const __grid_constant__ Ap
   const int np = lay.npairs;
   const bool gqa = lay.kind == KAMERA_GQA;
 
-  // rotated items: the query heads, then the key bands, of this group's token
+  // this group's token, its query heads and key bands h_first, h_first + groups, ...
   const int band = lay.rope_d, units = band >> 4;
-  int w = 1;
-  while (w < units) w <<= 1;
-  const int q = tid & (w - 1), groups = kThr / w / kTok;  // groups of lanes per token
-  const int sub = tid / w, tk = sub / groups, h_first = sub - tk * groups;
-  const int per_tok = a.hq + (gqa ? lay.H : 1);
-  const bool neox = lay.style == KAMERA_ROPE_NEOX_HALF;
-  const int ca = neox ? 8 * q : 16 * q, cb = neox ? ca + (band >> 1) : ca + 8;
+  const int wsh = units <= 1 ? 0 : 32 - __clz(units - 1), w = 1 << wsh;
+  const int q = tid & (w - 1), groups = kThr / kTok >> wsh;  // groups of lanes per token
+  const int tk = tid / (kThr / kTok), h_first = (tid - tk * (kThr / kTok)) >> wsh;
+  const int ca = kNeox ? 8 * q : 16 * q, cb = kNeox ? ca + (band >> 1) : ca + 8;
   const bool mine = q < units && tk < nt;
-  const long long tok = t0 + tk;
-  // column of head h in the queries' or keys' row
-  auto column = [&](int h) {
-    return gqa ? (h < a.hq ? h : h - a.hq) * lay.hd : (h < a.hq ? h * lay.row_k : 0) + lay.latent;
-  };
-  uint4 ra[kBatch], rb[kBatch];
-  auto load = [&](int h0) {
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int h = h0 + j * groups;
-      ra[j] = rb[j] = make_uint4(0, 0, 0, 0);
-      if (mine && h < per_tok) {
-        const __nv_bfloat16 *src =
-            (h < a.hq ? a.q + tok * a.q_stride : a.k + tok * a.k_stride) + column(h);
-        ra[j] = ld16(src + ca);
-        rb[j] = ld16(src + cb);
-      }
+  const int n_k = gqa ? lay.H : 1;
+  // the bands' columns: head h at off + h * pitch
+  const int pitch = gqa ? lay.hd : lay.row_k, off = gqa ? 0 : lay.latent;
+  const __nv_bfloat16 *qrow = a.q + (t0 + tk) * a.q_stride + off;
+  const __nv_bfloat16 *krow = a.k + (t0 + tk) * a.k_stride + off;
+  uint4 ra[kBatch], rb[kBatch], ka, kb;
+  auto load = [&](const __nv_bfloat16 *row, int h, int n, uint4 &x, uint4 &y) {
+    x = y = make_uint4(0, 0, 0, 0);
+    if (mine && h < n) {
+      x = ld16(row + h * pitch + ca);
+      y = ld16(row + h * pitch + cb);
     }
   };
-  load(h_first);
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j) load(qrow, h_first + j * groups, a.hq, ra[j], rb[j]);
+  load(krow, h_first, n_k, ka, kb);
 
   for (int e = tid; e < nt * np; e += kThr) {
     const int t = e / np, i = e - t * np;
@@ -106,67 +211,56 @@ __global__ void __launch_bounds__(kThr) append_kernel(const __grid_constant__ Ap
   __syncthreads();
 
   const long long layer_k = (long long)a.layer * a.pool.num_slots * lay.row_k;
-  const long long slot = tk < nt ? slots[tk] : -1;
-  const bool write_q = tk < nt && live[tk];
-  const bool norms = gqa && (a.q_weight || a.k_weight);
-  const float2 *c = cs + tk * np;
-  float2 ph[8];  // NeoX pairs 8 q ..; interleaved pairs of chunk a, then of chunk b: the same ones
-#pragma unroll
-  for (int e = 0; e < 8; ++e) ph[e] = mine ? c[8 * q + e] : make_float2(1.f, 0.f);
-  for (int base = 0; base < per_tok; base += groups * kBatch) {  // whole warps iterate alike
-    if (base > 0) load(base + h_first);
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int h = base + h_first + j * groups;
-      const bool isq = h < a.hq;
-      float xa[8], xb[8];
-      unpack8(ra[j], xa);
-      unpack8(rb[j], xb);
-      if (norms) {  // every lane takes part in the reduction
-        const __nv_bfloat16 *wt = isq ? a.q_weight : a.k_weight;
-        auto mean_sq = [&]() {
-          float s = sum_sq8(xa) + sum_sq8(xb);
-          for (int o = w >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          return s / (float)band;
-        };
-        float mean = mean_sq() + a.eps;
-        const float f = wt && h < per_tok ? norm_scale(mean) : 1.f;
-        if (__any_sync(0xffffffffu, f != 1.f)) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            xa[e] *= f;
-            xb[e] *= f;
-          }
-          mean = mean_sq() + a.eps * f * f;
-        }
-        if (wt && mine) {
-          const float r = rsqrtf(mean);
-          float wa[8], wb[8];
-          unpack8(__ldg(reinterpret_cast<const uint4 *>(wt + ca)), wa);
-          unpack8(__ldg(reinterpret_cast<const uint4 *>(wt + cb)), wb);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            xa[e] = xa[e] * r * wa[e];
-            xb[e] = xb[e] * r * wb[e];
-          }
-        }
+  const float2 *ph = cs + (mine ? tk * np + 8 * q : 0);
+  const float inv_band = 1.f / (float)band;
+  // one head: the norm (with weights), the rotation, the store. Whole warps come here alike: every
+  // lane takes part in the reduction
+  auto finish = [&](const uint4 &x, const uint4 &y, const Turn &turn, bool norm, bool write,
+                    __nv_bfloat16 *dst) {
+    Unit u = unpack_unit<kNeox>(x, y);
+    float r = 1.f;
+    if (norm) {
+      float mean = fmaf(unit_sum_sq(u, w), inv_band, a.eps);
+      const float f = norm_scale(mean);
+      if (__any_sync(0xffffffffu, f != 1.f)) {
+        scale_unit(u, f);
+        mean = fmaf(unit_sum_sq(u, w), inv_band, a.eps * f * f);
       }
-      if (!mine || h >= per_tok || (isq ? !write_q : slot < 0)) continue;
-      if (neox) {
+      r = rsqrtf(mean);
+    }
+    if (!write) return;
+    turn_unit(turn, u);
+    if (norm) scale_unit(u, r);
+    uint4 za, zb;
+    pack_unit<kNeox>(u, &za, &zb);
+    st16(dst + ca, za);
+    st16(dst + cb, zb);
+  };
+  if (a.hq > 0) {
+    const Turn turn = make_turn<kNeox>(ph, a.q_weight, mine ? ca : 0, mine ? cb : 8);
+    const bool write = mine && live[tk], norm = a.q_weight != nullptr;
+    __nv_bfloat16 *dst = a.q_out + (t0 + tk) * a.q_out_stride + off;
+    for (int base = h_first; base < a.hq + h_first; base += groups * kBatch) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) rot_pair(xa[e], xb[e], ph[e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          rot_pair(xa[e], xa[e + 1], ph[e >> 1]);
-          rot_pair(xb[e], xb[e + 1], ph[4 + (e >> 1)]);
-        }
+      for (int j = 0; j < kBatch; ++j) {
+        const int h = base + j * groups;
+        if (base > h_first) load(qrow, h, a.hq, ra[j], rb[j]);
       }
-      __nv_bfloat16 *dst = (isq ? a.q_out + tok * a.q_out_stride
-                                : a.pool.k + layer_k + slot * lay.row_k) +
-                           column(h);
-      st16(dst + ca, pack8_rn(xa));
-      st16(dst + cb, pack8_rn(xb));
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int h = base + j * groups;
+        finish(ra[j], rb[j], turn, norm, write && h < a.hq, dst + h * pitch);
+      }
+    }
+  }
+  {
+    const bool norm = gqa && a.k_weight;
+    const Turn turn = make_turn<kNeox>(ph, norm ? a.k_weight : nullptr, mine ? ca : 0, mine ? cb : 8);
+    const bool write = mine && slots[tk] >= 0;
+    __nv_bfloat16 *dst = a.pool.k + layer_k + (write ? slots[tk] * lay.row_k : 0) + off;
+    for (int h = h_first; h < n_k + h_first; h += groups) {
+      if (h > h_first) load(krow, h, n_k, ka, kb);
+      finish(ka, kb, turn, norm, write && h < n_k, dst + h * pitch);
     }
   }
 
@@ -255,13 +349,23 @@ __global__ void __launch_bounds__(kThr) append_kernel(const __grid_constant__ Ap
 
 }  // namespace
 
+namespace {
+
+template <int kTok>
+cudaError_t launch(const AppendArgs &a, cudaStream_t s) {
+  const unsigned grid = (unsigned)((a.T + kTok - 1) / kTok);
+  if (a.lay.style == KAMERA_ROPE_NEOX_HALF)
+    append_kernel<kTok, true><<<grid, kThr, 0, s>>>(a);
+  else
+    append_kernel<kTok, false><<<grid, kThr, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t s) {
   // a token to a CTA while that gives every SM no more than a few CTAs, else four
-  if (a.T <= 4 * kSms)
-    append_kernel<1><<<(unsigned)a.T, kThr, 0, s>>>(a);
-  else
-    append_kernel<4><<<(unsigned)((a.T + 3) / 4), kThr, 0, s>>>(a);
-  return cudaGetLastError();
+  return a.T <= 4 * kSms ? launch<1>(a, s) : launch<4>(a, s);
 }
 
 }  // namespace kamera
