@@ -6,16 +6,23 @@
 //   MLA: the latent c_KV normed with w_k and the k_pe band rotated into the row; the queries
 //        (absorbed form) keep their latent part and turn their rope band.
 //
-// One CTA of 256 threads per kTok tokens. W = 2^ceil(log2(band / 16)) lanes take one (token, head)
-// item: a lane holds the two 8-column chunks of a column unit, which are closed under pairing, so
-// the norm is one shuffle reduction over the W lanes and the rotation needs no exchange. A group
-// of W lanes stays with one token and takes several of its heads at a time, so that their loads
-// are in flight together, before the phases and slots are known, and its phases are read once.
-// The CTA computes the tokens' phases (each (token, pair) once, by the exact Q0.64 range reduction
-// of the other kernels) and resolves their slots while the first loads run. Sums of squares, the
-// norm and the rotation are float32; each output is rounded to bf16 once.
+// W = 2^ceil(log2(band / 16)) lanes take one (token, head) item: a lane holds the two 8-column
+// chunks of a column unit, which are closed under pairing, so the norm is one shuffle reduction
+// over the W lanes and the rotation needs no exchange; the weights are folded into the rotation.
+// Sums of squares, the norm and the rotation are float32; phases by the exact Q0.64 range
+// reduction of the other kernels; each output is rounded to bf16 once.
+//
+// append_kernel: a CTA of 256 threads per kTok tokens. A group of W lanes stays with one token and
+// takes several of its heads at a time, so that their loads are in flight together, before the
+// phases and slots are known. Few tokens (latency: 8 us at 8 tokens), or long rows.
+// append_stream_kernel: a warp to a token, in CTAs that stay, each lane's next chunks arriving by
+// cp.async while it works. 16381 tokens of 28/4 heads of 128: 66 us, 302 MB moved, 4.6 TB/s
+// (append_kernel 82 us); the instructions of the turn and norm take half of the issue slots.
 // Bound: HBM (every byte is read and written once) at many tokens, latency at few.
+#include <mutex>
+
 #include "kamera_dev.cuh"
+#include "kamera_ptx.cuh"
 #include "kamera_smem.cuh"
 
 namespace kamera {
@@ -157,6 +164,32 @@ __device__ __forceinline__ void st16(__nv_bfloat16 *p, const uint4 &v) {
   *reinterpret_cast<uint4 *>(p) = v;
 }
 
+// One head of a unit's lanes: the norm, the rotation, the store to chunks da and db. Whole warps
+// come here alike: every lane takes part in the reduction.
+template <bool kNeox>
+__device__ __forceinline__ void finish_head(const uint4 &x, const uint4 &y, const Turn &turn,
+                                            bool norm, float eps, int w, float inv_band, bool write,
+                                            __nv_bfloat16 *da, __nv_bfloat16 *db) {
+  Unit u = unpack_unit<kNeox>(x, y);
+  float r = 1.f;
+  if (norm) {
+    float mean = fmaf(unit_sum_sq(u, w), inv_band, eps);
+    const float f = norm_scale(mean);
+    if (__any_sync(0xffffffffu, f != 1.f)) {
+      scale_unit(u, f);
+      mean = fmaf(unit_sum_sq(u, w), inv_band, eps * f * f);
+    }
+    r = rsqrtf(mean);
+  }
+  if (!write) return;
+  turn_unit(turn, u);
+  if (norm) scale_unit(u, r);
+  uint4 za, zb;
+  pack_unit<kNeox>(u, &za, &zb);
+  st16(da, za);
+  st16(db, zb);
+}
+
 template <int kTok, bool kNeox>
 __global__ void __launch_bounds__(kThr, 2) append_kernel(const __grid_constant__ AppendArgs a) {
   __shared__ float2 cs[kTok * kMaxPairs];
@@ -181,6 +214,12 @@ __global__ void __launch_bounds__(kThr, 2) append_kernel(const __grid_constant__
   const int pitch = gqa ? lay.hd : lay.row_k, off = gqa ? 0 : lay.latent;
   const __nv_bfloat16 *qrow = a.q + (t0 + tk) * a.q_stride + off;
   const __nv_bfloat16 *krow = a.k + (t0 + tk) * a.k_stride + off;
+  // the tokens' places first: their slots take two dependent loads
+  int req = -1, at = 0;
+  if (tid < nt) {
+    req = __ldg(a.req + t0 + tid);
+    at = __ldg(a.tok + t0 + tid);
+  }
   uint4 ra[kBatch], rb[kBatch], ka, kb;
   auto load = [&](const __nv_bfloat16 *row, int h, int n, uint4 &x, uint4 &y) {
     x = y = make_uint4(0, 0, 0, 0);
@@ -192,15 +231,12 @@ __global__ void __launch_bounds__(kThr, 2) append_kernel(const __grid_constant__
 #pragma unroll
   for (int j = 0; j < kBatch; ++j) load(qrow, h_first + j * groups, a.hq, ra[j], rb[j]);
   load(krow, h_first, n_k, ka, kb);
-
-  for (int e = tid; e < nt * np; e += kThr) {
-    const int t = e / np, i = e - t * np;
-    const int axis = lay.mrope ? mrope_axis(lay, i) : 0;
-    const int stride = lay.mrope ? 3 : 1;
-    cs[e] = rope_phase(a.freq.q[i], __ldg(a.positions + (t0 + t) * stride + axis));
-  }
+  // V: kThr / kTok threads to a token, the first chunk of each
+  constexpr int kVThr = kThr / kTok;
+  const int nv = gqa ? lay.row_v >> 3 : 0, ve = tid - tk * kVThr;
+  uint4 v0;
+  if (tk < nt && ve < nv) v0 = ld16(a.v + (t0 + tk) * a.v_stride + 8 * ve);
   if (tid < nt) {
-    const int req = __ldg(a.req + t0 + tid), at = __ldg(a.tok + t0 + tid);
     const bool padding = req < 0;
     const bool bad = !padding && (req >= a.pool.num_reqs || at < 0 ||
                                   at >= (long long)a.pool.pt_stride * lay.page_size);
@@ -208,33 +244,20 @@ __global__ void __launch_bounds__(kThr, 2) append_kernel(const __grid_constant__
     live[tid] = !padding && !bad;
     slots[tid] = padding || bad ? -1 : slot_of(a.pool, lay.page_size, req, at, a.status);
   }
+
+  for (int e = tid; e < nt * np; e += kThr) {
+    const int t = e / np, i = e - t * np;
+    const int axis = lay.mrope ? mrope_axis(lay, i) : 0;
+    const int stride = lay.mrope ? 3 : 1;
+    cs[e] = rope_phase(a.freq.q[i], __ldg(a.positions + (t0 + t) * stride + axis));
+  }
   __syncthreads();
 
   const long long layer_k = (long long)a.layer * a.pool.num_slots * lay.row_k;
   const float2 *ph = cs + (mine ? tk * np + 8 * q : 0);
-  const float inv_band = 1.f / (float)band;
-  // one head: the norm (with weights), the rotation, the store. Whole warps come here alike: every
-  // lane takes part in the reduction
   auto finish = [&](const uint4 &x, const uint4 &y, const Turn &turn, bool norm, bool write,
                     __nv_bfloat16 *dst) {
-    Unit u = unpack_unit<kNeox>(x, y);
-    float r = 1.f;
-    if (norm) {
-      float mean = fmaf(unit_sum_sq(u, w), inv_band, a.eps);
-      const float f = norm_scale(mean);
-      if (__any_sync(0xffffffffu, f != 1.f)) {
-        scale_unit(u, f);
-        mean = fmaf(unit_sum_sq(u, w), inv_band, a.eps * f * f);
-      }
-      r = rsqrtf(mean);
-    }
-    if (!write) return;
-    turn_unit(turn, u);
-    if (norm) scale_unit(u, r);
-    uint4 za, zb;
-    pack_unit<kNeox>(u, &za, &zb);
-    st16(dst + ca, za);
-    st16(dst + cb, zb);
+    finish_head<kNeox>(x, y, turn, norm, a.eps, w, 1.f / (float)band, write, dst + ca, dst + cb);
   };
   if (a.hq > 0) {
     const Turn turn = make_turn<kNeox>(ph, a.q_weight, mine ? ca : 0, mine ? cb : 8);
@@ -264,20 +287,20 @@ __global__ void __launch_bounds__(kThr, 2) append_kernel(const __grid_constant__
     }
   }
 
-  if (gqa) {  // V rows, byte for byte: kThr / kTok threads to a token
-    const int nc = lay.row_v >> 3, t = tid / (kThr / kTok);
-    if (t >= nt || slots[t] < 0) return;
-    const __nv_bfloat16 *src = a.v + (t0 + t) * a.v_stride;
+  if (gqa) {  // V rows, byte for byte
+    if (tk >= nt || slots[tk] < 0) return;
+    const __nv_bfloat16 *src = a.v + (t0 + tk) * a.v_stride;
     __nv_bfloat16 *dst =
-        a.pool.v + ((long long)a.layer * a.pool.num_slots + slots[t]) * lay.row_v;
-    for (int e = tid % (kThr / kTok); e < nc; e += kThr / kTok * kBatch) {
+        a.pool.v + ((long long)a.layer * a.pool.num_slots + slots[tk]) * lay.row_v;
+    if (ve < nv) st16(dst + 8 * ve, v0);
+    for (int e = ve + kVThr; e < nv; e += kVThr * kBatch) {
       uint4 v[kBatch];
 #pragma unroll
       for (int j = 0; j < kBatch; ++j)
-        if (e + j * (kThr / kTok) < nc) v[j] = ld16(src + 8 * (e + j * (kThr / kTok)));
+        if (e + j * kVThr < nv) v[j] = ld16(src + 8 * (e + j * kVThr));
 #pragma unroll
       for (int j = 0; j < kBatch; ++j)
-        if (e + j * (kThr / kTok) < nc) st16(dst + 8 * (e + j * (kThr / kTok)), v[j]);
+        if (e + j * kVThr < nv) st16(dst + 8 * (e + j * kVThr), v[j]);
     }
     return;
   }
@@ -347,6 +370,238 @@ __global__ void __launch_bounds__(kThr, 2) append_kernel(const __grid_constant__
   }
 }
 
+// ---------------------------------------------------------------------------------------
+// Many tokens: a warp to a token, in CTAs that stay. A warp's lanes copy the 16-byte chunks that
+// they will themselves use of its next token by cp.async while it works on this one, so nothing
+// waits for another warp; the next token's page entry and position are on their way too. A lane
+// has the same column unit in all its heads, so phases and weights are folded once a token.
+// Bound: HBM.
+// ---------------------------------------------------------------------------------------
+
+constexpr int kStreamRoom = 214 * 1024;  // shared memory for the rows in flight (and 12 KB of phases)
+constexpr int kStreamWarps = 12;         // warps of a CTA at most (and 168 registers a thread)
+constexpr int kStreamLeast = 8;          // and at least: fewer are slower than the CTA kernel
+
+// Chunks of a token that a lane brings: two for each query head and key band of its group, then
+// V chunks (GQA) or the latent rows' (MLA: of the token, of its query heads).
+struct StreamPlan {
+  int q, k, v, lk, lq;  // first chunk of each kind
+  int chunks;           // in all
+  int warps;            // of a CTA, as many as fit
+};
+
+StreamPlan stream_plan(const DevLayout &l, int hq, bool copy_q) {
+  const int units = l.rope_d >> 4;
+  int w = 1;
+  while (w < units) w <<= 1;
+  const int groups = 32 / w, n_k = l.kind == KAMERA_GQA ? l.H : 1;
+  const int latent = ((l.latent >> 3) + 31) / 32;
+  StreamPlan p;
+  int n = 0;
+  p.q = n;
+  n += 2 * ((hq + groups - 1) / groups);
+  p.k = n;
+  n += 2 * ((n_k + groups - 1) / groups);
+  p.v = n;
+  if (l.kind == KAMERA_GQA) n += ((l.row_v >> 3) + 31) / 32;
+  p.lk = n;
+  n += latent;
+  p.lq = n;
+  if (l.kind == KAMERA_MLA && copy_q) n += latent * hq;
+  p.chunks = n;
+  p.warps = kStreamRoom / (2 * n * 512);
+  if (p.warps > kStreamWarps) p.warps = kStreamWarps;
+  return p;
+}
+
+template <bool kNeox>
+__global__ void __launch_bounds__(32 * kStreamWarps, 1) append_stream_kernel(const __grid_constant__ AppendArgs a,
+                                                                            const StreamPlan sp) {
+  extern __shared__ __align__(16) unsigned char smem[];  // [warps][2][chunks][32] of 16 bytes
+  __shared__ float2 phases[kStreamWarps][kMaxPairs];
+  const DevLayout &lay = a.lay;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int np = lay.npairs;
+  const bool gqa = lay.kind == KAMERA_GQA;
+  const int band = lay.rope_d, units = band >> 4;
+  const int wsh = units <= 1 ? 0 : 32 - __clz(units - 1), w = 1 << wsh;
+  const int q = lane & (w - 1), groups = 32 >> wsh, h_first = lane >> wsh;
+  const bool unit = q < units;
+  const int ca = unit ? (kNeox ? 8 * q : 16 * q) : 0;
+  const int cb = unit ? (kNeox ? ca + (band >> 1) : ca + 8) : 8;
+  const int n_k = gqa ? lay.H : 1, nv = gqa ? lay.row_v >> 3 : 0, nc = lay.latent >> 3;
+  const int pitch = gqa ? lay.hd : lay.row_k, off = gqa ? 0 : lay.latent;
+  const float inv_band = 1.f / (float)band;
+  const long long layer_k = (long long)a.layer * a.pool.num_slots * lay.row_k;
+  const long long layer_v = (long long)a.layer * a.pool.num_slots * lay.row_v;
+  const bool copy_q = !gqa && a.q_out != a.q;
+  const uint32_t stage = (uint32_t)sp.chunks * 512;
+  unsigned char *const mem = smem + warp * 2 * stage + 16 * lane;
+  const uint32_t sb = ptx::smem_addr(mem);
+  float2 *const cs = phases[warp];
+  auto copy = [&](uint32_t buf, int chunk, const __nv_bfloat16 *src) {
+    ptx::cp_async16(sb + buf + chunk * 512, src, 16);
+  };
+  auto chunk = [&](uint32_t buf, int c) {
+    return *reinterpret_cast<const uint4 *>(mem + buf + c * 512);
+  };
+  auto band_chunk = [&](uint32_t buf, int c) {  // zero where the lane has no unit: it is summed
+    return unit ? chunk(buf, c) : make_uint4(0, 0, 0, 0);
+  };
+  // a token's rows into a buffer (its offset)
+  auto fetch = [&](long long t, uint32_t buf) {
+    if (t < a.T) {
+      const __nv_bfloat16 *qr = a.q + t * a.q_stride, *kr = a.k + t * a.k_stride;
+      if (unit) {
+        const __nv_bfloat16 *p = qr + off + h_first * pitch;
+        for (int h = h_first, c = sp.q; h < a.hq; h += groups, c += 2, p += groups * pitch) {
+          copy(buf, c, p + ca);
+          copy(buf, c + 1, p + cb);
+        }
+        p = kr + off + h_first * pitch;
+        for (int h = h_first, c = sp.k; h < n_k; h += groups, c += 2, p += groups * pitch) {
+          copy(buf, c, p + ca);
+          copy(buf, c + 1, p + cb);
+        }
+      }
+      const __nv_bfloat16 *vr = a.v + t * a.v_stride;
+      for (int e = lane, c = sp.v; e < nv; e += 32, ++c) copy(buf, c, vr + 8 * e);
+      if (!gqa) {
+        for (int e = lane, c = sp.lk; e < nc; e += 32, ++c) copy(buf, c, kr + 8 * e);
+        if (copy_q) {
+          int c = sp.lq;
+          for (int h = 0; h < a.hq; ++h)
+            for (int e = lane; e < nc; e += 32, ++c) copy(buf, c, qr + h * lay.row_k + 8 * e);
+        }
+      }
+    }
+    ptx::cp_async_commit();
+  };
+  // what a token's place and phases are made of, fetched ahead; every lane has the same place
+  struct Place {
+    int req, tok;
+  };
+  auto load_place = [&](long long t) {
+    Place p{-1, 0};
+    if (t < a.T) {
+      p.req = __ldg(a.req + t);
+      p.tok = __ldg(a.tok + t);
+    }
+    return p;
+  };
+  auto load_page = [&](Place &p) {  // a place outside the table becomes padding, and is reported
+    if (p.req < 0) return 0;
+    if (p.req >= a.pool.num_reqs || p.tok < 0 ||
+        p.tok >= (long long)a.pool.pt_stride * lay.page_size) {
+      if (lane == 0) atomicOr(a.status, KAMERA_DEVICE_BAD_ITEM);
+      p.req = -1;
+      return 0;
+    }
+    return __ldg(a.pool.pt + (long long)p.req * a.pool.pt_stride + p.tok / lay.page_size);
+  };
+  constexpr int kPos = kMaxPairs / 32;  // lane e makes pairs e, e + 32, ...
+  long long pos[kPos];
+  auto load_pos = [&](long long t) {
+#pragma unroll
+    for (int j = 0; j < kPos; ++j) {
+      const int i = lane + 32 * j;
+      if (i >= np || t >= a.T) continue;
+      pos[j] = __ldg(a.positions + (lay.mrope ? 3 * t + mrope_axis(lay, i) : t));
+    }
+  };
+
+  const long long step = (long long)gridDim.x * sp.warps;
+  long long t = (long long)warp * gridDim.x + blockIdx.x;
+  fetch(t, 0);
+  Place now = load_place(t), next = load_place(t + step);
+  load_pos(t);
+  int page = load_page(now);
+  for (uint32_t buf = 0; t < a.T; t += step, buf ^= stage) {
+    fetch(t + step, buf ^ stage);
+    // this token's slot and phases; the next one's page entry and position
+    long long slot = -1;
+    if (now.req >= 0) {
+      if (page < 0 || ((long long)page + 1) * lay.page_size > a.pool.num_slots) {
+        if (lane == 0) atomicOr(a.status, KAMERA_DEVICE_SLOT_OOB);
+      } else {
+        slot = (long long)page * lay.page_size + now.tok % lay.page_size;
+      }
+    }
+    const bool live = now.req >= 0;
+    __syncwarp();  // the last token's phases have been read
+#pragma unroll
+    for (int j = 0; j < kPos; ++j)
+      if (lane + 32 * j < np) cs[lane + 32 * j] = rope_phase(a.freq.q[lane + 32 * j], pos[j]);
+    page = load_page(next);
+    now = next;
+    next = load_place(t + 2 * step);
+    load_pos(t + step);
+    ptx::cp_async_wait_group1();  // this lane's chunks of the token
+    __syncwarp();
+    if (!live) continue;
+    const float2 *ph = cs + (unit ? 8 * q : 0);
+    if (a.hq > 0) {
+      const Turn turn = make_turn<kNeox>(ph, a.q_weight, ca, cb);
+      const bool norm = a.q_weight != nullptr;
+      __nv_bfloat16 *dst = a.q_out + t * a.q_out_stride + off + h_first * pitch;
+      for (int h = h_first, c = sp.q; h < a.hq + h_first; h += groups, c += 2, dst += groups * pitch)
+        finish_head<kNeox>(band_chunk(buf, c), band_chunk(buf, c + 1), turn, norm, a.eps, w,
+                           inv_band, unit && h < a.hq, dst + ca, dst + cb);
+    }
+    if (slot >= 0) {
+      const bool norm = gqa && a.k_weight;
+      const Turn turn = make_turn<kNeox>(ph, norm ? a.k_weight : nullptr, ca, cb);
+      __nv_bfloat16 *row = a.pool.k + layer_k + slot * lay.row_k;
+      __nv_bfloat16 *dst = row + off + h_first * pitch;
+      for (int h = h_first, c = sp.k; h < n_k + h_first; h += groups, c += 2, dst += groups * pitch)
+        finish_head<kNeox>(band_chunk(buf, c), band_chunk(buf, c + 1), turn, norm, a.eps, w,
+                           inv_band, unit && h < n_k, dst + ca, dst + cb);
+      for (int e = lane, c = sp.v; e < nv; e += 32, ++c)
+        st16(a.pool.v + layer_v + slot * lay.row_v + 8 * e, chunk(buf, c));
+      if (!gqa) {
+        float r = 1.f, f = 1.f;
+        if (a.k_weight) {
+          auto mean_sq = [&]() {
+            float s = 0.f;
+            for (int e = lane, c = sp.lk; e < nc; e += 32, ++c) {
+              float x[8];
+              unpack8(chunk(buf, c), x);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) x[i] *= f;
+              s += sum_sq8(x);
+            }
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            return s / (float)lay.latent;
+          };
+          float mean = mean_sq() + a.eps;
+          f = norm_scale(mean);
+          if (f != 1.f) mean = mean_sq() + a.eps * f * f;
+          r = rsqrtf(mean);
+        }
+        for (int e = lane, c = sp.lk; e < nc; e += 32, ++c) {
+          uint4 v = chunk(buf, c);
+          if (a.k_weight) {
+            float x[8], wv[8];
+            unpack8(v, x);
+            unpack8(__ldg(reinterpret_cast<const uint4 *>(a.k_weight + 8 * e)), wv);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = x[i] * f * r * wv[i];
+            v = pack8_rn(x);
+          }
+          st16(row + 8 * e, v);
+        }
+      }
+    }
+    if (copy_q) {
+      __nv_bfloat16 *dst = a.q_out + t * a.q_out_stride;
+      int c = sp.lq;
+      for (int h = 0; h < a.hq; ++h, dst += lay.row_k)
+        for (int e = lane; e < nc; e += 32, ++c) st16(dst + 8 * e, chunk(buf, c));
+    }
+  }
+  ptx::cp_async_wait_all();
+}
+
 }  // namespace
 
 namespace {
@@ -364,8 +619,41 @@ cudaError_t launch(const AppendArgs &a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t s) {
-  // a token to a CTA while that gives every SM no more than a few CTAs, else four
-  return a.T <= 4 * kSms ? launch<1>(a, s) : launch<4>(a, s);
+  // One token a CTA, four, or a warp a token. Measured with a call's overhead, L2 flushed, in us:
+  //                             T = 304: one  four  warps   608: one  four  warps   16381: four  warps
+  //   28/4 heads of 128 (11 warps fit)   11    11     13          17    11     13            89     72
+  //   16 + 16 heads of 128 (5)           13    17     17          19    17     17           168    224
+  //   6/2 heads of 64 (12)               11    11     11          15    11     11            66     33
+  //   MLA, 16 heads copied (5)           13    15     14          20    15     15           142    154
+  //   MLA, queries in place (12)         11    12     11          17    11     11            79     40
+  // A CTA's few warps must hold the rows in flight that HBM wants, and eight do the arithmetic.
+  if (a.T <= 2 * kSms) return launch<1>(a, s);
+  const StreamPlan sp = stream_plan(a.lay, a.hq, a.q_out != a.q);
+  if (sp.warps < kStreamLeast) return launch<4>(a, s);
+  static int configured[64] = {0};
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!configured[dev]) {
+      e = cudaFuncSetAttribute(append_stream_kernel<true>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamRoom);
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(append_stream_kernel<false>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamRoom);
+      if (e != cudaSuccess) return e;
+      configured[dev] = 1;
+    }
+  }
+  const size_t bytes = (size_t)2 * sp.chunks * 512 * sp.warps;
+  if (a.lay.style == KAMERA_ROPE_NEOX_HALF)
+    append_stream_kernel<true><<<kSms, 32 * sp.warps, bytes, s>>>(a, sp);
+  else
+    append_stream_kernel<false><<<kSms, 32 * sp.warps, bytes, s>>>(a, sp);
+  return cudaGetLastError();
 }
 
 }  // namespace kamera
