@@ -195,6 +195,8 @@ __global__ void __launch_bounds__(kThr, 2) append_kernel(const __grid_constant__
   __shared__ float2 cs[kTok * kMaxPairs];
   __shared__ long long slots[kTok];  // -1: no slot, K and V are not written
   __shared__ int live[kTok];         // 0: padding or a bad token, nothing is written
+  ptx::launch_dependents();
+  ptx::wait_for_previous();
   const DevLayout &lay = a.lay;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long t0 = (long long)blockIdx.x * kTok;
@@ -419,6 +421,8 @@ __global__ void __launch_bounds__(32 * kStreamWarps, 1) append_stream_kernel(con
                                                                             const StreamPlan sp) {
   extern __shared__ __align__(16) unsigned char smem[];  // [warps][2][chunks][32] of 16 bytes
   __shared__ float2 phases[kStreamWarps][kMaxPairs];
+  ptx::launch_dependents();
+  ptx::wait_for_previous();
   const DevLayout &lay = a.lay;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int np = lay.npairs;
@@ -608,24 +612,22 @@ namespace {
 
 template <int kTok>
 cudaError_t launch(const AppendArgs &a, cudaStream_t s) {
-  const unsigned grid = (unsigned)((a.T + kTok - 1) / kTok);
-  if (a.lay.style == KAMERA_ROPE_NEOX_HALF)
-    append_kernel<kTok, true><<<grid, kThr, 0, s>>>(a);
-  else
-    append_kernel<kTok, false><<<grid, kThr, 0, s>>>(a);
-  return cudaGetLastError();
+  const dim3 grid((unsigned)((a.T + kTok - 1) / kTok));
+  return launch_early(a.lay.style == KAMERA_ROPE_NEOX_HALF ? append_kernel<kTok, true>
+                                                           : append_kernel<kTok, false>,
+                      grid, kThr, 0, s, a);
 }
 
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t s) {
   // One token a CTA, four, or a warp a token. Measured with a call's overhead, L2 flushed, in us:
-  //                             T = 304: one  four  warps   608: one  four  warps   16381: four  warps
-  //   28/4 heads of 128 (11 warps fit)   11    11     13          17    11     13            89     72
-  //   16 + 16 heads of 128 (5)           13    17     17          19    17     17           168    224
-  //   6/2 heads of 64 (12)               11    11     11          15    11     11            66     33
-  //   MLA, 16 heads copied (5)           13    15     14          20    15     15           142    154
-  //   MLA, queries in place (12)         11    12     11          17    11     11            79     40
+  //                             T = 304: one four warps  608: one four warps  16381: four warps
+  //   28/4 heads of 128 (11 warps fit)    11   11    13        17   11    13          89    72
+  //   16 + 16 heads of 128 (5)            13   17    17        19   17    17         168   224
+  //   6/2 heads of 64 (12)                11   11    11        15   11    11          66    33
+  //   MLA, 16 heads copied (5)            13   15    14        20   15    15         142   154
+  //   MLA, queries in place (12)          11   12    11        17   11    11          79    40
   // A CTA's few warps must hold the rows in flight that HBM wants, and eight do the arithmetic.
   if (a.T <= 2 * kSms) return launch<1>(a, s);
   const StreamPlan sp = stream_plan(a.lay, a.hq, a.q_out != a.q);
@@ -649,11 +651,9 @@ cudaError_t launch_append(const AppendArgs &a, cudaStream_t s) {
     }
   }
   const size_t bytes = (size_t)2 * sp.chunks * 512 * sp.warps;
-  if (a.lay.style == KAMERA_ROPE_NEOX_HALF)
-    append_stream_kernel<true><<<kSms, 32 * sp.warps, bytes, s>>>(a, sp);
-  else
-    append_stream_kernel<false><<<kSms, 32 * sp.warps, bytes, s>>>(a, sp);
-  return cudaGetLastError();
+  return launch_early(a.lay.style == KAMERA_ROPE_NEOX_HALF ? append_stream_kernel<true>
+                                                           : append_stream_kernel<false>,
+                      dim3(kSms), 32 * sp.warps, bytes, s, a, sp);
 }
 
 }  // namespace kamera

@@ -12,6 +12,7 @@
 //  * copy_kernel: listed pages.
 // Bound: the bytes moved (HBM) where pages are copied, launches and latency otherwise.
 #include "kamera_dev.cuh"
+#include "kamera_ptx.cuh"
 
 namespace kamera {
 
@@ -20,6 +21,7 @@ namespace {
 constexpr int kThr = 256;
 constexpr int kPer = 4;              // pages per thread
 constexpr int kChunk = kThr * kPer;  // pages per chunk
+constexpr int kOwnCount = 16;        // up to so many chunks, each listing CTA counts them itself
 
 struct Work {  // the workspace
   long long *rank;    // [n] free pages needed before each item
@@ -92,6 +94,8 @@ __device__ __forceinline__ void load_refs(const PageArgs &a, long long p0, int *
 }
 
 __global__ void __launch_bounds__(kThr) page_count_kernel(const __grid_constant__ PageArgs a) {
+  ptx::launch_dependents();
+  ptx::wait_for_previous();
   const Work w = work_of(a.ws, a.n, a.num_pages);
   int r[kPer];
   load_refs(a, (long long)blockIdx.x * kChunk + kPer * threadIdx.x, r);
@@ -127,6 +131,8 @@ __global__ void __launch_bounds__(kThr) page_list_kernel(const __grid_constant__
   const Work w = work_of(a.ws, a.n, a.num_pages);
   const int tid = threadIdx.x, chunks = page_chunks(a.num_pages);
   const bool compact = !a.forks && !a.spans;
+  ptx::launch_dependents();
+  ptx::wait_for_previous();
   if (blockIdx.x == chunks) {  // the items' ranks
     long long base = 0;
     for (int i0 = 0; i0 < a.n; i0 += kThr) {
@@ -140,10 +146,20 @@ __global__ void __launch_bounds__(kThr) page_list_kernel(const __grid_constant__
     return;
   }
   long long before = 0, all = 0;  // free pages in the chunks before this one, and in all
-  for (int c = tid; c < chunks; c += kThr) {
-    const int n = w.counts[c];
-    all += n;
-    if (c < blockIdx.x) before += n;
+  if (chunks <= kOwnCount) {
+    const int first = blockIdx.x * kChunk;
+#pragma unroll 8
+    for (int p = tid; p < (int)a.num_pages; p += kThr) {
+      const int n = a.refs[p] == 0;
+      all += n;
+      if (p < first) before += n;
+    }
+  } else {
+    for (int c = tid; c < chunks; c += kThr) {
+      const int n = w.counts[c];
+      all += n;
+      if (c < blockIdx.x) before += n;
+    }
   }
   before = block_sum(before);
   all = block_sum(all);
@@ -211,6 +227,8 @@ __device__ __forceinline__ void copy_rows(const PageArgs &a, int lc, long long s
 
 // Item x; slice y = (layer, channel). Slice 0 also writes the child's entries and the counts.
 __global__ void __launch_bounds__(kThr) fork_kernel(const __grid_constant__ PageArgs a) {
+  ptx::launch_dependents();
+  ptx::wait_for_previous();
   const Work w = work_of(a.ws, a.n, a.num_pages);
   const kamera_fork_item f = a.forks[blockIdx.x];
   const int tid = threadIdx.x;
@@ -255,6 +273,8 @@ __global__ void __launch_bounds__(kThr) fork_kernel(const __grid_constant__ Page
 }
 
 __global__ void __launch_bounds__(kThr) extend_kernel(const __grid_constant__ PageArgs a) {
+  ptx::launch_dependents();
+  ptx::wait_for_previous();
   const Work w = work_of(a.ws, a.n, a.num_pages);
   const kamera_page_span s = a.spans[blockIdx.x];
   if (!span_ok(a, s)) {
@@ -276,6 +296,8 @@ __global__ void __launch_bounds__(kThr) extend_kernel(const __grid_constant__ Pa
 }
 
 __global__ void __launch_bounds__(kThr) free_kernel(const __grid_constant__ PageArgs a) {
+  ptx::launch_dependents();
+  ptx::wait_for_previous();
   const kamera_page_span s = a.spans[blockIdx.x];
   if (!span_ok(a, s)) {
     if (threadIdx.x == 0) atomicOr(a.status, KAMERA_DEVICE_BAD_ITEM);
@@ -297,6 +319,8 @@ __global__ void __launch_bounds__(kThr) free_kernel(const __grid_constant__ Page
 // Move k takes the k-th live page above the border to the k-th free page below it. The CTAs
 // walk (move, layer, channel) units; the table and the counts are spread over the grid.
 __global__ void __launch_bounds__(kThr) compact_kernel(const __grid_constant__ PageArgs a) {
+  ptx::launch_dependents();
+  ptx::wait_for_previous();
   const Work w = work_of(a.ws, a.n, a.num_pages);
   const long long moves = w.scalar[1], live = a.num_pages - w.scalar[0];
   const long long gtid = (long long)blockIdx.x * kThr + threadIdx.x;
@@ -321,6 +345,8 @@ __global__ void __launch_bounds__(kThr) compact_kernel(const __grid_constant__ P
 }
 
 __global__ void __launch_bounds__(kThr) copy_kernel(const __grid_constant__ PageArgs a) {
+  ptx::launch_dependents();
+  ptx::wait_for_previous();
   const int nlc = a.lay.L * a.lay.n_ch;
   for (long long u = blockIdx.x; u < (long long)a.n * nlc; u += gridDim.x) {
     const long long k = u / nlc;
@@ -335,11 +361,11 @@ __global__ void __launch_bounds__(kThr) copy_kernel(const __grid_constant__ Page
 
 cudaError_t list_pages(const PageArgs &a, bool ranks, cudaStream_t s) {
   const int chunks = page_chunks(a.num_pages);
-  page_count_kernel<<<chunks, kThr, 0, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  page_list_kernel<<<chunks + (ranks ? 1 : 0), kThr, 0, s>>>(a);
-  return cudaGetLastError();
+  if (chunks > kOwnCount) {
+    const cudaError_t e = launch_early(page_count_kernel, dim3(chunks), kThr, 0, s, a);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_early(page_list_kernel, dim3(chunks + (ranks ? 1 : 0)), kThr, 0, s, a);
 }
 
 constexpr int kGrid = 152 * 8;  // CTAs that walk copy units: eight on each SM
@@ -354,33 +380,29 @@ cudaError_t launch_fork(const PageArgs &a, cudaStream_t s) {
   const cudaError_t e = list_pages(a, true, s);
   if (e != cudaSuccess) return e;
   const int nlc = a.lay.L * a.lay.n_ch;
-  fork_kernel<<<dim3((unsigned)a.n, (unsigned)(nlc < 65535 ? nlc : 65535)), kThr, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_early(fork_kernel, dim3((unsigned)a.n, (unsigned)(nlc < 65535 ? nlc : 65535)), kThr,
+                      0, s, a);
 }
 
 cudaError_t launch_extend(const PageArgs &a, cudaStream_t s) {
   const cudaError_t e = list_pages(a, true, s);
   if (e != cudaSuccess) return e;
-  extend_kernel<<<(unsigned)a.n, kThr, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_early(extend_kernel, dim3((unsigned)a.n), kThr, 0, s, a);
 }
 
 cudaError_t launch_free(const PageArgs &a, cudaStream_t s) {
-  free_kernel<<<(unsigned)a.n, kThr, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_early(free_kernel, dim3((unsigned)a.n), kThr, 0, s, a);
 }
 
 cudaError_t launch_compact(const PageArgs &a, cudaStream_t s) {
   const cudaError_t e = list_pages(a, false, s);
   if (e != cudaSuccess) return e;
-  compact_kernel<<<kGrid, kThr, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_early(compact_kernel, dim3(kGrid), kThr, 0, s, a);
 }
 
 cudaError_t launch_copy_pages(const PageArgs &a, cudaStream_t s) {
   const long long units = (long long)a.n * a.lay.L * a.lay.n_ch;
-  copy_kernel<<<(unsigned)(units < kGrid ? units : kGrid), kThr, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_early(copy_kernel, dim3((unsigned)(units < kGrid ? units : kGrid)), kThr, 0, s, a);
 }
 
 }  // namespace kamera

@@ -363,3 +363,49 @@ def test_norm_at_the_ends_of_the_range(name):
     want = r.want()
     assert r.call() == 0
     r.check(want)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("name", sorted(LAYOUTS))
+def test_many_tokens_with_padding_and_bad_rows(name, in_place):
+    # a warp has several tokens here, among them padding, rows outside the table and slots outside
+    # the pool; sums of squares beyond float32's range in some
+    r = Run(name, [1900, 3, 1, 577], seed=21, apart=True)
+    rs = np.random.RandomState(4)
+    for i in rs.choice(r.T, 40, replace=False):
+        for x in (r.q, r.k):
+            x[i] = x[i] * 2.0 ** 80
+    want = r.want()
+    pad, bad = rs.permutation(r.T)[:200].reshape(2, -1)
+    at = r.tok[1899] // r.lay.page_size
+    lost = (r.req == 0) & (r.tok // r.lay.page_size == at)
+    lost[np.r_[pad, bad]] = False
+    sl = r.slots()
+    r.pool.page_table[0, at] = r.pages + 3
+    r.req[pad], r.req[bad[:50]] = -1, len(r.pt)
+    r.tok[bad[50:]] = r.pt.shape[1] * r.lay.page_size
+    out = r.q if in_place else r.out
+    before = out.clone()
+    assert r.call(out=out) == km.KAMERA_DEVICE_BAD_ITEM | km.KAMERA_DEVICE_SLOT_OOB
+    skip = np.isin(np.arange(r.T), np.r_[pad, bad])
+    r.req[skip], r.tok[skip] = 0, 0
+    r.check(want, rows=np.flatnonzero(~skip & ~lost), q_rows=np.flatnonzero(~skip), out=out)
+    skip = torch.as_tensor(skip)
+    assert torch.equal(out[skip].view(torch.int16), before[skip].view(torch.int16))
+    assert np.all(wl.bf16_bits(r.pk)[1, sl[lost]] == wl.POOL_SENTINEL_BITS)
+
+
+def test_many_keys_alone_and_more_heads_than_fit():
+    # keys alone; and 5 / 7 heads of 128, a lane group without a head in its last turn
+    for hkv, hq in ((4, 28), (5, 35), (7, 7)):
+        LAYOUTS["here"] = (gqa(128, hkv), hq)
+        try:
+            r, r2 = Run("here", [901], seed=23), Run("here", [901], seed=23)
+        finally:
+            del LAYOUTS["here"]
+        assert r.call() == 0
+        r.check(r.want())
+        pos, req, tok = r2.dev()
+        km.kamera_append(r2.h, r2.pool, 1, None, r2.k, r2.v, None, r2.kw, pos, req, tok, r2.eps,
+                         None, r2.st)
+        assert torch.equal(r2.pk.view(torch.int16), r.pk.view(torch.int16))
