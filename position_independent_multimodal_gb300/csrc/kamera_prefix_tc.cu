@@ -33,11 +33,12 @@ namespace kamera {
 
 namespace {
 
-constexpr int kThr = 640;
-constexpr int kLoad = 64;              // threads that load K and V: two tokens each
+constexpr int kThr = 512;
+constexpr int kLoad = 128;             // threads that load K and V: a token each
 constexpr int kTok = 128;              // tokens per tile
 constexpr int kRow = 128;              // query rows per MMA
 constexpr int kChunk = kTok * 128;     // bytes of a 128 x 64 bf16 operand tile
+constexpr int kRegsSoft = 184, kRegsRest = 72;  // a thread; 8 warps each: 65536, as at the launch
 constexpr int kMasks = 8;              // tiles whose token masks are kept
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
@@ -50,11 +51,10 @@ struct Shape {
   static constexpr int q = 0;
   static constexpr int ring = QT * DK * kChunk;
   static constexpr int mask = ring + NST * kStage;  // uint32 [kMasks][4]
-  static constexpr int xch = mask + kMasks * 16;    // float [2][2][kRow]: maxima, then sums
-  static constexpr int bar = xch + 4 * kRow * 4;
-  // mbarriers
+  static constexpr int bar = mask + kMasks * 16;
+  // mbarriers; those of P: [buffer][half of the tokens]
   static constexpr int full = 0, empty = NST, q_full = empty + NST, q_empty = q_full + 1,
-                       s_full = q_empty + 1, p_full = s_full + 2, pv_done = p_full + 2,
+                       s_full = q_empty + 1, p_full = s_full + 2, pv_done = p_full + 4,
                        o_free = pv_done + 2, o_full = o_free + 2,
                        mk_full = o_full + 2, last = mk_full + kMasks, n_bar = last + 1;
   static constexpr int misc = bar + n_bar * 8;  // TMEM address, give-up flag
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
     if (tid == 0) atomicOr(a.status, KAMERA_DEVICE_TIMEOUT);
     return;
   }
-  if (warp == 18) {
+  if (warp == 12) {
     ptx::tmem_alloc(sb + S::misc, 512);
     ptx::tmem_relinquish();
   }
@@ -153,9 +153,10 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
     ptx::mbar_init(bar(S::q_empty), 1);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bar(S::s_full + i), 1);
-      ptx::mbar_init(bar(S::p_full + i), 256);
+      ptx::mbar_init(bar(S::p_full + 2 * i), 128);
+      ptx::mbar_init(bar(S::p_full + 2 * i + 1), 128);
       ptx::mbar_init(bar(S::pv_done + i), 1);
-      ptx::mbar_init(bar(S::o_free + i), 256);
+      ptx::mbar_init(bar(S::o_free + i), 128);
       ptx::mbar_init(bar(S::o_full + i), 1);
     }
     for (int i = 0; i < kMasks; ++i) ptx::mbar_init(bar(S::mk_full + i), kLoad / 32);
@@ -174,66 +175,73 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
   walk.start(a, plan, blockIdx.x);
   Segment s;
 
-  if (warp < 16) {
-    // ---- softmax: thread = half of a query row ----
-    const int w = S::QT == 2 ? warp >> 3 : 0;      // query tile (QT 1: warps 8-15 have none)
-    const int hf = (warp >> 2) & 1;                // half of the tokens, of O's columns
+  if (warp < 8) {
+    // ---- softmax: thread = query row ----
+    ptx::regs_more<kRegsSoft>();
+    const int w = warp >> 2;  // query tile (QT 1: warps 4-7 have none)
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const float c = fabsf(a.scale) * kLog2e;
     const bool flip = a.scale < 0.f;
     const float neg_inf = -__int_as_float(0x7f800000);
-    const uint32_t o_t = tmem + S::o_col + w * 128 + hf * (S::DV * 32) + lane_off;
+    const uint32_t o_t = tmem + S::o_col + w * 128 + lane_off;
     const uint32_t pv = bar(S::pv_done + w);
-    float *xch = reinterpret_cast<float *>(smem + S::xch);
-    // the two warps of a row's threads
-    auto pair_sync = [&]() {
-      asm volatile("bar.sync %0, 64;" ::"r"(2 + w * 4 + (warp & 3)) : "memory");
-    };
     uint32_t s_ph = 0;   // parity of each S buffer
     uint32_t o_ph = 0;   // parity of o_full
     uint32_t tiles = 0;  // tiles of this query tile so far (phases of pv_done)
     uint32_t seen = 0;   // tiles the loader has masked so far
     while (walk.next(a, plan, &s)) {
       const int n = tiles_of(s.tok0, s.tok1, kTok);
-      if (S::QT == 2 ? (w == 1 && s.rows <= kRow) : warp >= 8) {
+      if (w == 1 && (S::QT == 1 || s.rows <= kRow)) {
         seen += n;
         continue;
       }
       const bool live = kRow * w + (row & ~31) < s.rows;  // a warp without rows only keeps step
       float m = neg_inf, l = 0.f;
+      uint4 msk = make_uint4(0, 0, 0, 0);
+      auto read_mask = [&]() {
+        const int mk = seen % kMasks;
+        wait(bar(S::mk_full) + 8 * mk, (seen / kMasks) & 1);
+        __syncwarp();
+        msk = *reinterpret_cast<const uint4 *>(smem + S::mask + 16 * mk);
+      };
       for (int i = 0; i < n; ++i, ++seen, ++tiles) {
+        // the tile's mask. It is there before S is; of a segment's first tile it is read after
+        // S, as this thread may be more tiles ahead of the loader than masks are kept
+        if (live && i > 0) read_mask();
         const int b = S::QT == 2 ? w : (tiles & 1);
         wait(bar(S::s_full) + 8 * b, (s_ph >> b) & 1);
         __syncwarp();
         s_ph ^= 1u << b;
         ptx::tc_fence_after();
         if (live) {
-          const uint32_t st = tmem + b * 128 + hf * 64 + lane_off;
-          uint32_t x[32];
+          const uint32_t st = tmem + b * 128 + lane_off;
+          uint32_t x[kTok];
           ptx::tmem_ld32(st, x);
-          const int mk = seen % kMasks;
-          wait(bar(S::mk_full) + 8 * mk, (seen / kMasks) & 1);
-          __syncwarp();
-          const uint2 msk = *reinterpret_cast<const uint2 *>(smem + S::mask + 16 * mk + 8 * hf);
-          const bool whole = (msk.x & msk.y) == 0xffffffffu;
-          // pass 1: the maximum
+          ptx::tmem_ld32(st + 32, x + 32);
+          if (i == 0) read_mask();
+          const bool whole = (msk.x & msk.y & msk.z & msk.w) == 0xffffffffu;
+          const uint32_t bits[4] = {msk.x, msk.y, msk.z, msk.w};
+          // the maximum
           float top = neg_inf;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            if (j) ptx::tmem_ld32(st + 32, x);
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) ptx::tmem_ld_wait(x + e);
+            for (int e = 0; e < 64; e += 8) ptx::tmem_ld_wait(x + 64 * j + e);
+            if (j == 0) {
+              ptx::tmem_ld32(st + 64, x + 64);
+              ptx::tmem_ld32(st + 96, x + 96);
+            }
             if (!whole || flip) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
+              for (int e = 64 * j; e < 64 * j + 64; ++e) {
                 const float y = __uint_as_float(x[e]);
-                top = ((j ? msk.y : msk.x) >> e) & 1 ? fmaxf(top, flip ? -y : y) : top;
+                top = (bits[e >> 5] >> (e & 31)) & 1 ? fmaxf(top, flip ? -y : y) : top;
               }
             } else {
               float m0 = top, m1 = top, m2 = top, m3 = top;
 #pragma unroll
-              for (int e = 0; e < 32; e += 8) {
+              for (int e = 64 * j; e < 64 * j + 64; e += 8) {
                 m0 = fmaxf(fmaxf(m0, __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
                 m1 = fmaxf(fmaxf(m1, __uint_as_float(x[e + 2])), __uint_as_float(x[e + 3]));
                 m2 = fmaxf(fmaxf(m2, __uint_as_float(x[e + 4])), __uint_as_float(x[e + 5]));
@@ -242,11 +250,6 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
               top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
             }
           }
-          // the row's other half
-          float *mine = xch + ((b * 2 + hf) << 7) + row;
-          *mine = top;
-          pair_sync();
-          top = fmaxf(top, xch[((b * 2 + (hf ^ 1)) << 7) + row]);
           const bool first = m == neg_inf && top > neg_inf;
           const bool raise = first || (top - m) * c > 8.f;
           if (__any_sync(0xffffffffu, raise)) {
@@ -260,7 +263,7 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
               ptx::tc_fence_after();
               l *= f;
 #pragma unroll 1
-              for (int j = 0; j < S::DV * 2; ++j) {
+              for (int j = 0; j < S::DV * 4; ++j) {
                 uint32_t y[16];
                 ptx::tmem_ld16(o_t + 16 * j, y);
                 ptx::tmem_ld_wait(y);
@@ -275,27 +278,23 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
           const float cs = flip ? -c : c;
           const f32x2 c2 = f2(cs, cs), nb2 = f2(-base, -base);
           f32x2 la = f2(0.f, 0.f), lb = la;
-          // pass 2, the second half of S first (it is still in registers). Two copies of the loop:
-          // a test of the mask at each weight would cost as much as the weight
+          // the weights, over S. P V of the first half starts during the second. Two copies of the
+          // loop: a test of the mask at each weight would cost as much as the weight
           auto weights = [&](auto masked) {
 #pragma unroll
-            for (int j = 1; j >= 0; --j) {
-              if (j == 0) {
-                ptx::tmem_ld32(st, x);
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) ptx::tmem_ld_wait(x + e);
-              }
+            for (int j = 0; j < 4; ++j) {
               uint32_t h[16];
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
                 float p0, p1;
-                f2_split(fma2(f2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, nb2), p0,
-                         p1);
+                f2_split(fma2(f2(__uint_as_float(x[32 * j + e]), __uint_as_float(x[32 * j + e + 1])),
+                              c2, nb2),
+                         p0, p1);
                 p0 = exp2_approx(p0);
                 p1 = exp2_approx(p1);
                 if (masked.v) {
-                  p0 = ((j ? msk.y : msk.x) >> e) & 1 ? p0 : 0.f;
-                  p1 = ((j ? msk.y : msk.x) >> (e + 1)) & 1 ? p1 : 0.f;
+                  p0 = (bits[j] >> e) & 1 ? p0 : 0.f;
+                  p1 = (bits[j] >> (e + 1)) & 1 ? p1 : 0.f;
                 }
                 if (e & 2)
                   lb = add2(lb, f2(p0, p1));
@@ -303,7 +302,12 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
                   la = add2(la, f2(p0, p1));
                 h[e / 2] = pack_bf16(p0, p1);
               }
-              ptx::tmem_st16(st + 32 + 16 * j, h);  // over the second half
+              ptx::tmem_st16(st + 16 * j, h);
+              if (j == 1) {
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
+                arrive(bar(S::p_full) + 16 * b);
+              }
             }
           };
           if (whole)
@@ -314,26 +318,24 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
           f2_split(add2(la, lb), l0, l1);
           l += l0 + l1;
           ptx::tmem_st_wait();
+        } else {
+          arrive(bar(S::p_full) + 16 * b);
         }
         ptx::tc_fence_before();
-        arrive(bar(S::p_full) + 8 * b);
+        arrive(bar(S::p_full) + 16 * b + 8);
       }
       wait(bar(S::o_full + w), o_ph);
       o_ph ^= 1;
       __syncwarp();
       ptx::tc_fence_after();
       if (live) {
-        xch[((w * 2 + hf) << 7) + row] = l;
-        pair_sync();
-        l += xch[((w * 2 + (hf ^ 1)) << 7) + row];
-        pair_sync();  // read before the next segment writes
         const int i = kRow * w + row;
         float *o = nullptr, *lse = nullptr;
-        if (i < s.rows) segment_out<0>(a, plan, s, blockIdx.x, i, hf == 0, &o, &lse);
+        if (i < s.rows) segment_out<0>(a, plan, s, blockIdx.x, i, true, &o, &lse);
         const bool ok = l != 0.f && !*gave_up;
         const float inv = 1.f / l;
 #pragma unroll 1
-        for (int j = 0; j < S::DV; ++j) {
+        for (int j = 0; j < S::DV * 2; ++j) {
           uint32_t r[32];
           ptx::tmem_ld32(o_t + 32 * j, r);
 #pragma unroll
@@ -346,20 +348,21 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
               v.y = ok ? __uint_as_float(r[e + 1]) * inv : 0.f;
               v.z = ok ? __uint_as_float(r[e + 2]) * inv : 0.f;
               v.w = ok ? __uint_as_float(r[e + 3]) * inv : 0.f;
-              *reinterpret_cast<float4 *>(o + hf * (S::DV * 32) + 32 * j + e) = v;
+              *reinterpret_cast<float4 *>(o + 32 * j + e) = v;
             }
           }
         }
-        if (o && hf == 0) *lse = ok ? (m * c + log2f(l)) * kLn2 : neg_inf;
+        if (o) *lse = ok ? (m * c + log2f(l)) * kLn2 : neg_inf;
       }
       ptx::tc_fence_before();
       arrive(bar(S::o_free + w));
     }
-  } else if (warp < 18) {
-    // ---- K and V rows into the ring. A warp brings 64 tokens of each tile, a lane two of them:
-    // t0 and t0 + 32. Copies by tensor map are issued by one thread of the warp, which stands in
-    // for the others' arrivals ----
-    const int half = warp & 1, t0 = 64 * half + lane;
+  } else if (warp < 12) {
+    ptx::regs_fewer<kRegsRest>();
+    // ---- K and V rows into the ring: a warp brings 32 tokens of each tile, a lane holds the slot
+    // of one. Copies by tensor map are issued by one thread of the warp, which stands in for the
+    // others' arrivals: four warps, because one issues a copy in about 100 cycles ----
+    const int part = warp & 3, t0 = 32 * part + lane;
     const bool gqa = lay.kind == KAMERA_GQA;
     const __nv_bfloat16 *lk = a.pool.k + (long long)a.layer * a.pool.num_slots * lay.row_k;
     const __nv_bfloat16 *lv =
@@ -367,42 +370,42 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
     const int vrow = gqa ? lay.row_v : lay.row_k;
     uint32_t *masks = reinterpret_cast<uint32_t *>(smem + S::mask);
     const int piece = lane & 7;  // cp.async: 16-byte piece of a row
-    const int box = maps.box, boxes = box == kTok ? 1 - half : (box ? 64 / box : 0);
-    Place<S::NST> at;       // the next stage
-    uint32_t tile_no = 0;   // tiles so far
+    const int box = maps.box;    // slots of a copy; boxes: copies of this warp per 64 columns
+    const int boxes = box == 0 ? 0 : (box <= 32 ? 32 / box : 32 * part % box == 0);
+    Place<S::NST> at;            // the next stage
+    uint32_t tile_no = 0;        // tiles so far
     while (walk.next(a, plan, &s)) {
       const int n = tiles_of(s.tok0, s.tok1, kTok), a0 = s.tok0 / kTok;
       const int kcol = gqa ? s.kvh * lay.hd : 0;
       const int vcol = gqa ? kcol : s.half * (S::DV * 64);
-      auto token = [&](int i, int k) {  // below 2^31: the tile starts below it
-        const int tok = (a0 + i) * kTok + t0 + 32 * k;
+      auto token = [&](int i) {  // below 2^31: the tile starts below it
+        const int tok = (a0 + i) * kTok + t0;
         return tok >= s.tok0 && tok < s.tok1 ? tok : -1;
       };
-      auto page_at = [&](int i, int k) {
-        const int tok = token(i, k);
+      auto page_at = [&](int i) {
+        const int tok = token(i);
         return tok >= 0 ? load_page(a, s.lead, tok) : 0;
       };
-      // The next stages: `chunks` chunks from column `col` of a tile's rows, whose slots are this
-      // lane's s0 and s1 and the other lanes'; whole: every token is in.
+      // The next stages: `chunks` chunks from column `col` of a tile's rows, whose slots the lanes
+      // have; whole: every token is in.
       auto issue = [&](const void *map, const __nv_bfloat16 *rows, int row, int col, int chunks,
-                       int s0, int s1, bool whole) {
+                       int slot, bool whole) {
         if (box && whole) {
-          int y[8];  // first slots of the copies
+          int y[4];  // first slots of the copies
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            y[k] = __shfl_sync(0xffffffffu, k * box < 32 ? s0 : s1, (k * box) & 31);
+          for (int k = 0; k < 4; ++k) y[k] = __shfl_sync(0xffffffffu, slot, (k * box) & 31);
           if (ptx::elect_one()) {
             Place<S::NST> to = at;
             for (int u = 0; u < chunks / S::UC; ++u) {
               const uint32_t full = bar(S::full) + 8 * to.st;
-              uint32_t dst = sb + S::ring + to.st * S::kStage + half * 64 * 128;
+              uint32_t dst = sb + S::ring + to.st * S::kStage + part * 32 * 128;
               wait(bar(S::empty) + 8 * to.st, to.ph ^ 1);
               if (dead) break;
               if (boxes) {
                 ptx::mbar_arrive_n(full, 31);
                 ptx::mbar_arrive_expect_tx(full, boxes * box * S::UC * 128);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < 4; ++k) {
                   if (k < boxes) {
 #pragma unroll
                     for (int c = 0; c < S::UC; ++c)
@@ -429,10 +432,10 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
             continue;
           }
           const __nv_bfloat16 *src = rows + col + u * S::UC * 64 + 8 * piece;
-#pragma unroll 4
-          for (int j = 0; j < 16; ++j) {  // four of this warp's 64 tokens at a time
-            const int q = 4 * j + (lane >> 3), t = 64 * half + q;
-            const int sl = __shfl_sync(0xffffffffu, j < 8 ? s0 : s1, q & 31);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {  // four of this warp's tokens at a time
+            const int q = 4 * j + (lane >> 3), t = 32 * part + q;
+            const int sl = __shfl_sync(0xffffffffu, slot, q);
             const __nv_bfloat16 *p = sl >= 0 ? src + (long long)sl * row : a.pool.k;
 #pragma unroll
             for (int k = 0; k < S::UC; ++k)
@@ -442,43 +445,38 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
           ptx::cp_async_mbar_arrive(full);
         }
       };
-      int p0 = page_at(0, 0), p1 = page_at(0, 1);  // of the next tile, not looked at yet
-      int k0 = 0, k1 = 0;                          // slots of the last K tile
+      int page = page_at(0);  // of the next tile, not looked at yet
+      int k_slot = 0;         // of the last K tile
       bool whole = false;
       auto load_k = [&](int i) {
-        const int tok0 = token(i, 0), tok1 = token(i, 1);
-        k0 = tok0 >= 0 ? slot_in(a, p0, tok0) : -1;
-        k1 = tok1 >= 0 ? slot_in(a, p1, tok1) : -1;
-        if (i + 1 < n) {  // ahead of its use
-          p0 = page_at(i + 1, 0);
-          p1 = page_at(i + 1, 1);
-        }
+        const int tok = token(i);
+        k_slot = tok >= 0 ? slot_in(a, page, tok) : -1;
+        if (i + 1 < n) page = page_at(i + 1);  // ahead of its use
         const int mk = tile_no++ % kMasks;
-        const uint32_t b0 = __ballot_sync(0xffffffffu, k0 >= 0);
-        const uint32_t b1 = __ballot_sync(0xffffffffu, k1 >= 0);
+        const uint32_t bits = __ballot_sync(0xffffffffu, k_slot >= 0);
         if (lane == 0) {
-          masks[4 * mk + 2 * half] = b0;
-          masks[4 * mk + 2 * half + 1] = b1;
+          masks[4 * mk + part] = bits;
           arrive(bar(S::mk_full) + 8 * mk);
         }
         __syncwarp();
-        asm volatile("bar.sync 1, 64;" ::: "memory");
+        asm volatile("bar.sync 1, 128;" ::: "memory");
         const uint4 m = *reinterpret_cast<const uint4 *>(masks + 4 * mk);
         whole = (m.x & m.y & m.z & m.w) == 0xffffffffu;
-        issue(&maps.k, lk, lay.row_k, kcol, S::DK, k0, k1, whole);
+        issue(&maps.k, lk, lay.row_k, kcol, S::DK, k_slot, whole);
       };
       load_k(0);
       for (int i = 0; i < n; ++i) {
-        const int v0 = k0, v1 = k1;  // V of this tile may come after K of the next
-        const bool vw = whole;
+        const int v_slot = k_slot;  // V of this tile may come after K of the next
+        const bool v_whole = whole;
         if (S::QT == 1 && i + 1 < n) load_k(i + 1);
-        issue(&maps.v, lv, vrow, vcol, S::DV, v0, v1, vw);
+        issue(&maps.v, lv, vrow, vcol, S::DV, v_slot, v_whole);
         if (S::QT == 2 && i + 1 < n) load_k(i + 1);
       }
     }
     ptx::cp_async_wait_all();
   } else {
-    // ---- MMAs (warp 18) and Q (warp 19), one thread each. QT 2: S and P V of the two query tiles
+    ptx::regs_fewer<kRegsRest>();
+    // ---- MMAs (warp 12) and Q (warp 13), one thread each. QT 2: S and P V of the two query tiles
     // in turn, so that the tensor core works on one during the softmax of the other; QT 1: S of a
     // tile before P V of the one before it. Issuing an MMA takes a few instructions only: the
     // descriptors of a tile's steps differ by constants ----
@@ -496,10 +494,10 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
         ptx::tma_3d(sb + S::q + c * S::QT * kChunk, s.own ? &maps.q_own : &maps.q_group, c * 64, y,
                     z, bar(S::q_full));
     };
-    if (warp == 19) {
+    if (warp == 13) {
       if (ptx::elect_one())
         while (walk.next(a, plan, &s)) load_q();
-    } else if (ptx::elect_one()) {
+    } else if (warp == 12 && ptx::elect_one()) {
       constexpr uint32_t id_s = 1u << 4 | 1u << 7 | 1u << 10 | (kTok >> 3) << 17 | (kRow >> 4) << 24;
       // V is MN-major
       constexpr uint32_t id_o =
@@ -537,9 +535,8 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
         ptx::mma_commit(bar(S::s_full) + 8 * b);
         if (ends.v & 2) kp = at;
       };
-      // O of query tile t (+)= P in buffer b times the V tile at vp
+      // O of query tile t (+)= P in buffer b, [128][tokens], times the V tile at vp
       auto mma_o = [&](auto t, uint32_t b, bool first_tile, bool last_tile, auto ends) {
-        // P of tokens 0-63 in columns 32-63 of S, of 64-127 in 96-127
         const uint32_t p = tmem + b * 128, d = tmem + S::o_col + t.v * 128;
         Place<S::NST> at = vp;
         if (ends.v & 1) landed(at);  // before P is, as a rule
@@ -550,8 +547,7 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
           }
           o_any |= 1u << t.v;
         }
-        wait(bar(S::p_full) + 8 * b, (p_ph >> b) & 1);
-        p_ph ^= 1u << b;
+        wait(bar(S::p_full) + 16 * b, (p_ph >> b) & 1);
         if (dead) return;
         ptx::tc_fence_after();
 #pragma unroll
@@ -560,12 +556,19 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
           if (dead) return;
           const uint32_t v = desc_mn(ring + at.st * S::kStage);
 #pragma unroll
-          for (int x = 0; x < kTok / 16; ++x)
-            ptx::mma_bf16_ta(d + u * S::UC * 64, p + 32 + 8 * x + (x < 4 ? 0 : 32), desc(v + x * (2048 >> 4)), id_o,
+          for (int x = 0; x < kTok / 16; ++x) {
+            if (u == 0 && x == kTok / 32) {
+              wait(bar(S::p_full) + 16 * b + 8, (p_ph >> b) & 1);
+              if (dead) return;
+              ptx::tc_fence_after();
+            }
+            ptx::mma_bf16_ta(d + u * S::UC * 64, p + 8 * x, desc(v + x * (2048 >> 4)), id_o,
                              x ? 1u : (first_tile ? 0u : 1u));
+          }
           if (ends.v & 2) ptx::mma_commit(bar(S::empty) + 8 * at.st);
           at.advance(1);
         }
+        p_ph ^= 1u << b;
         ptx::mma_commit(bar(S::pv_done + t.v));
         if (last_tile) ptx::mma_commit(bar(S::o_full + t.v));
         if (ends.v & 2) vp = at;
@@ -640,7 +643,7 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
     }
     __syncthreads();
   }
-  if (warp == 18) ptx::tmem_dealloc(tmem, 512);
+  if (warp == 12) ptx::tmem_dealloc(tmem, 512);
 }
 
 template <class S>

@@ -150,6 +150,18 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const void *map, int x, int
       : "memory");
 }
 
+// ---- registers ----
+// The warps of a warpgroup (four from a multiple of four) take kRegs registers a thread each. The
+// shares of all warps of the block may not exceed the registers it was launched with.
+template <int kRegs>
+__device__ __forceinline__ void regs_more() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_fewer() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 // True in one thread of a converged warp. The compiler knows that at most one thread runs what
 // the result guards, so operands that an instruction takes in uniform registers (tcgen05.mma)
 // go there directly, without a loop over the threads that might differ.
