@@ -53,11 +53,13 @@ struct PrefixPlan {
 __host__ __device__ inline PrefixPlan prefix_plan(const PrefixShape &sh, void *ws, long long R,
                                                   int hq, int dv) {
   PrefixPlan p;
-  unsigned char *b = static_cast<unsigned char *>(ws);
+  // partial outputs are written by whole 32-byte sectors
+  const size_t skew = static_cast<size_t>(-reinterpret_cast<intptr_t>(ws)) & 31;
+  unsigned char *b = static_cast<unsigned char *>(ws) + skew;
   size_t o = 0;
   auto take = [&](size_t bytes) {
     unsigned char *at = b + o;
-    o += (bytes + 15) & ~static_cast<size_t>(15);
+    o += (bytes + 31) & ~static_cast<size_t>(31);
     return at;
   };
   auto i64 = [&]() { return reinterpret_cast<long long *>(take(8 * R)); };
@@ -91,7 +93,7 @@ __host__ __device__ inline PrefixPlan prefix_plan(const PrefixShape &sh, void *w
   p.home_lse = f32(4 * R * hq);
   p.home_more = reinterpret_cast<int2 *>(take(32 * R * hq));
   p.home_o = f32(2 * R * hq * dv);
-  p.total = o;
+  p.total = o + 16;  // the workspace is 16-byte aligned
   return p;
 }
 

@@ -33,25 +33,25 @@ namespace kamera {
 
 namespace {
 
-constexpr int kThr = 512;
-constexpr int kLoad = 128;             // threads that load K and V: a token each
 constexpr int kTok = 128;              // tokens per tile
 constexpr int kRow = 128;              // query rows per MMA
 constexpr int kChunk = kTok * 128;     // bytes of a 128 x 64 bf16 operand tile
-constexpr int kRegsSoft = 184, kRegsRest = 72;  // a thread; 8 warps each: 65536, as at the launch
 constexpr int kMasks = 8;              // tiles whose token masks are kept
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
 // DK, DV: 64-column chunks of K and of the CTA's V columns; QT: tiles of query rows; UC: chunks
-// per ring stage; NST: ring stages.
-template <int DK_, int DV_, int QT_, int UC_, int NST_>
+// per ring stage; NST: ring stages; NL: warps that load K and V.
+template <int DK_, int DV_, int QT_, int UC_, int NST_, int NL_>
 struct Shape {
-  static constexpr int DK = DK_, DV = DV_, QT = QT_, UC = UC_, NST = NST_;
+  static constexpr int DK = DK_, DV = DV_, QT = QT_, UC = UC_, NST = NST_, NL = NL_;
+  static constexpr int kSoft = 8 * QT, kMma = kSoft + NL, kQ = kMma + 1;  // warps: the first
+  static constexpr int kThr = 32 * (kQ + 1);
   static constexpr int kStage = UC * kChunk;
   static constexpr int q = 0;
   static constexpr int ring = QT * DK * kChunk;
   static constexpr int mask = ring + NST * kStage;  // uint32 [kMasks][4]
-  static constexpr int bar = mask + kMasks * 16;
+  static constexpr int xch = mask + kMasks * 16;    // float [2][2][kRow]: maxima, then sums
+  static constexpr int bar = xch + 4 * kRow * 4;
   // mbarriers; those of P: [buffer][half of the tokens]
   static constexpr int full = 0, empty = NST, q_full = empty + NST, q_empty = q_full + 1,
                        s_full = q_empty + 1, p_full = s_full + 2, pv_done = p_full + 4,
@@ -64,9 +64,9 @@ struct Shape {
   static_assert(DK % UC == 0 && DV % UC == 0, "whole stages");
 };
 
-using Gqa128 = Shape<2, 2, 2, 2, 5>;
-using Gqa64 = Shape<1, 1, 2, 1, 12>;
-using Mla512 = Shape<9, 4, 1, 1, 5>;
+using Gqa128 = Shape<2, 2, 2, 2, 5, 2>;
+using Gqa64 = Shape<1, 1, 2, 1, 12, 2>;
+using Mla512 = Shape<9, 4, 1, 1, 5, 4>;
 
 // Tensor maps of a call: pool rows of the layer (boxes of 64 columns and `box` slots) and query
 // rows (64 columns; a block of a group's rows, or one request's).
@@ -107,8 +107,8 @@ __device__ __forceinline__ uint64_t desc(uint32_t lo) {
 }
 
 template <class S>
-__global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constant__ PrefixArgs a,
-                                                          const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
+    const __grid_constant__ PrefixArgs a, const __grid_constant__ Maps maps) {
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t sb = ptx::smem_addr(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -140,13 +140,13 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
     if (tid == 0) atomicOr(a.status, KAMERA_DEVICE_TIMEOUT);
     return;
   }
-  if (warp == 12) {
+  if (warp == S::kMma) {
     ptx::tmem_alloc(sb + S::misc, 512);
     ptx::tmem_relinquish();
   }
   if (tid == 0) {
     for (int i = 0; i < S::NST; ++i) {
-      ptx::mbar_init(bar(S::full + i), kLoad);
+      ptx::mbar_init(bar(S::full + i), 32 * S::NL);
       ptx::mbar_init(bar(S::empty + i), 1);
     }
     ptx::mbar_init(bar(S::q_full), 1);
@@ -156,13 +156,17 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
       ptx::mbar_init(bar(S::p_full + 2 * i), 128);
       ptx::mbar_init(bar(S::p_full + 2 * i + 1), 128);
       ptx::mbar_init(bar(S::pv_done + i), 1);
-      ptx::mbar_init(bar(S::o_free + i), 128);
+      ptx::mbar_init(bar(S::o_free + i), 256);
       ptx::mbar_init(bar(S::o_full + i), 1);
     }
-    for (int i = 0; i < kMasks; ++i) ptx::mbar_init(bar(S::mk_full + i), kLoad / 32);
+    for (int i = 0; i < kMasks; ++i) ptx::mbar_init(bar(S::mk_full + i), S::NL);
     ptx::mbar_init(bar(S::last), 1);
     ptx::fence_mbar_init();
     *gave_up = 0;
+    ptx::prefetch_map(&maps.k);
+    ptx::prefetch_map(&maps.v);
+    ptx::prefetch_map(&maps.q_group);
+    ptx::prefetch_map(&maps.q_own);
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -173,37 +177,43 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
   ptx::launch_dependents();  // who starts from here on finds the plan complete
   SegmentWalk<0> walk;
   walk.start(a, plan, blockIdx.x);
-  Segment s;
+  // the segment that follows is looked up while this one's first copies are on their way
+  Segment s, after;
+  bool more = walk.next(a, plan, &after);
 
-  if (warp < 8) {
-    // ---- softmax: thread = query row ----
-    ptx::regs_more<kRegsSoft>();
-    const int w = warp >> 2;  // query tile (QT 1: warps 4-7 have none)
+  if (warp < S::kSoft) {
+    // ---- softmax: thread = half of a query row ----
+    const int w = warp >> 3;                       // query tile
+    const int hf = (warp >> 2) & 1;                // half of the tokens, of O's columns
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const float c = fabsf(a.scale) * kLog2e;
     const bool flip = a.scale < 0.f;
     const float neg_inf = -__int_as_float(0x7f800000);
-    const uint32_t o_t = tmem + S::o_col + w * 128 + lane_off;
+    const uint32_t o_t = tmem + S::o_col + w * 128 + hf * (S::DV * 32) + lane_off;
     const uint32_t pv = bar(S::pv_done + w);
+    float *xch = reinterpret_cast<float *>(smem + S::xch);
+    const int pair = 2 + w * 4 + (warp & 3);  // named barrier of a row's two warps
     uint32_t s_ph = 0;   // parity of each S buffer
     uint32_t o_ph = 0;   // parity of o_full
     uint32_t tiles = 0;  // tiles of this query tile so far (phases of pv_done)
     uint32_t seen = 0;   // tiles the loader has masked so far
-    while (walk.next(a, plan, &s)) {
+    while (more) {
+      s = after;
+      more = walk.next(a, plan, &after);
       const int n = tiles_of(s.tok0, s.tok1, kTok);
-      if (w == 1 && (S::QT == 1 || s.rows <= kRow)) {
+      if (w == 1 && s.rows <= kRow) {
         seen += n;
         continue;
       }
       const bool live = kRow * w + (row & ~31) < s.rows;  // a warp without rows only keeps step
       float m = neg_inf, l = 0.f;
-      uint4 msk = make_uint4(0, 0, 0, 0);
+      uint2 msk = make_uint2(0, 0);
       auto read_mask = [&]() {
         const int mk = seen % kMasks;
         wait(bar(S::mk_full) + 8 * mk, (seen / kMasks) & 1);
         __syncwarp();
-        msk = *reinterpret_cast<const uint4 *>(smem + S::mask + 16 * mk);
+        msk = *reinterpret_cast<const uint2 *>(smem + S::mask + 16 * mk + 8 * hf);
       };
       for (int i = 0; i < n; ++i, ++seen, ++tiles) {
         // the tile's mask. It is there before S is; of a segment's first tile it is read after
@@ -215,44 +225,63 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
         s_ph ^= 1u << b;
         ptx::tc_fence_after();
         if (live) {
-          const uint32_t st = tmem + b * 128 + lane_off;
-          uint32_t x[kTok];
+          const uint32_t st = tmem + b * 128 + hf * 64 + lane_off;
+          uint32_t x[64];
           ptx::tmem_ld32(st, x);
           ptx::tmem_ld32(st + 32, x + 32);
           if (i == 0) read_mask();
-          const bool whole = (msk.x & msk.y & msk.z & msk.w) == 0xffffffffu;
-          const uint32_t bits[4] = {msk.x, msk.y, msk.z, msk.w};
-          // the maximum
-          float top = neg_inf;
+          const bool whole = (msk.x & msk.y) == 0xffffffffu;
+          const float cs = flip ? -c : c;
+          const f32x2 c2 = f2(cs, cs);
+          float base = m > neg_inf ? m * c : 0.f;
+          f32x2 la, lb;
+          uint32_t h[32];
+          float top = neg_inf, top2 = neg_inf;
+          // the weights against `base`, their sums in la and lb, the maximum on the way. Two
+          // copies of the loop: a test of the mask at each weight would cost as much as the weight
+          auto weights = [&](auto masked) {
+            const f32x2 nb2 = f2(-base, -base);
+            la = lb = f2(0.f, 0.f);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-#pragma unroll
-            for (int e = 0; e < 64; e += 8) ptx::tmem_ld_wait(x + 64 * j + e);
-            if (j == 0) {
-              ptx::tmem_ld32(st + 64, x + 64);
-              ptx::tmem_ld32(st + 96, x + 96);
-            }
-            if (!whole || flip) {
-#pragma unroll
-              for (int e = 64 * j; e < 64 * j + 64; ++e) {
-                const float y = __uint_as_float(x[e]);
-                top = (bits[e >> 5] >> (e & 31)) & 1 ? fmaxf(top, flip ? -y : y) : top;
+            for (int e = 0; e < 64; e += 2) {
+              const float y0 = __uint_as_float(x[e]), y1 = __uint_as_float(x[e + 1]);
+              const bool in0 = ((e < 32 ? msk.x : msk.y) >> (e & 31)) & 1;
+              const bool in1 = ((e < 32 ? msk.x : msk.y) >> ((e & 31) + 1)) & 1;
+              float p0, p1;
+              f2_split(fma2(f2(y0, y1), c2, nb2), p0, p1);
+              p0 = exp2_approx(p0);
+              p1 = exp2_approx(p1);
+              if (masked.v) {
+                p0 = in0 ? p0 : 0.f;
+                p1 = in1 ? p1 : 0.f;
+                top = in0 ? fmaxf(top, flip ? -y0 : y0) : top;
+                top = in1 ? fmaxf(top, flip ? -y1 : y1) : top;
+              } else {
+                float &t = e & 2 ? top2 : top;
+                t = fmaxf(fmaxf(t, y0), y1);
               }
-            } else {
-              float m0 = top, m1 = top, m2 = top, m3 = top;
-#pragma unroll
-              for (int e = 64 * j; e < 64 * j + 64; e += 8) {
-                m0 = fmaxf(fmaxf(m0, __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
-                m1 = fmaxf(fmaxf(m1, __uint_as_float(x[e + 2])), __uint_as_float(x[e + 3]));
-                m2 = fmaxf(fmaxf(m2, __uint_as_float(x[e + 4])), __uint_as_float(x[e + 5]));
-                m3 = fmaxf(fmaxf(m3, __uint_as_float(x[e + 6])), __uint_as_float(x[e + 7]));
-              }
-              top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+              if (e & 2)
+                lb = add2(lb, f2(p0, p1));
+              else
+                la = add2(la, f2(p0, p1));
+              h[e / 2] = pack_bf16(p0, p1);
             }
-          }
-          const bool first = m == neg_inf && top > neg_inf;
-          const bool raise = first || (top - m) * c > 8.f;
-          if (__any_sync(0xffffffffu, raise)) {
+            top = fmaxf(top, top2);
+          };
+          ptx::tmem_ld_wait_all<64>(x);
+          if (whole && !flip)
+            weights(Int<0>());
+          else
+            weights(Int<1>());
+          // the weights stand unless the maximum is to be raised, for either half of the row
+          if (ptx::barrier_or(pair, 64,
+                              (m == neg_inf && top > neg_inf) || (top - m) * c > 8.f)) {
+            float *mine = xch + ((b * 2 + hf) << 7) + row;
+            *mine = top;
+            ptx::barrier_sync(pair, 64);
+            top = fmaxf(top, xch[((b * 2 + (hf ^ 1)) << 7) + row]);
+            const bool first = m == neg_inf && top > neg_inf;
+            const bool raise = first || (top - m) * c > 8.f;
             const float f = raise ? (first ? 0.f : exp2_approx((m - top) * c)) : 1.f;
             if (raise) m = top;
             if (i > 0) {
@@ -263,106 +292,70 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
               ptx::tc_fence_after();
               l *= f;
 #pragma unroll 1
-              for (int j = 0; j < S::DV * 4; ++j) {
+              for (int j = 0; j < S::DV * 2; ++j) {
                 uint32_t y[16];
                 ptx::tmem_ld16(o_t + 16 * j, y);
-                ptx::tmem_ld_wait(y);
-                ptx::tmem_ld_wait(y + 8);
+                ptx::tmem_ld_wait_all<16>(y);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
                 ptx::tmem_st16(o_t + 16 * j, y);
               }
             }
-          }
-          const float base = m > neg_inf ? m * c : 0.f;
-          const float cs = flip ? -c : c;
-          const f32x2 c2 = f2(cs, cs), nb2 = f2(-base, -base);
-          f32x2 la = f2(0.f, 0.f), lb = la;
-          // the weights, over S. P V of the first half starts during the second. Two copies of the
-          // loop: a test of the mask at each weight would cost as much as the weight
-          auto weights = [&](auto masked) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t h[16];
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                float p0, p1;
-                f2_split(fma2(f2(__uint_as_float(x[32 * j + e]), __uint_as_float(x[32 * j + e + 1])),
-                              c2, nb2),
-                         p0, p1);
-                p0 = exp2_approx(p0);
-                p1 = exp2_approx(p1);
-                if (masked.v) {
-                  p0 = (bits[j] >> e) & 1 ? p0 : 0.f;
-                  p1 = (bits[j] >> (e + 1)) & 1 ? p1 : 0.f;
-                }
-                if (e & 2)
-                  lb = add2(lb, f2(p0, p1));
-                else
-                  la = add2(la, f2(p0, p1));
-                h[e / 2] = pack_bf16(p0, p1);
-              }
-              ptx::tmem_st16(st + 16 * j, h);
-              if (j == 1) {
-                ptx::tmem_st_wait();
-                ptx::tc_fence_before();
-                arrive(bar(S::p_full) + 16 * b);
-              }
-            }
-          };
-          if (whole)
-            weights(Int<0>());
-          else
+            base = m > neg_inf ? m * c : 0.f;
+            ptx::tmem_ld32(st, x);
+            ptx::tmem_ld32(st + 32, x + 32);
+            ptx::tmem_ld_wait_all<64>(x);
             weights(Int<1>());
+          }
+          ptx::tmem_st32(st + 32, h);  // P over the end of its half of S
           float l0, l1;
           f2_split(add2(la, lb), l0, l1);
           l += l0 + l1;
           ptx::tmem_st_wait();
-        } else {
-          arrive(bar(S::p_full) + 16 * b);
         }
         ptx::tc_fence_before();
-        arrive(bar(S::p_full) + 16 * b + 8);
+        arrive(bar(S::p_full) + 16 * b + 8 * hf);
       }
       wait(bar(S::o_full + w), o_ph);
       o_ph ^= 1;
       __syncwarp();
       ptx::tc_fence_after();
       if (live) {
+        xch[((w * 2 + hf) << 7) + row] = l;
+        ptx::barrier_sync(pair, 64);
+        l += xch[((w * 2 + (hf ^ 1)) << 7) + row];
+        ptx::barrier_sync(pair, 64);  // read before the next segment writes
         const int i = kRow * w + row;
         float *o = nullptr, *lse = nullptr;
-        if (i < s.rows) segment_out<0>(a, plan, s, blockIdx.x, i, true, &o, &lse);
+        if (i < s.rows) segment_out<0>(a, plan, s, blockIdx.x, i, hf == 0, &o, &lse);
         const bool ok = l != 0.f && !*gave_up;
         const float inv = 1.f / l;
 #pragma unroll 1
-        for (int j = 0; j < S::DV * 2; ++j) {
+        for (int j = 0; j < S::DV; ++j) {
           uint32_t r[32];
           ptx::tmem_ld32(o_t + 32 * j, r);
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) ptx::tmem_ld_wait(r + e);
+          ptx::tmem_ld_wait_all<32>(r);
           if (o) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              float4 v;
-              v.x = ok ? __uint_as_float(r[e]) * inv : 0.f;
-              v.y = ok ? __uint_as_float(r[e + 1]) * inv : 0.f;
-              v.z = ok ? __uint_as_float(r[e + 2]) * inv : 0.f;
-              v.w = ok ? __uint_as_float(r[e + 3]) * inv : 0.f;
-              *reinterpret_cast<float4 *>(o + 32 * j + e) = v;
+            for (int e = 0; e < 32; e += 8) {
+              float v[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[k] = ok ? __uint_as_float(r[e + k]) * inv : 0.f;
+              ptx::st_global8(o + hf * (S::DV * 32) + 32 * j + e, v);
             }
           }
         }
-        if (o) *lse = ok ? (m * c + log2f(l)) * kLn2 : neg_inf;
+        if (o && hf == 0) *lse = ok ? (m * c + log2f(l)) * kLn2 : neg_inf;
       }
       ptx::tc_fence_before();
       arrive(bar(S::o_free + w));
     }
-  } else if (warp < 12) {
-    ptx::regs_fewer<kRegsRest>();
-    // ---- K and V rows into the ring: a warp brings 32 tokens of each tile, a lane holds the slot
-    // of one. Copies by tensor map are issued by one thread of the warp, which stands in for the
-    // others' arrivals: four warps, because one issues a copy in about 100 cycles ----
-    const int part = warp & 3, t0 = 32 * part + lane;
+  } else if (warp < S::kMma) {
+    // ---- K and V rows into the ring: a warp brings kPart tokens of each tile, a lane holds the
+    // slots of kLane. Copies by tensor map are issued by one thread of the warp, which stands in
+    // for the others' arrivals; one issues a copy in about 100 cycles ----
+    constexpr int kPart = kTok / S::NL, kLane = kPart / 32;
+    const int part = warp - S::kSoft, t0 = kPart * part + lane;
     const bool gqa = lay.kind == KAMERA_GQA;
     const __nv_bfloat16 *lk = a.pool.k + (long long)a.layer * a.pool.num_slots * lay.row_k;
     const __nv_bfloat16 *lv =
@@ -371,41 +364,52 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
     uint32_t *masks = reinterpret_cast<uint32_t *>(smem + S::mask);
     const int piece = lane & 7;  // cp.async: 16-byte piece of a row
     const int box = maps.box;    // slots of a copy; boxes: copies of this warp per 64 columns
-    const int boxes = box == 0 ? 0 : (box <= 32 ? 32 / box : 32 * part % box == 0);
+    const int boxes = box == 0 ? 0 : (box <= kPart ? kPart / box : kPart * part % box == 0);
+    struct Slots {
+      int at[kLane];
+      bool whole;  // every token of the tile is in
+    };
     Place<S::NST> at;            // the next stage
     uint32_t tile_no = 0;        // tiles so far
-    while (walk.next(a, plan, &s)) {
+    while (more) {
+      s = after;
       const int n = tiles_of(s.tok0, s.tok1, kTok), a0 = s.tok0 / kTok;
       const int kcol = gqa ? s.kvh * lay.hd : 0;
       const int vcol = gqa ? kcol : s.half * (S::DV * 64);
-      auto token = [&](int i) {  // below 2^31: the tile starts below it
-        const int tok = (a0 + i) * kTok + t0;
+      auto token = [&](int i, int k) {  // below 2^31: the tile starts below it
+        const int tok = (a0 + i) * kTok + t0 + 32 * k;
         return tok >= s.tok0 && tok < s.tok1 ? tok : -1;
       };
-      auto page_at = [&](int i) {
-        const int tok = token(i);
-        return tok >= 0 ? load_page(a, s.lead, tok) : 0;
-      };
-      // The next stages: `chunks` chunks from column `col` of a tile's rows, whose slots the lanes
-      // have; whole: every token is in.
-      auto issue = [&](const void *map, const __nv_bfloat16 *rows, int row, int col, int chunks,
-                       int slot, bool whole) {
-        if (box && whole) {
-          int y[4];  // first slots of the copies
+      int page[kLane];  // of the next tile, not looked at yet
+      auto load_pages = [&](int i) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) y[k] = __shfl_sync(0xffffffffu, slot, (k * box) & 31);
+        for (int k = 0; k < kLane; ++k) {
+          const int tok = token(i, k);
+          page[k] = tok >= 0 ? load_page(a, s.lead, tok) : 0;
+        }
+      };
+      // The next stages: `chunks` chunks from column `col` of a tile's rows
+      auto issue = [&](const void *map, const __nv_bfloat16 *rows, int row, int col, int chunks,
+                       const Slots &sl) {
+        if (box && sl.whole) {
+          int y[kPart / 8];  // first slots of the copies
+#pragma unroll
+          for (int k = 0; k < kPart / 8; ++k) {
+            const int q = k * box;
+            y[k] = __shfl_sync(0xffffffffu, q < 32 ? sl.at[0] : sl.at[kLane - 1], q & 31);
+          }
           if (ptx::elect_one()) {
             Place<S::NST> to = at;
             for (int u = 0; u < chunks / S::UC; ++u) {
               const uint32_t full = bar(S::full) + 8 * to.st;
-              uint32_t dst = sb + S::ring + to.st * S::kStage + part * 32 * 128;
+              uint32_t dst = sb + S::ring + to.st * S::kStage + kPart * part * 128;
               wait(bar(S::empty) + 8 * to.st, to.ph ^ 1);
               if (dead) break;
               if (boxes) {
                 ptx::mbar_arrive_n(full, 31);
                 ptx::mbar_arrive_expect_tx(full, boxes * box * S::UC * 128);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < kPart / 8; ++k) {
                   if (k < boxes) {
 #pragma unroll
                     for (int c = 0; c < S::UC; ++c)
@@ -432,51 +436,54 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
             continue;
           }
           const __nv_bfloat16 *src = rows + col + u * S::UC * 64 + 8 * piece;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {  // four of this warp's tokens at a time
-            const int q = 4 * j + (lane >> 3), t = 32 * part + q;
-            const int sl = __shfl_sync(0xffffffffu, slot, q);
-            const __nv_bfloat16 *p = sl >= 0 ? src + (long long)sl * row : a.pool.k;
+#pragma unroll 4
+          for (int j = 0; j < kPart / 4; ++j) {  // four of this warp's tokens at a time
+            const int q = 4 * j + (lane >> 3), t = kPart * part + q;
+            const int slot = __shfl_sync(0xffffffffu, j < 8 ? sl.at[0] : sl.at[kLane - 1], q & 31);
+            const __nv_bfloat16 *p = slot >= 0 ? src + (long long)slot * row : a.pool.k;
 #pragma unroll
             for (int k = 0; k < S::UC; ++k)
               ptx::cp_async16(dst + k * kChunk + t * 128 + ((piece ^ (t & 7)) << 4),
-                              sl >= 0 ? p + k * 64 : p, sl >= 0 ? 16u : 0u);
+                              slot >= 0 ? p + k * 64 : p, slot >= 0 ? 16u : 0u);
           }
           ptx::cp_async_mbar_arrive(full);
         }
       };
-      int page = page_at(0);  // of the next tile, not looked at yet
-      int k_slot = 0;         // of the last K tile
-      bool whole = false;
+      Slots kt;  // of the last K tile
       auto load_k = [&](int i) {
-        const int tok = token(i);
-        k_slot = tok >= 0 ? slot_in(a, page, tok) : -1;
-        if (i + 1 < n) page = page_at(i + 1);  // ahead of its use
         const int mk = tile_no++ % kMasks;
-        const uint32_t bits = __ballot_sync(0xffffffffu, k_slot >= 0);
+        uint32_t bits[kLane];
+#pragma unroll
+        for (int k = 0; k < kLane; ++k) {
+          const int tok = token(i, k);
+          kt.at[k] = tok >= 0 ? slot_in(a, page[k], tok) : -1;
+          bits[k] = __ballot_sync(0xffffffffu, kt.at[k] >= 0);
+        }
+        if (i + 1 < n) load_pages(i + 1);  // ahead of its use
         if (lane == 0) {
-          masks[4 * mk + part] = bits;
+#pragma unroll
+          for (int k = 0; k < kLane; ++k) masks[4 * mk + part * kLane + k] = bits[k];
           arrive(bar(S::mk_full) + 8 * mk);
         }
         __syncwarp();
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        ptx::barrier_sync(1, 32 * S::NL);
         const uint4 m = *reinterpret_cast<const uint4 *>(masks + 4 * mk);
-        whole = (m.x & m.y & m.z & m.w) == 0xffffffffu;
-        issue(&maps.k, lk, lay.row_k, kcol, S::DK, k_slot, whole);
+        kt.whole = (m.x & m.y & m.z & m.w) == 0xffffffffu;
+        issue(&maps.k, lk, lay.row_k, kcol, S::DK, kt);
       };
+      load_pages(0);
       load_k(0);
+      more = walk.next(a, plan, &after);
       for (int i = 0; i < n; ++i) {
-        const int v_slot = k_slot;  // V of this tile may come after K of the next
-        const bool v_whole = whole;
+        const Slots vt = kt;  // V of this tile may come after K of the next
         if (S::QT == 1 && i + 1 < n) load_k(i + 1);
-        issue(&maps.v, lv, vrow, vcol, S::DV, v_slot, v_whole);
+        issue(&maps.v, lv, vrow, vcol, S::DV, vt);
         if (S::QT == 2 && i + 1 < n) load_k(i + 1);
       }
     }
     ptx::cp_async_wait_all();
   } else {
-    ptx::regs_fewer<kRegsRest>();
-    // ---- MMAs (warp 12) and Q (warp 13), one thread each. QT 2: S and P V of the two query tiles
+    // ---- MMAs and Q, a warp and one thread of it each. QT 2: S and P V of the two query tiles
     // in turn, so that the tensor core works on one during the softmax of the other; QT 1: S of a
     // tile before P V of the one before it. Issuing an MMA takes a few instructions only: the
     // descriptors of a tile's steps differ by constants ----
@@ -494,10 +501,14 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
         ptx::tma_3d(sb + S::q + c * S::QT * kChunk, s.own ? &maps.q_own : &maps.q_group, c * 64, y,
                     z, bar(S::q_full));
     };
-    if (warp == 13) {
+    if (warp == S::kQ) {
       if (ptx::elect_one())
-        while (walk.next(a, plan, &s)) load_q();
-    } else if (warp == 12 && ptx::elect_one()) {
+        while (more) {
+          s = after;
+          load_q();
+          more = walk.next(a, plan, &after);
+        }
+    } else if (ptx::elect_one()) {
       constexpr uint32_t id_s = 1u << 4 | 1u << 7 | 1u << 10 | (kTok >> 3) << 17 | (kRow >> 4) << 24;
       // V is MN-major
       constexpr uint32_t id_o =
@@ -535,7 +546,7 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
         ptx::mma_commit(bar(S::s_full) + 8 * b);
         if (ends.v & 2) kp = at;
       };
-      // O of query tile t (+)= P in buffer b, [128][tokens], times the V tile at vp
+      // O of query tile t (+)= P in buffer b times the V tile at vp
       auto mma_o = [&](auto t, uint32_t b, bool first_tile, bool last_tile, auto ends) {
         const uint32_t p = tmem + b * 128, d = tmem + S::o_col + t.v * 128;
         Place<S::NST> at = vp;
@@ -562,8 +573,9 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
               if (dead) return;
               ptx::tc_fence_after();
             }
-            ptx::mma_bf16_ta(d + u * S::UC * 64, p + 8 * x, desc(v + x * (2048 >> 4)), id_o,
-                             x ? 1u : (first_tile ? 0u : 1u));
+            // P of tokens 0-63 is in columns 32-63 of S, of 64-127 in 96-127
+            ptx::mma_bf16_ta(d + u * S::UC * 64, p + 32 + 8 * x + (x < kTok / 32 ? 0 : 32),
+                             desc(v + x * (2048 >> 4)), id_o, x ? 1u : (first_tile ? 0u : 1u));
           }
           if (ends.v & 2) ptx::mma_commit(bar(S::empty) + 8 * at.st);
           at.advance(1);
@@ -580,7 +592,9 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
       constexpr Int<1> t1, first;
       constexpr Int<2> last;
       constexpr Int<3> only;
-      while (walk.next(a, plan, &s)) {
+      while (more) {
+        s = after;
+        more = walk.next(a, plan, &after);
         const int n = tiles_of(s.tok0, s.tok1, kTok);
         // the stages come in the order in which they are read:
         // QT 2: K0 V0 K1 V1 ...; QT 1: K0 K1 V0 K2 V1 ... V(n-1)
@@ -643,7 +657,7 @@ __global__ void __launch_bounds__(kThr, 1) prefix_tc_kernel(const __grid_constan
     }
     __syncthreads();
   }
-  if (warp == 12) ptx::tmem_dealloc(tmem, 512);
+  if (warp == S::kMma) ptx::tmem_dealloc(tmem, 512);
 }
 
 template <class S>
@@ -711,7 +725,7 @@ cudaError_t launch(const PrefixArgs &a, cudaStream_t s) {
     m.own_bytes = S::DK * 128 * hpk;
   }
   if (!ok) return cudaErrorInvalidValue;
-  return launch_early(prefix_tc_kernel<S>, dim3(a.shape.cls[0].n), kThr, S::total, s, a, m);
+  return launch_early(prefix_tc_kernel<S>, dim3(a.shape.cls[0].n), S::kThr, S::total, s, a, m);
 }
 
 }  // namespace

@@ -150,16 +150,34 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const void *map, int x, int
       : "memory");
 }
 
-// ---- registers ----
-// The warps of a warpgroup (four from a multiple of four) take kRegs registers a thread each. The
-// shares of all warps of the block may not exceed the registers it was launched with.
-template <int kRegs>
-__device__ __forceinline__ void regs_more() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+// The descriptor of a tensor map (a kernel parameter) into the cache.
+__device__ __forceinline__ void prefetch_map(const void *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
-template <int kRegs>
-__device__ __forceinline__ void regs_fewer() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+
+// ---- named barriers (whole warps) ----
+__device__ __forceinline__ void barrier_sync(int id, int threads) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// The same, and whether any of the threads came with `p`.
+__device__ __forceinline__ bool barrier_or(int id, int threads, bool p) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(threads), "r"((uint32_t)p)
+      : "memory");
+  return any != 0;
+}
+
+// Eight floats to a 32-byte aligned address: a whole sector by one thread.
+__device__ __forceinline__ void st_global8(float *p, const float *v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]),
+               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
 }
 
 // True in one thread of a converged warp. The compiler knows that at most one thread runs what
@@ -380,6 +398,20 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t *r) {
                  "+r"(r[6]), "+r"(r[7])
                :
                : "memory");
+}
+
+// The same for kN registers (a multiple of eight) with one wait instruction: the other groups are
+// tied to it by empty statements, which stay behind it.
+template <int kN>
+__device__ __forceinline__ void tmem_ld_wait_all(uint32_t *r) {
+  tmem_ld_wait(r);
+#pragma unroll
+  for (int e = 8; e < kN; e += 8)
+    asm volatile(""
+                 : "+r"(r[e]), "+r"(r[e + 1]), "+r"(r[e + 2]), "+r"(r[e + 3]), "+r"(r[e + 4]),
+                   "+r"(r[e + 5]), "+r"(r[e + 6]), "+r"(r[e + 7])
+                 :
+                 : "memory");
 }
 
 }  // namespace ptx
