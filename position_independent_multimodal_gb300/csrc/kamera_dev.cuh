@@ -196,7 +196,8 @@ constexpr int kSms = 152;  // of a GB300
 
 // How a layout's attention over shared prefixes is divided (kamera_prefix.cuh).
 struct PrefixClass {
-  int rb, tile, vh, n;  // rows of a block, tokens of a tile, column halves of V, workers
+  int rb, vh, n;        // rows of a block, column halves of V, workers
+  int tile_sh;          // a tile has 2^tile_sh tokens
   int least;            // units a worker takes at least
 };
 struct PrefixShape {

@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_cons
       if (l != 0x7FFFFFFF && prefix > 0) {
         c = class_of(a.shape, n * hpk);
         const PrefixClass &k = a.shape.cls[c];
-        units = (long long)a.n_kv * k.vh * ceil_div(n * hpk, k.rb) * ceil_div(prefix, k.tile);
+        units = (long long)a.n_kv * k.vh * ceil_div(n * hpk, k.rb) * tiles_of(0, prefix, k.tile_sh);
       }
     }
     const long long one = units > 0 ? 1ll << (32 * c) : 0;
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_cons
     const int r = r0 + tid;
     const int g = r < R ? p.req_group[r] : -1;
     const int prefix = g >= 0 ? p.req_prefix[r] : 0, ctx = g >= 0 ? a.ctx_len[r] : 0;
-    const long long units = (long long)blocks * tiles_of(prefix, ctx, ok.tile);
+    const long long units = (long long)blocks * tiles_of(prefix, ctx, ok.tile_sh);
     long long x[2] = {units, units > 0}, total[2];
     plan_scan(x, total);
     if (r < R) {
@@ -213,11 +213,16 @@ __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_cons
           hi = mid - 1;
       }
       const int from = own ? p.r_from[lo] : 0, to = own ? p.r_to[lo] : p.cls[c].g_prefix[lo];
-      const int tiles = tiles_of(from, to, k.tile);
-      const int nrb = ceil_div((own ? 1 : p.cls[c].g_size[lo]) * hpk, k.rb);
+      const int tiles = tiles_of(from, to, k.tile_sh);
+      const int first = own ? p.r_list[lo] : p.cls[c].g_first[lo];
+      const int size = own ? 1 : p.cls[c].g_size[lo], lead = own ? first : p.cls[c].g_lead[lo];
+      const int nrb = ceil_div(size * hpk, k.rb);
       const long long d = u - u0[lo], b = div_pos(d, tiles), kh = div_pos(b, nrb);
-      p.cls[c].start[w] = make_int4(lo | (own ? 1 << 30 : 0), (int)(b - kh * nrb), (int)kh,
-                                    (int)(d - b * tiles));
+      int4 *rec = p.cls[c].start + 3 * w;
+      rec[0] = make_int4(lo | (own ? 1 << 30 : 0), (int)(b - kh * nrb), (int)kh,
+                         (int)(d - b * tiles));
+      rec[1] = make_int4(first, size, lead, from);
+      rec[2] = make_int4(to, 0, 0, 0);
     }
     if (tid == 0) {
       long long *head = p.head + 8 * c;
@@ -240,7 +245,7 @@ __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_cons
 // ---------------------------------------------------------------------------------------
 
 constexpr int kThr = 256;
-constexpr int kTile = 256;
+constexpr int kTileSh = 8, kTile = 1 << kTileSh;
 constexpr int kRows = 8;
 constexpr int kBatch = 8;
 
@@ -554,8 +559,8 @@ PrefixShape prefix_shape(const DevLayout &l, int hq) {
     s.cls[1] = prefix_thin_class(l);
     s.wide_rows = 32;
   } else {
-    s.cls[0] = {1, 128, 1, 1, 1};  // not used: no block is wide
-    s.cls[1] = {kRows, kTile, 1, 2 * kSms, 1};
+    s.cls[0] = {1, 1, 1, 7, 1};  // not used: no block is wide
+    s.cls[1] = {kRows, 1, 2 * kSms, kTileSh, 1};
     s.wide_rows = 0x7FFFFFFF;
   }
   return s;

@@ -27,8 +27,9 @@ struct PrefixPlan {
   struct Lists {          // blocks of a class
     long long *g_u0;      // [R] first unit of the i-th listed group
     int *g_first, *g_size, *g_prefix, *g_lead;  // first request, requests, prefix, leader
-    int4 *start;          // [n] each worker's first block: list index (own: + 2^30), row block,
-                          //     KV head x half, tile
+    int4 *start;          // [n][3] each worker's first block: list index (own: + 2^30), row block,
+                          //     KV head x half, tile; the listed entry's first request, requests,
+                          //     leader, first token; end of its tokens
     float *carry_lse;     // [n][rb]
     float *carry_o;       // [n][rb][dv / vh]
   } cls[2];
@@ -53,13 +54,13 @@ struct PrefixPlan {
 __host__ __device__ inline PrefixPlan prefix_plan(const PrefixShape &sh, void *ws, long long R,
                                                   int hq, int dv) {
   PrefixPlan p;
-  // partial outputs are written by whole 32-byte sectors
-  const size_t skew = static_cast<size_t>(-reinterpret_cast<intptr_t>(ws)) & 31;
+  // partial outputs are written by whole lines of 128 bytes
+  const size_t skew = static_cast<size_t>(-reinterpret_cast<intptr_t>(ws)) & 127;
   unsigned char *b = static_cast<unsigned char *>(ws) + skew;
   size_t o = 0;
   auto take = [&](size_t bytes) {
     unsigned char *at = b + o;
-    o += (bytes + 31) & ~static_cast<size_t>(31);
+    o += (bytes + 127) & ~static_cast<size_t>(127);
     return at;
   };
   auto i64 = [&]() { return reinterpret_cast<long long *>(take(8 * R)); };
@@ -73,7 +74,7 @@ __host__ __device__ inline PrefixPlan prefix_plan(const PrefixShape &sh, void *w
     p.cls[c].g_size = i32(R);
     p.cls[c].g_prefix = i32(R);
     p.cls[c].g_lead = i32(R);
-    p.cls[c].start = reinterpret_cast<int4 *>(take(16ll * k.n));
+    p.cls[c].start = reinterpret_cast<int4 *>(take(48ll * k.n));
     p.cls[c].carry_lse = f32((long long)k.n * k.rb);
     p.cls[c].carry_o = f32((long long)k.n * k.rb * (dv / k.vh));
   }
@@ -93,15 +94,15 @@ __host__ __device__ inline PrefixPlan prefix_plan(const PrefixShape &sh, void *w
   p.home_lse = f32(4 * R * hq);
   p.home_more = reinterpret_cast<int2 *>(take(32 * R * hq));
   p.home_o = f32(2 * R * hq * dv);
-  p.total = o + 16;  // the workspace is 16-byte aligned
+  p.total = o + 112;  // the workspace is 16-byte aligned
   return p;
 }
 
 __host__ __device__ inline int ceil_div(int a, int b) { return (int)(((unsigned)a + b - 1) / b); }
 
-// Tiles that tokens [from, to) lie in.
-__host__ __device__ inline int tiles_of(int from, int to, int tile) {
-  return to > from ? ceil_div(to, tile) - from / tile : 0;
+// Tiles of 2^sh tokens that tokens [from, to) lie in.
+__host__ __device__ inline int tiles_of(int from, int to, int sh) {
+  return to > from ? (int)(((unsigned)to + (1u << sh) - 1) >> sh) - (from >> sh) : 0;
 }
 
 // The class of a block with that many rows.
@@ -109,7 +110,7 @@ __host__ __device__ inline int class_of(const PrefixShape &sh, int rows) {
   return rows > sh.wide_rows ? 0 : 1;
 }
 
-// First unit of worker w; the worker of unit u.
+// First unit of worker w.
 __device__ __forceinline__ long long first_unit(long long quot, long long rem, long long w) {
   return w * quot + (w < rem ? w : rem);
 }
@@ -117,9 +118,12 @@ __device__ __forceinline__ long long div_pos(long long a, long long b) {  // a >
   if (((a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
   return a / b;
 }
-__device__ __forceinline__ int worker_of(long long quot, long long rem, long long u) {
-  const long long edge = rem * (quot + 1);
-  return (int)(u < edge ? div_pos(u, quot + 1) : rem + div_pos(u - edge, quot));
+// Workers from w on that take `units` units, the last of them perhaps in part.
+__device__ __forceinline__ int workers_for(long long quot, long long rem, long long w,
+                                           long long units) {
+  const long long n = rem > w ? rem - w : 0, edge = n * (quot + 1);  // those with one unit more
+  return (int)(units <= edge ? div_pos(units + quot, quot + 1)
+                             : n + div_pos(units - edge + quot - 1, quot));
 }
 
 // A run of tiles of one block, as a worker takes it.
@@ -142,6 +146,8 @@ struct SegmentWalk {
   int first, size, lead, from, to;  // the listed group or request
   int tiles, nrb;            // tiles and row blocks of each of its blocks
   int rbk, kh, t;            // the next block (row block, KV head x half) and tile
+  int worker, groups;        // groups: of the class's list
+  long long quot, rem;       // U / n and U % n
 
   __device__ __forceinline__ void entry(const PrefixArgs &a, const PrefixPlan &p) {
     if (own) {
@@ -156,19 +162,35 @@ struct SegmentWalk {
       from = 0;
       to = p.cls[C].g_prefix[i];
     }
-    tiles = tiles_of(from, to, a.shape.cls[C].tile);
+    count(a);
+  }
+  __device__ __forceinline__ void count(const PrefixArgs &a) {
+    tiles = tiles_of(from, to, a.shape.cls[C].tile_sh);
     nrb = ceil_div(size * a.hpk, a.shape.cls[C].rb);
   }
-  __device__ __forceinline__ void start(const PrefixArgs &a, const PrefixPlan &p, int worker) {
+  // One round of loads: the place is there for every worker, whether or not it has units.
+  __device__ __forceinline__ void start(const PrefixArgs &a, const PrefixPlan &p, int worker_) {
     const long long *head = p.head + 8 * C;
+    const int4 *rec = p.cls[C].start + 3 * worker_;
+    const int4 at = rec[0], e = rec[1];
+    const int last = rec[2].x;
+    const long long n = head[4];
+    worker = worker_;
+    groups = (int)head[1];
+    quot = head[2];
+    rem = head[3];
     u = end = 0;
-    if (worker >= head[4]) return;
-    const int4 at = p.cls[C].start[worker];
-    u = first_unit(head[2], head[3], worker);
-    end = first_unit(head[2], head[3], worker + 1);
+    if (worker >= n) return;
+    u = first_unit(quot, rem, worker);
+    end = first_unit(quot, rem, worker + 1);
     own = at.x >> 30;
     i = at.x & 0x3FFFFFFF;
-    entry(a, p);
+    first = e.x;
+    size = e.y;
+    lead = e.z;
+    from = e.w;
+    to = last;
+    count(a);
     rbk = at.y;
     kh = at.z;
     t = at.w;
@@ -179,7 +201,7 @@ struct SegmentWalk {
     const PrefixClass &k = a.shape.cls[C];
     if (kh == a.n_kv * k.vh) {  // the entry is done
       ++i;
-      if (!own && i == (int)p.head[8 * C + 1]) {
+      if (!own && i == groups) {
         own = 1;
         i = 0;
       }
@@ -194,15 +216,11 @@ struct SegmentWalk {
     s->row0 = rbk * k.rb;
     s->rows = min(k.rb, size * a.hpk - s->row0);
     const long long left = end - u;
-    const int nt = (int)(left < tiles - t ? left : tiles - t), t0 = from / k.tile;
-    s->tok0 = t == 0 ? from : (t0 + t) * k.tile;
-    s->tok1 = t + nt == tiles ? to : (t0 + t + nt) * k.tile;
+    const int nt = (int)(left < tiles - t ? left : tiles - t), t0 = from >> k.tile_sh;
+    s->tok0 = t == 0 ? from : (t0 + t) << k.tile_sh;
+    s->tok1 = t + nt == tiles ? to : (t0 + t + nt) << k.tile_sh;
     s->carry = t > 0;
-    s->more = 0;
-    if (t == 0 && nt < tiles) {
-      const long long *head = p.head + 8 * C;
-      s->more = worker_of(head[2], head[3], u + tiles - 1) - worker_of(head[2], head[3], u);
-    }
+    s->more = t == 0 && nt < tiles ? workers_for(quot, rem, worker + 1, tiles - nt) : 0;
     u += nt;
     t = 0;
     if (++rbk == nrb) {

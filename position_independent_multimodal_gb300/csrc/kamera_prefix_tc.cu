@@ -33,7 +33,7 @@ namespace kamera {
 
 namespace {
 
-constexpr int kTok = 128;              // tokens per tile
+constexpr int kTokSh = 7, kTok = 1 << kTokSh;  // tokens per tile
 constexpr int kRow = 128;              // query rows per MMA
 constexpr int kChunk = kTok * 128;     // bytes of a 128 x 64 bf16 operand tile
 constexpr int kMasks = 8;              // tiles whose token masks are kept
@@ -48,7 +48,8 @@ struct Shape {
   static constexpr int kThr = 32 * (kQ + 1);
   static constexpr int kStage = UC * kChunk;
   static constexpr int q = 0;
-  static constexpr int ring = QT * DK * kChunk;
+  // the queries' place takes the output on its way out, 4 KB a softmax warp
+  static constexpr int ring = QT * DK * kChunk > kSoft * 4096 ? QT * DK * kChunk : kSoft * 4096;
   static constexpr int mask = ring + NST * kStage;  // uint32 [kMasks][4]
   static constexpr int xch = mask + kMasks * 16;    // float [2][2][kRow]: maxima, then sums
   static constexpr int bar = xch + 4 * kRow * 4;
@@ -65,7 +66,7 @@ struct Shape {
 };
 
 using Gqa128 = Shape<2, 2, 2, 2, 5, 2>;
-using Gqa64 = Shape<1, 1, 2, 1, 12, 2>;
+using Gqa64 = Shape<1, 1, 2, 1, 10, 2>;
 using Mla512 = Shape<9, 4, 1, 1, 5, 4>;
 
 // Tensor maps of a call: pool rows of the layer (boxes of 64 columns and `box` slots) and query
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
     while (more) {
       s = after;
       more = walk.next(a, plan, &after);
-      const int n = tiles_of(s.tok0, s.tok1, kTok);
+      const int n = tiles_of(s.tok0, s.tok1, kTokSh);
       if (w == 1 && s.rows <= kRow) {
         seen += n;
         continue;
@@ -330,21 +331,33 @@ __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
         if (i < s.rows) segment_out<0>(a, plan, s, blockIdx.x, i, hf == 0, &o, &lse);
         const bool ok = l != 0.f && !*gave_up;
         const float inv = 1.f / l;
+        // 32 columns at a time through shared memory (the queries are no longer needed), swizzled
+        // in 16-byte pieces, so that a warp writes four whole lines of 128 bytes at a time
+        uint4 *stage = reinterpret_cast<uint4 *>(smem + S::q + warp * 4096);
+        const int piece = lane & 7;
 #pragma unroll 1
         for (int j = 0; j < S::DV; ++j) {
           uint32_t r[32];
           ptx::tmem_ld32(o_t + 32 * j, r);
           ptx::tmem_ld_wait_all<32>(r);
-          if (o) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              float v[8];
+          for (int e = 0; e < 32; ++e)
+            r[e] = ok ? __float_as_uint(__uint_as_float(r[e]) * inv) : 0u;
+          __syncwarp();  // the columns before have been read
 #pragma unroll
-              for (int k = 0; k < 8; ++k) v[k] = ok ? __uint_as_float(r[e + k]) * inv : 0.f;
-              ptx::st_global8(o + hf * (S::DV * 32) + 32 * j + e, v);
-            }
+          for (int e = 0; e < 8; ++e)
+            stage[8 * lane + (e ^ piece)] = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int q = 4 * k + (lane >> 3);  // the row
+            float *to = reinterpret_cast<float *>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), q));
+            const uint4 v = stage[8 * q + (piece ^ (q & 7))];
+            if (to) *reinterpret_cast<uint4 *>(to + hf * (S::DV * 32) + 32 * j + 4 * piece) = v;
           }
         }
+        ptx::fence_proxy_async_smem();  // before the next queries are copied there
         if (o && hf == 0) *lse = ok ? (m * c + log2f(l)) * kLn2 : neg_inf;
       }
       ptx::tc_fence_before();
@@ -373,7 +386,7 @@ __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
     uint32_t tile_no = 0;        // tiles so far
     while (more) {
       s = after;
-      const int n = tiles_of(s.tok0, s.tok1, kTok), a0 = s.tok0 / kTok;
+      const int n = tiles_of(s.tok0, s.tok1, kTokSh), a0 = s.tok0 / kTok;
       const int kcol = gqa ? s.kvh * lay.hd : 0;
       const int vcol = gqa ? kcol : s.half * (S::DV * 64);
       auto token = [&](int i, int k) {  // below 2^31: the tile starts below it
@@ -489,10 +502,18 @@ __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
     // descriptors of a tile's steps differ by constants ----
     // Q of a segment, once S of the one before is complete. Rows of a copy past the block's are
     // other requests' or zero: their results go nowhere
-    uint32_t segs = 0;
+    uint32_t segs = 0, out_ph = 0;
+    bool two = false;  // the last segment had both query tiles
     auto load_q = [&]() {
-      if (segs) wait(bar(S::q_empty), (segs - 1) & 1);
+      if (segs) {
+        wait(bar(S::q_empty), (segs - 1) & 1);
+        for (int t = 0; t <= two; ++t) {  // its output has gone through the queries' place
+          wait(bar(S::o_free + t), (out_ph >> t) & 1);
+          out_ph ^= 1u << t;
+        }
+      }
       ++segs;
+      two = S::QT == 2 && s.rows > kRow;
       if (dead) return;
       ptx::mbar_arrive_expect_tx(bar(S::q_full), s.own ? maps.own_bytes : maps.group_bytes);
       const int y = maps.q_step ? 0 : s.kvh * a.hpk;
@@ -595,7 +616,7 @@ __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
       while (more) {
         s = after;
         more = walk.next(a, plan, &after);
-        const int n = tiles_of(s.tok0, s.tok1, kTok);
+        const int n = tiles_of(s.tok0, s.tok1, kTokSh);
         // the stages come in the order in which they are read:
         // QT 2: K0 V0 K1 V1 ...; QT 1: K0 K1 V0 K2 V1 ... V(n-1)
         vp = kp;
@@ -741,7 +762,7 @@ PrefixClass prefix_tc_class(const DevLayout &l, int hq) {
   PrefixClass c;
   // several KV heads: whole requests, so that one copy brings a block's queries
   c.rb = gqa && l.H > 1 && hpk > 0 ? most / hpk * hpk : most;
-  c.tile = kTok;
+  c.tile_sh = kTokSh;
   c.vh = gqa ? 1 : 2;
   c.n = kSms;
   c.least = 1;

@@ -526,11 +526,12 @@ PrefixClass prefix_thin_class(const DevLayout &l) {
   c.rb = kRows;
   c.vh = 1;
   if (l.kind == KAMERA_MLA) {
-    c.tile = ThinMla::kTok;
+    c.tile_sh = 6;
+    static_assert(ThinMla::kTok == 1 << 6, "a tile");
     c.n = kSms;
     c.least = 1;
   } else {
-    c.tile = 16;
+    c.tile_sh = 4;
     c.n = kSms * (l.hd == 128 ? Thin128::WARPS : Thin64::WARPS);
     c.least = 4;
   }

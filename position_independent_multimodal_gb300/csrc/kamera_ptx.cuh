@@ -173,13 +173,6 @@ __device__ __forceinline__ bool barrier_or(int id, int threads, bool p) {
   return any != 0;
 }
 
-// Eight floats to a 32-byte aligned address: a whole sector by one thread.
-__device__ __forceinline__ void st_global8(float *p, const float *v) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]),
-               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-               : "memory");
-}
-
 // True in one thread of a converged warp. The compiler knows that at most one thread runs what
 // the result guards, so operands that an instruction takes in uniform registers (tcgen05.mma)
 // go there directly, without a loop over the threads that might differ.
