@@ -25,6 +25,7 @@ namespace kamera {
 namespace {
 
 constexpr int kPlanThr = 256;
+constexpr int kSpanExtra = 6;    // tiles
 constexpr int kPlanNear = 1024;  // groups and listed entries kept in shared memory
 
 // Inclusive scans of N values at a time over the CTA's threads, in place; total: their sums.
@@ -68,14 +69,17 @@ __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_cons
   const PrefixPlan p = prefix_plan(a.shape, a.ws, a.n_reqs, a.hq, a.dv);
   __shared__ int near_start[kPlanNear + 1], near_lead[kPlanNear];
   __shared__ long long near_u0[2][kPlanNear], near_r[kPlanNear];
-  __shared__ int broken;
+  __shared__ int broken, least_tiles, most_tiles;
   const int tid = threadIdx.x, R = a.n_reqs, G = a.n_groups;
   const int hpk = a.hpk, own_cls = class_of(a.shape, hpk);
   const long long cap = (long long)a.pool.pt_stride * a.lay.page_size;
   const bool near_g = G <= kPlanNear;
   const int *start = near_g ? near_start : a.group_start;
   int *lead = near_g ? near_lead : p.lead;
-  if (tid == 0) broken = 0;
+  if (tid == 0) {
+    broken = most_tiles = 0;
+    least_tiles = 0x7FFFFFFF;
+  }
   __syncthreads();
   for (int g = tid; g <= G; g += kPlanThr) {
     const int s = a.group_start[g];
@@ -131,7 +135,12 @@ __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_cons
       if (l != 0x7FFFFFFF && prefix > 0) {
         c = class_of(a.shape, n * hpk);
         const PrefixClass &k = a.shape.cls[c];
-        units = (long long)a.n_kv * k.vh * ceil_div(n * hpk, k.rb) * tiles_of(0, prefix, k.tile_sh);
+        const int tiles = tiles_of(0, prefix, k.tile_sh);
+        units = (long long)a.n_kv * k.vh * ceil_div(n * hpk, k.rb) * tiles;
+        if (c == 0) {
+          atomicMin(&least_tiles, tiles);
+          atomicMax(&most_tiles, tiles);
+        }
       }
     }
     const long long one = units > 0 ? 1ll << (32 * c) : 0;
@@ -192,15 +201,28 @@ __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_cons
     const long long U = c ? base[1] : base[0], own0 = c ? prefix_units[1] : prefix_units[0];
     const int groups = c ? listed[1] : listed[0];
     const long long few = div_pos(U + k.least - 1, k.least);
-    const int n = (int)(few < k.n ? few : k.n);
+    int n = (int)(few < k.n ? few : k.n);
     if (n == 0) {
       if (tid == 0) p.head[8 * c + 4] = 0;
       continue;
     }
-    const long long quot = div_pos(U, n), rem = U - quot * n;
+    // spans: one of all units, or one a block. The latter where that costs a worker no more than
+    // kSpanExtra tiles, about what a part of a second block costs it
+    long long T = U;
+    int per = n;
+    if (c == 0 && own0 == U && least_tiles == most_tiles) {
+      const int spans = (int)(U / most_tiles < n ? U / most_tiles : n + 1), part = n / spans;
+      if (part > 0 && ceil_div(most_tiles, part) <= U / n + kSpanExtra) {
+        T = most_tiles;
+        per = part < most_tiles ? part : most_tiles;
+        n = per * spans;
+      }
+    }
+    const long long quot = div_pos(T, per), rem = T - quot * per;
     const long long *g_u0 = p.cls[c].g_u0;
     for (int w = tid; w < n; w += kPlanThr) {
-      const long long u = first_unit(quot, rem, w);
+      const int span = w / per;
+      const long long u = span * T + first_unit(quot, rem, w - span * per);
       const bool own = u >= own0;
       const int count = own ? own_listed : groups;
       const long long *u0 = count <= kPlanNear ? (own ? near_r : near_u0[c]) : (own ? p.r_u0 : g_u0);
@@ -231,6 +253,8 @@ __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_cons
       head[2] = quot;
       head[3] = rem;
       head[4] = n;
+      head[5] = T;
+      head[6] = per;
     }
   }
 }

@@ -8,11 +8,13 @@
 // bound them, and a tile of 128 rows would be idle for the most part). A unit is one tile of
 // tokens (at multiples of the class's tile) of one block of at most `rb` rows. A class's units
 // are numbered prefix blocks first (group, KV head and column half, row block, tile), then own
-// blocks (request, ...), and of n workers with units each takes U / n consecutive ones, the first
-// U % n one more: every worker has the same number of tiles whatever the lengths, and cuts at most its first and last block. A
-// block's first segment writes its rows' partial output to the rows' home place, with the number
-// of workers that follow on the block; those write to their carry places. The merge kernel joins
-// a row's parts by their log-sum-exp.
+// blocks (request, ...). Workers take consecutive units, as many as one another: every one has the
+// same number of tiles whatever the lengths, and cuts at most its first and last block. Where a
+// class's blocks all have as many tiles and there are workers enough, each block is shared out
+// among its own workers instead, so that no worker has parts of two blocks and those of the blocks
+// of one KV head read the same tokens at the same time. A block's first segment writes its rows'
+// partial output to the rows' home place, with the number of workers that follow on the block;
+// those write to their carry places. The merge kernel joins a row's parts by their log-sum-exp.
 #pragma once
 
 #include "kamera_dev.cuh"
@@ -21,8 +23,8 @@ namespace kamera {
 
 // What the plan kernel leaves for the others, in the workspace.
 struct PrefixPlan {
-  // per class c at head[8 c + .]: 0 units U, 1 groups listed, 2 U / n and 3 U % n for the n workers
-  // with units, 4 n
+  // per class c at head[8 c + .]: 0 units U, 1 groups listed, 4 workers n with units. k workers
+  // share a span of T units: 2 T / k, 3 T % k, 5 T, 6 k
   long long *head;
   struct Lists {          // blocks of a class
     long long *g_u0;      // [R] first unit of the i-th listed group
@@ -110,7 +112,7 @@ __host__ __device__ inline int class_of(const PrefixShape &sh, int rows) {
   return rows > sh.wide_rows ? 0 : 1;
 }
 
-// First unit of worker w.
+// First unit of a span's worker w.
 __device__ __forceinline__ long long first_unit(long long quot, long long rem, long long w) {
   return w * quot + (w < rem ? w : rem);
 }
@@ -118,7 +120,7 @@ __device__ __forceinline__ long long div_pos(long long a, long long b) {  // a >
   if (((a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
   return a / b;
 }
-// Workers from w on that take `units` units, the last of them perhaps in part.
+// A span's workers from w on that take `units` units, the last of them perhaps in part.
 __device__ __forceinline__ int workers_for(long long quot, long long rem, long long w,
                                            long long units) {
   const long long n = rem > w ? rem - w : 0, edge = n * (quot + 1);  // those with one unit more
@@ -146,8 +148,8 @@ struct SegmentWalk {
   int first, size, lead, from, to;  // the listed group or request
   int tiles, nrb;            // tiles and row blocks of each of its blocks
   int rbk, kh, t;            // the next block (row block, KV head x half) and tile
-  int worker, groups;        // groups: of the class's list
-  long long quot, rem;       // U / n and U % n
+  int worker, groups;        // its place in its span; groups of the class's list
+  long long quot, rem;       // T / k and T % k
 
   __device__ __forceinline__ void entry(const PrefixArgs &a, const PrefixPlan &p) {
     if (own) {
@@ -174,15 +176,16 @@ struct SegmentWalk {
     const int4 *rec = p.cls[C].start + 3 * worker_;
     const int4 at = rec[0], e = rec[1];
     const int last = rec[2].x;
-    const long long n = head[4];
-    worker = worker_;
+    const long long n = head[4], T = head[5], k = head[6];
     groups = (int)head[1];
     quot = head[2];
     rem = head[3];
     u = end = 0;
-    if (worker >= n) return;
-    u = first_unit(quot, rem, worker);
-    end = first_unit(quot, rem, worker + 1);
+    if (worker_ >= n) return;
+    const int span = (int)((unsigned)worker_ / (unsigned)k);
+    worker = worker_ - span * (int)k;
+    u = span * T + first_unit(quot, rem, worker);
+    end = span * T + first_unit(quot, rem, worker + 1);
     own = at.x >> 30;
     i = at.x & 0x3FFFFFFF;
     first = e.x;
