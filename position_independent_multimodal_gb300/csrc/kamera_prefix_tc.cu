@@ -44,8 +44,8 @@ constexpr unsigned long long kWaitNs = 2000000000ull;
 template <int DK_, int DV_, int QT_, int UC_, int NST_, int NL_>
 struct Shape {
   static constexpr int DK = DK_, DV = DV_, QT = QT_, UC = UC_, NST = NST_, NL = NL_;
-  static constexpr int kSoft = 8 * QT, kMma = kSoft + NL, kQ = kMma + 1;  // warps: the first
-  static constexpr int kThr = 32 * (kQ + 1);
+  static constexpr int kSoft = 8 * QT, kMma = kSoft + NL;  // softmax warps; the MMA warp
+  static constexpr int kThr = 32 * (kMma + 1);
   static constexpr int kStage = UC * kChunk;
   static constexpr int q = 0;
   // the queries' place takes the output on its way out, 4 KB a softmax warp
@@ -65,8 +65,8 @@ struct Shape {
   static_assert(DK % UC == 0 && DV % UC == 0, "whole stages");
 };
 
-using Gqa128 = Shape<2, 2, 2, 2, 5, 2>;
-using Gqa64 = Shape<1, 1, 2, 1, 10, 2>;
+using Gqa128 = Shape<2, 2, 2, 2, 5, 4>;
+using Gqa64 = Shape<1, 1, 2, 1, 10, 4>;
 using Mla512 = Shape<9, 4, 1, 1, 5, 4>;
 
 // Tensor maps of a call: pool rows of the layer (boxes of 64 columns and `box` slots) and query
@@ -227,9 +227,8 @@ __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
         ptx::tc_fence_after();
         if (live) {
           const uint32_t st = tmem + b * 128 + hf * 64 + lane_off;
-          uint32_t x[64];
+          uint32_t x[32];
           ptx::tmem_ld32(st, x);
-          ptx::tmem_ld32(st + 32, x + 32);
           if (i == 0) read_mask();
           const bool whole = (msk.x & msk.y) == 0xffffffffu;
           const float cs = flip ? -c : c;
@@ -238,38 +237,43 @@ __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
           f32x2 la, lb;
           uint32_t h[32];
           float top = neg_inf, top2 = neg_inf;
-          // the weights against `base`, their sums in la and lb, the maximum on the way. Two
-          // copies of the loop: a test of the mask at each weight would cost as much as the weight
+          // the weights against `base`, their sums in la and lb, the maximum on the way; 32 columns
+          // of S at a time, the first already on their way into x. Two copies of the loop: a test
+          // of the mask at each weight would cost as much as the weight
           auto weights = [&](auto masked) {
             const f32x2 nb2 = f2(-base, -base);
             la = lb = f2(0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < 64; e += 2) {
-              const float y0 = __uint_as_float(x[e]), y1 = __uint_as_float(x[e + 1]);
-              const bool in0 = ((e < 32 ? msk.x : msk.y) >> (e & 31)) & 1;
-              const bool in1 = ((e < 32 ? msk.x : msk.y) >> ((e & 31) + 1)) & 1;
-              float p0, p1;
-              f2_split(fma2(f2(y0, y1), c2, nb2), p0, p1);
-              p0 = exp2_approx(p0);
-              p1 = exp2_approx(p1);
-              if (masked.v) {
-                p0 = in0 ? p0 : 0.f;
-                p1 = in1 ? p1 : 0.f;
-                top = in0 ? fmaxf(top, flip ? -y0 : y0) : top;
-                top = in1 ? fmaxf(top, flip ? -y1 : y1) : top;
-              } else {
-                float &t = e & 2 ? top2 : top;
-                t = fmaxf(fmaxf(t, y0), y1);
+            for (int g = 0; g < 2; ++g) {
+              if (g) ptx::tmem_ld32(st + 32, x);
+              ptx::tmem_ld_wait_all<32>(x);
+              const uint32_t bits = g ? msk.y : msk.x;
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const float y0 = __uint_as_float(x[e]), y1 = __uint_as_float(x[e + 1]);
+                float p0, p1;
+                f2_split(fma2(f2(y0, y1), c2, nb2), p0, p1);
+                p0 = exp2_approx(p0);
+                p1 = exp2_approx(p1);
+                if (masked.v) {
+                  const bool in0 = (bits >> e) & 1, in1 = (bits >> (e + 1)) & 1;
+                  p0 = in0 ? p0 : 0.f;
+                  p1 = in1 ? p1 : 0.f;
+                  top = in0 ? fmaxf(top, flip ? -y0 : y0) : top;
+                  top = in1 ? fmaxf(top, flip ? -y1 : y1) : top;
+                } else {
+                  float &t = e & 2 ? top2 : top;
+                  t = fmaxf(fmaxf(t, y0), y1);
+                }
+                if (e & 2)
+                  lb = add2(lb, f2(p0, p1));
+                else
+                  la = add2(la, f2(p0, p1));
+                h[16 * g + e / 2] = pack_bf16(p0, p1);
               }
-              if (e & 2)
-                lb = add2(lb, f2(p0, p1));
-              else
-                la = add2(la, f2(p0, p1));
-              h[e / 2] = pack_bf16(p0, p1);
             }
             top = fmaxf(top, top2);
           };
-          ptx::tmem_ld_wait_all<64>(x);
           if (whole && !flip)
             weights(Int<0>());
           else
@@ -304,8 +308,6 @@ __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
             }
             base = m > neg_inf ? m * c : 0.f;
             ptx::tmem_ld32(st, x);
-            ptx::tmem_ld32(st + 32, x + 32);
-            ptx::tmem_ld_wait_all<64>(x);
             weights(Int<1>());
           }
           ptx::tmem_st32(st + 32, h);  // P over the end of its half of S
@@ -500,36 +502,29 @@ __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
     // in turn, so that the tensor core works on one during the softmax of the other; QT 1: S of a
     // tile before P V of the one before it. Issuing an MMA takes a few instructions only: the
     // descriptors of a tile's steps differ by constants ----
-    // Q of a segment, once S of the one before is complete. Rows of a copy past the block's are
-    // other requests' or zero: their results go nowhere
-    uint32_t segs = 0, out_ph = 0;
-    bool two = false;  // the last segment had both query tiles
-    auto load_q = [&]() {
-      if (segs) {
-        wait(bar(S::q_empty), (segs - 1) & 1);
-        for (int t = 0; t <= two; ++t) {  // its output has gone through the queries' place
-          wait(bar(S::o_free + t), (out_ph >> t) & 1);
-          out_ph ^= 1u << t;
+    if (ptx::elect_one()) {
+      // Q of a segment, once S of the one before is complete and its output has gone through Q's
+      // place. Rows of a copy past the block's are other requests' or zero: their results go nowhere
+      uint32_t segs = 0, o_ph = 0;  // o_ph: a bit for each query tile
+      bool two = false;             // the last segment had both
+      auto load_q = [&]() {
+        if (segs) {
+          wait(bar(S::q_empty), (segs - 1) & 1);
+          for (int t = 0; t <= two; ++t) {
+            wait(bar(S::o_free + t), (o_ph >> t) & 1);
+            o_ph ^= 1u << t;
+          }
         }
-      }
-      ++segs;
-      two = S::QT == 2 && s.rows > kRow;
-      if (dead) return;
-      ptx::mbar_arrive_expect_tx(bar(S::q_full), s.own ? maps.own_bytes : maps.group_bytes);
-      const int y = maps.q_step ? 0 : s.kvh * a.hpk;
-      const int z = maps.q_step ? s.r0 * a.hq + s.row0 : s.r0 + s.row0 / a.hpk;
-      for (int c = 0; c < S::DK; ++c)
-        ptx::tma_3d(sb + S::q + c * S::QT * kChunk, s.own ? &maps.q_own : &maps.q_group, c * 64, y,
-                    z, bar(S::q_full));
-    };
-    if (warp == S::kQ) {
-      if (ptx::elect_one())
-        while (more) {
-          s = after;
-          load_q();
-          more = walk.next(a, plan, &after);
-        }
-    } else if (ptx::elect_one()) {
+        ++segs;
+        two = S::QT == 2 && s.rows > kRow;
+        if (dead) return;
+        ptx::mbar_arrive_expect_tx(bar(S::q_full), s.own ? maps.own_bytes : maps.group_bytes);
+        const int y = maps.q_step ? 0 : s.kvh * a.hpk;
+        const int z = maps.q_step ? s.r0 * a.hq + s.row0 : s.r0 + s.row0 / a.hpk;
+        for (int c = 0; c < S::DK; ++c)
+          ptx::tma_3d(sb + S::q + c * S::QT * kChunk, s.own ? &maps.q_own : &maps.q_group, c * 64,
+                      y, z, bar(S::q_full));
+      };
       constexpr uint32_t id_s = 1u << 4 | 1u << 7 | 1u << 10 | (kTok >> 3) << 17 | (kRow >> 4) << 24;
       // V is MN-major
       constexpr uint32_t id_o =
@@ -538,7 +533,7 @@ __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
       const uint32_t ring = sb + S::ring;
       Place<S::NST> kp, vp;
       uint32_t tiles = 0;                                // QT 1: tile k has S buffer k % 2
-      uint32_t q_ph = 0, p_ph = 0, o_ph = 0, o_any = 0;  // a bit for each S buffer, query tile
+      uint32_t q_ph = 0, p_ph = 0;                       // p_ph: a bit for each S buffer
       const uint32_t q0 = desc_k(sb + S::q);             // [chunk][query tile][128 rows]
       auto landed = [&](const Place<S::NST> &at) {
         wait(bar(S::full) + 8 * at.st, at.ph);
@@ -572,13 +567,6 @@ __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
         const uint32_t p = tmem + b * 128, d = tmem + S::o_col + t.v * 128;
         Place<S::NST> at = vp;
         if (ends.v & 1) landed(at);  // before P is, as a rule
-        if (first_tile) {  // the last segment's output has been read
-          if ((o_any >> t.v) & 1) {
-            wait(bar(S::o_free + t.v), (o_ph >> t.v) & 1);
-            o_ph ^= 1u << t.v;
-          }
-          o_any |= 1u << t.v;
-        }
         wait(bar(S::p_full) + 16 * b, (p_ph >> b) & 1);
         if (dead) return;
         ptx::tc_fence_after();
@@ -615,6 +603,7 @@ __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
       constexpr Int<3> only;
       while (more) {
         s = after;
+        load_q();
         more = walk.next(a, plan, &after);
         const int n = tiles_of(s.tok0, s.tok1, kTokSh);
         // the stages come in the order in which they are read:
