@@ -45,7 +45,11 @@ template <int DK_, int DV_, int QT_, int UC_, int NST_, int NL_>
 struct Shape {
   static constexpr int DK = DK_, DV = DV_, QT = QT_, UC = UC_, NST = NST_, NL = NL_;
   static constexpr int kSoft = 8 * QT, kMma = kSoft + NL;  // softmax warps; the MMA warp
-  static constexpr int kThr = 32 * (kMma + 1);
+  // With two query tiles the softmax warps take registers of the others; whole warpgroups
+  static constexpr bool kShift = QT == 2;
+  static constexpr int kThr = 32 * (kShift ? (kMma + 4) / 4 * 4 : kMma + 1);
+  static constexpr int kRegsSoft = 96, kRegsRest = 48;
+  static constexpr int kRegs = 32 * kSoft * kRegsSoft + (kThr - 32 * kSoft) * kRegsRest;
   static constexpr int kStage = UC * kChunk;
   static constexpr int q = 0;
   // the queries' place takes the output on its way out, 4 KB a softmax warp
@@ -184,6 +188,7 @@ __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
 
   if (warp < S::kSoft) {
     // ---- softmax: thread = half of a query row ----
+    if (S::kShift) ptx::regs_more<S::kRegsSoft>();
     const int w = warp >> 3;                       // query tile
     const int hf = (warp >> 2) & 1;                // half of the tokens, of O's columns
     const int row = (warp & 3) * 32 + lane;
@@ -366,6 +371,7 @@ __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
       arrive(bar(S::o_free + w));
     }
   } else if (warp < S::kMma) {
+    if (S::kShift) ptx::regs_fewer<S::kRegsRest>();
     // ---- K and V rows into the ring: a warp brings kPart tokens of each tile, a lane holds the
     // slots of kLane. Copies by tensor map are issued by one thread of the warp, which stands in
     // for the others' arrivals; one issues a copy in about 100 cycles ----
@@ -498,11 +504,12 @@ __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
     }
     ptx::cp_async_wait_all();
   } else {
-    // ---- MMAs and Q, a warp and one thread of it each. QT 2: S and P V of the two query tiles
+    if (S::kShift) ptx::regs_fewer<S::kRegsRest>();
+    // ---- MMAs and Q, one thread. QT 2: S and P V of the two query tiles
     // in turn, so that the tensor core works on one during the softmax of the other; QT 1: S of a
     // tile before P V of the one before it. Issuing an MMA takes a few instructions only: the
     // descriptors of a tile's steps differ by constants ----
-    if (ptx::elect_one()) {
+    if (warp == S::kMma && ptx::elect_one()) {
       // Q of a segment, once S of the one before is complete and its output has gone through Q's
       // place. Rows of a copy past the block's are other requests' or zero: their results go nowhere
       uint32_t segs = 0, o_ph = 0;  // o_ph: a bit for each query tile
@@ -672,6 +679,11 @@ __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
 
 template <class S>
 cudaError_t configure() {
+  cudaFuncAttributes at;
+  cudaError_t e = cudaFuncGetAttributes(&at, prefix_tc_kernel<S>);
+  if (e != cudaSuccess) return e;
+  // the warps' shares come out of the registers that the block is launched with
+  if (S::kShift && at.numRegs * S::kThr < S::kRegs) return cudaErrorLaunchOutOfResources;
   return cudaFuncSetAttribute(prefix_tc_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               S::total);
 }
