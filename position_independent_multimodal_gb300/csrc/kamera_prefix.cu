@@ -62,6 +62,18 @@ __device__ __forceinline__ void plan_scan(long long (&x)[N], long long (&total)[
   }
 }
 
+// Picks of the classes without an index into registers, which would put them into local memory.
+template <class T>
+__device__ __forceinline__ T by_class(int c, const T &wide, const T &thin) {
+  return c ? thin : wide;
+}
+__device__ __forceinline__ PrefixPlan::Lists lists_of(const PrefixPlan &p, int c) {
+  const PrefixPlan::Lists &a = p.cls[0], &b = p.cls[1];
+  return {c ? b.g_u0 : a.g_u0,         c ? b.g_first : a.g_first,   c ? b.g_size : a.g_size,
+          c ? b.g_prefix : a.g_prefix, c ? b.g_lead : a.g_lead,     c ? b.start : a.start,
+          c ? b.carry_lse : a.carry_lse, c ? b.carry_o : a.carry_o};
+}
+
 // One CTA: checks the arguments, lists the groups and requests that have units, and finds each
 // worker's first block. Bound: the latency of its few dependent steps.
 __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_constant__ PrefixArgs a) {
@@ -134,7 +146,7 @@ __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_cons
       l = near_g ? near_lead[g] : __ldcg(p.lead + g);
       if (l != 0x7FFFFFFF && prefix > 0) {
         c = class_of(a.shape, n * hpk);
-        const PrefixClass &k = a.shape.cls[c];
+        const PrefixClass k = by_class(c, a.shape.cls[0], a.shape.cls[1]);
         const int tiles = tiles_of(0, prefix, k.tile_sh);
         units = (long long)a.n_kv * k.vh * ceil_div(n * hpk, k.rb) * tiles;
         if (c == 0) {
@@ -147,18 +159,20 @@ __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_cons
     long long x[3] = {c == 0 ? units : 0, c == 1 ? units : 0, one}, total[3];
     plan_scan(x, total);
     if (g < G) {
-      const long long at = base[c] + x[c] - units;
+      const long long at = by_class(c, base[0] + x[0], base[1] + x[1]) - units;
       if (units > 0) {
-        const int k = listed[c] + (int)((x[2] - one) >> (32 * c));
-        p.cls[c].g_u0[k] = at;
+        const int k = by_class(c, listed[0], listed[1]) + (int)((x[2] - one) >> (32 * c));
+        const PrefixPlan::Lists to = lists_of(p, c);
+        to.g_u0[k] = at;
         if (k < kPlanNear) near_u0[c][k] = at;
-        p.cls[c].g_first[k] = s0;
-        p.cls[c].g_size[k] = n;
-        p.cls[c].g_prefix[k] = prefix;
-        p.cls[c].g_lead[k] = l;
+        to.g_first[k] = s0;
+        to.g_size[k] = n;
+        to.g_prefix[k] = prefix;
+        to.g_lead[k] = l;
       }
       p.gr_u0[g] = units > 0 ? at : -1;
     }
+#pragma unroll
     for (int k = 0; k < 2; ++k) {
       base[k] += total[k];
       listed[k] += (int)(total[2] >> (32 * k));
@@ -167,7 +181,7 @@ __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_cons
   __syncthreads();
   // requests: the blocks of their own tokens
   const long long prefix_units[2] = {base[0], base[1]};
-  const PrefixClass &ok = a.shape.cls[own_cls];
+  const PrefixClass ok = by_class(own_cls, a.shape.cls[0], a.shape.cls[1]);
   const int blocks = a.n_kv * ok.vh * ceil_div(hpk, ok.rb);
   int own_listed = 0;
   for (int r0 = 0; r0 < R; r0 += kPlanThr) {
@@ -178,7 +192,7 @@ __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_cons
     long long x[2] = {units, units > 0}, total[2];
     plan_scan(x, total);
     if (r < R) {
-      const long long at = base[own_cls] + x[0] - units;
+      const long long at = by_class(own_cls, base[0], base[1]) + x[0] - units;
       p.req_pu0[r] = g >= 0 ? p.gr_u0[g] : -1;
       p.req_ou0[r] = units > 0 ? at : -1;
       if (units > 0) {
@@ -190,14 +204,16 @@ __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_cons
         p.r_to[k] = ctx;
       }
     }
-    base[own_cls] += total[0];
+    base[0] += own_cls ? 0 : total[0];
+    base[1] += own_cls ? total[0] : 0;
     own_listed += (int)total[1];
   }
   __syncthreads();
   // workers: with fewer units than would give each `least`, fewer have any
 #pragma unroll 1
   for (int c = 0; c < 2; ++c) {
-    const PrefixClass k = a.shape.cls[c];
+    const PrefixClass k = by_class(c, a.shape.cls[0], a.shape.cls[1]);
+    const PrefixPlan::Lists list = lists_of(p, c);
     const long long U = c ? base[1] : base[0], own0 = c ? prefix_units[1] : prefix_units[0];
     const int groups = c ? listed[1] : listed[0];
     const long long few = div_pos(U + k.least - 1, k.least);
@@ -219,13 +235,12 @@ __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_cons
       }
     }
     const long long quot = div_pos(T, per), rem = T - quot * per;
-    const long long *g_u0 = p.cls[c].g_u0;
     for (int w = tid; w < n; w += kPlanThr) {
       const int span = w / per;
       const long long u = span * T + first_unit(quot, rem, w - span * per);
       const bool own = u >= own0;
       const int count = own ? own_listed : groups;
-      const long long *u0 = count <= kPlanNear ? (own ? near_r : near_u0[c]) : (own ? p.r_u0 : g_u0);
+      const long long *u0 = count <= kPlanNear ? (own ? near_r : near_u0[c]) : (own ? p.r_u0 : list.g_u0);
       int lo = 0, hi = count - 1;  // the last listed one that starts at or before u
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -234,13 +249,13 @@ __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_cons
         else
           hi = mid - 1;
       }
-      const int from = own ? p.r_from[lo] : 0, to = own ? p.r_to[lo] : p.cls[c].g_prefix[lo];
+      const int from = own ? p.r_from[lo] : 0, to = own ? p.r_to[lo] : list.g_prefix[lo];
       const int tiles = tiles_of(from, to, k.tile_sh);
-      const int first = own ? p.r_list[lo] : p.cls[c].g_first[lo];
-      const int size = own ? 1 : p.cls[c].g_size[lo], lead = own ? first : p.cls[c].g_lead[lo];
+      const int first = own ? p.r_list[lo] : list.g_first[lo];
+      const int size = own ? 1 : list.g_size[lo], lead = own ? first : list.g_lead[lo];
       const int nrb = ceil_div(size * hpk, k.rb);
       const long long d = u - u0[lo], b = div_pos(d, tiles), kh = div_pos(b, nrb);
-      int4 *rec = p.cls[c].start + 3 * w;
+      int4 *rec = list.start + 3 * w;
       rec[0] = make_int4(lo | (own ? 1 << 30 : 0), (int)(b - kh * nrb), (int)kh,
                          (int)(d - b * tiles));
       rec[1] = make_int4(first, size, lead, from);
