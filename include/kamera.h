@@ -409,13 +409,13 @@ kamera_status kamera_decode_attention(const kamera_handle *handle, const kamera_
  * k_weight : bf16 [head_dim] (MLA: [latent_dim]), or NULL likewise.
  * positions: int64 [num_tokens], or [num_tokens][3] = (t, h, w) for M-RoPE layouts.
  * req, tok : int32 [num_tokens]: the page-table row and logical token of each. A negative req
- *            marks a row of padding: what its other inputs hold does not matter, nothing is written.
+ *            marks a row of padding: its other inputs do not matter, nothing of it is written.
  * q_out    : bf16, heads of token t at q_out + t * q_out_stride; may be q itself (with the same
  *            stride), and overlaps none of the inputs otherwise.
  * All device memory; q, k, v, weights and q_out 16-byte aligned, positions 8, req and tok 4.
  * A req or tok outside the page table sets KAMERA_DEVICE_BAD_ITEM and nothing of that token is
  * written; a page outside the pool sets KAMERA_DEVICE_SLOT_OOB and the token's K and V are not
- * written (its queries are). Tokens must not share a slot.
+ * written (its queries are). Tokens must not share a slot. Limit: num_q_heads <= 256.
  */
 typedef struct kamera_new_tokens {
   const void *q;

@@ -90,7 +90,8 @@ struct Turn {
 };
 
 template <bool kNeox>
-__device__ __forceinline__ Turn make_turn(const float2 *ph, const __nv_bfloat16 *w, int ca, int cb) {
+__device__ __forceinline__ Turn make_turn(const float2 *ph, const __nv_bfloat16 *w, int ca,
+                                          int cb) {
   Unit u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) u.a[i] = u.b[i] = f2(1.f, 1.f);
@@ -280,7 +281,8 @@ __global__ void __launch_bounds__(kThr, 2) append_kernel(const __grid_constant__
   }
   {
     const bool norm = gqa && a.k_weight;
-    const Turn turn = make_turn<kNeox>(ph, norm ? a.k_weight : nullptr, mine ? ca : 0, mine ? cb : 8);
+    const Turn turn =
+        make_turn<kNeox>(ph, norm ? a.k_weight : nullptr, mine ? ca : 0, mine ? cb : 8);
     const bool write = mine && slots[tk] >= 0;
     __nv_bfloat16 *dst = a.pool.k + layer_k + (write ? slots[tk] * lay.row_k : 0) + off;
     for (int h = h_first; h < n_k + h_first; h += groups) {
@@ -380,7 +382,7 @@ __global__ void __launch_bounds__(kThr, 2) append_kernel(const __grid_constant__
 // Bound: HBM.
 // ---------------------------------------------------------------------------------------
 
-constexpr int kStreamRoom = 214 * 1024;  // shared memory for the rows in flight (and 12 KB of phases)
+constexpr int kStreamRoom = 214 * 1024;  // shared memory for the rows in flight (phases: 12 KB)
 constexpr int kStreamWarps = 12;         // warps of a CTA at most (and 168 registers a thread)
 constexpr int kStreamLeast = 8;          // and at least: fewer are slower than the CTA kernel
 
@@ -417,8 +419,8 @@ StreamPlan stream_plan(const DevLayout &l, int hq, bool copy_q) {
 }
 
 template <bool kNeox>
-__global__ void __launch_bounds__(32 * kStreamWarps, 1) append_stream_kernel(const __grid_constant__ AppendArgs a,
-                                                                            const StreamPlan sp) {
+__global__ void __launch_bounds__(32 * kStreamWarps, 1) append_stream_kernel(
+    const __grid_constant__ AppendArgs a, const StreamPlan sp) {
   extern __shared__ __align__(16) unsigned char smem[];  // [warps][2][chunks][32] of 16 bytes
   __shared__ float2 phases[kStreamWarps][kMaxPairs];
   ptx::launch_dependents();
@@ -548,7 +550,8 @@ __global__ void __launch_bounds__(32 * kStreamWarps, 1) append_stream_kernel(con
       const Turn turn = make_turn<kNeox>(ph, a.q_weight, ca, cb);
       const bool norm = a.q_weight != nullptr;
       __nv_bfloat16 *dst = a.q_out + t * a.q_out_stride + off + h_first * pitch;
-      for (int h = h_first, c = sp.q; h < a.hq + h_first; h += groups, c += 2, dst += groups * pitch)
+      for (int h = h_first, c = sp.q; h < a.hq + h_first;
+           h += groups, c += 2, dst += groups * pitch)
         finish_head<kNeox>(band_chunk(buf, c), band_chunk(buf, c + 1), turn, norm, a.eps, w,
                            inv_band, unit && h < a.hq, dst + ca, dst + cb);
     }

@@ -25,7 +25,8 @@ namespace kamera {
 namespace {
 
 constexpr int kPlanThr = 256;
-constexpr int kSpanExtra = 6;    // tiles
+// Tiles. 128 requests of 28/4 heads of 128 over 65500 tokens: 161 us with spans, 168 without.
+constexpr int kSpanExtra = 6;
 constexpr int kPlanNear = 1024;  // groups and listed entries kept in shared memory
 
 // Inclusive scans of N values at a time over the CTA's threads, in place; total: their sums.
@@ -75,8 +76,10 @@ __device__ __forceinline__ PrefixPlan::Lists lists_of(const PrefixPlan &p, int c
 }
 
 // One CTA: checks the arguments, lists the groups and requests that have units, and finds each
-// worker's first block. Bound: the latency of its few dependent steps.
-__global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_constant__ PrefixArgs a) {
+// worker's first block. Bound: the latency of its few dependent steps (8 to 11 us for 4 to 128
+// requests; 512 or 1024 threads are slower, by their barriers).
+__global__ void __launch_bounds__(kPlanThr)
+    prefix_plan_kernel(const __grid_constant__ PrefixArgs a) {
   ptx::launch_dependents();
   const PrefixPlan p = prefix_plan(a.shape, a.ws, a.n_reqs, a.hq, a.dv);
   __shared__ int near_start[kPlanNear + 1], near_lead[kPlanNear];
@@ -240,7 +243,8 @@ __global__ void __launch_bounds__(kPlanThr) prefix_plan_kernel(const __grid_cons
       const long long u = span * T + first_unit(quot, rem, w - span * per);
       const bool own = u >= own0;
       const int count = own ? own_listed : groups;
-      const long long *u0 = count <= kPlanNear ? (own ? near_r : near_u0[c]) : (own ? p.r_u0 : list.g_u0);
+      const long long *u0 = count <= kPlanNear ? (own ? near_r : near_u0[c])
+                                               : (own ? p.r_u0 : list.g_u0);
       int lo = 0, hi = count - 1;  // the last listed one that starts at or before u
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -596,6 +600,10 @@ PrefixShape prefix_shape(const DevLayout &l, int hq) {
   if (prefix_tc_layout(l)) {
     s.cls[0] = prefix_tc_class(l, hq);
     s.cls[1] = prefix_thin_class(l);
+    // A wide tile costs the same for any number of rows up to 128, thin ones as many times 16 as
+    // there are rows. Eight groups over 4000 tokens, 28/4 heads of 128, thin | wide, in us: 14 rows
+    // 45 | 61, 28 rows 58 | 67, 35 rows 75 | 62, 56 rows 92 | 61. MLA: 32 rows 43 | 57, 64 rows
+    // 63 | 53.
     s.wide_rows = 32;
   } else {
     s.cls[0] = {1, 1, 1, 7, 1};  // not used: no block is wide

@@ -1,6 +1,6 @@
 // Thin blocks of attention over shared prefixes: at most 16 query rows against long rows of
-// tokens, as one request's heads of a KV head are. The bytes of K and V bound them, so the work is laid out for
-// loads: m16n8k16 tensor-core products on registers (16 rows are one such tile; a tcgen05 tile
+// tokens, as one request's heads of a KV head are. The bytes of K and V bound them, so the work is
+// laid out for loads: m16n8k16 tensor-core products on registers (16 rows are one such tile; a tcgen05 tile
 // would have 128), K and V straight from the page rows by cp.async, several stages ahead and
 // across the ends of segments.
 //
@@ -71,8 +71,8 @@ __device__ __forceinline__ uint32_t at16(int row, int piece) {
 }
 
 template <class T>
-__global__ void __launch_bounds__(T::WARPS * 32, 1) prefix_thin_kernel(const __grid_constant__ PrefixArgs a,
-                                                                         int beside) {
+__global__ void __launch_bounds__(T::WARPS * 32, 1)
+    prefix_thin_kernel(const __grid_constant__ PrefixArgs a, int beside) {
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int D = T::D, kTok = T::kTok;
   const PrefixPlan plan = prefix_plan(a.shape, a.ws, a.n_reqs, a.hq, a.dv);
@@ -292,8 +292,8 @@ __device__ __forceinline__ uint32_t mla16(int row, int piece) {
   return row * ThinMla::kRow + ((piece ^ (row & 7)) << 4);
 }
 
-__global__ void __launch_bounds__(ThinMla::kThr, 1) prefix_thin_mla_kernel(const __grid_constant__ PrefixArgs a,
-                                                                         int beside) {
+__global__ void __launch_bounds__(ThinMla::kThr, 1)
+    prefix_thin_mla_kernel(const __grid_constant__ PrefixArgs a, int beside) {
   extern __shared__ __align__(128) unsigned char smem[];
   using M = ThinMla;
   const PrefixPlan plan = prefix_plan(a.shape, a.ws, a.n_reqs, a.hq, a.dv);

@@ -425,3 +425,27 @@ def test_refusals():
         call(q=q[:, :27].contiguous(), out=b.out[:, :27].contiguous(), lse=b.lse[:, :27].contiguous())
     torch.cuda.synchronize()
     assert torch.all(b.out == -7) and int(b.st.item()) == 0
+
+
+@pytest.mark.parametrize("groups,prefix,size", [(1, 3000, 41), (1, 640, 130), (3, 2000, 9),
+                                                (40, 300, 6), (2, 129, 64)])
+@pytest.mark.parametrize("name", ["gqa128-group7", "gqa64-group3", "mla-16-heads"])
+def test_prefixes_of_one_length(name, groups, prefix, size):
+    # wide blocks that all have as many tiles: each is shared out among workers of its own, where
+    # there are workers enough
+    b = Batch(name, [(prefix, [(3 * i + k) % 5 for i in range(size)]) for k in range(groups)], seed=15)
+    assert b.run() == 0
+    n = groups * size
+    b.check(reqs=sorted({0, 1, size - 1, size // 2, n // 2, n - size, n - 1} & set(range(n))))
+
+
+@pytest.mark.parametrize("name", ["gqa128-group7", "mla-16-heads", "gqa80"])
+def test_workspace_at_any_16_bytes_and_nothing_behind_it(name):
+    b = Batch(name, [(300, [40, 1, 200, 7, 9, 4, 4, 4]), (0, [77])], seed=16)
+    size = len(b.ws)
+    for at in (16, 48, 112, 128):
+        room = torch.full((size + 512,), 0x5A, dtype=torch.uint8, device="cuda")
+        b.ws = room[at:at + size]
+        assert b.run() == 0
+        b.check()
+        assert torch.all(room[:at] == 0x5A) and torch.all(room[at + size:] == 0x5A)
