@@ -385,7 +385,7 @@ def _pool_c(handle: Handle, pool: Pool) -> tuple[kamera_pool, int]:
     are launched there, on the current stream unless another is given."""
     k, v, pt = pool.k, pool.v, pool.page_table
     dev = k.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError("the pool must be on the current CUDA device")
     c = handle._c
     gqa = c.kind == KAMERA_GQA

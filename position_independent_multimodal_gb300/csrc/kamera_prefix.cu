@@ -500,13 +500,15 @@ __global__ void __launch_bounds__(kThr) prefix_gen_kernel(const __grid_constant_
 // Merge: one warp per (request, query head) and kCols columns. The parts of a row are its home
 // places and the carries of the workers that start inside its blocks: the lanes take their
 // log-sum-exps, then every lane adds up its columns of eight parts at a time. One rounding to
-// bf16. Bound: latency, then the bytes of the parts.
+// bf16. Bound: the latency of a chain of loads (request, places, log-sum-exps, parts), then the
+// bytes of the parts. Three CTAs an SM (80 registers), so that a call is one wave: with 99 and two
+// CTAs 128 requests take 3 us more; with 64 registers spills cost as much.
 // ---------------------------------------------------------------------------------------
 
 constexpr int kCols = 128;  // columns of a warp: four a lane
 
-__global__ void __launch_bounds__(kThr) prefix_merge_kernel(const __grid_constant__ PrefixArgs a,
-                                                            int slices) {
+__global__ void __launch_bounds__(kThr, 3) prefix_merge_kernel(const __grid_constant__ PrefixArgs a,
+                                                               int slices) {
   const PrefixPlan p = prefix_plan(a.shape, a.ws, a.n_reqs, a.hq, a.dv);
   const int lane = threadIdx.x & 31;
   // fewer than 2^31 warps: 65535 requests x 256 heads x 8 slices
