@@ -16,8 +16,9 @@
 // takes several of its heads at a time, so that their loads are in flight together, before the
 // phases and slots are known. Few tokens (latency: 8 us at 8 tokens), or long rows.
 // append_stream_kernel: a warp to a token, in CTAs that stay, each lane's next chunks arriving by
-// cp.async while it works. 16381 tokens of 28/4 heads of 128: 66 us, 302 MB moved, 4.6 TB/s
-// (append_kernel 82 us); the instructions of the turn and norm take half of the issue slots.
+// cp.async while it works, two heads at a time (one at a time: 4 us more). 16381 tokens of 28/4
+// heads of 128: 62 us, 302 MB moved, 4.9 TB/s (append_kernel 82 us); few warps fit, and the chain of
+// a head's norm and rotation takes its time in each.
 // Bound: HBM (every byte is read and written once) at many tokens, latency at few.
 #include <mutex>
 
@@ -129,8 +130,8 @@ __device__ __forceinline__ void scale_unit(Unit &u, float f) {
   }
 }
 
-// Sum of squares over the unit's group of w lanes.
-__device__ __forceinline__ float unit_sum_sq(const Unit &u, int w) {
+// Sum of squares of a unit, and over its group of w lanes.
+__device__ __forceinline__ float sum_sq16(const Unit &u) {
   f32x2 s = f2(0.f, 0.f), v = s;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -139,9 +140,12 @@ __device__ __forceinline__ float unit_sum_sq(const Unit &u, int w) {
   }
   float lo, hi;
   f2_split(add2(s, v), lo, hi);
-  lo += hi;
-  for (int o = w >> 1; o > 0; o >>= 1) lo += __shfl_xor_sync(0xffffffffu, lo, o);
-  return lo;
+  return lo + hi;
+}
+__device__ __forceinline__ float unit_sum_sq(const Unit &u, int w) {
+  float s = sum_sq16(u);
+  for (int o = w >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
 }
 
 __device__ __forceinline__ float sum_sq8(const float *x) {
@@ -189,6 +193,52 @@ __device__ __forceinline__ void finish_head(const uint4 &x, const uint4 &y, cons
   pack_unit<kNeox>(u, &za, &zb);
   st16(da, za);
   st16(db, zb);
+}
+
+// Two heads of a unit's lanes, the second one's chunks `step` columns behind the first's, with
+// their reductions in flight together (chunks a and b of each in x).
+template <bool kNeox>
+__device__ __forceinline__ void finish_two(const uint4 (&x)[4], const Turn &turn, bool norm,
+                                           float eps, int w, float inv_band, bool write0,
+                                           bool write1, __nv_bfloat16 *da, __nv_bfloat16 *db,
+                                           int step) {
+  Unit u = unpack_unit<kNeox>(x[0], x[1]), v = unpack_unit<kNeox>(x[2], x[3]);
+  float ru = 1.f, rv = 1.f;
+  if (norm) {
+    float su = sum_sq16(u), sv = sum_sq16(v);
+    for (int o = w >> 1; o > 0; o >>= 1) {
+      const float tu = __shfl_xor_sync(0xffffffffu, su, o);
+      const float tv = __shfl_xor_sync(0xffffffffu, sv, o);
+      su += tu;
+      sv += tv;
+    }
+    su = fmaf(su, inv_band, eps);
+    sv = fmaf(sv, inv_band, eps);
+    const float fu = norm_scale(su), fv = norm_scale(sv);
+    if (__any_sync(0xffffffffu, fu != 1.f || fv != 1.f)) {
+      scale_unit(u, fu);
+      scale_unit(v, fv);
+      su = fmaf(unit_sum_sq(u, w), inv_band, eps * fu * fu);
+      sv = fmaf(unit_sum_sq(v, w), inv_band, eps * fv * fv);
+    }
+    ru = rsqrtf(su);
+    rv = rsqrtf(sv);
+  }
+  uint4 za, zb;
+  if (write0) {
+    turn_unit(turn, u);
+    if (norm) scale_unit(u, ru);
+    pack_unit<kNeox>(u, &za, &zb);
+    st16(da, za);
+    st16(db, zb);
+  }
+  if (write1) {
+    turn_unit(turn, v);
+    if (norm) scale_unit(v, rv);
+    pack_unit<kNeox>(v, &za, &zb);
+    st16(da + step, za);
+    st16(db + step, zb);
+  }
 }
 
 template <int kTok, bool kNeox>
@@ -550,8 +600,15 @@ __global__ void __launch_bounds__(32 * kStreamWarps, 1) append_stream_kernel(
       const Turn turn = make_turn<kNeox>(ph, a.q_weight, ca, cb);
       const bool norm = a.q_weight != nullptr;
       __nv_bfloat16 *dst = a.q_out + t * a.q_out_stride + off + h_first * pitch;
-      for (int h = h_first, c = sp.q; h < a.hq + h_first;
-           h += groups, c += 2, dst += groups * pitch)
+      // lanes of other groups may be out of heads a turn earlier: they take part all the same
+      int h = h_first, c = sp.q;
+      for (; h + groups < a.hq + h_first; h += 2 * groups, c += 4, dst += 2 * groups * pitch) {
+        const uint4 x[4] = {band_chunk(buf, c), band_chunk(buf, c + 1), band_chunk(buf, c + 2),
+                            band_chunk(buf, c + 3)};
+        finish_two<kNeox>(x, turn, norm, a.eps, w, inv_band, unit && h < a.hq,
+                          unit && h + groups < a.hq, dst + ca, dst + cb, groups * pitch);
+      }
+      if (h < a.hq + h_first)
         finish_head<kNeox>(band_chunk(buf, c), band_chunk(buf, c + 1), turn, norm, a.eps, w,
                            inv_band, unit && h < a.hq, dst + ca, dst + cb);
     }
@@ -626,7 +683,7 @@ cudaError_t launch(const AppendArgs &a, cudaStream_t s) {
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t s) {
   // One token a CTA, four, or a warp a token. Measured with a call's overhead, L2 flushed, in us:
   //                             T = 304: one four warps  608: one four warps  16381: four warps
-  //   28/4 heads of 128 (11 warps fit)    11   11    13        17   11    13          89    72
+  //   28/4 heads of 128 (11 warps fit)    11   11    13        17   11    13          89    68
   //   16 + 16 heads of 128 (5)            13   17    17        19   17    17         168   224
   //   6/2 heads of 64 (12)                11   11    11        15   11    11          66    33
   //   MLA, 16 heads copied (5)            13   15    14        20   15    15         142   154
