@@ -76,14 +76,14 @@ __device__ __forceinline__ PrefixPlan::Lists lists_of(const PrefixPlan &p, int c
 }
 
 // One CTA: checks the arguments, lists the groups and requests that have units, and finds each
-// worker's first block. Bound: the latency of its few dependent steps (8 to 11 us for 4 to 128
+// wide worker's first block. Bound: the latency of its few dependent steps (8 to 11 us for 4 to 128
 // requests; 512 or 1024 threads are slower, by their barriers).
 __global__ void __launch_bounds__(kPlanThr)
     prefix_plan_kernel(const __grid_constant__ PrefixArgs a) {
   ptx::launch_dependents();
   const PrefixPlan p = prefix_plan(a.shape, a.ws, a.n_reqs, a.hq, a.dv);
   __shared__ int near_start[kPlanNear + 1], near_lead[kPlanNear];
-  __shared__ long long near_u0[2][kPlanNear], near_r[kPlanNear];
+  __shared__ long long near_u0[kPlanNear], near_r[kPlanNear];  // of the wide class
   __shared__ int broken, least_tiles, most_tiles;
   const int tid = threadIdx.x, R = a.n_reqs, G = a.n_groups;
   const int hpk = a.hpk, own_cls = class_of(a.shape, hpk);
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kPlanThr)
   __syncthreads();
   if (broken) {  // the groups do not partition the requests: nothing is written
     for (int r = tid; r < R; r += kPlanThr) p.req_state[r] = 0;
-    if (tid < 16) p.head[tid] = 0;
+    if (tid <= 16) p.head[tid] = 0;
     if (tid == 0) atomicOr(a.status, KAMERA_DEVICE_BAD_ITEM);
     return;
   }
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kPlanThr)
         const int k = by_class(c, listed[0], listed[1]) + (int)((x[2] - one) >> (32 * c));
         const PrefixPlan::Lists to = lists_of(p, c);
         to.g_u0[k] = at;
-        if (k < kPlanNear) near_u0[c][k] = at;
+        if (c == 0 && k < kPlanNear) near_u0[k] = at;
         to.g_first[k] = s0;
         to.g_size[k] = n;
         to.g_prefix[k] = prefix;
@@ -238,12 +238,12 @@ __global__ void __launch_bounds__(kPlanThr)
       }
     }
     const long long quot = div_pos(T, per), rem = T - quot * per;
-    for (int w = tid; w < n; w += kPlanThr) {
+    for (int w = tid; c == 0 && w < n; w += kPlanThr) {
       const int span = w / per;
       const long long u = span * T + first_unit(quot, rem, w - span * per);
       const bool own = u >= own0;
       const int count = own ? own_listed : groups;
-      const long long *u0 = count <= kPlanNear ? (own ? near_r : near_u0[c])
+      const long long *u0 = count <= kPlanNear ? (own ? near_r : near_u0)
                                                : (own ? p.r_u0 : list.g_u0);
       int lo = 0, hi = count - 1;  // the last listed one that starts at or before u
       while (lo < hi) {
@@ -274,6 +274,8 @@ __global__ void __launch_bounds__(kPlanThr)
       head[4] = n;
       head[5] = T;
       head[6] = per;
+      head[7] = own0;
+      p.head[16] = own_listed;
     }
   }
 }

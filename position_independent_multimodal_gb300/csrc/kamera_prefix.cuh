@@ -23,15 +23,16 @@ namespace kamera {
 
 // What the plan kernel leaves for the others, in the workspace.
 struct PrefixPlan {
-  // per class c at head[8 c + .]: 0 units U, 1 groups listed, 4 workers n with units. k workers
-  // share a span of T units: 2 T / k, 3 T % k, 5 T, 6 k
+  // per class c at head[8 c + .]: 0 units U, 1 groups listed, 4 workers n with units, 7 units of
+  // prefixes. k workers share a span of T units: 2 T / k, 3 T % k, 5 T, 6 k. head[16]: requests
+  // listed
   long long *head;
   struct Lists {          // blocks of a class
     long long *g_u0;      // [R] first unit of the i-th listed group
     int *g_first, *g_size, *g_prefix, *g_lead;  // first request, requests, prefix, leader
-    int4 *start;          // [n][3] each worker's first block: list index (own: + 2^30), row block,
-                          //     KV head x half, tile; the listed entry's first request, requests,
-                          //     leader, first token; end of its tokens
+    int4 *start;          // [n][3] the wide class: each worker's first block: list index (own:
+                          //     + 2^30), row block, KV head x half, tile; the listed entry's first
+                          //     request, requests, leader, first token; end of its tokens
     float *carry_lse;     // [n][rb]
     float *carry_o;       // [n][rb][dv / vh]
   } cls[2];
@@ -68,7 +69,7 @@ __host__ __device__ inline PrefixPlan prefix_plan(const PrefixShape &sh, void *w
   auto i64 = [&]() { return reinterpret_cast<long long *>(take(8 * R)); };
   auto i32 = [&](long long n) { return reinterpret_cast<int *>(take(4 * n)); };
   auto f32 = [&](long long n) { return reinterpret_cast<float *>(take(4 * n)); };
-  p.head = reinterpret_cast<long long *>(take(128));
+  p.head = reinterpret_cast<long long *>(take(256));
   for (int c = 0; c < 2; ++c) {
     const PrefixClass &k = sh.cls[c];
     p.cls[c].g_u0 = i64();
@@ -76,7 +77,7 @@ __host__ __device__ inline PrefixPlan prefix_plan(const PrefixShape &sh, void *w
     p.cls[c].g_size = i32(R);
     p.cls[c].g_prefix = i32(R);
     p.cls[c].g_lead = i32(R);
-    p.cls[c].start = reinterpret_cast<int4 *>(take(48ll * k.n));
+    p.cls[c].start = reinterpret_cast<int4 *>(take(c == 0 ? 48ll * k.n : 0));
     p.cls[c].carry_lse = f32((long long)k.n * k.rb);
     p.cls[c].carry_o = f32((long long)k.n * k.rb * (dv / k.vh));
   }
@@ -170,13 +171,20 @@ struct SegmentWalk {
     tiles = tiles_of(from, to, a.shape.cls[C].tile_sh);
     nrb = ceil_div(size * a.hpk, a.shape.cls[C].rb);
   }
-  // One round of loads: the place is there for every worker, whether or not it has units.
+  // By whole warps. Wide: one round of loads; the place is there for every worker, whether or not it
+  // has units. Thin: a search by the warp; the plan would take 0.7 us for each 256 workers.
   __device__ __forceinline__ void start(const PrefixArgs &a, const PrefixPlan &p, int worker_) {
     const long long *head = p.head + 8 * C;
-    const int4 *rec = p.cls[C].start + 3 * worker_;
-    const int4 at = rec[0], e = rec[1];
-    const int last = rec[2].x;
-    const long long n = head[4], T = head[5], k = head[6];
+    int4 at, e;
+    int last;
+    if (C == 0) {
+      const int4 *rec = p.cls[C].start + 3 * worker_;
+      at = rec[0];
+      e = rec[1];
+      last = rec[2].x;
+    }
+    const long long n = head[4], T = head[5], k = head[6], own0 = head[7];
+    const int requests = (int)p.head[16];
     groups = (int)head[1];
     quot = head[2];
     rem = head[3];
@@ -186,6 +194,27 @@ struct SegmentWalk {
     worker = worker_ - span * (int)k;
     u = span * T + first_unit(quot, rem, worker);
     end = span * T + first_unit(quot, rem, worker + 1);
+    if (C == 1) {
+      own = u >= own0;
+      const long long *u0 = own ? p.r_u0 : p.cls[C].g_u0;
+      const int lane = threadIdx.x & 31;
+      long long from_u = 0;
+      i = 0;  // the last listed one that starts at or before u
+      for (int len = own ? requests : groups; len > 0;) {
+        const int step = (len + 31) >> 5, k = i + lane * step;
+        const long long v = lane * step < len ? u0[k] : 0x7FFFFFFFFFFFFFFFll;
+        const int j = __popc(__ballot_sync(0xffffffffu, v <= u)) - 1;
+        from_u = __shfl_sync(0xffffffffu, v, j);
+        i += j * step;
+        len = step == 1 ? 0 : min(step, len - j * step);
+      }
+      entry(a, p);
+      const long long d = u - from_u, b = div_pos(d, tiles), h = div_pos(b, nrb);
+      rbk = (int)(b - h * nrb);
+      kh = (int)h;
+      t = (int)(d - b * tiles);
+      return;
+    }
     own = at.x >> 30;
     i = at.x & 0x3FFFFFFF;
     first = e.x;
