@@ -25,8 +25,10 @@ namespace kamera {
 namespace {
 
 constexpr int kPlanThr = 256;
-// Tiles. 128 requests of 28/4 heads of 128 over 65500 tokens: 161 us with spans, 168 without.
-constexpr int kSpanExtra = 6;
+// Tiles. The wide kernel with workers of each block's own | with the units in equal parts, in us:
+// 128 requests of 28/4 heads of 128 over 65500 tokens 101 | 117, 40 requests of MLA over two prefixes
+// of 9003 41 | 49, 48 of 28/4 heads over three of 6001 18 | 21.
+constexpr int kOwnExtra = 6;
 constexpr int kPlanNear = 1024;  // groups and listed entries kept in shared memory
 
 // Inclusive scans of N values at a time over the CTA's threads, in place; total: their sums.
@@ -84,17 +86,14 @@ __global__ void __launch_bounds__(kPlanThr)
   const PrefixPlan p = prefix_plan(a.shape, a.ws, a.n_reqs, a.hq, a.dv);
   __shared__ int near_start[kPlanNear + 1], near_lead[kPlanNear];
   __shared__ long long near_u0[kPlanNear], near_r[kPlanNear];  // of the wide class
-  __shared__ int broken, least_tiles, most_tiles;
+  __shared__ int broken, worst, near_w0[kPlanThr], near_k[kPlanThr];
   const int tid = threadIdx.x, R = a.n_reqs, G = a.n_groups;
   const int hpk = a.hpk, own_cls = class_of(a.shape, hpk);
   const long long cap = (long long)a.pool.pt_stride * a.lay.page_size;
   const bool near_g = G <= kPlanNear;
   const int *start = near_g ? near_start : a.group_start;
   int *lead = near_g ? near_lead : p.lead;
-  if (tid == 0) {
-    broken = most_tiles = 0;
-    least_tiles = 0x7FFFFFFF;
-  }
+  if (tid == 0) broken = worst = 0;
   __syncthreads();
   for (int g = tid; g <= G; g += kPlanThr) {
     const int s = a.group_start[g];
@@ -150,12 +149,7 @@ __global__ void __launch_bounds__(kPlanThr)
       if (l != 0x7FFFFFFF && prefix > 0) {
         c = class_of(a.shape, n * hpk);
         const PrefixClass k = by_class(c, a.shape.cls[0], a.shape.cls[1]);
-        const int tiles = tiles_of(0, prefix, k.tile_sh);
-        units = (long long)a.n_kv * k.vh * ceil_div(n * hpk, k.rb) * tiles;
-        if (c == 0) {
-          atomicMin(&least_tiles, tiles);
-          atomicMax(&most_tiles, tiles);
-        }
+        units = (long long)a.n_kv * k.vh * ceil_div(n * hpk, k.rb) * tiles_of(0, prefix, k.tile_sh);
       }
     }
     const long long one = units > 0 ? 1ll << (32 * c) : 0;
@@ -225,22 +219,62 @@ __global__ void __launch_bounds__(kPlanThr)
       if (tid == 0) p.head[8 * c + 4] = 0;
       continue;
     }
-    // spans: one of all units, or one a block. The latter where that costs a worker no more than
-    // kSpanExtra tiles, about what a part of a second block costs it
-    long long T = U;
-    int per = n;
-    if (c == 0 && own0 == U && least_tiles == most_tiles) {
-      const int spans = (int)(U / most_tiles < n ? U / most_tiles : n + 1), part = n / spans;
-      if (part > 0 && ceil_div(most_tiles, part) <= U / n + kSpanExtra) {
-        T = most_tiles;
-        per = part < most_tiles ? part : most_tiles;
-        n = per * spans;
+    const long long quot = div_pos(U, n), rem = U - quot * n;
+    if (tid == 0) {
+      long long *head = p.head + 8 * c;
+      head[0] = U;
+      head[1] = groups;
+      head[2] = quot;
+      head[3] = rem;
+      head[4] = n;
+      head[7] = own0;
+      p.head[16] = own_listed;
+    }
+    if (c == 1) break;
+    // Workers for each block, in proportion to its tiles? Where that costs none more than kOwnExtra
+    // tiles, about what a part of a second block costs it.
+    if (own0 == U && groups <= kPlanThr) {
+      int tiles = 0, nrb = 0, per = 0;
+      if (tid < groups) {
+        tiles = tiles_of(0, list.g_prefix[tid], k.tile_sh);
+        nrb = ceil_div(list.g_size[tid] * hpk, k.rb);
+        per = (int)div_pos((long long)tiles * n, U);
+        const long long most = per ? ceil_div(tiles, per) : tiles;
+        if (per == 0 || most > quot + kOwnExtra) worst = 1;
+      }
+      long long x[1] = {(long long)a.n_kv * k.vh * nrb * per}, all[1];
+      plan_scan(x, all);  // at most n: each is rounded down
+      if (tid < groups) {
+        near_w0[tid] = (int)(x[0] - (long long)a.n_kv * k.vh * nrb * per);
+        near_k[tid] = per;
+      }
+      __syncthreads();
+      if (!worst) {
+        n = (int)all[0];
+        for (int w = tid; w < n; w += kPlanThr) {
+          int lo = 0, hi = groups - 1;
+          while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (near_w0[mid] <= w)
+              lo = mid;
+            else
+              hi = mid - 1;
+          }
+          const int to = list.g_prefix[lo], size = list.g_size[lo], per = near_k[lo];
+          const int tiles = tiles_of(0, to, k.tile_sh), nrb = ceil_div(size * hpk, k.rb);
+          const int b = (w - near_w0[lo]) / per, j = w - near_w0[lo] - b * per, kh = b / nrb;
+          const int q = tiles / per, r = tiles - q * per, t = (int)first_unit(q, r, j);
+          int4 *rec = list.start + 3 * w;
+          rec[0] = make_int4(lo, b - kh * nrb, kh, t);
+          rec[1] = make_int4(list.g_first[lo], size, list.g_lead[lo], 0);
+          rec[2] = make_int4(to, (int)first_unit(q, r, j + 1) - t, per - 1 - j, 0);
+        }
+        if (tid == 0) p.head[4] = n;
+        continue;
       }
     }
-    const long long quot = div_pos(T, per), rem = T - quot * per;
-    for (int w = tid; c == 0 && w < n; w += kPlanThr) {
-      const int span = w / per;
-      const long long u = span * T + first_unit(quot, rem, w - span * per);
+    for (int w = tid; w < n; w += kPlanThr) {
+      const long long u = first_unit(quot, rem, w);
       const bool own = u >= own0;
       const int count = own ? own_listed : groups;
       const long long *u0 = count <= kPlanNear ? (own ? near_r : near_u0)
@@ -263,19 +297,7 @@ __global__ void __launch_bounds__(kPlanThr)
       rec[0] = make_int4(lo | (own ? 1 << 30 : 0), (int)(b - kh * nrb), (int)kh,
                          (int)(d - b * tiles));
       rec[1] = make_int4(first, size, lead, from);
-      rec[2] = make_int4(to, 0, 0, 0);
-    }
-    if (tid == 0) {
-      long long *head = p.head + 8 * c;
-      head[0] = U;
-      head[1] = groups;
-      head[2] = quot;
-      head[3] = rem;
-      head[4] = n;
-      head[5] = T;
-      head[6] = per;
-      head[7] = own0;
-      p.head[16] = own_listed;
+      rec[2] = make_int4(to, 0, -1, 0);
     }
   }
 }

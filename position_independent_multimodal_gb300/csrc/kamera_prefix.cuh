@@ -9,12 +9,12 @@
 // tokens (at multiples of the class's tile) of one block of at most `rb` rows. A class's units
 // are numbered prefix blocks first (group, KV head and column half, row block, tile), then own
 // blocks (request, ...). Workers take consecutive units, as many as one another: every one has the
-// same number of tiles whatever the lengths, and cuts at most its first and last block. Where a
-// class's blocks all have as many tiles and there are workers enough, each block is shared out
-// among its own workers instead, so that no worker has parts of two blocks and those of the blocks
-// of one KV head read the same tokens at the same time. A block's first segment writes its rows'
-// partial output to the rows' home place, with the number of workers that follow on the block;
-// those write to their carry places. The merge kernel joins a row's parts by their log-sum-exp.
+// same number of tiles whatever the lengths, and cuts at most its first and last block. Where there
+// are wide blocks of prefixes alone and workers enough, each block is shared out among workers of
+// its own instead, so that no worker has parts of two blocks and those of the blocks of one KV head
+// read the same tokens at the same time. A block's first segment writes its rows' partial output to
+// the rows' home place, with the number of workers that follow on the block; those write to their
+// carry places. The merge kernel joins a row's parts by their log-sum-exp.
 #pragma once
 
 #include "kamera_dev.cuh"
@@ -23,16 +23,17 @@ namespace kamera {
 
 // What the plan kernel leaves for the others, in the workspace.
 struct PrefixPlan {
-  // per class c at head[8 c + .]: 0 units U, 1 groups listed, 4 workers n with units, 7 units of
-  // prefixes. k workers share a span of T units: 2 T / k, 3 T % k, 5 T, 6 k. head[16]: requests
-  // listed
+  // per class c at head[8 c + .]: 0 units U, 1 groups listed, 2 U / n and 3 U % n for the n workers
+  // with units, 4 n, 7 units of prefixes. head[16]: requests listed
   long long *head;
   struct Lists {          // blocks of a class
     long long *g_u0;      // [R] first unit of the i-th listed group
     int *g_first, *g_size, *g_prefix, *g_lead;  // first request, requests, prefix, leader
     int4 *start;          // [n][3] the wide class: each worker's first block: list index (own:
                           //     + 2^30), row block, KV head x half, tile; the listed entry's first
-                          //     request, requests, leader, first token; end of its tokens
+                          //     request, requests, leader, first token; end of its tokens, and if
+                          //     the block has workers of its own this one's tiles and how many
+                          //     workers follow, else -, -1
     float *carry_lse;     // [n][rb]
     float *carry_o;       // [n][rb][dv / vh]
   } cls[2];
@@ -113,7 +114,7 @@ __host__ __device__ inline int class_of(const PrefixShape &sh, int rows) {
   return rows > sh.wide_rows ? 0 : 1;
 }
 
-// First unit of a span's worker w.
+// First unit of worker w.
 __device__ __forceinline__ long long first_unit(long long quot, long long rem, long long w) {
   return w * quot + (w < rem ? w : rem);
 }
@@ -121,7 +122,7 @@ __device__ __forceinline__ long long div_pos(long long a, long long b) {  // a >
   if (((a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
   return a / b;
 }
-// A span's workers from w on that take `units` units, the last of them perhaps in part.
+// Workers from w on that take `units` units, the last of them perhaps in part.
 __device__ __forceinline__ int workers_for(long long quot, long long rem, long long w,
                                            long long units) {
   const long long n = rem > w ? rem - w : 0, edge = n * (quot + 1);  // those with one unit more
@@ -149,8 +150,9 @@ struct SegmentWalk {
   int first, size, lead, from, to;  // the listed group or request
   int tiles, nrb;            // tiles and row blocks of each of its blocks
   int rbk, kh, t;            // the next block (row block, KV head x half) and tile
-  int worker, groups;        // its place in its span; groups of the class's list
-  long long quot, rem;       // T / k and T % k
+  int worker, groups;        // groups: of the class's list
+  int follow;                // the block has workers of its own: those after this one; else -1
+  long long quot, rem;       // U / n and U % n
 
   __device__ __forceinline__ void entry(const PrefixArgs &a, const PrefixPlan &p) {
     if (own) {
@@ -175,25 +177,24 @@ struct SegmentWalk {
   // has units. Thin: a search by the warp; the plan would take 0.7 us for each 256 workers.
   __device__ __forceinline__ void start(const PrefixArgs &a, const PrefixPlan &p, int worker_) {
     const long long *head = p.head + 8 * C;
-    int4 at, e;
-    int last;
+    int4 at, e, last;
     if (C == 0) {
       const int4 *rec = p.cls[C].start + 3 * worker_;
       at = rec[0];
       e = rec[1];
-      last = rec[2].x;
+      last = rec[2];
     }
-    const long long n = head[4], T = head[5], k = head[6], own0 = head[7];
+    const long long n = head[4], own0 = head[7];
     const int requests = (int)p.head[16];
+    worker = worker_;
     groups = (int)head[1];
     quot = head[2];
     rem = head[3];
     u = end = 0;
-    if (worker_ >= n) return;
-    const int span = (int)((unsigned)worker_ / (unsigned)k);
-    worker = worker_ - span * (int)k;
-    u = span * T + first_unit(quot, rem, worker);
-    end = span * T + first_unit(quot, rem, worker + 1);
+    follow = -1;
+    if (worker >= n) return;
+    u = first_unit(quot, rem, worker);
+    end = first_unit(quot, rem, worker + 1);
     if (C == 1) {
       own = u >= own0;
       const long long *u0 = own ? p.r_u0 : p.cls[C].g_u0;
@@ -221,7 +222,12 @@ struct SegmentWalk {
     size = e.y;
     lead = e.z;
     from = e.w;
-    to = last;
+    to = last.x;
+    if (last.z >= 0) {
+      u = 0;
+      end = last.y;
+      follow = last.z;
+    }
     count(a);
     rbk = at.y;
     kh = at.z;
@@ -252,7 +258,9 @@ struct SegmentWalk {
     s->tok0 = t == 0 ? from : (t0 + t) << k.tile_sh;
     s->tok1 = t + nt == tiles ? to : (t0 + t + nt) << k.tile_sh;
     s->carry = t > 0;
-    s->more = t == 0 && nt < tiles ? workers_for(quot, rem, worker + 1, tiles - nt) : 0;
+    s->more = 0;
+    if (t == 0 && nt < tiles)
+      s->more = follow >= 0 ? follow : workers_for(quot, rem, worker + 1, tiles - nt);
     u += nt;
     t = 0;
     if (++rbk == nrb) {

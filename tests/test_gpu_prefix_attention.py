@@ -427,13 +427,15 @@ def test_refusals():
     assert torch.all(b.out == -7) and int(b.st.item()) == 0
 
 
-@pytest.mark.parametrize("groups,prefix,size", [(1, 3000, 41), (1, 640, 130), (3, 2000, 9),
-                                                (40, 300, 6), (2, 129, 64)])
+@pytest.mark.parametrize("groups,prefix,size,step", [
+    (1, 3000, 41, 0), (1, 640, 130, 0), (3, 2000, 9, 0), (40, 300, 6, 0), (2, 129, 64, 0),
+    (3, 1500, 12, 700), (9, 128, 9, 130), (2, 100, 40, 5000), (20, 400, 7, 37)])
 @pytest.mark.parametrize("name", ["gqa128-group7", "gqa64-group3", "mla-16-heads"])
-def test_prefixes_of_one_length(name, groups, prefix, size):
-    # wide blocks that all have as many tiles: each is shared out among workers of its own, where
-    # there are workers enough
-    b = Batch(name, [(prefix, [(3 * i + k) % 5 for i in range(size)]) for k in range(groups)], seed=15)
+def test_wide_blocks_with_workers_of_their_own(name, groups, prefix, size, step):
+    # wide blocks of prefixes alone, of one length and of several: each is shared out among workers
+    # of its own where there are workers enough for that
+    b = Batch(name, [(prefix + k * step, [(3 * i + k) % 5 for i in range(size)])
+                     for k in range(groups)], seed=15)
     assert b.run() == 0
     n = groups * size
     b.check(reqs=sorted({0, 1, size - 1, size // 2, n // 2, n - size, n - 1} & set(range(n))))
