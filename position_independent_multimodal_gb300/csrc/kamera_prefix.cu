@@ -78,7 +78,7 @@ __device__ __forceinline__ PrefixPlan::Lists lists_of(const PrefixPlan &p, int c
 }
 
 // One CTA: checks the arguments, lists the groups and requests that have units, and finds each
-// wide worker's first block. Bound: the latency of its few dependent steps (8 to 11 us for 4 to 128
+// wide worker's first block. Bound: the latency of its few dependent steps (6 to 8 us for 4 to 128
 // requests; 512 or 1024 threads are slower, by their barriers).
 __global__ void __launch_bounds__(kPlanThr)
     prefix_plan_kernel(const __grid_constant__ PrefixArgs a) {

@@ -23,15 +23,15 @@
 //        tile before: the chain S (512 cycles), softmax, P V (512) of a query tile is what bounds
 //        it. The softmax therefore takes its weights against the maximum so far, in one pass over
 //        S, and finds the tile's maximum on the way; only when that raises m are they taken again.
-//        3200 cycles a pair of tiles, of which the tensor core works 2050 (2 x 4 x 256): 104 us
-//        for 896 rows on 4 KV heads over 65500 tokens, 1.16 PFLOP/s, 60 % of a large library
+//        3200 cycles a pair of tiles, of which the tensor core works 2050 (2 x 4 x 256): 101 us
+//        for 896 rows on 4 KV heads over 65500 tokens, 1.19 PFLOP/s, 61 % of a large library
 //        product. Tried and slower: S of 64 tokens in two buffers (an MMA of N = 64 takes as long
 //        as one of N = 128), one thread to a row, two loading warps (a thread issues a 2 KB copy
 //        in about 107 cycles: 700 of 3500 cycles waiting for K and V).
 //   MLA: one tile of 128 rows and half of V's columns a CTA (O takes 256 TMEM columns; all 512
 //        would leave none for S), S of the next tile issued before P V of this one. 144 KB of Q
 //        leave a ring of 80 KB, whose latency bounds it (9000 cycles a tile, 4400 of them MMAs):
-//        49 us for 40 x 16 rows over two prefixes of 9003 tokens.
+//        41 us for 40 x 16 rows over two prefixes of 9003 tokens.
 // Layout: every operand tile is 128 rows of 128 bytes (64 elements), swizzled in 128-byte rows;
 // V is read MN-major, so its rows land unchanged too.
 #include <cuda.h>
