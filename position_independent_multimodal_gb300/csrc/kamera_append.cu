@@ -17,8 +17,8 @@
 // phases and slots are known. Few tokens (latency: 8 us at 8 tokens), or long rows.
 // append_stream_kernel: a warp to a token, in CTAs that stay, each lane's next chunks arriving by
 // cp.async while it works, two heads at a time (one at a time: 4 us more). 16381 tokens of 28/4
-// heads of 128: 62 us, 302 MB moved, 4.9 TB/s (append_kernel 82 us); few warps fit, and the chain of
-// a head's norm and rotation takes its time in each.
+// heads of 128: 62 us, 302 MB moved, 4.9 TB/s (append_kernel 82 us); few warps fit, and the chain
+// of a head's norm and rotation takes its time in each.
 // Bound: HBM (every byte is read and written once) at many tokens, latency at few.
 #include <mutex>
 

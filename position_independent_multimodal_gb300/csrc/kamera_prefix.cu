@@ -26,8 +26,8 @@ namespace {
 
 constexpr int kPlanThr = 256;
 // Tiles. The wide kernel with workers of each block's own | with the units in equal parts, in us:
-// 128 requests of 28/4 heads of 128 over 65500 tokens 101 | 117, 40 requests of MLA over two prefixes
-// of 9003 41 | 49, 48 of 28/4 heads over three of 6001 18 | 21.
+// 128 requests of 28/4 heads of 128 over 65500 tokens 101 | 117, 40 requests of MLA over two
+// prefixes of 9003 41 | 49, 48 of 28/4 heads over three of 6001 18 | 21.
 constexpr int kOwnExtra = 6;
 constexpr int kPlanNear = 1024;  // groups and listed entries kept in shared memory
 

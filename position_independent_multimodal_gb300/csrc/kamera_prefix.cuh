@@ -173,8 +173,8 @@ struct SegmentWalk {
     tiles = tiles_of(from, to, a.shape.cls[C].tile_sh);
     nrb = ceil_div(size * a.hpk, a.shape.cls[C].rb);
   }
-  // By whole warps. Wide: one round of loads; the place is there for every worker, whether or not it
-  // has units. Thin: a search by the warp; the plan would take 0.7 us for each 256 workers.
+  // By whole warps. Wide: one round of loads; the place is there for every worker, whether or not
+  // it has units. Thin: a search by the warp; the plan would take 0.7 us for each 256 workers.
   __device__ __forceinline__ void start(const PrefixArgs &a, const PrefixPlan &p, int worker_) {
     const long long *head = p.head + 8 * C;
     int4 at, e, last;
