@@ -283,3 +283,60 @@ def test_a_captured_decode_step_gives_the_same_bits():
     assert torch.equal(a.pt, b.pt) and torch.equal(a.refs, b.refs)
     assert torch.equal(a.k.view(torch.int16), b.k.view(torch.int16))
     assert int(a.st.item()) == int(b.st.item()) == 0
+
+
+@pytest.mark.parametrize("name", ["gqa", "mla"])
+def test_offsets_past_32_bits(name):
+    # a pool of more than 2^32 bytes and 2^31 elements a channel, its last pages in use
+    s = Server(name, seed=8)
+    lay, ps, hq = s.lay, s.ps, s.hq
+    pages = 2 ** 31 // (lay.num_layers * lay.row_k * ps) + 4000
+    shape = (lay.num_layers, pages * ps, lay.row_k)
+    s.k = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+    s.v = torch.empty(shape, dtype=torch.bfloat16, device="cuda") if s.gqa else None
+    assert s.k.numel() > 2 ** 31
+    P, n = 150, -(-150 // ps)
+    s.pt[0, :n] = torch.arange(pages - n, pages, dtype=torch.int32).flip(0).cuda()
+    s.pool = km.Pool(s.k, s.v, s.pt)
+    s.refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    s.refs[pages - n:] = 1
+    s.page_ws = torch.empty(km.kamera_page_workspace(s.h, pages * ps, ROWS), dtype=torch.uint8,
+                            device="cuda")
+    layer, tok = 1, np.arange(P)
+    i32 = lambda x: torch.as_tensor(np.asarray(x), dtype=torch.int32).cuda()  # noqa: E731
+
+    def enter(r, t, q):
+        x, k, v = s.inputs(len(t))
+        out = torch.zeros_like(x) if q else None
+        s.append(layer, x if q else None, k, v, torch.as_tensor(s.positions(t)).cuda(),
+                 i32(np.full(len(t), r)), i32(t), out)
+        return out, s.keep(layer, x if q else None, k, v, np.full(len(t), r), t, out)
+
+    _, (rk, rv) = enter(0, tok, False)
+
+    def attend(q, rows_k, rows_v):
+        o = torch.empty(1, hq, s.dv, dtype=torch.bfloat16, device="cuda")
+        lse = torch.empty(1, hq, device="cuda")
+        s.attend(layer, q, 1, i32([0, 1]), i32([P]), i32([len(rows_k)]), o, lse)
+        s.rows[0] = tuple(None if x is None else np.stack([np.zeros_like(x), x])
+                          for x in (rows_k, rows_v))
+        s.check_attention(layer, q, 1, o, lse)
+
+    q = s.inputs(1)[0].contiguous()
+    attend(q, rk, rv)
+    # a copy within the last pages, then the whole request drawn to the front of the pool
+    last = [x for x in (s.k, s.v) if x is not None]
+    km.kamera_copy_pages(s.h, s.pool, i32([pages - 2]), i32([pages - n - 5]), s.st)
+    for x in last:
+        a = x.view(lay.num_layers, pages, ps, -1)
+        assert torch.equal(a[:, pages - 2].view(torch.int16), a[:, pages - n - 5].view(torch.int16))
+    km.kamera_compact(s.h, s.pool, s.refs, s.live, s.page_ws, s.st)
+    assert int(s.live.item()) == n and int(s.pt[0, :n].max()) == n - 1
+    assert int(s.refs.sum()) == n and torch.all(s.refs[:n] == 1)
+    attend(q, rk, rv)
+    # and a branch whose new page is among the last: every page between is taken
+    s.refs[n:pages - 1] = 1
+    s.fork(0, [1], P)
+    assert int(s.pt[1, n - 1]) == pages - 1 and int(s.st.item()) == 0
+    assert torch.equal(s.k[layer][s.slots(np.full(P, 1), tok)].view(torch.int16),
+                       s.k[layer][s.slots(np.full(P, 0), tok)].view(torch.int16))
