@@ -241,6 +241,47 @@ __device__ __forceinline__ void finish_two(const uint4 (&x)[4], const Turn &turn
   }
 }
 
+// Whether the queries' latent parts are to be copied; whether by every second CTA of append_kernel,
+// beside the others' arithmetic. With the latter MLA with 16 heads takes 11 us instead of 13 at 150
+// tokens, 13 instead of 15 at 600, 47 instead of 48 at 5003 and 113 instead of 109 at 12000.
+__host__ __device__ inline bool copies_latents(const AppendArgs &a) {
+  return a.lay.kind == KAMERA_MLA && a.hq > 0 && a.q_out != a.q;
+}
+__host__ __device__ inline bool copies_beside(const AppendArgs &a) {
+  return copies_latents(a) && a.T <= 48 * kSms;
+}
+
+// The queries' latent parts of tokens t0 .. t0 + nt - 1, byte for byte: rows of nc chunks dealt to
+// the CTA's warps.
+__device__ __forceinline__ void copy_latents(const AppendArgs &a, long long t0, int nt,
+                                             const int *live) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rows = nt * a.hq, nc = a.lay.latent >> 3;
+  for (int i0 = warp; i0 < rows; i0 += kThr / 32 * kBatch) {
+    for (int c = lane; c < nc; c += 64) {
+      uint4 v[kBatch][2];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = i0 + j * (kThr / 32), t = i / a.hq;
+        const __nv_bfloat16 *src = a.q + (t0 + t) * a.q_stride + (i - t * a.hq) * a.lay.row_k;
+        if (i < rows && live[t]) {
+          v[j][0] = ld16(src + 8 * c);
+          if (c + 32 < nc) v[j][1] = ld16(src + 8 * (c + 32));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = i0 + j * (kThr / 32), t = i / a.hq;
+        __nv_bfloat16 *dst = a.q_out + (t0 + t) * a.q_out_stride + (i - t * a.hq) * a.lay.row_k;
+        if (i < rows && live[t]) {
+          st16(dst + 8 * c, v[j][0]);
+          if (c + 32 < nc) st16(dst + 8 * (c + 32), v[j][1]);
+        }
+      }
+    }
+  }
+}
+
 template <int kTok, bool kNeox>
 __global__ void __launch_bounds__(kThr, 2) append_kernel(const __grid_constant__ AppendArgs a) {
   __shared__ float2 cs[kTok * kMaxPairs];
@@ -250,10 +291,25 @@ __global__ void __launch_bounds__(kThr, 2) append_kernel(const __grid_constant__
   ptx::wait_for_previous();
   const DevLayout &lay = a.lay;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const long long t0 = (long long)blockIdx.x * kTok;
+  const bool copies = copies_beside(a);
+  const long long t0 = (long long)(copies ? blockIdx.x >> 1 : blockIdx.x) * kTok;
   const int nt = (int)min((long long)kTok, a.T - t0);
   const int np = lay.npairs;
   const bool gqa = lay.kind == KAMERA_GQA;
+
+  auto in_table = [&](int req, int at) {
+    return req < a.pool.num_reqs && at >= 0 &&
+           at < (long long)a.pool.pt_stride * lay.page_size;
+  };
+  if (copies && (blockIdx.x & 1)) {
+    if (tid < nt) {
+      const int req = __ldg(a.req + t0 + tid);
+      live[tid] = req >= 0 && in_table(req, __ldg(a.tok + t0 + tid));
+    }
+    __syncthreads();
+    copy_latents(a, t0, nt, live);
+    return;
+  }
 
   // this group's token, its query heads and key bands h_first, h_first + groups, ...
   const int band = lay.rope_d, units = band >> 4;
@@ -291,8 +347,7 @@ __global__ void __launch_bounds__(kThr, 2) append_kernel(const __grid_constant__
   if (tk < nt && ve < nv) v0 = ld16(a.v + (t0 + tk) * a.v_stride + 8 * ve);
   if (tid < nt) {
     const bool padding = req < 0;
-    const bool bad = !padding && (req >= a.pool.num_reqs || at < 0 ||
-                                  at >= (long long)a.pool.pt_stride * lay.page_size);
+    const bool bad = !padding && !in_table(req, at);
     if (bad) atomicOr(a.status, KAMERA_DEVICE_BAD_ITEM);
     live[tid] = !padding && !bad;
     slots[tid] = padding || bad ? -1 : slot_of(a.pool, lay.page_size, req, at, a.status);
@@ -396,32 +451,7 @@ __global__ void __launch_bounds__(kThr, 2) append_kernel(const __grid_constant__
       st16(dst + 8 * c, v);
     }
   }
-  // and the queries' latent parts, byte for byte: rows of nc chunks dealt to the warps
-  if (a.q_out == a.q) return;
-  const int rows = nt * a.hq;
-  for (int i0 = warp; i0 < rows; i0 += kThr / 32 * kBatch) {
-    for (int c = lane; c < nc; c += 64) {
-      uint4 v[kBatch][2];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int i = i0 + j * (kThr / 32), t = i / a.hq;
-        const __nv_bfloat16 *src = a.q + (t0 + t) * a.q_stride + (i - t * a.hq) * lay.row_k;
-        if (i < rows && live[t]) {
-          v[j][0] = ld16(src + 8 * c);
-          if (c + 32 < nc) v[j][1] = ld16(src + 8 * (c + 32));
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int i = i0 + j * (kThr / 32), t = i / a.hq;
-        __nv_bfloat16 *dst = a.q_out + (t0 + t) * a.q_out_stride + (i - t * a.hq) * lay.row_k;
-        if (i < rows && live[t]) {
-          st16(dst + 8 * c, v[j][0]);
-          if (c + 32 < nc) st16(dst + 8 * (c + 32), v[j][1]);
-        }
-      }
-    }
-  }
+  if (copies_latents(a) && !copies) copy_latents(a, t0, nt, live);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -672,7 +702,7 @@ namespace {
 
 template <int kTok>
 cudaError_t launch(const AppendArgs &a, cudaStream_t s) {
-  const dim3 grid((unsigned)((a.T + kTok - 1) / kTok));
+  const dim3 grid((unsigned)((a.T + kTok - 1) / kTok) * (copies_beside(a) ? 2 : 1));
   return launch_early(a.lay.style == KAMERA_ROPE_NEOX_HALF ? append_kernel<kTok, true>
                                                            : append_kernel<kTok, false>,
                       grid, kThr, 0, s, a);
@@ -686,10 +716,11 @@ cudaError_t launch_append(const AppendArgs &a, cudaStream_t s) {
   //   28/4 heads of 128 (11 warps fit)    11   11    13        17   11    13          89    68
   //   16 + 16 heads of 128 (5)            13   17    17        19   17    17         168   224
   //   6/2 heads of 64 (12)                11   11    11        15   11    11          66    33
-  //   MLA, 16 heads copied (5)            13   15    14        20   15    15         142   154
+  //   MLA, 16 heads copied (5)            17   11    14         -   13    15         142   154
   //   MLA, queries in place (12)          11   12    11        17   11    11          79    40
-  // A CTA's few warps must hold the rows in flight that HBM wants, and eight do the arithmetic.
-  if (a.T <= 2 * kSms) return launch<1>(a, s);
+  // (Copies beside them double the CTAs.) A CTA's few warps must hold the rows in flight that HBM
+  // wants, and eight do the arithmetic.
+  if (a.T * (copies_beside(a) ? 2 : 1) <= 2 * kSms) return launch<1>(a, s);
   const StreamPlan sp = stream_plan(a.lay, a.hq, a.q_out != a.q);
   if (sp.warps < kStreamLeast) return launch<4>(a, s);
   static int configured[64] = {0};
