@@ -714,7 +714,7 @@ cudaError_t launch_append(const AppendArgs &a, cudaStream_t s) {
   // One token a CTA, four, or a warp a token. Measured with a call's overhead, L2 flushed, in us:
   //                             T = 304: one four warps  608: one four warps  16381: four warps
   //   28/4 heads of 128 (11 warps fit)    11   11    13        17   11    13          89    68
-  //   16 + 16 heads of 128 (5)            13   17    17        19   17    17         168   224
+  //   32/32 heads of 128 (4)              13   17    17        19   17    17         168   224
   //   6/2 heads of 64 (12)                11   11    11        15   11    11          66    33
   //   MLA, 16 heads copied (5)            17   11    14         -   13    15         142   154
   //   MLA, queries in place (12)          11   12    11        17   11    11          79    40
