@@ -198,6 +198,15 @@ class Handle:
         h = ctypes.c_void_p()
         _check(lib().kamera_create(ctypes.byref(self._c), ctypes.byref(h)), "kamera_create")
         self.ptr = h
+        # of the layout, as the calls of every step want them
+        c = self._c
+        self._gqa = c.kind == KAMERA_GQA
+        self._heads, self._dk = (c.num_kv_heads, c.head_dim) if self._gqa else \
+            (1, c.latent_dim + c.rope_dim)
+        self._layers, self._row = c.num_layers, self._heads * self._dk
+        self._dv = c.head_dim if self._gqa else c.latent_dim
+        self._positions = 3 if any(c.mrope_section) else 1
+        self._page = c.page_size
 
     def close(self):
         if self.ptr:
@@ -373,6 +382,9 @@ def _reject(what: str, dtype, contiguous: bool = True) -> None:
                      "current CUDA device")
 
 
+_BF16, _I32, _I64 = torch.bfloat16, torch.int32, torch.int64
+
+
 def _need(what: str, t: torch.Tensor, dtype, dev: int) -> int:
     """The address of a contiguous tensor of ``dtype`` on CUDA device ``dev``."""
     if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
@@ -387,19 +399,17 @@ def _pool_c(handle: Handle, pool: Pool) -> tuple[kamera_pool, int]:
     dev = k.get_device()
     if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError("the pool must be on the current CUDA device")
-    c = handle._c
-    gqa = c.kind == KAMERA_GQA
-    want = (c.num_layers, pool.num_slots,
-            c.num_kv_heads * c.head_dim if gqa else c.latent_dim + c.rope_dim)
+    gqa = handle._gqa
+    want = (handle._layers, pool.num_slots, handle._row)
     if k.shape != want or (v is None) == gqa or (gqa and v.shape != want):
         raise ValueError(f"the pool's tensors must be {want}, K and V for GQA, K alone for MLA")
-    if pt.dtype is not torch.int32 or pt.get_device() != dev:
-        _reject("pool.page_table", torch.int32, contiguous=False)
+    if pt.dtype is not _I32 or pt.get_device() != dev:
+        _reject("pool.page_table", _I32, contiguous=False)
     st = pt.stride()
     if len(st) != 2 or st[1] != 1:
         raise ValueError("pool.page_table must be [num_reqs][pt_stride]")
-    return kamera_pool(_need("pool.k", k, torch.bfloat16, dev),
-                       _need("pool.v", v, torch.bfloat16, dev) if gqa else None, want[1],
+    return kamera_pool(_need("pool.k", k, _BF16, dev),
+                       _need("pool.v", v, _BF16, dev) if gqa else None, want[1],
                        pt.data_ptr(), pt.shape[0], st[0]), dev
 
 
@@ -421,8 +431,8 @@ def _bytes(t: Optional[torch.Tensor], dev: int) -> tuple[Optional[int], int]:
 
 def _heads(what: str, t: torch.Tensor, dev: int, tokens: int, heads: int, width: int) -> int:
     """The token stride of bf16 [tokens][heads][width] whose heads lie side by side."""
-    if t.dtype is not torch.bfloat16 or t.get_device() != dev:
-        _reject(what, torch.bfloat16, contiguous=False)
+    if t.dtype is not _BF16 or t.get_device() != dev:
+        _reject(what, _BF16, contiguous=False)
     st = t.stride()
     if t.shape != (tokens, heads, width) or st[2] != 1 or (heads > 1 and st[1] != width):
         raise ValueError(f"{what} must be [{tokens}][{heads}][{width}] with contiguous heads")
@@ -439,9 +449,7 @@ def kamera_append(handle: Handle, pool: Pool, layer: int, q: Optional[torch.Tens
     None) into the pool's layer, for tokens ``tok`` of page-table rows ``req`` (int32 [T]) at
     ``positions`` (int64 [T], or [T][3] under M-RoPE). Token strides are free."""
     p, dev = _pool_c(handle, pool)
-    c = handle._c
-    gqa = c.kind == KAMERA_GQA
-    dk, hk = (c.head_dim, c.num_kv_heads) if gqa else (c.latent_dim + c.rope_dim, 1)
+    gqa, dk, hk = handle._gqa, handle._dk, handle._heads
     T, hq = k.shape[0], 0
     k_stride = _heads("k", k, dev, T, hk, dk)
     if (v is None) == gqa:
@@ -456,23 +464,20 @@ def kamera_append(handle: Handle, pool: Pool, layer: int, q: Optional[torch.Tens
         out_ptr, out_stride = q_out.data_ptr(), _heads("q_out", q_out, dev, T, hq, dk)
     qw = kw = None
     if q_weight is not None:
-        qw = _need("q_weight", q_weight, torch.bfloat16, dev)
+        qw = _need("q_weight", q_weight, _BF16, dev)
     if k_weight is not None:
-        kw = _need("k_weight", k_weight, torch.bfloat16, dev)
-    if (qw and q_weight.numel() != dk) or \
-            (kw and k_weight.numel() != (dk if gqa else c.latent_dim)):
+        kw = _need("k_weight", k_weight, _BF16, dev)
+    if (qw and q_weight.numel() != dk) or (kw and k_weight.numel() != handle._dv):
         raise ValueError("a weight must have one element for each column that is normed")
-    sec = c.mrope_section
-    if positions.numel() != T * (3 if sec[0] or sec[1] or sec[2] else 1) or \
-            req.numel() != T or tok.numel() != T:
+    if positions.numel() != T * handle._positions or req.numel() != T or tok.numel() != T:
         raise ValueError(f"positions, req and tok must be of {T} tokens")
     t = kamera_new_tokens(q_ptr, k.data_ptr(), v_ptr, qw, kw,
-                          _need("positions", positions, torch.int64, dev),
-                          _need("req", req, torch.int32, dev),
-                          _need("tok", tok, torch.int32, dev), out_ptr, q_stride, k_stride,
+                          _need("positions", positions, _I64, dev),
+                          _need("req", req, _I32, dev),
+                          _need("tok", tok, _I32, dev), out_ptr, q_stride, k_stride,
                           v_stride, out_stride, T, hq, eps, 0)
     _check(lib().kamera_append(handle.ptr, ctypes.byref(p), layer, ctypes.byref(t),
-                               _need("status", status, torch.int32, dev),
+                               _need("status", status, _I32, dev),
                                _stream_on(stream, dev)), "kamera_append")
 
 
@@ -483,9 +488,9 @@ def kamera_page_workspace(handle: Handle, num_slots: int, num_items: int) -> int
 
 
 def _refs(pool: Pool, handle: Handle, refs: torch.Tensor, dev: int) -> int:
-    if refs.numel() * handle._c.page_size != pool.num_slots:
+    if refs.numel() * handle._page != pool.num_slots:
         raise ValueError("refs must have one count for each page of the pool")
-    return _need("refs", refs, torch.int32, dev)
+    return _need("refs", refs, _I32, dev)
 
 
 def _page_call(name: str, handle: Handle, pool: Pool, items: torch.Tensor, refs: torch.Tensor,
@@ -494,11 +499,11 @@ def _page_call(name: str, handle: Handle, pool: Pool, items: torch.Tensor, refs:
     shape = items.shape
     if len(shape) != 2 or shape[1] != 3:
         raise ValueError("items must be [n][3]")
-    args = [handle.ptr, ctypes.byref(p), _need("items", items, torch.int32, dev), shape[0],
+    args = [handle.ptr, ctypes.byref(p), _need("items", items, _I32, dev), shape[0],
             _refs(pool, handle, refs, dev)]
     if workspace is not False:
         args += _bytes(workspace, dev)
-    _check(getattr(lib(), name)(*args, _need("status", status, torch.int32, dev),
+    _check(getattr(lib(), name)(*args, _need("status", status, _I32, dev),
                                 _stream_on(stream, dev)), name)
 
 
@@ -526,9 +531,9 @@ def kamera_compact(handle: Handle, pool: Pool, refs: torch.Tensor, num_live: tor
     (int32 [1])."""
     p, dev = _pool_c(handle, pool)
     _check(lib().kamera_compact(handle.ptr, ctypes.byref(p), _refs(pool, handle, refs, dev),
-                                _need("num_live", num_live, torch.int32, dev),
+                                _need("num_live", num_live, _I32, dev),
                                 *_bytes(workspace, dev),
-                                _need("status", status, torch.int32, dev),
+                                _need("status", status, _I32, dev),
                                 _stream_on(stream, dev)), "kamera_compact")
 
 
@@ -540,9 +545,9 @@ def kamera_copy_pages(handle: Handle, pool: Pool, src: torch.Tensor, dst: torch.
     if n != dst.numel():
         raise ValueError("src and dst must have as many pages")
     _check(lib().kamera_copy_pages(handle.ptr, ctypes.byref(p),
-                                   _need("src", src, torch.int32, dev),
-                                   _need("dst", dst, torch.int32, dev), n,
-                                   _need("status", status, torch.int32, dev),
+                                   _need("src", src, _I32, dev),
+                                   _need("dst", dst, _I32, dev), n,
+                                   _need("status", status, _I32, dev),
                                    _stream_on(stream, dev)), "kamera_copy_pages")
 
 
@@ -561,9 +566,7 @@ def kamera_prefix_attention(handle: Handle, pool: Pool, layer: int, q: torch.Ten
     ``group_start[g]`` .. ``group_start[g + 1] - 1`` sharing their first ``prefix_len[g]``
     tokens, into ``out`` bf16 [R][H_q][Dv] and ``lse`` float32 [R][H_q]."""
     p, dev = _pool_c(handle, pool)
-    c = handle._c
-    dk, dv = (c.head_dim, c.head_dim) if c.kind == KAMERA_GQA else \
-        (c.latent_dim + c.rope_dim, c.latent_dim)
+    dk, dv = handle._dk, handle._dv
     R, hq, _ = shape = q.shape
     G = prefix_len.numel()
     if shape != (R, hq, dk) or out.shape != (R, hq, dv) or lse.shape != (R, hq) or \
@@ -571,12 +574,12 @@ def kamera_prefix_attention(handle: Handle, pool: Pool, layer: int, q: torch.Ten
         raise ValueError(f"q [R][H_q][{dk}], out [R][H_q][{dv}], lse [R][H_q], ctx_len [R], "
                          "group_start [G + 1] and prefix_len [G] are wanted")
     _check(lib().kamera_prefix_attention(
-        handle.ptr, ctypes.byref(p), layer, _need("q", q, torch.bfloat16, dev), R, hq,
-        _need("group_start", group_start, torch.int32, dev),
-        _need("prefix_len", prefix_len, torch.int32, dev), G,
-        _need("ctx_len", ctx_len, torch.int32, dev), scale,
-        _need("out", out, torch.bfloat16, dev), _need("lse", lse, torch.float32, dev),
-        *_bytes(workspace, dev), _need("status", status, torch.int32, dev),
+        handle.ptr, ctypes.byref(p), layer, _need("q", q, _BF16, dev), R, hq,
+        _need("group_start", group_start, _I32, dev),
+        _need("prefix_len", prefix_len, _I32, dev), G,
+        _need("ctx_len", ctx_len, _I32, dev), scale,
+        _need("out", out, _BF16, dev), _need("lse", lse, torch.float32, dev),
+        *_bytes(workspace, dev), _need("status", status, _I32, dev),
         _stream_on(stream, dev)), "kamera_prefix_attention")
 
 
