@@ -321,6 +321,13 @@ __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
                 for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
                 ptx::tmem_st16(o_t + 16 * j, y);
               }
+              // The products of either half's tokens go into all of O's columns (GQA), and those
+              // of the first half start on that half's arrival alone. So neither thread arrives
+              // before both have scaled their columns.
+              ptx::tmem_st_wait();
+              ptx::tc_fence_before();
+              ptx::barrier_sync(pair, 64);
+              ptx::tc_fence_after();
             }
             base = m > neg_inf ? m * c : 0.f;
             ptx::tmem_ld32(st, x);
