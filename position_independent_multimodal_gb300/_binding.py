@@ -260,7 +260,8 @@ def kamera_set_batch_workspace(handle: Handle, workspace: Optional[torch.Tensor]
 
 
 class Pool:
-    """The paged pool: k, v tensors [L][num_slots][row] and the int32 page table."""
+    """The paged pool: k, v tensors [L][num_slots][row] and the int32 page table [num_reqs][pages].
+    kamera_append, the page calls and kamera_prefix_attention want a contiguous table."""
 
     def __init__(self, k: torch.Tensor, v: Optional[torch.Tensor], page_table: torch.Tensor,
                  num_slots: Optional[int] = None):
@@ -403,14 +404,19 @@ def _pool_c(handle: Handle, pool: Pool) -> tuple[kamera_pool, int]:
     want = (handle._layers, pool.num_slots, handle._row)
     if k.shape != want or (v is None) == gqa or (gqa and v.shape != want):
         raise ValueError(f"the pool's tensors must be {want}, K and V for GQA, K alone for MLA")
-    if pt.dtype is not _I32 or pt.get_device() != dev:
-        _reject("pool.page_table", _I32, contiguous=False)
-    st = pt.stride()
-    if len(st) != 2 or st[1] != 1:
-        raise ValueError("pool.page_table must be [num_reqs][pt_stride]")
     return kamera_pool(_need("pool.k", k, _BF16, dev),
                        _need("pool.v", v, _BF16, dev) if gqa else None, want[1],
-                       pt.data_ptr(), pt.shape[0], st[0]), dev
+                       *_table(pt, dev)), dev
+
+
+def _table(pt: torch.Tensor, dev: int) -> tuple[int, int, int]:
+    """The address, rows and columns of a page table. It has to be whole rows: the C calls know a
+    row by its stride alone, so beside a slice of columns they would read, and the page calls
+    write, what is not of the table."""
+    if pt.dim() != 2 or not pt.is_contiguous():
+        raise ValueError("pool.page_table must be a contiguous [num_reqs][pt_stride]: of a table "
+                         "that is a slice of columns, pass the whole rows")
+    return _need("pool.page_table", pt, _I32, dev), pt.shape[0], pt.shape[1]
 
 
 def _stream_on(stream, dev: int) -> int:
