@@ -55,7 +55,8 @@ typedef enum kamera_status {
 #define KAMERA_DEVICE_BAD_ITEM 0x2u /* kamera_batch_reuse: an item failed the checks that
                                        kamera_reuse makes on the host; none of it was written */
 #define KAMERA_DEVICE_TIMEOUT 0x4u  /* a tensor-core tile did not complete within 2 s; its
-                                       rows were not written (never expected)               */
+                                       rows were not written (never expected;
+                                       kamera_prefix_attention: no output of the call was)  */
 #define KAMERA_DEVICE_NO_PAGES 0x8u /* kamera_fork, kamera_extend: the free pages ran out before
                                        an item; nothing of it was done                       */
 

@@ -205,6 +205,8 @@ struct PrefixShape {
   int wide_rows;        // blocks of more rows are wide
 };
 
+constexpr unsigned long long kPrefixWaitNs = 2000000000ull;
+
 struct PrefixArgs {
   DevLayout lay;
   DevPool pool;
@@ -219,6 +221,8 @@ struct PrefixArgs {
   int page_shift;          // log2 of the page size, -1 when that is no power of two
   PrefixShape shape;
   float scale;
+  unsigned long long wait_ns;  // limit of a wait in the wide blocks' kernel
+  int *gave_up;            // in the workspace
   void *ws;
   __nv_bfloat16 *out;      // [n_reqs][hq][dv]
   float *lse;              // [n_reqs][hq]

@@ -93,7 +93,10 @@ __global__ void __launch_bounds__(kPlanThr)
   const bool near_g = G <= kPlanNear;
   const int *start = near_g ? near_start : a.group_start;
   int *lead = near_g ? near_lead : p.lead;
-  if (tid == 0) broken = worst = 0;
+  if (tid == 0) {
+    broken = worst = 0;
+    *p.gave_up = 0;
+  }
   __syncthreads();
   for (int g = tid; g <= G; g += kPlanThr) {
     const int s = a.group_start[g];
@@ -544,7 +547,7 @@ __global__ void __launch_bounds__(kThr, 3) prefix_merge_kernel(const __grid_cons
   const float neg_inf = -__int_as_float(0x7f800000);
   ptx::wait_for_previous();
   const bool have[2] = {p.req_pu0[r] >= 0, p.req_ou0[r] >= 0};
-  if (!p.req_state[r]) return;
+  if (!p.req_state[r] | *a.gave_up) return;  // loaded together
   const int size = p.req_size[r];
   // the row's blocks: prefix, own part. Part 0 of a block is the home place, the rest are carries
   const float *home_o[2], *home_z[2], *carry_o[2], *carry_z[2];
@@ -643,7 +646,15 @@ size_t prefix_workspace(const DevLayout &l, long long n_reqs, int hq, int dv) {
   return prefix_plan(prefix_shape(l, hq), nullptr, n_reqs, hq, dv).total;
 }
 
-cudaError_t launch_prefix_attention(const PrefixArgs &a, cudaStream_t s) {
+// The limit of the wide kernel's waits, in ns. A test sets it to 0, with which a call gives up
+// before it has begun, to see what a call that gave up leaves.
+extern "C" unsigned long long kamera_prefix_wait_ns;
+unsigned long long kamera_prefix_wait_ns = kPrefixWaitNs;
+
+cudaError_t launch_prefix_attention(const PrefixArgs &args, cudaStream_t s) {
+  PrefixArgs a = args;
+  a.wait_ns = kamera_prefix_wait_ns;
+  a.gave_up = prefix_plan(a.shape, a.ws, a.n_reqs, a.hq, a.dv).gave_up;
   static int configured[64] = {0};
   static std::mutex mu;
   int dev = 0;

@@ -26,6 +26,7 @@ struct PrefixPlan {
   // per class c at head[8 c + .]: 0 units U, 1 groups listed, 2 U / n and 3 U % n for the n workers
   // with units, 4 n, 7 units of prefixes. head[16]: requests listed
   long long *head;
+  int *gave_up;           // 0 by the plan, 1 by a wide CTA that gave up
   struct Lists {          // blocks of a class
     long long *g_u0;      // [R] first unit of the i-th listed group
     int *g_first, *g_size, *g_prefix, *g_lead;  // first request, requests, prefix, leader
@@ -71,6 +72,7 @@ __host__ __device__ inline PrefixPlan prefix_plan(const PrefixShape &sh, void *w
   auto i32 = [&](long long n) { return reinterpret_cast<int *>(take(4 * n)); };
   auto f32 = [&](long long n) { return reinterpret_cast<float *>(take(4 * n)); };
   p.head = reinterpret_cast<long long *>(take(256));
+  p.gave_up = reinterpret_cast<int *>(p.head + 17);
   for (int c = 0; c < 2; ++c) {
     const PrefixClass &k = sh.cls[c];
     p.cls[c].g_u0 = i64();

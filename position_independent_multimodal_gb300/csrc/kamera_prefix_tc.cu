@@ -48,7 +48,6 @@ constexpr int kTokSh = 7, kTok = 1 << kTokSh;  // tokens per tile
 constexpr int kRow = 128;              // query rows per MMA
 constexpr int kChunk = kTok * 128;     // bytes of a 128 x 64 bf16 operand tile
 constexpr int kMasks = 8;              // tiles whose token masks are kept
-constexpr unsigned long long kWaitNs = 2000000000ull;
 
 // DK, DV: 64-column chunks of K and of the CTA's V columns; QT: tiles of query rows; UC: chunks
 // per ring stage; NST: ring stages; NL: warps that load K and V.
@@ -133,15 +132,16 @@ __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
   volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem + S::misc);
   volatile uint32_t *gave_up = misc + 1;
   auto bar = [&](int i) { return sb + S::bar + 8 * i; };
-  // Waits for a phase, giving up after kWaitNs or when another thread has. A thread that gave up
+  // Waits for a phase, giving up after a.wait_ns or when another thread has. A thread that gave up
   // runs on to its end without waiting, arriving, copying or multiplying: it keeps step with the
-  // named barriers only, and no barrier gets an arrival that it does not expect.
+  // named barriers only, and no barrier gets an arrival that it does not expect. Nothing of the
+  // call's outputs is written then.
   bool dead = false;
   auto wait = [&](uint32_t b, uint32_t parity) {
     if (dead || ptx::mbar_try_wait(b, parity)) return;
     const uint64_t t0 = ptx::globaltimer();
     while (!ptx::mbar_try_wait(b, parity)) {
-      if (*gave_up || ptx::globaltimer() - t0 > kWaitNs) {
+      if (*gave_up || ptx::globaltimer() - t0 > a.wait_ns) {
         *gave_up = 1;
         dead = true;
         return;
@@ -152,10 +152,9 @@ __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
     if (!dead) ptx::mbar_arrive(b);
   };
 
-  if (sb & 1023u) {  // the swizzled layouts want 1024-byte groups; there is no static memory here
-    if (tid == 0) atomicOr(a.status, KAMERA_DEVICE_TIMEOUT);
-    return;
-  }
+  // The swizzled layouts want 1024-byte groups (there is no static memory here, so they get them);
+  // without them, or without time to wait, nothing is begun and the kernel ends as one that gave up.
+  const bool begins = (sb & 1023u) == 0 && a.wait_ns != 0;
   if (warp == S::kMma) {
     ptx::tmem_alloc(sb + S::misc, 512);
     ptx::tmem_relinquish();
@@ -178,7 +177,7 @@ __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
     for (int i = 0; i < kMasks; ++i) ptx::mbar_init(bar(S::mk_full + i), S::NL);
     ptx::mbar_init(bar(S::last), 1);
     ptx::fence_mbar_init();
-    *gave_up = 0;
+    *gave_up = !begins;
     ptx::prefetch_map(&maps.k);
     ptx::prefetch_map(&maps.v);
     ptx::prefetch_map(&maps.q_group);
@@ -195,7 +194,7 @@ __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
   walk.start(a, plan, blockIdx.x);
   // the segment that follows is looked up while this one's first copies are on their way
   Segment s, after;
-  bool more = walk.next(a, plan, &after);
+  bool more = begins && walk.next(a, plan, &after);
 
   if (warp < S::kSoft) {
     // ---- softmax: thread = half of a query row ----
@@ -682,14 +681,17 @@ __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
         kp = vp;  // the segment's end
       }
       ptx::mma_commit(bar(S::last));  // no MMA is in flight when the TMEM goes back
-      if (!ptx::mbar_wait(bar(S::last), 0, kWaitNs)) *gave_up = 1;
+      if (!ptx::mbar_wait(bar(S::last), 0, kPrefixWaitNs)) *gave_up = 1;
     }
     __syncwarp();
   }
   ptx::tc_fence_before();
   __syncthreads();
   if (*gave_up) {  // copies and MMAs in flight end long before this
-    if (tid == 0) atomicOr(a.status, KAMERA_DEVICE_TIMEOUT);
+    if (tid == 0) {
+      atomicOr(a.status, KAMERA_DEVICE_TIMEOUT);
+      *a.gave_up = 1;  // the merge writes nothing
+    }
     const uint64_t t0 = ptx::globaltimer();
     while (ptx::globaltimer() - t0 < 1000000) {
     }
