@@ -445,6 +445,15 @@ def _heads(what: str, t: torch.Tensor, dev: int, tokens: int, heads: int, width:
     return st[0] if tokens > 1 else max(st[0], heads * width)
 
 
+def _check_positions(handle: Handle, positions: torch.Tensor, tokens: int) -> None:
+    # by shape under M-RoPE: [3][T] has as many elements and would turn tokens by one another's
+    if handle._positions == 1:
+        if positions.numel() != tokens:
+            raise ValueError(f"positions must be of {tokens} tokens")
+    elif positions.shape != (tokens, 3):
+        raise ValueError(f"positions must be [{tokens}][3] for an M-RoPE layout")
+
+
 def kamera_append(handle: Handle, pool: Pool, layer: int, q: Optional[torch.Tensor],
                   k: torch.Tensor, v: Optional[torch.Tensor], q_weight: Optional[torch.Tensor],
                   k_weight: Optional[torch.Tensor], positions: torch.Tensor, req: torch.Tensor,
@@ -475,8 +484,9 @@ def kamera_append(handle: Handle, pool: Pool, layer: int, q: Optional[torch.Tens
         kw = _need("k_weight", k_weight, _BF16, dev)
     if (qw and q_weight.numel() != dk) or (kw and k_weight.numel() != handle._dv):
         raise ValueError("a weight must have one element for each column that is normed")
-    if positions.numel() != T * handle._positions or req.numel() != T or tok.numel() != T:
-        raise ValueError(f"positions, req and tok must be of {T} tokens")
+    if req.numel() != T or tok.numel() != T:
+        raise ValueError(f"req and tok must be of {T} tokens")
+    _check_positions(handle, positions, T)
     t = kamera_new_tokens(q_ptr, k.data_ptr(), v_ptr, qw, kw,
                           _need("positions", positions, _I64, dev),
                           _need("req", req, _I32, dev),

@@ -1,4 +1,6 @@
 """What the Python binding checks of the serving calls' arguments (no GPU needed)."""
+import types
+
 import pytest
 import torch
 
@@ -24,3 +26,23 @@ def test_other_page_tables_are_refused(cut):
     t = torch.arange(35, dtype=torch.int32).reshape(5, 7)
     with pytest.raises(ValueError):
         kb._table(cut(t), CPU)
+
+
+def _handle(mrope):
+    return types.SimpleNamespace(_positions=3 if mrope else 1)
+
+
+@pytest.mark.parametrize("shape", [(3, 7), (21,), (1, 7, 3), (7, 1, 3), (7, 2), (6, 3), (7,)])
+def test_mrope_positions_of_other_shapes_are_refused(shape):
+    with pytest.raises(ValueError):
+        kb._check_positions(_handle(True), torch.zeros(shape, dtype=torch.int64), 7)
+
+
+def test_positions_that_are_taken():
+    kb._check_positions(_handle(True), torch.zeros(7, 3, dtype=torch.int64), 7)
+    kb._check_positions(_handle(True), torch.zeros(0, 3, dtype=torch.int64), 0)
+    for shape in ((7,), (7, 1), (1, 7)):
+        kb._check_positions(_handle(False), torch.zeros(shape, dtype=torch.int64), 7)
+    for shape in ((6,), (7, 3), (21,)):
+        with pytest.raises(ValueError):
+            kb._check_positions(_handle(False), torch.zeros(shape, dtype=torch.int64), 7)
