@@ -442,7 +442,7 @@ def _heads(what: str, t: torch.Tensor, dev: int, tokens: int, heads: int, width:
     st = t.stride()
     if t.shape != (tokens, heads, width) or st[2] != 1 or (heads > 1 and st[1] != width):
         raise ValueError(f"{what} must be [{tokens}][{heads}][{width}] with contiguous heads")
-    return st[0] if tokens > 1 else max(st[0], heads * width)
+    return st[0] if tokens > 1 else heads * width  # of one token the stride says nothing
 
 
 def _check_positions(handle: Handle, positions: torch.Tensor, tokens: int) -> None:

@@ -46,3 +46,13 @@ def test_positions_that_are_taken():
     for shape in ((6,), (7, 3), (21,)):
         with pytest.raises(ValueError):
             kb._check_positions(_handle(False), torch.zeros(shape, dtype=torch.int64), 7)
+
+
+def test_token_strides():
+    x = torch.zeros(5, 12 * 16 + 4, dtype=torch.bfloat16)[:, :192].unflatten(1, (12, 16))
+    assert kb._heads("k", x[:, 4:8], CPU, 5, 4, 16) == 196
+    for n in (0, 1):  # what the stride is does not matter
+        assert kb._heads("k", x[:n, 4:8], CPU, n, 4, 16) == 64
+    for bad in (x[:, ::2], x[:, :6], x[..., ::2], x.float(), x[:4]):
+        with pytest.raises(ValueError):
+            kb._heads("k", bad, CPU, 5, 12, 16)
