@@ -30,14 +30,16 @@ def test_positions_by_section_are_refused(name):
 @pytest.mark.parametrize("name", ["gqa128", "mla"])
 def test_one_token_of_any_stride(name):
     r = Run(name, [1])
-    whole = torch.zeros(3, r.q.stride(0) + 4, dtype=torch.bfloat16, device="cuda")
-    row = whole[:1]
-    row[:, :-4] = torch.as_strided(r.q, (1, r.q.stride(0)), (r.q.stride(0), 1))
-    parts = row[:, :-4].unflatten(1, (-1, r.q.shape[2]))
-    hq, hk = r.hq, r.k.shape[1]
-    r.q, r.k = parts[:, :hq], parts[:, hq:hq + hk]
+    n, dk, hq, hk = r.q.stride(0), r.q.shape[2], r.hq, r.k.shape[1]
+    whole = torch.zeros(3, n + 4, dtype=torch.bfloat16, device="cuda")
+    whole[0, :n] = torch.as_strided(r.q, (n,), (1,))
+
+    def heads(first, count):
+        return torch.as_strided(whole, (1, count, dk), (n + 4, dk, 1), first * dk)
+
+    r.q, r.k = heads(0, hq), heads(hq, hk)
     if r.v is not None:
-        r.v = parts[:, hq + hk:]
+        r.v = heads(hq + hk, hk)
     assert r.q.stride(0) % 8 != 0
     assert r.call() == 0
     r.check(r.want())
