@@ -33,6 +33,12 @@ namespace {
 constexpr int kThr = 256;
 constexpr int kBatch = 4;  // query heads a group of lanes (rows a warp) has in flight
 
+// Every load is an ordinary one: q_out may be q, and the kernels live beside the one before them in
+// the stream, which may write the page table or any input until ptx::wait_for_previous returns.
+__device__ __forceinline__ uint4 ld16(const __nv_bfloat16 *p) {
+  return *reinterpret_cast<const uint4 *>(p);
+}
+
 __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
   f32x2 d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -97,8 +103,7 @@ __device__ __forceinline__ Turn make_turn(const float2 *ph, const __nv_bfloat16 
 #pragma unroll
   for (int i = 0; i < 4; ++i) u.a[i] = u.b[i] = f2(1.f, 1.f);
   if (w)
-    u = unpack_unit<kNeox>(__ldg(reinterpret_cast<const uint4 *>(w + ca)),
-                           __ldg(reinterpret_cast<const uint4 *>(w + cb)));
+    u = unpack_unit<kNeox>(ld16(w + ca), ld16(w + cb));
   Turn t;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -162,9 +167,6 @@ __device__ __forceinline__ float norm_scale(float mean) {
   return mean > 0x1p126f ? 0x1p-70f : (mean < 0x1p-90f ? 0x1p70f : 1.f);
 }
 
-__device__ __forceinline__ uint4 ld16(const __nv_bfloat16 *p) {
-  return *reinterpret_cast<const uint4 *>(p);  // plain: q_out may be q
-}
 __device__ __forceinline__ void st16(__nv_bfloat16 *p, const uint4 &v) {
   *reinterpret_cast<uint4 *>(p) = v;
 }
@@ -303,8 +305,8 @@ __global__ void __launch_bounds__(kThr, 2) append_kernel(const __grid_constant__
   };
   if (copies && (blockIdx.x & 1)) {
     if (tid < nt) {
-      const int req = __ldg(a.req + t0 + tid);
-      live[tid] = req >= 0 && in_table(req, __ldg(a.tok + t0 + tid));
+      const int req = a.req[t0 + tid];
+      live[tid] = req >= 0 && in_table(req, a.tok[t0 + tid]);
     }
     __syncthreads();
     copy_latents(a, t0, nt, live);
@@ -326,8 +328,8 @@ __global__ void __launch_bounds__(kThr, 2) append_kernel(const __grid_constant__
   // the tokens' places first: their slots take two dependent loads
   int req = -1, at = 0;
   if (tid < nt) {
-    req = __ldg(a.req + t0 + tid);
-    at = __ldg(a.tok + t0 + tid);
+    req = a.req[t0 + tid];
+    at = a.tok[t0 + tid];
   }
   uint4 ra[kBatch], rb[kBatch], ka, kb;
   auto load = [&](const __nv_bfloat16 *row, int h, int n, uint4 &x, uint4 &y) {
@@ -350,14 +352,14 @@ __global__ void __launch_bounds__(kThr, 2) append_kernel(const __grid_constant__
     const bool bad = !padding && !in_table(req, at);
     if (bad) atomicOr(a.status, KAMERA_DEVICE_BAD_ITEM);
     live[tid] = !padding && !bad;
-    slots[tid] = padding || bad ? -1 : slot_of(a.pool, lay.page_size, req, at, a.status);
+    slots[tid] = padding || bad ? -1 : slot_of<false>(a.pool, lay.page_size, req, at, a.status);
   }
 
   for (int e = tid; e < nt * np; e += kThr) {
     const int t = e / np, i = e - t * np;
     const int axis = lay.mrope ? mrope_axis(lay, i) : 0;
     const int stride = lay.mrope ? 3 : 1;
-    cs[e] = rope_phase(a.freq.q[i], __ldg(a.positions + (t0 + t) * stride + axis));
+    cs[e] = rope_phase(a.freq.q[i], a.positions[(t0 + t) * stride + axis]);
   }
   __syncthreads();
 
@@ -443,7 +445,7 @@ __global__ void __launch_bounds__(kThr, 2) append_kernel(const __grid_constant__
       if (a.k_weight) {
         float x[8], wv[8];
         unpack8(v, x);
-        unpack8(__ldg(reinterpret_cast<const uint4 *>(a.k_weight + 8 * c)), wv);
+        unpack8(ld16(a.k_weight + 8 * c), wv);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = x[e] * f * r * wv[e];
         v = pack8_rn(x);
@@ -570,8 +572,8 @@ __global__ void __launch_bounds__(32 * kStreamWarps, 1) append_stream_kernel(
   auto load_place = [&](long long t) {
     Place p{-1, 0};
     if (t < a.T) {
-      p.req = __ldg(a.req + t);
-      p.tok = __ldg(a.tok + t);
+      p.req = a.req[t];
+      p.tok = a.tok[t];
     }
     return p;
   };
@@ -583,7 +585,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, 1) append_stream_kernel(
       p.req = -1;
       return 0;
     }
-    return __ldg(a.pool.pt + (long long)p.req * a.pool.pt_stride + p.tok / lay.page_size);
+    return a.pool.pt[(long long)p.req * a.pool.pt_stride + p.tok / lay.page_size];
   };
   constexpr int kPos = kMaxPairs / 32;  // lane e makes pairs e, e + 32, ...
   long long pos[kPos];
@@ -592,7 +594,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, 1) append_stream_kernel(
     for (int j = 0; j < kPos; ++j) {
       const int i = lane + 32 * j;
       if (i >= np || t >= a.T) continue;
-      pos[j] = __ldg(a.positions + (lay.mrope ? 3 * t + mrope_axis(lay, i) : t));
+      pos[j] = a.positions[lay.mrope ? 3 * t + mrope_axis(lay, i) : t];
     }
   };
 
@@ -677,7 +679,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, 1) append_stream_kernel(
           if (a.k_weight) {
             float x[8], wv[8];
             unpack8(v, x);
-            unpack8(__ldg(reinterpret_cast<const uint4 *>(a.k_weight + 8 * e)), wv);
+            unpack8(ld16(a.k_weight + 8 * e), wv);
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = x[i] * f * r * wv[i];
             v = pack8_rn(x);

@@ -407,7 +407,9 @@ __device__ __forceinline__ float2 rope_phase(unsigned long long q, long long del
 }
 
 // Physical slot of logical token tok of request req; -1 (and the OOB status bit) when the
-// page-table entry points outside the pool.
+// page-table entry points outside the pool. kFixed: nothing writes the table while the kernel
+// lives; a kernel that starts early may live beside one that does, and takes ordinary loads.
+template <bool kFixed = true>
 __device__ __forceinline__ long long slot_of(const DevPool &p, int page_size, int req,
                                              long long tok, unsigned *status) {
   const long long pi = tok / page_size;
@@ -415,7 +417,8 @@ __device__ __forceinline__ long long slot_of(const DevPool &p, int page_size, in
     atomicOr(status, KAMERA_DEVICE_SLOT_OOB);
     return -1;
   }
-  const int page = __ldg(p.pt + (long long)req * p.pt_stride + pi);
+  const int *entry = p.pt + (long long)req * p.pt_stride + pi;
+  const int page = kFixed ? __ldg(entry) : *entry;
   if (page < 0 || ((long long)page + 1) * page_size > p.num_slots) {
     atomicOr(status, KAMERA_DEVICE_SLOT_OOB);
     return -1;

@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kThr) copy_kernel(const __grid_constant__ Page
   const int nlc = a.lay.L * a.lay.n_ch;
   for (long long u = blockIdx.x; u < (long long)a.n * nlc; u += gridDim.x) {
     const long long k = u / nlc;
-    const int src = __ldg(a.src + k), dst = __ldg(a.dst + k);
+    const int src = a.src[k], dst = a.dst[k];
     if (!in_pool(a, src) || !in_pool(a, dst)) {
       if (threadIdx.x == 0) atomicOr(a.status, KAMERA_DEVICE_SLOT_OOB);
       continue;

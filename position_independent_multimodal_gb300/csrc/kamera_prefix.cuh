@@ -311,7 +311,8 @@ __device__ __forceinline__ int page_index(const PrefixArgs &a, int tok) {
   return a.page_shift >= 0 ? tok >> a.page_shift
                            : (int)((unsigned)tok / (unsigned)a.lay.page_size);
 }
-// A page-table entry as loaded, before its check.
+// A page-table entry as loaded, before its check. Read-only loads: the plan kernel does not start
+// early, so whatever wrote the table was complete before any kernel of the call.
 __device__ __forceinline__ int load_page(const PrefixArgs &a, int lead, int tok) {
   return __ldg(a.pool.pt + (long long)lead * a.pool.pt_stride + page_index(a, tok));
 }
