@@ -458,6 +458,10 @@ kamera_status kamera_append(const kamera_handle *handle, const kamera_pool *pool
  *   that is not full is copied to a new page in every layer (its first num_tokens % page_size
  *   rows). The child's row must hold nothing before. No request is a child twice, or a child
  *   and a parent, in one call; one parent may have many children.
+ *   An entry of the parent that lies outside the pool sets KAMERA_DEVICE_SLOT_OOB. One of a whole
+ *   page is copied as it is. Where the last page's does, the child still has a new page there,
+ *   with the rows that its last holder left: fork no parent whose pages are not all in the pool,
+ *   or release such a child before it is read.
  * kamera_extend: pages for tokens [from_tok, to_tok) of a request, each with count 1.
  *   When the free pages run out before an item of kamera_fork or kamera_extend, that item and
  *   later ones that need pages set KAMERA_DEVICE_NO_PAGES and nothing of them is done.
