@@ -110,8 +110,10 @@ struct Place {
   }
 };
 
-// Halves of the matrix descriptors (kamera_ptx.cuh): the start address and leading offset, to
-// which the steps inside a tile are added, and the constant rest.
+// Halves of the matrix descriptors of 128-byte swizzled operands, whose eight rows of 128 bytes make
+// a group of 1024 bytes (the stride offset): the start address and leading offset, to which the
+// steps inside a tile are added, and the constant rest. MN-major, 64 elements along M or N make a
+// row, and the leading offset is that of the next 64.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_k(uint32_t addr) { return (addr >> 4) | (1u << 16); }
 __device__ __forceinline__ uint32_t desc_mn(uint32_t addr) {

@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(T::WARPS * 32, 1)
 // ---------------------------------------------------------------------------------------
 
 struct ThinMla {
-  static constexpr int D = 576, DV = 512, kTok = 64, kThr = 256;
+  static constexpr int D = 576, kTok = 64, kThr = 256;
   static constexpr int kRow = D * 2;            // bytes of a row
   static constexpr int kTile = kTok * kRow;
   static constexpr int k = 0;                   // two stages
