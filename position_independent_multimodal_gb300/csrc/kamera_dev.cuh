@@ -662,10 +662,10 @@ size_t prefix_workspace(const DevLayout &l, long long n_reqs, int hq, int dv);
 cudaError_t launch_prefix_attention(const PrefixArgs &a, cudaStream_t s);
 bool prefix_tc_layout(const DevLayout &l);                          // kamera_prefix_tc.cu
 PrefixClass prefix_tc_class(const DevLayout &l, int hq);
-cudaError_t prepare_prefix_tc();
+cudaError_t prepare_prefix_tc(const DevLayout &l);
 cudaError_t launch_prefix_tc(const PrefixArgs &a, cudaStream_t s);
 PrefixClass prefix_thin_class(const DevLayout &l);                  // kamera_prefix_thin.cu
-cudaError_t prepare_prefix_thin();
+cudaError_t prepare_prefix_thin(const DevLayout &l);
 cudaError_t launch_prefix_thin(const PrefixArgs &a, bool beside, cudaStream_t s);
 cudaError_t launch_rope_phases(const FreqQ64 &f, int npairs, const long long *deltas, int n,
                                float *out, cudaStream_t s);

@@ -655,28 +655,36 @@ cudaError_t launch_prefix_attention(const PrefixArgs &args, cudaStream_t s) {
   PrefixArgs a = args;
   a.wait_ns = kamera_prefix_wait_ns;
   a.gave_up = prefix_plan(a.shape, a.ws, a.n_reqs, a.hq, a.dv).gave_up;
-  static int configured[64] = {0};
+  // per device and kind of layout, each with the kernels it runs: what one kind cannot have is
+  // nothing to the others
+  static int configured[64][4] = {{0}};
   static std::mutex mu;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  const int kind = !prefix_tc_layout(a.lay) ? 0
+                   : a.lay.kind == KAMERA_MLA ? 1
+                                              : (a.lay.hd == 128 ? 2 : 3);
   {
     std::lock_guard<std::mutex> lock(mu);
-    if (!configured[dev]) {
-      e = cudaFuncSetAttribute(prefix_gen_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               gen_plan(1024, 1024).total);
-      if (e == cudaSuccess) e = prepare_prefix_tc();
-      if (e == cudaSuccess) e = prepare_prefix_thin();
+    if (!configured[dev][kind]) {
+      if (kind == 0) {
+        e = cudaFuncSetAttribute(prefix_gen_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 gen_plan(1024, 1024).total);
+      } else {
+        e = prepare_prefix_tc(a.lay);
+        if (e == cudaSuccess) e = prepare_prefix_thin(a.lay);
+      }
       if (e != cudaSuccess) return e;
-      configured[dev] = 1;
+      configured[dev][kind] = 1;
     }
   }
   prefix_plan_kernel<<<1, kPlanThr, 0, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int hpk = a.hpk;
-  if (prefix_tc_layout(a.lay)) {
+  if (kind != 0) {
     // blocks can be wide only where the largest group would be, thin only where one request is
     const bool wide = (long long)a.n_reqs * hpk > a.shape.wide_rows;
     if (wide) e = launch_prefix_tc(a, s);

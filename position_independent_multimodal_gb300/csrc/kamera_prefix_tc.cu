@@ -795,11 +795,9 @@ PrefixClass prefix_tc_class(const DevLayout &l, int hq) {
   return c;
 }
 
-cudaError_t prepare_prefix_tc() {
-  cudaError_t e = configure<Gqa128>();
-  if (e == cudaSuccess) e = configure<Gqa64>();
-  if (e == cudaSuccess) e = configure<Mla512>();
-  return e;
+cudaError_t prepare_prefix_tc(const DevLayout &l) {
+  if (l.kind == KAMERA_MLA) return configure<Mla512>();
+  return l.hd == 128 ? configure<Gqa128>() : configure<Gqa64>();
 }
 
 cudaError_t launch_prefix_tc(const PrefixArgs &a, cudaStream_t s) {

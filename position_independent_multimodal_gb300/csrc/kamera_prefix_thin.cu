@@ -543,14 +543,13 @@ PrefixClass prefix_thin_class(const DevLayout &l) {
   return c;
 }
 
-cudaError_t prepare_prefix_thin() {
+cudaError_t prepare_prefix_thin(const DevLayout &l) {
   auto set = [](const void *f, int bytes) {
     return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   };
-  cudaError_t e = set((const void *)prefix_thin_kernel<Thin128>, Thin128::total);
-  if (e == cudaSuccess) e = set((const void *)prefix_thin_kernel<Thin64>, Thin64::total);
-  if (e == cudaSuccess) e = set((const void *)prefix_thin_mla_kernel, ThinMla::total);
-  return e;
+  if (l.kind == KAMERA_MLA) return set((const void *)prefix_thin_mla_kernel, ThinMla::total);
+  if (l.hd == 128) return set((const void *)prefix_thin_kernel<Thin128>, Thin128::total);
+  return set((const void *)prefix_thin_kernel<Thin64>, Thin64::total);
 }
 
 cudaError_t launch_prefix_thin(const PrefixArgs &a, bool beside, cudaStream_t s) {
