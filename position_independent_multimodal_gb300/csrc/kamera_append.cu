@@ -14,7 +14,8 @@
 //
 // append_kernel: a CTA of 256 threads per kTok tokens. A group of W lanes stays with one token and
 // takes several of its heads at a time, so that their loads are in flight together, before the
-// phases and slots are known. Few tokens (latency: 8 us at 8 tokens), or long rows.
+// phases and slots are known. Few tokens (latency: 8 us at 8 tokens), or long rows (the rule and its
+// measurements are at launch_append).
 // append_stream_kernel: a warp to a token, in CTAs that stay, each lane's next chunks arriving by
 // cp.async while it works, two heads at a time (one at a time: 4 us more). 16381 tokens of 28/4
 // heads of 128: 62 us, 302 MB moved, 4.9 TB/s (append_kernel 82 us); few warps fit, and the chain
@@ -466,7 +467,7 @@ __global__ void __launch_bounds__(kThr, 2) append_kernel(const __grid_constant__
 
 constexpr int kStreamRoom = 214 * 1024;  // shared memory for the rows in flight (phases: 12 KB)
 constexpr int kStreamWarps = 12;         // warps of a CTA at most (and 168 registers a thread)
-constexpr int kStreamLeast = 8;          // and at least: fewer are slower than the CTA kernel
+constexpr int kStreamLeast = 6;          // and at least: fewer are slower than the CTA kernel
 
 // Chunks of a token that a lane brings: two for each query head and key band of its group, then
 // V chunks (GQA) or the latent rows' (MLA: of the token, of its query heads).
@@ -713,18 +714,30 @@ cudaError_t launch(const AppendArgs &a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t s) {
-  // One token a CTA, four, or a warp a token. Measured with a call's overhead, L2 flushed, in us:
-  //                             T = 304: one four warps  608: one four warps  16381: four warps
-  //   28/4 heads of 128 (11 warps fit)    11   11    13        17   11    13          89    68
-  //   32/32 heads of 128 (4)              13   17    17        19   17    17         168   224
-  //   6/2 heads of 64 (12)                11   11    11        15   11    11          66    33
-  //   MLA, 16 heads copied (5)            17   11    14         -   13    15         142   154
-  //   MLA, queries in place (12)          11   12    11        17   11    11          79    40
-  // (Copies beside them double the CTAs.) A CTA's few warps must hold the rows in flight that HBM
-  // wants, and eight do the arithmetic.
-  if (a.T * (copies_beside(a) ? 2 : 1) <= 2 * kSms) return launch<1>(a, s);
+  // One token a CTA, four, or a warp a token, in us: calls one after another over 400 MB, from a
+  // graph (in brackets how many warps fit):
+  //                       T = 304          608          1216        2432        16381
+  //                     one four warps  four warps   four warps  four warps  four warps
+  //   28/4 x 128 (11)   6.3  6.1  6.9    6.8  7.4     8.6  9.0   15.9 15.0     85   62
+  //   32/8 x 128 (8)    6.6  7.2  7.5    8.0  8.2    10.2 10.6   19.0 17.4    103   91
+  //   40/8 x 128 (7)    6.7  8.6  8.0    9.6  8.9    11.9 15.6   22.1 22.9    122  106
+  //   48/8 x 128 (6)                                 12.4 16.4   22.9 24.8    126  129
+  //   56/8 x 128 (5)                                 13.5 17.3   24.1 32.6    131  164
+  //   32/32 x 128 (4)   8.0 10.8 10.3   12.2 12.1    16.2 20.3   29.2 36.7    171  206
+  //   6/2 x 64 (12)     5.5  4.9  4.6    5.0  4.6     5.6  4.9   10.4  7.1     68   33
+  //   16/2 x 128 (12)   6.1  5.7  6.0    6.0  6.2     7.3  7.2   13.6 11.2     81   49
+  //   MLA, in place (12) 6.4 6.0  5.3    6.4  5.6     7.5  6.6   13.2  9.2     81   40
+  //   MLA, 10 copied (7)                             13.3 13.8   23.4 20.0    121   90
+  //   MLA, 12 copied (6)                             13.6 14.5   24.1 21.0    127  108
+  //   MLA, 16 copied (5) 11.3 6.5 8.8    7.6  9.6    14.1 16.1   25.5 29.9    140  149
+  // CTAs of four tokens, two to an SM, are one wave up to 8 * kSms tokens (half as many with copies
+  // beside them, which double the CTAs), and hard to beat until then; rows so narrow that all the
+  // warps fit have more of them in flight as warps from the start. Six warps are the border: 15 %
+  // faster for MLA, 2 to 8 % slower for GQA; fewer do not hold the rows in flight that HBM wants.
+  const long long n = a.T * (copies_beside(a) ? 2 : 1);
+  if (n <= 2 * kSms) return launch<1>(a, s);
   const StreamPlan sp = stream_plan(a.lay, a.hq, a.q_out != a.q);
-  if (sp.warps < kStreamLeast) return launch<4>(a, s);
+  if (sp.warps < kStreamLeast || (sp.warps < kStreamWarps && n <= 8 * kSms)) return launch<4>(a, s);
   static int configured[64] = {0};
   static std::mutex mu;
   int dev = 0;
