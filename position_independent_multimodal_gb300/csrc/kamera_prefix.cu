@@ -25,10 +25,17 @@ namespace kamera {
 namespace {
 
 constexpr int kPlanThr = 256;
-// Tiles. The wide kernel with workers of each block's own | with the units in equal parts, in us:
-// 128 requests of 28/4 heads of 128 over 65500 tokens 101 | 117, 40 requests of MLA over two
-// prefixes of 9003 41 | 49, 48 of 28/4 heads over three of 6001 18 | 21.
-constexpr int kOwnExtra = 6;
+// Tiles that a worker may have more than its equal part for each wide block to have workers of its
+// own: blocks of two tiles of query rows, of one. Calls with workers of each block's own | with the
+// units in equal parts, in us, by the tiles more:
+//   two tiles of rows (28/4 heads of 128, 252 rows a block)
+//     1: 59 | 66, 62 | 71   2: 83 | 91, 60 | 61   4: 82 | 85, 132 | 138   6: 90 | 93, 87 | 88
+//     7: 136 | 138, 106 | 107, 110 | 106   8: 93 | 87   12: 138 | 136   16: 119 | 105
+//   one tile (63 rows a block; MLA)
+//     1: 39 | 45, 38 | 43, 77 | 71   2: 41 | 42, 48 | 48; 62 | 63, 95 | 99, 79 | 76
+//     3: 55 | 55; 89 | 87, 97 | 91   4: 67 | 63, 73 | 71; 112 | 106   6: 74 | 69; 132 | 124   8: 67 | 60
+constexpr int kOwnExtraTwo = 6, kOwnExtraOne = 2;
+constexpr int kOwnRows = 128;    // query rows of a tile
 constexpr int kPlanNear = 1024;  // groups and listed entries kept in shared memory
 
 // Inclusive scans of N values at a time over the CTA's threads, in place; total: their sums.
@@ -234,8 +241,8 @@ __global__ void __launch_bounds__(kPlanThr)
       p.head[16] = own_listed;
     }
     if (c == 1) break;
-    // Workers for each block, in proportion to its tiles? Where that costs none more than kOwnExtra
-    // tiles, about what a part of a second block costs it.
+    // Workers for each block, in proportion to its tiles? Where that costs none more tiles than
+    // about what a part of a second block costs it.
     if (own0 == U && groups <= kPlanThr) {
       int tiles = 0, nrb = 0, per = 0;
       if (tid < groups) {
@@ -243,7 +250,8 @@ __global__ void __launch_bounds__(kPlanThr)
         nrb = ceil_div(list.g_size[tid] * hpk, k.rb);
         per = (int)div_pos((long long)tiles * n, U);
         const long long most = per ? ceil_div(tiles, per) : tiles;
-        if (per == 0 || most > quot + kOwnExtra) worst = 1;
+        const bool two = min(list.g_size[tid] * hpk, k.rb) > kOwnRows;
+        if (per == 0 || most > quot + (two ? kOwnExtraTwo : kOwnExtraOne)) worst = 1;
       }
       long long x[1] = {(long long)a.n_kv * k.vh * nrb * per}, all[1];
       plan_scan(x, all);  // at most n: each is rounded down
