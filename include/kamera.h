@@ -477,7 +477,9 @@ kamera_status kamera_append(const kamera_handle *handle, const kamera_pool *pool
  *   layer, K and V. d_dst names no page twice and none of d_src. A page outside the pool sets
  *   KAMERA_DEVICE_SLOT_OOB and the pair is skipped. Table and counts stay.
  * d_workspace: kamera_page_workspace(handle, num_slots, num_items) bytes of device memory,
- *   16-byte aligned (num_items 0 for kamera_compact); contents ignored and left undefined.
+ *   16-byte aligned (num_items 0 for kamera_compact); contents ignored and left undefined. It
+ *   serves one call at a time: calls that share it, replays of captured ones among them, are
+ *   ordered, as on one stream.
  * num_items and num_pairs at most 65535; items 4-byte aligned.
  */
 typedef struct kamera_fork_item {
@@ -531,7 +533,8 @@ kamera_status kamera_copy_pages(const kamera_handle *handle, const kamera_pool *
  * d_out        : bf16 [num_reqs][num_q_heads][Dv]; d_lse: float32 [num_reqs][num_q_heads]
  *                (natural log).
  * d_workspace  : kamera_prefix_attention_workspace(handle, num_reqs, num_q_heads) bytes of
- *                device memory, 16-byte aligned; contents ignored and left undefined.
+ *                device memory, 16-byte aligned; contents ignored and left undefined. It serves
+ *                one call at a time, as that of the page calls.
  * GQA and MLA as in kamera_decode_attention; softmax statistics and sums in float32. Layouts
  * that take the tensor cores round the softmax weights to bf16. Pages outside the pool set
  * KAMERA_DEVICE_SLOT_OOB and their tokens are left out. Limits: num_reqs <= 65535 and at most

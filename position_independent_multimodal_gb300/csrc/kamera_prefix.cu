@@ -86,7 +86,9 @@ __device__ __forceinline__ PrefixPlan::Lists lists_of(const PrefixPlan &p, int c
 
 // One CTA: checks the arguments, lists the groups and requests that have units, and finds each
 // wide worker's first block. Bound: the latency of its few dependent steps (6 to 8 us for 4 to 128
-// requests; 512 or 1024 threads are slower, by their barriers).
+// requests; 512 or 1024 threads are slower, by their barriers), and from some thousand requests its
+// rounds of 256: 11 us for 1024 requests of one group, 104 for 16384; with a group to each request
+// 15 and 265 us.
 __global__ void __launch_bounds__(kPlanThr)
     prefix_plan_kernel(const __grid_constant__ PrefixArgs a) {
   ptx::launch_dependents();

@@ -11,6 +11,14 @@
 // then O is rescaled in TMEM; after the first tiles that is rare. The row sums l take the
 // float32 weights, so l and the log-sum-exp carry no bf16 rounding.
 //
+// P is rounded to bf16, the one rounding between the scores and the output's own: both operands of
+// a product have one type, and V is bf16. It moves an output by at most 2^-8 sum p|V| / l, the size
+// of the output's own rounding; over many tokens the errors' signs differ and their mean falls with
+// the square root of their number (against float64 the listed cases are 1.2 to 1.4 times as far off
+// as float32 weights rounded once at the end). Float32 weights would take V converted to tf32,
+// twice its bytes of shared memory and half the rate, or P in two bf16 terms, PV's products twice;
+// layouts on the CUDA cores keep them.
+//
 // Roles: warps 0-15 (MLA 0-7) softmax, rescaling and output, two threads (of two warps) to a query
 // row, 64 tokens and half of O's columns each; the next four bring K and V rows through the page
 // table into a ring of stages; one thread of the next issues the MMAs and the copies of Q. Whole
@@ -55,7 +63,9 @@ template <int DK_, int DV_, int QT_, int UC_, int NST_, int NL_>
 struct Shape {
   static constexpr int DK = DK_, DV = DV_, QT = QT_, UC = UC_, NST = NST_, NL = NL_;
   static constexpr int kSoft = 8 * QT, kMma = kSoft + NL;  // softmax warps; the MMA warp
-  // With two query tiles the softmax warps take registers of the others; whole warpgroups
+  // With two query tiles the softmax warps take registers of the others; whole warpgroups. The
+  // kernel is compiled under the cap of its threads all the same (80 registers a thread for 768):
+  // GQA 128 spills 412 bytes and loads 332, GQA 64 400 and 328; MLA (128 registers) 84 and 64
   static constexpr bool kShift = QT == 2;
   static constexpr int kThr = 32 * (kShift ? (kMma + 4) / 4 * 4 : kMma + 1);
   static constexpr int kRegsSoft = 96, kRegsRest = 48;
