@@ -462,13 +462,15 @@ kamera_status kamera_append(const kamera_handle *handle, const kamera_pool *pool
  *   page is copied as it is. Where the last page's does, the child still has a new page there,
  *   with the rows that its last holder left: fork no parent whose pages are not all in the pool,
  *   or release such a child before it is read.
- * kamera_extend: pages for tokens [from_tok, to_tok) of a request, each with count 1.
+ * kamera_extend: pages for tokens [from_tok, to_tok) of a request, each with count 1. The entries
+ *   hold nothing before, and no entry is named by two items of a call.
  *   When the free pages run out before an item of kamera_fork or kamera_extend, that item and
  *   later ones that need pages set KAMERA_DEVICE_NO_PAGES and nothing of them is done.
  * kamera_free: the entries of tokens [from_tok, to_tok) become -1 and their pages' counts drop;
  *   a page with count 0 is free. from_tok 0 releases a request, a later one its tail. An entry
  *   outside the pool sets KAMERA_DEVICE_SLOT_OOB, a page that nothing held
- *   KAMERA_DEVICE_BAD_ITEM; an entry that two items name is released once.
+ *   KAMERA_DEVICE_BAD_ITEM; an entry that two items name is released once (the second finds -1,
+ *   which is outside the pool).
  * kamera_compact: the live pages (count not 0) come to lie in pages 0 .. live - 1: the k-th live
  *   page above that border moves to the k-th free page below it, in every layer; counts and
  *   every page-table entry (of all num_reqs * pt_stride) that names a moved page follow. The rows
