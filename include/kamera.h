@@ -474,7 +474,8 @@ kamera_status kamera_append(const kamera_handle *handle, const kamera_pool *pool
  * kamera_compact: the live pages (count not 0) come to lie in pages 0 .. live - 1: the k-th live
  *   page above that border moves to the k-th free page below it, in every layer; counts and
  *   every page-table entry (of all num_reqs * pt_stride) that names a moved page follow. The rows
- *   of the freed pages are left as they were. d_num_live (int32, device) gets the number of live pages.
+ *   of the freed pages are left as they were. d_num_live (int32, device) gets the number of live
+ *   pages.
  * kamera_copy_pages: page d_src[i] onto page d_dst[i] for i < num_pairs (int32, device), every
  *   layer, K and V. d_dst names no page twice and none of d_src. A page outside the pool sets
  *   KAMERA_DEVICE_SLOT_OOB and the pair is skipped. Table and counts stay.

@@ -14,8 +14,8 @@
 //
 // append_kernel: a CTA of 256 threads per kTok tokens. A group of W lanes stays with one token and
 // takes several of its heads at a time, so that their loads are in flight together, before the
-// phases and slots are known. Few tokens (latency: 8 us at 8 tokens), or long rows (the rule and its
-// measurements are at launch_append).
+// phases and slots are known. Few tokens (latency: 8 us at 8 tokens), or long rows (the rule and
+// its measurements are at launch_append).
 // append_stream_kernel: a warp to a token, in CTAs that stay, each lane's next chunks arriving by
 // cp.async while it works, two heads at a time (one at a time: 4 us more). 16381 tokens of 28/4
 // heads of 128: 62 us, 302 MB moved, 4.9 TB/s (append_kernel 82 us); few warps fit, and the chain

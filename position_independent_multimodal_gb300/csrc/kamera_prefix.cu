@@ -33,7 +33,8 @@ constexpr int kPlanThr = 256;
 //     7: 136 | 138, 106 | 107, 110 | 106   8: 93 | 87   12: 138 | 136   16: 119 | 105
 //   one tile (63 rows a block; MLA)
 //     1: 39 | 45, 38 | 43, 77 | 71   2: 41 | 42, 48 | 48; 62 | 63, 95 | 99, 79 | 76
-//     3: 55 | 55; 89 | 87, 97 | 91   4: 67 | 63, 73 | 71; 112 | 106   6: 74 | 69; 132 | 124   8: 67 | 60
+//     3: 55 | 55; 89 | 87, 97 | 91   4: 67 | 63, 73 | 71; 112 | 106   6: 74 | 69; 132 | 124
+//     8: 67 | 60
 constexpr int kOwnExtraTwo = 6, kOwnExtraOne = 2;
 constexpr int kOwnRows = 128;    // query rows of a tile
 constexpr int kPlanNear = 1024;  // groups and listed entries kept in shared memory

@@ -120,8 +120,8 @@ struct Place {
   }
 };
 
-// Halves of the matrix descriptors of 128-byte swizzled operands, whose eight rows of 128 bytes make
-// a group of 1024 bytes (the stride offset): the start address and leading offset, to which the
+// Halves of the matrix descriptors of 128-byte swizzled operands, whose eight rows of 128 bytes
+// make a group of 1024 bytes (the stride offset): the start address and leading offset, to which the
 // steps inside a tile are added, and the constant rest. MN-major, 64 elements along M or N make a
 // row, and the leading offset is that of the next 64.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
   };
 
   // The swizzled layouts want 1024-byte groups (there is no static memory here, so they get them);
-  // without them, or without time to wait, nothing is begun and the kernel ends as one that gave up.
+  // without them, or without time to wait, nothing is begun and the kernel ends as if it gave up.
   const bool begins = (sb & 1023u) == 0 && a.wait_ns != 0;
   if (warp == S::kMma) {
     ptx::tmem_alloc(sb + S::misc, 512);

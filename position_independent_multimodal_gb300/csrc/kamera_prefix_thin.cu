@@ -7,8 +7,8 @@
 //   S = Q K^T, P = bf16(2^(c S - m)), O += P V,  c = scale log2 e,  m raised by at least 8 at once
 //
 // Sums l and maxima m are float32 and l takes the unrounded weights. P is rounded to bf16, as the
-// products with bf16 V want it; the reasons and the error are with the wide blocks' kernel, and rows
-// that both kernels work on have one accuracy.
+// products with bf16 V want it; the reasons and the error are with the wide blocks' kernel, and
+// rows that both kernels work on have one accuracy.
 //
 //  * prefix_thin_kernel (GQA, head_dim 64 or 128): each warp is a worker with a range of 16-token
 //    tiles of its own and its own ring of stages (K, V and, with a segment's first tile, Q); the

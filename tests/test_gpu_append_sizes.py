@@ -1,5 +1,6 @@
-"""kamera_append on both sides of the borders between its kernels: a token a CTA, four, a warp a token
-(multiples of the number of SMs, halved where the queries' latents are copied by CTAs of their own)."""
+"""kamera_append on both sides of the borders between its kernels: a token a CTA, four, a warp a
+token (multiples of the number of SMs, halved where the queries' latents are copied by CTAs of
+their own)."""
 import pytest
 
 from tests import test_gpu_append as base
