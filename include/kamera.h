@@ -555,6 +555,49 @@ kamera_status kamera_prefix_attention(const kamera_handle *handle, const kamera_
                                       uint32_t *d_status, kamera_stream_t stream);
 
 /*
+ * Attention of chunks of new tokens over the paged pool (the pages start from a pool that an engine
+ * has filled; kamera_append fills it, this call attends what it appended). The new tokens of a
+ * batch are rows of q, each request's next to one another: one for a request that decodes, up to a
+ * whole prompt for one that starts. They are the last of the request's context, and their K and V
+ * are in the pool. The token at logical token t sees tokens [0, t], or with a window the last
+ * `window` of them (itself among them):
+ *   s_u = scale * q . K_u,  o = sum_u softmax(s)_u V_u,  lse = log sum_u exp(s_u).
+ * d_q          : bf16, token i's num_q_heads heads of Dk at d_q + i * q_stride; the stride in
+ *                elements, at least num_q_heads * Dk and a multiple of 8 (as kamera_append's
+ *                q_out); 16-byte aligned.
+ * d_token_start: int32 [num_reqs + 1]: rows token_start[r] .. token_start[r + 1] - 1 are request
+ *                r's new tokens (none: it takes no part); never falling, from 0 or more to at most
+ *                num_tokens. Otherwise the whole call sets KAMERA_DEVICE_BAD_ITEM and writes no
+ *                output. Rows outside of it (a batch padded to num_tokens) are left as they were.
+ * d_ctx_len    : int32 [num_reqs]: the request's context, its new tokens included: at least their
+ *                number and at most pt_stride * page_size. Another value sets
+ *                KAMERA_DEVICE_BAD_ITEM and that request's outputs are not written.
+ * window       : 0, or how many tokens a token sees at most. Pages of tokens that no new token sees
+ *                are not looked at.
+ * d_out        : bf16 [num_tokens][num_q_heads][Dv], 16-byte aligned; d_lse: float32
+ *                [num_tokens][num_q_heads] (natural log).
+ * d_workspace  : kamera_chunk_attention_workspace(handle, num_tokens, num_reqs, num_q_heads) bytes
+ *                of device memory, 16-byte aligned; contents ignored and left undefined. It serves
+ *                one call at a time, as that of the page calls.
+ * GQA and MLA as in kamera_decode_attention; softmax statistics and sums in float32, the softmax
+ * weights rounded to bf16 for their product with V. Pages outside the pool set
+ * KAMERA_DEVICE_SLOT_OOB and their tokens are left out; a token that sees nothing gets o = 0 and
+ * lse = -inf. What a token does not see has no effect on it, whatever the values. After
+ * KAMERA_DEVICE_TIMEOUT some outputs are not written. Limits: num_reqs <= 65535 and at most the
+ * pool's num_reqs, num_q_heads <= 256 (GQA: a multiple of num_kv_heads), Dk <= 1024.
+ */
+size_t kamera_chunk_attention_workspace(const kamera_handle *handle, int32_t num_tokens,
+                                        int32_t num_reqs, int32_t num_q_heads);
+
+kamera_status kamera_chunk_attention(const kamera_handle *handle, const kamera_pool *pool,
+                                     int32_t layer, const void *d_q, int64_t q_stride,
+                                     int32_t num_tokens, int32_t num_q_heads,
+                                     const int32_t *d_token_start, const int32_t *d_ctx_len,
+                                     int32_t num_reqs, int32_t window, float scale, void *d_out,
+                                     float *d_lse, void *d_workspace, size_t workspace_bytes,
+                                     uint32_t *d_status, kamera_stream_t stream);
+
+/*
  * Patch forming (§3 "Forming and applying the patch"; App. A "form_patch"): for each of
  * num_problems deficits Delta = KV(B|A) - R(delta)KV(B|empty), one (layer, group) each, the
  * top-m factors U*Sigma [T x m] and V_m^T [m x W] in the patch store's bf16 format. The

@@ -147,8 +147,13 @@ def lib() -> ctypes.CDLL:
         L.kamera_prefix_attention_workspace.restype = st
         L.kamera_prefix_attention.argtypes = [vp, pp, i32, vp, i32, i32, vp, vp, i32, vp,
                                               ctypes.c_float, vp, vp, vp, st, vp, vp]
+        L.kamera_chunk_attention_workspace.argtypes = [vp, i32, i32, i32]
+        L.kamera_chunk_attention_workspace.restype = st
+        L.kamera_chunk_attention.argtypes = [vp, pp, i32, vp, i64, i32, i32, vp, vp, i32, i32,
+                                             ctypes.c_float, vp, vp, vp, st, vp, vp]
         for f in ("kamera_append", "kamera_fork", "kamera_extend", "kamera_free",
-                  "kamera_compact", "kamera_copy_pages", "kamera_prefix_attention"):
+                  "kamera_compact", "kamera_copy_pages", "kamera_prefix_attention",
+                  "kamera_chunk_attention"):
             getattr(L, f).restype = ctypes.c_int
         for f in ("kamera_create", "kamera_destroy", "kamera_relocate", "kamera_reuse",
                   "kamera_set_option", "kamera_set_batch_workspace",
@@ -597,6 +602,47 @@ def kamera_prefix_attention(handle: Handle, pool: Pool, layer: int, q: torch.Ten
         _need("out", out, _BF16, dev), _need("lse", lse, torch.float32, dev),
         *_bytes(workspace, dev), _need("status", status, _I32, dev),
         _stream_on(stream, dev)), "kamera_prefix_attention")
+
+
+def kamera_chunk_attention_workspace(handle: Handle, num_tokens: int, num_reqs: int,
+                                     num_q_heads: int) -> int:
+    """Bytes of workspace for kamera_chunk_attention of up to num_tokens tokens of num_reqs
+    requests."""
+    return int(lib().kamera_chunk_attention_workspace(handle.ptr, int(num_tokens), int(num_reqs),
+                                                      int(num_q_heads)))
+
+
+def _chunk(handle: Handle, dev: int, q: torch.Tensor, token_start: torch.Tensor,
+           ctx_len: torch.Tensor) -> tuple:
+    """The arguments of a batch of new tokens: q and its stride, sizes, the requests' places."""
+    if q.dim() != 3:
+        raise ValueError(f"q must be [T][H_q][{handle._dk}]")
+    T, hq, _ = q.shape
+    R = ctx_len.numel()
+    if token_start.numel() != R + 1:
+        raise ValueError("token_start [R + 1] and ctx_len [R] are wanted")
+    return (q.data_ptr(), _heads("q", q, dev, T, hq, handle._dk), T, hq,
+            _need("token_start", token_start, _I32, dev), _need("ctx_len", ctx_len, _I32, dev), R)
+
+
+def kamera_chunk_attention(handle: Handle, pool: Pool, layer: int, q: torch.Tensor,
+                           token_start: torch.Tensor, ctx_len: torch.Tensor, scale: float,
+                           out: torch.Tensor, lse: torch.Tensor, workspace: torch.Tensor,
+                           status: torch.Tensor, window: int = 0, stream=None) -> None:
+    """Attention of new tokens ``q`` bf16 [T][H_q][Dk] (any token stride) over pool layer
+    ``layer``: rows ``token_start[r]`` .. ``token_start[r + 1] - 1`` are the last tokens of request
+    ``r``, whose context is ``ctx_len[r]``; each sees the tokens before it and itself, at most
+    ``window`` of them (0: all). Into ``out`` bf16 [T][H_q][Dv] and ``lse`` float32 [T][H_q]."""
+    p, dev = _pool_c(handle, pool)
+    batch = _chunk(handle, dev, q, token_start, ctx_len)
+    T, hq = batch[2:4]
+    if out.shape != (T, hq, handle._dv) or lse.shape != (T, hq):
+        raise ValueError(f"out [T][H_q][{handle._dv}] and lse [T][H_q] are wanted")
+    _check(lib().kamera_chunk_attention(
+        handle.ptr, ctypes.byref(p), layer, *batch, window, scale,
+        _need("out", out, _BF16, dev), _need("lse", lse, torch.float32, dev),
+        *_bytes(workspace, dev), _need("status", status, _I32, dev),
+        _stream_on(stream, dev)), "kamera_chunk_attention")
 
 
 def kamera_rope_phases(handle: Handle, d_deltas: torch.Tensor, d_out: torch.Tensor,

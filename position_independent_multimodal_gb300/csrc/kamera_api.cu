@@ -793,6 +793,95 @@ kamera_status kamera_prefix_attention(const kamera_handle *h, const kamera_pool 
   return from_cuda(kamera::launch_prefix_attention(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+}  // extern "C"
+
+namespace {
+
+// What the calls over chunks of new tokens share: the pool, the queries and the batch.
+kamera_status chunk_args(const kamera_handle *h, const kamera_pool *pool, int32_t layer,
+                         const void *d_q, int64_t q_stride, int32_t num_tokens,
+                         int32_t num_q_heads, const int32_t *d_token_start,
+                         const int32_t *d_ctx_len, int32_t num_reqs, int32_t window, float scale,
+                         uint32_t *d_status, kamera::ChunkArgs *a) {
+  if (!h || !d_status) return KAMERA_ERR_INVALID_ARG;
+  std::memset(a, 0, sizeof(*a));
+  const DevLayout &l = h->lay;
+  a->lay = l;
+  const kamera_status st = check_pool(l, pool, &a->pool);
+  if (st != KAMERA_OK) return st;
+  const bool gqa = l.kind == KAMERA_GQA;
+  if (layer < 0 || layer >= l.L || num_tokens < 0 || num_reqs < 0 || num_q_heads < 1 || window < 0)
+    return KAMERA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return KAMERA_ERR_INVALID_ARG;
+  if (num_q_heads > 256 || num_reqs > 65535) return KAMERA_ERR_UNSUPPORTED;
+  if (gqa && num_q_heads % l.H != 0) return KAMERA_ERR_INVALID_ARG;
+  a->dk = gqa ? l.hd : l.latent + l.rope_d;
+  a->dv = gqa ? l.hd : l.latent;
+  if (a->dk > 1024) return KAMERA_ERR_UNSUPPORTED;
+  if (num_reqs > a->pool.num_reqs) return KAMERA_ERR_INVALID_ARG;
+  if (num_tokens == 0 || num_reqs == 0) return KAMERA_OK;
+  auto mis = [](const void *p, uintptr_t al) {
+    return !p || (reinterpret_cast<uintptr_t>(p) & (al - 1));
+  };
+  if (mis(d_q, 16) || mis(d_token_start, 4) || mis(d_ctx_len, 4)) return KAMERA_ERR_INVALID_ARG;
+  // (strides of 2^40 bytes and more do not fit a tensor map)
+  if (q_stride < (int64_t)num_q_heads * a->dk || (q_stride & 7) != 0) return KAMERA_ERR_INVALID_ARG;
+  if (q_stride >= (1ll << 39)) return KAMERA_ERR_UNSUPPORTED;
+  a->layer = layer;
+  a->q = static_cast<const __nv_bfloat16 *>(d_q);
+  a->q_stride = q_stride;
+  a->token_start = d_token_start;
+  a->ctx_len = d_ctx_len;
+  a->n_tokens = num_tokens;
+  a->n_reqs = num_reqs;
+  a->hq = num_q_heads;
+  a->n_kv = gqa ? l.H : 1;
+  a->hpk = num_q_heads / a->n_kv;
+  a->hpk_magic = (65536 + a->hpk - 1) / a->hpk;
+  a->page_shift = -1;
+  for (int s = 0; s < 31; ++s)
+    if (l.page_size == 1 << s) a->page_shift = s;
+  a->window = window;
+  a->scale = scale;
+  a->status = d_status;
+  return KAMERA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kamera_chunk_attention_workspace(const kamera_handle *h, int32_t num_tokens,
+                                        int32_t num_reqs, int32_t num_q_heads) {
+  if (!h || num_tokens < 0 || num_reqs < 0 || num_q_heads < 0) return 0;
+  return kamera::chunk_workspace(h->lay);
+}
+
+kamera_status kamera_chunk_attention(const kamera_handle *h, const kamera_pool *pool,
+                                     int32_t layer, const void *d_q, int64_t q_stride,
+                                     int32_t num_tokens, int32_t num_q_heads,
+                                     const int32_t *d_token_start, const int32_t *d_ctx_len,
+                                     int32_t num_reqs, int32_t window, float scale, void *d_out,
+                                     float *d_lse, void *d_workspace, size_t workspace_bytes,
+                                     uint32_t *d_status, kamera_stream_t stream) {
+  kamera::ChunkArgs a;
+  kamera_status st = chunk_args(h, pool, layer, d_q, q_stride, num_tokens, num_q_heads,
+                                d_token_start, d_ctx_len, num_reqs, window, scale, d_status, &a);
+  if (st != KAMERA_OK || num_tokens == 0 || num_reqs == 0) return st;
+  auto mis = [](const void *p, uintptr_t al) {
+    return !p || (reinterpret_cast<uintptr_t>(p) & (al - 1));
+  };
+  if (mis(d_out, 16) || mis(d_lse, 4) || mis(d_workspace, 16) ||
+      workspace_bytes < kamera::chunk_workspace(h->lay))
+    return KAMERA_ERR_INVALID_ARG;
+  a.shape = kamera::chunk_shape(h->lay);
+  kamera::chunk_blocks(&a);
+  a.ws = d_workspace;
+  a.out = static_cast<__nv_bfloat16 *>(d_out);
+  a.lse = d_lse;
+  return from_cuda(kamera::launch_chunk_attention(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 kamera_status kamera_rope_phases(const kamera_handle *h, const int64_t *d_deltas,
                                  int32_t num_deltas, float *d_out, kamera_stream_t stream) {
   if (!h || num_deltas < 0) return KAMERA_ERR_INVALID_ARG;

@@ -1,0 +1,321 @@
+// Work division of attention over chunks of new tokens, used by its kernels.
+//
+// Each request's new tokens are the last of its context; token t sees tokens [0, t], or the last
+// `window` of them. A block is a run of tb consecutive new tokens of a request with the query
+// heads of one KV head (and one part of V's columns): at most rb query rows that read the same
+// rows of K and V. A unit is one tile of 2^tile_sh cached tokens of a block, from the first that a
+// row of it sees to the last. Units are numbered by request, KV head, block, tile; workers take
+// consecutive ones, as many as one another, so that every worker has the same number of tiles
+// whatever the lengths and cuts at most its first and last block. Blocks that one worker has whole
+// are written at once. Of a cut block the worker of its first tile writes its part to the worker's
+// home place and the others theirs to their carry places; the join kernel merges them by their
+// log-sum-exp.
+//
+// No plan is made ahead: a request's units are counted by a closed form (sums of rounded linear
+// terms), so every CTA finds its first block by itself in one pass over the requests.
+#pragma once
+
+#include "kamera_prefix.cuh"
+
+namespace kamera {
+
+// What a worker leaves for the join kernel.
+struct ChunkRecord {
+  int head;        // 1: its last segment is the first part of a cut block
+  int more;        // of that block: workers that follow on it
+  int row, rows;   // of it: row of q of its first token, query rows
+  int h0, part;    // of it: first query head, part of V's columns
+  int gave_up;
+  int segments;    // segments of the worker
+  int carry;       // 1: the first of them starts inside its block
+  int odd0, odd1;  // first and last of them that ChunkOdd says must be taken again (odd0 > odd1: none)
+  int pad[5];
+};
+
+struct ChunkPlaces {
+  ChunkRecord *rec;   // [n]
+  float *lse;         // [n][2][rb]: carry, home
+  float *o;           // [n][2][rb][vw]
+  size_t total;
+};
+
+__host__ __device__ inline ChunkPlaces chunk_places(const ChunkShape &s, void *ws) {
+  ChunkPlaces p;
+  const size_t skew = static_cast<size_t>(-reinterpret_cast<intptr_t>(ws)) & 127;
+  unsigned char *b = static_cast<unsigned char *>(ws) + skew;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    unsigned char *at = b + o;
+    o += (bytes + 127) & ~static_cast<size_t>(127);
+    return at;
+  };
+  p.rec = reinterpret_cast<ChunkRecord *>(take(sizeof(ChunkRecord) * s.n));
+  p.lse = reinterpret_cast<float *>(take(8ull * s.n * s.rb));
+  p.o = reinterpret_cast<float *>(take(8ull * s.n * s.rb * s.vw));
+  p.total = o + 112;  // the workspace is 16-byte aligned
+  return p;
+}
+
+// Sum over i < n of floor((a i + b) / 2^sh), by Euclid's steps on (2^sh, a); a n + b < 2^32.
+__device__ __forceinline__ long long floor_sum(unsigned n, int sh, unsigned a, unsigned b) {
+  if (n == 0) return 0;
+  unsigned m = 1u << sh;
+  long long sum = (long long)(n & 1 ? (n - 1) / 2 : n / 2) * (n & 1 ? n : n - 1) * (a >> sh) +
+                  (long long)n * (b >> sh);
+  a &= m - 1;
+  b &= m - 1;
+  while (true) {
+    const unsigned y = a * n + b;
+    if (y < m) return sum;
+    n = y / m;
+    b = y % m;
+    const unsigned t = a;
+    a = m;
+    m = t;
+    sum += (long long)(n & 1 ? (n - 1) / 2 : n / 2) * (n & 1 ? n : n - 1) * (a / m) +
+           (long long)n * (b / m);
+    a %= m;
+    b %= m;
+  }
+}
+
+// A request of the call.
+struct ChunkRequest {
+  int row, n;       // its first row of q, its new tokens (0: nothing to do)
+  int ctx, past;    // its context, the part before the new tokens
+  int nb;           // blocks of tokens
+};
+
+template <class Args>
+__device__ __forceinline__ ChunkRequest chunk_request(const Args &a, int r, bool *bad_start,
+                                                      bool *bad_item) {
+  ChunkRequest q;
+  q.row = a.token_start[r];
+  const int end = a.token_start[r + 1];
+  q.ctx = a.ctx_len[r];
+  q.n = end - q.row;
+  *bad_start = q.row < 0 || end < q.row || end > a.n_tokens;
+  if (*bad_start) q.n = 0;
+  *bad_item = q.n > 0 && (q.ctx < q.n || q.ctx > (long long)a.pool.pt_stride * a.lay.page_size);
+  if (*bad_item) q.n = 0;
+  q.past = q.ctx - q.n;
+  q.nb = ceil_div(q.n, a.tb);
+  return q;
+}
+
+// First token seen by the token at `tok`.
+template <class Args>
+__device__ __forceinline__ int first_seen(const Args &a, int tok) {
+  return a.window > 0 && tok >= a.window ? tok - a.window + 1 : 0;
+}
+
+// Tiles of a request's first j blocks.
+__device__ __forceinline__ long long chunk_tiles(const ChunkArgs &a, const ChunkRequest &q, int j) {
+  const int sh = a.shape.tile_sh;
+  const unsigned up = (1u << sh) - 1u;
+  long long sum = 0;
+  int whole = j;
+  if (j == q.nb) {  // the last one may have fewer tokens
+    --whole;
+    sum += ((unsigned)q.ctx + up) >> sh;
+  }
+  sum += floor_sum(whole, sh, a.tb, (unsigned)q.past + a.tb + up);
+  if (a.window > 0) {
+    const int lead = a.window - 1 - q.past;  // blocks that start before it see from token 0 on
+    const int i0 = lead > 0 ? ceil_div(lead, a.tb) : 0;
+    if (j > i0) sum -= floor_sum(j - i0, sh, a.tb, (unsigned)(q.past + i0 * a.tb - (a.window - 1)));
+  }
+  return sum;
+}
+
+// Where a worker starts, found by all threads of the CTA.
+struct ChunkStart {
+  long long quot, rem;   // units of the call / workers and the rest
+  long long units;       // of this worker
+  long long off;         // of its first unit in its request
+  int r;                 // that request
+  int bad;               // the call's token_start is no such list: nothing is done
+};
+
+template <int THR>
+struct ChunkScratch {
+  long long sums[THR / 32];
+  long long off;
+  int r;
+};
+
+template <int THR>
+__device__ __forceinline__ ChunkStart chunk_start(const ChunkArgs &a, int worker,
+                                                  ChunkScratch<THR> *sh) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.n_reqs + THR - 1) / THR;
+  const int r0 = min(a.n_reqs, tid * per), r1 = min(a.n_reqs, r0 + per);
+  const long long heads = (long long)a.n_kv * a.pieces * a.shape.vh;
+  bool bad = false, bad_item = false;
+  long long mine = 0;
+  for (int r = r0; r < r1; ++r) {
+    bool bs, bi;
+    const ChunkRequest q = chunk_request(a, r, &bs, &bi);
+    bad |= bs;
+    bad_item |= bi;
+    if (q.n) mine += heads * chunk_tiles(a, q, q.nb);
+  }
+  long long incl = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sh->sums[warp] = incl;
+  if (worker == 0 && (bad || bad_item)) atomicOr(a.status, KAMERA_DEVICE_BAD_ITEM);
+  ChunkStart s;
+  s.bad = __syncthreads_or(bad);
+  long long before = 0, total = 0;
+  for (int i = 0; i < THR / 32; ++i) {
+    if (i < warp) before += sh->sums[i];
+    total += sh->sums[i];
+  }
+  if (s.bad) total = 0;
+  const long long n = a.shape.n;
+  s.quot = div_pos(total, n);
+  s.rem = total - s.quot * n;
+  const long long u0 = first_unit(s.quot, s.rem, worker);
+  s.units = first_unit(s.quot, s.rem, worker + 1) - u0;
+  const long long excl = before + incl - mine;
+  if (s.units > 0 && u0 >= excl && u0 < excl + mine) {
+    long long off = u0 - excl;
+    for (int r = r0; r < r1; ++r) {
+      bool bs, bi;
+      const ChunkRequest q = chunk_request(a, r, &bs, &bi);
+      const long long u = q.n ? heads * chunk_tiles(a, q, q.nb) : 0;
+      if (off < u) {
+        sh->off = off;
+        sh->r = r;
+        break;
+      }
+      off -= u;
+    }
+  }
+  __syncthreads();
+  s.off = sh->off;
+  s.r = sh->r;
+  return s;
+}
+
+// A run of tiles of one block, as a worker takes it.
+struct ChunkSegment {
+  int r;               // the request
+  int row, ntok;       // row of q of the block's first token, its tokens
+  int first, ctx;      // that token's place in the context, the context
+  int kvh, h0, heads;  // KV head, first query head, query heads of each token
+  int part;            // part of V's columns
+  int t0, t1;          // tiles
+  int carry, more;     // starts inside its block; its first part: workers that follow on the block
+};
+
+// Walks a worker's segments; by whole warps.
+struct ChunkWalk {
+  ChunkRequest q;
+  long long left, quot, rem;
+  int r, hb, j, t, worker;  // the next block (request, head x part, block), its next tile
+
+  __device__ __forceinline__ void start(const ChunkArgs &a, const ChunkStart &s, int worker_) {
+    worker = worker_;
+    left = s.units;
+    quot = s.quot;
+    rem = s.rem;
+    r = s.r;
+    if (left == 0) return;
+    bool bs, bi;
+    q = chunk_request(a, r, &bs, &bi);
+    const long long per = chunk_tiles(a, q, q.nb);
+    const long long h = div_pos(s.off, per), rest = s.off - h * per;
+    hb = (int)h;
+    const int lane = threadIdx.x & 31;
+    j = 0;  // the last block that starts at or before `rest`
+    for (int len = q.nb; len > 1;) {
+      const int step = (len + 31) >> 5, k = j + lane * step;
+      const bool in = lane * step < len && (lane == 0 || chunk_tiles(a, q, k) <= rest);
+      const int i = __popc(__ballot_sync(0xffffffffu, in)) - 1;
+      j += i * step;
+      len = step == 1 ? 1 : min(step, len - i * step);
+    }
+    t = (int)(rest - (j ? chunk_tiles(a, q, j) : 0));
+  }
+  __device__ __forceinline__ bool next(const ChunkArgs &a, ChunkSegment *s) {
+    if (left == 0) return false;
+    const int heads = a.n_kv * a.pieces * a.shape.vh;
+    if (hb == heads) {
+      do {
+        bool bs, bi;
+        q = chunk_request(a, ++r, &bs, &bi);
+      } while (q.n == 0);
+      hb = j = t = 0;
+    }
+    const int part = hb % a.shape.vh, hp = hb / a.shape.vh, piece = hp % a.pieces;
+    const int sh = a.shape.tile_sh;
+    s->r = r;
+    s->kvh = hp / a.pieces;
+    s->part = part;
+    s->h0 = s->kvh * a.hpk + piece * a.shape.rb;
+    s->heads = min(a.hpk - piece * a.shape.rb, a.shape.rb);
+    s->row = q.row + j * a.tb;
+    s->ntok = min(a.tb, q.n - j * a.tb);
+    s->first = q.past + j * a.tb;
+    s->ctx = q.ctx;
+    const int b0 = first_seen(a, s->first) >> sh;
+    const int b1 = (int)(((unsigned)(s->first + s->ntok) + (1u << sh) - 1u) >> sh);
+    const int nt = b1 - b0 - t, take = (int)(left < nt ? left : nt);
+    s->t0 = b0 + t;
+    s->t1 = s->t0 + take;
+    s->carry = t > 0;
+    s->more = t == 0 && take < nt ? workers_for(quot, rem, worker + 1, nt - take) : 0;
+    left -= take;
+    t = 0;
+    if (++j == q.nb) {
+      j = 0;
+      ++hb;
+    }
+    return true;
+  }
+};
+
+// Token of row i of a block (its place among the block's) and the row's head.
+__device__ __forceinline__ void chunk_row(const ChunkArgs &a, const ChunkSegment &s, int i,
+                                          int *tok, int *h) {
+  const int k = a.pieces > 1 ? 0 : (int)((unsigned)i * a.hpk_magic >> 16);  // i / hpk for i < 256
+  *tok = k;
+  *h = s.h0 + i - k * a.hpk;
+}
+
+// Whether a block's output goes straight to the caller's tensors.
+__device__ __forceinline__ bool chunk_whole(const ChunkSegment &s) { return !s.carry && !s.more; }
+
+// The record of a worker. `odd`: segments [odd0, odd1] hold values of V that are not finite in
+// tokens that not all rows of a block see: times a weight of 0 they would not vanish, so the join
+// kernel takes those blocks again, token by token.
+__device__ __forceinline__ void chunk_note(ChunkRecord *rec, const ChunkSegment &last, int segments,
+                                           bool carry, bool gave_up, int odd0, int odd1) {
+  ChunkRecord c;
+  c.head = segments > 0 && last.more > 0;
+  c.more = last.more;
+  c.row = last.row;
+  c.rows = last.ntok * last.heads;
+  c.h0 = last.h0;
+  c.part = last.part;
+  c.gave_up = gave_up;
+  c.segments = segments;
+  c.carry = carry;
+  c.odd0 = odd0;
+  c.odd1 = odd1;
+  *rec = c;
+}
+
+// A bf16 pair with a value that is not finite.
+__device__ __forceinline__ bool odd_pair(uint32_t w) {
+  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+__device__ __forceinline__ bool odd8(const uint4 &v) {
+  return odd_pair(v.x) | odd_pair(v.y) | odd_pair(v.z) | odd_pair(v.w);
+}
+
+}  // namespace kamera

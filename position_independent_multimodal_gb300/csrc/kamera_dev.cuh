@@ -229,6 +229,35 @@ struct PrefixArgs {
   unsigned *status;
 };
 
+// How a layout's attention over chunks of new tokens is divided (kamera_chunk.cuh).
+struct ChunkShape {
+  int rb, tile_sh;      // rows of a block; a tile has 2^tile_sh tokens
+  int vh, vw;           // parts of V's columns, columns of a part
+  int n;                // workers
+};
+
+struct ChunkArgs {
+  DevLayout lay;
+  DevPool pool;
+  int layer;
+  const __nv_bfloat16 *q;   // token t's heads [hq][dk] at q + t * q_stride
+  long long q_stride;
+  const int *token_start;   // [n_reqs + 1]
+  const int *ctx_len;       // [n_reqs]
+  int n_tokens, n_reqs, hq, n_kv, dk, dv;
+  int hpk, pieces, tb;      // query heads of a KV head, pieces of at most rb of them, tokens a block
+  unsigned hpk_magic;       // ceil(2^16 / hpk)
+  int page_shift;           // log2 of the page size, -1 when that is no power of two
+  int window;               // 0: all tokens before
+  float scale;
+  ChunkShape shape;
+  unsigned long long wait_ns;
+  void *ws;
+  __nv_bfloat16 *out;       // [n_tokens][hq][dv]
+  float *lse;               // [n_tokens][hq]
+  unsigned *status;
+};
+
 // The rules an item must satisfy (host: kamera_reuse; device: each batch item).
 __host__ __device__ inline bool aligned16(const void *p) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
@@ -667,6 +696,13 @@ cudaError_t launch_prefix_tc(const PrefixArgs &a, cudaStream_t s);
 PrefixClass prefix_thin_class(const DevLayout &l);                  // kamera_prefix_thin.cu
 cudaError_t prepare_prefix_thin(const DevLayout &l);
 cudaError_t launch_prefix_thin(const PrefixArgs &a, bool beside, cudaStream_t s);
+ChunkShape chunk_shape(const DevLayout &l);                         // kamera_chunk.cu
+void chunk_blocks(ChunkArgs *a);  // pieces and tb, of its shape and heads
+size_t chunk_workspace(const DevLayout &l);
+cudaError_t launch_chunk_attention(const ChunkArgs &a, cudaStream_t s);
+ChunkShape chunk_tc_shape(const DevLayout &l);                      // kamera_chunk_tc.cu
+cudaError_t prepare_chunk_tc(const DevLayout &l);
+cudaError_t launch_chunk_tc(const ChunkArgs &a, cudaStream_t s);
 cudaError_t launch_rope_phases(const FreqQ64 &f, int npairs, const long long *deltas, int n,
                                float *out, cudaStream_t s);
 

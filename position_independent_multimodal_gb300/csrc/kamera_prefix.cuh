@@ -307,17 +307,20 @@ __device__ __forceinline__ void segment_out(const PrefixArgs &a, const PrefixPla
 }
 
 // Logical token tok's index in the page table and within its page.
-__device__ __forceinline__ int page_index(const PrefixArgs &a, int tok) {
+template <class Args>
+__device__ __forceinline__ int page_index(const Args &a, int tok) {
   return a.page_shift >= 0 ? tok >> a.page_shift
                            : (int)((unsigned)tok / (unsigned)a.lay.page_size);
 }
-// A page-table entry as loaded, before its check. Read-only loads: the plan kernel does not start
-// early, so whatever wrote the table was complete before any kernel of the call.
-__device__ __forceinline__ int load_page(const PrefixArgs &a, int lead, int tok) {
+// A page-table entry as loaded, before its check. Read-only loads: the first kernel of a call does
+// not start early, so whatever wrote the table was complete before any kernel of the call.
+template <class Args>
+__device__ __forceinline__ int load_page(const Args &a, int lead, int tok) {
   return __ldg(a.pool.pt + (long long)lead * a.pool.pt_stride + page_index(a, tok));
 }
 // Its token's slot; -1 (and the OOB bit) when the page ends outside the pool.
-__device__ __forceinline__ int slot_in(const PrefixArgs &a, int page, int tok) {
+template <class Args>
+__device__ __forceinline__ int slot_in(const Args &a, int page, int tok) {
   const int ps = a.lay.page_size;
   if (page < 0 || ((long long)page + 1) * ps > a.pool.num_slots) {
     atomicOr(a.status, KAMERA_DEVICE_SLOT_OOB);
