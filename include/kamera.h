@@ -598,6 +598,80 @@ kamera_status kamera_chunk_attention(const kamera_handle *handle, const kamera_p
                                      uint32_t *d_status, kamera_stream_t stream);
 
 /*
+ * Attention masses of cached tokens, for deciding what stays when a request outgrows its budget:
+ * what the softmax weights of the new tokens' query heads sum to on each token,
+ *   mass[r][u] = decay * mass[r][u] + sum over new tokens t that see u, heads h of
+ *                exp(scale * q_th . K_u - lse_th)             for u < ctx_len[r].
+ * The batch (d_q, q_stride, num_tokens, num_q_heads, d_token_start, d_ctx_len, num_reqs, window,
+ * scale) is that of kamera_chunk_attention and d_lse what that call left; the last tokens of a
+ * prompt alone may be given, with their rows of q and lse. decay 0 sets the masses (what was there
+ * is not read), 1 adds to them (over layers, or steps), anything between lets old weight fade.
+ * d_mass       : float32, the masses of request r at d_mass + r * mass_stride. A request whose
+ *                ctx_len is above mass_stride sets KAMERA_DEVICE_BAD_ITEM and keeps its masses, as
+ *                do requests without new tokens and those that kamera_chunk_attention refuses.
+ *                Entries from ctx_len on are left as they were.
+ * decay        : finite, 0 or more.
+ * d_workspace  : kamera_attention_mass_workspace(handle, num_tokens, num_reqs, num_q_heads) bytes,
+ *                16-byte aligned; contents ignored and left undefined. It serves one call at a
+ *                time, as that of the page calls.
+ * Products, weights and sums in float32, added in an order that the arguments fix. A token of a
+ * page outside the pool sets KAMERA_DEVICE_SLOT_OOB and is laid nothing on (only its mass fades).
+ * A row with lse = -inf (a token that saw nothing) lays nothing on any token. Limits as in
+ * kamera_chunk_attention.
+ */
+size_t kamera_attention_mass_workspace(const kamera_handle *handle, int32_t num_tokens,
+                                       int32_t num_reqs, int32_t num_q_heads);
+
+kamera_status kamera_attention_mass(const kamera_handle *handle, const kamera_pool *pool,
+                                    int32_t layer, const void *d_q, int64_t q_stride,
+                                    int32_t num_tokens, int32_t num_q_heads,
+                                    const int32_t *d_token_start, const int32_t *d_ctx_len,
+                                    int32_t num_reqs, int32_t window, float scale,
+                                    const float *d_lse, float decay, float *d_mass,
+                                    int64_t mass_stride, void *d_workspace,
+                                    size_t workspace_bytes, uint32_t *d_status,
+                                    kamera_stream_t stream);
+
+/*
+ * Eviction by mass (App. E: the window as an editable state; here the edit is chosen by what
+ * attention has looked at). Of tokens [0, num_tokens) of an item's request `keep` stay: the first
+ * `first`, the last `last`, and of the others those with the greatest mass, the lowest tokens where
+ * masses are equal. They keep their order and their keys' rotation: the j-th that stays moves to
+ * logical token j, in every layer, K and V, and its mass to mass[r][j]; masses [keep, num_tokens)
+ * become 0. With keep >= num_tokens nothing moves. The pages of tokens [keep, num_tokens) still
+ * belong to the request: kamera_free releases them.
+ * d_items : device array, 4-byte aligned; at most 65535. No request is named twice.
+ * d_refs  : the pages' counts (as for the page calls), only read.
+ * d_mass  : float32, the masses of page-table row r at d_mass + r * mass_stride. NaN counts as
+ *           greater than every number.
+ * d_kept  : int32: the tokens of item i that stayed, in order, at d_kept + i * kept_stride, for a
+ *           caller's own arrays (positions, token ids). What lies behind them is left as it was.
+ * d_workspace: kamera_evict_workspace(handle, num_items) bytes, 16-byte aligned; contents ignored
+ *           and left undefined. It serves one call at a time, as that of the page calls.
+ * An item sets KAMERA_DEVICE_BAD_ITEM and nothing of it is done where a number is out of range
+ * (req; num_tokens above pt_stride * page_size or mass_stride; first + last above keep; more tokens
+ * stay than kept_stride), or where a page that would be written is held more than once (a prefix
+ * shared by kamera_fork may stay as it is, but not be drawn together). An entry outside the pool
+ * below num_tokens sets KAMERA_DEVICE_SLOT_OOB and nothing of the item is done, unless all its
+ * tokens stay.
+ */
+typedef struct kamera_evict_item {
+  int32_t req;
+  int32_t num_tokens;
+  int32_t keep;
+  int32_t first;
+  int32_t last;
+} kamera_evict_item;
+
+size_t kamera_evict_workspace(const kamera_handle *handle, int32_t num_items);
+
+kamera_status kamera_evict(const kamera_handle *handle, const kamera_pool *pool,
+                           const kamera_evict_item *d_items, int32_t num_items,
+                           const int32_t *d_refs, float *d_mass, int64_t mass_stride,
+                           int32_t *d_kept, int64_t kept_stride, void *d_workspace,
+                           size_t workspace_bytes, uint32_t *d_status, kamera_stream_t stream);
+
+/*
  * Patch forming (§3 "Forming and applying the patch"; App. A "form_patch"): for each of
  * num_problems deficits Delta = KV(B|A) - R(delta)KV(B|empty), one (layer, group) each, the
  * top-m factors U*Sigma [T x m] and V_m^T [m x W] in the patch store's bf16 format. The

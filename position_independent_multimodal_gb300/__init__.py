@@ -18,7 +18,8 @@ from ._binding import (  # noqa: F401
     kamera_form_patch, kamera_form_patch_static_scratch, kamera_form_patch_workspace,
     kamera_decode_attention, kamera_decode_attention_workspace, kamera_patch_inplace,
     kamera_reanchor, pack_anchor_items, kamera_relocate,
-    kamera_chunk_attention, kamera_chunk_attention_workspace,
+    kamera_attention_mass, kamera_attention_mass_workspace, kamera_chunk_attention,
+    kamera_chunk_attention_workspace, kamera_evict, kamera_evict_workspace,
     kamera_append, kamera_compact, kamera_copy_pages, kamera_extend, kamera_fork, kamera_free,
     kamera_page_workspace, kamera_prefix_attention, kamera_prefix_attention_workspace,
     kamera_reuse, kamera_rope_phases, lib, make_item, make_layout,

@@ -151,9 +151,17 @@ def lib() -> ctypes.CDLL:
         L.kamera_chunk_attention_workspace.restype = st
         L.kamera_chunk_attention.argtypes = [vp, pp, i32, vp, i64, i32, i32, vp, vp, i32, i32,
                                              ctypes.c_float, vp, vp, vp, st, vp, vp]
+        L.kamera_attention_mass_workspace.argtypes = [vp, i32, i32, i32]
+        L.kamera_attention_mass_workspace.restype = st
+        L.kamera_attention_mass.argtypes = [vp, pp, i32, vp, i64, i32, i32, vp, vp, i32, i32,
+                                            ctypes.c_float, vp, ctypes.c_float, vp, i64, vp, st,
+                                            vp, vp]
+        L.kamera_evict_workspace.argtypes = [vp, i32]
+        L.kamera_evict_workspace.restype = st
+        L.kamera_evict.argtypes = [vp, pp, vp, i32, vp, vp, i64, vp, i64, vp, st, vp, vp]
         for f in ("kamera_append", "kamera_fork", "kamera_extend", "kamera_free",
                   "kamera_compact", "kamera_copy_pages", "kamera_prefix_attention",
-                  "kamera_chunk_attention"):
+                  "kamera_chunk_attention", "kamera_attention_mass", "kamera_evict"):
             getattr(L, f).restype = ctypes.c_int
         for f in ("kamera_create", "kamera_destroy", "kamera_relocate", "kamera_reuse",
                   "kamera_set_option", "kamera_set_batch_workspace",
@@ -643,6 +651,61 @@ def kamera_chunk_attention(handle: Handle, pool: Pool, layer: int, q: torch.Tens
         _need("out", out, _BF16, dev), _need("lse", lse, torch.float32, dev),
         *_bytes(workspace, dev), _need("status", status, _I32, dev),
         _stream_on(stream, dev)), "kamera_chunk_attention")
+
+
+def kamera_attention_mass_workspace(handle: Handle, num_tokens: int, num_reqs: int,
+                                    num_q_heads: int) -> int:
+    """Bytes of workspace for kamera_attention_mass of up to num_tokens tokens of num_reqs
+    requests."""
+    return int(lib().kamera_attention_mass_workspace(handle.ptr, int(num_tokens), int(num_reqs),
+                                                     int(num_q_heads)))
+
+
+def kamera_attention_mass(handle: Handle, pool: Pool, layer: int, q: torch.Tensor,
+                          token_start: torch.Tensor, ctx_len: torch.Tensor, scale: float,
+                          lse: torch.Tensor, decay: float, mass: torch.Tensor,
+                          workspace: torch.Tensor, status: torch.Tensor, window: int = 0,
+                          stream=None) -> None:
+    """Softmax weights of the new tokens of a batch (as for kamera_chunk_attention, with the
+    ``lse`` float32 [T][H_q] that it left) summed over query heads and new tokens, for each cached
+    token: ``mass`` float32 [R][columns] becomes ``decay * mass`` plus the sums."""
+    p, dev = _pool_c(handle, pool)
+    batch = _chunk(handle, dev, q, token_start, ctx_len)
+    if lse.shape != batch[2:4]:
+        raise ValueError("lse [T][H_q] is wanted")
+    if mass.dim() != 2 or mass.shape[0] != batch[-1]:
+        raise ValueError("mass must be [R][columns]")
+    _check(lib().kamera_attention_mass(
+        handle.ptr, ctypes.byref(p), layer, *batch, window, scale,
+        _need("lse", lse, torch.float32, dev), decay, _need("mass", mass, torch.float32, dev),
+        mass.shape[1],
+        *_bytes(workspace, dev), _need("status", status, _I32, dev),
+        _stream_on(stream, dev)), "kamera_attention_mass")
+
+
+def kamera_evict_workspace(handle: Handle, num_items: int) -> int:
+    """Bytes of workspace for kamera_evict of up to num_items items."""
+    return int(lib().kamera_evict_workspace(handle.ptr, int(num_items)))
+
+
+def kamera_evict(handle: Handle, pool: Pool, items: torch.Tensor, refs: torch.Tensor,
+                 mass: torch.Tensor, kept: torch.Tensor, workspace: torch.Tensor,
+                 status: torch.Tensor, stream=None) -> None:
+    """``items`` int32 [n][5] on the device: (req, num_tokens, keep, first, last). Of each
+    request's tokens ``keep`` stay, by ``mass`` float32 [num_reqs][columns]; which ones goes to
+    ``kept`` int32 [n][columns]."""
+    p, dev = _pool_c(handle, pool)
+    if items.dim() != 2 or items.shape[1] != 5:
+        raise ValueError("items must be [n][5]")
+    n = items.shape[0]
+    if mass.dim() != 2 or mass.shape[0] != pool.page_table.shape[0] or kept.dim() != 2 or \
+            kept.shape[0] != n:
+        raise ValueError("mass [num_reqs][columns] and kept [n][columns] are wanted")
+    _check(lib().kamera_evict(
+        handle.ptr, ctypes.byref(p), _need("items", items, _I32, dev), n,
+        _refs(pool, handle, refs, dev), _need("mass", mass, torch.float32, dev), mass.shape[1],
+        _need("kept", kept, _I32, dev), kept.shape[1], *_bytes(workspace, dev),
+        _need("status", status, _I32, dev), _stream_on(stream, dev)), "kamera_evict")
 
 
 def kamera_rope_phases(handle: Handle, d_deltas: torch.Tensor, d_out: torch.Tensor,

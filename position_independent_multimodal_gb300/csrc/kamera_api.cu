@@ -841,6 +841,8 @@ kamera_status chunk_args(const kamera_handle *h, const kamera_pool *pool, int32_
   a->page_shift = -1;
   for (int s = 0; s < 31; ++s)
     if (l.page_size == 1 << s) a->page_shift = s;
+  const long long most = (long long)a->pool.pt_stride * l.page_size;
+  a->max_ctx = most < 0x7FFFFFFF ? (int)most : 0x7FFFFFFF;
   a->window = window;
   a->scale = scale;
   a->status = d_status;
@@ -875,11 +877,85 @@ kamera_status kamera_chunk_attention(const kamera_handle *h, const kamera_pool *
       workspace_bytes < kamera::chunk_workspace(h->lay))
     return KAMERA_ERR_INVALID_ARG;
   a.shape = kamera::chunk_shape(h->lay);
-  kamera::chunk_blocks(&a);
+  kamera::chunk_blocks(&a, a.shape.rb);
   a.ws = d_workspace;
   a.out = static_cast<__nv_bfloat16 *>(d_out);
   a.lse = d_lse;
   return from_cuda(kamera::launch_chunk_attention(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t kamera_attention_mass_workspace(const kamera_handle *h, int32_t num_tokens,
+                                       int32_t num_reqs, int32_t num_q_heads) {
+  if (!h || num_tokens < 0 || num_reqs < 0 || num_q_heads < 0) return 0;
+  return kamera::mass_workspace(h->lay);
+}
+
+kamera_status kamera_attention_mass(const kamera_handle *h, const kamera_pool *pool, int32_t layer,
+                                    const void *d_q, int64_t q_stride, int32_t num_tokens,
+                                    int32_t num_q_heads, const int32_t *d_token_start,
+                                    const int32_t *d_ctx_len, int32_t num_reqs, int32_t window,
+                                    float scale, const float *d_lse, float decay, float *d_mass,
+                                    int64_t mass_stride, void *d_workspace, size_t workspace_bytes,
+                                    uint32_t *d_status, kamera_stream_t stream) {
+  kamera::MassArgs a;
+  std::memset(&a, 0, sizeof(a));
+  kamera_status st = chunk_args(h, pool, layer, d_q, q_stride, num_tokens, num_q_heads,
+                                d_token_start, d_ctx_len, num_reqs, window, scale, d_status, &a.b);
+  if (st != KAMERA_OK) return st;
+  if (!std::isfinite(decay) || decay < 0.f || mass_stride < 1) return KAMERA_ERR_INVALID_ARG;
+  if (num_tokens == 0 || num_reqs == 0) return KAMERA_OK;
+  auto mis = [](const void *p, uintptr_t al) {
+    return !p || (reinterpret_cast<uintptr_t>(p) & (al - 1));
+  };
+  if (mis(d_lse, 4) || mis(d_mass, 4) || mis(d_workspace, 16) ||
+      workspace_bytes < kamera::mass_workspace(h->lay))
+    return KAMERA_ERR_INVALID_ARG;
+  a.b.max_ctx = mass_stride < a.b.max_ctx ? static_cast<int>(mass_stride) : a.b.max_ctx;
+  a.shape = kamera::mass_shape(h->lay);
+  kamera::chunk_blocks(&a.b, a.shape.qr);
+  a.lse = d_lse;
+  a.decay = decay;
+  a.mass = d_mass;
+  a.mass_stride = mass_stride;
+  a.ws = d_workspace;
+  return from_cuda(kamera::launch_attention_mass(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t kamera_evict_workspace(const kamera_handle *h, int32_t num_items) {
+  if (!h || num_items < 0) return 0;
+  return kamera::evict_workspace(num_items);
+}
+
+kamera_status kamera_evict(const kamera_handle *h, const kamera_pool *pool,
+                           const kamera_evict_item *d_items, int32_t num_items,
+                           const int32_t *d_refs, float *d_mass, int64_t mass_stride,
+                           int32_t *d_kept, int64_t kept_stride, void *d_workspace,
+                           size_t workspace_bytes, uint32_t *d_status, kamera_stream_t stream) {
+  if (!h || !d_status) return KAMERA_ERR_INVALID_ARG;
+  kamera::EvictArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.lay = h->lay;
+  const kamera_status st = check_pool(h->lay, pool, &a.pool);
+  if (st != KAMERA_OK) return st;
+  if (num_items < 0 || mass_stride < 1 || kept_stride < 1) return KAMERA_ERR_INVALID_ARG;
+  if (num_items > 65535) return KAMERA_ERR_UNSUPPORTED;
+  if (num_items == 0) return KAMERA_OK;
+  auto mis = [](const void *p, uintptr_t al) {
+    return !p || (reinterpret_cast<uintptr_t>(p) & (al - 1));
+  };
+  if (mis(d_items, 4) || mis(d_refs, 4) || mis(d_mass, 4) || mis(d_kept, 4) ||
+      mis(d_workspace, 16) || workspace_bytes < kamera::evict_workspace(num_items))
+    return KAMERA_ERR_INVALID_ARG;
+  a.items = d_items;
+  a.n = num_items;
+  a.refs = d_refs;
+  a.mass = d_mass;
+  a.mass_stride = mass_stride;
+  a.kept = d_kept;
+  a.kept_stride = kept_stride;
+  a.ws = d_workspace;
+  a.status = d_status;
+  return from_cuda(kamera::launch_evict(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 kamera_status kamera_rope_phases(const kamera_handle *h, const int64_t *d_deltas,

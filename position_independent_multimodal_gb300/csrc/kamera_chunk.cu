@@ -381,9 +381,9 @@ ChunkShape chunk_shape(const DevLayout &l) {
   return {kRows, kTileSh, (dv + kCols - 1) / kCols, kCols, kSms};
 }
 
-void chunk_blocks(ChunkArgs *a) {
-  a->pieces = (a->hpk + a->shape.rb - 1) / a->shape.rb;
-  a->tb = a->hpk > a->shape.rb ? 1 : a->shape.rb / a->hpk;
+void chunk_blocks(ChunkArgs *a, int rows) {
+  a->pieces = (a->hpk + rows - 1) / rows;
+  a->tb = a->hpk > rows ? 1 : rows / a->hpk;
 }
 
 size_t chunk_workspace(const DevLayout &l) { return chunk_places(chunk_shape(l), nullptr).total; }

@@ -56,27 +56,22 @@ __host__ __device__ inline ChunkPlaces chunk_places(const ChunkShape &s, void *w
   return p;
 }
 
-// Sum over i < n of floor((a i + b) / 2^sh), by Euclid's steps on (2^sh, a); a n + b < 2^32.
-__device__ __forceinline__ long long floor_sum(unsigned n, int sh, unsigned a, unsigned b) {
-  if (n == 0) return 0;
-  unsigned m = 1u << sh;
-  long long sum = (long long)(n & 1 ? (n - 1) / 2 : n / 2) * (n & 1 ? n : n - 1) * (a >> sh) +
-                  (long long)n * (b >> sh);
-  a &= m - 1;
-  b &= m - 1;
-  while (true) {
-    const unsigned y = a * n + b;
-    if (y < m) return sum;
-    n = y / m;
-    b = y % m;
-    const unsigned t = a;
-    a = m;
-    m = t;
+// Sum over i < n of floor((a i + b) / m), by Euclid's steps on (m, a); a n + b < 2^32, m > 0.
+__device__ __forceinline__ long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
+  long long sum = 0;
+  while (n > 0) {
     sum += (long long)(n & 1 ? (n - 1) / 2 : n / 2) * (n & 1 ? n : n - 1) * (a / m) +
            (long long)n * (b / m);
     a %= m;
     b %= m;
+    const unsigned y = a * n + b;
+    n = y / m;
+    b = y - n * m;
+    const unsigned t = a;
+    a = m;
+    m = t;
   }
+  return sum;
 }
 
 // A request of the call.
@@ -96,7 +91,7 @@ __device__ __forceinline__ ChunkRequest chunk_request(const Args &a, int r, bool
   q.n = end - q.row;
   *bad_start = q.row < 0 || end < q.row || end > a.n_tokens;
   if (*bad_start) q.n = 0;
-  *bad_item = q.n > 0 && (q.ctx < q.n || q.ctx > (long long)a.pool.pt_stride * a.lay.page_size);
+  *bad_item = q.n > 0 && (q.ctx < q.n || q.ctx > a.max_ctx);
   if (*bad_item) q.n = 0;
   q.past = q.ctx - q.n;
   q.nb = ceil_div(q.n, a.tb);
@@ -112,18 +107,18 @@ __device__ __forceinline__ int first_seen(const Args &a, int tok) {
 // Tiles of a request's first j blocks.
 __device__ __forceinline__ long long chunk_tiles(const ChunkArgs &a, const ChunkRequest &q, int j) {
   const int sh = a.shape.tile_sh;
-  const unsigned up = (1u << sh) - 1u;
+  const unsigned m = 1u << sh, up = m - 1u;
   long long sum = 0;
   int whole = j;
   if (j == q.nb) {  // the last one may have fewer tokens
     --whole;
     sum += ((unsigned)q.ctx + up) >> sh;
   }
-  sum += floor_sum(whole, sh, a.tb, (unsigned)q.past + a.tb + up);
+  sum += floor_sum(whole, m, a.tb, (unsigned)q.past + a.tb + up);
   if (a.window > 0) {
     const int lead = a.window - 1 - q.past;  // blocks that start before it see from token 0 on
     const int i0 = lead > 0 ? ceil_div(lead, a.tb) : 0;
-    if (j > i0) sum -= floor_sum(j - i0, sh, a.tb, (unsigned)(q.past + i0 * a.tb - (a.window - 1)));
+    if (j > i0) sum -= floor_sum(j - i0, m, a.tb, (unsigned)(q.past + i0 * a.tb - (a.window - 1)));
   }
   return sum;
 }
@@ -144,13 +139,13 @@ struct ChunkScratch {
   int r;
 };
 
-template <int THR>
-__device__ __forceinline__ ChunkStart chunk_start(const ChunkArgs &a, int worker,
-                                                  ChunkScratch<THR> *sh) {
+// `units_of`: a request's units. `a`: the batch, `n`: workers.
+template <int THR, class Units>
+__device__ __forceinline__ ChunkStart units_start(const ChunkArgs &a, int n, int worker,
+                                                  ChunkScratch<THR> *sh, Units units_of) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.n_reqs + THR - 1) / THR;
   const int r0 = min(a.n_reqs, tid * per), r1 = min(a.n_reqs, r0 + per);
-  const long long heads = (long long)a.n_kv * a.pieces * a.shape.vh;
   bool bad = false, bad_item = false;
   long long mine = 0;
   for (int r = r0; r < r1; ++r) {
@@ -158,7 +153,7 @@ __device__ __forceinline__ ChunkStart chunk_start(const ChunkArgs &a, int worker
     const ChunkRequest q = chunk_request(a, r, &bs, &bi);
     bad |= bs;
     bad_item |= bi;
-    if (q.n) mine += heads * chunk_tiles(a, q, q.nb);
+    if (q.n) mine += units_of(q);
   }
   long long incl = mine;
   for (int o = 1; o < 32; o <<= 1) {
@@ -175,7 +170,6 @@ __device__ __forceinline__ ChunkStart chunk_start(const ChunkArgs &a, int worker
     total += sh->sums[i];
   }
   if (s.bad) total = 0;
-  const long long n = a.shape.n;
   s.quot = div_pos(total, n);
   s.rem = total - s.quot * n;
   const long long u0 = first_unit(s.quot, s.rem, worker);
@@ -186,7 +180,7 @@ __device__ __forceinline__ ChunkStart chunk_start(const ChunkArgs &a, int worker
     for (int r = r0; r < r1; ++r) {
       bool bs, bi;
       const ChunkRequest q = chunk_request(a, r, &bs, &bi);
-      const long long u = q.n ? heads * chunk_tiles(a, q, q.nb) : 0;
+      const long long u = q.n ? units_of(q) : 0;
       if (off < u) {
         sh->off = off;
         sh->r = r;
@@ -199,6 +193,14 @@ __device__ __forceinline__ ChunkStart chunk_start(const ChunkArgs &a, int worker
   s.off = sh->off;
   s.r = sh->r;
   return s;
+}
+
+template <int THR>
+__device__ __forceinline__ ChunkStart chunk_start(const ChunkArgs &a, int worker,
+                                                  ChunkScratch<THR> *sh) {
+  return units_start<THR>(a, a.shape.n, worker, sh, [&](const ChunkRequest &q) {
+    return (long long)a.n_kv * a.pieces * a.shape.vh * chunk_tiles(a, q, q.nb);
+  });
 }
 
 // A run of tiles of one block, as a worker takes it.

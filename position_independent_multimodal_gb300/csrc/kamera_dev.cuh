@@ -245,6 +245,7 @@ struct ChunkArgs {
   const int *token_start;   // [n_reqs + 1]
   const int *ctx_len;       // [n_reqs]
   int n_tokens, n_reqs, hq, n_kv, dk, dv;
+  int max_ctx;              // the longest context that is taken
   int hpk, pieces, tb;      // query heads of a KV head, pieces of at most rb of them, tokens a block
   unsigned hpk_magic;       // ceil(2^16 / hpk)
   int page_shift;           // log2 of the page size, -1 when that is no power of two
@@ -255,6 +256,36 @@ struct ChunkArgs {
   void *ws;
   __nv_bfloat16 *out;       // [n_tokens][hq][dv]
   float *lse;               // [n_tokens][hq]
+  unsigned *status;
+};
+
+// How a layout's attention masses are divided (kamera_mass.cuh).
+struct MassShape {
+  int kt, qr;           // tokens of a block, query rows of a tile
+  int n;                // workers
+};
+
+struct MassArgs {
+  ChunkArgs b;          // the batch; its pieces and tb are of `shape`
+  const float *lse;     // [n_tokens][hq]
+  float decay;
+  float *mass;          // [n_reqs] rows
+  long long mass_stride;
+  MassShape shape;
+  void *ws;
+};
+
+struct EvictArgs {
+  DevLayout lay;
+  DevPool pool;
+  const kamera_evict_item *items;
+  int n;                // items
+  const int *refs;      // [num_pages]
+  float *mass;          // [num_reqs] rows
+  long long mass_stride;
+  int *kept;            // [n] rows
+  long long kept_stride;
+  void *ws;
   unsigned *status;
 };
 
@@ -697,12 +728,20 @@ PrefixClass prefix_thin_class(const DevLayout &l);                  // kamera_pr
 cudaError_t prepare_prefix_thin(const DevLayout &l);
 cudaError_t launch_prefix_thin(const PrefixArgs &a, bool beside, cudaStream_t s);
 ChunkShape chunk_shape(const DevLayout &l);                         // kamera_chunk.cu
-void chunk_blocks(ChunkArgs *a);  // pieces and tb, of its shape and heads
+void chunk_blocks(ChunkArgs *a, int rows);  // pieces and tb, of blocks of that many rows
 size_t chunk_workspace(const DevLayout &l);
 cudaError_t launch_chunk_attention(const ChunkArgs &a, cudaStream_t s);
 ChunkShape chunk_tc_shape(const DevLayout &l);                      // kamera_chunk_tc.cu
 cudaError_t prepare_chunk_tc(const DevLayout &l);
 cudaError_t launch_chunk_tc(const ChunkArgs &a, cudaStream_t s);
+MassShape mass_shape(const DevLayout &l);                           // kamera_mass.cu
+size_t mass_workspace(const DevLayout &l);
+cudaError_t launch_attention_mass(const MassArgs &a, cudaStream_t s);
+MassShape mass_tc_shape(const DevLayout &l);                        // kamera_mass_tc.cu
+cudaError_t prepare_mass_tc(const DevLayout &l);
+cudaError_t launch_mass_tc(const MassArgs &a, cudaStream_t s);
+size_t evict_workspace(int n);                                      // kamera_evict.cu
+cudaError_t launch_evict(const EvictArgs &a, cudaStream_t s);
 cudaError_t launch_rope_phases(const FreqQ64 &f, int npairs, const long long *deltas, int n,
                                float *out, cudaStream_t s);
 
