@@ -372,11 +372,10 @@ __global__ void __launch_bounds__(kJoinThr) chunk_join_kernel(const __grid_const
       for (int i = first; i < s.ntok * s.heads; i += step) chunk_row_again(a, s, i);
 }
 
-bool chunk_tc_layout(const DevLayout &l) { return false; }
-
 }  // namespace
 
 ChunkShape chunk_shape(const DevLayout &l) {
+  if (chunk_tc_layout(l)) return chunk_tc_shape(l);
   const int dv = l.kind == KAMERA_GQA ? l.hd : l.latent;
   return {kRows, kTileSh, (dv + kCols - 1) / kCols, kCols, kSms};
 }
@@ -403,14 +402,19 @@ cudaError_t launch_chunk_attention(const ChunkArgs &args, cudaStream_t s) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!configured[dev][kind]) {
-      e = cudaFuncSetAttribute(chunk_gen_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               gen_plan(1024).total);
+      e = kind ? prepare_chunk_tc(a.lay)
+               : cudaFuncSetAttribute(chunk_gen_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      gen_plan(1024).total);
       if (e != cudaSuccess) return e;
       configured[dev][kind] = 1;
     }
   }
-  chunk_gen_kernel<<<a.shape.n, kThr, gen_plan(a.dk).total, s>>>(a);
-  e = cudaGetLastError();
+  if (kind) {
+    e = launch_chunk_tc(a, s);
+  } else {
+    chunk_gen_kernel<<<a.shape.n, kThr, gen_plan(a.dk).total, s>>>(a);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
   return launch_early(chunk_join_kernel, dim3(a.shape.n, kJoinY), kJoinThr, 0, s, a);
 }

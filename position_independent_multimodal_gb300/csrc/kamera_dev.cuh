@@ -731,7 +731,8 @@ ChunkShape chunk_shape(const DevLayout &l);                         // kamera_ch
 void chunk_blocks(ChunkArgs *a, int rows);  // pieces and tb, of blocks of that many rows
 size_t chunk_workspace(const DevLayout &l);
 cudaError_t launch_chunk_attention(const ChunkArgs &a, cudaStream_t s);
-ChunkShape chunk_tc_shape(const DevLayout &l);                      // kamera_chunk_tc.cu
+bool chunk_tc_layout(const DevLayout &l);                           // kamera_chunk_tc.cu
+ChunkShape chunk_tc_shape(const DevLayout &l);
 cudaError_t prepare_chunk_tc(const DevLayout &l);
 cudaError_t launch_chunk_tc(const ChunkArgs &a, cudaStream_t s);
 MassShape mass_shape(const DevLayout &l);                           // kamera_mass.cu

@@ -42,11 +42,10 @@
 //        41 us for 40 x 16 rows over two prefixes of 9003 tokens.
 // Layout: every operand tile is 128 rows of 128 bytes (64 elements), swizzled in 128-byte rows;
 // V is read MN-major, so its rows land unchanged too.
-#include <cuda.h>
-
 #include "kamera_prefix.cuh"
 #include "kamera_ptx.cuh"
 #include "kamera_smem.cuh"
+#include "kamera_tc.cuh"
 
 namespace kamera {
 
@@ -54,7 +53,6 @@ namespace {
 
 constexpr int kTokSh = 7, kTok = 1 << kTokSh;  // tokens per tile
 constexpr int kRow = 128;              // query rows per MMA
-constexpr int kChunk = kTok * 128;     // bytes of a 128 x 64 bf16 operand tile
 constexpr int kMasks = 8;              // tiles whose token masks are kept
 
 // DK, DV: 64-column chunks of K and of the CTA's V columns; QT: tiles of query rows; UC: chunks
@@ -101,37 +99,6 @@ struct Maps {
   int q_step;                 // 1: the rows of a block are consecutive rows of q
   int group_bytes, own_bytes; // of the query copies
 };
-
-template <int V>
-struct Int {
-  static constexpr int v = V;
-};
-
-// A place in the ring of N stages and the parity of its phase.
-template <int N>
-struct Place {
-  uint32_t st = 0, ph = 0;
-  __device__ __forceinline__ void advance(int n) {
-    st += n;
-    while (st >= (uint32_t)N) {
-      st -= N;
-      ph ^= 1;
-    }
-  }
-};
-
-// Halves of the matrix descriptors of 128-byte swizzled operands, whose eight rows of 128 bytes
-// make a group of 1024 bytes (the stride offset): the start address and leading offset, to which the
-// steps inside a tile are added, and the constant rest. MN-major, 64 elements along M or N make a
-// row, and the leading offset is that of the next 64.
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t desc_k(uint32_t addr) { return (addr >> 4) | (1u << 16); }
-__device__ __forceinline__ uint32_t desc_mn(uint32_t addr) {
-  return (addr >> 4) | (uint32_t)(kChunk >> 4) << 16;
-}
-__device__ __forceinline__ uint64_t desc(uint32_t lo) {
-  return (uint64_t)kDescHi << 32 | lo;
-}
 
 template <class S>
 __global__ void __launch_bounds__(S::kThr, 1) prefix_tc_kernel(
@@ -721,35 +688,6 @@ cudaError_t configure() {
   if (S::kShift && at.numRegs * S::kThr < S::kRegs) return cudaErrorLaunchOutOfResources;
   return cudaFuncSetAttribute(prefix_tc_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               S::total);
-}
-
-typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                             const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                             const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn() {
-  static const EncodeFn fn = [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeFn>(p);
-  }();
-  return fn;
-}
-
-// bf16 [n2][n1][n0] (row strides in elements), boxes of 64 x b1 x b2, 128-byte swizzle.
-bool encode(CUtensorMap *m, const void *base, int rank, uint64_t n0, uint64_t n1, uint64_t n2,
-            uint64_t s1, uint64_t s2, uint32_t b1, uint32_t b2) {
-  const cuuint64_t dims[3] = {n0, n1, n2}, strides[2] = {2 * s1, 2 * s2};
-  const cuuint32_t box[3] = {64, b1, b2}, step[3] = {1, 1, 1};
-  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims,
-                     strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <class S>
