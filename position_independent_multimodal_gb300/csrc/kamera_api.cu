@@ -842,7 +842,7 @@ kamera_status chunk_args(const kamera_handle *h, const kamera_pool *pool, int32_
   for (int s = 0; s < 31; ++s)
     if (l.page_size == 1 << s) a->page_shift = s;
   const long long most = (long long)a->pool.pt_stride * l.page_size;
-  a->max_ctx = most < 0x7FFFFFFF ? (int)most : 0x7FFFFFFF;
+  a->max_ctx = most < 0x7FFFFF00 ? (int)most : 0x7FFFFF00;  // (a tile's end is an int)
   a->window = window;
   a->scale = scale;
   a->status = d_status;

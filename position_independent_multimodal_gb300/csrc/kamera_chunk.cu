@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kThr) chunk_gen_kernel(const __grid_constant__
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ ChunkScratch<kThr> found;
   __shared__ uint32_t valid;  // tokens of the tile that have a slot
-  __shared__ int slots[kTile], odd;
+  __shared__ int slots[kTile];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, w = blockIdx.x;
   const DevLayout &lay = a.lay;
   const GenPlan pl = gen_plan(a.dk);
@@ -57,15 +57,14 @@ __global__ void __launch_bounds__(kThr) chunk_gen_kernel(const __grid_constant__
   ChunkWalk walk;
   walk.start(a, st, w);
   ChunkSegment s = {};
-  int segments = 0, odd0 = 0x7FFFFFFF, odd1 = -1;
-  bool carry = false;
+  int segments = 0;
+  bool odd = false;
   for (; walk.next(a, &s); ++segments) {
-    if (segments == 0) carry = s.carry;
     const int rows = s.ntok * s.heads;
     const int kcol = gqa ? s.kvh * lay.hd : 0, vcol = kcol + s.part * kCols;
     const int cols = min(kCols, a.dv - s.part * kCols);
     __syncthreads();
-    if (tid == 0) odd = 0;
+    odd |= !s.carry() && chunk_odd(a, s, tid, kThr);
     const int qp = a.dk >> 3;  // 16-byte pieces of a row
     for (int e = tid; e < kRows * qp; e += kThr) {
       const int i = e / qp, p = e - i * qp;
@@ -85,9 +84,7 @@ __global__ void __launch_bounds__(kThr) chunk_gen_kernel(const __grid_constant__
       see1[y] = s.first + k + 1;
       see0[y] = first_seen(a, s.first + k);
     }
-    const int lo = first_seen(a, s.first);                      // first token that a row sees
-    const int all0 = first_seen(a, s.first + s.ntok - 1);       // tokens that all rows see
-    const int all1 = s.first + 1;
+    const int lo = first_seen(a, s.first);  // first token that a row sees
     float m[2] = {neg_inf, neg_inf}, l[2] = {0.f, 0.f};
     float o[kCols / 8][4];
 #pragma unroll
@@ -120,16 +117,6 @@ __global__ void __launch_bounds__(kThr) chunk_gen_kernel(const __grid_constant__
       }
       ptx::cp_async_commit();
       ptx::cp_async_wait_all();
-      const bool edge = tok0 < all0 || tok0 + kTile > all1;
-      if (edge) {  // this thread's own copies
-        bool bad = false;
-        for (int e = tid; e < kTile * vp; e += kThr) {
-          const int i = e / vp, p = e - i * vp;
-          const bool part = tok0 + i < all0 || tok0 + i >= all1;
-          bad |= part && odd8(*reinterpret_cast<const uint4 *>(smem + pl.v + i * pl.vpitch + 16 * p));
-        }
-        if (bad) odd = 1;
-      }
       __syncthreads();
       float x[kTile / 8][4];
 #pragma unroll
@@ -205,7 +192,7 @@ __global__ void __launch_bounds__(kThr) chunk_gen_kernel(const __grid_constant__
       const float inv = l[y] == 0.f ? 0.f : 1.f / l[y];
       const float z = l[y] == 0.f ? neg_inf : (m[y] + log2f(l[y])) * kLn2;
       const long long rh = (long long)(s.row + k) * a.hq + h;
-      const long long place = (long long)(2 * w + (s.carry ? 0 : 1)) * kRows + i;
+      const long long place = (long long)(2 * w + (s.carry() ? 0 : 1)) * kRows + i;
       const bool whole = chunk_whole(s);
 #pragma unroll
       for (int n = 0; n < kCols / 8; ++n) {
@@ -224,13 +211,9 @@ __global__ void __launch_bounds__(kThr) chunk_gen_kernel(const __grid_constant__
           a.lse[rh] = z;
       }
     }
-    __syncthreads();
-    if (odd) {
-      odd0 = min(odd0, segments);
-      odd1 = segments;
-    }
   }
-  if (tid == 0) chunk_note(places.rec + w, s, segments, carry, false, odd0, odd1);
+  odd = __syncthreads_or(odd);
+  if (tid == 0) chunk_note(places.rec + w, s, segments, false, odd);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -291,7 +274,8 @@ __device__ __noinline__ void chunk_row_again(const ChunkArgs &a, const ChunkSegm
 }
 
 // Worker blockIdx.x's cut block: a warp to a row, the parts' log-sum-exps a lane each, then four
-// columns a lane. Then the blocks that it noted to be taken again.
+// columns a lane. Then, where a worker has found odd values, those of the blocks that the worker
+// starts which multiply such a value for a row that does not see it.
 __global__ void __launch_bounds__(kJoinThr) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
   __shared__ ChunkScratch<kJoinThr> found;
   const int w = blockIdx.x, lane = threadIdx.x & 31;
@@ -301,14 +285,15 @@ __global__ void __launch_bounds__(kJoinThr) chunk_join_kernel(const __grid_const
   const float neg_inf = -__int_as_float(0x7f800000);
   ptx::wait_for_previous();
   const ChunkRecord rec = places.rec[w];
-  bool again = rec.odd0 <= rec.odd1;
-  if (rec.head && !rec.gave_up && !(again && rec.odd1 == rec.segments - 1)) {
+  int odd = 0;
+  for (int i = threadIdx.x; i < a.shape.n; i += kJoinThr) odd |= places.rec[i].odd;
+  odd = __syncthreads_or(odd);
+  if (rec.head && !rec.gave_up) {
     const int rb = a.shape.rb, vw = a.shape.vw, np = 1 + rec.more;
     const int cols = min(vw, a.dv - rec.part * vw);
     bool skip = false;
     for (int i = lane; i < rec.more; i += 32) {
-      const ChunkRecord &f = places.rec[w + 1 + i];
-      skip |= f.gave_up || (f.odd0 == 0 && f.odd1 >= 0);
+      skip |= places.rec[w + 1 + i].gave_up;
     }
     if (!__any_sync(0xffffffffu, skip)) {
       auto place = [&](int p) { return (long long)(2 * (w + p) + (p == 0)) * rb; };
@@ -362,14 +347,22 @@ __global__ void __launch_bounds__(kJoinThr) chunk_join_kernel(const __grid_const
       }
     }
   }
-  if (!again || rec.gave_up) return;
+  if (!odd || rec.gave_up) return;
   const ChunkStart st = chunk_start<kJoinThr>(a, w, &found);
   ChunkWalk walk;
   walk.start(a, st, w);
   ChunkSegment s;
-  for (int n = 0; n <= rec.odd1 && walk.next(a, &s); ++n)
-    if (n >= rec.odd0)
+  while (walk.next(a, &s)) {
+    // tokens that are multiplied for rows that do not see them: from the first tile's start to the
+    // last one's end
+    const int end = (int)min((long long)s.ctx, ((long long)((s.first + s.ntok - 1) >> a.shape.tile_sh) + 1)
+                                                   << a.shape.tile_sh);
+    ChunkSegment wide = s;
+    wide.ntok = end - s.first;
+    const bool again = !s.carry() && chunk_odd(a, wide, threadIdx.x, kJoinThr);
+    if (__syncthreads_or(again))
       for (int i = first; i < s.ntok * s.heads; i += step) chunk_row_again(a, s, i);
+  }
 }
 
 }  // namespace

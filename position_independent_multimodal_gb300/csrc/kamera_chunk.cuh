@@ -27,9 +27,8 @@ struct ChunkRecord {
   int h0, part;    // of it: first query head, part of V's columns
   int gave_up;
   int segments;    // segments of the worker
-  int carry;       // 1: the first of them starts inside its block
-  int odd0, odd1;  // first and last of them that ChunkOdd says must be taken again (odd0 > odd1: none)
-  int pad[5];
+  int odd;         // 1: chunk_odd holds for a block that starts with it
+  int pad[7];
 };
 
 struct ChunkPlaces {
@@ -208,10 +207,12 @@ struct ChunkSegment {
   int r;               // the request
   int row, ntok;       // row of q of the block's first token, its tokens
   int first, ctx;      // that token's place in the context, the context
-  int kvh, h0, heads;  // KV head, first query head, query heads of each token
-  int part;            // part of V's columns
+  int h0, heads;       // first query head, query heads of each token
+  int kvh, part;       // KV head, part of V's columns
   int t0, t1;          // tiles
-  int carry, more;     // starts inside its block; its first part: workers that follow on the block
+  int more;            // -1: starts inside its block; else workers that follow on the block
+
+  __device__ __forceinline__ bool carry() const { return more < 0; }
 };
 
 // Walks a worker's segments; by whole warps.
@@ -269,8 +270,7 @@ struct ChunkWalk {
     const int nt = b1 - b0 - t, take = (int)(left < nt ? left : nt);
     s->t0 = b0 + t;
     s->t1 = s->t0 + take;
-    s->carry = t > 0;
-    s->more = t == 0 && take < nt ? workers_for(quot, rem, worker + 1, nt - take) : 0;
+    s->more = t > 0 ? -1 : take < nt ? workers_for(quot, rem, worker + 1, nt - take) : 0;
     left -= take;
     t = 0;
     if (++j == q.nb) {
@@ -290,13 +290,48 @@ __device__ __forceinline__ void chunk_row(const ChunkArgs &a, const ChunkSegment
 }
 
 // Whether a block's output goes straight to the caller's tensors.
-__device__ __forceinline__ bool chunk_whole(const ChunkSegment &s) { return !s.carry && !s.more; }
+__device__ __forceinline__ bool chunk_whole(const ChunkSegment &s) { return s.more == 0; }
 
-// The record of a worker. `odd`: segments [odd0, odd1] hold values of V that are not finite in
-// tokens that not all rows of a block see: times a weight of 0 they would not vanish, so the join
-// kernel takes those blocks again, token by token.
+// A bf16 pair with a value that is not finite.
+__device__ __forceinline__ bool odd_pair(uint32_t w) {
+  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+__device__ __forceinline__ bool odd8(const uint4 &v) {
+  return odd_pair(v.x) | odd_pair(v.y) | odd_pair(v.z) | odd_pair(v.w);
+}
+
+// Whether V of tokens that some of the block's rows do not see holds a value that is not finite: of
+// its own new tokens, and of those that the window leaves behind between its first row and its last.
+// Every token that is multiplied for a row which does not see it is such a one of some block. By
+// `threads` threads, each its share.
+__device__ __forceinline__ bool chunk_odd(const ChunkArgs &a, const ChunkSegment &s, int thread,
+                                          int threads) {
+  if (s.ntok == 1 && s.first + 1 == s.ctx) return false;  // the request has no other new tokens behind
+  const DevLayout &lay = a.lay;
+  const bool gqa = lay.kind == KAMERA_GQA;
+  const int row = gqa ? lay.row_v : lay.row_k;
+  const __nv_bfloat16 *v = (gqa ? a.pool.v : a.pool.k) +
+                           (long long)a.layer * a.pool.num_slots * row + (gqa ? s.kvh * lay.hd : 0) +
+                           s.part * a.shape.vw;
+  const int pieces = min(a.shape.vw, a.dv - s.part * a.shape.vw) >> 3;  // of 16 bytes
+  bool odd = false;
+  for (int side = 0; side < 2; ++side) {
+    const int from = side ? first_seen(a, s.first) : s.first;
+    const int to = side ? first_seen(a, s.first + s.ntok - 1) : s.first + s.ntok;
+#pragma unroll 8
+    for (int e = thread; e < (to - from) * pieces; e += threads) {
+      const int tok = from + e / pieces, page = load_page(a, s.r, tok);
+      if (page < 0 || ((long long)page + 1) * lay.page_size > a.pool.num_slots) continue;
+      const int slot = page * lay.page_size + tok - page_index(a, tok) * lay.page_size;
+      odd |= odd8(__ldg(reinterpret_cast<const uint4 *>(v + (long long)slot * row) + e % pieces));
+    }
+  }
+  return odd;
+}
+
+// The record of a worker.
 __device__ __forceinline__ void chunk_note(ChunkRecord *rec, const ChunkSegment &last, int segments,
-                                           bool carry, bool gave_up, int odd0, int odd1) {
+                                           bool gave_up, bool odd) {
   ChunkRecord c;
   c.head = segments > 0 && last.more > 0;
   c.more = last.more;
@@ -306,18 +341,8 @@ __device__ __forceinline__ void chunk_note(ChunkRecord *rec, const ChunkSegment 
   c.part = last.part;
   c.gave_up = gave_up;
   c.segments = segments;
-  c.carry = carry;
-  c.odd0 = odd0;
-  c.odd1 = odd1;
+  c.odd = odd;
   *rec = c;
-}
-
-// A bf16 pair with a value that is not finite.
-__device__ __forceinline__ bool odd_pair(uint32_t w) {
-  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-}
-__device__ __forceinline__ bool odd8(const uint4 &v) {
-  return odd_pair(v.x) | odd_pair(v.y) | odd_pair(v.z) | odd_pair(v.w);
 }
 
 }  // namespace kamera
