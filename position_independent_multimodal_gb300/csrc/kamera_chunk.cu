@@ -7,6 +7,7 @@
 // at most 128 of V's columns a worker (wider V in parts, each with its own S). Widths are any
 // multiple of 16, up to 1024. Sums and maxima are float32; P is rounded to bf16 for the product with
 // V, as in the other kernels of this kind, and l takes the unrounded weights.
+#include <algorithm>
 #include <mutex>
 
 #include "kamera_chunk.cuh"
@@ -64,7 +65,7 @@ __global__ void __launch_bounds__(kThr) chunk_gen_kernel(const __grid_constant__
     const int kcol = gqa ? s.kvh * lay.hd : 0, vcol = kcol + s.part * kCols;
     const int cols = min(kCols, a.dv - s.part * kCols);
     __syncthreads();
-    odd |= !s.carry() && chunk_odd(a, s, tid, kThr);
+    odd |= !s.carry() && chunk_odd(a, s, warp, kThr / 32);
     const int qp = a.dk >> 3;  // 16-byte pieces of a row
     for (int e = tid; e < kRows * qp; e += kThr) {
       const int i = e / qp, p = e - i * qp;
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kThr) chunk_gen_kernel(const __grid_constant__
 // join
 // ---------------------------------------------------------------------------------------
 
-constexpr int kJoinThr = 256, kJoinY = 4;
+constexpr int kJoinThr = 256;
 
 // One row of a block from its definition, token by token, by a warp: nothing that the row does not
 // see is read. For blocks with values of V that are not finite in such places.
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(kJoinThr) chunk_join_kernel(const __grid_const
   __shared__ ChunkScratch<kJoinThr> found;
   const int w = blockIdx.x, lane = threadIdx.x & 31;
   const int first = blockIdx.y * (kJoinThr / 32) + (threadIdx.x >> 5);
-  constexpr int step = kJoinY * (kJoinThr / 32);
+  const int step = gridDim.y * (kJoinThr / 32);
   const ChunkPlaces places = chunk_places(a.shape, a.ws);
   const float neg_inf = -__int_as_float(0x7f800000);
   ptx::wait_for_previous();
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(kJoinThr) chunk_join_kernel(const __grid_const
                                                    << a.shape.tile_sh);
     ChunkSegment wide = s;
     wide.ntok = end - s.first;
-    const bool again = !s.carry() && chunk_odd(a, wide, threadIdx.x, kJoinThr);
+    const bool again = !s.carry() && chunk_odd(a, wide, threadIdx.x >> 5, kJoinThr / 32);
     if (__syncthreads_or(again))
       for (int i = first; i < s.ntok * s.heads; i += step) chunk_row_again(a, s, i);
   }
@@ -409,7 +410,11 @@ cudaError_t launch_chunk_attention(const ChunkArgs &args, cudaStream_t s) {
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  return launch_early(chunk_join_kernel, dim3(a.shape.n, kJoinY), kJoinThr, 0, s, a);
+  // a warp to a row of a cut block
+  const long long rows = std::min<long long>(a.shape.rb, (long long)a.n_tokens * a.hpk);
+  const int per = kJoinThr / 32;
+  return launch_early(chunk_join_kernel, dim3(a.shape.n, (unsigned)((rows + per - 1) / per)), kJoinThr,
+                      0, s, a);
 }
 
 }  // namespace kamera

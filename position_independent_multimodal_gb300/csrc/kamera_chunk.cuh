@@ -303,27 +303,47 @@ __device__ __forceinline__ bool odd8(const uint4 &v) {
 // Whether V of tokens that some of the block's rows do not see holds a value that is not finite: of
 // its own new tokens, and of those that the window leaves behind between its first row and its last.
 // Every token that is multiplied for a row which does not see it is such a one of some block. By
-// `threads` threads, each its share.
-__device__ __forceinline__ bool chunk_odd(const ChunkArgs &a, const ChunkSegment &s, int thread,
-                                          int threads) {
-  if (s.ntok == 1 && s.first + 1 == s.ctx) return false;  // the request has no other new tokens behind
+// `warps` whole warps, each its share of 32 tokens at a time: a lane to a token's slot, then a lane to
+// 16 bytes.
+__device__ __forceinline__ bool chunk_odd(const ChunkArgs &a, const ChunkSegment &s, int warp,
+                                          int warps) {
+  if (s.ntok == 1 && s.first + 1 == s.ctx) return false;  // there are no other new tokens
   const DevLayout &lay = a.lay;
   const bool gqa = lay.kind == KAMERA_GQA;
+  const int lane = threadIdx.x & 31;
   const int row = gqa ? lay.row_v : lay.row_k;
   const __nv_bfloat16 *v = (gqa ? a.pool.v : a.pool.k) +
                            (long long)a.layer * a.pool.num_slots * row + (gqa ? s.kvh * lay.hd : 0) +
                            s.part * a.shape.vw;
   const int pieces = min(a.shape.vw, a.dv - s.part * a.shape.vw) >> 3;  // of 16 bytes
   bool odd = false;
+#pragma unroll 1
   for (int side = 0; side < 2; ++side) {
     const int from = side ? first_seen(a, s.first) : s.first;
     const int to = side ? first_seen(a, s.first + s.ntok - 1) : s.first + s.ntok;
-#pragma unroll 8
-    for (int e = thread; e < (to - from) * pieces; e += threads) {
-      const int tok = from + e / pieces, page = load_page(a, s.r, tok);
-      if (page < 0 || ((long long)page + 1) * lay.page_size > a.pool.num_slots) continue;
-      const int slot = page * lay.page_size + tok - page_index(a, tok) * lay.page_size;
-      odd |= odd8(__ldg(reinterpret_cast<const uint4 *>(v + (long long)slot * row) + e % pieces));
+#pragma unroll 1
+    for (int t = from + 32 * warp; t < to; t += 32 * warps) {
+      int slot = -1;
+      if (t + lane < to) {
+        const int page = load_page(a, s.r, t + lane);
+        if (page >= 0 && ((long long)page + 1) * lay.page_size <= a.pool.num_slots)
+          slot = page * lay.page_size + (t + lane - page_index(a, t + lane) * lay.page_size);
+      }
+      const int count = min(32, to - t) * pieces;
+#pragma unroll 1
+      for (int e0 = 0; e0 < count; e0 += 256) {
+        uint4 x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int e = e0 + 32 * k + lane, i = e / pieces;
+          const int at = __shfl_sync(0xffffffffu, slot, min(i, 31));
+          x[k] = e < count && at >= 0 ? __ldg(reinterpret_cast<const uint4 *>(
+                                                  v + (long long)at * row) + (e - i * pieces))
+                                      : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) odd |= odd8(x[k]);
+      }
     }
   }
   return odd;

@@ -13,8 +13,8 @@
 // to bf16 as the product with V wants it.
 //
 // Roles: sixteen warps (MLA eight) softmax, rescaling and output, two threads to a query row; one
-// brings K and V rows through the page table into a ring of stages; one thread of the next issues the
-// MMAs and the copies of Q. Whole tiles of pages of 8, 16, 32 or 64 slots, or a multiple of 128, come
+// (MLA four) brings Q and, through the page table, K and V rows into a ring of stages; one thread of the next issues the
+// MMAs. Whole tiles of pages of 8, 16, 32 or 64 slots, or a multiple of 128, come
 // as tensor-map copies, one per page and 64 columns; tiles with tokens left out and other page sizes
 // as 16-byte cp.async, zero-filled where a token has no slot, so that nothing of a row that no token
 // holds is ever multiplied. Tokens that not all rows of a block see are: their V times a weight of 0,
@@ -43,14 +43,14 @@ constexpr int kMasks = 8;              // tiles whose token masks are kept
 constexpr int kSegs = 8;               // segments that are kept
 
 // DK, DV: 64-column chunks of K and of the CTA's V columns; QT: tiles of query rows; UC: chunks
-// per ring stage; NST: ring stages.
-template <int DK_, int DV_, int QT_, int UC_, int NST_>
+// per ring stage; NST: ring stages; NL: warps that load K and V.
+template <int DK_, int DV_, int QT_, int UC_, int NST_, int NL_>
 struct Shape {
-  static constexpr int DK = DK_, DV = DV_, QT = QT_, UC = UC_, NST = NST_;
-  // softmax warps; the loading warp, the MMA warp, two that look at V
-  static constexpr int kSoft = 8 * QT, kLoad = kSoft, kMma = kSoft + 1, kLook = 2;
+  static constexpr int DK = DK_, DV = DV_, QT = QT_, UC = UC_, NST = NST_, NL = NL_;
+  // softmax warps; NL loading warps, the MMA warp, two that look at V
+  static constexpr int kSoft = 8 * QT, kMma = kSoft + NL, kLook0 = kMma + 1, kLook = 2;
   static constexpr bool kTwo = QT == 2;
-  static constexpr int kThr = 32 * (kMma + 1 + kLook);
+  static constexpr int kThr = 32 * (kLook0 + kLook);
   // With two query tiles the softmax warps take registers of the others; whole warpgroups
   static constexpr int kRegsSoft = 104, kRegsRest = 64;
   static constexpr int kRegs = 32 * kSoft * kRegsSoft + (kThr - 32 * kSoft) * kRegsRest;
@@ -79,9 +79,9 @@ struct Shape {
   static_assert(!kTwo || kThr % 128 == 0, "whole warpgroups");
 };
 
-using Gqa128 = Shape<2, 2, 2, 2, 5>;
-using Gqa64 = Shape<1, 1, 2, 1, 10>;
-using Mla512 = Shape<9, 4, 1, 1, 5>;
+using Gqa128 = Shape<2, 2, 2, 2, 5, 1>;
+using Gqa64 = Shape<1, 1, 2, 1, 10, 1>;
+using Mla512 = Shape<9, 4, 1, 1, 5, 4>;
 
 // Tensor maps of a call: pool rows of the layer (boxes of 64 columns and `box` slots) and query
 // rows (64 columns of a block's heads, of all its tokens or of one).
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
   }
   if (tid == 0) {
     for (int i = 0; i < S::NST; ++i) {
-      ptx::mbar_init(bar(S::full + i), 32);
+      ptx::mbar_init(bar(S::full + i), 32 * S::NL);
       ptx::mbar_init(bar(S::empty + i), 1);
     }
     ptx::mbar_init(bar(S::q_full), 1);
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
     ++seg_no;
     return s;
   };
-  if (warp == S::kLoad) {
+  if (warp == S::kSoft) {
     ChunkWalk w;
     w.start(a, st, blockIdx.x);
     if (!begins) w.left = 0;
@@ -253,10 +253,13 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
             };
             msk.x &= seen_of(see0 - t0, see1 - t0);
             msk.y &= seen_of(see0 - t0 - 32, see1 - t0 - 32);
-            const uint32_t sign = flip ? 0x80000000u : 0u;
+            if (flip) {
+#pragma unroll
+              for (int e = 0; e < 64; ++e) x[e] ^= 0x80000000u;
+            }
 #pragma unroll
             for (int e = 0; e < 64; ++e)
-              x[e] = ((e < 32 ? msk.x : msk.y) >> (e & 31)) & 1 ? x[e] ^ sign : 0xff800000u;
+              x[e] = (e < 32 ? msk.x : msk.y) & (1u << (e & 31)) ? x[e] : 0xff800000u;
           }
           auto y = [&](int e) { return __uint_as_float(x[e]); };
           float top;
@@ -359,7 +362,7 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
       if (live) {
         const bool ok = l != 0.f && !*gave_up;
         const float inv = 1.f / l, g0 = f0 * inv, g1 = f1 * inv;
-        const bool whole = chunk_whole(s);
+        const bool whole = chunk_whole(s), whole32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
         const long long rh = (long long)(s.row + tok) * a.hq + h;
         const long long place = (long long)(2 * blockIdx.x + (s.carry() ? 0 : 1)) * a.shape.rb + i_row;
         __nv_bfloat16 *out = a.out + rh * a.dv + s.part * a.shape.vw;
@@ -387,20 +390,19 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
                         : 0u;
           }
           if (write && whole) {
+            uint32_t v[8];
 #pragma unroll
-            for (int e = 0; e < 16; e += 8) {
-              uint4 v;
-              v.x = pack_bf16(__uint_as_float(z[e]), __uint_as_float(z[e + 1]));
-              v.y = pack_bf16(__uint_as_float(z[e + 2]), __uint_as_float(z[e + 3]));
-              v.z = pack_bf16(__uint_as_float(z[e + 4]), __uint_as_float(z[e + 5]));
-              v.w = pack_bf16(__uint_as_float(z[e + 6]), __uint_as_float(z[e + 7]));
-              *reinterpret_cast<uint4 *>(out + j + e) = v;
+            for (int e = 0; e < 8; ++e)
+              v[e] = pack_bf16(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1]));
+            if (whole32) {
+              ptx::stg32(out + j, v);
+            } else {
+              *reinterpret_cast<uint4 *>(out + j) = make_uint4(v[0], v[1], v[2], v[3]);
+              *reinterpret_cast<uint4 *>(out + j + 8) = make_uint4(v[4], v[5], v[6], v[7]);
             }
           } else if (write) {
-#pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<uint4 *>(part + j + e) =
-                  make_uint4(z[e], z[e + 1], z[e + 2], z[e + 3]);
+            ptx::stg32(part + j, z);
+            ptx::stg32(part + j + 8, z + 8);
           }
         }
         if (write && from == 0) {
@@ -416,12 +418,14 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
     }
     if (tid == 0)
       chunk_note(places.rec + blockIdx.x, last, seg_no, false, false);
-  } else if (warp == S::kLoad) {
+  } else if (warp < S::kMma) {
     if (S::kTwo) ptx::regs_fewer<S::kRegsRest>();
-    // ---- K and V rows into the ring, by one warp: it issues the sixteen copies of a 32 KB stage in
+    // ---- Q, and K and V rows into the ring: a warp issues the sixteen copies of a 32 KB stage in
     // about 450 cycles. What a warp does alone takes about five cycles an instruction, so whole tiles
     // take as few as may be: a lane to a page, one load and one test ahead of its tile. Copies are
-    // issued by one thread, which stands in for the others' arrivals ----
+    // issued by one thread, which stands in for the others' arrivals. Several warps (MLA) each do all
+    // of it but the copies, of which each has its share ----
+    const int part = warp - S::kSoft;
     const bool gqa = lay.kind == KAMERA_GQA;
     const int box = maps.box, each = maps.copies;  // slots of a copy, copies of a tile's 64 columns
     const int per_page = maps.per_page;            // tiles of a page (each == 1)
@@ -430,7 +434,7 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
     uint32_t tile_no = 0;        // tiles so far
     uint32_t published = 0;
     auto publish = [&]() {       // the next segment
-      if (lane == 0) {
+      if (part == 0 && lane == 0) {
         ChunkSegment *to = segs + published % kSegs;
         if (!walk->next(a, to)) to->t0 = to->t1 = 0;
         if (!dead) ptx::mbar_arrive(bar(S::sg_full) + 8 * (published % kSegs));
@@ -470,37 +474,39 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
         const int col = is_k ? kcol : vcol, stages = (is_k ? S::DK : S::DV) / S::UC;
         if (tile.whole) {
           const void *map = is_k ? &maps.k : &maps.v;
-          for (int k0 = 0; k0 < each; k0 += 8) {  // (twice with pages of 8 slots)
-            int y[8];
+          // copies [k0, k0 + mine) of each 64 columns are this warp's
+          const int mine = S::NL == 1 ? each : each >= S::NL ? each / S::NL : part < each;
+          const int k0 = part * mine;
+          constexpr int kMost = 16 / S::NL;  // (with pages of 8 slots)
+          int y[kMost];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] = __shfl_sync(0xffffffffu, tile.y, k0 + k);
-            if (ptx::elect_one()) {
-              Place<S::NST> to = at;
+          for (int k = 0; k < kMost; ++k) y[k] = __shfl_sync(0xffffffffu, tile.y, (k0 + k) & 31);
+          if (ptx::elect_one()) {
+            Place<S::NST> to = at;
 #pragma unroll 1
-              for (int u = 0; u < stages; ++u) {
-                const uint32_t full = bar(S::full) + 8 * to.st;
-                uint32_t dst = sb + S::ring + to.st * S::kStage + k0 * 1024;
-                if (k0 == 0) {
-                  wait(bar(S::empty) + 8 * to.st, to.ph ^ 1);
-                  if (dead) break;
-                  ptx::mbar_arrive_n(full, 31);
-                  ptx::mbar_arrive_expect_tx(full, S::kStage);
-                }
-                if (dead) break;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  if (k < each) {
-#pragma unroll
-                    for (int c = 0; c < S::UC; ++c)
-                      ptx::tma_2d(dst + c * kChunk, map, col + (u * S::UC + c) * 64, y[k], full);
-                  }
-                  dst += box * 128;
-                }
-                to.advance(1);
+            for (int u = 0; u < stages; ++u) {
+              const uint32_t full = bar(S::full) + 8 * to.st;
+              uint32_t dst = sb + S::ring + to.st * S::kStage + k0 * box * 128;
+              wait(bar(S::empty) + 8 * to.st, to.ph ^ 1);
+              if (dead) break;
+              if (S::NL > 1 && mine == 0) {
+                ptx::mbar_arrive_n(full, 32);
+              } else {
+                ptx::mbar_arrive_n(full, 31);
+                ptx::mbar_arrive_expect_tx(full, mine * box * S::UC * 128);
               }
+#pragma unroll
+              for (int k = 0; k < kMost; ++k) {
+                if (k >= mine) break;
+#pragma unroll
+                for (int c = 0; c < S::UC; ++c)
+                  ptx::tma_2d(dst + c * kChunk, map, col + (u * S::UC + c) * 64, y[k], full);
+                dst += box * 128;
+              }
+              to.advance(1);
             }
-            __syncwarp();
           }
+          __syncwarp();
           at.advance(stages);
           return;
         }
@@ -520,7 +526,8 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
             continue;
           }
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < 4; ++k) {
+            if (S::NL > 1 && k != part) continue;  // a warp's 32 tokens
 #pragma unroll 2
             for (int j = 0; j < 8; ++j) {  // four tokens at a time
               const int t = 32 * k + 4 * j + (lane >> 3);
@@ -531,9 +538,27 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
                 ptx::cp_async16(dst + c * kChunk + t * 128 + ((piece ^ (t & 7)) << 4), p + c * 64,
                                 sl >= 0 ? 16u : 0u);
             }
-          ptx::cp_async_mbar_arrive(full);
+          }
+          // made visible to the tensor core here, as the MMA thread does not stop for it
+          ptx::cp_async_commit();
+          ptx::cp_async_wait_all();
+          ptx::fence_proxy_async_smem();
+          ptx::mbar_arrive(full);
         }
       };
+      if (part == 0) {
+        // Q, once S of the segment before is complete. Rows of a copy past the block's are other
+        // tokens' or zero: their results go nowhere
+        if (seg_no > 1) wait(bar(S::q_empty), seg_no & 1);
+        if (!__any_sync(0xffffffffu, dead) && ptx::elect_one()) {
+          const bool one = sp->ntok == 1;
+          ptx::mbar_arrive_expect_tx(bar(S::q_full), one ? maps.token_bytes : maps.block_bytes);
+          for (int c = 0; c < S::DK; ++c)
+            ptx::tma_3d(sb + S::q + c * S::QT * kChunk, one ? &maps.q_token : &maps.q_block,
+                        c * 64, sp->h0, sp->row, bar(S::q_full));
+        }
+        __syncwarp();
+      }
       // the stages come in the order K0 V0 K1 V1 ..., in MLA's one query tile, whose tiles take more
       // stages than there are, in that in which they are read: K0 K1 V0 K2 V1 ... V(n-1)
 #pragma unroll 1
@@ -554,7 +579,7 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
           bits.z = __ballot_sync(0xffffffffu, slot[2] >= 0);
           bits.w = __ballot_sync(0xffffffffu, slot[3] >= 0);
         }
-        if (lane == 0) {
+        if (part == 0 && lane == 0) {
           *reinterpret_cast<uint4 *>(smem + S::mask + 16 * mk) = bits;
           if (!dead) ptx::mbar_arrive(bar(S::mk_full) + 8 * mk);
         }
@@ -573,13 +598,13 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
     if (S::kTwo) ptx::regs_fewer<S::kRegsRest>();
     // ---- two warps look at V of the tokens that only some of a block's rows see ----
     while (const ChunkSegment *sp = take_segment()) {
-      if (!sp->carry() && chunk_odd(a, *sp, 32 * (warp - S::kMma - 1) + lane, 64)) *odd = 1;
+      if (!sp->carry() && chunk_odd(a, *sp, warp - S::kLook0, S::kLook)) *odd = 1;
       __syncwarp();
       if (lane == 0 && !dead) ptx::mbar_arrive(bar(S::o_free));
     }
   } else {
     if (S::kTwo) ptx::regs_fewer<S::kRegsRest>();
-    // ---- MMAs and Q, one thread. Issuing an MMA takes a few instructions only: the descriptors of
+    // ---- MMAs, one thread. Issuing an MMA takes a few instructions only: the descriptors of
     // a tile's steps differ by constants ----
     if (warp == S::kMma && ptx::elect_one()) {
       constexpr uint32_t id_s =
@@ -595,7 +620,6 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
       const uint32_t q0 = desc_k(sb + S::q);             // [chunk][query tile][128 rows]
       auto landed = [&](const Place<S::NST> &at) {
         wait(bar(S::full) + 8 * at.st, at.ph);
-        ptx::fence_proxy_async_smem();
       };
       auto commit = [&](int b) {
         if (!dead) ptx::mma_commit(bar(b));
@@ -652,19 +676,8 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
       };
       while (const ChunkSegment *sp = take_segment()) {
         const int n = sp->t1 - sp->t0;
-        // Q, once S of the segment before is complete. Rows of a copy past the block's are other
-        // tokens' or zero: their results go nowhere
         const bool before = seg_no > 1;
-        if (before) wait(bar(S::q_empty), seg_no & 1);
-        if (!dead) {
-          const bool one = sp->ntok == 1;
-          ptx::mbar_arrive_expect_tx(bar(S::q_full), one ? maps.token_bytes : maps.block_bytes);
-          for (int c = 0; c < S::DK; ++c)
-            ptx::tma_3d(sb + S::q + c * S::QT * kChunk, one ? &maps.q_token : &maps.q_block, c * 64,
-                        sp->h0, sp->row, bar(S::q_full));
-        }
         wait(bar(S::q_full), (seg_no - 1) & 1);
-        ptx::fence_proxy_async_smem();
         vp = kp;
         if constexpr (S::kTwo) {
           // Steps, each S of one query tile and then its P V: of a pair, S of the two query tiles

@@ -138,6 +138,13 @@ __device__ __forceinline__ void prefetch_map(const void *map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
+// 32 bytes to global memory at a multiple of 32 (one sector a thread).
+__device__ __forceinline__ void stg32(void *p, const uint32_t *v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // ---- registers ----
 // The warps of a warpgroup (four from a multiple of four) take kRegs registers a thread each. The
 // shares of all warps of the block may not exceed the registers it was launched with.
