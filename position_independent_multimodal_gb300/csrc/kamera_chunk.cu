@@ -277,7 +277,7 @@ __device__ __noinline__ void chunk_row_again(const ChunkArgs &a, const ChunkSegm
 // Worker blockIdx.x's cut block: a warp to a row, the parts' log-sum-exps a lane each, then four
 // columns a lane. Then, where a worker has found odd values, those of the blocks that the worker
 // starts which multiply such a value for a row that does not see it.
-__global__ void __launch_bounds__(kJoinThr) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
+__global__ void __launch_bounds__(kJoinThr, 4) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
   __shared__ ChunkScratch<kJoinThr> found;
   const int w = blockIdx.x, lane = threadIdx.x & 31;
   const int first = blockIdx.y * (kJoinThr / 32) + (threadIdx.x >> 5);
@@ -293,17 +293,62 @@ __global__ void __launch_bounds__(kJoinThr) chunk_join_kernel(const __grid_const
     const int rb = a.shape.rb, vw = a.shape.vw, np = 1 + rec.more;
     const int cols = min(vw, a.dv - rec.part * vw);
     bool skip = false;
-    for (int i = lane; i < rec.more; i += 32) {
-      skip |= places.rec[w + 1 + i].gave_up;
-    }
+    for (int i = lane; i < rec.more; i += 32) skip |= places.rec[w + 1 + i].gave_up;
     if (!__any_sync(0xffffffffu, skip)) {
       auto place = [&](int p) { return (long long)(2 * (w + p) + (p == 0)) * rb; };
-      for (int i = first; i < rec.rows; i += step) {
+      auto row_of = [&](int i) {  // of q and its head, in out and lse
+        const int k = a.pieces > 1 ? 0 : (int)((unsigned)i * a.hpk_magic >> 16);
+        return (long long)(rec.row + k) * a.hq + rec.h0 + i - k * a.hpk;
+      };
+      auto put = [&](long long rh, int col, const float *acc, float inv) {
+        uint2 v;
+        v.x = pack_bf16(acc[0] * inv, acc[1] * inv);
+        v.y = pack_bf16(acc[2] * inv, acc[3] * inv);
+        *reinterpret_cast<uint2 *>(a.out + rh * a.dv + rec.part * vw + col) = v;
+      };
+      constexpr int kAtOnce = 4;
+      for (int i0 = first * kAtOnce; np == 2 && i0 < rec.rows; i0 += step * kAtOnce) {
+        // two parts, as most cut blocks have: several rows' loads together
+        for (int col = 4 * lane; col < cols; col += 128) {
+          float4 v[kAtOnce][2];
+          float z[kAtOnce][2];
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              const long long at = place(p) + min(i0 + j, rec.rows - 1);
+              z[j][p] = places.lse[at];
+              v[j][p] = *reinterpret_cast<const float4 *>(places.o + at * vw + col);
+            }
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j) {
+            if (i0 + j >= rec.rows) break;
+            // a part of no mass is left out; a NaN goes on
+            const float top = fmaxf(z[j][0], z[j][1]);
+            const float f0 = z[j][0] == neg_inf ? 0.f : exp2_approx((z[j][0] - top) * kLog2e);
+            const float f1 = z[j][1] == neg_inf ? 0.f : exp2_approx((z[j][1] - top) * kLog2e);
+            const float sum = f0 + f1, inv = sum == 0.f ? 0.f : 1.f / sum;
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              const float f = p ? f1 : f0;
+              if (f == 0.f) continue;
+              acc[0] = fmaf(f, v[j][p].x, acc[0]);
+              acc[1] = fmaf(f, v[j][p].y, acc[1]);
+              acc[2] = fmaf(f, v[j][p].z, acc[2]);
+              acc[3] = fmaf(f, v[j][p].w, acc[3]);
+            }
+            const long long rh = row_of(i0 + j);
+            put(rh, col, acc, inv);
+            if (col == 0 && rec.part == 0) a.lse[rh] = sum == 0.f ? neg_inf : top + logf(sum);
+          }
+        }
+      }
+      for (int i = first; np > 2 && i < rec.rows; i += step) {
         float top = neg_inf;
         for (int p = lane; p < np; p += 32) top = fmaxf(top, places.lse[place(p) + i]);
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const int k = a.pieces > 1 ? 0 : (int)((unsigned)i * a.hpk_magic >> 16);
-        const long long rh = (long long)(rec.row + k) * a.hq + rec.h0 + i - k * a.hpk;
+        const long long rh = row_of(i);
         for (int col = 0; col < cols; col += 128) {
           const bool in = col + 4 * lane < cols;
           float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -336,12 +381,7 @@ __global__ void __launch_bounds__(kJoinThr) chunk_join_kernel(const __grid_const
             }
           }
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          if (in) {
-            uint2 v;
-            v.x = pack_bf16(acc[0] * inv, acc[1] * inv);
-            v.y = pack_bf16(acc[2] * inv, acc[3] * inv);
-            *reinterpret_cast<uint2 *>(a.out + rh * a.dv + rec.part * vw + col + 4 * lane) = v;
-          }
+          if (in) put(rh, col + 4 * lane, acc, inv);
           if (lane == 0 && col == 0 && rec.part == 0)
             a.lse[rh] = sum == 0.f ? neg_inf : top + logf(sum);
         }
@@ -410,9 +450,9 @@ cudaError_t launch_chunk_attention(const ChunkArgs &args, cudaStream_t s) {
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  // a warp to a row of a cut block
+  // a warp to a few rows of a cut block
   const long long rows = std::min<long long>(a.shape.rb, (long long)a.n_tokens * a.hpk);
-  const int per = kJoinThr / 32;
+  const int per = kJoinThr / 32 * (rows > 64 ? 4 : 1);
   return launch_early(chunk_join_kernel, dim3(a.shape.n, (unsigned)((rows + per - 1) / per)), kJoinThr,
                       0, s, a);
 }

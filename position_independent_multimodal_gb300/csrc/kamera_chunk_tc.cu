@@ -43,12 +43,13 @@ constexpr int kMasks = 8;              // tiles whose token masks are kept
 constexpr int kSegs = 8;               // segments that are kept
 
 // DK, DV: 64-column chunks of K and of the CTA's V columns; QT: tiles of query rows; UC: chunks
-// per ring stage; NST: ring stages; NL: warps that load K and V.
-template <int DK_, int DV_, int QT_, int UC_, int NST_, int NL_>
+// per ring stage; NST: ring stages; NL: warps that load K and V;
+// SW: threads to a query row.
+template <int DK_, int DV_, int QT_, int UC_, int NST_, int NL_, int SW_>
 struct Shape {
-  static constexpr int DK = DK_, DV = DV_, QT = QT_, UC = UC_, NST = NST_, NL = NL_;
+  static constexpr int DK = DK_, DV = DV_, QT = QT_, UC = UC_, NST = NST_, NL = NL_, SW = SW_;
   // softmax warps; NL loading warps, the MMA warp, two that look at V
-  static constexpr int kSoft = 8 * QT, kMma = kSoft + NL, kLook0 = kMma + 1, kLook = 2;
+  static constexpr int kSoft = 4 * SW, kMma = kSoft + NL, kLook0 = kMma + 1, kLook = 2;
   static constexpr bool kTwo = QT == 2;
   static constexpr int kThr = 32 * (kLook0 + kLook);
   // With two query tiles the softmax warps take registers of the others; whole warpgroups
@@ -58,11 +59,11 @@ struct Shape {
   static constexpr int q = 0;
   static constexpr int ring = QT * DK * kChunk;
   static constexpr int mask = ring + NST * kStage;  // uint32 [kMasks][4]
-  static constexpr int xch = mask + kMasks * 16;    // float [2 QT][kRow]: maxima, sums
-  static constexpr int bar = xch + 2 * QT * kRow * 4;
-  // mbarriers; those of P: [buffer][half of the tokens]
+  static constexpr int xch = mask + kMasks * 16;    // float [SW][kRow]: maxima, sums
+  static constexpr int bar = xch + SW * kRow * 4;
+  // mbarriers
   static constexpr int full = 0, empty = NST, q_full = empty + NST, q_empty = q_full + 1,
-                       s_full = q_empty + 1, p_full = s_full + 2, pv_done = p_full + 4,
+                       s_full = q_empty + 1, p_full = s_full + 2, pv_done = p_full + 2,
                        o_free = pv_done + 1, o_full = o_free + 1,
                        mk_full = o_full + 2, sg_full = mk_full + kMasks, last = sg_full + kSegs,
                        n_bar = last + 1;
@@ -79,9 +80,9 @@ struct Shape {
   static_assert(!kTwo || kThr % 128 == 0, "whole warpgroups");
 };
 
-using Gqa128 = Shape<2, 2, 2, 2, 5, 1>;
-using Gqa64 = Shape<1, 1, 2, 1, 10, 1>;
-using Mla512 = Shape<9, 4, 1, 1, 5, 4>;
+using Gqa128 = Shape<2, 2, 2, 2, 5, 1, 4>;
+using Gqa64 = Shape<1, 1, 2, 1, 10, 1, 4>;
+using Mla512 = Shape<9, 4, 1, 1, 5, 4, 2>;
 
 // Tensor maps of a call: pool rows of the layer (boxes of 64 columns and `box` slots) and query
 // rows (64 columns of a block's heads, of all its tokens or of one).
@@ -136,8 +137,7 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
     ptx::mbar_init(bar(S::q_empty), 1);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bar(S::s_full + i), 1);
-      ptx::mbar_init(bar(S::p_full + 2 * i), 4);
-      ptx::mbar_init(bar(S::p_full + 2 * i + 1), 4);
+      ptx::mbar_init(bar(S::p_full + i), S::kSoft);
       ptx::mbar_init(bar(S::o_full + i), 1);
     }
     ptx::mbar_init(bar(S::pv_done), 1);
@@ -186,232 +186,274 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
 
   if (warp < S::kSoft) {
     if (S::kTwo) ptx::regs_more<S::kRegsSoft>();
-    // ---- softmax: two threads (of two warps) to a query row, 64 tokens of each tile and half of
-    // O's columns each ----
-    const int w = warp >> 3;                       // query tile
-    const int hf = (warp >> 2) & 1;                // half of the tokens, of O's columns
-    const int row = (warp & 3) * 32 + lane;
+    // ---- softmax: all warps on one S tile at a time, SW threads (of as many warps) to a query row,
+    // kCols tokens of the tile and as large a part of O's columns each. That is what makes the way
+    // from S to P short: while it is gone the tensor core has the other tile's products only ----
+    constexpr int kCols = kTok / S::SW, kOut = S::DV * 64 / S::SW;
+    const int qr = warp >> 2;                      // the thread's part of the tokens and columns
+    const int lane_row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     // (a scale of 0 is one that makes nothing of any score: -inf, where a token is not seen, times
     // it is -inf)
     const float c = fmaxf(fabsf(a.scale) * kLog2e, 1.2e-38f);
     const bool flip = a.scale < 0.f;
     const float inf = __int_as_float(0x7f800000);
-    const uint32_t o_t = tmem + S::o_col + w * 128 + lane_off;
-    float *xch = reinterpret_cast<float *>(smem + S::xch);  // [2 w + half][row]
-    const int pair = 3 + w * 4 + (warp & 3);  // named barrier of a row's two warps
+    float *xch = reinterpret_cast<float *>(smem + S::xch);  // [part][row]
+    const int group = 3 + (warp & 3);  // named barrier of the rows' warps
     auto arrive = [&](uint32_t b) {  // once for the warp
       __syncwarp();
       if (lane == 0 && !dead) ptx::mbar_arrive(b);
     };
-    uint32_t mine = 0;   // tiles of this warp so far: phases of its buffers
+    // the sum over a row's threads
+    auto row_sum = [&](float v) {
+      xch[qr * kRow + lane_row] = v;
+      ptx::barrier_sync(group, 32 * S::SW);
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < S::SW; ++k) sum += xch[k * kRow + lane_row];
+      ptx::barrier_sync(group, 32 * S::SW);
+      return sum;
+    };
+    // A thread's row of an S tile, or of the tiles of tokens that the tile takes.
+    struct Row {
+      int i;            // its row of the block
+      int see0, see1;   // tokens that it sees
+      int in0, in1;     // tiles of which all the warp's rows see the warp's part
+      float m;
+      f32x2 l;
+      bool live;        // a warp without rows only keeps step
+    };
+    auto begin = [&](const ChunkSegment &s, int i) {
+      const int rows = s.ntok * s.heads;
+      Row r;
+      r.i = i;
+      int tok, h;
+      chunk_row(a, s, i < rows ? i : 0, &tok, &h);
+      // a thread without a row sees all, against a maximum that leaves nothing
+      r.see1 = i < rows ? s.first + tok + 1 : 0x7FFFFFFF;
+      r.see0 = i < rows ? first_seen(a, s.first + tok) : 0;
+      r.in0 = (__reduce_max_sync(0xffffffffu, r.see0) - kCols * qr + kTok - 1) >> kTokSh;
+      r.in1 = flip ? 0 : (__reduce_min_sync(0xffffffffu, r.see1) - kCols * (qr + 1) + kTok) >> kTokSh;
+      r.m = i < rows ? -inf : inf;
+      r.l = f2(0.f, 0.f);
+      r.live = i - lane < rows;
+      return r;
+    };
+    uint32_t ph = 0;     // parity of each S buffer, a bit each
     uint32_t seen = 0;   // tiles of the CTA's segments so far
+    uint32_t tiles = 0;  // one query tile: tile k has S buffer k % 2
     ChunkSegment last = {};
     while (const ChunkSegment *sp = take_segment()) {
       const ChunkSegment &s = *sp;
       const uint32_t parity = (seg_no - 1) & 1;
       if (tid == 0) last = s;
       const int n = s.t1 - s.t0, tile0 = s.t0, rows = s.ntok * s.heads;
-      const bool turns = S::kTwo && rows <= kRow;  // the tiles of tokens in turn
-      const int i_row = (turns ? 0 : kRow * w) + row;
-      const bool live = i_row - lane < rows;  // a warp without rows only keeps step
-      int tok, h;
-      chunk_row(a, s, i_row < rows ? i_row : 0, &tok, &h);
-      // a thread without a row sees all, against a maximum that leaves nothing
-      const int see1 = i_row < rows ? s.first + tok + 1 : 0x7FFFFFFF;
-      const int see0 = i_row < rows ? first_seen(a, s.first + tok) : 0;
-      float m = i_row < rows ? -inf : inf;
-      f32x2 la = f2(0.f, 0.f), lb = la;
-      // of the warp's half of each tile, those whose tokens all its rows see: [in0, in1)
-      const int in0 = (__reduce_max_sync(0xffffffffu, see0) - 64 * hf + kTok - 1) >> kTokSh;
-      const int in1 = flip ? 0 : (__reduce_min_sync(0xffffffffu, see1) - 64 * hf + 64) >> kTokSh;
-      int done = 0;  // tiles of this segment
-      for (int i = turns ? w : 0; i < n; i += turns ? 2 : 1, ++done, ++mine) {
-        const int b = S::kTwo ? w : (mine & 1);
-        const uint32_t ph = S::kTwo ? mine & 1 : mine >> 1 & 1;
-        wait(bar(S::s_full + b), ph);
+      // the steps of the MMA thread
+      const bool pairs = S::kTwo && rows > kRow;
+      const int steps = pairs ? 2 * n : n;
+      Row r = begin(s, lane_row), other = r;
+      if (pairs) other = begin(s, kRow + lane_row);
+#pragma unroll 1
+      for (int v = 0; v < steps; ++v) {
+        const int t = S::kTwo ? v & 1 : 0, i = pairs ? v >> 1 : v;
+        const uint32_t b = S::kTwo ? t : (tiles + v) & 1;
+        const uint32_t o_t = tmem + S::o_col + t * 128 + lane_off + qr * kOut;
+        wait(bar(S::s_full) + 8 * b, ph >> b & 1);
+        ph ^= 1u << b;
         __syncwarp();
         ptx::tc_fence_after();
-        if (live) {
-          const uint32_t s_t = tmem + b * 128 + hf * 64 + lane_off;
-          uint32_t x[64];
-          ptx::tmem_ld32(s_t, x);
-          ptx::tmem_ld32(s_t + 32, x + 32);
+        if (r.live) {
+          const uint32_t s_t = tmem + b * 128 + qr * kCols + lane_off;
+          uint32_t x[kCols];
+#pragma unroll
+          for (int k = 0; k < kCols; k += 32) ptx::tmem_ld32(s_t + k, x + k);
           // the tile's mask, which is there before S is
           const uint32_t mk = (seen + i) % kMasks;
-          wait(bar(S::mk_full + mk), ((seen + i) / kMasks) & 1);
-          uint2 msk = *reinterpret_cast<const uint2 *>(smem + S::mask + 16 * mk + 8 * hf);
-          const bool plain =
-              tile0 + i >= in0 && tile0 + i < in1 && (msk.x & msk.y) == 0xffffffffu;
-          ptx::tmem_ld_wait_all<64>(x);
+          wait(bar(S::mk_full) + 8 * mk, (seen + i) / kMasks & 1);
+          const uint32_t *mask = reinterpret_cast<const uint32_t *>(smem + S::mask + 16 * mk) +
+                                 qr * (kCols / 32);
+          uint32_t msk[kCols / 32], all = 0xffffffffu;
+#pragma unroll
+          for (int k = 0; k < kCols / 32; ++k) all &= msk[k] = mask[k];
+          const int tile = tile0 + i;
+          const bool plain = tile >= r.in0 && tile < r.in1 && all == 0xffffffffu;
+          ptx::tmem_ld_wait_all<kCols>(x);
           if (!plain) {
-            const int t0 = ((tile0 + i) << kTokSh) + 64 * hf;
-            auto seen_of = [&](int from, int to) {  // of 32 tokens, those in [from, to)
-              const uint32_t up = from <= 0 ? 0xffffffffu : from >= 32 ? 0u : 0xffffffffu << from;
-              const uint32_t dn = to >= 32 ? 0xffffffffu : to <= 0 ? 0u : (1u << to) - 1u;
-              return up & dn;
-            };
-            msk.x &= seen_of(see0 - t0, see1 - t0);
-            msk.y &= seen_of(see0 - t0 - 32, see1 - t0 - 32);
             if (flip) {
 #pragma unroll
-              for (int e = 0; e < 64; ++e) x[e] ^= 0x80000000u;
+              for (int e = 0; e < kCols; ++e) x[e] ^= 0x80000000u;
             }
 #pragma unroll
-            for (int e = 0; e < 64; ++e)
-              x[e] = (e < 32 ? msk.x : msk.y) & (1u << (e & 31)) ? x[e] : 0xff800000u;
+            for (int k = 0; k < kCols / 32; ++k) {
+              const int t0 = (tile << kTokSh) + kCols * qr + 32 * k;
+              const int from = r.see0 - t0, to = r.see1 - t0;
+              const uint32_t up = from <= 0 ? 0xffffffffu : from >= 32 ? 0u : 0xffffffffu << from;
+              const uint32_t dn = to >= 32 ? 0xffffffffu : to <= 0 ? 0u : (1u << to) - 1u;
+              const uint32_t bits = msk[k] & up & dn;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                x[32 * k + e] = bits & (1u << e) ? x[32 * k + e] : 0xff800000u;
+            }
           }
           auto y = [&](int e) { return __uint_as_float(x[e]); };
           float top;
           {
-            float t[4];
+            float u[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) t[k] = fmaxf(fmaxf(y(k), y(k + 4)), y(k + 8));
+            for (int k = 0; k < 4; ++k) u[k] = fmaxf(y(k), y(k + 4));
 #pragma unroll
-            for (int e = 12; e < 60; e += 8)
+            for (int e = 8; e < kCols; e += 8)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) t[k] = fmaxf(fmaxf(t[k], y(e + k)), y(e + k + 4));
-#pragma unroll
-            for (int k = 0; k < 4; ++k) t[k] = fmaxf(t[k], y(60 + k));
-            top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+              for (int k = 0; k < 4; ++k) u[k] = fmaxf(fmaxf(u[k], y(e + k)), y(e + k + 4));
+            top = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3]));
           }
-          // the maximum is raised where either half of the row wants it
-          if (ptx::barrier_or(pair, 64, (m == -inf && top > -inf) || (top - m) * c > 8.f)) {
-            xch[(2 * w + hf) * kRow + row] = top;
-            ptx::barrier_sync(pair, 64);
-            top = fmaxf(top, xch[(2 * w + (hf ^ 1)) * kRow + row]);
-            const bool first = m == -inf && top > -inf;
-            const bool up = first || (top - m) * c > 8.f;
-            const float f = up ? (first ? 0.f : exp2_approx((m - top) * c)) : 1.f;
-            if (up) m = top;
-            const f32x2 ff = f2(f, f), zero = f2(0.f, 0.f);
-            la = fma2(la, ff, zero);
-            lb = fma2(lb, ff, zero);
-            if (done > 0) {
+          // the maximum is raised where any part of the row wants it
+          if (ptx::barrier_or(group, 32 * S::SW,
+                              (r.m == -inf && top > -inf) || (top - r.m) * c > 8.f)) {
+            xch[qr * kRow + lane_row] = top;
+            ptx::barrier_sync(group, 32 * S::SW);
+#pragma unroll
+            for (int k = 0; k < S::SW; ++k) top = fmaxf(top, xch[k * kRow + lane_row]);
+            const bool first = r.m == -inf && top > -inf;
+            const bool up = first || (top - r.m) * c > 8.f;
+            const float f = up ? (first ? 0.f : exp2_approx((r.m - top) * c)) : 1.f;
+            if (up) r.m = top;
+            r.l = fma2(r.l, f2(f, f), f2(0.f, 0.f));
+            if (v >= (S::kTwo ? 2 : 1)) {
               // P V of the tile before is complete: S of this one says so, where it was issued
               // behind it (else S says so of the one before that, and the parity is unambiguous)
               if (!S::kTwo) {
-                wait(bar(S::pv_done), (mine - 1) & 1);
+                wait(bar(S::pv_done), (tiles + v - 1) & 1);
                 __syncwarp();
                 ptx::tc_fence_after();
               }
 #pragma unroll 1
-              for (int j = 0; j < S::DV * 2; ++j) {
+              for (int j = 0; j < kOut; j += 16) {
                 uint32_t z[16];
-                ptx::tmem_ld16(o_t + hf * (S::DV * 32) + 16 * j, z);
+                ptx::tmem_ld16(o_t + j, z);
                 ptx::tmem_ld_wait_all<16>(z);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) z[e] = __float_as_uint(__uint_as_float(z[e]) * f);
-                ptx::tmem_st16(o_t + hf * (S::DV * 32) + 16 * j, z);
+                ptx::tmem_st16(o_t + j, z);
               }
               ptx::tmem_st_wait();
             }
-            // neither thread's weights may be multiplied before both have scaled their columns
-            ptx::tc_fence_before();
-            ptx::barrier_sync(pair, 64);
-            ptx::tc_fence_after();
+            // (what the row's threads have scaled is multiplied after all of them have arrived)
+            ptx::barrier_sync(group, 32 * S::SW);
           }
-          const float base = m > -inf ? m * c : 0.f;
-          uint32_t p[32];
+          const float base = r.m > -inf ? r.m * c : 0.f;
+          f32x2 l2 = f2(0.f, 0.f);
+          uint32_t p[kCols / 2];
 #pragma unroll
-          for (int e = 0; e < 64; e += 2) {
+          for (int e = 0; e < kCols; e += 2) {
             const float p0 = exp2_approx(fmaf(y(e), c, -base));
             const float p1 = exp2_approx(fmaf(y(e + 1), c, -base));
             if (e & 2)
-              lb = add2(lb, f2(p0, p1));
+              l2 = add2(l2, f2(p0, p1));
             else
-              la = add2(la, f2(p0, p1));
+              r.l = add2(r.l, f2(p0, p1));
             p[e / 2] = pack_bf16(p0, p1);
           }
-          ptx::tmem_st32(s_t, p);  // P over its half of S
+          r.l = add2(r.l, l2);
+          // P over the thread's part of S
+          if constexpr (kCols == 64)
+            ptx::tmem_st32(s_t, p);
+          else
+            ptx::tmem_st16(s_t, p);
           ptx::tmem_st_wait();
         }
         ptx::tc_fence_before();
-        arrive(bar(S::p_full + 2 * b + hf));
+        arrive(bar(S::p_full) + 8 * b);
+        if (S::kTwo) {  // the other tile's turn
+          const Row x = r;
+          r = other;
+          other = x;
+        }
       }
       seen += n;
+      tiles += n;
+      if (S::kTwo && (steps & 1)) {
+        const Row x = r;
+        r = other;
+        other = x;
+      }
       // ---- output ----
-      wait(bar(S::o_full + w), parity);
-      if (turns) wait(bar(S::o_full + (w ^ 1)), parity);
-      __syncwarp();
-      ptx::tc_fence_after();
-      float l;
-      {
+      const bool whole = chunk_whole(s), whole32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
+      auto sum_of = [&](const Row &x) {
         float l0, l1;
-        f2_split(add2(la, lb), l0, l1);
-        l = l0 + l1;
-      }
-      float f0 = 1.f, f1 = 0.f;  // factors of this query tile's O and of the other's
-      float *at = xch + 2 * w * kRow + row;
-      if (turns) {
-        at[hf * kRow] = m;
-        ptx::barrier_sync(2, 4 * kRow);
-        const float mo = xch[2 * (w ^ 1) * kRow + row], top = fmaxf(m, mo);  // (never NaN)
-        f0 = m == -inf ? 0.f : exp2_approx((m - top) * c);
-        f1 = mo == -inf ? 0.f : exp2_approx((mo - top) * c);
-        m = top;
-        ptx::barrier_sync(2, 4 * kRow);
-        at[hf * kRow] = n > w ? l * f0 : 0.f;
-        ptx::barrier_sync(2, 4 * kRow);
-        l = (xch[row] + xch[kRow + row]) + (xch[2 * kRow + row] + xch[3 * kRow + row]);
-      } else if (live) {
-        at[hf * kRow] = l;
-        ptx::barrier_sync(pair, 64);
-        l = at[0] + at[kRow];
-      }
-      if (live) {
-        const bool ok = l != 0.f && !*gave_up;
-        const float inv = 1.f / l, g0 = f0 * inv, g1 = f1 * inv;
-        const bool whole = chunk_whole(s), whole32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
-        const long long rh = (long long)(s.row + tok) * a.hq + h;
-        const long long place = (long long)(2 * blockIdx.x + (s.carry() ? 0 : 1)) * a.shape.rb + i_row;
-        __nv_bfloat16 *out = a.out + rh * a.dv + s.part * a.shape.vw;
-        float *part = places.o + place * a.shape.vw;
-        const bool write = i_row < rows && !*gave_up;
-        // of a row's columns, this thread's: half, in turns a quarter
-        const int cols = S::DV * 32 / (turns ? 2 : 1), from = (turns ? 2 * w + hf : hf) * cols;
-        const bool has = !turns || n > w, other = turns && n > 1 - w;
-        const uint32_t o_other = tmem + S::o_col + lane_off + (w ^ 1) * 128;
+        f2_split(x.l, l0, l1);
+        return row_sum(l0 + l1);
+      };
+      // of a block of one query tile the two turns' sums and O are joined
+      const bool turns = S::kTwo && !pairs;
 #pragma unroll 1
-        for (int j = from; j < from + cols; j += 16) {
-          uint32_t z[16];
-          ptx::tmem_ld16(o_t + j, z);
-          ptx::tmem_ld_wait_all<16>(z);
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            z[e] = ok && has ? __float_as_uint(__uint_as_float(z[e]) * g0) : 0u;
-          if (other) {
-            uint32_t z1[16];
-            ptx::tmem_ld16(o_other + j, z1);
-            ptx::tmem_ld_wait_all<16>(z1);
+      for (int t = 0; t < (pairs ? 2 : 1); ++t) {
+        wait(bar(S::o_full) + 8 * t, parity);
+        if (turns) wait(bar(S::o_full) + 8, parity);
+        __syncwarp();
+        ptx::tc_fence_after();
+        if (r.live) {
+          float l = sum_of(r), m = r.m, f0 = 1.f, f1 = 0.f;
+          const bool second = turns && n > 1;
+          if (second) {
+            const float l1 = sum_of(other), top = fmaxf(m, other.m);  // (never NaN)
+            f0 = m == -inf ? 0.f : exp2_approx((m - top) * c);
+            f1 = other.m == -inf ? 0.f : exp2_approx((other.m - top) * c);
+            l = l * f0 + l1 * f1;
+            m = top;
+          }
+          const bool ok = l != 0.f && !*gave_up;
+          const float inv = 1.f / l, g0 = f0 * inv, g1 = f1 * inv;
+          int tok, h;
+          chunk_row(a, s, r.i < rows ? r.i : 0, &tok, &h);
+          const long long rh = (long long)(s.row + tok) * a.hq + h;
+          const long long place = (long long)(2 * blockIdx.x + (s.carry() ? 0 : 1)) * a.shape.rb + r.i;
+          __nv_bfloat16 *out = a.out + rh * a.dv + s.part * a.shape.vw + qr * kOut;
+          float *part = places.o + place * a.shape.vw + qr * kOut;
+          const bool write = r.i < rows && !*gave_up;
+          const uint32_t o_t = tmem + S::o_col + t * 128 + lane_off + qr * kOut;
+#pragma unroll 1
+          for (int j = 0; j < kOut; j += 16) {
+            uint32_t z[16];
+            ptx::tmem_ld16(o_t + j, z);
+            ptx::tmem_ld_wait_all<16>(z);
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              z[e] = ok ? __float_as_uint(fmaf(__uint_as_float(z1[e]), g1, __uint_as_float(z[e])))
-                        : 0u;
-          }
-          if (write && whole) {
-            uint32_t v[8];
+              z[e] = ok ? __float_as_uint(__uint_as_float(z[e]) * g0) : 0u;
+            if (second) {
+              uint32_t z1[16];
+              ptx::tmem_ld16(o_t + 128 + j, z1);
+              ptx::tmem_ld_wait_all<16>(z1);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              v[e] = pack_bf16(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1]));
-            if (whole32) {
-              ptx::stg32(out + j, v);
-            } else {
-              *reinterpret_cast<uint4 *>(out + j) = make_uint4(v[0], v[1], v[2], v[3]);
-              *reinterpret_cast<uint4 *>(out + j + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+              for (int e = 0; e < 16; ++e)
+                z[e] = ok ? __float_as_uint(fmaf(__uint_as_float(z1[e]), g1, __uint_as_float(z[e])))
+                          : 0u;
             }
-          } else if (write) {
-            ptx::stg32(part + j, z);
-            ptx::stg32(part + j + 8, z + 8);
+            if (write && whole) {
+              uint32_t u[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                u[e] = pack_bf16(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1]));
+              if (whole32) {
+                ptx::stg32(out + j, u);
+              } else {
+                *reinterpret_cast<uint4 *>(out + j) = make_uint4(u[0], u[1], u[2], u[3]);
+                *reinterpret_cast<uint4 *>(out + j + 8) = make_uint4(u[4], u[5], u[6], u[7]);
+              }
+            } else if (write) {
+              ptx::stg32(part + j, z);
+              ptx::stg32(part + j + 8, z + 8);
+            }
+          }
+          if (write && qr == 0) {
+            const float z = l != 0.f ? (m * c + log2f(l)) * kLn2 : -inf;
+            if (!whole)
+              places.lse[place] = z;
+            else if (s.part == 0)
+              a.lse[rh] = z;
           }
         }
-        if (write && from == 0) {
-          const float z = l != 0.f ? (m * c + log2f(l)) * kLn2 : -inf;
-          if (!whole)
-            places.lse[place] = z;
-          else if (s.part == 0)
-            a.lse[rh] = z;
-        }
+        r = other;
       }
       ptx::tc_fence_before();
       arrive(bar(S::o_free));
@@ -649,7 +691,7 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
         const uint32_t p = tmem + b * 128, d = tmem + S::o_col + t * 128;
         Place<S::NST> at = vp;
         if (lands) landed(at);  // before P is, as a rule
-        wait(bar(S::p_full) + 16 * b, (p_ph >> b) & 1);
+        wait(bar(S::p_full) + 8 * b, (p_ph >> b) & 1);
         if (dead) return;
         ptx::tc_fence_after();
 #pragma unroll
@@ -659,13 +701,9 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
           const uint32_t v = desc_mn(ring + at.st * S::kStage);
 #pragma unroll
           for (int x = 0; x < kTok / 16; ++x) {
-            if (u == 0 && x == kTok / 32) {
-              wait(bar(S::p_full) + 16 * b + 8, (p_ph >> b) & 1);
-              if (dead) return;
-              ptx::tc_fence_after();
-            }
-            // P of tokens 0-63 is in columns 0-31 of S, of 64-127 in 64-95
-            ptx::mma_bf16_ta(d + u * S::UC * 64, p + 8 * x + (x < kTok / 32 ? 0 : 32),
+            // P of a softmax thread's tokens is in the first half of its part of S
+            constexpr int kPart = kTok / S::SW / 16;  // steps of a part
+            ptx::mma_bf16_ta(d + u * S::UC * 64, p + x / kPart * (16 * kPart) + x % kPart * 8,
                              desc(v + x * (2048 >> 4)), id_o, x ? 1u : (first_tile ? 0u : 1u));
           }
           if (frees) ptx::mma_commit(bar(S::empty) + 8 * at.st);
