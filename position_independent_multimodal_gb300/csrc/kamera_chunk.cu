@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kThr) chunk_gen_kernel(const __grid_constant__
     const int kcol = gqa ? s.kvh * lay.hd : 0, vcol = kcol + s.part * kCols;
     const int cols = min(kCols, a.dv - s.part * kCols);
     __syncthreads();
-    odd |= !s.carry() && chunk_odd(a, s, warp, kThr / 32);
+    odd |= !s.carry() && chunk_odd<0>(a, s, warp, kThr / 32);
     const int qp = a.dk >> 3;  // 16-byte pieces of a row
     for (int e = tid; e < kRows * qp; e += kThr) {
       const int i = e / qp, p = e - i * qp;
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kJoinThr, 4) chunk_join_kernel(const __grid_co
                                                    << a.shape.tile_sh);
     ChunkSegment wide = s;
     wide.ntok = end - s.first;
-    const bool again = !s.carry() && chunk_odd(a, wide, threadIdx.x >> 5, kJoinThr / 32);
+    const bool again = !s.carry() && chunk_odd<0>(a, wide, threadIdx.x >> 5, kJoinThr / 32);
     if (__syncthreads_or(again))
       for (int i = first; i < s.ntok * s.heads; i += step) chunk_row_again(a, s, i);
   }

@@ -304,7 +304,8 @@ __device__ __forceinline__ bool odd8(const uint4 &v) {
 // its own new tokens, and of those that the window leaves behind between its first row and its last.
 // Every token that is multiplied for a row which does not see it is such a one of some block. By
 // `warps` whole warps, each its share of 32 tokens at a time: a lane to a token's slot, then a lane to
-// 16 bytes.
+// 16 bytes. kPieces: 16-byte pieces of a row's part, a power of two below 64, or 0.
+template <int kPieces>
 __device__ __forceinline__ bool chunk_odd(const ChunkArgs &a, const ChunkSegment &s, int warp,
                                           int warps) {
   if (s.ntok == 1 && s.first + 1 == s.ctx) return false;  // there are no other new tokens
@@ -315,20 +316,23 @@ __device__ __forceinline__ bool chunk_odd(const ChunkArgs &a, const ChunkSegment
   const __nv_bfloat16 *v = (gqa ? a.pool.v : a.pool.k) +
                            (long long)a.layer * a.pool.num_slots * row + (gqa ? s.kvh * lay.hd : 0) +
                            s.part * a.shape.vw;
-  const int pieces = min(a.shape.vw, a.dv - s.part * a.shape.vw) >> 3;  // of 16 bytes
+  const int pieces = kPieces ? kPieces : min(a.shape.vw, a.dv - s.part * a.shape.vw) >> 3;
   bool odd = false;
+  auto slot_at = [&](int t, int to) {
+    if (t + lane >= to) return -1;
+    const int page = load_page(a, s.r, t + lane);
+    if (page < 0 || ((long long)page + 1) * lay.page_size > a.pool.num_slots) return -1;
+    return page * lay.page_size + (t + lane - page_index(a, t + lane) * lay.page_size);
+  };
 #pragma unroll 1
   for (int side = 0; side < 2; ++side) {
     const int from = side ? first_seen(a, s.first) : s.first;
     const int to = side ? first_seen(a, s.first + s.ntok - 1) : s.first + s.ntok;
+    int next = slot_at(from + 32 * warp, to);
 #pragma unroll 1
     for (int t = from + 32 * warp; t < to; t += 32 * warps) {
-      int slot = -1;
-      if (t + lane < to) {
-        const int page = load_page(a, s.r, t + lane);
-        if (page >= 0 && ((long long)page + 1) * lay.page_size <= a.pool.num_slots)
-          slot = page * lay.page_size + (t + lane - page_index(a, t + lane) * lay.page_size);
-      }
+      const int slot = next;
+      next = slot_at(t + 32 * warps, to);  // ahead of its use
       const int count = min(32, to - t) * pieces;
 #pragma unroll 1
       for (int e0 = 0; e0 < count; e0 += 256) {

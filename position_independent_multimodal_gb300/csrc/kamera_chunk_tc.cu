@@ -13,8 +13,8 @@
 // to bf16 as the product with V wants it.
 //
 // Roles: sixteen warps (MLA eight) softmax, rescaling and output, two threads to a query row; one
-// (MLA four) brings Q and, through the page table, K and V rows into a ring of stages; one thread of the next issues the
-// MMAs. Whole tiles of pages of 8, 16, 32 or 64 slots, or a multiple of 128, come
+// (MLA four) brings Q and, through the page table, K and V rows into a ring of stages; a thread for each
+// query tile issues the MMAs. Whole tiles of pages of 8, 16, 32 or 64 slots, or a multiple of 128, come
 // as tensor-map copies, one per page and 64 columns; tiles with tokens left out and other page sizes
 // as 16-byte cp.async, zero-filled where a token has no slot, so that nothing of a row that no token
 // holds is ever multiplied. Tokens that not all rows of a block see are: their V times a weight of 0,
@@ -43,15 +43,14 @@ constexpr int kMasks = 8;              // tiles whose token masks are kept
 constexpr int kSegs = 8;               // segments that are kept
 
 // DK, DV: 64-column chunks of K and of the CTA's V columns; QT: tiles of query rows; UC: chunks
-// per ring stage; NST: ring stages; NL: warps that load K and V;
-// SW: threads to a query row.
-template <int DK_, int DV_, int QT_, int UC_, int NST_, int NL_, int SW_>
+// per ring stage; NST: ring stages; NL: warps that load K and V.
+template <int DK_, int DV_, int QT_, int UC_, int NST_, int NL_>
 struct Shape {
-  static constexpr int DK = DK_, DV = DV_, QT = QT_, UC = UC_, NST = NST_, NL = NL_, SW = SW_;
-  // softmax warps; NL loading warps, the MMA warp, two that look at V
-  static constexpr int kSoft = 4 * SW, kMma = kSoft + NL, kLook0 = kMma + 1, kLook = 2;
+  static constexpr int DK = DK_, DV = DV_, QT = QT_, UC = UC_, NST = NST_, NL = NL_;
+  // softmax warps; NL loading warps, an MMA warp for each query tile, one that looks at V
+  static constexpr int kSoft = 8 * QT, kMma = kSoft + NL, kLook = kMma + QT;
   static constexpr bool kTwo = QT == 2;
-  static constexpr int kThr = 32 * (kLook0 + kLook);
+  static constexpr int kThr = 32 * (kLook + 1);
   // With two query tiles the softmax warps take registers of the others; whole warpgroups
   static constexpr int kRegsSoft = 104, kRegsRest = 64;
   static constexpr int kRegs = 32 * kSoft * kRegsSoft + (kThr - 32 * kSoft) * kRegsRest;
@@ -59,14 +58,14 @@ struct Shape {
   static constexpr int q = 0;
   static constexpr int ring = QT * DK * kChunk;
   static constexpr int mask = ring + NST * kStage;  // uint32 [kMasks][4]
-  static constexpr int xch = mask + kMasks * 16;    // float [SW][kRow]: maxima, sums
-  static constexpr int bar = xch + SW * kRow * 4;
+  static constexpr int xch = mask + kMasks * 16;    // float [2 QT][kRow]: maxima, sums
+  static constexpr int bar = xch + 2 * QT * kRow * 4;
   // mbarriers
   static constexpr int full = 0, empty = NST, q_full = empty + NST, q_empty = q_full + 1,
                        s_full = q_empty + 1, p_full = s_full + 2, pv_done = p_full + 2,
                        o_free = pv_done + 1, o_full = o_free + 1,
                        mk_full = o_full + 2, sg_full = mk_full + kMasks, last = sg_full + kSegs,
-                       n_bar = last + 1;
+                       turn = last + 2, n_bar = turn + 2;
   static constexpr int misc = bar + n_bar * 8;  // TMEM address, give-up flag, odd values
   static constexpr int walk = misc + 16;        // ChunkWalk
   static constexpr int seg = walk + sizeof(ChunkWalk);  // ChunkSegment [kSegs]
@@ -80,9 +79,9 @@ struct Shape {
   static_assert(!kTwo || kThr % 128 == 0, "whole warpgroups");
 };
 
-using Gqa128 = Shape<2, 2, 2, 2, 5, 1, 4>;
-using Gqa64 = Shape<1, 1, 2, 1, 10, 1, 4>;
-using Mla512 = Shape<9, 4, 1, 1, 5, 4, 2>;
+using Gqa128 = Shape<2, 2, 2, 2, 5, 1>;
+using Gqa64 = Shape<1, 1, 2, 1, 10, 1>;
+using Mla512 = Shape<9, 4, 1, 1, 5, 4>;
 
 // Tensor maps of a call: pool rows of the layer (boxes of 64 columns and `box` slots) and query
 // rows (64 columns of a block's heads, of all its tokens or of one).
@@ -131,21 +130,25 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
   if (tid == 0) {
     for (int i = 0; i < S::NST; ++i) {
       ptx::mbar_init(bar(S::full + i), 32 * S::NL);
-      ptx::mbar_init(bar(S::empty + i), 1);
+      ptx::mbar_init(bar(S::empty + i), S::QT);
     }
     ptx::mbar_init(bar(S::q_full), 1);
-    ptx::mbar_init(bar(S::q_empty), 1);
+    ptx::mbar_init(bar(S::q_empty), S::QT);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bar(S::s_full + i), 1);
-      ptx::mbar_init(bar(S::p_full + i), S::kSoft);
+      ptx::mbar_init(bar(S::p_full + i), 8);
       ptx::mbar_init(bar(S::o_full + i), 1);
     }
     ptx::mbar_init(bar(S::pv_done), 1);
-    ptx::mbar_init(bar(S::o_free), S::kSoft + S::kLook);
+    ptx::mbar_init(bar(S::o_free), S::kSoft);
     for (int i = 0; i < kMasks; ++i) ptx::mbar_init(bar(S::mk_full + i), 1);
     for (int i = 0; i < kSegs; ++i) ptx::mbar_init(bar(S::sg_full + i), 1);
-    ptx::mbar_init(bar(S::last), 1);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(bar(S::last + i), 1);
+      ptx::mbar_init(bar(S::turn + i), 1);
+    }
     ptx::fence_mbar_init();
+    ptx::mbar_arrive(bar(S::turn));  // the first query tile begins
     *gave_up = !begins;
     *odd = 0;
     ptx::prefetch_map(&maps.k);
@@ -186,11 +189,11 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
 
   if (warp < S::kSoft) {
     if (S::kTwo) ptx::regs_more<S::kRegsSoft>();
-    // ---- softmax: all warps on one S tile at a time, SW threads (of as many warps) to a query row,
-    // kCols tokens of the tile and as large a part of O's columns each. That is what makes the way
-    // from S to P short: while it is gone the tensor core has the other tile's products only ----
-    constexpr int kCols = kTok / S::SW, kOut = S::DV * 64 / S::SW;
-    const int qr = warp >> 2;                      // the thread's part of the tokens and columns
+    // ---- softmax: two threads (of two warps) to a query row, kCols tokens of each tile and half of
+    // O's columns each; of two query tiles each has warps of its own ----
+    constexpr int kCols = kTok / 2, kOut = S::DV * 32;
+    const int w = warp >> 3;                       // query tile
+    const int qr = (warp >> 2) & 1;                // the thread's half of the tokens and columns
     const int lane_row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     // (a scale of 0 is one that makes nothing of any score: -inf, where a token is not seen, times
@@ -198,132 +201,123 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
     const float c = fmaxf(fabsf(a.scale) * kLog2e, 1.2e-38f);
     const bool flip = a.scale < 0.f;
     const float inf = __int_as_float(0x7f800000);
-    float *xch = reinterpret_cast<float *>(smem + S::xch);  // [part][row]
-    const int group = 3 + (warp & 3);  // named barrier of the rows' warps
+    float *xch = reinterpret_cast<float *>(smem + S::xch) + 2 * w * kRow;  // [half][row]
+    const int pair = 3 + w * 4 + (warp & 3);  // named barrier of a row's two warps
     auto arrive = [&](uint32_t b) {  // once for the warp
       __syncwarp();
       if (lane == 0 && !dead) ptx::mbar_arrive(b);
     };
-    // the sum over a row's threads
-    auto row_sum = [&](float v) {
-      xch[qr * kRow + lane_row] = v;
-      ptx::barrier_sync(group, 32 * S::SW);
-      float sum = 0.f;
-#pragma unroll
-      for (int k = 0; k < S::SW; ++k) sum += xch[k * kRow + lane_row];
-      ptx::barrier_sync(group, 32 * S::SW);
-      return sum;
-    };
-    // A thread's row of an S tile, or of the tiles of tokens that the tile takes.
-    struct Row {
-      int i;            // its row of the block
-      int see0, see1;   // tokens that it sees
-      int in0, in1;     // tiles of which all the warp's rows see the warp's part
-      float m;
-      f32x2 l;
-      bool live;        // a warp without rows only keeps step
-    };
-    auto begin = [&](const ChunkSegment &s, int i) {
-      const int rows = s.ntok * s.heads;
-      Row r;
-      r.i = i;
-      int tok, h;
-      chunk_row(a, s, i < rows ? i : 0, &tok, &h);
-      // a thread without a row sees all, against a maximum that leaves nothing
-      r.see1 = i < rows ? s.first + tok + 1 : 0x7FFFFFFF;
-      r.see0 = i < rows ? first_seen(a, s.first + tok) : 0;
-      r.in0 = (__reduce_max_sync(0xffffffffu, r.see0) - kCols * qr + kTok - 1) >> kTokSh;
-      r.in1 = flip ? 0 : (__reduce_min_sync(0xffffffffu, r.see1) - kCols * (qr + 1) + kTok) >> kTokSh;
-      r.m = i < rows ? -inf : inf;
-      r.l = f2(0.f, 0.f);
-      r.live = i - lane < rows;
-      return r;
-    };
-    uint32_t ph = 0;     // parity of each S buffer, a bit each
+    uint32_t mine = 0;   // tiles of this warp so far: phases of its buffers
     uint32_t seen = 0;   // tiles of the CTA's segments so far
-    uint32_t tiles = 0;  // one query tile: tile k has S buffer k % 2
     ChunkSegment last = {};
     while (const ChunkSegment *sp = take_segment()) {
       const ChunkSegment &s = *sp;
       const uint32_t parity = (seg_no - 1) & 1;
       if (tid == 0) last = s;
       const int n = s.t1 - s.t0, tile0 = s.t0, rows = s.ntok * s.heads;
-      // the steps of the MMA thread
-      const bool pairs = S::kTwo && rows > kRow;
-      const int steps = pairs ? 2 * n : n;
-      Row r = begin(s, lane_row), other = r;
-      if (pairs) other = begin(s, kRow + lane_row);
-#pragma unroll 1
-      for (int v = 0; v < steps; ++v) {
-        const int t = S::kTwo ? v & 1 : 0, i = pairs ? v >> 1 : v;
-        const uint32_t b = S::kTwo ? t : (tiles + v) & 1;
-        const uint32_t o_t = tmem + S::o_col + t * 128 + lane_off + qr * kOut;
-        wait(bar(S::s_full) + 8 * b, ph >> b & 1);
-        ph ^= 1u << b;
-        __syncwarp();
-        ptx::tc_fence_after();
-        if (r.live) {
-          const uint32_t s_t = tmem + b * 128 + qr * kCols + lane_off;
-          uint32_t x[kCols];
-#pragma unroll
-          for (int k = 0; k < kCols; k += 32) ptx::tmem_ld32(s_t + k, x + k);
-          // the tile's mask, which is there before S is
+      const bool turns = S::kTwo && rows <= kRow;  // the tiles of tokens in turn
+      const int i_row = (turns ? 0 : kRow * w) + lane_row;
+      const bool live = i_row - lane < rows;  // a warp without rows only keeps step
+      int tok, h;
+      chunk_row(a, s, i_row < rows ? i_row : 0, &tok, &h);
+      // a thread without a row sees all, against a maximum that leaves nothing
+      const int see1 = i_row < rows ? s.first + tok + 1 : 0x7FFFFFFF;
+      const int see0 = i_row < rows ? first_seen(a, s.first + tok) : 0;
+      // tiles of which all the warp's rows see the warp's half
+      const int in0 = (__reduce_max_sync(0xffffffffu, see0) - kCols * qr + kTok - 1) >> kTokSh;
+      const int in1 =
+          flip ? 0 : (__reduce_min_sync(0xffffffffu, see1) - kCols * (qr + 1) + kTok) >> kTokSh;
+      float m = i_row < rows ? -inf : inf;
+      f32x2 la = f2(0.f, 0.f), lb = la;
+      const uint32_t o_t = tmem + S::o_col + w * 128 + lane_off + qr * kOut;
+      bool done = false;  // a tile of this segment
+      for (int i = turns ? w : 0; i < n; i += turns ? 2 : 1, ++mine) {
+        const uint32_t b = S::kTwo ? w : mine & 1;
+        uint2 msk;
+        bool plain;
+        // The tile's mask. It is there before S is; of a segment's first tile it is read after S, as
+        // this thread may be more tiles ahead of the loader than masks are kept
+        auto read_mask = [&]() {
           const uint32_t mk = (seen + i) % kMasks;
           wait(bar(S::mk_full) + 8 * mk, (seen + i) / kMasks & 1);
-          const uint32_t *mask = reinterpret_cast<const uint32_t *>(smem + S::mask + 16 * mk) +
-                                 qr * (kCols / 32);
-          uint32_t msk[kCols / 32], all = 0xffffffffu;
-#pragma unroll
-          for (int k = 0; k < kCols / 32; ++k) all &= msk[k] = mask[k];
-          const int tile = tile0 + i;
-          const bool plain = tile >= r.in0 && tile < r.in1 && all == 0xffffffffu;
-          ptx::tmem_ld_wait_all<kCols>(x);
+          __syncwarp();
+          msk = *reinterpret_cast<const uint2 *>(smem + S::mask + 16 * mk + 8 * qr);
+          plain = tile0 + i >= in0 && tile0 + i < in1 && (msk.x & msk.y) == 0xffffffffu;
+        };
+        if (live && done) read_mask();
+        wait(bar(S::s_full) + 8 * b, (S::kTwo ? mine : mine >> 1) & 1);
+        __syncwarp();
+        ptx::tc_fence_after();
+        if (live) {
+          const uint32_t s_t = tmem + b * 128 + qr * kCols + lane_off;
+          uint32_t x[32];
+          ptx::tmem_ld32(s_t, x);
+          if (!done) read_mask();
           if (!plain) {
-            if (flip) {
-#pragma unroll
-              for (int e = 0; e < kCols; ++e) x[e] ^= 0x80000000u;
-            }
-#pragma unroll
-            for (int k = 0; k < kCols / 32; ++k) {
-              const int t0 = (tile << kTokSh) + kCols * qr + 32 * k;
-              const int from = r.see0 - t0, to = r.see1 - t0;
+            const int t0 = ((tile0 + i) << kTokSh) + kCols * qr;
+            auto seen_of = [&](int from, int to) {  // of 32 tokens, those in [from, to)
               const uint32_t up = from <= 0 ? 0xffffffffu : from >= 32 ? 0u : 0xffffffffu << from;
               const uint32_t dn = to >= 32 ? 0xffffffffu : to <= 0 ? 0u : (1u << to) - 1u;
-              const uint32_t bits = msk[k] & up & dn;
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                x[32 * k + e] = bits & (1u << e) ? x[32 * k + e] : 0xff800000u;
-            }
+              return up & dn;
+            };
+            msk.x &= seen_of(see0 - t0, see1 - t0);
+            msk.y &= seen_of(see0 - t0 - 32, see1 - t0 - 32);
           }
-          auto y = [&](int e) { return __uint_as_float(x[e]); };
+          float base = m > -inf ? m * c : 0.f;
+          uint32_t p[kCols / 2];
+          f32x2 ha, hb;       // this tile's sums
           float top;
-          {
-            float u[4];
+          // The weights against `base`, their sums and the maximum on the way, 32 columns of S at a
+          // time, the first already on their way into x
+          auto weights = [&]() {
+            ha = hb = f2(0.f, 0.f);
+            float t0 = -inf, t1 = -inf;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) u[k] = fmaxf(y(k), y(k + 4));
+            for (int g = 0; g < 2; ++g) {
+              if (g) ptx::tmem_ld32(s_t + 32, x);
+              ptx::tmem_ld_wait_all<32>(x);
+              if (!plain) {
+                if (flip) {
 #pragma unroll
-            for (int e = 8; e < kCols; e += 8)
+                  for (int e = 0; e < 32; ++e) x[e] ^= 0x80000000u;
+                }
+                const uint32_t bits = g ? msk.y : msk.x;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) u[k] = fmaxf(fmaxf(u[k], y(e + k)), y(e + k + 4));
-            top = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3]));
-          }
-          // the maximum is raised where any part of the row wants it
-          if (ptx::barrier_or(group, 32 * S::SW,
-                              (r.m == -inf && top > -inf) || (top - r.m) * c > 8.f)) {
+                for (int e = 0; e < 32; ++e) x[e] = bits & (1u << e) ? x[e] : 0xff800000u;
+              }
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const float y0 = __uint_as_float(x[e]), y1 = __uint_as_float(x[e + 1]);
+                const float p0 = exp2_approx(fmaf(y0, c, -base));
+                const float p1 = exp2_approx(fmaf(y1, c, -base));
+                float &t = e & 2 ? t1 : t0;
+                t = fmaxf(fmaxf(t, y0), y1);
+                if (e & 2)
+                  hb = add2(hb, f2(p0, p1));
+                else
+                  ha = add2(ha, f2(p0, p1));
+                p[16 * g + e / 2] = pack_bf16(p0, p1);
+              }
+            }
+            top = fmaxf(t0, t1);
+          };
+          weights();
+          // the weights stand unless the maximum is to be raised, for either half of the row
+          if (ptx::barrier_or(pair, 64, (m == -inf && top > -inf) || (top - m) * c > 8.f)) {
             xch[qr * kRow + lane_row] = top;
-            ptx::barrier_sync(group, 32 * S::SW);
-#pragma unroll
-            for (int k = 0; k < S::SW; ++k) top = fmaxf(top, xch[k * kRow + lane_row]);
-            const bool first = r.m == -inf && top > -inf;
-            const bool up = first || (top - r.m) * c > 8.f;
-            const float f = up ? (first ? 0.f : exp2_approx((r.m - top) * c)) : 1.f;
-            if (up) r.m = top;
-            r.l = fma2(r.l, f2(f, f), f2(0.f, 0.f));
-            if (v >= (S::kTwo ? 2 : 1)) {
+            ptx::barrier_sync(pair, 64);
+            top = fmaxf(top, xch[(qr ^ 1) * kRow + lane_row]);
+            const bool first = m == -inf && top > -inf;
+            const bool up = first || (top - m) * c > 8.f;
+            const float f = up ? (first ? 0.f : exp2_approx((m - top) * c)) : 1.f;
+            if (up) m = top;
+            la = fma2(la, f2(f, f), f2(0.f, 0.f));
+            lb = fma2(lb, f2(f, f), f2(0.f, 0.f));
+            if (done) {
               // P V of the tile before is complete: S of this one says so, where it was issued
               // behind it (else S says so of the one before that, and the parity is unambiguous)
               if (!S::kTwo) {
-                wait(bar(S::pv_done), (tiles + v - 1) & 1);
+                wait(bar(S::pv_done), (mine - 1) & 1);
                 __syncwarp();
                 ptx::tc_fence_after();
               }
@@ -338,122 +332,104 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
               }
               ptx::tmem_st_wait();
             }
-            // (what the row's threads have scaled is multiplied after all of them have arrived)
-            ptx::barrier_sync(group, 32 * S::SW);
+            // (what a row's threads have scaled is multiplied after both have arrived)
+            ptx::barrier_sync(pair, 64);
+            base = m > -inf ? m * c : 0.f;
+            ptx::tmem_ld32(s_t, x);
+            weights();
           }
-          const float base = r.m > -inf ? r.m * c : 0.f;
-          f32x2 l2 = f2(0.f, 0.f);
-          uint32_t p[kCols / 2];
-#pragma unroll
-          for (int e = 0; e < kCols; e += 2) {
-            const float p0 = exp2_approx(fmaf(y(e), c, -base));
-            const float p1 = exp2_approx(fmaf(y(e + 1), c, -base));
-            if (e & 2)
-              l2 = add2(l2, f2(p0, p1));
-            else
-              r.l = add2(r.l, f2(p0, p1));
-            p[e / 2] = pack_bf16(p0, p1);
-          }
-          r.l = add2(r.l, l2);
-          // P over the thread's part of S
-          if constexpr (kCols == 64)
-            ptx::tmem_st32(s_t, p);
-          else
-            ptx::tmem_st16(s_t, p);
+          la = add2(la, ha);
+          lb = add2(lb, hb);
+          ptx::tmem_st32(s_t, p);  // P over its half of S
           ptx::tmem_st_wait();
         }
         ptx::tc_fence_before();
         arrive(bar(S::p_full) + 8 * b);
-        if (S::kTwo) {  // the other tile's turn
-          const Row x = r;
-          r = other;
-          other = x;
-        }
+        done = true;
       }
       seen += n;
-      tiles += n;
-      if (S::kTwo && (steps & 1)) {
-        const Row x = r;
-        r = other;
-        other = x;
-      }
       // ---- output ----
-      const bool whole = chunk_whole(s), whole32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
-      auto sum_of = [&](const Row &x) {
+      wait(bar(S::o_full) + 8 * w, parity);
+      if (turns) wait(bar(S::o_full) + 8 * (w ^ 1), parity);
+      __syncwarp();
+      ptx::tc_fence_after();
+      float l, f0 = 1.f, f1 = 0.f;  // factors of this query tile's O and of the other's
+      {
         float l0, l1;
-        f2_split(x.l, l0, l1);
-        return row_sum(l0 + l1);
-      };
-      // of a block of one query tile the two turns' sums and O are joined
-      const bool turns = S::kTwo && !pairs;
+        f2_split(add2(la, lb), l0, l1);
+        l = l0 + l1;
+      }
+      if (turns) {  // the two turns' sums and O are joined
+        float *all = reinterpret_cast<float *>(smem + S::xch) + lane_row;
+        xch[qr * kRow + lane_row] = m;
+        ptx::barrier_sync(2, 4 * kRow);
+        const float mo = all[2 * (w ^ 1) * kRow], top = fmaxf(m, mo);  // (never NaN)
+        f0 = m == -inf ? 0.f : exp2_approx((m - top) * c);
+        f1 = mo == -inf ? 0.f : exp2_approx((mo - top) * c);
+        m = top;
+        ptx::barrier_sync(2, 4 * kRow);
+        xch[qr * kRow + lane_row] = n > w ? l * f0 : 0.f;
+        ptx::barrier_sync(2, 4 * kRow);
+        l = (all[0] + all[kRow]) + (all[2 * kRow] + all[3 * kRow]);
+      } else if (live) {
+        xch[qr * kRow + lane_row] = l;
+        ptx::barrier_sync(pair, 64);
+        l = xch[lane_row] + xch[kRow + lane_row];
+      }
+      if (live) {
+        const bool ok = l != 0.f && !*gave_up;
+        const float inv = 1.f / l, g0 = f0 * inv, g1 = f1 * inv;
+        const bool whole = chunk_whole(s), whole32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
+        const long long rh = (long long)(s.row + tok) * a.hq + h;
+        const long long place = (long long)(2 * blockIdx.x + (s.carry() ? 0 : 1)) * a.shape.rb + i_row;
+        __nv_bfloat16 *out = a.out + rh * a.dv + s.part * a.shape.vw;
+        float *part = places.o + place * a.shape.vw;
+        const bool write = i_row < rows && !*gave_up;
+        // of a row's columns, this thread's: half, in turns a quarter
+        const int cols = kOut / (turns ? 2 : 1), from = (turns ? 2 * w + qr : qr) * cols;
+        const bool has = !turns || n > w, other = turns && n > 1 - w;
+        const uint32_t o_mine = tmem + S::o_col + lane_off + w * 128;
+        const uint32_t o_other = tmem + S::o_col + lane_off + (w ^ 1) * 128;
 #pragma unroll 1
-      for (int t = 0; t < (pairs ? 2 : 1); ++t) {
-        wait(bar(S::o_full) + 8 * t, parity);
-        if (turns) wait(bar(S::o_full) + 8, parity);
-        __syncwarp();
-        ptx::tc_fence_after();
-        if (r.live) {
-          float l = sum_of(r), m = r.m, f0 = 1.f, f1 = 0.f;
-          const bool second = turns && n > 1;
-          if (second) {
-            const float l1 = sum_of(other), top = fmaxf(m, other.m);  // (never NaN)
-            f0 = m == -inf ? 0.f : exp2_approx((m - top) * c);
-            f1 = other.m == -inf ? 0.f : exp2_approx((other.m - top) * c);
-            l = l * f0 + l1 * f1;
-            m = top;
-          }
-          const bool ok = l != 0.f && !*gave_up;
-          const float inv = 1.f / l, g0 = f0 * inv, g1 = f1 * inv;
-          int tok, h;
-          chunk_row(a, s, r.i < rows ? r.i : 0, &tok, &h);
-          const long long rh = (long long)(s.row + tok) * a.hq + h;
-          const long long place = (long long)(2 * blockIdx.x + (s.carry() ? 0 : 1)) * a.shape.rb + r.i;
-          __nv_bfloat16 *out = a.out + rh * a.dv + s.part * a.shape.vw + qr * kOut;
-          float *part = places.o + place * a.shape.vw + qr * kOut;
-          const bool write = r.i < rows && !*gave_up;
-          const uint32_t o_t = tmem + S::o_col + t * 128 + lane_off + qr * kOut;
-#pragma unroll 1
-          for (int j = 0; j < kOut; j += 16) {
-            uint32_t z[16];
-            ptx::tmem_ld16(o_t + j, z);
-            ptx::tmem_ld_wait_all<16>(z);
+        for (int j = from; j < from + cols; j += 16) {
+          uint32_t z[16];
+          ptx::tmem_ld16(o_mine + j, z);
+          ptx::tmem_ld_wait_all<16>(z);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            z[e] = ok && has ? __float_as_uint(__uint_as_float(z[e]) * g0) : 0u;
+          if (other) {
+            uint32_t z1[16];
+            ptx::tmem_ld16(o_other + j, z1);
+            ptx::tmem_ld_wait_all<16>(z1);
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              z[e] = ok ? __float_as_uint(__uint_as_float(z[e]) * g0) : 0u;
-            if (second) {
-              uint32_t z1[16];
-              ptx::tmem_ld16(o_t + 128 + j, z1);
-              ptx::tmem_ld_wait_all<16>(z1);
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                z[e] = ok ? __float_as_uint(fmaf(__uint_as_float(z1[e]), g1, __uint_as_float(z[e])))
-                          : 0u;
-            }
-            if (write && whole) {
-              uint32_t u[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                u[e] = pack_bf16(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1]));
-              if (whole32) {
-                ptx::stg32(out + j, u);
-              } else {
-                *reinterpret_cast<uint4 *>(out + j) = make_uint4(u[0], u[1], u[2], u[3]);
-                *reinterpret_cast<uint4 *>(out + j + 8) = make_uint4(u[4], u[5], u[6], u[7]);
-              }
-            } else if (write) {
-              ptx::stg32(part + j, z);
-              ptx::stg32(part + j + 8, z + 8);
-            }
+              z[e] = ok ? __float_as_uint(fmaf(__uint_as_float(z1[e]), g1, __uint_as_float(z[e])))
+                        : 0u;
           }
-          if (write && qr == 0) {
-            const float z = l != 0.f ? (m * c + log2f(l)) * kLn2 : -inf;
-            if (!whole)
-              places.lse[place] = z;
-            else if (s.part == 0)
-              a.lse[rh] = z;
+          if (write && whole) {
+            uint32_t u[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              u[e] = pack_bf16(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1]));
+            if (whole32) {
+              ptx::stg32(out + j, u);
+            } else {
+              *reinterpret_cast<uint4 *>(out + j) = make_uint4(u[0], u[1], u[2], u[3]);
+              *reinterpret_cast<uint4 *>(out + j + 8) = make_uint4(u[4], u[5], u[6], u[7]);
+            }
+          } else if (write) {
+            ptx::stg32(part + j, z);
+            ptx::stg32(part + j + 8, z + 8);
           }
         }
-        r = other;
+        if (write && from == 0) {
+          const float z = l != 0.f ? (m * c + log2f(l)) * kLn2 : -inf;
+          if (!whole)
+            places.lse[place] = z;
+          else if (s.part == 0)
+            a.lse[rh] = z;
+        }
       }
       ptx::tc_fence_before();
       arrive(bar(S::o_free));
@@ -636,19 +612,22 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
       if (!S::kTwo) bring(false, n - 1, cur);
     }
     ptx::cp_async_wait_all();
-  } else if (warp > S::kMma) {
+  } else if (warp == S::kLook) {
     if (S::kTwo) ptx::regs_fewer<S::kRegsRest>();
-    // ---- two warps look at V of the tokens that only some of a block's rows see ----
-    while (const ChunkSegment *sp = take_segment()) {
-      if (!sp->carry() && chunk_odd(a, *sp, warp - S::kLook0, S::kLook)) *odd = 1;
-      __syncwarp();
-      if (lane == 0 && !dead) ptx::mbar_arrive(bar(S::o_free));
-    }
+    // ---- V of the tokens that only some of a block's rows see, at a pace of its own ----
+    ChunkWalk look;
+    look.start(a, st, blockIdx.x);
+    ChunkSegment s;
+    bool found = false;
+    while (begins && look.next(a, &s)) found |= !s.carry() && chunk_odd<S::DV * 8>(a, s, 0, 1);
+    if (found) *odd = 1;
   } else {
     if (S::kTwo) ptx::regs_fewer<S::kRegsRest>();
-    // ---- MMAs, one thread. Issuing an MMA takes a few instructions only: the descriptors of
+    // ---- MMAs, one thread for each query tile: a wait, a commit and the way round the loop take it
+    // some hundred cycles each, and while it is on them the other's products go on. The descriptors of
     // a tile's steps differ by constants ----
-    if (warp == S::kMma && ptx::elect_one()) {
+    if (ptx::elect_one()) {
+      const int t = warp - S::kMma;
       constexpr uint32_t id_s =
           1u << 4 | 1u << 7 | 1u << 10 | (kTok >> 3) << 17 | (kRow >> 4) << 24;
       // V is MN-major
@@ -656,24 +635,20 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
           1u << 4 | 1u << 7 | 1u << 10 | 1u << 16 | (S::UC * 64 >> 3) << 17 | (kRow >> 4) << 24;
       constexpr int ku = S::DK / S::UC, vu = S::DV / S::UC;  // stages of a K and a V tile
       const uint32_t ring = sb + S::ring;
-      Place<S::NST> kp, vp;                              // the next K and V tile
-      uint32_t tiles = 0;                                // one query tile: k has S buffer k % 2
+      Place<S::NST> kp;                                  // the next K tile (two query tiles: stage)
+      uint32_t tiles = 0;                                // tiles so far; one query tile: k has S buffer
+                                                         // k % 2
       uint32_t p_ph = 0;                                 // a bit for each S buffer
-      const uint32_t q0 = desc_k(sb + S::q);             // [chunk][query tile][128 rows]
-      auto landed = [&](const Place<S::NST> &at) {
-        wait(bar(S::full) + 8 * at.st, at.ph);
-      };
       auto commit = [&](int b) {
         if (!dead) ptx::mma_commit(bar(b));
       };
-      // S of query tile t into TMEM buffer b against the K tile at kp; lands, frees: the first and
-      // the last reader of its stages
-      auto mma_s = [&](int t, uint32_t b, bool lands, bool frees) {
-        const uint32_t d = tmem + b * 128, qt = q0 + t * (kChunk >> 4);
-        Place<S::NST> at = kp;
+      // S of the query tile at qt into TMEM buffer b against the K tile at `at`; `passes` is called
+      // when the MMAs have been issued
+      auto mma_s = [&](uint32_t qt, uint32_t b, Place<S::NST> &at, auto passes) {
+        const uint32_t d = tmem + b * 128;
 #pragma unroll
         for (int u = 0; u < ku; ++u) {
-          if (lands) landed(at);
+          wait(bar(S::full) + 8 * at.st, at.ph);
           if (dead) return;
           const uint32_t k = desc_k(ring + at.st * S::kStage);
 #pragma unroll
@@ -681,79 +656,112 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
             ptx::mma_bf16(
                 d, desc(qt + (((u * S::UC + (x >> 2)) * S::QT * kChunk + (x & 3) * 32) >> 4)),
                 desc(k + (((x >> 2) * kChunk + (x & 3) * 32) >> 4)), id_s, (u | x) ? 1u : 0u);
-          if (frees) ptx::mma_commit(bar(S::empty) + 8 * at.st);
+          if (u == ku - 1) {
+            passes();
+            ptx::mma_commit(bar(S::s_full) + 8 * b);
+          }
+          ptx::mma_commit(bar(S::empty) + 8 * at.st);
           at.advance(1);
         }
-        ptx::mma_commit(bar(S::s_full) + 8 * b);
       };
-      // O of tile t (+)= P in buffer b times the V tile at vp
-      auto mma_o = [&](int t, uint32_t b, bool first_tile, bool lands, bool frees) {
-        const uint32_t p = tmem + b * 128, d = tmem + S::o_col + t * 128;
-        Place<S::NST> at = vp;
-        if (lands) landed(at);  // before P is, as a rule
-        wait(bar(S::p_full) + 8 * b, (p_ph >> b) & 1);
+      // What O of that buffer waits for.
+      auto ready_o = [&](uint32_t b, const Place<S::NST> &at) {
+        wait(bar(S::full) + 8 * at.st, at.ph);  // before P is, as a rule
+        wait(bar(S::p_full) + 8 * b, p_ph >> b & 1);
+        p_ph ^= 1u << b;
+      };
+      // O at d (+)= P in buffer b times the V tile at `at`
+      auto mma_o = [&](uint32_t d, uint32_t b, bool first_tile, Place<S::NST> &at) {
+        const uint32_t p = tmem + b * 128;
         if (dead) return;
         ptx::tc_fence_after();
 #pragma unroll
         for (int u = 0; u < vu; ++u) {
-          if (lands && u > 0) landed(at);
+          if (u > 0) wait(bar(S::full) + 8 * at.st, at.ph);
           if (dead) return;
           const uint32_t v = desc_mn(ring + at.st * S::kStage);
 #pragma unroll
           for (int x = 0; x < kTok / 16; ++x) {
-            // P of a softmax thread's tokens is in the first half of its part of S
-            constexpr int kPart = kTok / S::SW / 16;  // steps of a part
-            ptx::mma_bf16_ta(d + u * S::UC * 64, p + x / kPart * (16 * kPart) + x % kPart * 8,
+            // P of tokens 0-63 is in columns 0-31 of S, of 64-127 in 64-95
+            ptx::mma_bf16_ta(d + u * S::UC * 64, p + 8 * x + (x < kTok / 32 ? 0 : 32),
                              desc(v + x * (2048 >> 4)), id_o, x ? 1u : (first_tile ? 0u : 1u));
           }
-          if (frees) ptx::mma_commit(bar(S::empty) + 8 * at.st);
+          ptx::mma_commit(bar(S::empty) + 8 * at.st);
           at.advance(1);
         }
-        p_ph ^= 1u << b;
         if (!S::kTwo) ptx::mma_commit(bar(S::pv_done));
       };
+      uint32_t turns = 0;  // of this thread so far
+      auto pass = [&]() {
+        if (!dead) ptx::mbar_arrive(bar(S::turn) + 8 * (t ^ 1));
+      };
+      auto stay = []() {};
+      const uint32_t q0 = desc_k(sb + S::q);  // [chunk][query tile][128 rows]
       while (const ChunkSegment *sp = take_segment()) {
         const int n = sp->t1 - sp->t0;
         const bool before = seg_no > 1;
+        auto o_free = [&]() {  // O of the segment before has been read
+          if (before) wait(bar(S::o_free), seg_no & 1);
+        };
         wait(bar(S::q_full), (seg_no - 1) & 1);
-        vp = kp;
         if constexpr (S::kTwo) {
-          // Steps, each S of one query tile and then its P V: of a pair, S of the two query tiles
-          // against each tile of tokens; of one query tile, S in the two buffers in turn. S of step
-          // v + 2 follows P V of step v.
           const bool pairs = sp->ntok * sp->heads > kRow;
-          const int steps = pairs ? 2 * n : n;
-          vp.advance(ku);
+          const uint32_t o = tmem + S::o_col + t * 128;
+          if (pairs) {
+            // Of a pair of query tiles each takes every tile of tokens. They go in turn, each P V of
+            // its tile before and S of the next: without an order the two come to do the same at the
+            // same time, and the tensor core waits for both softmaxes (4100 cycles a tile).
 #pragma unroll 1
-          for (int v = -2; v < steps; ++v) {
-            const int t = v & 1;
-            const bool second = !pairs || t, lands = !pairs || !t;
-            if (v >= 0) {
-              if (v == 0 && before) wait(bar(S::o_free), seg_no & 1);  // O before it has been read
-              mma_o(t, t, v < 2, lands, second);
-              if (v + 2 >= steps) commit(S::o_full + t);
-              if (second) vp.advance(vu + ku);
+            for (int i = 0; i <= n; ++i) {
+              if (i > 0) ready_o(t, kp);
+              if (i == 1) o_free();
+              wait(bar(S::turn) + 8 * t, turns++ & 1);
+              if (i > 0) mma_o(o, t, i == 1, kp);
+              if (i < n)
+                mma_s(q0 + t * (kChunk >> 4), t, kp, pass);
+              else
+                pass();
+              if (i == n - 1) commit(S::q_empty);
             }
-            if (v + 2 < steps) {
-              mma_s(pairs ? t : 0, t, lands, second);
-              if (second) kp.advance(ku + vu);
-              if (v + 3 == steps) commit(S::q_empty);
+          } else {
+            // of a block of one query tile the two take the tiles of tokens in turn, and only give
+            // back the others' stages
+            const int last = n - 1 - ((n - 1 - t) & 1);  // this one's last tile
+            if (last < 0 && !dead) ptx::mbar_arrive(bar(S::q_empty));
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) {
+              if ((i & 1) != t) {
+#pragma unroll 1
+                for (int u = 0; u < ku + vu; ++u) {
+                  wait(bar(S::full) + 8 * kp.st, kp.ph);
+                  if (!dead) ptx::mbar_arrive(bar(S::empty) + 8 * kp.st);
+                  kp.advance(1);
+                }
+                continue;
+              }
+              mma_s(q0, t, kp, stay);
+              if (i == last) commit(S::q_empty);
+              ready_o(t, kp);
+              if (i < 2) o_free();
+              mma_o(o, t, i < 2, kp);
             }
           }
-          if (steps == 1) commit(S::o_full + 1);
+          commit(S::o_full + t);
         } else {
+          Place<S::NST> vp = kp;
           vp.advance(n > 1 ? 2 * ku : ku);
 #pragma unroll 1
           for (int v = -1; v < n; ++v) {
             if (v + 1 < n) {
-              mma_s(0, (tiles + v + 1) & 1, true, true);
-              kp.advance(v == -1 ? ku : ku + vu);
+              mma_s(q0, (tiles + v + 1) & 1, kp, stay);
+              if (v >= 0) kp.advance(vu);
               if (v + 2 == n) commit(S::q_empty);
             }
             if (v >= 0) {
-              if (v == 0 && before) wait(bar(S::o_free), seg_no & 1);
-              mma_o(0, (tiles + v) & 1, v == 0, true, true);
-              vp.advance(v + 2 < n ? vu + ku : vu);
+              if (v == 0) o_free();
+              ready_o((tiles + v) & 1, vp);
+              mma_o(tmem + S::o_col, (tiles + v) & 1, v == 0, vp);
+              if (v + 2 < n) vp.advance(ku);
             }
           }
           commit(S::o_full);
@@ -761,8 +769,8 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
           kp = vp;
         }
       }
-      ptx::mma_commit(bar(S::last));  // no MMA is in flight when the TMEM goes back
-      if (!ptx::mbar_wait(bar(S::last), 0, kPrefixWaitNs)) *gave_up = 1;
+      ptx::mma_commit(bar(S::last + t));  // no MMA is in flight when the TMEM goes back
+      if (!ptx::mbar_wait(bar(S::last + t), 0, kPrefixWaitNs)) *gave_up = 1;
     }
     __syncwarp();
   }
