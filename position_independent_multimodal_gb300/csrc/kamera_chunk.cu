@@ -59,13 +59,12 @@ __global__ void __launch_bounds__(kThr) chunk_gen_kernel(const __grid_constant__
   walk.start(a, st, w);
   ChunkSegment s = {};
   int segments = 0;
-  bool odd = false;
+  bool odd = false;  // an output is not finite
   for (; walk.next(a, &s); ++segments) {
     const int rows = s.ntok * s.heads;
     const int kcol = gqa ? s.kvh * lay.hd : 0, vcol = kcol + s.part * kCols;
     const int cols = min(kCols, a.dv - s.part * kCols);
     __syncthreads();
-    odd |= !s.carry() && chunk_odd<0>(a, s, warp, kThr / 32);
     const int qp = a.dk >> 3;  // 16-byte pieces of a row
     for (int e = tid; e < kRows * qp; e += kThr) {
       const int i = e / qp, p = e - i * qp;
@@ -200,6 +199,7 @@ __global__ void __launch_bounds__(kThr) chunk_gen_kernel(const __grid_constant__
         if (8 * n >= cols) break;
         const int col = 8 * n + 2 * (lane & 3);
         const float v0 = o[n][2 * y] * inv, v1 = o[n][2 * y + 1] * inv;
+        odd |= v0 * 0.f + v1 * 0.f != 0.f;  // not finite
         if (whole)
           *reinterpret_cast<uint32_t *>(a.out + rh * a.dv + s.part * kCols + col) = pack_bf16(v0, v1);
         else
@@ -275,8 +275,8 @@ __device__ __noinline__ void chunk_row_again(const ChunkArgs &a, const ChunkSegm
 }
 
 // Worker blockIdx.x's cut block: a warp to a row, the parts' log-sum-exps a lane each, then four
-// columns a lane. Then, where a worker has found odd values, those of the blocks that the worker
-// starts which multiply such a value for a row that does not see it.
+// columns a lane. Then, where an output of the call is not finite, those of the blocks that the
+// worker starts which multiply a value that is not finite for a row that does not see it.
 __global__ void __launch_bounds__(kJoinThr, 4) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
   __shared__ ChunkScratch<kJoinThr> found;
   const int w = blockIdx.x, lane = threadIdx.x & 31;
@@ -394,13 +394,7 @@ __global__ void __launch_bounds__(kJoinThr, 4) chunk_join_kernel(const __grid_co
   walk.start(a, st, w);
   ChunkSegment s;
   while (walk.next(a, &s)) {
-    // tokens that are multiplied for rows that do not see them: from the first tile's start to the
-    // last one's end
-    const int end = (int)min((long long)s.ctx, ((long long)((s.first + s.ntok - 1) >> a.shape.tile_sh) + 1)
-                                                   << a.shape.tile_sh);
-    ChunkSegment wide = s;
-    wide.ntok = end - s.first;
-    const bool again = !s.carry() && chunk_odd<0>(a, wide, threadIdx.x >> 5, kJoinThr / 32);
+    const bool again = !s.carry() && chunk_odd(a, s, threadIdx.x >> 5, kJoinThr / 32);
     if (__syncthreads_or(again))
       for (int i = first; i < s.ntok * s.heads; i += step) chunk_row_again(a, s, i);
   }

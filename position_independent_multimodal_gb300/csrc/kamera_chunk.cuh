@@ -27,7 +27,7 @@ struct ChunkRecord {
   int h0, part;    // of it: first query head, part of V's columns
   int gave_up;
   int segments;    // segments of the worker
-  int odd;         // 1: chunk_odd holds for a block that starts with it
+  int odd;         // 1: some of its outputs are not finite
   int pad[7];
 };
 
@@ -300,15 +300,12 @@ __device__ __forceinline__ bool odd8(const uint4 &v) {
   return odd_pair(v.x) | odd_pair(v.y) | odd_pair(v.z) | odd_pair(v.w);
 }
 
-// Whether V of tokens that some of the block's rows do not see holds a value that is not finite: of
-// its own new tokens, and of those that the window leaves behind between its first row and its last.
-// Every token that is multiplied for a row which does not see it is such a one of some block. By
-// `warps` whole warps, each its share of 32 tokens at a time: a lane to a token's slot, then a lane to
-// 16 bytes. kPieces: 16-byte pieces of a row's part, a power of two below 64, or 0.
-template <int kPieces>
+// Whether V of tokens that are multiplied for the block, but not seen by all of its rows, holds a value
+// that is not finite: its new tokens behind the first and what follows in its last tile, and those that
+// the window leaves behind between its first row and its last. By `warps` whole warps, each its share
+// of 32 tokens at a time: a lane to a token's slot, then a lane to 16 bytes.
 __device__ __forceinline__ bool chunk_odd(const ChunkArgs &a, const ChunkSegment &s, int warp,
                                           int warps) {
-  if (s.ntok == 1 && s.first + 1 == s.ctx) return false;  // there are no other new tokens
   const DevLayout &lay = a.lay;
   const bool gqa = lay.kind == KAMERA_GQA;
   const int lane = threadIdx.x & 31;
@@ -316,7 +313,8 @@ __device__ __forceinline__ bool chunk_odd(const ChunkArgs &a, const ChunkSegment
   const __nv_bfloat16 *v = (gqa ? a.pool.v : a.pool.k) +
                            (long long)a.layer * a.pool.num_slots * row + (gqa ? s.kvh * lay.hd : 0) +
                            s.part * a.shape.vw;
-  const int pieces = kPieces ? kPieces : min(a.shape.vw, a.dv - s.part * a.shape.vw) >> 3;
+  const int pieces = min(a.shape.vw, a.dv - s.part * a.shape.vw) >> 3;  // of 16 bytes
+  const int sh = a.shape.tile_sh, end = (((s.first + s.ntok - 1) >> sh) + 1) << sh;
   bool odd = false;
   auto slot_at = [&](int t, int to) {
     if (t + lane >= to) return -1;
@@ -326,8 +324,8 @@ __device__ __forceinline__ bool chunk_odd(const ChunkArgs &a, const ChunkSegment
   };
 #pragma unroll 1
   for (int side = 0; side < 2; ++side) {
-    const int from = side ? first_seen(a, s.first) : s.first;
-    const int to = side ? first_seen(a, s.first + s.ntok - 1) : s.first + s.ntok;
+    const int from = side ? first_seen(a, s.first) : s.first + 1;
+    const int to = side ? first_seen(a, s.first + s.ntok - 1) : min(s.ctx, end);
     int next = slot_at(from + 32 * warp, to);
 #pragma unroll 1
     for (int t = from + 32 * warp; t < to; t += 32 * warps) {

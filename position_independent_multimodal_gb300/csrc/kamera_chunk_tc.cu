@@ -18,8 +18,8 @@
 // as tensor-map copies, one per page and 64 columns; tiles with tokens left out and other page sizes
 // as 16-byte cp.async, zero-filled where a token has no slot, so that nothing of a row that no token
 // holds is ever multiplied. Tokens that not all rows of a block see are: their V times a weight of 0,
-// which is no 0 where V is not finite. So two warps look at V of such tokens, and where they find one
-// that is not finite the join kernel takes the blocks that it is in again, token by token.
+// which is no 0 where V is not finite. Where an output is not finite the join kernel therefore looks at
+// V of such tokens, and takes the blocks where one is not finite again, token by token.
 //   GQA: O and S of two query tiles fill the TMEM. A block of more than 128 rows has two tiles of
 //        them that share each K and V tile; of a smaller one (requests that decode) the two take
 //        turns with the tiles of tokens, each with a maximum, sum and O of its own, joined at the
@@ -47,10 +47,10 @@ constexpr int kSegs = 8;               // segments that are kept
 template <int DK_, int DV_, int QT_, int UC_, int NST_, int NL_>
 struct Shape {
   static constexpr int DK = DK_, DV = DV_, QT = QT_, UC = UC_, NST = NST_, NL = NL_;
-  // softmax warps; NL loading warps, an MMA warp for each query tile, one that looks at V
-  static constexpr int kSoft = 8 * QT, kMma = kSoft + NL, kLook = kMma + QT;
+  // softmax warps; NL loading warps, an MMA warp for each query tile
+  static constexpr int kSoft = 8 * QT, kMma = kSoft + NL;
   static constexpr bool kTwo = QT == 2;
-  static constexpr int kThr = 32 * (kLook + 1);
+  static constexpr int kThr = 32 * (kTwo ? (kMma + QT + 3) / 4 * 4 : kMma + QT);
   // With two query tiles the softmax warps take registers of the others; whole warpgroups
   static constexpr int kRegsSoft = 104, kRegsRest = 64;
   static constexpr int kRegs = 32 * kSoft * kRegsSoft + (kThr - 32 * kSoft) * kRegsRest;
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
   // named barriers only, and no barrier gets an arrival that it does not expect.
   bool dead = false;
   auto wait = [&](uint32_t b, uint32_t parity) {
-    if (dead || ptx::mbar_try_wait(b, parity)) return;
+    if (__builtin_expect(dead || ptx::mbar_try_wait(b, parity), 1)) return;
     const uint64_t t0 = ptx::globaltimer();
     while (!ptx::mbar_try_wait_for(b, parity, 20000)) {
       if (*gave_up || ptx::globaltimer() - t0 > a.wait_ns) {
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
           uint32_t x[32];
           ptx::tmem_ld32(s_t, x);
           if (!done) read_mask();
-          if (!plain) {
+          if (__builtin_expect(!plain, 0)) {
             const int t0 = ((tile0 + i) << kTokSh) + kCols * qr;
             auto seen_of = [&](int from, int to) {  // of 32 tokens, those in [from, to)
               const uint32_t up = from <= 0 ? 0xffffffffu : from >= 32 ? 0u : 0xffffffffu << from;
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
             for (int g = 0; g < 2; ++g) {
               if (g) ptx::tmem_ld32(s_t + 32, x);
               ptx::tmem_ld_wait_all<32>(x);
-              if (!plain) {
+              if (__builtin_expect(!plain, 0)) {
                 if (flip) {
 #pragma unroll
                   for (int e = 0; e < 32; ++e) x[e] ^= 0x80000000u;
@@ -303,7 +303,8 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
           };
           weights();
           // the weights stand unless the maximum is to be raised, for either half of the row
-          if (ptx::barrier_or(pair, 64, (m == -inf && top > -inf) || (top - m) * c > 8.f)) {
+          if (__builtin_expect(
+                  ptx::barrier_or(pair, 64, (m == -inf && top > -inf) || (top - m) * c > 8.f), 0)) {
             xch[qr * kRow + lane_row] = top;
             ptx::barrier_sync(pair, 64);
             top = fmaxf(top, xch[(qr ^ 1) * kRow + lane_row]);
@@ -390,6 +391,7 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
         const bool has = !turns || n > w, other = turns && n > 1 - w;
         const uint32_t o_mine = tmem + S::o_col + lane_off + w * 128;
         const uint32_t o_other = tmem + S::o_col + lane_off + (w ^ 1) * 128;
+        float odd_sum = 0.f;
 #pragma unroll 1
         for (int j = from; j < from + cols; j += 16) {
           uint32_t z[16];
@@ -407,6 +409,8 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
               z[e] = ok ? __float_as_uint(fmaf(__uint_as_float(z1[e]), g1, __uint_as_float(z[e])))
                         : 0u;
           }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) odd_sum = fmaf(__uint_as_float(z[e]), 0.f, odd_sum);
           if (write && whole) {
             uint32_t u[8];
 #pragma unroll
@@ -423,6 +427,7 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
             ptx::stg32(part + j + 8, z + 8);
           }
         }
+        if (write && odd_sum != 0.f) *odd = 1;
         if (write && from == 0) {
           const float z = l != 0.f ? (m * c + log2f(l)) * kLn2 : -inf;
           if (!whole)
@@ -612,21 +617,12 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
       if (!S::kTwo) bring(false, n - 1, cur);
     }
     ptx::cp_async_wait_all();
-  } else if (warp == S::kLook) {
-    if (S::kTwo) ptx::regs_fewer<S::kRegsRest>();
-    // ---- V of the tokens that only some of a block's rows see, at a pace of its own ----
-    ChunkWalk look;
-    look.start(a, st, blockIdx.x);
-    ChunkSegment s;
-    bool found = false;
-    while (begins && look.next(a, &s)) found |= !s.carry() && chunk_odd<S::DV * 8>(a, s, 0, 1);
-    if (found) *odd = 1;
   } else {
     if (S::kTwo) ptx::regs_fewer<S::kRegsRest>();
     // ---- MMAs, one thread for each query tile: a wait, a commit and the way round the loop take it
     // some hundred cycles each, and while it is on them the other's products go on. The descriptors of
     // a tile's steps differ by constants ----
-    if (ptx::elect_one()) {
+    if (warp < S::kMma + S::QT && ptx::elect_one()) {
       const int t = warp - S::kMma;
       constexpr uint32_t id_s =
           1u << 4 | 1u << 7 | 1u << 10 | (kTok >> 3) << 17 | (kRow >> 4) << 24;
