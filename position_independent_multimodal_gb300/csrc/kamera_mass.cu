@@ -182,29 +182,39 @@ __global__ void __launch_bounds__(kJoinThr) mass_join_kernel(const __grid_consta
 
 }  // namespace
 
-MassShape mass_shape(const DevLayout &l) { return {kToks, kQ, kSms}; }
+MassShape mass_shape(const DevLayout &l) {
+  return chunk_tc_layout(l) ? mass_tc_shape(l) : MassShape{kToks, kQ, kSms};
+}
 
 size_t mass_workspace(const DevLayout &l) { return mass_places(mass_shape(l), nullptr).total; }
 
 cudaError_t launch_attention_mass(const MassArgs &args, cudaStream_t s) {
   MassArgs a = args;
-  static int configured[64] = {0};
+  a.b.wait_ns = kPrefixWaitNs;
+  static int configured[64][4] = {{0}};
   static std::mutex mu;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  const DevLayout &l = a.b.lay;
+  const int kind = !chunk_tc_layout(l) ? 0 : l.kind == KAMERA_MLA ? 1 : (l.hd == 128 ? 2 : 3);
   {
     std::lock_guard<std::mutex> lock(mu);
-    if (!configured[dev]) {
-      e = cudaFuncSetAttribute(mass_gen_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               gen_smem(1024));
+    if (!configured[dev][kind]) {
+      e = kind ? prepare_mass_tc(l)
+               : cudaFuncSetAttribute(mass_gen_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      gen_smem(1024));
       if (e != cudaSuccess) return e;
-      configured[dev] = 1;
+      configured[dev][kind] = 1;
     }
   }
-  mass_gen_kernel<<<a.shape.n, kThr, gen_smem(a.b.dk), s>>>(a);
-  e = cudaGetLastError();
+  if (kind) {
+    e = launch_mass_tc(a, s);
+  } else {
+    mass_gen_kernel<<<a.shape.n, kThr, gen_smem(a.b.dk), s>>>(a);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
   return launch_early(mass_join_kernel, dim3(a.shape.n), kJoinThr, 0, s, a);
 }
