@@ -48,8 +48,8 @@ struct Shape {
   static constexpr int ring = k + SETS * kSet;
   static constexpr int z = ring + NST * kStage;      // float [kZ][kRow]: c' lse, inf for no row
   static constexpr int xch = z + kZ * kRow * 4;      // float [kParts - 1][KT * kTok]: sums
-  static constexpr int flags = xch + (kParts - 1) * KT * kTok * 4;  // int [kZ][4]: rows, plain for
-                                                     // tile 0, tile 1, first new token
+  static constexpr int flags = xch + (kParts - 1) * KT * kTok * 4;  // int [kZ][4]: rows, how tile 0
+                                                     // and tile 1 are taken
   static constexpr int bar = flags + kZ * 16;
   static constexpr int k_full = 0, k_empty = k_full + SETS * DK, q_full = k_empty + SETS * DK,
                        q_empty = q_full + NST, s_full = q_empty + NST, s_free = s_full + 2 * KT,
@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
     const int quarter = warp & 3, mine = w * kTok + quarter * 32 + lane;  // the token in the block
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const float c = b.scale * kLog2e, inf = __int_as_float(0x7f800000);
+    const uint32_t nothing = c < 0.f ? 0x7f800000u : 0xff800000u;  // a score of no weight
     const int group = 1 + w * 4 + quarter;           // named barrier of the tokens' warps
     float *xch = reinterpret_cast<float *>(smem + S::xch);
     auto arrive = [&](uint32_t at) {  // once for the warp
@@ -224,7 +225,14 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
         wait(bar(S::z_full) + 8 * zs, u / kZ & 1);
         const int *flags = reinterpret_cast<const int *>(smem + S::flags) + 4 * zs;
         const int rows = flags[0];
-        const bool plain = flags[1 + w];
+        // 0: all columns are seen by the tile's tokens; 1: a run of them by each token; 2: and their
+        // log-sum-exps are to be looked at
+        const int how = flags[1 + w];
+        // the columns whose tokens see this one: [see0, see1)
+        const int ahead = tok - past - i * b.tb;
+        const int see0 = ahead > 0 ? min(ahead, kRow) * b.hpk : 0;
+        const int see1 = min(
+            rows, b.window > 0 && ahead < kRow - b.window ? max(ahead + b.window, 0) * b.hpk : kRow);
         const float *z = reinterpret_cast<const float *>(smem + S::z) + zs * kRow + part * S::kCols;
         wait(bar(S::s_full) + 8 * buf, u >> 1 & 1);
         __syncwarp();
@@ -236,18 +244,22 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
           uint32_t x[32];
           ptx::tmem_ld32(tmem + buf * 128 + col0 + lane_off, x);
           ptx::tmem_ld_wait_all<32>(x);
-          if (__builtin_expect(!plain, 0)) {
-            const int first_row = i * b.tb;
+          if (__builtin_expect(how == 2, 0)) {
             float s0 = 0.f;
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              const int d =
-                  first_row + (b.pieces > 1 ? 0 : (int)((unsigned)(col0 + e) * b.hpk_magic >> 16));
-              const bool on = z[g + e] != inf && tok <= past + d && tok >= first_seen(b, past + d);
+              const bool on = col0 + e >= see0 && col0 + e < see1 && z[g + e] != inf;
               s0 += on ? exp2_approx(fmaf(__uint_as_float(x[e]), c, -z[g + e])) : 0.f;
             }
             sa = add2(sa, f2(s0, 0.f));
             continue;
+          }
+          if (how == 1) {
+            const int from = see0 - col0, to = see1 - col0;
+            const uint32_t up = from <= 0 ? 0xffffffffu : from >= 32 ? 0u : 0xffffffffu << from;
+            const uint32_t dn = to >= 32 ? 0xffffffffu : to <= 0 ? 0u : (1u << to) - 1u;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = up & dn & (1u << e) ? x[e] : nothing;
           }
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
@@ -310,23 +322,29 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
       ++published;
       __syncwarp();
     };
+    // Of a segment: the first slot of the lane's copy (tile lane / copies, its page), -1 in no page of
+    // the pool, -2 where the block's tokens are not all in [lo, ctx)
+    auto look_up = [&](const Seg *sp) {
+      const int tok0 = sp->tok0, lo = first_seen(b, sp->past + sp->i0 * b.tb);
+      if (sp->k0 == sp->k1 || !box || tok0 < lo || tok0 + S::KT * kTok > sp->ctx) return -2;
+      if (lane >= each * S::KT) return 0;
+      const int t = (tok0 >> kTokSh) + lane / each;
+      const int entry = __ldg(b.pool.pt + (long long)sp->r * b.pool.pt_stride +
+                              (each == 1 ? t / per_page : t * each + lane % each));
+      return (unsigned)entry < pages ? entry * lay.page_size + (each == 1 ? t % per_page * kTok : 0)
+                                     : -1;
+    };
     publish();
+    wait(bar(S::sg_full), 0);
+    int next_y = look_up(segs);
     while (const Seg *sp = take_segment()) {
       const int tok0 = sp->tok0, ctx = sp->ctx, r = sp->r;
       const int lo = first_seen(b, sp->past + sp->i0 * b.tb);  // no new token of the block sees one before
-      const int *table = b.pool.pt + (long long)r * b.pool.pt_stride;
-      // the lane's copy: tile lane / each, its page
-      const int t = (tok0 >> kTokSh) + lane / each, pg = lane % each;
-      const bool on = lane < each * S::KT;
-      const bool inside = box && tok0 >= lo && tok0 + S::KT * kTok <= ctx;
-      int y = 0;
-      if (inside && on) {
-        const int entry = __ldg(table + (each == 1 ? t / per_page : t * each + pg));
-        y = (unsigned)entry < pages
-                ? entry * lay.page_size + (each == 1 ? t % per_page * kTok : 0)
-                : -1;
-      }
-      const bool whole = inside && __all_sync(0xffffffffu, !on || y >= 0);
+      const int y = next_y, count = each * S::KT;
+      const bool whole = __all_sync(0xffffffffu, y >= 0);
+      int ys[8 * S::KT];
+#pragma unroll
+      for (int k = 0; k < 8 * S::KT; ++k) ys[k] = __shfl_sync(0xffffffffu, y, k);
       bool first_unit = true;
       each_unit(sp, [&](uint32_t, int kvh, int piece, int i, bool first, bool) {
         if (first) {
@@ -339,18 +357,23 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
             for (int c = 0; c < S::DK; ++c) {
               const uint32_t full = bar(S::k_full + set * S::DK + c);
               wait(bar(S::k_empty + set * S::DK + c), parity);
-              if (lane == 0 && !dead) {
+              if (ptx::elect_one() && !dead) {
                 ptx::mbar_arrive_n(full, 31);
                 ptx::mbar_arrive_expect_tx(full, S::KT * kChunk);
+#pragma unroll
+                for (int k = 0; k < 8 * S::KT; ++k)
+                  if (k < count)
+                    ptx::tma_2d(to + c * S::KT * kChunk + k * box * 128, &maps.k, kcol + c * 64, ys[k],
+                                full);
               }
               __syncwarp();
 #pragma unroll 1
-              for (int k = 0; k < each * S::KT; ++k) {
+              for (int k = 8 * S::KT; k < count; ++k) {  // (pages of 8 slots)
                 const int row = __shfl_sync(0xffffffffu, y, k);
                 if (ptx::elect_one() && !dead)
-                  ptx::tma_2d(to + c * S::KT * kChunk + k * box * 128, &maps.k, kcol + c * 64, row, full);
+                  ptx::tma_2d(to + c * S::KT * kChunk + k * box * 128, &maps.k, kcol + c * 64, row,
+                              full);
               }
-              __syncwarp();
             }
           } else {
             const int p = lane & 7;  // 16-byte piece of a row
@@ -391,29 +414,35 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
         const int h0 = kvh * b.hpk + piece * a.shape.qr, z = sp->row + i * b.tb;
         const bool one = min(b.tb, sp->n - i * b.tb) == 1;
         const int bytes = one ? maps.token_bytes : maps.block_bytes;
+        if (ptx::elect_one()) {
 #pragma unroll 1
-        for (int s = 0; s < S::DK / S::UC; ++s, ++stages) {
-          const uint32_t at = stages % S::NST, full = bar(S::q_full) + 8 * at;
-          wait(bar(S::q_empty) + 8 * at, (stages / S::NST & 1) ^ 1);
-          if (ptx::elect_one() && !dead) {
+          for (int s = 0; s < S::DK / S::UC; ++s) {
+            const uint32_t n = stages + s, at = n % S::NST, full = bar(S::q_full) + 8 * at;
+            wait(bar(S::q_empty) + 8 * at, (n / S::NST & 1) ^ 1);
+            if (dead) break;
             ptx::mbar_arrive_expect_tx(full, bytes * S::UC);
 #pragma unroll
             for (int c = 0; c < S::UC; ++c)
               ptx::tma_3d(sb + S::ring + at * S::kStage + c * kChunk,
                           one ? &maps.q_token : &maps.q_block, (s * S::UC + c) * 64, h0, z, full);
           }
-          __syncwarp();
         }
-        if (first_unit) publish();
+        __syncwarp();
+        stages += S::DK / S::UC;
+        if (first_unit) {
+          publish();
+          next_y = look_up(segs + (published - 1) % kSegs);
+        }
         first_unit = false;
       });
     }
     ptx::cp_async_wait_all();
   } else if (warp == S::kLse) {
-    // ---- c' lse of the query rows, four a lane, and whether the rest may take the tiles plainly ----
+    // ---- c' lse of the query rows, four a lane, and how the weights are to be taken ----
     const float inf = __int_as_float(0x7f800000);
     float *z = reinterpret_cast<float *>(smem + S::z);
     int *flags = reinterpret_cast<int *>(smem + S::flags);
+    const bool counts = b.scale != 0.f;
     while (const Seg *sp = take_segment()) {
       each_unit(sp, [&](uint32_t u, int kvh, int piece, int i, bool, bool) {
         const uint32_t zs = u % kZ;
@@ -421,27 +450,33 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
         const int heads = min(b.hpk - piece * a.shape.qr, a.shape.qr), rows = ntok * heads;
         const float *lse = a.lse + (long long)(sp->row + i * b.tb) * b.hq + h0;
         float v[4];
-        bool all = ntok == b.tb && heads == min(b.hpk, a.shape.qr);
+        bool finite = counts;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int row = 32 * k + lane;
           const int d = b.pieces > 1 ? 0 : (int)((unsigned)row * b.hpk_magic >> 16);
           v[k] = row < rows ? lse[(long long)d * b.hq + row - d * b.hpk] : inf;
-          v[k] = v[k] == -inf ? inf : v[k] * kLog2e;  // what saw nothing lays nothing on any token
-          all = all && (row >= rows || v[k] != inf);
         }
-        all = __all_sync(0xffffffffu, all);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          finite = finite && (32 * k + lane >= rows || fabsf(v[k]) < inf);
+          v[k] = v[k] == -inf ? inf : v[k] * kLog2e;  // what saw nothing lays nothing on any token
+        }
+        finite = __all_sync(0xffffffffu, finite);
         if (u >= kZ) wait(bar(S::z_free) + 8 * zs, (u / kZ & 1) ^ 1);
 #pragma unroll
         for (int k = 0; k < 4; ++k) z[zs * kRow + 32 * k + lane] = v[k];
         if (lane == 0) {
           flags[4 * zs] = rows;
           const int first = sp->past + i * b.tb;
+          // (rows that a copy of a whole tile does not write are 0, others may be anything)
+          const bool full = ntok == b.tb && heads == min(b.hpk, a.shape.qr);
 #pragma unroll
           for (int w = 0; w < S::KT; ++w) {
             const int t0 = sp->tok0 + w * kTok;
             flags[4 * zs + 1 + w] =
-                all && first + 1 - t0 >= kTok && first_seen(b, first + ntok - 1) <= t0;
+                !finite ? 2
+                        : !(full && first + 1 - t0 >= kTok && first_seen(b, first + ntok - 1) <= t0);
           }
         }
         __syncwarp();
