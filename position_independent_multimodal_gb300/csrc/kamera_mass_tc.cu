@@ -301,8 +301,9 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
     }
     if (tid == 0) places.rec[blockIdx.x] = rec;
   } else if (warp == S::kLoad) {
-    // ---- K and Q into shared memory. A whole block's tiles come as copies by tensor map, a lane to a
-    // page; other blocks piece by piece, as in kamera_chunk_tc.cu ----
+    // ---- K and Q into shared memory. K comes as copies by tensor map, a lane to a page, or for page
+    // sizes that are no box of one piece by piece. What is in the rows of tokens that no one sees, or
+    // that have no slot, does not matter: a row of S^T is a token's own, and theirs are left out ----
     const bool gqa = lay.kind == KAMERA_GQA;
     const int box = maps.box, each = maps.copies, per_page = maps.per_page;
     const unsigned pages = (unsigned)(b.pool.num_slots / lay.page_size);
@@ -322,17 +323,19 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
       ++published;
       __syncwarp();
     };
-    // Of a segment: the first slot of the lane's copy (tile lane / copies, its page), -1 in no page of
-    // the pool, -2 where the block's tokens are not all in [lo, ctx)
+    // Of a segment: the first slot of the lane's copy (tile lane / copies, its page), -1 where none of
+    // its tokens is looked at or the page is outside the pool
     auto look_up = [&](const Seg *sp) {
-      const int tok0 = sp->tok0, lo = first_seen(b, sp->past + sp->i0 * b.tb);
-      if (sp->k0 == sp->k1 || !box || tok0 < lo || tok0 + S::KT * kTok > sp->ctx) return -2;
-      if (lane >= each * S::KT) return 0;
-      const int t = (tok0 >> kTokSh) + lane / each;
+      if (sp->k0 == sp->k1 || !box || lane >= each * S::KT) return -1;
+      const long long tok = sp->tok0 + (long long)lane * box;
+      if (tok + box <= first_seen(b, sp->past + sp->i0 * b.tb) || tok >= sp->ctx) return -1;
+      const int t = (int)(tok >> kTokSh);
       const int entry = __ldg(b.pool.pt + (long long)sp->r * b.pool.pt_stride +
                               (each == 1 ? t / per_page : t * each + lane % each));
-      return (unsigned)entry < pages ? entry * lay.page_size + (each == 1 ? t % per_page * kTok : 0)
-                                     : -1;
+      if ((unsigned)entry < pages)
+        return entry * lay.page_size + (each == 1 ? t % per_page * kTok : 0);
+      atomicOr(b.status, KAMERA_DEVICE_SLOT_OOB);
+      return -1;
     };
     publish();
     wait(bar(S::sg_full), 0);
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
       const int tok0 = sp->tok0, ctx = sp->ctx, r = sp->r;
       const int lo = first_seen(b, sp->past + sp->i0 * b.tb);  // no new token of the block sees one before
       const int y = next_y, count = each * S::KT;
-      const bool whole = __all_sync(0xffffffffu, y >= 0);
+      const uint32_t copied = __ballot_sync(0xffffffffu, y >= 0);
       int ys[8 * S::KT];
 #pragma unroll
       for (int k = 0; k < 8 * S::KT; ++k) ys[k] = __shfl_sync(0xffffffffu, y, k);
@@ -352,17 +355,17 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
           const uint32_t to = sb + S::k + set * S::kSet;
           const int kcol = gqa ? kvh * lay.hd : 0;
           ++sets;
-          if (whole) {
+          if (box) {
 #pragma unroll 1
             for (int c = 0; c < S::DK; ++c) {
               const uint32_t full = bar(S::k_full + set * S::DK + c);
               wait(bar(S::k_empty + set * S::DK + c), parity);
               if (ptx::elect_one() && !dead) {
                 ptx::mbar_arrive_n(full, 31);
-                ptx::mbar_arrive_expect_tx(full, S::KT * kChunk);
+                ptx::mbar_arrive_expect_tx(full, __popc(copied) * box * 128);
 #pragma unroll
                 for (int k = 0; k < 8 * S::KT; ++k)
-                  if (k < count)
+                  if (copied >> k & 1)
                     ptx::tma_2d(to + c * S::KT * kChunk + k * box * 128, &maps.k, kcol + c * 64, ys[k],
                                 full);
               }
@@ -370,7 +373,7 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
 #pragma unroll 1
               for (int k = 8 * S::KT; k < count; ++k) {  // (pages of 8 slots)
                 const int row = __shfl_sync(0xffffffffu, y, k);
-                if (ptx::elect_one() && !dead)
+                if (ptx::elect_one() && !dead && row >= 0)
                   ptx::tma_2d(to + c * S::KT * kChunk + k * box * 128, &maps.k, kcol + c * 64, row,
                               full);
               }
