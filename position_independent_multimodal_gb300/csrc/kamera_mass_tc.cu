@@ -41,7 +41,9 @@ template <int DK_, int KT_, int SETS_, int UC_, int NST_>
 struct Shape {
   static constexpr int DK = DK_, KT = KT_, SETS = SETS_, UC = UC_, NST = NST_;
   static constexpr int kSoft = 16, kLoad = 16, kLse = 17, kMma = 18;
-  static constexpr int kThr = 32 * (kMma + KT);
+  // (one tile of tokens takes more of Q than of K: a warp of its own brings it)
+  static constexpr int kQ = KT == 1 ? kMma + KT : kLoad;
+  static constexpr int kThr = 32 * (KT == 1 ? kQ + 1 : kMma + KT);
   static constexpr int kParts = 4 / KT, kCols = kRow / kParts;  // parts of the columns, columns of one
   static constexpr int kStage = UC * kChunk, kSet = DK * KT * kChunk;
   static constexpr int k = 0;                        // [set][chunk][tile][128 rows]
@@ -300,7 +302,7 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
       ptx::barrier_sync(group, 32 * S::kParts);  // read before the next block's are written
     }
     if (tid == 0) places.rec[blockIdx.x] = rec;
-  } else if (warp == S::kLoad) {
+  } else if (warp == S::kLoad || warp == S::kQ) {
     // ---- K and Q into shared memory. K comes as copies by tensor map, a lane to a page, or for page
     // sizes that are no box of one piece by piece. What is in the rows of tokens that no one sees, or
     // that have no slot, does not matter: a row of S^T is a token's own, and theirs are left out ----
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
     const unsigned pages = (unsigned)(b.pool.num_slots / lay.page_size);
     uint32_t sets = 0, stages = 0, published = 0;
     auto publish = [&]() {  // the next segment
-      if (lane == 0) {
+      if (warp == S::kLoad && lane == 0) {
         Seg *to = segs + published % kSegs;
         MassSegment m;
         if (walk->next(a, &m)) {
@@ -326,7 +328,7 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
     // Of a segment: the first slot of the lane's copy (tile lane / copies, its page), -1 where none of
     // its tokens is looked at or the page is outside the pool
     auto look_up = [&](const Seg *sp) {
-      if (sp->k0 == sp->k1 || !box || lane >= each * S::KT) return -1;
+      if (warp != S::kLoad || sp->k0 == sp->k1 || !box || lane >= each * S::KT) return -1;
       const long long tok = sp->tok0 + (long long)lane * box;
       if (tok + box <= first_seen(b, sp->past + sp->i0 * b.tb) || tok >= sp->ctx) return -1;
       const int t = (int)(tok >> kTokSh);
@@ -350,7 +352,7 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
       for (int k = 0; k < 8 * S::KT; ++k) ys[k] = __shfl_sync(0xffffffffu, y, k);
       bool first_unit = true;
       each_unit(sp, [&](uint32_t, int kvh, int piece, int i, bool first, bool) {
-        if (first) {
+        if (first && warp == S::kLoad) {
           const uint32_t set = sets % S::SETS, parity = (sets / S::SETS & 1) ^ 1;
           const uint32_t to = sb + S::k + set * S::kSet;
           const int kcol = gqa ? kvh * lay.hd : 0;
@@ -417,7 +419,7 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
         const int h0 = kvh * b.hpk + piece * a.shape.qr, z = sp->row + i * b.tb;
         const bool one = min(b.tb, sp->n - i * b.tb) == 1;
         const int bytes = one ? maps.token_bytes : maps.block_bytes;
-        if (ptx::elect_one()) {
+        if (warp == S::kQ && ptx::elect_one()) {
 #pragma unroll 1
           for (int s = 0; s < S::DK / S::UC; ++s) {
             const uint32_t n = stages + s, at = n % S::NST, full = bar(S::q_full) + 8 * at;
@@ -434,7 +436,7 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
         stages += S::DK / S::UC;
         if (first_unit) {
           publish();
-          next_y = look_up(segs + (published - 1) % kSegs);
+          if (warp == S::kLoad) next_y = look_up(segs + (published - 1) % kSegs);
         }
         first_unit = false;
       });
