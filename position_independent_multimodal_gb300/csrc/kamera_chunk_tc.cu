@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
   }
   if (tid == 0) {
     for (int i = 0; i < S::NST; ++i) {
-      ptx::mbar_init(bar(S::full + i), 32 * S::NL);
+      ptx::mbar_init(bar(S::full + i), 32);
       ptx::mbar_init(bar(S::empty + i), S::QT);
     }
     ptx::mbar_init(bar(S::q_full), 1);
@@ -446,14 +446,16 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
     // ---- Q, and K and V rows into the ring: a warp issues the sixteen copies of a 32 KB stage in
     // about 450 cycles. What a warp does alone takes about five cycles an instruction, so whole tiles
     // take as few as may be: a lane to a page, one load and one test ahead of its tile. Copies are
-    // issued by one thread, which stands in for the others' arrivals. Several warps (MLA) each do all
-    // of it but the copies, of which each has its share ----
+    // issued by one thread, which stands in for the others' arrivals. Several warps (MLA) bring a stage
+    // in turn ----
     const int part = warp - S::kSoft;
     const bool gqa = lay.kind == KAMERA_GQA;
     const int box = maps.box, each = maps.copies;  // slots of a copy, copies of a tile's 64 columns
     const int per_page = maps.per_page;            // tiles of a page (each == 1)
     const unsigned pages = (unsigned)(a.pool.num_slots / lay.page_size);
+    const uint32_t all_pages = box ? (1u << each) - 1u : 0xffffffffu;
     Place<S::NST> at;            // the next stage
+    uint32_t stage_no = 0;       // of that stage, since the start: every NL-th is a warp's
     uint32_t tile_no = 0;        // tiles so far
     uint32_t published = 0;
     auto publish = [&]() {       // the next segment
@@ -471,20 +473,21 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
       const int kcol = gqa ? sp->kvh * lay.hd : 0, vcol = kcol + sp->part * a.shape.vw;
       const int lo = first_seen(a, sp->first);  // tokens that a row sees: from here on
       const int *table = a.pool.pt + (long long)sp->r * a.pool.pt_stride;
-      // tiles [in0, in1) hold tokens that are all in [lo, ctx)
-      const int in0 = box ? (lo + kTok - 1) >> kTokSh : 0x7FFFFFFF, in1 = ctx >> kTokSh;
-      auto load_entry = [&](int i) {  // of the lane's page in a tile
+      // the lane's page-table entry in a tile, -1 where none of the page's tokens is in [lo, ctx)
+      auto load_entry = [&](int i) {
+        const long long tok = ((long long)(tile0 + i) << kTokSh) + lane * box;
+        const bool on = i < n && lane < each && tok + box > lo && tok < ctx;
         const int t = tile0 + i;
-        const bool on = i < n && t >= in0 && t < in1 && lane < each;
-        return on ? __ldg(table + (each == 1 ? t / per_page : t * each + lane)) : 0;
+        return on ? __ldg(table + (each == 1 ? t / per_page : t * each + lane)) : -1;
       };
-      int entry = load_entry(0);
+      int entry = box ? load_entry(0) : -1;
       struct Tile {
-        int y;       // first slot of the lane's copy
-        bool whole;  // all tokens are in
+        int y;           // first slot of the lane's page
+        uint32_t pages;  // pages of the pool with tokens in [lo, ctx), a bit each
+        uint32_t inner;  // those with no others
       } cur, prev;
       cur.y = 0;
-      cur.whole = false;
+      cur.pages = cur.inner = 0;
       // slots of four tokens of a tile, for those that come piece by piece
       auto slots = [&](int i, int *to) {
 #pragma unroll
@@ -495,62 +498,106 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
       };
       auto bring = [&](bool is_k, int i, const Tile &tile) {
         const int col = is_k ? kcol : vcol, stages = (is_k ? S::DK : S::DV) / S::UC;
-        if (tile.whole) {
-          const void *map = is_k ? &maps.k : &maps.v;
-          // copies [k0, k0 + mine) of each 64 columns are this warp's
-          const int mine = S::NL == 1 ? each : each >= S::NL ? each / S::NL : part < each;
-          const int k0 = part * mine;
-          constexpr int kMost = 16 / S::NL;  // (with pages of 8 slots)
-          int y[kMost];
+        const void *map = is_k ? &maps.k : &maps.v;
+        // What is in K's rows that no token of [lo, ctx) has does not matter, as a token's scores are
+        // a column of their own and such columns are masked. V's have to be 0: a weight of 0 times
+        // what is not finite is no 0.
+        const uint32_t copied = is_k ? tile.pages : tile.pages & tile.inner;
+        if (copied == all_pages) {
+          int y[16];
 #pragma unroll
-          for (int k = 0; k < kMost; ++k) y[k] = __shfl_sync(0xffffffffu, tile.y, (k0 + k) & 31);
+          for (int k = 0; k < 16; ++k) y[k] = __shfl_sync(0xffffffffu, tile.y, k);
           if (ptx::elect_one()) {
             Place<S::NST> to = at;
 #pragma unroll 1
-            for (int u = 0; u < stages; ++u) {
+            for (int u = 0; u < stages; ++u, to.advance(1)) {
+              if (S::NL > 1 && (stage_no + u) % S::NL != part) continue;  // another warp's
               const uint32_t full = bar(S::full) + 8 * to.st;
-              uint32_t dst = sb + S::ring + to.st * S::kStage + k0 * box * 128;
+              uint32_t dst = sb + S::ring + to.st * S::kStage;
               wait(bar(S::empty) + 8 * to.st, to.ph ^ 1);
               if (dead) break;
-              if (S::NL > 1 && mine == 0) {
-                ptx::mbar_arrive_n(full, 32);
-              } else {
-                ptx::mbar_arrive_n(full, 31);
-                ptx::mbar_arrive_expect_tx(full, mine * box * S::UC * 128);
-              }
+              ptx::mbar_arrive_n(full, 31);
+              ptx::mbar_arrive_expect_tx(full, S::kStage);
 #pragma unroll
-              for (int k = 0; k < kMost; ++k) {
-                if (k >= mine) break;
+              for (int k = 0; k < 16; ++k) {
+                if (k >= each) break;
 #pragma unroll
                 for (int c = 0; c < S::UC; ++c)
                   ptx::tma_2d(dst + c * kChunk, map, col + (u * S::UC + c) * 64, y[k], full);
                 dst += box * 128;
               }
-              to.advance(1);
             }
           }
           __syncwarp();
           at.advance(stages);
+          stage_no += stages;
           return;
         }
-        const int piece = lane & 7;  // 16-byte piece of a row
         const __nv_bfloat16 *base = is_k || !gqa ? a.pool.k : a.pool.v;
         const int row = is_k || !gqa ? lay.row_k : lay.row_v;
+        const int piece = lane & 7;  // 16-byte piece of a row
         base += (long long)a.layer * a.pool.num_slots * row + col + 8 * piece;
+        if (box) {
+          const long long t0 = (long long)(tile0 + i) << kTokSh;
+#pragma unroll 1
+          for (int u = 0; u < stages; ++u, at.advance(1), ++stage_no) {
+            if (S::NL > 1 && stage_no % S::NL != part) continue;
+            const uint32_t full = bar(S::full) + 8 * at.st;
+            const uint32_t dst = S::ring + at.st * S::kStage;
+            wait(bar(S::empty) + 8 * at.st, at.ph ^ 1);
+            if (__any_sync(0xffffffffu, dead)) {
+              dead = true;
+              continue;
+            }
+            if (lane == 0) ptx::mbar_arrive_expect_tx(full, __popc(copied) * box * S::UC * 128);
+            __syncwarp();
+#pragma unroll 1
+            for (int k = 0; k < each; ++k) {
+              const int first = __shfl_sync(0xffffffffu, tile.y, k);
+              if (copied >> k & 1) {
+                if (ptx::elect_one())
+#pragma unroll
+                  for (int c = 0; c < S::UC; ++c)
+                    ptx::tma_2d(sb + dst + c * kChunk + k * box * 128, map,
+                                col + (u * S::UC + c) * 64, first, full);
+                __syncwarp();
+              } else if (!is_k) {
+#pragma unroll 4
+                for (int j = lane >> 3; j < box; j += 4) {  // four tokens at a time
+                  const int t = k * box + j;
+                  const bool has = tile.pages >> k & 1 && t0 + t >= lo && t0 + t < ctx;
+#pragma unroll
+                  for (int c = 0; c < S::UC; ++c) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (has)
+                      v = __ldg(reinterpret_cast<const uint4 *>(
+                          base + (long long)(first + j) * row + (u * S::UC + c) * 64));
+                    *reinterpret_cast<uint4 *>(smem + dst + c * kChunk + t * 128 +
+                                               ((piece ^ (t & 7)) << 4)) = v;
+                  }
+                }
+                __syncwarp();
+              }
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_n(full, 31);
+          }
+          return;
+        }
         int slot[4];
         slots(i, slot);
 #pragma unroll 1
-        for (int u = 0; u < stages; ++u) {
+        for (int u = 0; u < stages; ++u, at.advance(1), ++stage_no) {
+          if (S::NL > 1 && stage_no % S::NL != part) continue;
           const uint32_t dst = sb + S::ring + at.st * S::kStage, full = bar(S::full) + 8 * at.st;
           wait(bar(S::empty) + 8 * at.st, at.ph ^ 1);
-          at.advance(1);
           if (__any_sync(0xffffffffu, dead)) {
             dead = true;
             continue;
           }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (S::NL > 1 && k != part) continue;  // a warp's 32 tokens
+          for (int k = 0; k < 4; ++k)
 #pragma unroll 2
             for (int j = 0; j < 8; ++j) {  // four tokens at a time
               const int t = 32 * k + 4 * j + (lane >> 3);
@@ -561,7 +608,6 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
                 ptx::cp_async16(dst + c * kChunk + t * 128 + ((piece ^ (t & 7)) << 4), p + c * 64,
                                 sl >= 0 ? 16u : 0u);
             }
-          }
           // made visible to the tensor core here, as the MMA thread does not stop for it
           ptx::cp_async_commit();
           ptx::cp_async_wait_all();
@@ -587,14 +633,28 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
         const uint32_t mk = tile_no++ % kMasks;
-        const int t = tile0 + i;
+        const long long t0 = (long long)(tile0 + i) << kTokSh;
         prev = cur;
-        cur.y = entry * lay.page_size + (each == 1 ? t % per_page * kTok : 0);
-        cur.whole = t >= in0 && t < in1 &&
-                    __all_sync(0xffffffffu, lane >= each || (unsigned)entry < pages);
-        entry = load_entry(i + 1);  // ahead of its use
-        uint4 bits = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
-        if (!cur.whole) {
+        uint4 bits;
+        if (box) {
+          const long long tok = t0 + lane * box;
+          const bool on = lane < each && tok + box > lo && tok < ctx, in = (unsigned)entry < pages;
+          if (on && !in) atomicOr(a.status, KAMERA_DEVICE_SLOT_OOB);
+          cur.y = entry * lay.page_size + (each == 1 ? (tile0 + i) % per_page * kTok : 0);
+          cur.pages = __ballot_sync(0xffffffffu, on && in);
+          cur.inner = __ballot_sync(0xffffffffu, on && tok >= lo && tok + box <= ctx);
+          if (i + 1 < n) entry = load_entry(i + 1);  // ahead of its use
+          if ((cur.pages & cur.inner) == all_pages) {
+            bits = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
+          } else {
+            auto word = [&](int k) {  // of 32 tokens, those that are in
+              const int t = 32 * k + lane;
+              return __ballot_sync(0xffffffffu, (cur.pages >> (t / box) & 1) && t0 + t >= lo &&
+                                                    t0 + t < ctx);
+            };
+            bits = make_uint4(word(0), word(1), word(2), word(3));
+          }
+        } else {
           int slot[4];
           slots(i, slot);
           bits.x = __ballot_sync(0xffffffffu, slot[0] >= 0);
