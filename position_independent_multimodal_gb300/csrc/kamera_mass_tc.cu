@@ -7,12 +7,19 @@
 // The transposed product leaves a cached token to a thread (of each part of the columns), so its sum
 // stays in a register over all query rows of a block and no two threads add to one number. K rows of
 // a block stay in shared memory while the query rows of a KV head pass through a ring; S has two
-// buffers a tile, so products and weights never wait for one another but where one is slower: 32768
-// weights a unit take the special-function units 1024 cycles, the products of two tiles 1040.
+// buffers a tile (MLA four, for pieces of its sums), so products and weights never wait for one another
+// but where one is slower: 32768 weights a unit take the special-function units 1024 cycles, the
+// products of two tiles 1040.
 //
 // Roles: sixteen warps take weights (GQA: two tiles of 128 tokens, two parts of 64 columns; MLA: one
-// tile, four parts of 32), one brings K and Q, one the rows' log-sum-exps, and a thread for each
-// tile of tokens issues the MMAs. Copies of K as in kamera_chunk_tc.cu.
+// tile, four parts of 32), one brings K (and GQA's Q; MLA's has a warp of its own, as each of its units
+// takes nine stages of Q), one the rows' log-sum-exps, and a thread for each tile of tokens issues the
+// MMAs. Copies of K as in kamera_chunk_tc.cu.
+//
+// Measured: 32 requests that decode over 3000 to 6001 tokens (28 query heads, 4 KV heads of 128) in 49
+// us, 3.0 TB/s of K: a block's copies and its few columns take turns with the pages' ids ahead of them.
+// 250 new tokens over 30000 in 67 us, 1570 weights a clock of the chip's 4860: the units of a block wait
+// for its K, and each CTA has only 5 or 6 blocks.
 #include "kamera_mass.cuh"
 #include "kamera_ptx.cuh"
 #include "kamera_smem.cuh"
@@ -36,10 +43,18 @@ struct Seg {
 };
 
 // DK: 64-column chunks of K; KT: tiles of 128 tokens; SETS: sets of K tiles; UC: chunks of a stage of
-// Q; NST: stages of Q.
-template <int DK_, int KT_, int SETS_, int UC_, int NST_>
+// Q; NST: stages of Q; AC: chunks that a score is summed over in TMEM. The tensor core cuts its sums
+// off where it should round them, so each of its steps takes a little of a score's size: 8e-8 of it
+// over the 8 steps of 128 columns, 4.3e-7 over the 36 of MLA, where weights of large scores come out
+// 4e-6 too small. There the sum is taken in pieces, which take four TMEM buffers in turn and are added
+// in registers, rounded. Measured over six requests of 100 new tokens over 5000 (the masses' error, the
+// time): in one piece 3.8e-6, 62 us; pieces of three chunks 1.2e-6, 63; of two 8.5e-7, 63.5; of one
+// 5.5e-7, 65.5 us. Products in float32 with rounded sums give 7e-7: a chunk a piece it is.
+template <int DK_, int KT_, int SETS_, int UC_, int NST_, int AC_>
 struct Shape {
-  static constexpr int DK = DK_, KT = KT_, SETS = SETS_, UC = UC_, NST = NST_;
+  static constexpr int DK = DK_, KT = KT_, SETS = SETS_, UC = UC_, NST = NST_, AC = AC_;
+  static constexpr int kPieces = (DK + AC - 1) / AC;  // pieces of a sum
+  static constexpr int kBuf = 4 / KT;                 // TMEM buffers of a tile
   static constexpr int kSoft = 16, kLoad = 16, kLse = 17, kMma = 18;
   // (one tile of tokens takes more of Q than of K: a warp of its own brings it)
   static constexpr int kQ = KT == 1 ? kMma + KT : kLoad;
@@ -54,8 +69,8 @@ struct Shape {
                                                      // and tile 1 are taken
   static constexpr int bar = flags + kZ * 16;
   static constexpr int k_full = 0, k_empty = k_full + SETS * DK, q_full = k_empty + SETS * DK,
-                       q_empty = q_full + NST, s_full = q_empty + NST, s_free = s_full + 2 * KT,
-                       z_full = s_free + 2 * KT, z_free = z_full + kZ, sg_full = z_free + kZ,
+                       q_empty = q_full + NST, s_full = q_empty + NST, s_free = s_full + kBuf * KT,
+                       z_full = s_free + kBuf * KT, z_free = z_full + kZ, sg_full = z_free + kZ,
                        last = sg_full + kSegs, n_bar = last + KT;
   static constexpr int misc = bar + n_bar * 8;       // TMEM address, give-up flag
   static constexpr int walk = misc + 16;
@@ -63,13 +78,14 @@ struct Shape {
   static constexpr int total = seg + kSegs * sizeof(Seg);
   static constexpr int scratch = z;                  // of the start
   static_assert(total <= 232448, "shared memory of one CTA");
-  static_assert(DK % UC == 0 && walk % 8 == 0 && scratch % 8 == 0, "whole stages, 64-bit numbers");
+  static_assert(DK % UC == 0 && AC % UC == 0 && walk % 8 == 0 && scratch % 8 == 0, "whole stages, 64-bit numbers");
+  static_assert(kPieces == 1 || kCols == 32, "a piece's columns in registers");
   static_assert(sizeof(ChunkScratch<kThr>) <= kZ * kRow * 4, "the start's scratch");
 };
 
-using Gqa128 = Shape<2, 2, 2, 2, 3>;
-using Gqa64 = Shape<1, 2, 3, 1, 4>;
-using Mla512 = Shape<9, 1, 1, 1, 4>;
+using Gqa128 = Shape<2, 2, 2, 2, 3, 2>;
+using Gqa64 = Shape<1, 2, 3, 1, 4, 1>;
+using Mla512 = Shape<9, 1, 1, 1, 4, 1>;
 
 struct Maps {
   CUtensorMap k, q_block, q_token;
@@ -121,7 +137,7 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
       ptx::mbar_init(bar(S::q_full + i), 1);
       ptx::mbar_init(bar(S::q_empty + i), S::KT);
     }
-    for (int i = 0; i < 2 * S::KT; ++i) {
+    for (int i = 0; i < S::kBuf * S::KT; ++i) {
       ptx::mbar_init(bar(S::s_full + i), 1);
       ptx::mbar_init(bar(S::s_free + i), S::kSoft / S::KT);
     }
@@ -223,7 +239,7 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
       }
       f32x2 sa = f2(0.f, 0.f), sc = sa;
       each_unit(sp, [&](uint32_t u, int, int, int i, bool, bool) {
-        const uint32_t buf = w * 2 + (u & 1), zs = u % kZ;
+        const uint32_t zs = u % kZ;
         wait(bar(S::z_full) + 8 * zs, u / kZ & 1);
         const int *flags = reinterpret_cast<const int *>(smem + S::flags) + 4 * zs;
         const int rows = flags[0];
@@ -236,16 +252,9 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
         const int see1 = min(
             rows, b.window > 0 && ahead < kRow - b.window ? max(ahead + b.window, 0) * b.hpk : kRow);
         const float *z = reinterpret_cast<const float *>(smem + S::z) + zs * kRow + part * S::kCols;
-        wait(bar(S::s_full) + 8 * buf, u >> 1 & 1);
-        __syncwarp();
-        ptx::tc_fence_after();
-#pragma unroll 1
-        for (int g = 0; g < S::kCols; g += 32) {
+        // the weights of 32 columns, from col0 on
+        auto weigh = [&](uint32_t *x, int g) {
           const int col0 = part * S::kCols + g;
-          if (col0 >= rows) break;
-          uint32_t x[32];
-          ptx::tmem_ld32(tmem + buf * 128 + col0 + lane_off, x);
-          ptx::tmem_ld_wait_all<32>(x);
           if (__builtin_expect(how == 2, 0)) {
             float s0 = 0.f;
 #pragma unroll
@@ -254,7 +263,7 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
               s0 += on ? exp2_approx(fmaf(__uint_as_float(x[e]), c, -z[g + e])) : 0.f;
             }
             sa = add2(sa, f2(s0, 0.f));
-            continue;
+            return;
           }
           if (how == 1) {
             const int from = see0 - col0, to = see1 - col0;
@@ -273,9 +282,48 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
             sa = add2(sa, f2(p0, p1));
             sc = add2(sc, f2(p2, p3));
           }
+        };
+        // S of buffer n, of this unit or a piece of its sum
+        auto take = [&](uint32_t n) {
+          wait(bar(S::s_full + w * S::kBuf) + 8 * (n % S::kBuf), n / S::kBuf & 1);
+          __syncwarp();
+          ptx::tc_fence_after();
+          return tmem + (w * S::kBuf + n % S::kBuf) * 128 + part * S::kCols + lane_off;
+        };
+        auto give = [&](uint32_t n) {
+          ptx::tc_fence_before();
+          arrive(bar(S::s_free + w * S::kBuf) + 8 * (n % S::kBuf));
+        };
+        const int cols = rows - part * S::kCols;  // that this part has
+        if constexpr (S::kPieces == 1) {
+          const uint32_t at = take(u);
+#pragma unroll 1
+          for (int g = 0; g < S::kCols && g < cols; g += 32) {
+            uint32_t x[32];
+            ptx::tmem_ld32(at + g, x);
+            ptx::tmem_ld_wait_all<32>(x);
+            weigh(x, g);
+          }
+          give(u);
+        } else {
+          uint32_t x[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = 0;
+#pragma unroll 1
+          for (int k = 0; k < S::kPieces; ++k) {
+            const uint32_t n = u * S::kPieces + k, at = take(n);
+            if (cols > 0) {
+              uint32_t y[32];
+              ptx::tmem_ld32(at, y);
+              ptx::tmem_ld_wait_all<32>(y);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                x[e] = __float_as_uint(__uint_as_float(x[e]) + __uint_as_float(y[e]));
+            }
+            give(n);
+          }
+          if (cols > 0) weigh(x, 0);
         }
-        ptx::tc_fence_before();
-        arrive(bar(S::s_free) + 8 * buf);
         if (lane == 0 && !dead) ptx::mbar_arrive(bar(S::z_free) + 8 * zs);
       });
       float sum;
@@ -497,12 +545,18 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
     uint32_t sets = 0, stages = 0;
     while (const Seg *sp = take_segment()) {
       each_unit(sp, [&](uint32_t u, int, int, int, bool first, bool last) {
-        const uint32_t set = sets % S::SETS, buf = w * 2 + (u & 1);
-        if (u >= 2) wait(bar(S::s_free) + 8 * buf, (u >> 1 & 1) ^ 1);
-        if (!dead) ptx::tc_fence_after();
+        const uint32_t set = sets % S::SETS;
+        uint32_t n = u * S::kPieces, buf = 0;  // the next piece's number, the present one's buffer
 #pragma unroll 1
         for (int s = 0; s < S::DK / S::UC; ++s, ++stages) {
           const uint32_t at = stages % S::NST;
+          const bool begins_piece = s * S::UC % S::AC == 0;
+          if (begins_piece) {
+            buf = w * S::kBuf + n % S::kBuf;
+            if (n >= S::kBuf) wait(bar(S::s_free) + 8 * buf, (n / S::kBuf & 1) ^ 1);
+            if (!dead) ptx::tc_fence_after();
+            ++n;
+          }
           if (first)
             for (int c = 0; c < S::UC; ++c)
               wait(bar(S::k_full + set * S::DK + s * S::UC + c), sets / S::SETS & 1);
@@ -514,13 +568,15 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
           for (int x = 0; x < S::UC * 4; ++x)
             ptx::mma_bf16(tmem + buf * 128,
                           desc(kd + (((x >> 2) * S::KT * kChunk + (x & 3) * 32) >> 4)),
-                          desc(qd + (((x >> 2) * kChunk + (x & 3) * 32) >> 4)), id, s | x ? 1u : 0u);
+                          desc(qd + (((x >> 2) * kChunk + (x & 3) * 32) >> 4)), id,
+                          !begins_piece || x ? 1u : 0u);
           ptx::mma_commit(bar(S::q_empty) + 8 * at);
           if (last)
             for (int c = 0; c < S::UC; ++c)
               ptx::mma_commit(bar(S::k_empty + set * S::DK + s * S::UC + c));
+          if ((s + 1) * S::UC % S::AC == 0 || (s + 1) * S::UC == S::DK)
+            ptx::mma_commit(bar(S::s_full) + 8 * buf);
         }
-        ptx::mma_commit(bar(S::s_full) + 8 * buf);
         if (last) ++sets;
       });
     }
