@@ -246,13 +246,28 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
         // 0: all columns are seen by the tile's tokens; 1: a run of them by each token; 2: and their
         // log-sum-exps are to be looked at
         const int how = flags[1 + w];
-        // the columns whose tokens see this one: [see0, see1)
-        const int ahead = tok - past - i * b.tb;
-        const int see0 = ahead > 0 ? min(ahead, kRow) * b.hpk : 0;
-        const int see1 = min(
-            rows, b.window > 0 && ahead < kRow - b.window ? max(ahead + b.window, 0) * b.hpk : kRow);
+        int see0, see1;  // the columns whose tokens see this one: [see0, see1)
+        if (how) {
+          const int ahead = tok - past - i * b.tb;
+          see0 = ahead > 0 ? min(ahead, kRow) * b.hpk : 0;
+          see1 = min(rows, b.window > 0 && ahead < kRow - b.window ? max(ahead + b.window, 0) * b.hpk
+                                                                   : kRow);
+        }
         const float *z = reinterpret_cast<const float *>(smem + S::z) + zs * kRow + part * S::kCols;
-        // the weights of 32 columns, from col0 on
+        // the weights of 16 columns from g on, all of which are seen
+        auto some = [&](const uint32_t *x, int g) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const float4 z4 = *reinterpret_cast<const float4 *>(z + g + e);
+            const float p0 = exp2_approx(fmaf(__uint_as_float(x[e]), c, -z4.x));
+            const float p1 = exp2_approx(fmaf(__uint_as_float(x[e + 1]), c, -z4.y));
+            const float p2 = exp2_approx(fmaf(__uint_as_float(x[e + 2]), c, -z4.z));
+            const float p3 = exp2_approx(fmaf(__uint_as_float(x[e + 3]), c, -z4.w));
+            sa = add2(sa, f2(p0, p1));
+            sc = add2(sc, f2(p2, p3));
+          }
+        };
+        // the weights of 32 columns
         auto weigh = [&](uint32_t *x, int g) {
           const int col0 = part * S::kCols + g;
           if (__builtin_expect(how == 2, 0)) {
@@ -272,16 +287,8 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[e] = up & dn & (1u << e) ? x[e] : nothing;
           }
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 z4 = *reinterpret_cast<const float4 *>(z + g + e);
-            const float p0 = exp2_approx(fmaf(__uint_as_float(x[e]), c, -z4.x));
-            const float p1 = exp2_approx(fmaf(__uint_as_float(x[e + 1]), c, -z4.y));
-            const float p2 = exp2_approx(fmaf(__uint_as_float(x[e + 2]), c, -z4.z));
-            const float p3 = exp2_approx(fmaf(__uint_as_float(x[e + 3]), c, -z4.w));
-            sa = add2(sa, f2(p0, p1));
-            sc = add2(sc, f2(p2, p3));
-          }
+          some(x, g);
+          some(x + 16, g + 16);
         };
         // S of buffer n, of this unit or a piece of its sum
         auto take = [&](uint32_t n) {
@@ -297,14 +304,31 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
         const int cols = rows - part * S::kCols;  // that this part has
         if constexpr (S::kPieces == 1) {
           const uint32_t at = take(u);
+          if (how == 0 && cols > S::kCols - 16) {
+            // S comes sixteen columns ahead of the weights, and its buffer goes back before the last
+            uint32_t x[2][16];
+            ptx::tmem_ld16(at, x[0]);
+            ptx::tmem_ld_wait_all<16>(x[0]);
+#pragma unroll
+            for (int g = 0; g < S::kCols; g += 16) {
+              uint32_t *next = x[(g >> 4 & 1) ^ 1];
+              if (g + 16 < S::kCols)
+                ptx::tmem_ld16(at + g + 16, next);
+              else
+                give(u);
+              some(x[g >> 4 & 1], g);
+              if (g + 16 < S::kCols) ptx::tmem_ld_wait_all<16>(next);
+            }
+          } else {
 #pragma unroll 1
-          for (int g = 0; g < S::kCols && g < cols; g += 32) {
-            uint32_t x[32];
-            ptx::tmem_ld32(at + g, x);
-            ptx::tmem_ld_wait_all<32>(x);
-            weigh(x, g);
+            for (int g = 0; g < S::kCols && g < cols; g += 32) {
+              uint32_t x[32];
+              ptx::tmem_ld32(at + g, x);
+              ptx::tmem_ld_wait_all<32>(x);
+              weigh(x, g);
+            }
+            give(u);
           }
-          give(u);
         } else {
           uint32_t x[32];
 #pragma unroll
@@ -395,6 +419,7 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
       const int lo = first_seen(b, sp->past + sp->i0 * b.tb);  // no new token of the block sees one before
       const int y = next_y, count = each * S::KT;
       const uint32_t copied = __ballot_sync(0xffffffffu, y >= 0);
+      const bool whole = count == 8 * S::KT && copied == (uint32_t)((1ull << (8 * S::KT)) - 1);
       int ys[8 * S::KT];
 #pragma unroll
       for (int k = 0; k < 8 * S::KT; ++k) ys[k] = __shfl_sync(0xffffffffu, y, k);
@@ -405,7 +430,22 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
           const uint32_t to = sb + S::k + set * S::kSet;
           const int kcol = gqa ? kvh * lay.hd : 0;
           ++sets;
-          if (box) {
+          if (whole) {  // a warp alone takes some five cycles an instruction: few of them
+            if (ptx::elect_one()) {
+#pragma unroll 1
+              for (int c = 0; c < S::DK; ++c) {
+                const uint32_t full = bar(S::k_full + set * S::DK + c);
+                wait(bar(S::k_empty + set * S::DK + c), parity);
+                if (dead) break;
+                ptx::mbar_arrive_n(full, 31);
+                ptx::mbar_arrive_expect_tx(full, S::KT * kChunk);
+#pragma unroll
+                for (int k = 0; k < 8 * S::KT; ++k)
+                  ptx::tma_2d(to + c * S::KT * kChunk + k * 2048, &maps.k, kcol + c * 64, ys[k], full);
+              }
+            }
+            __syncwarp();
+          } else if (box) {
 #pragma unroll 1
             for (int c = 0; c < S::DK; ++c) {
               const uint32_t full = bar(S::k_full + set * S::DK + c);
