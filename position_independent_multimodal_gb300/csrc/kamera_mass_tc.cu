@@ -16,10 +16,10 @@
 // takes nine stages of Q), one the rows' log-sum-exps, and a thread for each tile of tokens issues the
 // MMAs. Copies of K as in kamera_chunk_tc.cu.
 //
-// Measured: 32 requests that decode over 3000 to 6001 tokens (28 query heads, 4 KV heads of 128) in 49
-// us, 3.0 TB/s of K: a block's copies and its few columns take turns with the pages' ids ahead of them.
-// 250 new tokens over 30000 in 67 us, 1570 weights a clock of the chip's 4860: the units of a block wait
-// for its K, and each CTA has only 5 or 6 blocks.
+// Measured: 32 requests that decode over 3000 to 6001 tokens (28 query heads, 4 KV heads of 128) in 41
+// us, 3.6 TB/s of K; 250 new tokens over 30000 in 61 us, 1730 weights a clock of the chip's 4860. The
+// weights' warps have 184 instructions for 64 weights and some 150 more around them; tokens next to
+// the new ones, whose columns are seen in part, take longer, and the CTA that has them ends last.
 #include "kamera_mass.cuh"
 #include "kamera_ptx.cuh"
 #include "kamera_smem.cuh"
@@ -65,8 +65,10 @@ struct Shape {
   static constexpr int ring = k + SETS * kSet;
   static constexpr int z = ring + NST * kStage;      // float [kZ][kRow]: c' lse, inf for no row
   static constexpr int xch = z + kZ * kRow * 4;      // float [kParts - 1][KT * kTok]: sums
-  static constexpr int flags = xch + (kParts - 1) * KT * kTok * 4;  // int [kZ][4]: rows, how tile 0
-                                                     // and tile 1 are taken
+  // int [kZ][4] of a unit: its rows; how tile 0 and tile 1 are taken (0: all columns are seen by the
+  // tile's tokens; 1: a run of them by each token; 2: and their log-sum-exps are to be looked at); its
+  // first of its request's new tokens
+  static constexpr int flags = xch + (kParts - 1) * KT * kTok * 4;
   static constexpr int bar = flags + kZ * 16;
   static constexpr int k_full = 0, k_empty = k_full + SETS * DK, q_full = k_empty + SETS * DK,
                        q_empty = q_full + NST, s_full = q_empty + NST, s_free = s_full + kBuf * KT,
@@ -78,7 +80,7 @@ struct Shape {
   static constexpr int total = seg + kSegs * sizeof(Seg);
   static constexpr int scratch = z;                  // of the start
   static_assert(total <= 232448, "shared memory of one CTA");
-  static_assert(DK % UC == 0 && AC % UC == 0 && walk % 8 == 0 && scratch % 8 == 0, "whole stages, 64-bit numbers");
+  static_assert(DK % UC == 0 && AC % UC == 0 && walk % 8 == 0 && scratch % 8 == 0 && flags % 16 == 0, "whole stages, 64-bit numbers");
   static_assert(kPieces == 1 || kCols == 32, "a piece's columns in registers");
   static_assert(sizeof(ChunkScratch<kThr>) <= kZ * kRow * 4, "the start's scratch");
 };
@@ -238,17 +240,17 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
         have = page >= 0 && ((long long)page + 1) * lay.page_size <= b.pool.num_slots;
       }
       f32x2 sa = f2(0.f, 0.f), sc = sa;
-      each_unit(sp, [&](uint32_t u, int, int, int i, bool, bool) {
-        const uint32_t zs = u % kZ;
+      // (what a unit is comes with its log-sum-exps: these warps have no instructions to spare)
+      const uint32_t end = units + (sp->k1 - sp->k0);
+#pragma unroll 1
+      for (; units != end; ++units) {
+        const uint32_t u = units, zs = u % kZ;
         wait(bar(S::z_full) + 8 * zs, u / kZ & 1);
-        const int *flags = reinterpret_cast<const int *>(smem + S::flags) + 4 * zs;
-        const int rows = flags[0];
-        // 0: all columns are seen by the tile's tokens; 1: a run of them by each token; 2: and their
-        // log-sum-exps are to be looked at
-        const int how = flags[1 + w];
+        const int4 flags = *reinterpret_cast<const int4 *>(smem + S::flags + 16 * zs);
+        const int rows = flags.x, how = w ? flags.z : flags.y;
         int see0, see1;  // the columns whose tokens see this one: [see0, see1)
         if (how) {
-          const int ahead = tok - past - i * b.tb;
+          const int ahead = tok - past - flags.w;
           see0 = ahead > 0 ? min(ahead, kRow) * b.hpk : 0;
           see1 = min(rows, b.window > 0 && ahead < kRow - b.window ? max(ahead + b.window, 0) * b.hpk
                                                                    : kRow);
@@ -284,8 +286,12 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
             const int from = see0 - col0, to = see1 - col0;
             const uint32_t up = from <= 0 ? 0xffffffffu : from >= 32 ? 0u : 0xffffffffu << from;
             const uint32_t dn = to >= 32 ? 0xffffffffu : to <= 0 ? 0u : (1u << to) - 1u;
+            const uint32_t seen = up & dn;
+            if (__all_sync(0xffffffffu, seen == 0)) return;
+            if (!__all_sync(0xffffffffu, seen == 0xffffffffu)) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = up & dn & (1u << e) ? x[e] : nothing;
+              for (int e = 0; e < 32; ++e) x[e] = seen & (1u << e) ? x[e] : nothing;
+            }
           }
           some(x, g);
           some(x + 16, g + 16);
@@ -349,7 +355,7 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
           if (cols > 0) weigh(x, 0);
         }
         if (lane == 0 && !dead) ptx::mbar_arrive(bar(S::z_free) + 8 * zs);
-      });
+      }
       float sum;
       {
         float s0, s1;
@@ -534,7 +540,6 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
     // ---- c' lse of the query rows, four a lane, and how the weights are to be taken ----
     const float inf = __int_as_float(0x7f800000);
     float *z = reinterpret_cast<float *>(smem + S::z);
-    int *flags = reinterpret_cast<int *>(smem + S::flags);
     const bool counts = b.scale != 0.f;
     while (const Seg *sp = take_segment()) {
       each_unit(sp, [&](uint32_t u, int kvh, int piece, int i, bool, bool) {
@@ -560,17 +565,19 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
 #pragma unroll
         for (int k = 0; k < 4; ++k) z[zs * kRow + 32 * k + lane] = v[k];
         if (lane == 0) {
-          flags[4 * zs] = rows;
           const int first = sp->past + i * b.tb;
           // (rows that a copy of a whole tile does not write are 0, others may be anything)
           const bool full = ntok == b.tb && heads == min(b.hpk, a.shape.qr);
+          int how[2] = {0, 0};
 #pragma unroll
           for (int w = 0; w < S::KT; ++w) {
             const int t0 = sp->tok0 + w * kTok;
-            flags[4 * zs + 1 + w] =
-                !finite ? 2
-                        : !(full && first + 1 - t0 >= kTok && first_seen(b, first + ntok - 1) <= t0);
+            how[w] = !finite ? 2
+                             : !(full && first + 1 - t0 >= kTok &&
+                                 first_seen(b, first + ntok - 1) <= t0);
           }
+          *reinterpret_cast<int4 *>(smem + S::flags + 16 * zs) =
+              make_int4(rows, how[0], how[1], i * b.tb);
         }
         __syncwarp();
         if (lane == 0 && !dead) ptx::mbar_arrive(bar(S::z_full) + 8 * zs);
