@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kJoinThr, 4) chunk_join_kernel(const __grid_co
 ChunkShape chunk_shape(const DevLayout &l) {
   if (chunk_tc_layout(l)) return chunk_tc_shape(l);
   const int dv = l.kind == KAMERA_GQA ? l.hd : l.latent;
-  return {kRows, kTileSh, (dv + kCols - 1) / kCols, kCols, kSms};
+  return {kRows, kTileSh, (dv + kCols - 1) / kCols, kCols, kSms, 1, 1, 0};
 }
 
 void chunk_blocks(ChunkArgs *a, int rows) {

@@ -3,10 +3,11 @@
 // Each request's new tokens are the last of its context; token t sees tokens [0, t], or the last
 // `window` of them. A block is a run of tb consecutive new tokens of a request with the query
 // heads of one KV head (and one part of V's columns): at most rb query rows that read the same
-// rows of K and V. A unit is one tile of 2^tile_sh cached tokens of a block, from the first that a
-// row of it sees to the last. Units are numbered by request, KV head, block, tile; workers take
-// consecutive ones, as many as one another, so that every worker has the same number of tiles
-// whatever the lengths and cuts at most its first and last block. Blocks that one worker has whole
+// rows of K and V. A block's work is its tiles of 2^tile_sh cached tokens, from the first that a row of
+// it sees to the last. It counts in units: some for each tile, more where the block has more rows than
+// fill a tensor-core tile, and some for its start and end. Units are numbered by request, KV head,
+// block, tile; workers take consecutive ones, as many as one another, whatever the lengths, and cut at
+// most their first and last block, between tiles. Blocks that one worker has whole
 // are written at once. Of a cut block the worker of its first tile writes its part to the worker's
 // home place and the others theirs to their carry places; the join kernel merges them by their
 // log-sum-exp.
@@ -122,6 +123,28 @@ __device__ __forceinline__ long long chunk_tiles(const ChunkArgs &a, const Chunk
   return sum;
 }
 
+// Units of a tile of a block of `ntok` tokens.
+__device__ __forceinline__ int chunk_weight(const ChunkArgs &a, int ntok) {
+  return a.pieces > 1 || ntok * a.hpk > a.shape.rb >> 1 ? a.shape.wide : a.shape.thin;
+}
+// Units of a request's first j blocks, of one KV head (and piece, and part of V's columns).
+__device__ __forceinline__ long long chunk_units(const ChunkArgs &a, const ChunkRequest &q, int j) {
+  const int w = chunk_weight(a, a.tb);
+  long long sum = w * chunk_tiles(a, q, j) + (long long)a.shape.extra * j;
+  if (j == q.nb) {  // the last one may have fewer tokens
+    const int first = (q.nb - 1) * a.tb, sh = a.shape.tile_sh;
+    const int tiles = (int)(((unsigned)q.ctx + (1u << sh) - 1u) >> sh) -
+                      (first_seen(a, q.past + first) >> sh);
+    sum += (long long)(chunk_weight(a, q.n - first) - w) * tiles;
+  }
+  return sum;
+}
+// The tile of a block that its unit u is of, with w units to a tile; a block's first units, for its
+// start and end, go with its first tile.
+__device__ __forceinline__ int chunk_tile(const ChunkArgs &a, int u, int w) {
+  return max(u - a.shape.extra, 0) / w;
+}
+
 // Where a worker starts, found by all threads of the CTA.
 struct ChunkStart {
   long long quot, rem;   // units of the call / workers and the rest
@@ -138,10 +161,11 @@ struct ChunkScratch {
   int r;
 };
 
-// `units_of`: a request's units. `a`: the batch, `n`: workers.
+// `units_of`: a request's units. `a`: the batch, `workers`: at most; each has `least` units or more.
 template <int THR, class Units>
-__device__ __forceinline__ ChunkStart units_start(const ChunkArgs &a, int n, int worker,
-                                                  ChunkScratch<THR> *sh, Units units_of) {
+__device__ __forceinline__ ChunkStart units_start(const ChunkArgs &a, int workers, int least,
+                                                  int worker, ChunkScratch<THR> *sh,
+                                                  Units units_of) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.n_reqs + THR - 1) / THR;
   const int r0 = min(a.n_reqs, tid * per), r1 = min(a.n_reqs, r0 + per);
@@ -169,10 +193,11 @@ __device__ __forceinline__ ChunkStart units_start(const ChunkArgs &a, int n, int
     total += sh->sums[i];
   }
   if (s.bad) total = 0;
+  const int n = total < (long long)workers * least ? max((int)total / least, 1) : workers;
   s.quot = div_pos(total, n);
   s.rem = total - s.quot * n;
-  const long long u0 = first_unit(s.quot, s.rem, worker);
-  s.units = first_unit(s.quot, s.rem, worker + 1) - u0;
+  const long long u0 = first_unit(s.quot, s.rem, min(worker, n));
+  s.units = first_unit(s.quot, s.rem, min(worker + 1, n)) - u0;
   const long long excl = before + incl - mine;
   if (s.units > 0 && u0 >= excl && u0 < excl + mine) {
     long long off = u0 - excl;
@@ -197,8 +222,8 @@ __device__ __forceinline__ ChunkStart units_start(const ChunkArgs &a, int n, int
 template <int THR>
 __device__ __forceinline__ ChunkStart chunk_start(const ChunkArgs &a, int worker,
                                                   ChunkScratch<THR> *sh) {
-  return units_start<THR>(a, a.shape.n, worker, sh, [&](const ChunkRequest &q) {
-    return (long long)a.n_kv * a.pieces * a.shape.vh * chunk_tiles(a, q, q.nb);
+  return units_start<THR>(a, a.shape.n, a.shape.wide, worker, sh, [&](const ChunkRequest &q) {
+    return (long long)a.n_kv * a.pieces * a.shape.vh * chunk_units(a, q, q.nb);
   });
 }
 
@@ -219,7 +244,7 @@ struct ChunkSegment {
 struct ChunkWalk {
   ChunkRequest q;
   long long left, quot, rem;
-  int r, hb, j, t, worker;  // the next block (request, head x part, block), its next tile
+  int r, hb, j, u, worker;  // the next block (request, head x part, block), its next unit
 
   __device__ __forceinline__ void start(const ChunkArgs &a, const ChunkStart &s, int worker_) {
     worker = worker_;
@@ -230,29 +255,36 @@ struct ChunkWalk {
     if (left == 0) return;
     bool bs, bi;
     q = chunk_request(a, r, &bs, &bi);
-    const long long per = chunk_tiles(a, q, q.nb);
+    const long long per = chunk_units(a, q, q.nb);
     const long long h = div_pos(s.off, per), rest = s.off - h * per;
     hb = (int)h;
     const int lane = threadIdx.x & 31;
     j = 0;  // the last block that starts at or before `rest`
     for (int len = q.nb; len > 1;) {
       const int step = (len + 31) >> 5, k = j + lane * step;
-      const bool in = lane * step < len && (lane == 0 || chunk_tiles(a, q, k) <= rest);
+      const bool in = lane * step < len && (lane == 0 || chunk_units(a, q, k) <= rest);
       const int i = __popc(__ballot_sync(0xffffffffu, in)) - 1;
       j += i * step;
       len = step == 1 ? 1 : min(step, len - i * step);
     }
-    t = (int)(rest - (j ? chunk_tiles(a, q, j) : 0));
+    u = (int)(rest - (j ? chunk_units(a, q, j) : 0));
   }
+  // The next segment, which has a tile: a cut between two units of one tile is before that tile, so a
+  // worker may have units of a block and no tile of it, at its end alone: with `wide` units or more a
+  // worker that begins behind a block's first tile has one.
   __device__ __forceinline__ bool next(const ChunkArgs &a, ChunkSegment *s) {
-    if (left == 0) return false;
+    while (left > 0)
+      if (step(a, s)) return true;
+    return false;
+  }
+  __device__ __forceinline__ bool step(const ChunkArgs &a, ChunkSegment *s) {
     const int heads = a.n_kv * a.pieces * a.shape.vh;
     if (hb == heads) {
       do {
         bool bs, bi;
         q = chunk_request(a, ++r, &bs, &bi);
       } while (q.n == 0);
-      hb = j = t = 0;
+      hb = j = u = 0;
     }
     const int part = hb % a.shape.vh, hp = hb / a.shape.vh, piece = hp % a.pieces;
     const int sh = a.shape.tile_sh;
@@ -267,17 +299,19 @@ struct ChunkWalk {
     s->ctx = q.ctx;
     const int b0 = first_seen(a, s->first) >> sh;
     const int b1 = (int)(((unsigned)(s->first + s->ntok) + (1u << sh) - 1u) >> sh);
-    const int nt = b1 - b0 - t, take = (int)(left < nt ? left : nt);
-    s->t0 = b0 + t;
-    s->t1 = s->t0 + take;
-    s->more = t > 0 ? -1 : take < nt ? workers_for(quot, rem, worker + 1, nt - take) : 0;
-    left -= take;
-    t = 0;
+    const int w = chunk_weight(a, s->ntok), all = (b1 - b0) * w + a.shape.extra;
+    const int end = left < all - u ? u + (int)left : all;
+    const int t0 = chunk_tile(a, u, w), t1 = chunk_tile(a, end, w);
+    s->t0 = b0 + t0;
+    s->t1 = b0 + t1;
+    s->more = t0 > 0 ? -1 : end < all ? workers_for(quot, rem, worker + 1, all - end) : 0;
+    left -= end - u;
+    u = 0;
     if (++j == q.nb) {
       j = 0;
       ++hb;
     }
-    return true;
+    return t0 < t1;
   }
 };
 

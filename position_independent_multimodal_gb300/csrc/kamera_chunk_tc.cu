@@ -891,9 +891,16 @@ bool chunk_tc_layout(const DevLayout &l) {
          (l.kind == KAMERA_MLA && l.latent == 512 && l.rope_d == 64);
 }
 
+// Two query tiles: a tile of a block of one of them takes about five sixths of the time of one of two,
+// and a block's start and end that of a tile. With tiles alone counted the CTAs of 40 requests, 36 of
+// which decode, end at 513000 to 664000 cycles, those of three prompts of 4001 tokens at 449000 to
+// 598000, and take 372 and 342 us; with 6, 5 and 6 units 344 and 330, 64-wide heads with a window 73.7
+// for 76, but eight requests that decode over 700 tokens, one or two tiles a CTA, 26.2 for 24.6. (4, 3
+// and 4: 347, 337, 74.1 and 25.7; a block counted as a tile, tiles alike: 370, 328, 73.8 and 24.8.)
+// MLA's blocks are alike and have many tiles.
 ChunkShape chunk_tc_shape(const DevLayout &l) {
-  if (l.kind == KAMERA_MLA) return {kRow, kTokSh, 2, 256, kSms};
-  return {2 * kRow, kTokSh, 1, l.hd, kSms};
+  if (l.kind == KAMERA_MLA) return {kRow, kTokSh, 2, 256, kSms, 1, 1, 0};
+  return {2 * kRow, kTokSh, 1, l.hd, kSms, 6, 5, 6};
 }
 
 cudaError_t prepare_chunk_tc(const DevLayout &l) {

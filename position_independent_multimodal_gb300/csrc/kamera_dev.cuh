@@ -234,6 +234,8 @@ struct ChunkShape {
   int rb, tile_sh;      // rows of a block; a tile has 2^tile_sh tokens
   int vh, vw;           // parts of V's columns, columns of a part
   int n;                // workers
+  int wide, thin;       // units of a tile of a block of more than rb / 2 rows, of another
+  int extra;            // units of a block besides
 };
 
 struct ChunkArgs {

@@ -80,7 +80,7 @@ __device__ __forceinline__ long long mass_units(const MassArgs &a, const ChunkRe
 template <int THR>
 __device__ __forceinline__ ChunkStart mass_start(const MassArgs &a, int worker,
                                                  ChunkScratch<THR> *sh) {
-  return units_start<THR>(a.b, a.shape.n, worker, sh, [&](const ChunkRequest &q) {
+  return units_start<THR>(a.b, a.shape.n, 1, worker, sh, [&](const ChunkRequest &q) {
     return (long long)a.b.n_kv * a.b.pieces *
            mass_units(a, q, mass_tile0(a, q), mass_tiles(a, q));
   });
