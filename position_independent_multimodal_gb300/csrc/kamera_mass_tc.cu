@@ -80,7 +80,8 @@ struct Shape {
   static constexpr int total = seg + kSegs * sizeof(Seg);
   static constexpr int scratch = z;                  // of the start
   static_assert(total <= 232448, "shared memory of one CTA");
-  static_assert(DK % UC == 0 && AC % UC == 0 && walk % 8 == 0 && scratch % 8 == 0 && flags % 16 == 0, "whole stages, 64-bit numbers");
+  static_assert(DK % UC == 0 && AC % UC == 0, "whole stages");
+  static_assert(walk % 8 == 0 && scratch % 8 == 0 && flags % 16 == 0, "of wide loads and stores");
   static_assert(kPieces == 1 || kCols == 32, "a piece's columns in registers");
   static_assert(sizeof(ChunkScratch<kThr>) <= kZ * kRow * 4, "the start's scratch");
 };
