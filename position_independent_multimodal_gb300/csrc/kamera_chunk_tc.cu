@@ -30,8 +30,9 @@
 // Measured: 2011 new tokens over 60000 (28 query heads, 4 KV heads of 128) at 1280 TFLOP/s, two thirds of
 // the dense rate: 3400 cycles a tile of tokens for two query tiles, 2080 of them products, the rest the
 // chain from S over the weights to P V that two tiles do not fill (with weights left out 931 us of 1370).
-// MLA, 16 heads, 4 x 300 tokens over 9003: 429 us, 8000 cycles a tile for 3328 of products: one thread
-// issues 100 of them a tile, and waits for thirteen stages.
+// MLA, 16 heads, 4 x 300 tokens over 9003: 429 us, 5350 cycles a tile for 3330 of products: Q leaves
+// room for five stages of 16 KB, and a tile takes thirteen. With a thread and a ring of its own for K
+// (three stages) and for V (two) 457 us: the ring's latency counts, not the issue.
 // Layout: every operand tile is 128 rows of 128 bytes (64 elements), swizzled in 128-byte rows;
 // V is read MN-major, so its rows land unchanged too.
 #include "kamera_chunk.cuh"
