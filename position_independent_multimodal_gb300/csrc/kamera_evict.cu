@@ -37,6 +37,7 @@ __device__ __forceinline__ uint32_t mass_key(float x) {
 }
 
 constexpr int kPickThr = 1024, kBins = 2048;
+constexpr int kLoads = 8;  // masses that a thread asks for together
 
 __global__ void __launch_bounds__(kPickThr) evict_pick_kernel(const __grid_constant__ EvictArgs a) {
   __shared__ int bins[kBins], sums[32], chosen[2];
@@ -65,6 +66,9 @@ __global__ void __launch_bounds__(kPickThr) evict_pick_kernel(const __grid_const
   }
   const float *mass = a.mass + (long long)it.req * a.mass_stride;
   const int c0 = it.first, c1 = n - it.last;  // the tokens that are judged
+  auto of_warps_before = [&]() {
+    return __reduce_add_sync(0xffffffffu, lane < warp ? sums[lane] : 0);
+  };
   // the smallest key that stays, found from its upper bits down, and how many of that key stay
   uint32_t key = 0;
   int need = k - it.first - it.last;
@@ -74,10 +78,18 @@ __global__ void __launch_bounds__(kPickThr) evict_pick_kernel(const __grid_const
       const int shift = round == 0 ? 21 : round == 1 ? 10 : 0, bits = round == 2 ? 10 : 11;
       for (int i = tid; i < kBins; i += kPickThr) bins[i] = 0;
       __syncthreads();
-      for (int i = c0 + tid; i < c1; i += kPickThr) {
-        const uint32_t x = mass_key(mass[i]);
-        if (round == 0 || x >> (shift + bits) == key >> (shift + bits))
-          atomicAdd(bins + (x >> shift & ((1u << bits) - 1u)), 1);
+      for (int i0 = c0 + tid; i0 < c1; i0 += kLoads * kPickThr) {
+        float m[kLoads];
+#pragma unroll
+        for (int e = 0; e < kLoads; ++e)
+          m[e] = i0 + e * kPickThr < c1 ? mass[i0 + e * kPickThr] : 0.f;
+#pragma unroll
+        for (int e = 0; e < kLoads; ++e) {
+          const uint32_t x = mass_key(m[e]);
+          if (i0 + e * kPickThr < c1 &&
+              (round == 0 || x >> (shift + bits) == key >> (shift + bits)))
+            atomicAdd(bins + (x >> shift & ((1u << bits) - 1u)), 1);
+        }
       }
       __syncthreads();
       // bins from the greatest down: thread t has bins kBins - 1 - 2 t and the one below
@@ -89,8 +101,7 @@ __global__ void __launch_bounds__(kPickThr) evict_pick_kernel(const __grid_const
       }
       if (lane == 31) sums[warp] = incl;
       __syncthreads();
-      int before = incl - b0 - b1;
-      for (int i = 0; i < warp; ++i) before += sums[i];
+      const int before = incl - b0 - b1 + of_warps_before();
       if (before < need && before + b0 + b1 >= need) {
         const bool low = before + b0 < need;
         chosen[0] = kBins - 1 - 2 * tid - low;
@@ -105,51 +116,61 @@ __global__ void __launch_bounds__(kPickThr) evict_pick_kernel(const __grid_const
   // Each warp has a run of tokens: its ties, then (with the ties before it) what it keeps.
   const int per = ((n + 31) / 32 + 31) & ~31, t0 = min(n, warp * per), t1 = min(n, t0 + per);
   const bool judged = k > it.first + it.last;
-  auto state = [&](int t) {  // 0 goes, 1 a tie, 2 stays
+  auto state = [&](int t, float m) {  // 0 goes, 1 a tie, 2 stays
     if (t >= t1) return 0;
     if (t < c0 || t >= c1) return 2;
     if (!judged) return 0;
-    const uint32_t x = mass_key(mass[t]);
+    const uint32_t x = mass_key(m);
     return x > key ? 2 : (x == key ? 1 : 0);
   };
+  // calls f(token of the lane, its state) for the warp's tokens, 32 at a time
+  auto each = [&](auto f) {
+    for (int t = t0 + lane; t - lane < t1; t += 32 * kLoads) {
+      float m[kLoads];
+#pragma unroll
+      for (int e = 0; e < kLoads; ++e) {
+        const int u = t + 32 * e;
+        m[e] = judged && u < t1 && u >= c0 && u < c1 ? mass[u] : 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < kLoads; ++e)
+        if (t - lane + 32 * e < t1) f(t + 32 * e, state(t + 32 * e, m[e]));
+    }
+  };
   int ties = 0, sure = 0;
-  for (int t = t0; t < t1; t += 32) {
-    const int v = state(t + lane);
+  each([&](int, int v) {
     ties += __popc(__ballot_sync(0xffffffffu, v == 1));
     sure += __popc(__ballot_sync(0xffffffffu, v == 2));
-  }
+  });
   if (lane == 0) sums[warp] = ties;
   __syncthreads();
-  int tie0 = 0;
-  for (int i = 0; i < warp; ++i) tie0 += sums[i];
+  const int tie0 = of_warps_before();
   __syncthreads();
   const int mine = sure + max(0, min(ties, need - tie0));
   if (lane == 0) sums[warp] = mine;
   if (tid == 0) chosen[0] = k;
   __syncthreads();
-  int at = 0;
-  for (int i = 0; i < warp; ++i) at += sums[i];
+  const int at = of_warps_before();
   int from = k;  // the first token that moves
   int *list = kept;
   // what stays is listed, unless pages forbid it: so the first token that moves is found first
   for (int pass = 0; pass < 2; ++pass) {
     int j = at, tie = tie0;
-    for (int t = t0; t < t1; t += 32) {
-      const int v = state(t + lane);
+    each([&](int t, int v) {
       const uint32_t eq = __ballot_sync(0xffffffffu, v == 1), below = (1u << lane) - 1u;
       const bool stays = v == 2 || (v == 1 && tie + __popc(eq & below) < need);
       const uint32_t in = __ballot_sync(0xffffffffu, stays);
       const int to = j + __popc(in & below);
       if (stays) {
         if (pass == 0) {
-          if (to != t + lane) from = min(from, to);
+          if (to != t) from = min(from, to);
         } else {
-          list[to] = t + lane;
+          list[to] = t;
         }
       }
       j += __popc(in);
       tie += __popc(eq);
-    }
+    });
     if (pass == 1) break;
     for (int o = 16; o > 0; o >>= 1) from = min(from, __shfl_xor_sync(0xffffffffu, from, o));
     if (lane == 0 && from < k) atomicMin(chosen, from);
@@ -178,7 +199,9 @@ __global__ void __launch_bounds__(kPickThr) evict_pick_kernel(const __grid_const
 // rows
 // ---------------------------------------------------------------------------------------
 
-constexpr int kMoveThr = 256, kStages = 3;
+constexpr int kMoveThr = 256;
+constexpr int kAhead = 3;                          // stages of rows on their way
+constexpr int kStages = kAhead + 1, kLists = kAhead + 2;
 constexpr int kPieces = 16;                        // 16-byte pieces of a strip
 constexpr int kStageRows = 64;
 constexpr int kStageBytes = kStageRows * kPieces * 16;
@@ -186,7 +209,7 @@ constexpr int kStageBytes = kStageRows * kPieces * 16;
 __global__ void __launch_bounds__(kMoveThr) evict_move_kernel(const __grid_constant__ EvictArgs a,
                                                               int strips_k, int strips) {
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ int src[kStages][kStageRows], dst[kStages][kStageRows];
+  __shared__ int rows_at[kLists][2][kStageRows];  // slots that rows come from, go to
   const int tid = threadIdx.x, ps = a.lay.page_size;
   ptx::wait_for_previous();
   const EvictPlan plan = static_cast<const EvictPlan *>(a.ws)[blockIdx.y];
@@ -213,14 +236,23 @@ __global__ void __launch_bounds__(kMoveThr) evict_move_kernel(const __grid_const
   const int *pages = a.pool.pt + (long long)plan.req * a.pool.pt_stride;
   const int stages = (plan.keep - plan.from + kStageRows - 1) / kStageRows;
   const uint32_t sb = ptx::smem_addr(smem);
-  auto slot = [&](int tok) { return pages[tok / ps] * ps + tok % ps; };
-  auto look_up = [&](int st) {  // the rows of a stage
-    const int i = tid & (kStageRows - 1), j = plan.from + st * kStageRows + i;
-    if (st >= stages || j >= plan.keep) return;
-    if (tid < kStageRows)
-      src[st % kStages][i] = slot(kept[j]);
-    else if (tid < 2 * kStageRows)
-      dst[st % kStages][i] = slot(j);
+  // The rows of a stage, a thread to the slot that one comes from or goes to. Its token and its page
+  // are asked for a stage ahead each, so no stage waits for them.
+  const int part = tid / kStageRows, mine = tid & (kStageRows - 1);
+  int tok = 0, was = 0, page = 0, tok_of = 0, page_of = 0;  // stages with a token, with a page
+  auto look_up = [&](bool list) {
+    if (part > 1) return;
+    if (list) {
+      rows_at[(page_of - 1) % kLists][part][mine] = page * ps + was % ps;
+    }
+    if (page_of < tok_of) {
+      was = tok;
+      page = pages[tok / ps];
+      ++page_of;
+    }
+    const int j = min(plan.from + tok_of * kStageRows + mine, plan.keep - 1);
+    tok = part ? j : kept[j];
+    ++tok_of;
   };
   auto rows_of = [&](int st) { return min(kStageRows, plan.keep - plan.from - st * kStageRows); };
   auto read = [&](int st) {
@@ -229,26 +261,28 @@ __global__ void __launch_bounds__(kMoveThr) evict_move_kernel(const __grid_const
       for (int e = tid; e < kStageRows * kPieces; e += kMoveThr) {
         const int i = e / kPieces, p = e % kPieces;
         if (i < rows && p < np)
-          ptx::cp_async16(sb + b * kStageBytes + e * 16, base + (long long)src[b][i] * row + p * 8,
-                          16u);
+          ptx::cp_async16(sb + b * kStageBytes + e * 16,
+                          base + (long long)rows_at[st % kLists][0][i] * row + p * 8, 16u);
       }
     }
     ptx::cp_async_commit();
   };
-  look_up(0);
-  look_up(1);
+  if (stages == 0) return;
+  look_up(false);                                      // tokens of stage 0
+  look_up(false);                                      // its pages, tokens of stage 1
+  for (int k = 0; k <= kAhead; ++k) look_up(true);     // lists of stages 0 to kAhead
   __syncthreads();
-  read(0);
+  for (int k = 0; k < kAhead; ++k) read(k);
   for (int st = 0; st < stages; ++st) {
-    read(st + 1);
-    look_up(st + 2);
-    ptx::cp_async_wait_group1();
+    read(st + kAhead);
+    look_up(true);                                     // of stage st + kAhead + 1
+    ptx::cp_async_wait_group<kAhead>();
     __syncthreads();  // the stage has been read by all
     const int b = st % kStages, rows = rows_of(st);
     for (int e = tid; e < kStageRows * kPieces; e += kMoveThr) {
       const int i = e / kPieces, p = e % kPieces;
       if (i < rows && p < np)
-        *reinterpret_cast<uint4 *>(base + (long long)dst[b][i] * row + p * 8) =
+        *reinterpret_cast<uint4 *>(base + (long long)rows_at[st % kLists][1][i] * row + p * 8) =
             *reinterpret_cast<const uint4 *>(smem + b * kStageBytes + e * 16);
     }
     __syncthreads();

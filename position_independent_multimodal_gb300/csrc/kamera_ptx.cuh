@@ -34,6 +34,11 @@ __device__ __forceinline__ void cp_async_wait_all() {
 __device__ __forceinline__ void cp_async_wait_group1() {
   asm volatile("cp.async.wait_group 1;" ::: "memory");
 }
+// all but the kN most recently committed groups have landed
+template <int kN>
+__device__ __forceinline__ void cp_async_wait_group() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
+}
 // 4-byte copy through L1 (page-table entries)
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
