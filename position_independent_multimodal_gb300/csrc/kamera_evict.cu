@@ -3,16 +3,18 @@
 //
 //  * evict_pick_kernel, a CTA to a request: the mass of the last token that stays is found by three
 //    rounds of counting (11, 11 and 10 bits of the masses' order), then every warp lists what stays
-//    of its part of the tokens, in order. Ties go to the lowest token. The masses are read four times
-//    from L2 by one SM: 10 us for 701 tokens, 14 for 20 requests of 4000, 40 for six of 30000, next
-//    to 17, 562 and 381 of the moves.
+//    of its part of the tokens, in order. Ties go to the lowest token. The masses are read six times
+//    from L2 by one SM: 10 us for 701 tokens, 13 for 20 requests of 4000, 40 for six of 30000, next
+//    to 15, 552 and 335 of the moves. It is bound by its instructions (equal masses of a warp counted
+//    as one by a match: 54 us for 40).
 //  * evict_move_kernel: token kept[j] moves to token j <= kept[j]. A CTA takes one strip of columns
 //    of one layer and walks the tokens upwards, several stages of rows on their way through shared
 //    memory: rows are written only after all rows up to them have been read, and what later stages
 //    read lies above all that has been written, so reads may run ahead of the writes. The masses
-//    move likewise. It is bound by HBM: 3.76 GB of rows of 512 columns read and written in 562 us, 6.7
+//    move likewise. It is bound by HBM: 3.76 GB of rows of 512 columns read and written in 552 us, 6.8
 //    TB/s, as fast as a copy; 2.1 GB of MLA's, whose 816 strips do not fill the last round of CTAs, in
-//    381 us, 5.5 TB/s.
+//    335 us, 6.2 TB/s. Two, three and five stages of 64 rows on their way: 395, 388 and 399 us of the
+//    call for MLA; strips of 128 bytes 393 to 401, and 604 to 616 of the call for 582 at 20 requests.
 #include <mutex>
 
 #include "kamera_dev.cuh"
