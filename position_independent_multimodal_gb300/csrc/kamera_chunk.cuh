@@ -27,9 +27,8 @@ struct ChunkRecord {
   int row, rows;   // of it: row of q of its first token, query rows
   int h0, part;    // of it: first query head, part of V's columns
   int gave_up;
-  int segments;    // segments of the worker
   int odd;         // 1: some of its outputs are not finite
-  int pad[7];
+  int pad[8];
 };
 
 struct ChunkPlaces {
@@ -396,7 +395,6 @@ __device__ __forceinline__ void chunk_note(ChunkRecord *rec, const ChunkSegment 
   c.h0 = last.h0;
   c.part = last.part;
   c.gave_up = gave_up;
-  c.segments = segments;
   c.odd = odd;
   *rec = c;
 }
