@@ -341,12 +341,17 @@ __device__ __forceinline__ void task_loop(const ReuseArgs &a, uint32_t s0, unsig
   }
   ptx::cp_async_commit();
   ptx::cp_async_wait_group1();  // tile 0 (and V_m^T)
-  if (INPLACE && a.sign < 0)  // subtraction: negate V_m^T exactly (bf16 sign bits)
-    for (int e = tid; e < Kp * NCORE * 4; e += kThrT) {
-      const uint32_t ad = v_op + 4 * e;
-      uint32_t w;
-      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(ad));
-      asm volatile("st.shared.b32 [%0], %1;" ::"r"(ad), "r"(w ^ 0x80008000u) : "memory");
+  if (INPLACE && a.sign < 0)  // subtraction: negate V_m^T exactly (bf16 sign bits); a thread what it
+    for (int e = tid; e < Kp * NCORE; e += kThrT) {  // has copied, as others' copies may not be there
+      const int k = e / NCORE, j = e % NCORE;
+      const uint32_t ad = v_op + ((k >> 3) * NCORE + j) * 128 + (k & 7) * 16;
+      uint4 w;
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                   : "r"(ad)
+                   : "memory");
+      sts16(ad, make_uint4(w.x ^ 0x80008000u, w.y ^ 0x80008000u, w.z ^ 0x80008000u,
+                           w.w ^ 0x80008000u));
     }
   ptx::fence_proxy_async_smem();
   ptx::tc_fence_before();
