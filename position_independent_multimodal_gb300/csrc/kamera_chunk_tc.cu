@@ -379,6 +379,8 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
         xch[qr * kRow + lane_row] = n > w ? l * f0 : 0.f;
         ptx::barrier_sync(2, 4 * kRow);
         l = (all[0] + all[kRow]) + (all[2 * kRow] + all[3 * kRow]);
+        // (the other tile's warps write maxima over these sums in the next segment, whose S may be there)
+        ptx::barrier_sync(2, 4 * kRow);
       } else if (live) {
         xch[qr * kRow + lane_row] = l;
         ptx::barrier_sync(pair, 64);
