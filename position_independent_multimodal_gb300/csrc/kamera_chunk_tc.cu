@@ -810,6 +810,10 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
               if (i < 2) o_free();
               mma_o(o, t, i < 2, kp);
             }
+            // Without a tile of its own it has not waited for the softmax warps to leave the segment
+            // before. It has to: with two phases of o_full behind one another they would wait for the
+            // first and take it for one that is still to come.
+            if (last < 0) o_free();
           }
           commit(S::o_full + t);
         } else {

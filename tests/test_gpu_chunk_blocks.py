@@ -1,4 +1,5 @@
 """kamera_chunk_attention: workers that take several blocks one after another."""
+import numpy as np
 import pytest
 import torch
 
@@ -34,3 +35,22 @@ def test_blocks_whose_tiles_are_taken_in_turns(name, reqs, ctx, sharp):
     # requests that decode, as many blocks of one length for each of 152 workers: each takes two or
     # more whole ones, and its two query tiles join their sums at the end of each
     repeat(Chunks(name, [(1, ctx - 1)] * reqs, seed=20, sharp=sharp), 20)
+
+
+@pytest.mark.parametrize("name,reqs", [("gqa128-group7", 400), ("gqa64-group3", 900),
+                                       ("gqa128-group4-page64", 900), ("mha64-page5", 400)])
+def test_blocks_of_one_tile(name, reqs):
+    # a context of 128 is one whole tile: the other query tile has nothing to do but keep step, for
+    # several blocks in a row and in the last
+    repeat(Chunks(name, [(1, 127)] * reqs, seed=21), 40)
+
+
+@pytest.mark.parametrize("name,many", [("gqa128-group7", 36), ("gqa64-group3", 84),
+                                       ("gqa128-group4-page64", 60)])
+@pytest.mark.parametrize("seed", [22, 23])
+def test_blocks_of_one_tile_behind_others(name, many, seed):
+    # behind blocks of two query tiles, of one tile of tokens and of more, and before them
+    pattern = [(many, 128 - many), (1, 127), (1, 127), (many, 300), (1, 127), (1, 40), (1, 200)]
+    rs = np.random.RandomState(seed)
+    reqs = [pattern[k] for k in rs.randint(0, len(pattern), 300)]
+    repeat(Chunks(name, reqs, seed=seed), 20)
