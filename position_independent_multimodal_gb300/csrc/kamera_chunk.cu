@@ -281,6 +281,7 @@ __device__ __noinline__ void chunk_row_again(const ChunkArgs &a, const ChunkSegm
 // worker starts which multiply a value that is not finite for a row that does not see it.
 __global__ void __launch_bounds__(kJoinThr, 4) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
   __shared__ ChunkScratch<kJoinThr> found;
+  constexpr int kAtOnce = 4;  // rows that a warp joins together, of blocks of two parts
   const int w = blockIdx.x, lane = threadIdx.x & 31;
   const int first = blockIdx.y * (kJoinThr / 32) + (threadIdx.x >> 5);
   const int step = gridDim.y * (kJoinThr / 32);
@@ -308,7 +309,6 @@ __global__ void __launch_bounds__(kJoinThr, 4) chunk_join_kernel(const __grid_co
         v.y = pack_bf16(acc[2] * inv, acc[3] * inv);
         *reinterpret_cast<uint2 *>(a.out + rh * a.dv + rec.part * vw + col) = v;
       };
-      constexpr int kAtOnce = 4;
       for (int i0 = first * kAtOnce; np == 2 && i0 < rec.rows; i0 += step * kAtOnce) {
         // two parts, as most cut blocks have: several rows' loads together
         for (int col = 4 * lane; col < cols; col += 128) {
@@ -397,8 +397,12 @@ __global__ void __launch_bounds__(kJoinThr, 4) chunk_join_kernel(const __grid_co
   ChunkSegment s;
   while (walk.next(a, &s)) {
     const bool again = !s.carry() && chunk_odd(a, s, threadIdx.x >> 5, kJoinThr / 32);
-    if (__syncthreads_or(again))
-      for (int i = first; i < s.ntok * s.heads; i += step) chunk_row_again(a, s, i);
+    if (__syncthreads_or(again)) {
+      // each row by the warp that has joined it, so that this is what is written last
+      const int rows = s.ntok * s.heads, run = s.more == 1 ? kAtOnce : 1;
+      for (int i0 = first * run; i0 < rows; i0 += step * run)
+        for (int i = i0; i < min(i0 + run, rows); ++i) chunk_row_again(a, s, i);
+    }
   }
 }
 
