@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
           }
           if (cols > 0) weigh(x, 0);
         }
-        if (lane == 0 && !dead) ptx::mbar_arrive(bar(S::z_free) + 8 * zs);
+        arrive(bar(S::z_free) + 8 * zs);  // (all lanes have read theirs)
       }
       float sum;
       {
