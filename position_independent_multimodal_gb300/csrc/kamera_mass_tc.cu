@@ -65,9 +65,9 @@ struct Shape {
   static constexpr int ring = k + SETS * kSet;
   static constexpr int z = ring + NST * kStage;      // float [kZ][kRow]: c' lse, inf for no row
   static constexpr int xch = z + kZ * kRow * 4;      // float [kParts - 1][KT * kTok]: sums
-  // int [kZ][4] of a unit: its rows; how tile 0 and tile 1 are taken (0: all columns are seen by the
-  // tile's tokens; 1: a run of them by each token; 2: and their log-sum-exps are to be looked at); its
-  // first of its request's new tokens
+  // int [kZ][4] of a unit: its rows; how tile 0 and tile 1 are taken (0: all rows see the tile's
+  // tokens; 1: a run of them each token; 2: and their log-sum-exps are to be looked at); its first of
+  // its request's new tokens
   static constexpr int flags = xch + (kParts - 1) * KT * kTok * 4;
   static constexpr int bar = flags + kZ * 16;
   static constexpr int k_full = 0, k_empty = k_full + SETS * DK, q_full = k_empty + SETS * DK,
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
         wait(bar(S::z_full) + 8 * zs, u / kZ & 1);
         const int4 flags = *reinterpret_cast<const int4 *>(smem + S::flags + 16 * zs);
         const int rows = flags.x, how = w ? flags.z : flags.y;
-        int see0, see1;  // the columns whose tokens see this one: [see0, see1)
+        int see0 = 0, see1 = rows;  // the columns whose tokens see this one: [see0, see1)
         if (how) {
           const int ahead = tok - past - flags.w;
           see0 = ahead > 0 ? min(ahead, kRow) * b.hpk : 0;
@@ -283,7 +283,8 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
             sa = add2(sa, f2(s0, 0.f));
             return;
           }
-          if (how == 1) {
+          // (columns behind the rows too: of a key with an infinity they are 0 times it, NaN)
+          if (how == 1 || col0 + 32 > rows) {
             const int from = see0 - col0, to = see1 - col0;
             const uint32_t up = from <= 0 ? 0xffffffffu : from >= 32 ? 0u : 0xffffffffu << from;
             const uint32_t dn = to >= 32 ? 0xffffffffu : to <= 0 ? 0u : (1u << to) - 1u;
@@ -319,10 +320,18 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
 #pragma unroll
             for (int g = 0; g < S::kCols; g += 16) {
               uint32_t *next = x[(g >> 4 & 1) ^ 1];
-              if (g + 16 < S::kCols)
+              if (g + 16 < S::kCols) {
                 ptx::tmem_ld16(at + g + 16, next);
-              else
+              } else {
                 give(u);
+                if (cols < S::kCols) {  // as in weigh
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) {
+                    uint32_t &y = x[g >> 4 & 1][e];
+                    y = g + e < cols ? y : nothing;
+                  }
+                }
+              }
               some(x[g >> 4 & 1], g);
               if (g + 16 < S::kCols) ptx::tmem_ld_wait_all<16>(next);
             }
