@@ -421,9 +421,14 @@ void chunk_blocks(ChunkArgs *a, int rows) {
 
 size_t chunk_workspace(const DevLayout &l) { return chunk_places(chunk_shape(l), nullptr).total; }
 
+// How long a wait of the tcgen05 kernels over chunks may take. Tests set it to 0, which makes every
+// CTA give up before it begins; not for other use.
+extern "C" unsigned long long kamera_chunk_wait_ns;
+unsigned long long kamera_chunk_wait_ns = kPrefixWaitNs;
+
 cudaError_t launch_chunk_attention(const ChunkArgs &args, cudaStream_t s) {
   ChunkArgs a = args;
-  a.wait_ns = kPrefixWaitNs;
+  a.wait_ns = kamera_chunk_wait_ns;
   static int configured[64][4] = {{0}};
   static std::mutex mu;
   int dev = 0;

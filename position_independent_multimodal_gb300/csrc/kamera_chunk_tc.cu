@@ -112,8 +112,9 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
   const ChunkPlaces places = chunk_places(a.shape, a.ws);
   auto bar = [&](int i) { return sb + S::bar + 8 * i; };
   // Waits for a phase, giving up after a.wait_ns or when another thread has. A thread that gave up
-  // runs on to its end without waiting, arriving, copying or multiplying: it keeps step with the
-  // named barriers only, and no barrier gets an arrival that it does not expect.
+  // runs on to the end of its segment without waiting, arriving, copying or multiplying: it keeps step
+  // with the named barriers only, and no barrier gets an arrival that it does not expect. Threads that
+  // meet (a warp, the softmax warps) leave together.
   bool dead = false;
   auto wait = [&](uint32_t b, uint32_t parity) {
     if (__builtin_expect(dead || ptx::mbar_try_wait(b, parity), 1)) return;
@@ -186,6 +187,19 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
     ++seg_no;
     return s;
   };
+  // The same for a whole warp: of its threads one alone may have given up (the elected one, on a stage),
+  // and none may leave while the others go on to what they do together.
+  auto take_whole = [&]() -> const ChunkSegment * {
+    const ChunkSegment *s = take_segment();
+    dead = __any_sync(0xffffffffu, dead);
+    return dead ? nullptr : s;
+  };
+  // And for all softmax warps, which meet at named barriers in every segment. What they have read of the
+  // exchange buffer in the segment before, too, they have read before any of them writes to it again.
+  auto take_together = [&]() -> const ChunkSegment * {
+    const ChunkSegment *s = take_segment();
+    return ptx::barrier_or(2, 32 * S::kSoft, dead) ? nullptr : s;
+  };
   if (warp == S::kSoft) {
     ChunkWalk w;
     w.start(a, st, blockIdx.x);
@@ -217,7 +231,7 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
     uint32_t mine = 0;   // tiles of this warp so far: phases of its buffers
     uint32_t seen = 0;   // tiles of the CTA's segments so far
     ChunkSegment last = {};
-    while (const ChunkSegment *sp = take_segment()) {
+    while (const ChunkSegment *sp = take_together()) {
       const ChunkSegment &s = *sp;
       const uint32_t parity = (seg_no - 1) & 1;
       if (tid == 0) last = s;
@@ -379,8 +393,6 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
         xch[qr * kRow + lane_row] = n > w ? l * f0 : 0.f;
         ptx::barrier_sync(2, 4 * kRow);
         l = (all[0] + all[kRow]) + (all[2 * kRow] + all[3 * kRow]);
-        // (the other tile's warps write maxima over these sums in the next segment, whose S may be there)
-        ptx::barrier_sync(2, 4 * kRow);
       } else if (live) {
         xch[qr * kRow + lane_row] = l;
         ptx::barrier_sync(pair, 64);
@@ -477,7 +489,7 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
       __syncwarp();
     };
     publish();
-    while (const ChunkSegment *sp = take_segment()) {
+    while (const ChunkSegment *sp = take_whole()) {
       const int n = sp->t1 - sp->t0, tile0 = sp->t0, ctx = sp->ctx;
       const int kcol = gqa ? sp->kvh * lay.hd : 0, vcol = kcol + sp->part * a.shape.vw;
       const int lo = first_seen(a, sp->first);  // tokens that a row sees: from here on
