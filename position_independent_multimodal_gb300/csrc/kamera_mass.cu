@@ -189,9 +189,11 @@ MassShape mass_shape(const DevLayout &l) {
 
 size_t mass_workspace(const DevLayout &l) { return mass_places(mass_shape(l), nullptr).total; }
 
+extern "C" unsigned long long kamera_chunk_wait_ns;  // kamera_chunk.cu
+
 cudaError_t launch_attention_mass(const MassArgs &args, cudaStream_t s) {
   MassArgs a = args;
-  a.b.wait_ns = kPrefixWaitNs;
+  a.b.wait_ns = kamera_chunk_wait_ns;
   static int configured[64][4] = {{0}};
   static std::mutex mu;
   int dev = 0;

@@ -109,8 +109,9 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
   const MassPlaces places = mass_places(a.shape, a.ws);
   auto bar = [&](int i) { return sb + S::bar + 8 * i; };
   // Waits for a phase, giving up after b.wait_ns or when another thread has. A thread that gave up
-  // runs on to its end without waiting, arriving, copying or multiplying: it keeps step with the
-  // named barriers only, and no barrier gets an arrival that it does not expect.
+  // runs on to the end of its segment without waiting, arriving, copying or multiplying: it keeps step
+  // with the named barriers only, and no barrier gets an arrival that it does not expect. Threads that
+  // meet (a warp, the warps of a token's parts) leave together.
   bool dead = false;
   auto wait = [&](uint32_t at, uint32_t parity) {
     if (__builtin_expect(dead || ptx::mbar_try_wait(at, parity), 1)) return;
@@ -182,6 +183,13 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
     ++seg_no;
     return s;
   };
+  // The same for a whole warp: of its threads one alone may have given up (the elected one, on a stage),
+  // and none may leave while the others go on to what they do together.
+  auto take_whole = [&]() -> const Seg * {
+    const Seg *s = take_segment();
+    dead = __any_sync(0xffffffffu, dead);
+    return dead ? nullptr : s;
+  };
   // Calls f(unit so far, KV head, piece of its query heads, tile of new tokens, first unit of the KV
   // head's K rows, last one) for the units of a segment.
   uint32_t units = 0;
@@ -229,7 +237,13 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
       if (lane == 0 && !dead) ptx::mbar_arrive(at);
     };
     MassRecord rec = {0, 0, 0, 0, 0, {0, 0, 0}};
-    while (const Seg *sp = take_segment()) {
+    // The warps of a token's parts meet at a barrier in every segment, so they leave together. Then all
+    // of them have read the sums of the segment before, too, which the next one's are written over.
+    auto take_together = [&]() -> const Seg * {
+      const Seg *s = take_segment();
+      return ptx::barrier_or(group, 32 * S::kParts, dead) ? nullptr : s;
+    };
+    while (const Seg *sp = take_together()) {
       const int tok = sp->tok0 + mine, ctx = sp->ctx, past = sp->past, more = sp->more, r = sp->r;
       rec.head = more > 0;
       rec.more = more;
@@ -247,6 +261,7 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
       for (; units != end; ++units) {
         const uint32_t u = units, zs = u % kZ;
         wait(bar(S::z_full) + 8 * zs, u / kZ & 1);
+        __syncwarp();  // (all take the same flags, also where they gave up)
         const int4 flags = *reinterpret_cast<const int4 *>(smem + S::flags + 16 * zs);
         const int rows = flags.x, how = w ? flags.z : flags.y;
         int see0 = 0, see1 = rows;  // the columns whose tokens see this one: [see0, see1)
@@ -387,7 +402,6 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
           }
         }
       }
-      ptx::barrier_sync(group, 32 * S::kParts);  // read before the next block's are written
     }
     if (tid == 0) places.rec[blockIdx.x] = rec;
   } else if (warp == S::kLoad || warp == S::kQ) {
@@ -430,7 +444,7 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
     publish();
     wait(bar(S::sg_full), 0);
     int next_y = look_up(segs);
-    while (const Seg *sp = take_segment()) {
+    while (const Seg *sp = take_whole()) {
       const int tok0 = sp->tok0, ctx = sp->ctx, r = sp->r;
       const int lo = first_seen(b, sp->past + sp->i0 * b.tb);  // no new token of the block sees one before
       const int y = next_y, count = each * S::KT;
@@ -551,7 +565,7 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
     const float inf = __int_as_float(0x7f800000);
     float *z = reinterpret_cast<float *>(smem + S::z);
     const bool counts = b.scale != 0.f;
-    while (const Seg *sp = take_segment()) {
+    while (const Seg *sp = take_whole()) {
       each_unit(sp, [&](uint32_t u, int kvh, int piece, int i, bool, bool) {
         const uint32_t zs = u % kZ;
         const int ntok = min(b.tb, sp->n - i * b.tb), h0 = kvh * b.hpk + piece * a.shape.qr;

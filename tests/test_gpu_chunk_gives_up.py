@@ -8,6 +8,7 @@ import torch
 import position_independent_multimodal_gb300 as km
 from tests.chunk_checks import check_rows
 from tests.chunk_testlib import Chunks
+from tests.test_gpu_attention_mass import Masses, check
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +49,25 @@ def test_attention_writes_nothing(limit, name):
 def test_other_widths_have_no_such_waits(limit):
     limit.value = 0
     check_rows(Chunks("gqa80", REQS, seed=31).run())
+
+
+@pytest.mark.parametrize("name", TENSOR)
+@pytest.mark.parametrize("decay", [0.0, 0.5])
+def test_masses_stay(limit, name, decay):
+    # (no window: the tokens before one only fade, by a kernel that waits for nothing)
+    b = Masses(name, REQS, seed=32, decay=decay).dev()
+    limit.value = 0
+    b.call()
+    torch.cuda.synchronize()
+    assert int(b.st.item()) == km.KAMERA_DEVICE_TIMEOUT
+    assert torch.equal(b.mass.cpu().nan_to_num(-1), b.before.nan_to_num(-1))
+    limit.value = 2_000_000_000
+    b.st.zero_()
+    b.call()
+    torch.cuda.synchronize()
+    check(b)
+
+
+def test_masses_of_other_widths_have_no_such_waits(limit):
+    limit.value = 0
+    check(Masses("gqa80", REQS, seed=33).run())
