@@ -582,9 +582,11 @@ kamera_status kamera_prefix_attention(const kamera_handle *handle, const kamera_
  * GQA and MLA as in kamera_decode_attention; softmax statistics and sums in float32, the softmax
  * weights rounded to bf16 for their product with V. Pages outside the pool set
  * KAMERA_DEVICE_SLOT_OOB and their tokens are left out; a token that sees nothing gets o = 0 and
- * lse = -inf. What a token does not see has no effect on it, whatever the values. After
- * KAMERA_DEVICE_TIMEOUT some outputs are not written. Limits: num_reqs <= 65535 and at most the
- * pool's num_reqs, num_q_heads <= 256 (GQA: a multiple of num_kv_heads), Dk <= 1024.
+ * lse = -inf. What a token does not see has no effect on it, whatever the values; where such a V is not
+ * finite it costs time, as the rows next to it are taken again one cached token after another (one in
+ * 2011 new tokens over 60000: 0.4 s). After KAMERA_DEVICE_TIMEOUT some outputs are not written.
+ * Limits: num_reqs <= 65535 and at most the pool's num_reqs, num_q_heads <= 256 (GQA: a multiple of
+ * num_kv_heads), Dk <= 1024.
  */
 size_t kamera_chunk_attention_workspace(const kamera_handle *handle, int32_t num_tokens,
                                         int32_t num_reqs, int32_t num_q_heads);
@@ -610,14 +612,16 @@ kamera_status kamera_chunk_attention(const kamera_handle *handle, const kamera_p
  *                ctx_len is above mass_stride sets KAMERA_DEVICE_BAD_ITEM and keeps its masses, as
  *                do requests without new tokens and those that kamera_chunk_attention refuses.
  *                Entries from ctx_len on are left as they were.
- * decay        : finite, 0 or more.
+ * decay        : finite, 0 or more. Above 0 all entries below ctx_len are read, those of the new
+ *                tokens too: a caller sets the entries of tokens that it appends to 0 (or to what
+ *                they are to begin with) before the first such call that sees them.
  * d_workspace  : kamera_attention_mass_workspace(handle, num_tokens, num_reqs, num_q_heads) bytes,
  *                16-byte aligned; contents ignored and left undefined. It serves one call at a
  *                time, as that of the page calls.
  * Products, weights and sums in float32, added in an order that the arguments fix. A token of a
  * page outside the pool sets KAMERA_DEVICE_SLOT_OOB and is laid nothing on (only its mass fades).
- * A row with lse = -inf (a token that saw nothing) lays nothing on any token. Limits as in
- * kamera_chunk_attention.
+ * A row with lse = -inf (a token that saw nothing) lays nothing on any token. After
+ * KAMERA_DEVICE_TIMEOUT some masses are as they were. Limits as in kamera_chunk_attention.
  */
 size_t kamera_attention_mass_workspace(const kamera_handle *handle, int32_t num_tokens,
                                        int32_t num_reqs, int32_t num_q_heads);

@@ -668,7 +668,8 @@ def kamera_attention_mass(handle: Handle, pool: Pool, layer: int, q: torch.Tenso
                           stream=None) -> None:
     """Softmax weights of the new tokens of a batch (as for kamera_chunk_attention, with the
     ``lse`` float32 [T][H_q] that it left) summed over query heads and new tokens, for each cached
-    token: ``mass`` float32 [R][columns] becomes ``decay * mass`` plus the sums."""
+    token: ``mass`` float32 [R][columns] becomes ``decay * mass`` plus the sums. With a ``decay`` above
+    0 the entries of new tokens are read too: they are to be set, to 0 as a rule, when these come."""
     p, dev = _pool_c(handle, pool)
     batch = _chunk(handle, dev, q, token_start, ctx_len)
     if lse.shape != batch[2:4]:

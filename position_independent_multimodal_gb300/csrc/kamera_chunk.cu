@@ -226,7 +226,10 @@ __global__ void __launch_bounds__(kThr) chunk_gen_kernel(const __grid_constant__
 constexpr int kJoinThr = 256;
 
 // One row of a block from its definition, token by token, by a warp: nothing that the row does not
-// see is read. For blocks with values of V that are not finite in such places.
+// see is read. For blocks with values of V that are not finite in such places, which are rare: it is as
+// slow as it is short. One such value among the last new tokens of 2011 over 60000 takes the call from 1.4
+// to 380 ms, of 4 x 300 over 9003 (MLA) from 0.43 to 195, of a batch over 8000 from 0.35 to 44, with 64-wide
+// heads and a window of 1000 from 0.08 to 5.
 __device__ __noinline__ void chunk_row_again(const ChunkArgs &a, const ChunkSegment &s, int i) {
   const int lane = threadIdx.x & 31;
   const DevLayout &lay = a.lay;

@@ -20,7 +20,7 @@
 // that nothing of a row that no token holds is ever multiplied. Tokens that not all rows of a block see
 // are: their V times a weight of 0, which is no 0 where V is not finite. Where an output is not finite
 // the join kernel therefore looks at V of such tokens, and takes the blocks where one is not finite
-// again, token by token.
+// again, token by token (right, and slow: kamera_chunk.cu).
 //   GQA: O and S of two query tiles fill the TMEM. A block of more than 128 rows has two tiles of
 //        them that share each K and V tile; of a smaller one (requests that decode) the two take
 //        turns with the tiles of tokens, each with a maximum, sum and O of its own, joined at the
@@ -30,7 +30,7 @@
 // Measured: 2011 new tokens over 60000 (28 query heads, 4 KV heads of 128) at 1280 TFLOP/s, two thirds of
 // the dense rate: 3400 cycles a tile of tokens for two query tiles, 2080 of them products, the rest the
 // chain from S over the weights to P V that two tiles do not fill (with weights left out 931 us of 1370).
-// MLA, 16 heads, 4 x 300 tokens over 9003: 429 us, 5350 cycles a tile for 3330 of products: Q leaves
+// MLA, 16 heads, 4 x 300 tokens over 9003: 430 us, 5350 cycles a tile for 3330 of products: Q leaves
 // room for five stages of 16 KB, and a tile takes thirteen. With a thread and a ring of its own for K
 // (three stages) and for V (two) 457 us: the ring's latency counts, not the issue.
 // Layout: every operand tile is 128 rows of 128 bytes (64 elements), swizzled in 128-byte rows;
@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(S::kThr, 1) chunk_tc_kernel(
   };
   // And for all softmax warps, which meet at named barriers in every segment. What they have read of the
   // exchange buffer in the segment before, too, they have read before any of them writes to it again.
+  // (Three prompts of 4001 tokens, 8 blocks a CTA: 328 us without this barrier, 333 with it.)
   auto take_together = [&]() -> const ChunkSegment * {
     const ChunkSegment *s = take_segment();
     return ptx::barrier_or(2, 32 * S::kSoft, dead) ? nullptr : s;
@@ -921,7 +922,8 @@ bool chunk_tc_layout(const DevLayout &l) {
 // which decode, end at 513000 to 664000 cycles, those of three prompts of 4001 tokens at 449000 to
 // 598000, and take 372 and 342 us; with 6, 5 and 6 units 344 and 330, 64-wide heads with a window 73.7
 // for 76, but eight requests that decode over 700 tokens, one or two tiles a CTA, 26.2 for 24.6. (4, 3
-// and 4: 347, 337, 74.1 and 25.7; a block counted as a tile, tiles alike: 370, 328, 73.8 and 24.8.)
+// and 4: 347, 337, 74.1 and 25.7; a block counted as a tile, tiles alike: 370, 328, 73.8 and 24.8. All
+// before the softmax warps met at each segment's start, which takes the prompts to 333.)
 // MLA's blocks are alike and have many tiles.
 ChunkShape chunk_tc_shape(const DevLayout &l) {
   if (l.kind == KAMERA_MLA) return {kRow, kTokSh, 2, 256, kSms, 1, 1, 0};

@@ -16,8 +16,8 @@
 // takes nine stages of Q), one the rows' log-sum-exps, and a thread for each tile of tokens issues the
 // MMAs. Copies of K as in kamera_chunk_tc.cu.
 //
-// Measured: 32 requests that decode over 3000 to 6001 tokens (28 query heads, 4 KV heads of 128) in 41
-// us, 3.6 TB/s of K; 250 new tokens over 30000 in 61 us, 1730 weights a clock of the chip's 4860. The
+// Measured: 32 requests that decode over 3000 to 6001 tokens (28 query heads, 4 KV heads of 128) in 42
+// us, 3.5 TB/s of K; 250 new tokens over 30000 in 62 us, 1700 weights a clock of the chip's 4860. The
 // weights' warps have 184 instructions for 64 weights and some 150 more around them; tokens next to
 // the new ones, whose columns are seen in part, take longer, and the CTA that has them ends last.
 #include "kamera_mass.cuh"
@@ -48,8 +48,8 @@ struct Seg {
 // over the 8 steps of 128 columns, 4.3e-7 over the 36 of MLA, where weights of large scores come out
 // 4e-6 too small. There the sum is taken in pieces, which take four TMEM buffers in turn and are added
 // in registers, rounded. Measured over six requests of 100 new tokens over 5000 (the masses' error, the
-// time): in one piece 3.8e-6, 62 us; pieces of three chunks 1.2e-6, 63; of two 8.5e-7, 63.5; of one
-// 5.5e-7, 65.5 us. Products in float32 with rounded sums give 7e-7: a chunk a piece it is.
+// time): in one piece 3.8e-6, 47 us; pieces of three chunks 1.2e-6, 48; of two 8.5e-7, 49; of one
+// 5.5e-7, 51 us. Products in float32 with rounded sums give 7e-7: a chunk a piece it is.
 template <int DK_, int KT_, int SETS_, int UC_, int NST_, int AC_>
 struct Shape {
   static constexpr int DK = DK_, KT = KT_, SETS = SETS_, UC = UC_, NST = NST_, AC = AC_;
