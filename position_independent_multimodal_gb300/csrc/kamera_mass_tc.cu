@@ -16,8 +16,8 @@
 // takes nine stages of Q), one the rows' log-sum-exps, and a thread for each tile of tokens issues the
 // MMAs. Copies of K as in kamera_chunk_tc.cu.
 //
-// Measured: 32 requests that decode over 3000 to 6001 tokens (28 query heads, 4 KV heads of 128) in 42
-// us, 3.5 TB/s of K; 250 new tokens over 30000 in 62 us, 1700 weights a clock of the chip's 4860. The
+// Measured: 32 requests that decode over 3000 to 6001 tokens (28 query heads, 4 KV heads of 128) in 41
+// us, 3.6 TB/s of K; 250 new tokens over 30000 in 61.5 us, 1730 weights a clock of the chip's 4860. The
 // weights' warps have 184 instructions for 64 weights and some 150 more around them; tokens next to
 // the new ones, whose columns are seen in part, take longer, and the CTA that has them ends last.
 #include "kamera_mass.cuh"
@@ -339,12 +339,14 @@ __global__ void __launch_bounds__(S::kThr, 1) mass_tc_kernel(const __grid_consta
                 ptx::tmem_ld16(at + g + 16, next);
               } else {
                 give(u);
-                if (cols < S::kCols) {  // as in weigh
+                uint32_t *y = x[g >> 4 & 1];
+                // as in weigh, four columns at a time (4 x 250 over 30000: 150 us, 154 with all sixteen
+                // looked at, 148 with none)
 #pragma unroll
-                  for (int e = 0; e < 16; ++e) {
-                    uint32_t &y = x[g >> 4 & 1][e];
-                    y = g + e < cols ? y : nothing;
-                  }
+                for (int q = 16; q > 0; q -= 4) {
+                  if (g + q <= cols) break;
+#pragma unroll
+                  for (int e = q - 4; e < q; ++e) y[e] = g + e < cols ? y[e] : nothing;
                 }
               }
               some(x[g >> 4 & 1], g);
